@@ -168,6 +168,10 @@ va_status varlen_attn_tile_sizes(int32_t kind, int32_t d, int32_t* BM, int32_t* 
  * (for_bwd = 1) needs for this shape.  Depends on T, B, Hq, Hkv, d, max_seqlen. */
 size_t varlen_attn_workspace_size(const va_shape* shape, int32_t for_bwd);
 
+/* varlen_attn_workspace_size for a call with this window and sink count (varlen_attn_fwd_sinks,
+ * varlen_attn_bwd_sinks); 0 when the shape, window or sinks are refused. */
+size_t varlen_attn_workspace_size_sinks(const va_shape* shape, int32_t window, int32_t sinks, int32_t for_bwd);
+
 /* Builds a tile map on the device.  Source: "Packing与 FlashAttention
  * Varlen", section 5 (a q block exists only while m*BM < l; its key blocks
  * stop at ceil(min(l, (m+1)*BM)/BN) when causal, ceil(l/BN) otherwise).  The
@@ -212,6 +216,17 @@ va_status varlen_attn_plan_window(const va_shape* shape, const int32_t* cu_seqle
                                   int32_t causal, int32_t window, int32_t* tile_map_dev, int32_t capacity,
                                   int32_t* n_items_dev, int32_t* scratch_dev, va_stream_t stream);
 
+/* varlen_attn_plan_window with sinks: the first `sinks` tokens of every segment stay visible to
+ * all later queries of it (query i sees the keys j <= i with j >= i - window or j < sinks).  A
+ * q block also lists the key blocks [0, ceil(min(sinks, l) / BN)) that lie before its window's
+ * first one, count = both parts; a kv block that holds a sink lists its q blocks from its
+ * diagonal to the segment's end.  Orders as varlen_attn_plan_window; sinks = 0 is that call.
+ * Errors as it, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */
+va_status varlen_attn_plan_sinks(const va_shape* shape, const int32_t* cu_seqlens_dev, int32_t kind,
+                                 int32_t causal, int32_t window, int32_t sinks, int32_t* tile_map_dev,
+                                 int32_t capacity, int32_t* n_items_dev, int32_t* scratch_dev,
+                                 va_stream_t stream);
+
 /* ---------------------------------------------------------------- attention
  * Forward.  Source: "Packing与 FlashAttention Varlen", section 5 (each segment
  * b reads Q/K/V at offset cu[b]*row_stride with extent cu[b+1]-cu[b]; the
@@ -243,6 +258,21 @@ va_status varlen_attn_fwd_window(const void* q_dev, const void* k_dev, const voi
                                  int32_t causal, int32_t window, void* out_dev, float* lse_dev, void* ws_dev,
                                  size_t ws_bytes, va_stream_t stream);
 
+/* varlen_attn_fwd_window with sinks: the first `sinks` tokens of every segment stay visible to
+ * all later queries of it,
+ *     query i sees key j  when  j <= i and (j >= i - window or j < sinks)   (segment-local),
+ * one softmax over both parts.  The pages have no counterpart: it is the local window of
+ * varlen_attn_fwd_window for models whose softmax leans on the first tokens of a document.
+ * sinks = 0 is varlen_attn_fwd_window; a window or a sink count beyond max_seqlen means all of
+ * the segment.  No token tiles, no cross-attention.  As in every attention call, the tiles read
+ * K and V rows past a query's visible keys (later tokens, neighbouring segments): their values
+ * carry weight zero and must be finite.  Workspace as varlen_attn_fwd.  Errors as
+ * varlen_attn_fwd_window, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */
+va_status varlen_attn_fwd_sinks(const void* q_dev, const void* k_dev, const void* v_dev,
+                                const int32_t* cu_seqlens_dev, const va_shape* shape, float scale,
+                                int32_t causal, int32_t window, int32_t sinks, void* out_dev,
+                                float* lse_dev, void* ws_dev, size_t ws_bytes, va_stream_t stream);
+
 /* Backward.  The analytic gradient of the forward definition, with P
  * recomputed from lse ("Packing与 FlashAttention Varlen", section 5 names the
  * training branch; the gradient itself is the plain derivative):
@@ -266,6 +296,14 @@ va_status varlen_attn_bwd_window(const void* q_dev, const void* k_dev, const voi
                                  const int32_t* cu_seqlens_dev, const va_shape* shape, float scale,
                                  int32_t causal, int32_t window, void* dq_dev, void* dk_dev, void* dv_dev,
                                  void* ws_dev, size_t ws_bytes, va_stream_t stream);
+
+/* varlen_attn_bwd for the window and sinks of varlen_attn_fwd_sinks (the same ones as the
+ * forward that produced out and lse); sinks = 0 is varlen_attn_bwd_window. */
+va_status varlen_attn_bwd_sinks(const void* q_dev, const void* k_dev, const void* v_dev,
+                                const void* out_dev, const float* lse_dev, const void* dout_dev,
+                                const int32_t* cu_seqlens_dev, const va_shape* shape, float scale,
+                                int32_t causal, int32_t window, int32_t sinks, void* dq_dev, void* dk_dev,
+                                void* dv_dev, void* ws_dev, size_t ws_bytes, va_stream_t stream);
 
 /* Forward without a workspace, for callers that cannot allocate device memory
  * where they run attention (a plugin inside a host runtime that owns all device

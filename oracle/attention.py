@@ -27,6 +27,8 @@ Local window ("Packing与 FlashAttention Varlen", section 5: a local window furt
 narrows the key blocks a query block may see): with ``window = w`` (causal only),
 query i sees the keys i - w <= j <= i of its segment, i.e. itself and the w keys
 before it (FlashAttention's left window size; its right size is 0 under causality).
+With ``sinks = s`` as well, the segment's first s tokens stay visible: query i sees the
+keys j <= i with j >= i - w or j < s.
 
 Cross-attention (``cu_k`` given, blog section 3: cu_q and cu_k cut Q and K/V separately,
 the b-th Q slice and K/V slice belong to the same sample; section 5: the causal bound is
@@ -67,29 +69,31 @@ def _expand(x: np.ndarray, g: int) -> np.ndarray:
     return np.repeat(x, g, axis=1).transpose(1, 0, 2)
 
 
-def _visible(i, j, causal: bool, window, off: int = 0):
+def _visible(i, j, causal: bool, window, off: int = 0, sinks: int = 0):
     """Permission of query rows i (column vector) on key columns j (row vector); off is the
     bottom-right causal offset lk - lq (0 for self-attention)."""
     if not causal:
         return np.ones(np.broadcast(i, j).shape, dtype=bool)
     vis = j <= i + off
     if window is not None:
-        vis = vis & (j >= i - window)
+        vis = vis & ((j >= i - window) | (j < sinks))
     return vis
 
 
-def _check_window(causal: bool, window):
+def _check_window(causal: bool, window, sinks: int = 0):
     if window is not None and (not causal or window < 0):
         raise ValueError("a local window needs causal attention and window >= 0")
+    if sinks < 0 or (sinks and window is None):
+        raise ValueError("sinks >= 0, and sinks need a local window")
 
 
-def segment_forward(q, k, v, scale: float, causal: bool = True, window=None):
+def segment_forward(q, k, v, scale: float, causal: bool = True, window=None, sinks: int = 0):
     """One segment, all heads.  q [lq,Hq,d], k/v [lk,Hkv,d] (float64); lq == lk unless
     cross-attention (bottom-right causal alignment, lq <= lk when causal).
 
     Returns (o [lq,Hq,d], lse [Hq,lq]).
     """
-    _check_window(causal, window)
+    _check_window(causal, window, sinks)
     l, Hq, d = q.shape
     lk = k.shape[0]
     off = lk - l
@@ -111,7 +115,7 @@ def segment_forward(q, k, v, scale: float, causal: bool = True, window=None):
         if causal:
             i = np.arange(r0, r1)[:, None]
             j = np.arange(kend)[None, :]
-            s = np.where(_visible(i, j, causal, window, off), s, -np.inf)
+            s = np.where(_visible(i, j, causal, window, off, sinks), s, -np.inf)
         mx = s.max(axis=2, keepdims=True)
         e = np.exp(s - mx)
         z = e.sum(axis=2, keepdims=True)
@@ -120,13 +124,13 @@ def segment_forward(q, k, v, scale: float, causal: bool = True, window=None):
     return o.transpose(1, 0, 2), lse
 
 
-def segment_backward(q, k, v, o, lse, do, scale: float, causal: bool = True, window=None):
+def segment_backward(q, k, v, o, lse, do, scale: float, causal: bool = True, window=None, sinks: int = 0):
     """Analytic backward of ``segment_forward`` for one segment.
 
     ``o``/``lse`` are this oracle's own forward results.  Returns (dq, dk, dv)
     with the shapes of q, k, v.
     """
-    _check_window(causal, window)
+    _check_window(causal, window, sinks)
     l, Hq, d = q.shape
     Hkv = k.shape[1]
     g = Hq // Hkv
@@ -151,7 +155,7 @@ def segment_backward(q, k, v, o, lse, do, scale: float, causal: bool = True, win
         if causal:
             i = np.arange(r0, r1)[:, None]
             j = np.arange(kend)[None, :]
-            p = np.where(_visible(i, j, causal, window, off), p, 0.0)
+            p = np.where(_visible(i, j, causal, window, off, sinks), p, 0.0)
         dVx[:, :kend] += p.transpose(0, 2, 1) @ dO[:, r0:r1]
         dp = dO[:, r0:r1] @ V[:, :kend].transpose(0, 2, 1)
         ds = p * (dp - D[:, r0:r1, None])
@@ -171,7 +175,7 @@ def _head_slices(Hq: int, Hkv: int, kv_heads):
 
 
 def varlen_forward(q, k, v, cu_seqlens, scale=None, causal=True, kv_heads=None, window=None,
-                   cu_seqlens_k=None):
+                   cu_seqlens_k=None, sinks: int = 0):
     """Packed forward: every segment of ``cu_seqlens`` is its own attention.
 
     q [T,Hq,d], k/v [T,Hkv,d] float64.  Returns (o [T,Hq,d], lse [Hq,T]).
@@ -197,14 +201,14 @@ def varlen_forward(q, k, v, cu_seqlens, scale=None, causal=True, kv_heads=None, 
         for hk in kvh:
             hq = slice(hk * g, (hk + 1) * g)
             ob, lb = segment_forward(q[s:e, hq], k[sk:ek, hk:hk + 1], v[sk:ek, hk:hk + 1],
-                                     scale, causal, window)
+                                     scale, causal, window, sinks)
             o[s:e, hq] = ob
             lse[hq, s:e] = lb
     return o, lse
 
 
 def varlen_backward(q, k, v, o, lse, do, cu_seqlens, scale=None, causal=True,
-                    kv_heads=None, window=None, cu_seqlens_k=None):
+                    kv_heads=None, window=None, cu_seqlens_k=None, sinks: int = 0):
     """Packed backward (dq, dk, dv); entries of heads outside ``kv_heads`` are NaN."""
     T, Hq, d = q.shape
     Hkv = k.shape[1]
@@ -222,7 +226,7 @@ def varlen_backward(q, k, v, o, lse, do, cu_seqlens, scale=None, causal=True,
             hq = slice(hk * g, (hk + 1) * g)
             a, bk, c = segment_backward(q[s:e, hq], k[sk:ek, hk:hk + 1], v[sk:ek, hk:hk + 1],
                                         o[s:e, hq], lse[hq, s:e], do[s:e, hq],
-                                        scale, causal, window)
+                                        scale, causal, window, sinks)
             dq[s:e, hq] = a
             dk[sk:ek, hk:hk + 1] = bk
             dv[sk:ek, hk:hk + 1] = c

@@ -53,7 +53,10 @@ n_block_min/max"): q block m's key blocks run from n_min = floor(max(0, m*BM - w
 to its diagonal, count = n_max - n_min; kv block n's q blocks run from its diagonal
 floor(n*BN / BM) to floor((n*BN + BN - 1 + w) / BM) (capped by the segment).  Window
 maps have no token records and keep each segment's blocks in block order (q blocks
-descending, kv blocks ascending), which is the no-window order as well.
+descending, kv blocks ascending), which is the no-window order as well.  With sinks s a
+q block also lists the key blocks that hold the segment's first s keys and that lie before
+n_min, count = both parts, and a kv block with n*BN < s keeps its q blocks to the segment's
+end.
 """
 from __future__ import annotations
 
@@ -79,8 +82,13 @@ def window_q_end(n: int, l: int, BM: int, BN: int, window) -> int:
     return Mq if window is None else min(Mq, (n * BN + BN - 1 + window) // BM + 1)
 
 
+def sink_blocks(m: int, l: int, BM: int, BN: int, window, sinks: int) -> int:
+    """Key blocks before the window of q block m that hold sinks."""
+    return min(window_key_start(m, BM, BN, window), _ceil(min(sinks, l), BN))
+
+
 def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, short: int = 0, window=None,
-                 cu_k=None):
+                 cu_k=None, sinks: int = 0):
     """Items as an int32 array [N, 4], in the order above: segment records
     (b, m, h, n_blocks), then (causal, short > 0) token records (-1 - f, t0, h, rows)."""
     cu = [int(x) for x in cu_seqlens]
@@ -97,7 +105,7 @@ def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, sho
         blocks = []
         for m in range(_ceil(l, BM)):
             nb = _ceil(min(lk, (m + 1) * BM + lk - l), BN) if causal else _ceil(lk, BN)
-            blocks.append((m, nb - window_key_start(m, BM, BN, window)))
+            blocks.append((m, nb - window_key_start(m, BM, BN, window) + sink_blocks(m, l, BM, BN, window, sinks)))
         cls = _cost_class(sum(nb for _, nb in blocks))
         for h in range(Hq):
             for m, nb in blocks:
@@ -109,7 +117,7 @@ def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, sho
 
 
 def bwd_tile_map(cu_seqlens, Hkv: int, BM: int, BN: int, causal: bool = True, short: int = 0, window=None,
-                 cu_k=None):
+                 cu_k=None, sinks: int = 0):
     """Items as an int32 array [N, 4], in the order above: segment records
     (b, n, h_kv, n_q), then (causal, short > 0) token records (-1 - f, t0, h_kv, rows)
     whose BN-row tiles hold the key rows [t0, t0 + rows) of a run of short segments."""
@@ -127,7 +135,7 @@ def bwd_tile_map(cu_seqlens, Hkv: int, BM: int, BN: int, causal: bool = True, sh
         blocks = []
         for n in range(_ceil(lk, BN)):
             m_start = max(0, n * BN - (lk - l)) // BM if causal else 0
-            blocks.append((n, window_q_end(n, l, BM, BN, window) - m_start))
+            blocks.append((n, window_q_end(n, l, BM, BN, None if n * BN < sinks else window) - m_start))
         cls = _cost_class(sum(nq for _, nq in blocks))
         for h in range(Hkv):
             for n, nq in blocks:

@@ -147,19 +147,22 @@ def tile_sizes(kind: int, d: int):
     return bm.value, bn.value
 
 
-def workspace_size(T, B, Hq, Hkv, d, max_seqlen, for_bwd: bool) -> int:
+def workspace_size(T, B, Hq, Hkv, d, max_seqlen, for_bwd: bool, window: int | None = None, sinks: int = 0) -> int:
     s = _contig_shape(T, B, Hq, Hkv, d, max_seqlen)
     lib = _lib.load()
-    n = lib.varlen_attn_workspace_size(ctypes.byref(s), int(for_bwd))
+    n = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), -1 if window is None else int(window), int(sinks),
+                                             int(for_bwd))
     if n == 0:  # the shape check failed: the plan entry point reports why
-        check(lib.varlen_attn_plan(ctypes.byref(s), None, 0, 1, None, 0, None, None, None))
+        check(lib.varlen_attn_plan_sinks(ctypes.byref(s), None, 0, 1, -1 if window is None else int(window),
+                                         int(sinks), None, 0, None, None, None))
     return n
 
 
 def plan(cu_seqlens: torch.Tensor, T: int, Hq: int, Hkv: int, d: int, max_seqlen: int,
-         kind: int = 0, causal: bool = True, window: int | None = None):
+         kind: int = 0, causal: bool = True, window: int | None = None, sinks: int = 0):
     """Tile map on the device: (records int32 [n, 4], n).  ``window``: causal local window
-    (query i sees keys i - window .. i), None for none."""
+    (query i sees keys i - window .. i), None for none; ``sinks``: first tokens of every segment
+    that stay visible beyond the window."""
     B = cu_seqlens.numel() - 1
     s = _contig_shape(T, B, Hq, Hkv, d, max_seqlen)
     BM, BN = tile_sizes(kind, d)
@@ -169,9 +172,9 @@ def plan(cu_seqlens: torch.Tensor, T: int, Hq: int, Hkv: int, d: int, max_seqlen
     tm = torch.empty((max(cap, 1), 4), dtype=torch.int32, device=cu_seqlens.device)
     n = torch.zeros(1, dtype=torch.int32, device=cu_seqlens.device)
     scratch = torch.empty(B + 4, dtype=torch.int32, device=cu_seqlens.device)
-    check(_lib.load().varlen_attn_plan_window(ctypes.byref(s), _ptr(cu_seqlens), kind, int(causal),
-                                              -1 if window is None else int(window), _ptr(tm), cap, _ptr(n),
-                                              _ptr(scratch), _stream(cu_seqlens.device)))
+    check(_lib.load().varlen_attn_plan_sinks(ctypes.byref(s), _ptr(cu_seqlens), kind, int(causal),
+                                             -1 if window is None else int(window), int(sinks), _ptr(tm), cap,
+                                             _ptr(n), _ptr(scratch), _stream(cu_seqlens.device)))
     k = int(n.item())
     return tm[:k], k
 
@@ -198,9 +201,10 @@ def _check_inputs(*ts):
 
 def varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = None,
                     causal: bool = True, out=None, lse=None, workspace=None, check_status=False,
-                    window: int | None = None):
+                    window: int | None = None, sinks: int = 0):
     """Forward: returns (out [T,Hq,d] bf16, lse [Hq,T] fp32).  ``window``: causal local window
-    (query i sees keys i - window .. i of its segment), None for none."""
+    (query i sees keys i - window .. i of its segment), None for none.  ``sinks`` (with a
+    window): every segment's first tokens that stay visible to all its later queries."""
     win = -1 if window is None else int(window)
     _check_inputs(q, k, v)
     T, Hq, d = q.shape
@@ -214,14 +218,14 @@ def varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = 
     lib = _lib.load()
     need = lib.varlen_attn_workspace_size(ctypes.byref(s), 0)
     if need == 0:
-        check(lib.varlen_attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s),
-                                         scale, int(causal), win, _ptr(out), _ptr(lse), _ptr(None), 0,
-                                         _stream(q.device)))
+        check(lib.varlen_attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s),
+                                        scale, int(causal), win, int(sinks), _ptr(out), _ptr(lse), _ptr(None), 0,
+                                        _stream(q.device)))
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    check(lib.varlen_attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s), scale,
-                                     int(causal), win, _ptr(out), _ptr(lse), _ptr(workspace),
-                                     workspace.numel(), _stream(q.device)))
+    check(lib.varlen_attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s), scale,
+                                    int(causal), win, int(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
+                                    workspace.numel(), _stream(q.device)))
     if check_status:
         _raise_status(workspace)
     return out, lse
@@ -229,9 +233,9 @@ def varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = 
 
 def varlen_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int,
                     scale: float | None = None, causal: bool = True, dq=None, dk=None, dv=None,
-                    workspace=None, check_status=False, window: int | None = None):
-    """Backward: returns (dq, dk, dv) bf16 with the shapes of q, k, v (``window`` as in the
-    forward that produced out and lse)."""
+                    workspace=None, check_status=False, window: int | None = None, sinks: int = 0):
+    """Backward: returns (dq, dk, dv) bf16 with the shapes of q, k, v (``window`` and ``sinks``
+    as in the forward that produced out and lse)."""
     _check_inputs(q, k, v, out, dout)
     if out.stride() != dout.stride():
         raise ValueError("out and dout must share strides")
@@ -248,13 +252,13 @@ def varlen_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int,
         raise ValueError("dq must share out's strides and dk/dv k's strides")
     s = make_shape(q, k, v, B, max_seqlen, out)
     lib = _lib.load()
-    need = lib.varlen_attn_workspace_size(ctypes.byref(s), 1)
+    need = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), -1 if window is None else int(window), int(sinks), 1)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    check(lib.varlen_attn_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                                     _ptr(cu_seqlens), ctypes.byref(s), scale, int(causal),
-                                     -1 if window is None else int(window), _ptr(dq), _ptr(dk), _ptr(dv),
-                                     _ptr(workspace), workspace.numel(), _stream(q.device)))
+    check(lib.varlen_attn_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                    _ptr(cu_seqlens), ctypes.byref(s), scale, int(causal),
+                                    -1 if window is None else int(window), int(sinks), _ptr(dq), _ptr(dk),
+                                    _ptr(dv), _ptr(workspace), workspace.numel(), _stream(q.device)))
     if check_status:
         _raise_status(workspace)
     return dq, dk, dv
@@ -262,10 +266,10 @@ def varlen_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int,
 
 class _VarlenAttn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens, max_seqlen, scale, causal, window):
-        out, lse = varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen, scale, causal, window=window)
+    def forward(ctx, q, k, v, cu_seqlens, max_seqlen, scale, causal, window, sinks):
+        out, lse = varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen, scale, causal, window=window, sinks=sinks)
         ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
-        ctx.max_seqlen, ctx.scale, ctx.causal, ctx.window = max_seqlen, scale, causal, window
+        ctx.max_seqlen, ctx.scale, ctx.causal, ctx.window, ctx.sinks = max_seqlen, scale, causal, window, sinks
         return out
 
     @staticmethod
@@ -273,14 +277,15 @@ class _VarlenAttn(torch.autograd.Function):
         q, k, v, out, lse, cu = ctx.saved_tensors
         dout = dout.contiguous() if dout.stride() != out.stride() else dout
         dq, dk, dv = varlen_attn_bwd(q, k, v, out, lse, dout, cu, ctx.max_seqlen, ctx.scale,
-                                     ctx.causal, window=ctx.window)
-        return dq, dk, dv, None, None, None, None, None
+                                     ctx.causal, window=ctx.window, sinks=ctx.sinks)
+        return dq, dk, dv, None, None, None, None, None, None
 
 
 def varlen_attn(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = None,
-                causal: bool = True, window: int | None = None):
-    """Differentiable packed attention: out [T, Hq, d] (``window``: causal local window)."""
-    return _VarlenAttn.apply(q, k, v, cu_seqlens, max_seqlen, scale, causal, window)
+                causal: bool = True, window: int | None = None, sinks: int = 0):
+    """Differentiable packed attention: out [T, Hq, d] (``window``: causal local window;
+    ``sinks``: first tokens of every segment that stay visible beyond it)."""
+    return _VarlenAttn.apply(q, k, v, cu_seqlens, max_seqlen, scale, causal, window, sinks)
 
 
 # ----------------------------------------------------------------- cross-attention

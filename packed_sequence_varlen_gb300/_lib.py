@@ -31,6 +31,7 @@ EXPORTS = (
     "varlen_attn_plan_window", "varlen_attn_fwd_window", "varlen_attn_bwd_window",
     "varlen_attn_workspace_size_cross", "varlen_attn_plan_cross", "varlen_attn_fwd_cross",
     "varlen_attn_bwd_cross", "varlen_test_stall_next_forward",
+    "varlen_attn_workspace_size_sinks", "varlen_attn_plan_sinks", "varlen_attn_fwd_sinks", "varlen_attn_bwd_sinks",
 )
 
 
@@ -83,6 +84,15 @@ def _declare(lib):
         "varlen_attn_bwd_window": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                              c_void_p, POINTER(VaShape), c_float, c_int32, c_int32,
                                              c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "varlen_attn_workspace_size_sinks": (c_size_t, [POINTER(VaShape), c_int32, c_int32, c_int32]),
+        "varlen_attn_plan_sinks": (c_int32, [POINTER(VaShape), c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                             c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
+        "varlen_attn_fwd_sinks": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(VaShape),
+                                            c_float, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                            c_size_t, c_void_p]),
+        "varlen_attn_bwd_sinks": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                            c_void_p, POINTER(VaShape), c_float, c_int32, c_int32, c_int32,
+                                            c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "varlen_attn_workspace_size_cross": (c_size_t, [POINTER(VaShape), c_int32, c_int32]),
         "varlen_attn_plan_cross": (c_int32, [POINTER(VaShape), c_void_p, c_void_p, c_int32, c_int32, c_int32,
                                              c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),

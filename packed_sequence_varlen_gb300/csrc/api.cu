@@ -155,6 +155,18 @@ va_status check_shape(const va_shape* s) {
   return VA_OK;
 }
 
+// Window and sink arguments of a valid shape.  No query sees further back than the longest
+// segment, so both are cut to it: the kernels' column arithmetic then stays far inside 32 bits.
+va_status check_window(const va_shape* s, int32_t causal, int32_t* window, int32_t* sinks, const char* where) {
+  if (*window < -1 || (*window >= 0 && !causal))
+    return fail(VA_ERR_INVALID_ARG, std::string(where) + ": window needs causal and >= 0 (-1 = none)");
+  if (*sinks < 0 || (*sinks > 0 && *window < 0))
+    return fail(VA_ERR_INVALID_ARG, std::string(where) + ": sinks >= 0, and sinks need a window");
+  *window = std::min(*window, s->max_seqlen);
+  *sinks = std::min(*sinks, s->max_seqlen);
+  return VA_OK;
+}
+
 struct FwdLayout {
   size_t map, segoff, total;
   int64_t cap;
@@ -190,15 +202,15 @@ BwdLayout bwd_layout(const va_shape& s, int Tk = -1) {
 using namespace va;
 
 static va_status plan_impl(const va_shape* s, const int32_t* cu_dev, const int32_t* cu_k, int32_t Tk, int32_t kind,
-                           int32_t causal, int32_t window, int32_t* map_dev, int32_t capacity, int32_t* n_items_dev,
-                           int32_t* scratch_dev, va_stream_t stream);
+                           int32_t causal, int32_t window, int32_t sinks, int32_t* map_dev, int32_t capacity,
+                           int32_t* n_items_dev, int32_t* scratch_dev, va_stream_t stream);
 static va_status fwd_impl(const void* q, const void* k, const void* v, const int32_t* cu, const int32_t* cu_k,
                           int32_t Tk, int32_t max_k, const va_shape* s, float scale, int32_t causal, int32_t window,
-                          void* out, float* lse, void* ws, size_t ws_bytes, va_stream_t stream);
+                          int32_t sinks, void* out, float* lse, void* ws, size_t ws_bytes, va_stream_t stream);
 static va_status bwd_impl(const void* q, const void* k, const void* v, const void* out, const float* lse,
                           const void* dout, const int32_t* cu, const int32_t* cu_k, int32_t Tk, int32_t max_k,
-                          const va_shape* s, float scale, int32_t causal, int32_t window, void* dq, void* dk, void* dv,
-                          void* ws, size_t ws_bytes, va_stream_t stream);
+                          const va_shape* s, float scale, int32_t causal, int32_t window, int32_t sinks, void* dq,
+                          void* dk, void* dv, void* ws, size_t ws_bytes, va_stream_t stream);
 
 extern "C" {
 
@@ -287,6 +299,11 @@ size_t varlen_attn_workspace_size(const va_shape* s, int32_t for_bwd) {
   return for_bwd ? bwd_layout(*s).total : fwd_layout(*s).total;
 }
 
+size_t varlen_attn_workspace_size_sinks(const va_shape* s, int32_t window, int32_t sinks, int32_t for_bwd) {
+  if (check_shape(s) != VA_OK || check_window(s, 1, &window, &sinks, "workspace_size") != VA_OK) return 0;
+  return for_bwd ? bwd_layout(*s).total : fwd_layout(*s).total;
+}
+
 va_status varlen_attn_plan(const va_shape* s, const int32_t* cu_dev, int32_t kind, int32_t causal,
                            int32_t* map_dev, int32_t capacity, int32_t* n_items_dev,
                            int32_t* scratch_dev, va_stream_t stream) {
@@ -296,24 +313,31 @@ va_status varlen_attn_plan(const va_shape* s, const int32_t* cu_dev, int32_t kin
 va_status varlen_attn_plan_window(const va_shape* s, const int32_t* cu_dev, int32_t kind, int32_t causal,
                                   int32_t window, int32_t* map_dev, int32_t capacity, int32_t* n_items_dev,
                                   int32_t* scratch_dev, va_stream_t stream) {
-  return plan_impl(s, cu_dev, nullptr, -1, kind, causal, window, map_dev, capacity, n_items_dev, scratch_dev, stream);
+  return plan_impl(s, cu_dev, nullptr, -1, kind, causal, window, 0, map_dev, capacity, n_items_dev, scratch_dev, stream);
+}
+
+va_status varlen_attn_plan_sinks(const va_shape* s, const int32_t* cu_dev, int32_t kind, int32_t causal,
+                                 int32_t window, int32_t sinks, int32_t* map_dev, int32_t capacity,
+                                 int32_t* n_items_dev, int32_t* scratch_dev, va_stream_t stream) {
+  return plan_impl(s, cu_dev, nullptr, -1, kind, causal, window, sinks, map_dev, capacity, n_items_dev, scratch_dev,
+                   stream);
 }
 
 va_status varlen_attn_plan_cross(const va_shape* s, const int32_t* cu_q, const int32_t* cu_k, int32_t Tk, int32_t kind,
                                  int32_t causal, int32_t* map_dev, int32_t capacity, int32_t* n_items_dev,
                                  int32_t* scratch_dev, va_stream_t stream) {
-  return plan_impl(s, cu_q, cu_k, Tk, kind, causal, -1, map_dev, capacity, n_items_dev, scratch_dev, stream);
+  return plan_impl(s, cu_q, cu_k, Tk, kind, causal, -1, 0, map_dev, capacity, n_items_dev, scratch_dev, stream);
 }
 
 }  // extern "C"
 
 static va_status plan_impl(const va_shape* s, const int32_t* cu_dev, const int32_t* cu_k, int32_t Tk, int32_t kind,
-                           int32_t causal, int32_t window, int32_t* map_dev, int32_t capacity, int32_t* n_items_dev,
-                           int32_t* scratch_dev, va_stream_t stream) {
+                           int32_t causal, int32_t window, int32_t sinks, int32_t* map_dev, int32_t capacity,
+                           int32_t* n_items_dev, int32_t* scratch_dev, va_stream_t stream) {
   va_status st = check_shape(s);
   if (st != VA_OK) return st;
   if (cu_k && (st = check_cross(s, cu_k, Tk, std::max(Tk, 1), window)) != VA_OK) return st;
-  if (window < -1 || (window >= 0 && !causal)) return fail(VA_ERR_INVALID_ARG, "plan: window needs causal and >= 0 (-1 = none)");
+  if ((st = check_window(s, causal, &window, &sinks, "plan")) != VA_OK) return st;
   if (kind < 0 || kind > 2 || !cu_dev || !map_dev || !n_items_dev || !scratch_dev || capacity < 0)
     return fail(VA_ERR_INVALID_ARG, "plan: bad kind or null pointer");
   if (!aligned16(map_dev)) return fail(VA_ERR_INVALID_ARG, "plan: tile map must be 16-byte aligned");
@@ -328,7 +352,7 @@ static va_status plan_impl(const va_shape* s, const int32_t* cu_dev, const int32
                     (cu_k || !token_tiles(*s, causal, window)) ? 0
                     : kind == 0                                ? fwd_tc_token_short()
                                                                : bwd_tc_token_short(),
-                    nullptr, nullptr, window, cu_k};
+                    nullptr, nullptr, window, cu_k, sinks};
   cudaError_t e = launch(K_PLAN, cs, [&] { return launch_plan(pa, cs); });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "plan");
 }
@@ -344,24 +368,30 @@ va_status varlen_attn_fwd(const void* q, const void* k, const void* v, const int
 va_status varlen_attn_fwd_window(const void* q, const void* k, const void* v, const int32_t* cu,
                                  const va_shape* s, float scale, int32_t causal, int32_t window, void* out,
                                  float* lse, void* ws, size_t ws_bytes, va_stream_t stream) {
-  return fwd_impl(q, k, v, cu, nullptr, -1, 0, s, scale, causal, window, out, lse, ws, ws_bytes, stream);
+  return fwd_impl(q, k, v, cu, nullptr, -1, 0, s, scale, causal, window, 0, out, lse, ws, ws_bytes, stream);
+}
+
+va_status varlen_attn_fwd_sinks(const void* q, const void* k, const void* v, const int32_t* cu, const va_shape* s,
+                                float scale, int32_t causal, int32_t window, int32_t sinks, void* out, float* lse,
+                                void* ws, size_t ws_bytes, va_stream_t stream) {
+  return fwd_impl(q, k, v, cu, nullptr, -1, 0, s, scale, causal, window, sinks, out, lse, ws, ws_bytes, stream);
 }
 
 va_status varlen_attn_fwd_cross(const void* q, const void* k, const void* v, const int32_t* cu_q,
                                 const int32_t* cu_k, const va_shape* s, int32_t Tk, int32_t max_seqlen_k, float scale,
                                 int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, va_stream_t stream) {
-  return fwd_impl(q, k, v, cu_q, cu_k, Tk, max_seqlen_k, s, scale, causal, -1, out, lse, ws, ws_bytes, stream);
+  return fwd_impl(q, k, v, cu_q, cu_k, Tk, max_seqlen_k, s, scale, causal, -1, 0, out, lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"
 
 static va_status fwd_impl(const void* q, const void* k, const void* v, const int32_t* cu, const int32_t* cu_k,
                           int32_t Tk, int32_t max_k, const va_shape* s, float scale, int32_t causal, int32_t window,
-                          void* out, float* lse, void* ws, size_t ws_bytes, va_stream_t stream) {
+                          int32_t sinks, void* out, float* lse, void* ws, size_t ws_bytes, va_stream_t stream) {
   va_status st = check_shape(s);
   if (st != VA_OK) return st;
   if (cu_k && (st = check_cross(s, cu_k, Tk, max_k, window)) != VA_OK) return st;
-  if (window < -1 || (window >= 0 && !causal)) return fail(VA_ERR_INVALID_ARG, "fwd: window needs causal and >= 0 (-1 = none)");
+  if ((st = check_window(s, causal, &window, &sinks, "fwd")) != VA_OK) return st;
   if (!q || !k || !v || !cu || !out || !lse || !ws)
     return fail(VA_ERR_INVALID_ARG, "fwd: null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(ws))
@@ -386,7 +416,7 @@ static va_status fwd_impl(const void* q, const void* k, const void* v, const int
                     &hdr->status, &hdr->n_items[0],
                     reinterpret_cast<int32_t*>(w + L.segoff), &hdr->counter[0],
                     tok ? fwd_tc_token_short() : 0, &hdr->n_items[kTokSlot],
-                    &hdr->counter[kTokSlot], window, cu_k};
+                    &hdr->counter[kTokSlot], window, cu_k, sinks};
   cudaError_t e = launch(K_VALIDATE_PLAN, cs, [&] {
     return launch_validate_plan(&pa, 1, s->T, s->max_seqlen, cu_k ? Tk : 0, cu_k ? max_k : 0, cs);
   });
@@ -418,6 +448,7 @@ static va_status fwd_impl(const void* q, const void* k, const void* v, const int
   p.scale_log2 = scale * kLog2e;
   p.causal = causal ? 1 : 0;
   p.window = window;
+  p.sinks = sinks;
   p.cu_k = cu_k;
   p.Tk = cu_k ? Tk : 0;
   const long long stall_ns = g_stall_next_fwd.exchange(0);
@@ -449,15 +480,23 @@ va_status varlen_attn_bwd_window(const void* q, const void* k, const void* v, co
                                  const float* lse, const void* dout, const int32_t* cu, const va_shape* s,
                                  float scale, int32_t causal, int32_t window, void* dq, void* dk, void* dv,
                                  void* ws, size_t ws_bytes, va_stream_t stream) {
-  return bwd_impl(q, k, v, out, lse, dout, cu, nullptr, -1, 0, s, scale, causal, window, dq, dk, dv, ws, ws_bytes,
+  return bwd_impl(q, k, v, out, lse, dout, cu, nullptr, -1, 0, s, scale, causal, window, 0, dq, dk, dv, ws, ws_bytes,
                   stream);
+}
+
+va_status varlen_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                const void* dout, const int32_t* cu, const va_shape* s, float scale, int32_t causal,
+                                int32_t window, int32_t sinks, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                va_stream_t stream) {
+  return bwd_impl(q, k, v, out, lse, dout, cu, nullptr, -1, 0, s, scale, causal, window, sinks, dq, dk, dv, ws,
+                  ws_bytes, stream);
 }
 
 va_status varlen_attn_bwd_cross(const void* q, const void* k, const void* v, const void* out, const float* lse,
                                 const void* dout, const int32_t* cu_q, const int32_t* cu_k, const va_shape* s,
                                 int32_t Tk, int32_t max_seqlen_k, float scale, int32_t causal, void* dq, void* dk,
                                 void* dv, void* ws, size_t ws_bytes, va_stream_t stream) {
-  return bwd_impl(q, k, v, out, lse, dout, cu_q, cu_k, Tk, max_seqlen_k, s, scale, causal, -1, dq, dk, dv, ws,
+  return bwd_impl(q, k, v, out, lse, dout, cu_q, cu_k, Tk, max_seqlen_k, s, scale, causal, -1, 0, dq, dk, dv, ws,
                   ws_bytes, stream);
 }
 
@@ -470,12 +509,12 @@ size_t varlen_attn_workspace_size_cross(const va_shape* s, int32_t Tk, int32_t f
 
 static va_status bwd_impl(const void* q, const void* k, const void* v, const void* out, const float* lse,
                           const void* dout, const int32_t* cu, const int32_t* cu_k, int32_t Tk, int32_t max_k,
-                          const va_shape* s, float scale, int32_t causal, int32_t window, void* dq, void* dk, void* dv,
-                          void* ws, size_t ws_bytes, va_stream_t stream) {
+                          const va_shape* s, float scale, int32_t causal, int32_t window, int32_t sinks, void* dq,
+                          void* dk, void* dv, void* ws, size_t ws_bytes, va_stream_t stream) {
   va_status st = check_shape(s);
   if (st != VA_OK) return st;
   if (cu_k && (st = check_cross(s, cu_k, Tk, max_k, window)) != VA_OK) return st;
-  if (window < -1 || (window >= 0 && !causal)) return fail(VA_ERR_INVALID_ARG, "bwd: window needs causal and >= 0 (-1 = none)");
+  if ((st = check_window(s, causal, &window, &sinks, "bwd")) != VA_OK) return st;
   if (!q || !k || !v || !out || !lse || !dout || !cu || !dq || !dk || !dv || !ws)
     return fail(VA_ERR_INVALID_ARG, "bwd: null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) ||
@@ -503,10 +542,10 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   const PlanArgs pa[2] = {
       {cu, s->B, s->Hkv, BM, BN, 1, causal ? 1 : 0, kvmap, static_cast<int>(L.cap_kv), &hdr->status,
        &hdr->n_items[1], segoff, &hdr->counter[1], tok ? bwd_tc_token_short() : 0,
-       &hdr->n_items[kKvTokSlot], nullptr, window, cu_k},
+       &hdr->n_items[kKvTokSlot], nullptr, window, cu_k, sinks},
       {cu, s->B, s->Hq, BM2, BN2, 2, causal ? 1 : 0, qmap, static_cast<int>(L.cap_q), &hdr->status,
        &hdr->n_items[2], segoff, &hdr->counter[2], tok ? bwd_tc_token_short() : 0,
-       &hdr->n_items[kQTokSlot], nullptr, window, cu_k}};
+       &hdr->n_items[kQTokSlot], nullptr, window, cu_k, sinks}};
   BwdParams p{};
   p.q = static_cast<const bf16*>(q);
   p.k = static_cast<const bf16*>(k);
@@ -545,6 +584,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   p.scale_log2 = scale * kLog2e;
   p.causal = causal ? 1 : 0;
   p.window = window;
+  p.sinks = sinks;
   p.cu_k = cu_k;
   p.Tk = cu_k ? Tk : 0;
   // one launch validates, plans both maps and computes D = rowsum(dO * O)

@@ -6,6 +6,9 @@ namespace va {
 
 using bf16 = __nv_bfloat16;
 
+// Forms of the attention kernels: no local window, a causal local window, a window with sinks.
+enum WinForm : int { kWinNone = 0, kWinLocal = 1, kWinSinks = 2 };
+
 struct FwdParams {
   const bf16* q;
   const bf16* k;
@@ -23,6 +26,7 @@ struct FwdParams {
   float scale_log2;  // scale * log2(e)
   int causal;
   int window = -1;   // causal local window: query i sees keys i-w..i; -1 = none
+  int sinks = 0;     // with a window: a segment's first keys that every later query still sees
   const int32_t* cu_k = nullptr;  // cross-attention: K/V boundaries (cu is Q's); null = cu
   int Tk = 0;                     // cross-attention: rows of K and V
   // Test hook of the failure path (varlen_test_stall_next_forward): a wait limit in ns
@@ -58,6 +62,7 @@ struct BwdParams {
   float scale_log2;
   int causal;
   int window = -1;   // causal local window: query i sees keys i-w..i; -1 = none
+  int sinks = 0;     // with a window: a segment's first keys that every later query still sees
   const int32_t* cu_k = nullptr;  // cross-attention: K/V boundaries (cu is Q's); null = cu
   int Tk = 0;                     // cross-attention: rows of K and V
 };

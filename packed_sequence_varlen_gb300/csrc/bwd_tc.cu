@@ -107,7 +107,7 @@ struct KvItem {
 };
 static_assert(sizeof(KvItem) <= 48, "queue slots are 48 bytes");
 
-template <bool WIN, bool X>
+template <int WIN, bool X>
 __device__ __forceinline__ KvItem kv_decode(const BwdParams& p, int idx) {
   const TileItem it = p.kv_items[idx];
   KvItem r;
@@ -181,9 +181,12 @@ __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx,
 
 // WIN: causal local window p.window: a kv block's q steps stop at the window of its last key
 // row, and steps that cross a key's window edge also mask the queries past key + w.
+// kWinSinks: as the window, and the segment's first p.sinks keys are seen by every later query:
+// a kv block that holds one takes its q steps to the segment's end, and those keys are masked
+// on the causal side only.
 // X: cross-attention (p.cu_k): the kv block's keys come from their own boundaries; query i
 // sees key j when j <= i + lk - lq, so the q steps start at floor(max(0, n*128 - off) / 64).
-template <int D, bool TOK, bool WIN, bool X>
+template <int D, bool TOK, int WIN, bool X>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -570,9 +573,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int q0 = (I.m_start + i / p.g) * 64 + cw;  // this warpgroup's first query column
         const int lim = kvrow - (X ? I.off : 0) - q0;  // query columns c < lim are masked (key after query)
         // (window) query columns c >= hi are masked too: past the key's window
-        const int hi = WIN ? kvrow + p.window + 1 - q0 : 0;
+        // (no bound for a sink)
+        const int hi = WIN ? (WIN == kWinSinks && kvrow < p.sinks ? INT_MAX : kvrow + p.window + 1 - q0) : 0;
         const bool need_mask =
-            p.causal && (I.n * 128 + 127 - (X ? I.off : 0) > q0 || (WIN && q0 + 31 > I.n * 128 + p.window));
+            p.causal && (I.n * 128 + 127 - (X ? I.off : 0) > q0 ||
+                         (WIN && q0 + 31 > I.n * 128 + p.window && (WIN != kWinSinks || I.n * 128 + 128 > p.sinks)));
         const float* L = ldring + ls * 128 + cw;
         const float* Dd = L + 64;
         // one TMEM round trip: this warpgroup's 32 scores and 32 dP values of this kv row
@@ -739,10 +744,11 @@ struct QItem {
   int valid;
   int kb;
   int lk, off;  // cross-attention: the keys' count, the causal offset lk - l
+  int ns;       // sinks: step n < ns covers the 64 key rows from s0 + 64 n instead
 };
 static_assert(sizeof(QItem) <= 48, "queue slots are 48 bytes");
 
-template <bool WIN, bool X>
+template <int WIN, bool X>
 __device__ __forceinline__ QItem q_decode(const BwdParams& p, int idx) {
   const TileItem it = p.q_items[idx];
   QItem r;
@@ -754,12 +760,22 @@ __device__ __forceinline__ QItem q_decode(const BwdParams& p, int idx) {
   r.nb = it.count;
   // key steps from the segment start, or (window) from the window of the item's first row
   r.kb = WIN ? r.s0 + max(0, it.blk * 128 - p.window) / 64 * 64 : r.s0;
+  if (WIN == kWinSinks) {  // the sink steps that the window does not reach come first
+    r.ns = min((r.kb - r.s0) / 64, (min(r.l, p.sinks) + 63) / 64);
+    r.kb -= r.ns * 64;
+  }
   if (X) {  // keys from cu_k, the causal bound moved by lk - l (bottom-right alignment)
     r.kb = p.cu_k[it.seg];
     r.lk = p.cu_k[it.seg + 1] - r.kb;
     r.off = p.causal ? r.lk - r.l : 0;
   }
   return r;
+}
+
+// The first key row (of the stream) of an item's step n.
+template <int WIN>
+__device__ __forceinline__ int key_row(const QItem& I, int n) {
+  return (WIN == kWinSinks && n < I.ns ? I.s0 : I.kb) + n * 64;
 }
 
 // Decodes dQ token record idx, {-1 - f, t0, q head, rows} (whole warp, every lane gets the
@@ -805,9 +821,11 @@ __device__ __forceinline__ QItem q_token_decode_w(const BwdParams& p, int idx, u
 
 // WIN: causal local window p.window: an item's key steps start at the window of its first
 // row, and steps that cross a query's window edge also mask the keys before query - w.
+// kWinSinks: as the window, with the steps that hold the segment's first p.sinks keys (visible to
+// every later query) and that the window does not reach before the window's steps.
 // X: cross-attention (p.cu_k): the keys come from their own boundaries and query i sees key
 // j when j <= i + lk - lq.
-template <int D, bool TOK, bool WIN, bool X>
+template <int D, bool TOK, int WIN, bool X>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -963,8 +981,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mbar_expect_tx_w(bar(C::B_KF + s), 2 * C::TKV);
           const uint32_t dst = base + C::RING_OFF + s * 2 * C::TKV;
           for (int pn = 0; pn < D / 64; ++pn) {
-            tma_load_3d_w(dst + pn * C::PKV, &tk, bar(C::B_KF + s), pn * 64, I.hk, I.kb + n * 64);
-            tma_load_3d_w(dst + C::TKV + pn * C::PKV, &tv, bar(C::B_KF + s), pn * 64, I.hk, I.kb + n * 64);
+            tma_load_3d_w(dst + pn * C::PKV, &tk, bar(C::B_KF + s), pn * 64, I.hk, key_row<WIN>(I, n));
+            tma_load_3d_w(dst + C::TKV + pn * C::PKV, &tv, bar(C::B_KF + s), pn * 64, I.hk, key_row<WIN>(I, n));
           }
           ++kit;
         }
@@ -1162,10 +1180,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float lse2 = qin ? lse_raw * kLog2e : INFINITY;
         // key columns c > lim are masked: after the query (causal) or past the segment end;
         // (window) key columns c < lo too: before the query's window
-        const int kn = (WIN ? I.kb - I.s0 : 0) + n * 64 + cw;  // this warpgroup's first key, segment-local
+        const int kn = (WIN ? key_row<WIN>(I, n) - I.s0 : n * 64) + cw;  // this warpgroup's first key, segment-local
         int lim = p.causal ? qrow - kn : I.l - 1 - kn;
-        const int lo = WIN ? qrow - p.window - kn : 0;
-        bool need_mask = p.causal ? (kn + 31 > I.m * 128 || (WIN && kn < I.m * 128 + 127 - p.window))
+        const int lo = WIN ? qrow - p.window - kn : 0, sk = WIN == kWinSinks ? p.sinks - kn : 0;  // (but not the sinks)
+        bool need_mask = p.causal ? (kn + 31 > I.m * 128 || (WIN && kn < I.m * 128 + 127 - p.window &&
+                                                          (WIN != kWinSinks || kn + 32 > p.sinks)))
                                   : (kn + 32 > I.l);
         if constexpr (X) {
           lim = p.causal ? qrow + I.off - kn : I.lk - 1 - kn;
@@ -1182,8 +1201,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ffma2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2, -lse2, -lse2);
           float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
           if (need_mask) {
-            if (c > lim || (WIN && c < lo)) p0 = 0.f;
-            if (c + 1 > lim || (WIN && c + 1 < lo)) p1 = 0.f;
+            if (c > lim || (WIN && c < lo && c >= sk)) p0 = 0.f;
+            if (c + 1 > lim || (WIN && c + 1 < lo && c + 1 >= sk)) p1 = 0.f;
           }
           float t0, t1;
           fadd2(t0, t1, __uint_as_float(dpv[c]), __uint_as_float(dpv[c + 1]), -dsum, -dsum);
@@ -1289,7 +1308,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------- host side
 
 
-template <int D, bool TOK, bool WIN, bool X>
+template <int D, bool TOK, int WIN, bool X>
 static cudaError_t launch_dkdv_d(const BwdParams& p, int cap, cudaStream_t st) {
   using C = KvCfg<D>;
   CUtensorMap tq, tk, tv, tdo;
@@ -1313,7 +1332,7 @@ static cudaError_t launch_dkdv_d(const BwdParams& p, int cap, cudaStream_t st) {
   return launch_pdl(dkdv_tc_kernel<D, TOK, WIN, X>, dim3(grid), dim3(kBwdThreads), C::SMEM, st, tq, tk, tv, tdo, p);
 }
 
-template <int D, bool TOK, bool WIN, bool X>
+template <int D, bool TOK, int WIN, bool X>
 static cudaError_t launch_dq_d(const BwdParams& p, int cap, cudaStream_t st) {
   using C = QCfg<D>;
   CUtensorMap tq, tk, tv, tdo;
@@ -1342,22 +1361,26 @@ static cudaError_t launch_dq_d(const BwdParams& p, int cap, cudaStream_t st) {
 // measured 15% slower on segment records.
 cudaError_t launch_bwd_dkdv_tc(const BwdParams& p, int d, int cap, bool tok, cudaStream_t st) {
   if (p.cu_k)  // cross and window calls plan no token records
-    return d == 64 ? launch_dkdv_d<64, false, false, true>(p, cap, st) : launch_dkdv_d<128, false, false, true>(p, cap, st);
+    return d == 64 ? launch_dkdv_d<64, false, kWinNone, true>(p, cap, st) : launch_dkdv_d<128, false, kWinNone, true>(p, cap, st);
+  if (p.window >= 0 && p.sinks > 0)
+    return d == 64 ? launch_dkdv_d<64, false, kWinSinks, false>(p, cap, st) : launch_dkdv_d<128, false, kWinSinks, false>(p, cap, st);
   if (p.window >= 0)
-    return d == 64 ? launch_dkdv_d<64, false, true, false>(p, cap, st) : launch_dkdv_d<128, false, true, false>(p, cap, st);
+    return d == 64 ? launch_dkdv_d<64, false, kWinLocal, false>(p, cap, st) : launch_dkdv_d<128, false, kWinLocal, false>(p, cap, st);
   if (tok)
-    return d == 64 ? launch_dkdv_d<64, true, false, false>(p, cap, st) : launch_dkdv_d<128, true, false, false>(p, cap, st);
-  return d == 64 ? launch_dkdv_d<64, false, false, false>(p, cap, st) : launch_dkdv_d<128, false, false, false>(p, cap, st);
+    return d == 64 ? launch_dkdv_d<64, true, kWinNone, false>(p, cap, st) : launch_dkdv_d<128, true, kWinNone, false>(p, cap, st);
+  return d == 64 ? launch_dkdv_d<64, false, kWinNone, false>(p, cap, st) : launch_dkdv_d<128, false, kWinNone, false>(p, cap, st);
 }
 
 cudaError_t launch_bwd_dq_tc(const BwdParams& p, int d, int cap, bool tok, cudaStream_t st) {
   if (p.cu_k)
-    return d == 64 ? launch_dq_d<64, false, false, true>(p, cap, st) : launch_dq_d<128, false, false, true>(p, cap, st);
+    return d == 64 ? launch_dq_d<64, false, kWinNone, true>(p, cap, st) : launch_dq_d<128, false, kWinNone, true>(p, cap, st);
+  if (p.window >= 0 && p.sinks > 0)
+    return d == 64 ? launch_dq_d<64, false, kWinSinks, false>(p, cap, st) : launch_dq_d<128, false, kWinSinks, false>(p, cap, st);
   if (p.window >= 0)
-    return d == 64 ? launch_dq_d<64, false, true, false>(p, cap, st) : launch_dq_d<128, false, true, false>(p, cap, st);
+    return d == 64 ? launch_dq_d<64, false, kWinLocal, false>(p, cap, st) : launch_dq_d<128, false, kWinLocal, false>(p, cap, st);
   if (tok)
-    return d == 64 ? launch_dq_d<64, true, false, false>(p, cap, st) : launch_dq_d<128, true, false, false>(p, cap, st);
-  return d == 64 ? launch_dq_d<64, false, false, false>(p, cap, st) : launch_dq_d<128, false, false, false>(p, cap, st);
+    return d == 64 ? launch_dq_d<64, true, kWinNone, false>(p, cap, st) : launch_dq_d<128, true, kWinNone, false>(p, cap, st);
+  return d == 64 ? launch_dq_d<64, false, kWinNone, false>(p, cap, st) : launch_dq_d<128, false, kWinNone, false>(p, cap, st);
 }
 
 int bwd_tc_token_short() { return kBwdTokenShort; }

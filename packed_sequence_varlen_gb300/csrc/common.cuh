@@ -55,6 +55,7 @@ struct PlanArgs {
   int window = -1;       // causal local window w >= 0 (query i sees keys i-w..i), -1 = none;
                          // window maps have no token records
   const int32_t* cu_k = nullptr;  // cross-attention: the K/V boundaries (cu is Q's); null = cu
+  int sinks = 0;         // with a window: a segment's first keys that every later query still sees
 };
 
 __device__ __forceinline__ void set_status(WsHeader* h, int code) {

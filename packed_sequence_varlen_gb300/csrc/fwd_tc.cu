@@ -69,12 +69,13 @@ struct Item {
   int s0, l, h, hk, m, nb, nb0;
   int t1;
   int valid;
-  int kb;  // local window: the item's first key tile (its key tiles are kb .. kb + nb - 1)
+  int kb;  // local window: the item's step n takes key tile kb + n (kWinSinks: from step ns on)
   int s0k, lk, off;  // cross-attention: the keys' first row and count, the causal offset lk - l
+  int ns;  // sinks: the first ns steps take the segment's key tiles 0 .. ns - 1
 };
 static_assert(sizeof(Item) <= 64, "queue slots are 64 bytes");
 
-template <bool WIN, bool X>
+template <int WIN, bool X>
 __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
   const TileItem it = p.items[idx];
   Item r;
@@ -87,6 +88,10 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
   r.t1 = r.m * kTcBM + 128 < r.l ? 1 : 0;
   r.nb0 = (p.causal && r.t1) ? r.nb - 1 : r.nb;
   if (WIN) r.kb = max(0, r.m * kTcBM - p.window) / kTcBN;
+  if (WIN == kWinSinks) {  // the sink tiles that the window does not reach come first
+    r.ns = min(r.kb, (min(r.l, p.sinks) + kTcBN - 1) / kTcBN);
+    r.kb -= r.ns;
+  }
   if (X) {  // keys from cu_k; q tile 0 may share its diagonal key tile with tile 1
     r.s0k = p.cu_k[it.seg];
     r.lk = p.cu_k[it.seg + 1] - r.s0k;
@@ -96,12 +101,19 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
   return r;
 }
 
-// Masks columns j < lo and j > lim, and returns the row max x sl2 (local window: the left
-// edge of the row's window and its diagonal).
-__device__ __forceinline__ float row_max2(uint32_t* v, int lo, int lim, float sl2) {
+// The key tile of an item's step n.
+template <int WIN>
+__device__ __forceinline__ int key_tile(const Item& I, int n) {
+  return WIN == kWinSinks ? (n < I.ns ? n : I.kb + n) : (WIN ? I.kb + n : n);
+}
+
+// Masks columns j < lo (but not the sinks j < sk) and j > lim, and returns the row max x sl2
+// (local window: the left edge of the row's window and its diagonal).
+template <bool SINKS>
+__device__ __forceinline__ float row_max2(uint32_t* v, int sk, int lo, int lim, float sl2) {
 #pragma unroll
   for (int j = 0; j < 128; ++j)
-    if (j < lo || j > lim) v[j] = __float_as_uint(-INFINITY);
+    if ((j < lo && (!SINKS || j >= sk)) || j > lim) v[j] = __float_as_uint(-INFINITY);
   float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -168,10 +180,13 @@ __device__ __forceinline__ float row_exp(uint32_t* v, float sl2, float mu) {
 // the window of its first row, and tiles that cross a row's window edge are masked on both
 // sides; a row may see nothing in its first tiles (its running max stays -inf and the first
 // visible tile takes over with a zero-weight rescale).
+// kWinSinks: as the window, and the segment's first p.sinks keys are visible to every later
+// query: the key tiles that hold them and that the window does not reach come before the
+// window's tiles, and a column is masked on the left only when it is no sink.
 // X: cross-attention (p.cu_k): keys from their own boundaries, the causal bound aligned
 // bottom-right (key j visible to query i when j <= i + lk - lq), so the masked key tiles are
 // the one or two that cross a q tile's diagonal band.
-template <int D, bool WIN, bool X>
+template <int D, int WIN, bool X>
 __global__ void __launch_bounds__(kTcThreads, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const FwdParams p) {
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_expect_tx_w(bar(C::B_KVF + s), C::TILE);
             for (int pn = 0; pn < D / 64; ++pn)
               tma_load_3d_w(base + C::KV_OFF + s * C::TILE + pn * C::PANEL, kv ? &tv : &tk,
-                          bar(C::B_KVF + s), pn * 64, I.hk, (X ? I.s0k : I.s0) + (WIN ? I.kb + n : n) * kTcBN);
+                          bar(C::B_KVF + s), pn * 64, I.hk, (X ? I.s0k : I.s0) + key_tile<WIN>(I, n) * kTcBN);
             ++kv_it;
           }
         }
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The causal mask touches only the last key tile of each q tile (its diagonal
         // tile); non-causal masks only key columns past the segment end.
         bool need_mask = p.causal ? (n == nbt - 1) : (n * kTcBN + kTcBN > I.l);
-        int lim = p.causal ? qrow - (WIN ? I.kb + n : n) * kTcBN : I.l - 1 - n * kTcBN;  // mask j > lim
+        int lim = p.causal ? qrow - key_tile<WIN>(I, n) * kTcBN : I.l - 1 - n * kTcBN;  // mask j > lim
         if constexpr (X) {  // bottom-right alignment: the diagonal band may span two key tiles
           need_mask = p.causal ? (n * kTcBN + kTcBN - 1 > I.m * kTcBM + t * 128 + I.off) : (n * kTcBN + kTcBN > I.lk);
           lim = p.causal ? qrow + I.off - n * kTcBN : I.lk - 1 - n * kTcBN;
@@ -441,10 +456,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t v[128];
         row_load(s_addr, v);
         float mt;
-        if constexpr (WIN) {  // keys before qrow - w are outside the window
-          const int ka = (I.kb + n) * kTcBN;
-          const bool need_w = ka < I.m * kTcBM + t * 128 + 127 - p.window;
-          mt = (need_mask || need_w) ? row_max2(v, qrow - p.window - ka, lim, sl2) : row_max<false>(v, lim, sl2);
+        if constexpr (WIN != kWinNone) {  // keys before qrow - w are outside the window, unless sinks
+          constexpr bool SINKS = WIN == kWinSinks;
+          const int ka = key_tile<WIN>(I, n) * kTcBN;
+          const bool need_w =
+              ka < I.m * kTcBM + t * 128 + 127 - p.window && (!SINKS || ka + kTcBN > p.sinks);
+          mt = (need_mask || need_w) ? row_max2<SINKS>(v, p.sinks - ka, qrow - p.window - ka, lim, sl2)
+                                     : row_max<false>(v, lim, sl2);
         } else {
           mt = need_mask ? row_max<true>(v, lim, sl2) : row_max<false>(v, lim, sl2);
         }
@@ -524,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-template <int D, bool WIN, bool X>
+template <int D, int WIN, bool X>
 static cudaError_t launch_d(const FwdParams& p, int cap, cudaStream_t st) {
   using C = TcCfg<D>;
   CUtensorMap tq, tk, tv;
@@ -548,9 +566,13 @@ static cudaError_t launch_d(const FwdParams& p, int cap, cudaStream_t st) {
 }
 
 cudaError_t launch_fwd_tc(const FwdParams& p, int d, int cap, cudaStream_t st) {
-  if (p.cu_k) return d == 64 ? launch_d<64, false, true>(p, cap, st) : launch_d<128, false, true>(p, cap, st);
-  if (p.window >= 0) return d == 64 ? launch_d<64, true, false>(p, cap, st) : launch_d<128, true, false>(p, cap, st);
-  return d == 64 ? launch_d<64, false, false>(p, cap, st) : launch_d<128, false, false>(p, cap, st);
+  if (p.cu_k)
+    return d == 64 ? launch_d<64, kWinNone, true>(p, cap, st) : launch_d<128, kWinNone, true>(p, cap, st);
+  if (p.window >= 0 && p.sinks > 0)
+    return d == 64 ? launch_d<64, kWinSinks, false>(p, cap, st) : launch_d<128, kWinSinks, false>(p, cap, st);
+  if (p.window >= 0)
+    return d == 64 ? launch_d<64, kWinLocal, false>(p, cap, st) : launch_d<128, kWinLocal, false>(p, cap, st);
+  return d == 64 ? launch_d<64, kWinNone, false>(p, cap, st) : launch_d<128, kWinNone, false>(p, cap, st);
 }
 
 void fwd_tc_tiles(int* BM, int* BN) {

@@ -58,7 +58,9 @@ __device__ __forceinline__ bool token_mode(const PlanArgs& a) { return a.causal 
 // WIN: causal local window a.window (query i sees keys i-w..i): a q block m's key blocks
 // start at floor(max(0, m*BM - w) / BN); a kv block n's q blocks stop after
 // floor((n*BN + BN - 1 + w) / BM) ("Packing与 FlashAttention Varlen", section 5: the local
-// window narrows n_block_min/max).
+// window narrows n_block_min/max).  a.sinks > 0: the segment's first a.sinks keys stay visible
+// to every later query, so a q block also lists the key blocks that hold them and that its
+// window does not reach, and a kv block that holds one lists its q blocks to the segment's end.
 // X: cross-attention (a.cu_k): a segment has lq queries and lk keys, the causal bound is
 // aligned bottom-right (key j visible to query i when j <= i + lk - lq): q block m has
 // ceil(min(lk, (m+1)*BM + lk - lq) / BN) key blocks, kv block n its q blocks from
@@ -80,9 +82,11 @@ template <class M>
 __device__ __forceinline__ int win_count(const PlanArgs& a, int l, int blk) {
   if (!M::kv) {
     const int nmax = ceil_p2(min(l, (blk + 1) * a.BM), a.BN);
-    return nmax - div_p2(max(0, blk * a.BM - a.window), a.BN);
+    const int k0 = div_p2(max(0, blk * a.BM - a.window), a.BN);
+    return nmax - k0 + min(k0, ceil_p2(min(l, a.sinks), a.BN));
   }
   const int Mq = ceil_p2(l, a.BM);
+  if (blk * a.BN < a.sinks) return Mq - div_p2(blk * a.BN, a.BM);
   return min(Mq, div_p2(blk * a.BN + a.BN - 1 + a.window, a.BM) + 1) - div_p2(blk * a.BN, a.BM);
 }
 

@@ -1,0 +1,211 @@
+"""GPU parity of the local window with sinks (query i sees the keys j <= i with j >= i - w or
+j < s of its segment) against the float64 oracle: tile maps bit-exact, O / LSE / dQ / dK / dV
+within the attention tolerances, closed forms, strides, streams, graphs and refusals."""
+import numpy as np
+import pytest
+import torch
+
+import seeded_inputs as si
+from oracle import attention as oa
+from oracle import packing as op
+from oracle import tiles as ot
+import _workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+EDGE = [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 1, 383, 384, 385, 700]
+
+
+@pytest.fixture(scope="module")
+def va():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from packed_sequence_varlen_gb300 import build as b
+    b.build()
+    import packed_sequence_varlen_gb300 as pkg
+    pkg._lib.load()
+    return pkg
+
+
+def boundaries(lengths):
+    cu, _, _, mx = op.build_metadata(lengths)
+    return cu, torch.tensor(cu, dtype=torch.int32, device=DEV), mx
+
+
+@pytest.mark.parametrize("w,s", [(0, 1), (1, 4), (63, 64), (128, 127), (200, 129), (512, 4), (100, 600), (5000, 4),
+                                 (64, 5000)])
+def test_sink_maps_bit_exact(va, w, s):
+    for lengths, Hq, Hkv, d in ((EDGE, 4, 2, 128), (wl.pack("sft8k", 0), 32, 32, 128),
+                                (wl.pack("tiny4k")[:300], 8, 8, 64), (wl.pack("long64k"), 16, 16, 128)):
+        cu, cud, mx = boundaries(lengths)
+        for kind in (0, 1, 2):
+            BM, BN = va.tile_sizes(kind, d)
+            ref = (ot.bwd_tile_map(cu, Hkv, BM, BN, True, 0, window=w, sinks=s) if kind == 1 else
+                   ot.fwd_tile_map(cu, Hq, BM, BN, True, 0, window=w, sinks=s))
+            tm, n = va.plan(cud, int(cu[-1]), Hq, Hkv, d, mx, kind, True, window=w, sinks=s)
+            assert n == len(ref)
+            assert np.array_equal(tm.cpu().numpy(), ref)
+
+
+def run_both(va, q, k, v, do, cud, mx, w, s, ws=(None, None)):
+    qd, kd, vd, dod = (x.to(DEV) for x in (q, k, v, do))
+    o, lse = va.varlen_attn_fwd(qd, kd, vd, cud, mx, None, True, check_status=True, window=w, sinks=s, workspace=ws[0])
+    g = va.varlen_attn_bwd(qd, kd, vd, o, lse, dod, cud, mx, None, True, check_status=True, window=w, sinks=s,
+                           workspace=ws[1])
+    torch.cuda.synchronize()
+    return o.cpu().double().numpy(), lse.cpu().double().numpy(), tuple(x.cpu().double().numpy() for x in g)
+
+
+def against_oracle(got, q, k, v, do, cu, w, s, kv_heads=None, chunked=True):
+    qq, kk, vv, dd = (si.to_f64(x) for x in (q, k, v, do))
+    ro, rl = oa.varlen_forward(qq, kk, vv, cu, window=w, sinks=s, kv_heads=kv_heads)
+    rg = oa.varlen_backward(qq, kk, vv, ro, rl, dd, cu, window=w, sinks=s, kv_heads=kv_heads)
+    o, lse, gr = got
+    wl.assert_close_outputs(o, lse, ro, rl)
+    wl.assert_close_grads(gr, rg)
+    if chunked:
+        wl.assert_close_grads_chunked(gr, rg)
+
+
+# w = 0 leaves a query itself and the sinks; sinks inside one tile, at its edges, across several
+@pytest.mark.parametrize("w,s", [(0, 1), (0, 130), (1, 4), (63, 64), (100, 7), (128, 127), (200, 129), (300, 300)])
+@pytest.mark.parametrize("d,g", [(64, 1), (128, 2)])
+def test_sink_parity_ragged(va, w, s, d, g):
+    cu, cud, mx = boundaries(EDGE)
+    T, Hkv = int(cu[-1]), 2
+    q, k, v, do = si.tensors(T, Hkv * g, Hkv, d, seed_offset=700 + w + d + g + s)
+    against_oracle(run_both(va, q, k, v, do, cud, mx, w, s), q, k, v, do, cu, w, s)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(12, 1, 128), (8, 8, 64)])
+def test_sink_parity_one_long_segment(va, Hq, Hkv, d):
+    """A segment whose sink block is seen by many more queries than any other key block."""
+    cu, cud, mx = boundaries([9001])
+    q, k, v, do = si.tensors(9001, Hq, Hkv, d, seed_offset=60 + Hq)
+    got = run_both(va, q, k, v, do, cud, mx, 130, 5)
+    # dK of the sink rows is a sum over 9000 queries: compared by itself too
+    qq, kk, vv, dd = (si.to_f64(x) for x in (q, k, v, do))
+    heads = None if Hkv == 1 else [2, 7]
+    ro, rl = oa.varlen_forward(qq, kk, vv, cu, window=130, sinks=5, kv_heads=heads)
+    rg = oa.varlen_backward(qq, kk, vv, ro, rl, dd, cu, window=130, sinks=5, kv_heads=heads)
+    wl.assert_close_outputs(got[0], got[1], ro, rl)
+    wl.assert_close_grads(got[2], rg)
+    hs = [0] if Hkv == 1 else heads
+    for i in (1, 2):
+        assert wl.rel_l2(got[2][i][:5, hs], rg[i][:5, hs]) <= wl.GRAD_REL_L2
+
+
+def test_sinks_degenerate_forms(va):
+    """sinks = 0 and a window or sink count over the whole segment give the results of the
+    window and of the plain causal call on the same inputs."""
+    cu, cud, mx = boundaries(EDGE)
+    q, k, v, do = si.tensors(int(cu[-1]), 4, 2, 128, seed_offset=11)
+    for (w, s), (w2, s2) in (((77, 0), (77, 0)), ((5000, 3), (5000, 0)), ((10, 5000), (5000, 0)),
+                             ((2 ** 31 - 1, 2 ** 31 - 1), (5000, 0))):
+        a, b = run_both(va, q, k, v, do, cud, mx, w, s), run_both(va, q, k, v, do, cud, mx, w2, s2)
+        if (w, s) == (w2, s2):
+            assert np.array_equal(a[0], b[0])
+        assert np.abs(a[0] - b[0]).max() <= wl.O_MAX_ABS and np.abs(a[1] - b[1]).max() <= wl.LSE_MAX_ABS
+        for x, y in zip(a[2], b[2]):
+            assert wl.rel_l2(x, y) <= wl.GRAD_REL_L2
+
+
+def test_sinks_only_the_sinks_carry_weight(va):
+    """Large positive scores on the sinks: O is their mean value for every later query."""
+    cu, cud, mx = boundaries([1000])
+    T, s = 1000, 4
+    q, k, v = torch.zeros(T, 1, 64), torch.zeros(T, 1, 64), torch.randn(T, 1, 64, generator=torch.Generator().manual_seed(3))
+    q[..., 0] = 32.0
+    k[:s, :, 0] = 32.0                                   # scores 128 against 0
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    o, lse = va.varlen_attn_fwd(q.to(DEV), k.to(DEV), v.to(DEV), cud, mx, window=50, sinks=s, check_status=True)
+    ref = v[:s].double().mean(0).numpy()
+    o = o.cpu().double().numpy()
+    assert np.abs(o[s:] - ref).max() <= wl.O_MAX_ABS
+    assert np.abs(lse.cpu().double().numpy()[:, s:] - (128 + np.log(4))).max() <= wl.LSE_MAX_ABS
+
+
+def test_sink_workload_packs(va):
+    """An sft8k pack and a gqa16k bin, all heads on the GPU, some against the oracle."""
+    for name, idx, w, s, heads in (("sft8k", 1, 511, 4, [3, 20]), ("gqa16k", 0, 1023, 66, [5])):
+        w_ = si.WORKLOADS[name]
+        cu, cud, mx = boundaries(wl.pack(name, idx))
+        q, k, v, do = si.tensors(int(cu[-1]), w_.Hq, w_.Hkv, w_.d, seed_offset=911)
+        against_oracle(run_both(va, q, k, v, do, cud, mx, w, s), q, k, v, do, cu, w, s, heads, chunked=False)
+
+
+def test_sinks_strided_side_stream_and_graph(va):
+    """Views into one fused projection, on a side stream, captured and replayed on new inputs:
+    bit-equal to contiguous eager calls; a workspace left dirty by another call does not matter."""
+    cu, cud, mx = boundaries([300, 17, 640, 1])
+    T, Hq, Hkv, d = int(cu[-1]), 4, 2, 128
+    q, k, v, do = (x.to(DEV) for x in si.tensors(T, Hq, Hkv, d, seed_offset=21))
+    fused = torch.empty(T, Hq + 2 * Hkv, d, dtype=torch.bfloat16, device=DEV)
+    fq, fk, fv = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    dof = torch.empty(T, Hq, d, dtype=torch.bfloat16, device=DEV)
+    o = torch.empty(T, Hq, d, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(Hq, T, device=DEV)
+    kw = dict(window=70, sinks=9)
+    n = max(va.workspace_size(T, 4, Hq, Hkv, d, mx, b, **kw) for b in (False, True))
+    ws = torch.full((n,), 0x7f, dtype=torch.uint8, device=DEV)
+
+    def step():
+        va.varlen_attn_fwd(fq, fk, fv, cud, mx, out=o, lse=lse, workspace=ws, **kw)
+        return va.varlen_attn_bwd(fq, fk, fv, o, lse, dof, cud, mx, workspace=ws, **kw)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()
+        graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        got = step()
+    for off in (0, 5):
+        q, k, v, do = (x.to(DEV) for x in si.tensors(T, Hq, Hkv, d, seed_offset=21 + off))
+        fq.copy_(q), fk.copy_(k), fv.copy_(v), dof.copy_(do)
+        graph.replay()
+        torch.cuda.synchronize()
+        o2, lse2 = va.varlen_attn_fwd(q, k, v, cud, mx, **kw)
+        ref = va.varlen_attn_bwd(q, k, v, o2, lse2, do, cud, mx, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert va.read_status(ws) == 0
+
+
+def test_sinks_autograd_differences_and_refusals(va):
+    """Autograd through varlen_attn: against the oracle's gradient, and the directional
+    derivative of the float64 oracle forward (central differences)."""
+    cu, cud, mx = boundaries([70, 5, 200])
+    T = int(cu[-1])
+    q, k, v, do = si.tensors(T, 2, 2, 64, seed_offset=5)
+    qd, kd, vd = (x.to(DEV).requires_grad_(True) for x in (q, k, v))
+    out = va.varlen_attn(qd, kd, vd, cud, mx, window=33, sinks=3)
+    out.backward(do.to(DEV))
+    got = tuple(x.grad.cpu().double().numpy() for x in (qd, kd, vd))
+    qq, kk, vv, dd = (si.to_f64(x) for x in (q, k, v, do))
+    ro, rl = oa.varlen_forward(qq, kk, vv, cu, window=33, sinks=3)
+    wl.assert_close_grads(got, oa.varlen_backward(qq, kk, vv, ro, rl, dd, cu, window=33, sinks=3))
+    rng = np.random.default_rng(0)
+    base = [qq, kk, vv]
+    for a in range(3):
+        u = rng.standard_normal(base[a].shape)
+        f = [0.0, 0.0]
+        for sgn in (0, 1):
+            x = list(base)
+            x[a] = base[a] + (1e-4 if sgn else -1e-4) * u
+            f[sgn] = float((oa.varlen_forward(*x, cu, window=33, sinks=3)[0] * dd).sum())
+        # the kernel's gradient has a relative L2 error of at most 1e-2, so along u its error is at
+        # most that times |grad| |u|
+        assert abs((f[1] - f[0]) / 2e-4 - (got[a] * u).sum()) <= \
+            wl.GRAD_REL_L2 * np.linalg.norm(got[a]) * np.linalg.norm(u)
+    q, k, v = (x.detach() for x in (qd, kd, vd))
+    for kw in (dict(sinks=3), dict(window=3, sinks=-1), dict(window=3, sinks=2, causal=False)):
+        with pytest.raises(va.VarlenError) as e:
+            va.varlen_attn_fwd(q, k, v, cud, mx, **kw)
+        assert e.value.status == 1
+    bad = torch.tensor([0, 70, 70, 275], dtype=torch.int32, device=DEV)     # an empty segment
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    va.varlen_attn_fwd(q, k, v, bad, mx, window=3, sinks=2, workspace=ws)
+    assert va.read_status(ws) == 5

@@ -453,6 +453,43 @@ va_status varlen_token_ce(const void* logits_dev, int32_t dtype, int64_t logits_
                           double* loss_dev, int32_t* count_dev, void* grad_dev, int64_t grad_row_stride,
                           void* ws_dev, size_t ws_bytes, va_stream_t stream);
 
+/* Bytes of workspace varlen_token_distill needs for T rows (status word at byte 0). */
+size_t varlen_token_distill_workspace_size(int32_t T);
+
+/* Distillation of the packed stream from a teacher's top logits, and its logit gradient.  The
+ * pages have no counterpart; the objective is weighted as varlen_token_ce's (every eligible row
+ * has equal weight, the sum divided once by their count N).  Row t has K entries (id, teacher
+ * logit a); with the temperature tau, p = softmax(a / tau) over the row's present entries and
+ * q = softmax(z / tau) over all V classes,
+ *     L_t = tau^2 sum_k p_k (ln p_k - ln q_{id_k}),
+ *     d(mean)/d(z_tc) = tau (q_c - sum_{k : id_k = c} p_k) / N.
+ * Log-probabilities serve as a as well (p is normalised over the entries).  An entry is absent
+ * when its id is negative or its logit is -inf or NaN; a class may be listed more than once (its
+ * weights add up).  A row is eligible when its target is not ignore_index (targets NULL: always)
+ * and it has a present entry; other rows are skipped before any arithmetic (logits never read,
+ * gradient row zero).  The value of a target is not used.
+ *   logits_dev          [T, V], row stride logits_row_stride elements; dtype 0 = fp32, 1 = bf16
+ *   teacher_ids_dev     int32 [T, K] (row stride teacher_ids_row_stride)
+ *   teacher_logits_dev  [T, K] (row stride teacher_logits_row_stride); teacher_dtype 0 = fp32, 1 = bf16
+ *   targets_dev         int32 [T], or NULL
+ *   loss_dev            float [2] out: {sum, sum / N}; NaN on a device-detected error
+ *   count_dev           int32 [1] out: N
+ *   grad_dev            [T, V] out (row stride grad_row_stride), the dtype of the logits, or NULL
+ *   ws_dev / ws_bytes   workspace (>= varlen_token_distill_workspace_size(T), 16-byte aligned)
+ * Rows need no alignment beyond their type's.  grad may be the logits themselves (same strides).
+ * Arithmetic in fp32 per row, the sum over rows in fp64 in a fixed order (deterministic), rounded
+ * once.  Limits: K <= 1024, a row of logits within 1,638,400 bytes (VA_ERR_UNSUPPORTED beyond).
+ * Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED, VA_ERR_WORKSPACE, VA_ERR_CUDA; the status word
+ * gets VA_ERR_BAD_TARGETS when an eligible row lists a class >= V or no row is eligible (then
+ * loss is NaN and no gradient is written).  Asynchronous. */
+va_status varlen_token_distill(const void* logits_dev, int32_t dtype, int64_t logits_row_stride,
+                               const int32_t* teacher_ids_dev, int64_t teacher_ids_row_stride,
+                               const void* teacher_logits_dev, int32_t teacher_dtype,
+                               int64_t teacher_logits_row_stride, const int32_t* targets_dev, int32_t T,
+                               int32_t V, int32_t K, int32_t ignore_index, float temperature,
+                               float* loss_dev, int32_t* count_dev, void* grad_dev, int64_t grad_row_stride,
+                               void* ws_dev, size_t ws_bytes, va_stream_t stream);
+
 /* ---------------------------------------------------------------- tracing
  * Per-launch timing.  With capacity > 0, the library records a CUDA event pair
  * on the launching stream around each of the next `capacity` kernel launches

@@ -68,3 +68,36 @@ def token_weighted_loss(logits, targets, eligible):
     grad = np.zeros_like(logits)
     grad[idx] = (p - onehot) / N
     return loss_sum, loss_sum / N, grad
+
+
+def top_logit_distillation(logits, ids, teacher_logits, has_target, temperature: float = 1.0):
+    """(loss_sum, mean, N, grad) of the distillation from a teacher's top logits, float64.
+
+    Row t: p = softmax(a / tau) over its present entries (id >= 0, a > -inf), q = softmax(z / tau)
+    over all classes, loss tau^2 sum_k p_k (ln p_k - ln q_{id_k}).  Rows with a target and an entry
+    are eligible; the mean divides by their count N, ``grad`` is d(mean)/d(logits).
+    """
+    z = np.asarray(logits, dtype=np.float64)
+    ids = np.asarray(ids, dtype=np.int64)
+    a = np.asarray(teacher_logits, dtype=np.float64)
+    has_target = np.asarray(has_target, dtype=bool)
+    grad = np.zeros_like(z)
+    rows, total = [], 0.0
+    for t in range(z.shape[0]):
+        keep = (ids[t] >= 0) & (a[t] > -np.inf)
+        if not has_target[t] or not keep.any():
+            continue
+        rows.append(t)
+        x = a[t][keep] / temperature
+        e = np.exp(x - x.max())
+        p = e / e.sum()
+        y = z[t] / temperature
+        lse = y.max() + np.log(np.exp(y - y.max()).sum())
+        for c, w in zip(ids[t][keep], p):
+            grad[t, c] -= w
+            if w > 0:
+                total += temperature ** 2 * w * (np.log(w) - (y[c] - lse))
+        grad[t] = temperature * (np.exp(y - lse) + grad[t])
+    if not rows:
+        raise ValueError("no eligible rows: the mean has no denominator")
+    return total, total / len(rows), len(rows), grad / len(rows)

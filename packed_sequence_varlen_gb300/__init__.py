@@ -24,7 +24,7 @@ __all__ = [
     "tile_sizes", "workspace_size", "plan", "varlen_attn_fwd", "varlen_attn_bwd", "varlen_attn",
     "read_status", "VarlenError", "make_shape", "library_path", "loss_targets", "token_ce",
     "IGNORE_INDEX", "unpad_index", "gather_rows", "unpad", "pad", "plan_cross", "varlen_attn_fwd_cross",
-    "varlen_attn_bwd_cross",
+    "varlen_attn_bwd_cross", "token_distill",
 ]
 
 
@@ -402,6 +402,72 @@ def token_ce(logits: torch.Tensor, targets: torch.Tensor, ignore_index: int = IG
                               _ptr(targets), T, V, int(ignore_index), _ptr(loss), _ptr(count), _ptr(g),
                               g.stride(0) if g is not None else 0, _ptr(workspace), workspace.numel(),
                               _stream(dev)))
+    if check_status:
+        _raise_status(workspace)
+    return loss, count, g
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows of a 2-D tensor (one row: any stride is right)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                  targets: torch.Tensor | None = None, temperature: float = 1.0,
+                  ignore_index: int = IGNORE_INDEX, grad: bool | torch.Tensor = True, workspace=None,
+                  check_status=False):
+    """Distillation from a teacher's top logits over the packed stream: returns (loss [2] fp32
+    device tensor {sum, mean}, count [1] int32, grad or None).
+
+    ``logits`` CUDA fp32 or bf16 [T, V]; ``teacher_ids`` int32 [T, K] (negative: no entry) and
+    ``teacher_logits`` fp32 or bf16 [T, K]; ``targets`` int32 [T] whose ``ignore_index`` rows are
+    skipped (None: no row is).  Row t adds temperature^2 KL(p || q), p the softmax of its teacher
+    logits / temperature, q the softmax of all its logits / temperature; the mean is over the rows
+    that have a target and an entry.  ``grad`` True allocates d(mean)/d(logits) like ``logits``, a
+    tensor receives it (``logits`` itself is fine), False skips it."""
+    if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1 or \
+            logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")
+    T, V = logits.shape
+    dev = logits.device
+    if teacher_ids.dim() != 2 or teacher_ids.dtype != torch.int32 or teacher_ids.shape[0] != T or \
+            (teacher_ids.shape[1] > 1 and teacher_ids.stride(1) != 1):
+        raise ValueError("teacher_ids must be an int32 [T, K] tensor with a contiguous last dim")
+    if teacher_logits.shape != teacher_ids.shape or teacher_logits.dtype not in (torch.float32, torch.bfloat16) or \
+            (teacher_logits.shape[1] > 1 and teacher_logits.stride(1) != 1):
+        raise ValueError("teacher_logits must be fp32/bf16 in teacher_ids' shape, with a contiguous last dim")
+    if targets is not None and (targets.dtype != torch.int32 or targets.shape != (T,) or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous int32 [T] tensor")
+    if grad is True:
+        g = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    elif grad is False or grad is None:
+        g = None
+    else:
+        g = grad
+        if g.shape != logits.shape or g.dtype != logits.dtype or g.stride(1) != 1:
+            raise ValueError("grad must match logits in shape and dtype, with a contiguous last dim")
+    _same_device(dev, teacher_ids=teacher_ids, teacher_logits=teacher_logits, targets=targets, grad=g,
+                 workspace=workspace)
+    lib = _lib.load()
+    need = lib.varlen_token_distill_workspace_size(T)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    loss = torch.empty(2, dtype=torch.float32, device=dev)
+    count = torch.empty(1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        check(lib.varlen_token_distill(_ptr(logits), int(logits.dtype == torch.bfloat16), _row_stride(logits),
+                                       _ptr(teacher_ids), _row_stride(teacher_ids), _ptr(teacher_logits),
+                                       int(teacher_logits.dtype == torch.bfloat16), _row_stride(teacher_logits),
+                                       _ptr(targets), T, V, teacher_ids.shape[1], int(ignore_index),
+                                       float(temperature), _ptr(loss), _ptr(count), _ptr(g),
+                                       _row_stride(g) if g is not None else 0, _ptr(workspace), workspace.numel(),
+                                       _stream(dev)))
     if check_status:
         _raise_status(workspace)
     return loss, count, g

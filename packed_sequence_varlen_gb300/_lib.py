@@ -32,6 +32,7 @@ EXPORTS = (
     "varlen_attn_workspace_size_cross", "varlen_attn_plan_cross", "varlen_attn_fwd_cross",
     "varlen_attn_bwd_cross", "varlen_test_stall_next_forward",
     "varlen_attn_workspace_size_sinks", "varlen_attn_plan_sinks", "varlen_attn_fwd_sinks", "varlen_attn_bwd_sinks",
+    "varlen_token_distill_workspace_size", "varlen_token_distill",
 )
 
 
@@ -117,6 +118,11 @@ def _declare(lib):
         "varlen_token_ce": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32,
                                       c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
                                       c_void_p]),
+        "varlen_token_distill_workspace_size": (c_size_t, [c_int32]),
+        "varlen_token_distill": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int64, c_void_p, c_int32,
+                                           c_int64, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
+                                           c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
+                                           c_void_p]),
         "varlen_read_status": (c_int32, [c_void_p, i32p, c_void_p]),
         "varlen_clear_status": (c_int32, [c_void_p, c_void_p]),
         "varlen_profile_enable": (c_int32, [c_int32]),

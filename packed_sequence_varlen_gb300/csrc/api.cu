@@ -32,6 +32,11 @@ cudaError_t launch_gather_rows(const void*, int64_t, const int32_t*, int, int64_
 cudaError_t launch_loss_targets(const int32_t*, const int32_t*, int, int, int, int32_t*, cudaStream_t);
 cudaError_t launch_token_ce(int, const void*, int, int64_t, const int32_t*, int, int, int, void*, int64_t, float*,
                             int32_t*, int32_t*, double*, cudaStream_t);
+bool distill_row_fits(int, int);
+size_t distill_parts_bytes();
+cudaError_t launch_token_distill(int, const void*, int, int64_t, const int32_t*, int64_t, const void*, int, int64_t,
+                                 const int32_t*, int, int, int, int, float, void*, int64_t, void*, int32_t*, uint8_t*,
+                                 float*, float*, int32_t*, cudaStream_t);
 cudaError_t launch_bwd_dkdv_tc(const BwdParams&, int, int, bool, cudaStream_t);
 cudaError_t launch_bwd_dq_tc(const BwdParams&, int, int, bool, cudaStream_t);
 void bwd_tc_tiles(int*, int*, int*, int*);
@@ -46,13 +51,14 @@ void set_error(const char* msg) { g_error = msg; }
 enum KernelId {
   K_VALIDATE = 0, K_META_SCAN, K_META_FILL, K_PLAN, K_FWD, K_BWD_PREP, K_BWD_DKDV, K_BWD_DQ,
   K_VALIDATE_PLAN, K_FWD_TOK, K_CU_FROM_POS, K_LOSS_TARGETS, K_CE_COUNT, K_CE_ROWS, K_CE_REDUCE, K_PAD_COUNT,
-  K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_COUNT
+  K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "validate_cu_seqlens", "metadata_scan", "metadata_fill", "plan",          "fwd",
     "bwd_prep",            "bwd_dkdv",      "bwd_dq",        "validate_plan", "fwd_tok",
     "cu_from_positions",   "loss_targets",  "ce_count",      "ce_rows",       "ce_reduce",
-    "pad_count",           "pad_scan",      "pad_index",     "gather_rows"};
+    "pad_count",           "pad_scan",      "pad_index",     "gather_rows", "distill_count", "distill_rows",
+    "distill_reduce"};
 
 struct Profiler {
   std::vector<cudaEvent_t> start, stop;
@@ -661,6 +667,48 @@ va_status varlen_token_ce(const void* logits, int32_t dtype, int64_t l_rs, const
                              &hdr->status, loss, cs);
     });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_ce");
+}
+
+size_t varlen_token_distill_workspace_size(int32_t T) {
+  if (T < 0) return 0;
+  return align256(sizeof(WsHeader) + distill_parts_bytes() + static_cast<size_t>(T) * sizeof(float)) +
+         align256(static_cast<size_t>(T));
+}
+
+va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, const int32_t* ids, int64_t ids_rs,
+                               const void* tl, int32_t t_dtype, int64_t t_rs, const int32_t* targets, int32_t T,
+                               int32_t V, int32_t K, int32_t ignore_index, float temperature, float* loss,
+                               int32_t* count, void* grad, int64_t g_rs, void* ws, size_t ws_bytes,
+                               va_stream_t stream) {
+  if (!logits || !ids || !tl || !loss || !count || !ws) return fail(VA_ERR_INVALID_ARG, "token_distill: null pointer");
+  if (T < 1 || V < 1 || K < 1 || (dtype != 0 && dtype != 1) || (t_dtype != 0 && t_dtype != 1))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: T, V, K >= 1, dtypes 0 or 1");
+  if (K > 1024) return fail(VA_ERR_UNSUPPORTED, "token_distill: at most 1024 teacher entries per row");
+  if (!distill_row_fits(V, dtype == 1 ? 2 : 4))
+    return fail(VA_ERR_UNSUPPORTED, "token_distill: a row of logits must stay within 1,638,400 bytes");
+  if (l_rs < V || ids_rs < K || t_rs < K || (grad && g_rs < V))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: row strides must be >= the row");
+  const uintptr_t ea = dtype == 1 ? 1 : 3;
+  if ((reinterpret_cast<uintptr_t>(logits) & ea) || (reinterpret_cast<uintptr_t>(grad) & ea))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: logits and grad must be aligned to their type");
+  if (!(temperature > 0.f) || !(temperature < INFINITY))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: temperature must be finite and > 0");
+  if (!aligned16(ws)) return fail(VA_ERR_INVALID_ARG, "token_distill: workspace must be 16-byte aligned");
+  if (ws_bytes < varlen_token_distill_workspace_size(T))
+    return fail(VA_ERR_WORKSPACE, "token_distill: workspace too small");
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  int32_t* parts = reinterpret_cast<int32_t*>(w + sizeof(WsHeader));
+  float* kl = reinterpret_cast<float*>(w + sizeof(WsHeader) + distill_parts_bytes());
+  uint8_t* flags = reinterpret_cast<uint8_t*>(kl + T);
+  cudaError_t e = cudaSuccess;
+  const KernelId kid[3] = {K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE};
+  for (int stage = 0; stage < 3 && e == cudaSuccess; ++stage)
+    e = launch(kid[stage], cs, [&] {
+      return launch_token_distill(stage, logits, dtype, l_rs, ids, ids_rs, tl, t_dtype, t_rs, targets, T, V, K,
+                                  ignore_index, temperature, grad, g_rs, w, parts, flags, kl, loss, count, cs);
+    });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_distill");
 }
 
 va_status varlen_read_status(const void* ws, int32_t* out, va_stream_t stream) {

@@ -52,7 +52,8 @@ typedef enum {
   VA_ERR_BAD_SEQLENS = 5,  /* cu_seqlens breaks the contract (device-detected or host) */
   VA_ERR_TIMEOUT = 6,      /* a bounded device wait gave up (device-detected) */
   VA_ERR_CAPACITY = 7,     /* planner: a document longer than the pack capacity */
-  VA_ERR_BAD_TARGETS = 8   /* loss: an eligible target outside [0, V), or none eligible (device-detected) */
+  VA_ERR_BAD_TARGETS = 8,  /* loss: an eligible target outside [0, V), or none eligible (device-detected) */
+  VA_ERR_BAD_IDS = 9       /* embedding: a token id >= V (device-detected) */
 } va_status;
 
 /* Shape and strides of one packed call.  Strides are in elements.
@@ -489,6 +490,40 @@ va_status varlen_token_distill(const void* logits_dev, int32_t dtype, int64_t lo
                                int32_t V, int32_t K, int32_t ignore_index, float temperature,
                                float* loss_dev, int32_t* count_dev, void* grad_dev, int64_t grad_row_stride,
                                void* ws_dev, size_t ws_bytes, va_stream_t stream);
+
+/* ---------------------------------------------------------------- embedding
+ * Token embedding of the packed stream, out[t] = scale * table[ids[t]].  The pages start at Q, K
+ * and V and have no counterpart; it is the step before them.  A negative id is a padding token:
+ * a zero row.  An id >= V gives a row of NaN and sets *status_dev to VA_ERR_BAD_IDS (left
+ * untouched otherwise; NULL: not reported); nothing outside the table is read.
+ *   table_dev   [V, D], row stride table_row_stride elements; dtype 0 = fp32, 1 = bf16
+ *   ids_dev     int32 [T]
+ *   out_dev     [T, D] out, row stride out_row_stride, the dtype of the table
+ * The product is formed in fp32 and rounded once.  Rows need no alignment beyond their type's
+ * (16-byte rows are faster).  Errors: VA_ERR_INVALID_ARG (null pointer, T outside [0, 2^30), V or D < 1,
+ * strides below D, alignment, scale not finite), VA_ERR_CUDA.  T = 0 does nothing.  Asynchronous. */
+va_status varlen_embed_fwd(const void* table_dev, int32_t dtype, int64_t table_row_stride,
+                           const int32_t* ids_dev, int32_t T, int32_t V, int32_t D, float scale,
+                           void* out_dev, int64_t out_row_stride, int32_t* status_dev, va_stream_t stream);
+
+/* Bytes of workspace varlen_embed_bwd needs (status word at byte 0). */
+size_t varlen_embed_bwd_workspace_size(int32_t T, int32_t D);
+
+/* The gradient of varlen_embed_fwd with respect to the table,
+ *     dtable[v] = scale * sum_{t : ids[t] = v} dout[t]        (accumulate: added to what is there).
+ * Tokens are sorted by id on the device; every row is a sum in token order in fp32, so the result
+ * does not change from call to call.  Negative ids add nothing; ids >= V add nothing and set
+ * VA_ERR_BAD_IDS in the status word (the other rows are still right).
+ *   dout_dev    [T, D], row stride dout_row_stride; dtype 0 = fp32, 1 = bf16 (NULL when T = 0)
+ *   dtable_dev  [V, D] out, row stride dtable_row_stride; table_dtype 0 = fp32, 1 = bf16.  Without
+ *               accumulate every row is written (zeros where no token has the id); with it only
+ *               the rows of ids that occur are read and written
+ *   ws_dev / ws_bytes  workspace (>= varlen_embed_bwd_workspace_size(T, D), 16-byte aligned)
+ * Errors: VA_ERR_INVALID_ARG, VA_ERR_WORKSPACE, VA_ERR_CUDA.  Asynchronous. */
+va_status varlen_embed_bwd(const void* dout_dev, int32_t dtype, int64_t dout_row_stride,
+                           const int32_t* ids_dev, int32_t T, int32_t V, int32_t D, float scale,
+                           void* dtable_dev, int32_t table_dtype, int64_t dtable_row_stride,
+                           int32_t accumulate, void* ws_dev, size_t ws_bytes, va_stream_t stream);
 
 /* ---------------------------------------------------------------- tracing
  * Per-launch timing.  With capacity > 0, the library records a CUDA event pair

@@ -24,7 +24,7 @@ __all__ = [
     "tile_sizes", "workspace_size", "plan", "varlen_attn_fwd", "varlen_attn_bwd", "varlen_attn",
     "read_status", "VarlenError", "make_shape", "library_path", "loss_targets", "token_ce",
     "IGNORE_INDEX", "unpad_index", "gather_rows", "unpad", "pad", "plan_cross", "varlen_attn_fwd_cross",
-    "varlen_attn_bwd_cross", "token_distill",
+    "varlen_attn_bwd_cross", "token_distill", "embed_fwd", "embed_bwd", "embed",
 ]
 
 
@@ -471,6 +471,102 @@ def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
     if check_status:
         _raise_status(workspace)
     return loss, count, g
+
+
+# ----------------------------------------------------------------- embedding
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _check_rows(name: str, t: torch.Tensor):
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in _FLOATS or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA fp32/bf16 matrix with a contiguous last dim")
+
+
+def _check_ids(ids: torch.Tensor, dev: torch.device):
+    if ids.dim() != 1 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T] tensor")
+    _same_device(dev, ids=ids)
+
+
+def embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+              check_status=False) -> torch.Tensor:
+    """out[t] = scale * table[ids[t]]: ``table`` CUDA fp32/bf16 [V, D], ``ids`` int32 [T] (negative:
+    a zero row; >= V: a row of NaN, an error with ``check_status``); out [T, D] in table's dtype."""
+    _check_rows("table", table)
+    dev = table.device
+    _check_ids(ids, dev)
+    (V, D), T = table.shape, ids.numel()
+    if out is None:
+        out = torch.empty((T, D), dtype=table.dtype, device=dev)
+    else:
+        _check_rows("out", out)
+        if out.shape != (T, D) or out.dtype != table.dtype:
+            raise ValueError("out must be [T, D] in table's dtype")
+        _same_device(dev, out=out)
+    status = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
+    with torch.cuda.device(dev):
+        check(_lib.load().varlen_embed_fwd(_ptr(table), int(table.dtype == torch.bfloat16), _row_stride(table),
+                                           _ptr(ids) if T else ctypes.c_void_p(0), T, V, D, float(scale),
+                                           _ptr(out) if T else _ptr(table), _row_stride(out), _ptr(status),
+                                           _stream(dev)))
+    if check_status and int(status.item()) != 0:
+        raise VarlenError(int(status.item()), "embed_fwd: a token id is past the table")
+    return out
+
+
+def embed_bwd(dout: torch.Tensor, ids: torch.Tensor, num_rows: int, scale: float = 1.0,
+              dtable: torch.Tensor | None = None, accumulate: bool = False, workspace=None,
+              check_status=False) -> torch.Tensor:
+    """Gradient of ``embed_fwd`` with respect to its table: dtable[v] = scale * the sum of dout[t]
+    over ids[t] == v, in token order (deterministic), [num_rows, D].  ``dtable`` None allocates
+    one in dout's dtype; an fp32 or bf16 tensor receives it, and with ``accumulate`` it is added to
+    what the tensor holds (rows whose id does not occur are not touched)."""
+    _check_rows("dout", dout)
+    dev = dout.device
+    _check_ids(ids, dev)
+    T, D, V = ids.numel(), dout.shape[1], int(num_rows)
+    if dout.shape[0] != T:
+        raise ValueError("dout must be [T, D] with ids [T]")
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs the tensor to add to")
+        dtable = torch.empty((V, D), dtype=dout.dtype, device=dev)
+    else:
+        _check_rows("dtable", dtable)
+        if dtable.shape != (V, D):
+            raise ValueError("dtable must be [num_rows, D]")
+    _same_device(dev, dtable=dtable, workspace=workspace)
+    lib = _lib.load()
+    need = lib.varlen_embed_bwd_workspace_size(T, D)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        check(lib.varlen_embed_bwd(_ptr(dout) if T else ctypes.c_void_p(0), int(dout.dtype == torch.bfloat16),
+                                   _row_stride(dout), _ptr(ids) if T else ctypes.c_void_p(0), T, V, D, float(scale),
+                                   _ptr(dtable), int(dtable.dtype == torch.bfloat16), _row_stride(dtable),
+                                   int(bool(accumulate)), _ptr(workspace), workspace.numel(), _stream(dev)))
+    if check_status:
+        _raise_status(workspace)
+    return dtable
+
+
+class _Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, ids, scale):
+        ctx.save_for_backward(ids)
+        ctx.num_rows, ctx.scale = table.shape[0], scale
+        return embed_fwd(table, ids, scale)
+
+    @staticmethod
+    def backward(ctx, dout):
+        (ids,) = ctx.saved_tensors
+        return embed_bwd(dout.contiguous(), ids, ctx.num_rows, ctx.scale), None, None
+
+
+def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """Differentiable token embedding of the packed stream: scale * table[ids], [T, D]."""
+    return _Embed.apply(table, ids, scale)
 
 
 # ----------------------------------------------------------------- padded-batch bridge

@@ -15,7 +15,7 @@ VA_OK = 0
 STATUS_NAMES = {
     0: "VA_OK", 1: "VA_ERR_INVALID_ARG", 2: "VA_ERR_UNSUPPORTED", 3: "VA_ERR_WORKSPACE",
     4: "VA_ERR_CUDA", 5: "VA_ERR_BAD_SEQLENS", 6: "VA_ERR_TIMEOUT", 7: "VA_ERR_CAPACITY",
-    8: "VA_ERR_BAD_TARGETS",
+    8: "VA_ERR_BAD_TARGETS", 9: "VA_ERR_BAD_IDS",
 }
 
 # every symbol include/varlen_attn.h declares
@@ -33,6 +33,7 @@ EXPORTS = (
     "varlen_attn_bwd_cross", "varlen_test_stall_next_forward",
     "varlen_attn_workspace_size_sinks", "varlen_attn_plan_sinks", "varlen_attn_fwd_sinks", "varlen_attn_bwd_sinks",
     "varlen_token_distill_workspace_size", "varlen_token_distill",
+    "varlen_embed_fwd", "varlen_embed_bwd_workspace_size", "varlen_embed_bwd",
 )
 
 
@@ -123,6 +124,11 @@ def _declare(lib):
                                            c_int64, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
                                            c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
                                            c_void_p]),
+        "varlen_embed_fwd": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32, c_float,
+                                       c_void_p, c_int64, c_void_p, c_void_p]),
+        "varlen_embed_bwd_workspace_size": (c_size_t, [c_int32, c_int32]),
+        "varlen_embed_bwd": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32, c_float,
+                                       c_void_p, c_int32, c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
         "varlen_read_status": (c_int32, [c_void_p, i32p, c_void_p]),
         "varlen_clear_status": (c_int32, [c_void_p, c_void_p]),
         "varlen_profile_enable": (c_int32, [c_int32]),

@@ -37,6 +37,11 @@ size_t distill_parts_bytes();
 cudaError_t launch_token_distill(int, const void*, int, int64_t, const int32_t*, int64_t, const void*, int, int64_t,
                                  const int32_t*, int, int, int, int, float, void*, int64_t, void*, int32_t*, uint8_t*,
                                  float*, float*, int32_t*, cudaStream_t);
+size_t embed_bwd_workspace(int, int);
+cudaError_t launch_embed_fwd(const void*, int, int64_t, const int32_t*, int, int, int, float, void*, int64_t, int32_t*,
+                             cudaStream_t);
+cudaError_t launch_embed_bwd(int, const void*, int, int64_t, const int32_t*, int, int, int, float, void*, int, int64_t,
+                             int, void*, cudaStream_t);
 cudaError_t launch_bwd_dkdv_tc(const BwdParams&, int, int, bool, cudaStream_t);
 cudaError_t launch_bwd_dq_tc(const BwdParams&, int, int, bool, cudaStream_t);
 void bwd_tc_tiles(int*, int*, int*, int*);
@@ -51,14 +56,15 @@ void set_error(const char* msg) { g_error = msg; }
 enum KernelId {
   K_VALIDATE = 0, K_META_SCAN, K_META_FILL, K_PLAN, K_FWD, K_BWD_PREP, K_BWD_DKDV, K_BWD_DQ,
   K_VALIDATE_PLAN, K_FWD_TOK, K_CU_FROM_POS, K_LOSS_TARGETS, K_CE_COUNT, K_CE_ROWS, K_CE_REDUCE, K_PAD_COUNT,
-  K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE, K_COUNT
+  K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE,
+  K_EMBED_FWD, K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "validate_cu_seqlens", "metadata_scan", "metadata_fill", "plan",          "fwd",
     "bwd_prep",            "bwd_dkdv",      "bwd_dq",        "validate_plan", "fwd_tok",
     "cu_from_positions",   "loss_targets",  "ce_count",      "ce_rows",       "ce_reduce",
     "pad_count",           "pad_scan",      "pad_index",     "gather_rows", "distill_count", "distill_rows",
-    "distill_reduce"};
+    "distill_reduce", "embed_fwd", "embed_sort", "embed_reduce", "embed_join"};
 
 struct Profiler {
   std::vector<cudaEvent_t> start, stop;
@@ -709,6 +715,56 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
                                   ignore_index, temperature, grad, g_rs, w, parts, flags, kl, loss, count, cs);
     });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_distill");
+}
+
+static va_status check_embed(const char* where, const void* a, const void* b, const int32_t* ids, int32_t dtype_a,
+                             int32_t dtype_b, int64_t a_rs, int64_t b_rs, int32_t T, int32_t V, int32_t D,
+                             float scale) {
+  const std::string w(where);
+  if (!a || !b || (T > 0 && !ids)) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+  if (T < 0 || T >= (1 << 30) || V < 1 || D < 1 || V == INT32_MAX || dtype_a < 0 || dtype_a > 1 || dtype_b < 0 || dtype_b > 1)
+    return fail(VA_ERR_INVALID_ARG, w + ": 0 <= T < 2^30, V and D >= 1, V < 2^31 - 1, dtypes 0 or 1");
+  if (a_rs < D || b_rs < D) return fail(VA_ERR_INVALID_ARG, w + ": row strides must be >= D");
+  if ((reinterpret_cast<uintptr_t>(a) & (dtype_a == 1 ? 1 : 3)) || (reinterpret_cast<uintptr_t>(b) & (dtype_b == 1 ? 1 : 3)))
+    return fail(VA_ERR_INVALID_ARG, w + ": pointers must be aligned to their type");
+  if (!(scale > -INFINITY && scale < INFINITY)) return fail(VA_ERR_INVALID_ARG, w + ": scale must be finite");
+  return VA_OK;
+}
+
+va_status varlen_embed_fwd(const void* table, int32_t dtype, int64_t t_rs, const int32_t* ids, int32_t T, int32_t V,
+                           int32_t D, float scale, void* out, int64_t o_rs, int32_t* status, va_stream_t stream) {
+  const va_status st = check_embed("embed_fwd", table, out, ids, dtype, dtype, t_rs, o_rs, T, V, D, scale);
+  if (st != VA_OK) return st;
+  if (T == 0) return VA_OK;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch(K_EMBED_FWD, cs, [&] {
+    return launch_embed_fwd(table, dtype, t_rs, ids, T, V, D, scale, out, o_rs, status, cs);
+  });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "embed_fwd");
+}
+
+size_t varlen_embed_bwd_workspace_size(int32_t T, int32_t D) {
+  return T < 0 || D < 1 ? 0 : embed_bwd_workspace(T, D);
+}
+
+va_status varlen_embed_bwd(const void* dout, int32_t dtype, int64_t i_rs, const int32_t* ids, int32_t T, int32_t V,
+                           int32_t D, float scale, void* dtable, int32_t table_dtype, int64_t o_rs, int32_t accumulate,
+                           void* ws, size_t ws_bytes, va_stream_t stream) {
+  // without tokens dout is not read and may be null
+  const va_status st = check_embed("embed_bwd", T == 0 && !dout ? dtable : dout, dtable, ids, T == 0 ? table_dtype : dtype,
+                                   table_dtype, i_rs, o_rs, T, V, D, scale);
+  if (st != VA_OK) return st;
+  if (!ws || !aligned16(ws)) return fail(VA_ERR_INVALID_ARG, "embed_bwd: workspace must be 16-byte aligned");
+  if (ws_bytes < varlen_embed_bwd_workspace_size(T, D)) return fail(VA_ERR_WORKSPACE, "embed_bwd: workspace too small");
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  const KernelId kid[3] = {K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN};
+  for (int stage = 0; stage < (T > 0 ? 3 : 1) && e == cudaSuccess; ++stage)
+    e = launch(kid[stage], cs, [&] {
+      return launch_embed_bwd(stage, dout, dtype, i_rs, ids, T, V, D, scale, dtable, table_dtype, o_rs,
+                              accumulate ? 1 : 0, ws, cs);
+    });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "embed_bwd");
 }
 
 va_status varlen_read_status(const void* ws, int32_t* out, va_stream_t stream) {

@@ -1,0 +1,559 @@
+// Embedding of the packed stream and its gradient by sorted tokens.
+//
+//     out[t] = scale * table[ids[t]]                      (a negative id: a zero row)
+//     dtable[v] = scale * sum_{t : ids[t] = v} dout[t]    (negative ids add nothing)
+//
+// The gradient is deterministic: every row of dtable is a sum in token order, in fp32, rounded
+// once.  Tokens are sorted by id (stable), equal ids form runs of the sorted order, and the runs
+// are summed.  Kernels (one stream, programmatic dependent launches):
+//   embed_fwd_kernel     one 16-byte vector per thread and step, several rows per block when rows
+//                        are short; HBM-bound
+//   embed_sort_kernel    cluster 0: least-significant-digit radix sort of (id, token) in one launch,
+//                        eight CTAs that exchange digit counts through distributed shared memory
+//                        (the sorted pairs stay in L2); the other clusters meanwhile write the zero
+//                        rows of the ids that no token has, so the sort costs no time of its own
+//                        when a whole table is written
+//   embed_reduce_kernel  chunks of P sorted tokens x columns: rows of dout are read once, eight loads
+//                        in flight per thread, sums of runs that lie inside a chunk are final, the
+//                        others go to two fp32 rows per chunk
+//   embed_join_kernel    runs over several chunks: the chunks' sums in order
+// What bounds the gradient: dout read once and dtable written once (HBM).
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace va {
+
+namespace {
+
+constexpr int kFwdThreads = 256, kFwdUnroll = 2;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortCtas = 8;               // one cluster
+constexpr int kMaxBins = 512;
+constexpr int kPresentWords = 16384;       // ids a filling CTA looks at together: 32 per word
+constexpr int kReduceThreads = 256;
+constexpr int kRows = 8;                   // rows of dout in flight per thread
+
+struct EmbedParams {
+  const int32_t* ids;
+  int T, V, D;
+  float scale;
+  const void* src;  // table (forward), dout (gradient)
+  int64_t s_rs;
+  void* dst;  // out, dtable
+  int64_t d_rs;
+  int32_t* status;
+  // gradient
+  int accumulate;
+  int32_t *key0, *tok0, *key1, *tok1;  // [T] ping-pong
+  int bits, passes, width;             // radix: `passes` digits of `width` bits
+  float* part;                         // [chunks][2][D]
+  int P;                               // sorted tokens per chunk
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// W consecutive values of a row from column c on (c + W <= D unless GUARD); VEC: 16-byte accesses.
+template <bool VEC, int W>
+__device__ __forceinline__ void load_row(const float* p, int n, float (&x)[W]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 u = __ldcs(reinterpret_cast<const float4*>(p + i));
+      x[i] = u.x;
+      x[i + 1] = u.y;
+      x[i + 2] = u.z;
+      x[i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = i < n ? p[i] : 0.f;
+  }
+}
+template <bool VEC, int W>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int n, float (&x)[W]) {
+  if constexpr (VEC) {
+    static_assert(W == 8, "one vector");
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = i < n ? to_f(p[i]) : 0.f;
+  }
+}
+template <bool VEC, int W>
+__device__ __forceinline__ void store_row(float* p, int n, const float (&x)[W]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) p[i] = x[i];
+  }
+}
+template <bool VEC, int W>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, int n, const float (&x)[W]) {
+  if constexpr (VEC) {
+    static_assert(W == 8, "one vector");
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                              pack_bf16(x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) p[i] = from_f<__nv_bfloat16>(x[i]);
+  }
+}
+
+constexpr int kW = 8;  // columns per thread
+
+// Threads that share a row: enough for its columns, at most a block.
+int lanes_per_row(int D, int threads) {
+  int n = 1;
+  while (n < threads && n * kW < D) n *= 2;
+  return n;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int load_remote(const int* p, int rank) {
+  int v;
+  asm volatile("{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %1, %2;\n ld.shared::cluster.u32 %0, [ra];\n}\n"
+               : "=r"(v)
+               : "r"(smem_u32(p)), "r"(rank)
+               : "memory");
+  return v;
+}
+
+}  // namespace
+
+// Row group g of block b handles token b * groups + g; its lanes take the columns in vectors.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedParams p, int lpr) {
+  griddep_begin();
+  const int groups = kFwdThreads / lpr, g = threadIdx.x / lpr, lane = threadIdx.x % lpr;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+  if (t >= p.T) return;
+  const int id = __ldg(p.ids + t);
+  T* dst = static_cast<T*>(p.dst) + t * p.d_rs;
+  const bool in = id >= 0 && id < p.V;
+  const T* src = static_cast<const T*>(p.src) + (in ? id : 0) * p.s_rs;
+  // an id past the table: a row of NaN (the error shows without a synchronisation) and the status
+  const float fill = id < 0 ? 0.f : NAN;
+  if (id >= p.V && lane == 0 && p.status) atomicCAS(p.status, 0, VA_ERR_BAD_IDS);
+  for (int c0 = lane * kW; c0 < p.D; c0 += kFwdUnroll * lpr * kW) {
+    float x[kFwdUnroll][kW];
+#pragma unroll
+    for (int u = 0; u < kFwdUnroll; ++u) {
+      const int c = c0 + u * lpr * kW;
+      if (in && c < p.D) load_row<VEC>(src + c, p.D - c, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kFwdUnroll; ++u) {
+      const int c = c0 + u * lpr * kW;
+      if (c >= p.D) break;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) x[u][i] = in ? x[u][i] * p.scale : fill;
+      store_row<VEC>(dst + c, p.D - c, x[u]);
+    }
+  }
+}
+
+// The zero rows of [v0, v1) that no token has (clusters after the first).
+template <class T, bool VEC>
+__device__ void fill_absent(const EmbedParams& p, uint32_t* present, int v0, int v1) {
+  T* dst = static_cast<T*>(p.dst);
+  for (int a = v0; a < v1; a += kPresentWords * 32) {
+    const int n = min(v1 - a, kPresentWords * 32);
+    __syncthreads();
+    for (int i = threadIdx.x; i < (n + 31) / 32; i += kSortThreads) present[i] = 0;
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.T; t += kSortThreads) {
+      const unsigned r = static_cast<unsigned>(__ldg(p.ids + t)) - static_cast<unsigned>(a);
+      if (r < static_cast<unsigned>(n)) atomicOr(&present[r >> 5], 1u << (r & 31));
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float zero[kW] = {};
+    for (int r = warp; r < n; r += kSortWarps) {
+      if ((present[r >> 5] >> (r & 31)) & 1u) continue;
+      T* row = dst + static_cast<int64_t>(a + r) * p.d_rs;
+      for (int c = lane * kW; c < p.D; c += 32 * kW) store_row<VEC>(row + c, p.D - c, zero);
+    }
+  }
+}
+
+// Cluster 0 sorts, the others fill.  Stable: warp g of the cluster owns the g-th contiguous share
+// of the input, and equal digits keep the order (warp, round, lane).
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedParams p) {
+  extern __shared__ __align__(16) int sm[];
+  griddep_begin();
+  if (blockIdx.x >= kSortCtas) {
+    const int n = gridDim.x - kSortCtas, i = blockIdx.x - kSortCtas;
+    const int per = (p.V + n - 1) / n;
+    const int64_t v0 = static_cast<int64_t>(per) * i;
+    if (v0 < p.V)
+      fill_absent<T, VEC>(p, reinterpret_cast<uint32_t*>(sm), static_cast<int>(v0),
+                          static_cast<int>(std::min<int64_t>(p.V, v0 + per)));
+    return;
+  }
+  int* cnt = sm;                              // [warps][bins]: counts, then next ranks
+  int* hist = sm + kSortWarps * kMaxBins;     // [bins] of this CTA, read by the others
+  int* scan = hist + kMaxBins;                // [warps]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int share = ((p.T + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
+  const int64_t b0 = static_cast<int64_t>(rank * kSortWarps + warp) * share;
+  const int beg = static_cast<int>(std::min<int64_t>(p.T, b0)), end = static_cast<int>(std::min<int64_t>(p.T, b0 + share));
+  if (rank == 0 && tid == 0) *p.status = VA_OK;
+  bool bad = false;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.width, bins = 1 << p.width;
+    const int32_t* ki = (pass & 1) ? p.key1 : p.key0;
+    const int32_t* ti = (pass & 1) ? p.tok1 : p.tok0;
+    int32_t* ko = (pass & 1) ? p.key0 : p.key1;
+    int32_t* to = (pass & 1) ? p.tok0 : p.tok1;
+    // ids outside [0, V) take the key V: they follow every other and are left out
+    auto key_of = [&](int i) -> int {
+      if (pass > 0) return __ldcg(ki + i);
+      const int id = __ldg(p.ids + i);
+      if (id >= p.V) bad = true;
+      return id < 0 || id >= p.V ? p.V : id;
+    };
+    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+    __syncthreads();
+    int* mine = cnt + warp * bins;
+    for (int i0 = beg; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      const int d = i < end ? (key_of(i) >> shift) & (bins - 1) : bins;
+      const unsigned peers = __match_any_sync(0xffffffffu, d);
+      if (d < bins && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    int total = 0;  // of this CTA, bin tid
+    if (tid < bins) {
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int x = cnt[w * bins + tid];
+        cnt[w * bins + tid] = total;
+        total += x;
+      }
+      hist[tid] = total;
+    }
+    cluster_barrier();
+    int all = 0, before = 0;
+    if (tid < bins) {
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) {
+        const int x = load_remote(hist + tid, r);
+        if (r < rank) before += x;
+        all += x;
+      }
+    }
+    // exclusive scan of `all` over the bins
+    int incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int base = before + incl - all;
+    for (int w = 0; w < warp; ++w) base += scan[w];
+    if (tid < bins)
+      for (int w = 0; w < kSortWarps; ++w) cnt[w * bins + tid] += base;
+    __syncthreads();
+    for (int i0 = beg; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      const int k = i < end ? key_of(i) : 0;
+      const int d = i < end ? (k >> shift) & (bins - 1) : bins;
+      const unsigned peers = __match_any_sync(0xffffffffu, d);
+      const int at = d < bins ? mine[d] + __popc(peers & ((1u << lane) - 1)) : 0;
+      __syncwarp();
+      if (d < bins) {
+        if (lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+        ko[at] = k;
+        to[at] = pass > 0 ? __ldcg(ti + i) : i;
+      }
+      __syncwarp();
+    }
+    cluster_barrier();  // the sorted pairs are visible, and no CTA's counts are read any more
+  }
+  if (bad) atomicExch(p.status, VA_ERR_BAD_IDS);
+}
+
+// One group of lpr threads per chunk of P sorted tokens (grid.y: further columns).
+template <class TI, class TO, bool VI, bool VO>
+__global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const EmbedParams p, const int32_t* key,
+                                                                      const int32_t* tok, int lpr) {
+  griddep_begin();
+  const int groups = kReduceThreads / lpr;
+  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lpr;
+  const int64_t b0 = chunk * p.P;
+  const int c = (blockIdx.y * lpr + threadIdx.x % lpr) * kW;
+  if (b0 >= p.T || c >= p.D) return;
+  const int beg = static_cast<int>(b0), end = min(p.T, beg + p.P);
+  const TI* src = static_cast<const TI*>(p.src) + c;
+  TO* dst = static_cast<TO*>(p.dst) + c;
+  float* part = p.part + chunk * 2 * p.D + c;
+  int cur = __ldg(key + beg);
+  if (cur >= p.V) return;
+  const bool joined = beg > 0 && __ldg(key + beg - 1) == cur;  // the first run began before the chunk
+  bool first = true;
+  float acc[kW] = {};
+  auto put = [&]() {  // the run that ends here
+    if (first && joined) {
+#pragma unroll
+      for (int i = 0; i < kW; ++i)
+        if (i < p.D - c) part[i] = acc[i];
+    } else {
+      float x[kW];
+      TO* row = dst + cur * p.d_rs;
+      if (p.accumulate) load_row<VO>(row, p.D - c, x);
+#pragma unroll
+      for (int i = 0; i < kW; ++i) x[i] = p.accumulate ? fmaf(acc[i], p.scale, x[i]) : acc[i] * p.scale;
+      store_row<VO>(row, p.D - c, x);
+    }
+    first = false;
+  };
+  for (int i0 = beg; i0 < end; i0 += kRows) {
+    int k[kRows];
+    float x[kRows][kW];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) k[u] = i0 + u < end ? __ldg(key + i0 + u) : p.V;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (k[u] < p.V) load_row<VI>(src + __ldg(tok + i0 + u) * p.s_rs, p.D - c, x[u]);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (k[u] >= p.V) break;
+      if (k[u] != cur) {
+        put();
+        cur = k[u];
+#pragma unroll
+        for (int i = 0; i < kW; ++i) acc[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kW; ++i) acc[i] += x[u][i];
+    }
+  }
+  if (end < p.T && __ldg(key + end) == cur) {  // goes on in the next chunk
+    float* q = first && joined ? part : part + p.D;
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      if (i < p.D - c) q[i] = acc[i];
+  } else {
+    put();
+  }
+}
+
+// Runs over several chunks: the chunk that a run starts in adds the chunks' sums in order.
+template <class TO, bool VO>
+__global__ void __launch_bounds__(kReduceThreads) embed_join_kernel(const EmbedParams p, const int32_t* key, int lpr) {
+  griddep_begin();
+  const int groups = kReduceThreads / lpr;
+  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lpr;
+  const int64_t b0 = chunk * p.P;
+  const int c = (blockIdx.y * lpr + threadIdx.x % lpr) * kW;
+  if (b0 + p.P >= p.T || c >= p.D) return;  // the last chunk's runs end in it
+  const int beg = static_cast<int>(b0), end = beg + p.P;
+  const int cur = __ldg(key + end - 1);
+  if (cur >= p.V || __ldg(key + end) != cur) return;                       // ends in this chunk
+  if (__ldg(key + beg) == cur && beg > 0 && __ldg(key + beg - 1) == cur) return;  // began before it
+  int lo = end, hi = p.T;  // first sorted token with a larger key
+  while (lo < hi) {
+    const int mid = lo + ((hi - lo) >> 1);
+    if (__ldg(key + mid) > cur) hi = mid;
+    else lo = mid + 1;
+  }
+  const int last = (lo - 1) / p.P;
+  const int n = p.D - c;
+  const float* part = p.part + c;
+  float acc[kW];
+#pragma unroll
+  for (int i = 0; i < kW; ++i) acc[i] = i < n ? part[(chunk * 2 + 1) * p.D + i] : 0.f;
+  for (int64_t q = chunk + 1; q <= last; q += 4) {
+    float x[4][kW];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < kW; ++i) x[u][i] = q + u <= last && i < n ? part[(q + u) * 2 * p.D + i] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < kW; ++i) acc[i] += x[u][i];
+  }
+  TO* row = static_cast<TO*>(p.dst) + cur * p.d_rs + c;
+  float x[kW];
+  if (p.accumulate) load_row<VO>(row, n, x);
+#pragma unroll
+  for (int i = 0; i < kW; ++i) x[i] = p.accumulate ? fmaf(acc[i], p.scale, x[i]) : acc[i] * p.scale;
+  store_row<VO>(row, n, x);
+}
+
+// ---------------------------------------------------------------- host side
+
+namespace {
+
+bool rows_vec(const void* p, int64_t rs, int D, int elem) {
+  return D % kW == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && rs * elem % 16 == 0;
+}
+
+// Sorted tokens per chunk: enough chunks to fill the GPU (two thousand threads an SM), few enough
+// that runs are mostly inside one.
+int chunk_tokens(int T, int D) {
+  const int64_t vecs = static_cast<int64_t>(T) * ((D + kW - 1) / kW);
+  int P = 16;
+  while (P < 128 && vecs / P > 152 * 2048) P *= 2;
+  return P;
+}
+
+template <class T, bool VEC>
+cudaError_t launch_sort(const EmbedParams& p, int ctas, cudaStream_t st) {
+  const auto kernel = embed_sort_kernel<T, VEC>;
+  const size_t smem = std::max<size_t>((kSortWarps * kMaxBins + kMaxBins + kSortWarps) * sizeof(int),
+                                       kPresentWords * sizeof(uint32_t));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSortCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class TI, class TO, bool VI>
+cudaError_t launch_reduce(const EmbedParams& p, bool vo, dim3 grid, const int32_t* key, const int32_t* tok, int lpr,
+                          cudaStream_t st) {
+  return vo ? launch_pdl(embed_reduce_kernel<TI, TO, VI, true>, grid, dim3(kReduceThreads), 0, st, p, key, tok, lpr)
+            : launch_pdl(embed_reduce_kernel<TI, TO, VI, false>, grid, dim3(kReduceThreads), 0, st, p, key, tok, lpr);
+}
+template <class TI, class TO>
+cudaError_t launch_reduce(const EmbedParams& p, bool vi, bool vo, dim3 grid, const int32_t* key, const int32_t* tok,
+                          int lpr, cudaStream_t st) {
+  return vi ? launch_reduce<TI, TO, true>(p, vo, grid, key, tok, lpr, st)
+            : launch_reduce<TI, TO, false>(p, vo, grid, key, tok, lpr, st);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+size_t embed_bwd_workspace(int T, int D) {
+  const int P = chunk_tokens(T, D);
+  const size_t chunks = (static_cast<size_t>(T) + P - 1) / P;
+  return sizeof(WsHeader) + 4 * align256(static_cast<size_t>(T) * sizeof(int32_t)) +
+         align256(chunks * 2 * D * sizeof(float));
+}
+
+cudaError_t launch_embed_fwd(const void* table, int bf16, int64_t t_rs, const int32_t* ids, int T, int V, int D,
+                             float scale, void* out, int64_t o_rs, int32_t* status, cudaStream_t st) {
+  EmbedParams p{};
+  p.ids = ids;
+  p.T = T;
+  p.V = V;
+  p.D = D;
+  p.scale = scale;
+  p.src = table;
+  p.s_rs = t_rs;
+  p.dst = out;
+  p.d_rs = o_rs;
+  p.status = status;
+  const int elem = bf16 ? 2 : 4;
+  const bool vec = rows_vec(table, t_rs, D, elem) && rows_vec(out, o_rs, D, elem);
+  const int lpr = lanes_per_row(D, kFwdThreads), groups = kFwdThreads / lpr;
+  const dim3 grid((T + groups - 1) / groups), block(kFwdThreads);
+  if (bf16)
+    return vec ? launch_pdl(embed_fwd_kernel<__nv_bfloat16, true>, grid, block, 0, st, p, lpr)
+               : launch_pdl(embed_fwd_kernel<__nv_bfloat16, false>, grid, block, 0, st, p, lpr);
+  return vec ? launch_pdl(embed_fwd_kernel<float, true>, grid, block, 0, st, p, lpr)
+             : launch_pdl(embed_fwd_kernel<float, false>, grid, block, 0, st, p, lpr);
+}
+
+// The three launches of varlen_embed_bwd, in this order on one stream (without tokens the first one
+// alone: it writes every row's zeros).
+cudaError_t launch_embed_bwd(int stage, const void* dout, int in_bf16, int64_t i_rs, const int32_t* ids, int T, int V,
+                             int D, float scale, void* dtable, int out_bf16, int64_t o_rs, int accumulate, void* ws,
+                             cudaStream_t st) {
+  EmbedParams p{};
+  p.ids = ids;
+  p.T = T;
+  p.V = V;
+  p.D = D;
+  p.scale = scale;
+  p.src = dout;
+  p.s_rs = i_rs;
+  p.dst = dtable;
+  p.d_rs = o_rs;
+  p.accumulate = accumulate;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.status = &reinterpret_cast<WsHeader*>(w)->status;
+  int32_t** arrays[4] = {&p.key0, &p.tok0, &p.key1, &p.tok1};
+  const size_t one = align256(static_cast<size_t>(T) * sizeof(int32_t));
+  for (int i = 0; i < 4; ++i) *arrays[i] = reinterpret_cast<int32_t*>(w + sizeof(WsHeader) + i * one);
+  p.part = reinterpret_cast<float*>(w + sizeof(WsHeader) + 4 * one);
+  p.P = chunk_tokens(T, D);
+  p.bits = 1;
+  while (p.bits < 31 && (V >> p.bits) > 0) ++p.bits;  // keys 0 .. V
+  p.passes = (p.bits + 8) / 9;
+  p.width = (p.bits + p.passes - 1) / p.passes;
+  const bool vi = rows_vec(dout, i_rs, D, in_bf16 ? 2 : 4), vo = rows_vec(dtable, o_rs, D, out_bf16 ? 2 : 4);
+  if (stage == 0) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int fill = accumulate ? 0 : std::max(1, sms / kSortCtas - 1);  // clusters
+    const int ctas = kSortCtas * (1 + fill);
+    if (out_bf16) return vo ? launch_sort<__nv_bfloat16, true>(p, ctas, st) : launch_sort<__nv_bfloat16, false>(p, ctas, st);
+    return vo ? launch_sort<float, true>(p, ctas, st) : launch_sort<float, false>(p, ctas, st);
+  }
+  const int32_t* key = (p.passes & 1) ? p.key1 : p.key0;
+  const int32_t* tok = (p.passes & 1) ? p.tok1 : p.tok0;
+  const int lpr = lanes_per_row(D, kReduceThreads), groups = kReduceThreads / lpr;
+  const int64_t chunks = (static_cast<int64_t>(T) + p.P - 1) / p.P;
+  const dim3 grid(static_cast<unsigned>((chunks + groups - 1) / groups), (D + lpr * kW - 1) / (lpr * kW));
+  if (stage == 1) {
+    if (in_bf16)
+      return out_bf16 ? launch_reduce<__nv_bfloat16, __nv_bfloat16>(p, vi, vo, grid, key, tok, lpr, st)
+                      : launch_reduce<__nv_bfloat16, float>(p, vi, vo, grid, key, tok, lpr, st);
+    return out_bf16 ? launch_reduce<float, __nv_bfloat16>(p, vi, vo, grid, key, tok, lpr, st)
+                    : launch_reduce<float, float>(p, vi, vo, grid, key, tok, lpr, st);
+  }
+  const dim3 block(kReduceThreads);
+  if (out_bf16)
+    return vo ? launch_pdl(embed_join_kernel<__nv_bfloat16, true>, grid, block, 0, st, p, key, lpr)
+              : launch_pdl(embed_join_kernel<__nv_bfloat16, false>, grid, block, 0, st, p, key, lpr);
+  return vo ? launch_pdl(embed_join_kernel<float, true>, grid, block, 0, st, p, key, lpr)
+            : launch_pdl(embed_join_kernel<float, false>, grid, block, 0, st, p, key, lpr);
+}
+
+}  // namespace va

@@ -479,7 +479,7 @@ size_t varlen_token_distill_workspace_size(int32_t T);
  *   ws_dev / ws_bytes   workspace (>= varlen_token_distill_workspace_size(T), 16-byte aligned)
  * Rows need no alignment beyond their type's.  grad may be the logits themselves (same strides).
  * Arithmetic in fp32 per row, the sum over rows in fp64 in a fixed order (deterministic), rounded
- * once.  Limits: K <= 1024, a row of logits within 1,638,400 bytes (VA_ERR_UNSUPPORTED beyond).
+ * once.  Limits: K <= 1024, a row of logits within 1,310,720 bytes (VA_ERR_UNSUPPORTED beyond).
  * Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED, VA_ERR_WORKSPACE, VA_ERR_CUDA; the status word
  * gets VA_ERR_BAD_TARGETS when an eligible row lists a class >= V or no row is eligible (then
  * loss is NaN and no gradient is written).  Asynchronous. */

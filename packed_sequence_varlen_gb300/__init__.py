@@ -10,6 +10,7 @@ Layout: q [T, Hq, d], k/v [T, Hkv, d] bf16 with the last dim contiguous;
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -32,12 +33,21 @@ def library_path() -> str:
     return _lib.LIB_PATH
 
 
-def _stream(dev: torch.device | None = None):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+# Pointers and streams go to the library as plain integers (ctypes converts them): building torch's
+# and ctypes' objects for them costs more host time than the rest of a small call.
+
+def _stream(dev: torch.device | None = None) -> int:
+    index = torch._C._cuda_getDevice() if dev is None or dev.index is None else dev.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _ptr(t: torch.Tensor | None):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _on(dev: torch.device):
+    """Makes ``dev`` the current device for a ``with`` block (nothing to do where it is already)."""
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
 # ----------------------------------------------------------------- host planner
@@ -460,7 +470,7 @@ def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     loss = torch.empty(2, dtype=torch.float32, device=dev)
     count = torch.empty(1, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check(lib.varlen_token_distill(_ptr(logits), int(logits.dtype == torch.bfloat16), _row_stride(logits),
                                        _ptr(teacher_ids), _row_stride(teacher_ids), _ptr(teacher_logits),
                                        int(teacher_logits.dtype == torch.bfloat16), _row_stride(teacher_logits),
@@ -505,9 +515,9 @@ def embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: t
             raise ValueError("out must be [T, D] in table's dtype")
         _same_device(dev, out=out)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         check(_lib.load().varlen_embed_fwd(_ptr(table), int(table.dtype == torch.bfloat16), _row_stride(table),
-                                           _ptr(ids) if T else ctypes.c_void_p(0), T, V, D, float(scale),
+                                           _ptr(ids) if T else 0, T, V, D, float(scale),
                                            _ptr(out) if T else _ptr(table), _row_stride(out), _ptr(status),
                                            _stream(dev)))
     if check_status and int(status.item()) != 0:
@@ -541,9 +551,9 @@ def embed_bwd(dout: torch.Tensor, ids: torch.Tensor, num_rows: int, scale: float
     need = lib.varlen_embed_bwd_workspace_size(T, D)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        check(lib.varlen_embed_bwd(_ptr(dout) if T else ctypes.c_void_p(0), int(dout.dtype == torch.bfloat16),
-                                   _row_stride(dout), _ptr(ids) if T else ctypes.c_void_p(0), T, V, D, float(scale),
+    with _on(dev):
+        check(lib.varlen_embed_bwd(_ptr(dout) if T else 0, int(dout.dtype == torch.bfloat16),
+                                   _row_stride(dout), _ptr(ids) if T else 0, T, V, D, float(scale),
                                    _ptr(dtable), int(dtable.dtype == torch.bfloat16), _row_stride(dtable),
                                    int(bool(accumulate)), _ptr(workspace), workspace.numel(), _stream(dev)))
     if check_status:

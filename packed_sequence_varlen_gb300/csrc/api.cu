@@ -36,7 +36,7 @@ bool distill_row_fits(int, int);
 size_t distill_parts_bytes();
 cudaError_t launch_token_distill(int, const void*, int, int64_t, const int32_t*, int64_t, const void*, int, int64_t,
                                  const int32_t*, int, int, int, int, float, void*, int64_t, void*, int32_t*, uint8_t*,
-                                 float*, float*, int32_t*, cudaStream_t);
+                                 float*, int32_t*, cudaStream_t);
 size_t embed_bwd_workspace(int, int);
 cudaError_t launch_embed_fwd(const void*, int, int64_t, const int32_t*, int, int, int, float, void*, int64_t, int32_t*,
                              cudaStream_t);
@@ -677,8 +677,7 @@ va_status varlen_token_ce(const void* logits, int32_t dtype, int64_t l_rs, const
 
 size_t varlen_token_distill_workspace_size(int32_t T) {
   if (T < 0) return 0;
-  return align256(sizeof(WsHeader) + distill_parts_bytes() + static_cast<size_t>(T) * sizeof(float)) +
-         align256(static_cast<size_t>(T));
+  return align256(sizeof(WsHeader) + distill_parts_bytes() + static_cast<size_t>(T));
 }
 
 va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, const int32_t* ids, int64_t ids_rs,
@@ -691,7 +690,7 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
     return fail(VA_ERR_INVALID_ARG, "token_distill: T, V, K >= 1, dtypes 0 or 1");
   if (K > 1024) return fail(VA_ERR_UNSUPPORTED, "token_distill: at most 1024 teacher entries per row");
   if (!distill_row_fits(V, dtype == 1 ? 2 : 4))
-    return fail(VA_ERR_UNSUPPORTED, "token_distill: a row of logits must stay within 1,638,400 bytes");
+    return fail(VA_ERR_UNSUPPORTED, "token_distill: a row of logits must stay within 1,310,720 bytes");
   if (l_rs < V || ids_rs < K || t_rs < K || (grad && g_rs < V))
     return fail(VA_ERR_INVALID_ARG, "token_distill: row strides must be >= the row");
   const uintptr_t ea = dtype == 1 ? 1 : 3;
@@ -705,14 +704,13 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
   int32_t* parts = reinterpret_cast<int32_t*>(w + sizeof(WsHeader));
-  float* kl = reinterpret_cast<float*>(w + sizeof(WsHeader) + distill_parts_bytes());
-  uint8_t* flags = reinterpret_cast<uint8_t*>(kl + T);
+  uint8_t* flags = w + sizeof(WsHeader) + distill_parts_bytes();
   cudaError_t e = cudaSuccess;
   const KernelId kid[3] = {K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE};
   for (int stage = 0; stage < 3 && e == cudaSuccess; ++stage)
     e = launch(kid[stage], cs, [&] {
       return launch_token_distill(stage, logits, dtype, l_rs, ids, ids_rs, tl, t_dtype, t_rs, targets, T, V, K,
-                                  ignore_index, temperature, grad, g_rs, w, parts, flags, kl, loss, count, cs);
+                                  ignore_index, temperature, grad, g_rs, w, parts, flags, loss, count, cs);
     });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_distill");
 }

@@ -18,11 +18,16 @@
 //
 // Rows.  What bounds it: HBM, z read once and the gradient written once.  So a row stays in
 // shared memory between its log-sum-exp and its gradient: CTA rank c of the cluster holds the
-// c-th slice, and each of its warps a piece of the slice that it loads with one bulk copy, scans
-// for its maximum, sums, overwrites with the gradient and hands to one bulk store, on its own;
-// the only barriers of a row are the ones of the (max, sum) exchange.  Rows may start anywhere:
-// the elements before the first and after the last 16-byte boundary (at most 7 each) go through
-// registers.  The log-sum-exp, p and the row losses are fp32, a gradient value is rounded once.
+// c-th slice (one bulk copy in, one out), and its NW working warps each scan a piece of it for the
+// maximum, sum it and overwrite it with the gradient.  A CTA takes its rows one after the other; three
+// CTAs share an SM, so one's copies run under the others' arithmetic.  (Deeper pipelines inside one
+// CTA of 16 warps measured no faster: what a row costs there is the latency of its reductions.)
+// One more warp per CTA prepares the teacher's entries a row ahead (loaded two rows ahead), and handles
+// the elements before the row's first and after its last 16-byte boundary (at most 7 each), so rows may
+// start anywhere.  The (max, sum) pairs cross the cluster by asynchronous stores that count on the
+// receiver's barrier: a release at cluster scope instead cost 2000 cycles a row.  The log-sum-exp, p
+// and the row losses are fp32, a gradient value is rounded once; every CTA adds its rows' losses in
+// fp64.
 #include <algorithm>
 #include <cstddef>
 #include <type_traits>
@@ -34,11 +39,15 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kDistWarps = 8;
-constexpr int kDistThreads = 32 * kDistWarps;
+constexpr int kCountWarps = 8;
+constexpr int kMaxWarps = 8;         // working warps of a CTA of the rows kernel
 constexpr int kMaxCluster = 8;
+constexpr int kEdge = 16;            // elements outside the 16-byte vectors: < 8 on each side
 constexpr int kMaxParts = 512;       // blocks of the count kernel
-constexpr int kMaxSlice = 200 << 10; // bytes of a row's slice that one CTA can hold
+constexpr int kMaxCtas = 4096;       // of the rows kernel
+constexpr int kSeenBits = 15;
+constexpr int kMaxSlice = 160 << 10; // bytes of a row's slice that one CTA can hold
+constexpr int kSmemBytes = 227 << 10;
 constexpr int kReduceThreads = 1024;
 
 struct DistillParams {
@@ -58,11 +67,13 @@ struct DistillParams {
   int32_t* parts;  // [nparts] eligible rows per count block, bit 30: an id outside [0, V)
   int nparts;
   uint8_t* flags;  // [T] eligible
-  float* kl;       // [T] row losses
+  double* sums;    // [CTAs of the rows kernel] row losses
+  int ctas;
   float* loss;     // {sum, mean}
   int32_t* count;
   int pv;  // 16-byte vectors of a warp's piece (capacity)
   int C;   // CTAs per row
+  int NW;  // working warps per CTA
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -93,31 +104,37 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Merges running (max, sum of exp2((x - max) sl2)) pairs; a NaN sum stays NaN.  The maximum is
-// kept in the logits' own units and subtracted before the scale: the difference is exact where it
-// matters whatever the logits' common offset, and rows filled with the type's lowest value stay
-// finite.
-__device__ __forceinline__ void ms_merge(float& m, float& s, float m2, float s2, float sl2) {
-  const float mx = fmaxf(m, m2);
-  if (mx == -INFINITY) {
-    s += s2;
-    return;
-  }
-  s = s * fast_exp2((m - mx) * sl2) + s2 * fast_exp2((m2 - mx) * sl2);
-  m = mx;
-}
-
-// x[e] = exp2((x[e] - m) sl2 + b), in place.
-template <int W>
+// Exponents are formed as (x - max) * (log2(e) / tau): the difference comes first, so it is exact
+// where it matters whatever the logits' common offset, and rows filled with the type's lowest value
+// stay finite.
+//
+// x[e] = exp2((x[e] - m) sl2 + b), in place.  ONE: as x[e] sl2 + b with b = (its b) - m sl2, a third
+// fewer instructions before the exponential; b's rounding costs 2^-24 |m sl2| then, which kOneLimit
+// keeps at 2^-16 of the result, against bf16's half step of 2^-8 (fp32 rows do not use it).
+constexpr float kOneLimit = 256.f;
+template <bool ONE, int W>
 __device__ __forceinline__ void exp_row(float (&x)[W], float m, float sl2, float b) {
 #pragma unroll
   for (int e = 0; e < W; e += 2) {
-    float d0, d1;
-    fadd2(d0, d1, x[e], x[e + 1], -m, -m);
+    float d0 = x[e], d1 = x[e + 1];
+    if (!ONE) fadd2(d0, d1, d0, d1, -m, -m);
     ffma2(d0, d1, d0, d1, sl2, sl2, b, b);
     x[e] = fast_exp2(d0);
     x[e + 1] = fast_exp2(d1);
   }
+}
+
+// Calls f(vectors) on `n` 16-byte vectors of shared memory, a warp's lanes in turn; four per lane
+// are loaded together.
+template <class F>
+__device__ __forceinline__ void each_vec(uint4* v, int n, F&& f) {
+  int i = threadIdx.x & 31;
+  for (; i + 96 < n; i += 128) {
+    uint4 u[4] = {v[i], v[i + 32], v[i + 64], v[i + 96]};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f(u[j], i + 32 * j);
+  }
+  for (; i < n; i += 32) f(v[i], i);
 }
 
 // Untiled bulk copies: both addresses 16-byte aligned, a positive multiple of 16 bytes.
@@ -136,16 +153,24 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Writes a float pair at the same shared-memory offset of the cluster's CTA `rank`.
-__device__ __forceinline__ void store_remote2(uint32_t addr, uint32_t rank, float x, float y) {
-  asm volatile("{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n st.shared::cluster.v2.f32 [ra], {%2, %3};\n}\n" ::"r"(
-                   addr),
-               "r"(rank), "f"(x), "f"(y)
-               : "memory");
+// Writes a float pair at this CTA's address `addr`, taken in the cluster's CTA `rank`, and counts its 8
+// bytes on that CTA's barrier at `bar`: no fence, the data travels with its completion.
+__device__ __forceinline__ void send_pair(uint32_t addr, uint32_t bar, uint32_t rank, float x, float y) {
+  asm volatile(
+      "{\n .reg .b32 ra, rb;\n mapa.shared::cluster.u32 ra, %0, %2;\n mapa.shared::cluster.u32 rb, %1, %2;\n"
+      " st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [ra], {%3, %4}, [rb];\n}\n" ::"r"(addr),
+      "r"(bar), "r"(rank), "f"(x), "f"(y)
+      : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() {
+// Barrier of the cluster's threads (a CTA launched alone is a cluster of its own), in two halves:
+// what was written before the arrival is visible after the wait.
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float teacher(const DistillParams& p, int64_t row, int k) {
@@ -153,15 +178,55 @@ __device__ __forceinline__ float teacher(const DistillParams& p, int64_t row, in
                   : static_cast<const float*>(p.a)[row * p.a_rs + k];
 }
 
-// Shared memory behind the pieces.
+// Elementwise maximum of a vector's values, kept packed for bf16.
+struct VecMaxF {
+  float m = -INFINITY;
+  __device__ __forceinline__ void add(const uint4& u) {
+    m = fmax3(m, __uint_as_float(u.x), __uint_as_float(u.y));
+    m = fmax3(m, __uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  __device__ __forceinline__ float get() const { return m; }
+};
+struct VecMaxB {
+  uint32_t m = 0xff80ff80u;  // (-inf, -inf)
+  __device__ __forceinline__ void one(uint32_t x) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x)); }
+  __device__ __forceinline__ void add(const uint4& u) {
+    one(u.x);
+    one(u.y);
+    one(u.z);
+    one(u.w);
+  }
+  __device__ __forceinline__ float get() const {
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <class T> struct VecMax;
+template <> struct VecMax<float> : VecMaxF {};
+template <> struct VecMax<__nv_bfloat16> : VecMaxB {};
+
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Shared memory behind the slice.
 struct DistillSmem {
-  uint64_t full[kDistWarps];  // one mbarrier per warp: its piece has landed
-  float2 red[2][kDistWarps];        // (max, sum) of each warp, by row parity
-  float2 cred[2][kMaxCluster];      // (max, sum) of each CTA of the cluster
-  float entropy[2];                 // sum_k p_k log2 p_k
-  int pad_, abort_flag;
+  uint64_t full, done;                            // the slice has landed / holds the gradient
+  uint64_t swapped[2];                            // every warp's pair of a row is here, by row parity
+  float2 pair[2][kMaxCluster * (kMaxWarps + 1)];  // (max, sum) of every warp of the cluster
+  float edge[2][kEdge];                           // logits outside the vectors
+  float entropy[2];                               // sum_k p_k log2 p_k
+  int twice[2];                                   // the row may list a class more than once
+  uint32_t seen[1 << (kSeenBits - 5)];            // hashes of the classes of the row being prepared
+  int total[kMaxWarps + 1], bad[kMaxWarps + 1];
+  int abort_flag_pad, abort_flag;
   uint64_t wait_limit;  // right behind the abort flag (wait_limit_slot), 8-byte aligned
-  int total[kDistWarps], bad[kDistWarps];
 };
 static_assert(offsetof(DistillSmem, wait_limit) == offsetof(DistillSmem, abort_flag) + 4 &&
                   offsetof(DistillSmem, wait_limit) % 8 == 0,
@@ -169,12 +234,12 @@ static_assert(offsetof(DistillSmem, wait_limit) == offsetof(DistillSmem, abort_f
 
 }  // namespace
 
-__global__ void __launch_bounds__(kDistThreads) distill_count_kernel(DistillParams p) {
+__global__ void __launch_bounds__(32 * kCountWarps) distill_count_kernel(DistillParams p) {
   griddep_begin();
-  __shared__ int tot[kDistWarps];
+  __shared__ int tot[kCountWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int n = 0, bad = 0;
-  for (int row = blockIdx.x * kDistWarps + warp; row < p.T; row += gridDim.x * kDistWarps) {
+  for (int row = blockIdx.x * kCountWarps + warp; row < p.T; row += gridDim.x * kCountWarps) {
     bool any = false;
     if (!p.targets || __ldg(p.targets + row) != p.ignore) {
       for (int k = lane; k < p.K; k += 32) {
@@ -185,10 +250,7 @@ __global__ void __launch_bounds__(kDistThreads) distill_count_kernel(DistillPara
       }
     }
     any = __any_sync(0xffffffffu, any);
-    if (lane == 0) {
-      p.flags[row] = any;
-      p.kl[row] = 0.f;
-    }
+    if (lane == 0) p.flags[row] = any;
     n += any;
   }
   bad = __any_sync(0xffffffffu, bad);
@@ -196,7 +258,7 @@ __global__ void __launch_bounds__(kDistThreads) distill_count_kernel(DistillPara
   __syncthreads();
   if (threadIdx.x == 0) {
     int N = 0, b = 0;
-    for (int w = 0; w < kDistWarps; ++w) {
+    for (int w = 0; w < kCountWarps; ++w) {
       N += tot[w] & ((1 << 30) - 1);
       b |= tot[w] >> 30;
     }
@@ -205,26 +267,54 @@ __global__ void __launch_bounds__(kDistThreads) distill_count_kernel(DistillPara
   }
 }
 
-// GRAD: write the gradient.  CL: more than one CTA per row.
-template <class T, bool GRAD, bool CL>
-__global__ void __launch_bounds__(kDistThreads, 3) distill_rows_kernel(const DistillParams p) {
+// The rows of one cluster in order, r = first, first + step, ...: next() gives the next eligible
+// one (-1: none left) and calls skip(r) for every other.  Whole warp; flags are read 32 at a time.
+struct RowList {
+  const uint8_t* flags;
+  int64_t at;  // next row to look at
+  int T, step, i = 32;
+  unsigned mask = 0;
+  template <class Skip>
+  __device__ __forceinline__ int next(Skip&& skip) {
+    for (; at < T; at += step, ++i) {
+      if (i == 32) {
+        const int64_t r = at + static_cast<int64_t>(threadIdx.x & 31) * step;
+        mask = __ballot_sync(0xffffffffu, r < T && flags[r]);
+        i = 0;
+      }
+      if ((mask >> i) & 1u) {
+        const int r = static_cast<int>(at);
+        at += step;
+        ++i;
+        return r;
+      }
+      skip(static_cast<int>(at));
+    }
+    return -1;
+  }
+};
+
+// GRAD: write the gradient.
+template <class T, bool GRAD>
+__global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(const DistillParams p) {
   constexpr int W = 16 / sizeof(T);
+  constexpr bool kBf = sizeof(T) == 2;
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_begin();
-  uint4* pieces = reinterpret_cast<uint4*>(smem);
-  DistillSmem& sh = *reinterpret_cast<DistillSmem*>(smem + static_cast<size_t>(kDistWarps) * p.pv * 16);
+  const int NW = p.NW, C = p.C, nthreads = (NW + 1) * 32;
+  uint4* slice = reinterpret_cast<uint4*>(smem);
+  DistillSmem& sh = *reinterpret_cast<DistillSmem*>(smem + static_cast<size_t>(NW) * p.pv * 16);
   int* id_s = reinterpret_cast<int*>(&sh + 1);             // [2][K] ids (-1: no entry), by row parity
   float* p_s = reinterpret_cast<float*>(id_s + 2 * p.K);   // [2][K] p_k
   float* z_s = p_s + 2 * p.K;                              // [2][K] z_{id_k}
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
-  const int C = CL ? p.C : 1;
+  const int rank = static_cast<int>(cluster_rank());
   const int first = blockIdx.x / C, step = gridDim.x / C;
   volatile int* abort_flag = &sh.abort_flag;
 
   // N and the id check
   int n = 0, bad = 0;
-  for (int i = tid; i < p.nparts; i += kDistThreads) {
+  for (int i = tid; i < p.nparts; i += nthreads) {
     const int x = p.parts[i];
     n += x & ((1 << 30) - 1);
     bad |= x >> 30;
@@ -234,16 +324,19 @@ __global__ void __launch_bounds__(kDistThreads, 3) distill_rows_kernel(const Dis
   if (lane == 0) {
     sh.total[warp] = n;
     sh.bad[warp] = bad;
-    mbar_init(smem_u32(&sh.full[warp]), 1);
-    fence_barrier_init();
   }
   if (tid == 0) {
+    mbar_init(smem_u32(&sh.full), 1);
+    mbar_init(smem_u32(&sh.done), NW);
+    for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&sh.swapped[x]), NW + 1);
+    fence_barrier_init();
     sh.abort_flag = 0;
     sh.wait_limit = kTimeoutNs;
   }
-  __syncthreads();
+  cluster_arrive();  // (also: every CTA of the cluster runs before one writes into another)
+  cluster_wait();
   n = bad = 0;
-  for (int w = 0; w < kDistWarps; ++w) {
+  for (int w = 0; w <= NW; ++w) {
     n += sh.total[w];
     bad |= sh.bad[w];
   }
@@ -251,90 +344,265 @@ __global__ void __launch_bounds__(kDistThreads, 3) distill_rows_kernel(const Dis
     if (blockIdx.x == 0 && tid == 0) set_status(p.hdr, VA_ERR_BAD_TARGETS);
     return;
   }
-  if (CL) cluster_barrier();  // every CTA of the cluster runs before one writes into another
 
   const float sl2 = kLog2e / p.temperature;
   const float gmul = p.temperature / static_cast<float>(n), lgm = __log2f(gmul);
   const T* z = static_cast<const T*>(p.z);
   T* grad = static_cast<T*>(p.grad);
-  uint4* piece = pieces + static_cast<size_t>(warp) * p.pv;
-  const uint32_t piece_a = smem_u32(piece), bar = smem_u32(&sh.full[warp]);
 
-  // A row's cut: `head` elements up to its first 16-byte boundary, vectors, the tail; this
-  // warp's piece is the vectors [v0, v0 + nv).
-  struct Cut {
-    int head, body, v0, nv;
-  };
-  auto cut = [&](const T* zr) {
-    Cut c;
+  // A row's cut: `head` elements up to its first 16-byte boundary, `body` vectors, the tail; warp w
+  // of rank r holds the vectors [r NW + w, r NW + w + 1) pv.
+  const auto head_of = [&](const T* zr) {
     const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(zr) & 15u);
-    c.head = min(p.V, static_cast<int>(((16u - mis) & 15u) / sizeof(T)));
-    c.body = (p.V - c.head) / W;  // vectors
-    const int per = (c.body + C * kDistWarps - 1) / (C * kDistWarps);  // <= p.pv
-    c.v0 = min(c.body, (rank * kDistWarps + warp) * per);
-    c.nv = min(c.body, c.v0 + per) - c.v0;
-    return c;
+    return min(p.V, static_cast<int>(((16u - mis) & 15u) / sizeof(T)));
   };
-  uint32_t phase = 0;
-  auto load = [&](int row) {  // whole warp; the piece has been handed out
-    const T* zr = z + row * p.z_rs;
-    const Cut c = cut(zr);
-    if (lane == 0 && c.nv > 0) {
-      mbar_expect_tx(bar, c.nv * 16);
-      bulk_load(piece_a, zr + c.head + static_cast<int64_t>(c.v0) * W, c.nv * 16, bar);
+  bool ok = true;
+  // (max, sum of exp2) of this warp's part of the it-th row, to every CTA of the cluster.  A pair of
+  // row it + 2 may overwrite one of row it: its warp has seen every pair of row it + 1, and a warp
+  // gives that one after it has read those of row it.
+  const auto publish = [&](int it, float m, float s) {
+    __syncwarp();
+    float2* at = &sh.pair[it & 1][rank * (NW + 1) + warp];
+    const uint32_t bar = smem_u32(&sh.swapped[it & 1]);
+    if (lane < C && lane != rank) send_pair(smem_u32(at), bar, lane, m, s);
+    if (lane == rank) {
+      *at = make_float2(m, s);
+      if (warp == NW && C > 1) mbar_expect_tx(bar, (C - 1) * (NW + 1) * 8);  // the other CTAs' pairs
+      else mbar_arrive(bar);
     }
+    __syncwarp();
+  };
+  // the row's (max, log2 of the sum) from every warp's pair
+  const int npairs = C * (NW + 1);
+  const auto merge = [&](int it, float& m, float& ls) {
+    if (ok) ok = wwait(smem_u32(&sh.swapped[it & 1]), (it >> 1) & 1, abort_flag, p.hdr, 62);
+    const float2* pair = sh.pair[it & 1];
+    float mx = -INFINITY;
+    for (int i = lane; i < npairs; i += 32) mx = fmaxf(mx, pair[i].x);
+    m = warp_max(mx);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+    for (int i = lane; i < npairs; i += 32) {
+      const float2 q = pair[i];
+      s += q.x == -INFINITY ? q.y : q.y * fast_exp2((q.x - m0) * sl2);  // (a NaN sum stays NaN)
+    }
+    ls = __log2f(warp_sum(s));
   };
 
-  int row = first;
-  bool have = row < p.T && p.flags[row];
-  if (have) load(row);
-  int par = 0;
-  bool ok = true;
-  for (; row < p.T; row += step) {
-    const int next = row + step;
-    const bool next_have = next < p.T && p.flags[next];
-    const T* zr = z + row * p.z_rs;
-    T* gr = GRAD ? grad + row * p.g_rs : nullptr;
-    const Cut c = cut(zr);
-    const int tail0 = c.head + c.body * W;  // first element of the tail
-    T* gp = GRAD ? gr + c.head + static_cast<int64_t>(c.v0) * W : nullptr;
-    const bool vec = GRAD && (reinterpret_cast<uintptr_t>(gp) & 15u) == 0;
-    // the elements outside the vectors: rank 0's first threads take the head, the next the tail
-    int edge = -1;
-    if (rank == 0 && tid < 2 * W) edge = tid < W ? (tid < c.head ? tid : -1) : (tail0 + tid - W < p.V ? tail0 + tid - W : -1);
-    if (!have) {  // not eligible: no arithmetic on its logits, a zero gradient row
-      if (GRAD) {
-        if (vec) {
-          for (int i = lane; i < c.nv; i += 32) __stcs(reinterpret_cast<uint4*>(gp) + i, make_uint4(0, 0, 0, 0));
-        } else {
-          for (int i = lane; i < c.nv * W; i += 32) gp[i] = from_f<T>(0.f);
-        }
-        if (edge >= 0) gr[edge] = from_f<T>(0.f);
+  RowList rows{p.flags, first, p.T, step};
+  if (warp < NW) {
+    // ------------------------------------------------------------ a piece of every row
+    struct Cut {
+      int c0, nv;  // first element, vectors
+    };
+    const int at_vec = (rank * NW + warp) * p.pv;  // C NW pv >= body
+    const auto cut = [&](const T* zr) {
+      const int head = head_of(zr), body = (p.V - head) / W, v0 = min(body, at_vec);
+      return Cut{head + v0 * W, min(body - v0, p.pv)};
+    };
+    const auto zero = [&](int row) {  // not eligible: no arithmetic on its logits, a zero gradient row
+      if (!GRAD) return;
+      const Cut c = cut(z + row * p.z_rs);
+      T* g = grad + row * p.g_rs + c.c0;
+      if ((reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
+        for (int i = lane; i < c.nv; i += 32) __stcs(reinterpret_cast<uint4*>(g) + i, make_uint4(0, 0, 0, 0));
+      } else {
+        for (int i = lane; i < c.nv * W; i += 32) g[i] = from_f<T>(0.f);
       }
-      if (next_have) load(next);
-      have = next_have;
-      continue;
+    };
+    // warp 0 moves the slice (its own piece is the slice's first one)
+    const auto slice_bytes = [&](const T* zr, const Cut& c) {
+      const int body = (p.V - head_of(zr)) / W;
+      return min(body - min(body, at_vec), NW * p.pv) * 16;
+    };
+    const auto load = [&](int row) {
+      const T* zr = z + row * p.z_rs;
+      const Cut c = cut(zr);
+      const int bytes = slice_bytes(zr, c);
+      if (lane != 0) return;
+      if (bytes > 0) {
+        mbar_expect_tx(smem_u32(&sh.full), bytes);
+        bulk_load(smem_u32(smem), zr + c.c0, bytes, smem_u32(&sh.full));
+      } else {
+        mbar_arrive(smem_u32(&sh.full));
+      }
+    };
+    uint4* piece = slice + static_cast<size_t>(warp) * p.pv;
+    T* cell = reinterpret_cast<T*>(piece);
+    int r0 = rows.next(zero);
+    bool loading = r0 >= 0;
+    if (warp == 0 && r0 >= 0) load(r0);
+    int it = 0;
+    for (; r0 >= 0; ++it) {
+      const int slot = it & 1;
+      const Cut c = cut(z + r0 * p.z_rs);
+      const int c0 = c.c0, c1 = c0 + c.nv * W;
+      if (ok) ok = wwait(smem_u32(&sh.full), it & 1, abort_flag, p.hdr, 60);
+      loading = loading && !ok;
+      VecMax<T> vm;
+      each_vec(piece, c.nv, [&](const uint4& u, int) { vm.add(u); });
+      float m = warp_max(vm.get());
+      {
+        const float m0 = m == -INFINITY ? 0.f : m;
+        float s0 = 0.f, s1 = 0.f;
+        const auto sum = [&](auto one, float b) {
+          each_vec(piece, c.nv, [&](const uint4& u, int) {
+            float x[W];
+            unpack(u, x);
+            exp_row<decltype(one)::value>(x, m0, sl2, b);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) fadd2(s0, s1, s0, s1, x[e], x[e + 1]);
+          });
+        };
+        if (kBf && fabsf(m0 * sl2) < kOneLimit) sum(std::true_type{}, -m0 * sl2);
+        else sum(std::false_type{}, 0.f);
+        publish(it, m, warp_sum(s0 + s1));
+      }
+      const int r1 = rows.next(zero);
+      float ls;
+      merge(it, m, ls);
+      // the logits of the listed classes of this piece
+      const int* ids = id_s + slot * p.K;
+      const float* pk = p_s + slot * p.K;
+      float* zk = z_s + slot * p.K;
+      unsigned hits = 0;  // this lane's entries (lane + 32 u) whose class is in the piece
+      for (int k = lane, u = 0; k < p.K; k += 32, ++u) {
+        const int id = ids[k];
+        if (id < c0 || id >= c1) continue;
+        hits |= 1u << u;
+        zk[k] = to_f(cell[id - c0]);
+      }
+      if (GRAD) {
+        // tau / N (q_c - P_c), P_c the teacher's weight on class c: the piece first gets the q part,
+        // then its teacher entries are written over
+        __syncwarp();
+        const float off = lgm - ls;
+        const auto fill = [&](auto one, float b) {
+          each_vec(piece, c.nv, [&](const uint4& u, int i) {
+            float x[W];
+            unpack(u, x);
+            exp_row<decltype(one)::value>(x, m, sl2, b);
+            piece[i] = pack(x);
+          });
+        };
+        if (kBf && fabsf(m * sl2) < kOneLimit) fill(std::true_type{}, off - m * sl2);
+        else fill(std::false_type{}, off);
+        // A class may be listed twice: where the row's hashes say so, each entry first leaves its
+        // number in its cell; one that finds another number there shares the class, and then every
+        // entry sums over its equals.
+        using Raw = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+        const auto each_hit = [&](auto&& f) {
+          for (unsigned h = hits; h; h &= h - 1) f(lane + 32 * (__ffs(h) - 1));
+        };
+        __syncwarp();
+        bool twice = sh.twice[slot] != 0;
+        if (twice) {
+          each_hit([&](int k) { reinterpret_cast<Raw*>(cell)[ids[k] - c0] = static_cast<Raw>(k); });
+          __syncwarp();
+          twice = false;
+          each_hit([&](int k) { twice |= reinterpret_cast<Raw*>(cell)[ids[k] - c0] != static_cast<Raw>(k); });
+          twice = __any_sync(0xffffffffu, twice);
+        }
+        each_hit([&](int k) {
+          const int id = ids[k];
+          float P = pk[k];
+          if (twice) {
+            P = 0.f;
+            for (int k2 = 0; k2 < p.K; ++k2) P += ids[k2] == id ? pk[k2] : 0.f;
+          }
+          cell[id - c0] = from_f<T>(fast_exp2(fmaf(zk[k] - m, sl2, off)) - P * gmul);
+        });
+        T* g = grad + r0 * p.g_rs + c0;
+        if ((reinterpret_cast<uintptr_t>(g) & 15u) != 0) {  // on another 16-byte phase than the logits
+          __syncwarp();
+          for (int i = lane; i < c.nv * W; i += 32) g[i] = cell[i];
+        }
+      }
+      fence_proxy_async_smem();  // the accesses above come before the copies below
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.done));
+      if (warp == 0) {
+        if (ok) ok = wwait(smem_u32(&sh.done), it & 1, abort_flag, p.hdr, 61);
+        const T* zr = z + r0 * p.z_rs;
+        T* g = GRAD ? grad + r0 * p.g_rs + c0 : nullptr;
+        if (GRAD && ok && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
+          const int bytes = slice_bytes(zr, c);
+          if (lane == 0 && bytes > 0) {
+            bulk_store(g, smem_u32(smem), bytes);
+            tma_store_commit();
+            tma_store_wait_read();
+          }
+          __syncwarp();
+        }
+        if (r1 >= 0 && ok) {
+          load(r1);
+          loading = true;
+        }
+      }
+      r0 = r1;
     }
-    int* ids = id_s + par * p.K;
-    float* pk = p_s + par * p.K;
-    float* zk = z_s + par * p.K;
-    if (warp == kDistWarps - 1) {  // the teacher's entries, while the pieces arrive
+    if (warp == 0 && lane == 0) {
+      tma_store_wait_all();
+      const uint64_t t0 = globaltimer();  // a wait gave up: let the copy under way land (bounded again)
+      while (!ok && loading && !mbar_try_wait(smem_u32(&sh.full), (it + 1) & 1) && globaltimer() - t0 < 50000000ull) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ the teacher's entries, the edges
+    const auto edge_of = [&](const T* zr) {  // this lane's element (rank 0), or -1
+      const int head = head_of(zr), tail = head + (p.V - head) / W * W;
+      if (rank != 0 || lane >= 2 * W) return -1;
+      const int e = lane < W ? lane : tail + lane - W;
+      return lane < W ? (e < head ? e : -1) : (e < p.V ? e : -1);
+    };
+    const auto zero = [&](int row) {
+      const int e = GRAD ? edge_of(z + row * p.z_rs) : -1;
+      if (e >= 0) grad[row * p.g_rs + e] = from_f<T>(0.f);
+    };
+    // A row's first entries and its edge element, loaded a row before teach() takes them.
+    constexpr int kAhead = 4;
+    int fid[kAhead];
+    float fa[kAhead], fe = -INFINITY;
+    const auto fetch = [&](int row) {
+      const T* zr = z + row * p.z_rs;
+      const int e = edge_of(zr);
+      fe = e >= 0 ? to_f(zr[e]) : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = lane + 32 * u;
+        fid[u] = k < p.K ? __ldg(p.ids + row * p.ids_rs + k) : -1;
+        fa[u] = k < p.K ? teacher(p, row, k) : -INFINITY;
+      }
+    };
+    const auto teach = [&](int row, int slot) {
+      int* ids = id_s + slot * p.K;
+      float* pk = p_s + slot * p.K;
+      if (lane < kEdge) sh.edge[slot][lane] = fe;
+      const auto hash = [](int id) { return (static_cast<uint32_t>(id) * 2654435761u) >> (32 - kSeenBits); };
       float mx = -INFINITY;
-      for (int k = lane; k < p.K; k += 32) {
-        const int id = __ldg(p.ids + row * p.ids_rs + k);
-        const float a = teacher(p, row, k);
+      bool twice = false;  // one hash seen twice: perhaps a class listed twice
+      const auto take = [&](int k, int id, float a) {
         const bool in = id >= 0 && a > -INFINITY;
         ids[k] = in ? id : -1;
         pk[k] = in ? a : -INFINITY;
-        zk[k] = in ? to_f(zr[id]) : 0.f;
         mx = fmaxf(mx, in ? a : -INFINITY);
-      }
+        const uint32_t h = hash(id), bit = 1u << (h & 31);
+        if (in) twice |= (atomicOr(&sh.seen[h >> 5], bit) & bit) != 0;
+      };
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int u = 0; u < kAhead; ++u)
+        if (lane + 32 * u < p.K) take(lane + 32 * u, fid[u], fa[u]);
+#pragma unroll 4
+      for (int k = lane + 32 * kAhead; k < p.K; k += 32) take(k, __ldg(p.ids + row * p.ids_rs + k), teacher(p, row, k));
+      mx = warp_max(mx);
+      twice = __any_sync(0xffffffffu, twice);
       float s = 0.f;
-      for (int k = lane; k < p.K; k += 32) s += ids[k] >= 0 ? fast_exp2((pk[k] - mx) * sl2) : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      for (int k = lane; k < p.K; k += 32) {
+        if (ids[k] < 0) continue;
+        s += fast_exp2((pk[k] - mx) * sl2);
+        sh.seen[hash(ids[k]) >> 5] = 0;
+      }
+      s = warp_sum(s);
       const float ls = __log2f(s), inv = 1.f / s;
       float ent = 0.f;
       for (int k = lane; k < p.K; k += 32) {
@@ -342,136 +610,73 @@ __global__ void __launch_bounds__(kDistThreads, 3) distill_rows_kernel(const Dis
         pk[k] = pr;
         if (pr != 0.f) ent += pr * (x - ls);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ent += __shfl_xor_sync(0xffffffffu, ent, o);
-      if (lane == 0) sh.entropy[par] = ent;
-    }
-    // (max, sum of exp2) of this warp's piece and of the row's edge elements
-    const float ze = edge >= 0 ? to_f(zr[edge]) : -INFINITY;
-    if (c.nv > 0) {
-      if (ok) ok = wwait(bar, phase, abort_flag, p.hdr, 60);
-      phase ^= 1;
-    }
-    float m = ze == ze ? ze : -INFINITY;  // (a NaN reaches the sum)
-    for (int i = lane; i < c.nv; i += 32) {
-      float x[W];
-      unpack(piece[i], x);
-#pragma unroll
-      for (int e = 0; e < W; ++e) m = fmaxf(m, x[e]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = 0.f;
-    const float m0 = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < c.nv; i += 32) {
-      float x[W];
-      unpack(piece[i], x);
-      exp_row(x, m0, sl2, 0.f);
-#pragma unroll
-      for (int e = 0; e < W; ++e) s += x[e];
-    }
-    if (edge >= 0) s += fast_exp2((ze - m0) * sl2);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sh.red[par][warp] = make_float2(m, s);
-    __syncthreads();
-    m = sh.red[par][0].x;
-    s = sh.red[par][0].y;
-#pragma unroll
-    for (int w = 1; w < kDistWarps; ++w) ms_merge(m, s, sh.red[par][w].x, sh.red[par][w].y, sl2);
-    if (CL) {
-      if (tid < C) store_remote2(smem_u32(&sh.cred[par][rank]), tid, m, s);
-      cluster_barrier();
-      m = sh.cred[par][0].x;
-      s = sh.cred[par][0].y;
-      for (int r = 1; r < C; ++r) ms_merge(m, s, sh.cred[par][r].x, sh.cred[par][r].y, sl2);
-    }
-    const float ls2 = __log2f(s);
-    if (rank == 0 && warp == 0) {  // the row loss: sum_k p_k (ln p_k - (z_k - max) / tau + ln s)
-      float cross = 0.f;
-      for (int k = lane; k < p.K; k += 32)
-        if (pk[k] != 0.f) cross += pk[k] * ((zk[k] - m) / p.temperature);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, o);
-      if (lane == 0) p.kl[row] = p.temperature * p.temperature * ((sh.entropy[par] + ls2) * kLn2 - cross);
-    }
-    if (GRAD) {
-      // gradient tau / N (q_c - P_c), P_c the teacher's weight on class c; the piece first gets
-      // the q part, then its teacher entries are written over
-      const float b = lgm - ls2;
-      for (int i = lane; i < c.nv; i += 32) {
-        float x[W];
-        unpack(piece[i], x);
-        exp_row(x, m, sl2, b);
-        piece[i] = pack(x);
-      }
-      if (edge >= 0) {
-        float P = 0.f;
-        for (int k = 0; k < p.K; ++k) P += ids[k] == edge ? pk[k] : 0.f;
-        gr[edge] = from_f<T>(fast_exp2(fmaf(ze - m, sl2, b)) - P * gmul);
-      }
-      // A class may be listed twice: each entry first leaves its number in its cell; one that finds
-      // another number there shares the class, and then every entry sums over its equals.
-      T* cell = reinterpret_cast<T*>(piece);
-      const int c0 = c.head + c.v0 * W, c1 = c0 + c.nv * W;
-      using Raw = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
-      __syncwarp();
-      for (int k = lane; k < p.K; k += 32) {
-        const int id = ids[k];
-        if (id >= c0 && id < c1) reinterpret_cast<Raw*>(cell)[id - c0] = static_cast<Raw>(k);
+      ent = warp_sum(ent);
+      if (lane == 0) {
+        sh.twice[slot] = twice;
+        sh.entropy[slot] = ent;
       }
       __syncwarp();
-      bool twice = false;
-      for (int k = lane; k < p.K; k += 32) {
-        const int id = ids[k];
-        if (id >= c0 && id < c1) twice |= reinterpret_cast<Raw*>(cell)[id - c0] != static_cast<Raw>(k);
-      }
-      twice = __any_sync(0xffffffffu, twice);
-      for (int k = lane; k < p.K; k += 32) {
-        const int id = ids[k];
-        if (id < c0 || id >= c1) continue;
-        float P = pk[k];
-        if (twice) {
-          P = 0.f;
-          for (int k2 = 0; k2 < p.K; ++k2) P += ids[k2] == id ? pk[k2] : 0.f;
-        }
-        cell[id - c0] = from_f<T>(fast_exp2(fmaf(zk[k] - m, sl2, b)) - P * gmul);
-      }
-      if (vec) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && c.nv > 0 && ok) {
-          bulk_store(gp, piece_a, c.nv * 16);
-          tma_store_commit();
-          tma_store_wait_read();
-        }
-      } else {
-        __syncwarp();
-        for (int i = lane; i < c.nv * W; i += 32) gp[i] = cell[i];
-        fence_proxy_async_smem();  // the reads above come before the next bulk load's writes
-      }
-    } else {
-      fence_proxy_async_smem();
-    }
+    };
+    for (int i = lane; i < (1 << (kSeenBits - 5)); i += 32) sh.seen[i] = 0;
     __syncwarp();
-    if (next_have && ok) load(next);
-    have = next_have;
-    par ^= 1;
-  }
-  tma_store_wait_all();
-  if (!ok && lane == 0) {  // a wait gave up: let this warp's own copy land (bounded again)
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, phase ^ 1) && globaltimer() - t0 < 50000000ull) {
+    const float t2 = p.temperature * p.temperature, tau = p.temperature;
+    double loss = 0.0;  // lane 0: this CTA's part of its rows' losses, in row order
+    int r0 = rows.next(zero), r1 = -1;
+    if (r0 >= 0) {
+      fetch(r0);
+      teach(r0, 0);
+      r1 = rows.next(zero);
+      if (r1 >= 0) fetch(r1);
     }
+    for (int it = 0; r0 >= 0; ++it) {
+      const int slot = it & 1;
+      const int* ids = id_s + slot * p.K;
+      const float *pk = p_s + slot * p.K, *zk = z_s + slot * p.K;
+      const float x = lane < kEdge ? sh.edge[slot][lane] : -INFINITY;
+      float m = warp_max(x), ls;
+      const float m0 = m == -INFINITY ? 0.f : m;
+      publish(it, m, warp_sum(lane < kEdge ? fast_exp2((x - m0) * sl2) : 0.f));
+      int r2 = -1;
+      if (r1 >= 0) {
+        teach(r1, slot ^ 1);
+        r2 = rows.next(zero);
+        if (r2 >= 0) fetch(r2);
+      }
+      merge(it, m, ls);
+      // The row loss tau^2 sum_k p_k (ln p_k - (z_k - max) / tau + ln s): rank 0 has the first and last
+      // term and the edges' classes, every CTA adds the classes of its slice
+      const T* zr = z + r0 * p.z_rs;
+      const int e = edge_of(zr);
+      float cross = 0.f;
+      if (e >= 0) {
+        float P = 0.f;
+        for (int k = 0; k < p.K; ++k) P += ids[k] == e ? pk[k] : 0.f;
+        if (P != 0.f) cross = P * (x - m);
+        if (GRAD) grad[r0 * p.g_rs + e] = from_f<T>(fast_exp2(fmaf(x - m, sl2, lgm - ls)) - P * gmul);
+      }
+      const int head = head_of(zr), body = (p.V - head) / W;
+      const int s0 = head + min(body, rank * NW * p.pv) * W, s1 = head + min(body, (rank + 1) * NW * p.pv) * W;
+      if (ok) ok = wwait(smem_u32(&sh.done), it & 1, abort_flag, p.hdr, 61);  // zk is there
+      for (int k = lane; k < p.K; k += 32)
+        if (ids[k] >= s0 && ids[k] < s1 && pk[k] != 0.f) cross += pk[k] * (zk[k] - m);
+      cross = warp_sum(cross);
+      if (lane == 0) loss += t2 * ((rank == 0 ? (sh.entropy[slot] + ls) * kLn2 : 0.f) - cross / tau);
+      r0 = r1;
+      r1 = r2;
+    }
+    if (lane == 0) p.sums[blockIdx.x] = loss;
   }
+  cluster_arrive();  // no CTA leaves while another one may still write into it
+  cluster_wait();
 }
 
 __global__ void __launch_bounds__(kReduceThreads) distill_reduce_kernel(DistillParams p) {
   griddep_begin();
   __shared__ double part[kReduceThreads / 32];
   __shared__ int tot[kReduceThreads / 32];
-  double acc = 0.0;  // fixed assignment of rows to threads and a fixed reduction order
-  for (int t = threadIdx.x; t < p.T; t += kReduceThreads) acc += static_cast<double>(p.kl[t]);
+  double acc = 0.0;  // fixed assignment of rows to CTAs, of those to threads, and a fixed order
+  if (p.hdr->status == VA_OK)
+    for (int t = threadIdx.x; t < p.ctas; t += kReduceThreads) acc += p.sums[t];
   int n = 0;
   for (int i = threadIdx.x; i < p.nparts; i += kReduceThreads) n += p.parts[i] & ((1 << 30) - 1);
 #pragma unroll
@@ -500,34 +705,33 @@ __global__ void __launch_bounds__(kReduceThreads) distill_reduce_kernel(DistillP
 
 namespace {
 
-int count_blocks(int T) { return std::min(kMaxParts, (T + kDistWarps - 1) / kDistWarps); }
+int count_blocks(int T) { return std::min(kMaxParts, (T + kCountWarps - 1) / kCountWarps); }
 
-template <class T, bool GRAD, bool CL>
+template <class T, bool GRAD>
 cudaError_t launch_rows_t(const DistillParams& p, int grid, size_t smem, cudaStream_t st) {
-  const auto kernel = distill_rows_kernel<T, GRAD, CL>;
+  const auto kernel = distill_rows_kernel<T, GRAD>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kDistThreads);
+  cfg.blockDim = dim3((p.NW + 1) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CL ? p.C : 1;
+  attr[1].val.clusterDim.x = p.C;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CL ? 2 : 1;
+  cfg.numAttrs = p.C > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <class T>
 cudaError_t launch_rows(const DistillParams& p, int grid, size_t smem, cudaStream_t st) {
-  if (p.C > 1) return p.grad ? launch_rows_t<T, true, true>(p, grid, smem, st) : launch_rows_t<T, false, true>(p, grid, smem, st);
-  return p.grad ? launch_rows_t<T, true, false>(p, grid, smem, st) : launch_rows_t<T, false, false>(p, grid, smem, st);
+  return p.grad ? launch_rows_t<T, true>(p, grid, smem, st) : launch_rows_t<T, false>(p, grid, smem, st);
 }
 
 }  // namespace
@@ -537,34 +741,38 @@ bool distill_row_fits(int V, int elem) {
   return static_cast<int64_t>(V) * elem <= static_cast<int64_t>(kMaxSlice) * kMaxCluster;
 }
 
-size_t distill_parts_bytes() { return kMaxParts * sizeof(int32_t); }
+size_t distill_parts_bytes() { return kMaxParts * sizeof(int32_t) + kMaxCtas * sizeof(double); }
 
 // The three launches of varlen_token_distill, in this order on one stream.
 cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_rs, const int32_t* ids, int64_t ids_rs,
                                  const void* a, int a_bf16, int64_t a_rs, const int32_t* targets, int T, int V, int K,
                                  int ignore, float temperature, void* grad, int64_t g_rs, void* hdr, int32_t* parts,
-                                 uint8_t* flags, float* kl, float* loss, int32_t* count, cudaStream_t st) {
+                                 uint8_t* flags, float* loss, int32_t* count, cudaStream_t st) {
   DistillParams p{z, z_rs, ids, ids_rs, a, a_rs, a_bf16, targets, T, V, K, ignore, temperature, grad, g_rs,
-                  static_cast<WsHeader*>(hdr), parts, count_blocks(T), flags, kl, loss, count, 0, 1};
-  if (stage == 0) return launch_pdl(distill_count_kernel, dim3(p.nparts), dim3(kDistThreads), 0, st, p);
-  if (stage == 2) return launch_pdl(distill_reduce_kernel, dim3(1), dim3(kReduceThreads), 0, st, p);
+                  static_cast<WsHeader*>(hdr), parts, count_blocks(T), flags,
+                  reinterpret_cast<double*>(parts + kMaxParts), 0, loss, count, 0, 1, kMaxWarps};
+  if (stage == 0) return launch_pdl(distill_count_kernel, dim3(p.nparts), dim3(32 * kCountWarps), 0, st, p);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int elem = bf16 ? 2 : 4;
-  // CTAs per row: the fewest whose slices leave room for three CTAs on an SM (loads, arithmetic
-  // and stores of different rows overlap), more while the rows alone leave SMs idle.
-  const int64_t bytes = static_cast<int64_t>(V) * elem;
+  const int64_t bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
   const auto slice = [&](int C) { return (bytes + C - 1) / C; };
-  while (p.C < kMaxCluster && slice(p.C) > (68 << 10)) p.C *= 2;
-  while (p.C < kMaxCluster && static_cast<int64_t>(T) * p.C < 2 * sms && slice(p.C) > (8 << 10)) p.C *= 2;
+  const size_t fixed = sizeof(DistillSmem) + static_cast<size_t>(K) * 24 + 1024;
+  // CTAs per row: the fewest whose slice fits an SM twice (T = 2047, V = 50003 fp32: 145 us with two
+  // CTAs of 100 KB, 193 with four of 50 KB that fit three times), more while the rows alone leave
+  // SMs idle.  Working warps: 2 KB of the slice and more each.
+  while (p.C < kMaxCluster && slice(p.C) + 16 * kMaxWarps + fixed > kSmemBytes / 2) p.C *= 2;
+  while (p.C < kMaxCluster && static_cast<int64_t>(T) * p.C * 2 <= sms && slice(p.C) > (8 << 10)) p.C *= 2;
+  while (p.NW > 1 && slice(p.C) <= static_cast<int64_t>(p.NW) * 2048) p.NW /= 2;
   const int64_t body = bytes / 16;
-  p.pv = static_cast<int>((body + p.C * kDistWarps - 1) / (p.C * kDistWarps));
-  const size_t smem = static_cast<size_t>(kDistWarps) * p.pv * 16 + sizeof(DistillSmem) + static_cast<size_t>(K) * 24;
-  const int per_sm = std::max<int>(1, std::min<int>(3, (227 << 10) / static_cast<int>(smem + 1024)));
-  const int clusters = std::max(1, std::min(T, sms * per_sm / p.C));
-  return bf16 ? launch_rows<__nv_bfloat16>(p, clusters * p.C, smem, st) : launch_rows<float>(p, clusters * p.C, smem, st);
+  p.pv = static_cast<int>((body + p.C * p.NW - 1) / (p.C * p.NW));
+  const size_t smem = static_cast<size_t>(p.NW) * p.pv * 16 + fixed - 1024;
+  const int per_sm = std::max<int>(1, std::min<int>(27 / (p.NW + 1), kSmemBytes / static_cast<int>(smem + 1024)));
+  const int clusters = std::max(1, std::min(std::min(T, kMaxCtas / p.C), sms * per_sm / p.C));
+  p.ctas = clusters * p.C;
+  if (stage == 2) return launch_pdl(distill_reduce_kernel, dim3(1), dim3(kReduceThreads), 0, st, p);
+  return bf16 ? launch_rows<__nv_bfloat16>(p, p.ctas, smem, st) : launch_rows<float>(p, p.ctas, smem, st);
 }
 
 }  // namespace va

@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld32(s_addr + b * 64, sv);
         tmem_ld32(dp_addr + b * 64, dpv);
         tmem_wait_ld();
+        const uint32_t vis = WIN ? bits_below(hi) & ~bits_below(lim) : 0u;  // (window) the visible columns
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(L + c);
@@ -598,8 +599,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const float x0 = fmaf(__uint_as_float(sv[j]), sl2, la), x1 = fmaf(__uint_as_float(sv[j + 1]), sl2, lb);
             float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             if (need_mask) {
-              if (j < lim || (WIN && j >= hi)) p0 = 0.f;
-              if (j + 1 < lim || (WIN && j + 1 >= hi)) p1 = 0.f;
+              if (WIN ? !(vis & (1u << j)) : j < lim) p0 = 0.f;
+              if (WIN ? !(vis & (2u << j)) : j + 1 < lim) p1 = 0.f;
             }
             const float t0 = __uint_as_float(dpv[j]) + da, t1 = __uint_as_float(dpv[j + 1]) + db;
             sv[j >> 1] = pack_bf16(p0, p1);
@@ -1182,7 +1183,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // (window) key columns c < lo too: before the query's window
         const int kn = (WIN ? key_row<WIN>(I, n) - I.s0 : n * 64) + cw;  // this warpgroup's first key, segment-local
         int lim = p.causal ? qrow - kn : I.l - 1 - kn;
-        const int lo = WIN ? qrow - p.window - kn : 0, sk = WIN == kWinSinks ? p.sinks - kn : 0;  // (but not the sinks)
+        // (but not the sinks); vis: the visible columns
+        const uint32_t vis =
+            WIN ? (~bits_below(qrow - p.window - kn) | (WIN == kWinSinks ? bits_below(p.sinks - kn) : 0u)) &
+                      bits_below(lim + 1)
+                : 0u;
         bool need_mask = p.causal ? (kn + 31 > I.m * 128 || (WIN && kn < I.m * 128 + 127 - p.window &&
                                                           (WIN != kWinSinks || kn + 32 > p.sinks)))
                                   : (kn + 32 > I.l);
@@ -1201,8 +1206,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ffma2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2, -lse2, -lse2);
           float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
           if (need_mask) {
-            if (c > lim || (WIN && c < lo && c >= sk)) p0 = 0.f;
-            if (c + 1 > lim || (WIN && c + 1 < lo && c + 1 >= sk)) p1 = 0.f;
+            if (WIN ? !(vis & (1u << c)) : c > lim) p0 = 0.f;
+            if (WIN ? !(vis & (2u << c)) : c + 1 > lim) p1 = 0.f;
           }
           float t0, t1;
           fadd2(t0, t1, __uint_as_float(dpv[c]), __uint_as_float(dpv[c + 1]), -dsum, -dsum);

@@ -99,6 +99,13 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// The bits below bit n of a word, n <= 0 none and n >= 32 all (the shift clamps at 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t x;
+  asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(x) : "r"(max(n, 0)));
+  return ~x;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -45,6 +45,7 @@ constexpr int kLaunchRegs = 168;
 constexpr int kRegsCtl = 80, kRegsSoftmax = 208;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= kTcThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kNarrow = 32;                 // columns of a sink step that holds few sinks
 
 template <int D>
 struct TcCfg {
@@ -71,7 +72,9 @@ struct Item {
   int valid;
   int kb;  // local window: the item's step n takes key tile kb + n (kWinSinks: from step ns on)
   int s0k, lk, off;  // cross-attention: the keys' first row and count, the causal offset lk - l
-  int ns;  // sinks: the first ns steps take the segment's key tiles 0 .. ns - 1
+  short ns;    // sinks: the first ns steps take the segment's key tiles 0 .. ns - 1
+  short nar;   // the step whose tile holds at most kNarrow sinks and nothing else visible, or -1
+  int skip1;   // window: the step that q tile 1 does not take (its window starts later), or -1
 };
 static_assert(sizeof(Item) <= 64, "queue slots are 64 bytes");
 
@@ -89,8 +92,17 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
   r.nb0 = (p.causal && r.t1) ? r.nb - 1 : r.nb;
   if (WIN) r.kb = max(0, r.m * kTcBM - p.window) / kTcBN;
   if (WIN == kWinSinks) {  // the sink tiles that the window does not reach come first
-    r.ns = min(r.kb, (min(r.l, p.sinks) + kTcBN - 1) / kTcBN);
+    const int s = min(r.l, p.sinks);
+    r.ns = static_cast<short>(min(r.kb, (s + kTcBN - 1) / kTcBN));
+    // the last of them, when it is the tile that the sinks end in, after at most kNarrow columns
+    const int in_last = s - (r.ns - 1) * kTcBN;
+    r.nar = static_cast<short>(r.ns > 0 && in_last <= kNarrow ? r.ns - 1 : -1);
     r.kb -= r.ns;
+  }
+  if (WIN) {
+    // q tile 1's rows start 128 later: the item's first window tile may end before its window
+    const int first = WIN == kWinSinks ? r.ns : 0, end = (r.kb + first + 1) * kTcBN;
+    r.skip1 = r.t1 && end <= r.m * kTcBM + 128 - p.window && (WIN != kWinSinks || end - kTcBN >= p.sinks) ? first : -1;
   }
   if (X) {  // keys from cu_k; q tile 0 may share its diagonal key tile with tile 1
     r.s0k = p.cu_k[it.seg];
@@ -108,12 +120,21 @@ __device__ __forceinline__ int key_tile(const Item& I, int n) {
 }
 
 // Masks columns j < lo (but not the sinks j < sk) and j > lim, and returns the row max x sl2
-// (local window: the left edge of the row's window and its diagonal).
+// (local window: the left edge of the row's window and its diagonal).  The conditions are formed
+// once per 32 columns as a word of visible bits; groups that every row of the warp sees whole are
+// left alone.
 template <bool SINKS>
 __device__ __forceinline__ float row_max2(uint32_t* v, int sk, int lo, int lim, float sl2) {
 #pragma unroll
-  for (int j = 0; j < 128; ++j)
-    if ((j < lo && (!SINKS || j >= sk)) || j > lim) v[j] = __float_as_uint(-INFINITY);
+  for (int c = 0; c < 4; ++c) {
+    uint32_t vis = ~bits_below(lo - 32 * c);
+    if (SINKS) vis |= bits_below(sk - 32 * c);
+    vis &= bits_below(lim + 1 - 32 * c);
+    if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!(vis & (1u << j))) v[32 * c + j] = __float_as_uint(-INFINITY);
+  }
   float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -159,11 +180,25 @@ __device__ __forceinline__ float row_max(uint32_t* v, int lim, float sl2) {
   return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
 }
 
-// p = exp2(s * sl2 - mu) packed in place as bf16 pairs into v[0..63]; returns the row sum.
+// Keeps the first sk of kNarrow columns and returns their max x sl2.
+__device__ __forceinline__ float row_max_narrow(uint32_t* v, int sk, float sl2) {
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kNarrow; j += 2) {
+    if (j >= sk) v[j] = __float_as_uint(-INFINITY);
+    if (j + 1 >= sk) v[j + 1] = __float_as_uint(-INFINITY);
+    m0 = fmaxf(m0, __uint_as_float(v[j]));
+    m1 = fmaxf(m1, __uint_as_float(v[j + 1]));
+  }
+  return fmaxf(m0, m1) * sl2;
+}
+
+// p = exp2(s * sl2 - mu) of N columns packed in place as bf16 pairs; returns the row sum.
+template <int N>
 __device__ __forceinline__ float row_exp(uint32_t* v, float sl2, float mu) {
   float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
 #pragma unroll
-  for (int j = 0; j < 64; ++j) {
+  for (int j = 0; j < N / 2; ++j) {
     float x0, x1;
     ffma2(x0, x1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sl2, sl2, -mu, -mu);
     const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
@@ -308,21 +343,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t qlo[2] = {sdesc_lo(base + C::Q_OFF, 16), sdesc_lo(base + C::Q_OFF + C::TILE, 16)};
       const uint32_t klo0 = sdesc_lo(base + C::KV_OFF, 16);
       const uint32_t vlo0 = sdesc_lo(base + C::KV_OFF, C::PANEL);
-      auto issue_S = [&](int t, int slot) {
+      // nar: the narrow sink step (32 columns of S, 32 rows of V)
+      constexpr uint32_t idN = idesc_bf16(128, kNarrow, false, false);
+      auto issue_S = [&](int t, int slot, bool nar) {
         const uint32_t qd = qlo[t], kd = klo0 + ((slot * C::TILE) >> 4);
+        const uint32_t id = WIN == kWinSinks && nar ? idN : idS;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::PANEL + (kk & 3) * 32) >> 4;
-          mma_ss_w(tmem + t * 128, qd + off, kd + off, idS, kk > 0);
+          mma_ss_w(tmem + t * 128, qd + off, kd + off, id, kk > 0);
         }
         mma_commit_w(bar(C::B_SF + t));
       };
-      auto issue_PV = [&](int t, int slot, bool acc) {
+      auto issue_PV = [&](int t, int slot, bool acc, bool nar) {
         const uint32_t vd = vlo0 + ((slot * C::TILE) >> 4);
         const uint32_t d_tm = tmem + 256 + t * C::OCOLS, p_tm = tmem + t * 128;
 #pragma unroll
-        for (int kk = 0; kk < kTcBN / 16; ++kk)
+        for (int kk = 0; kk < kTcBN / 16; ++kk) {
+          if (WIN == kWinSinks && nar && kk >= kNarrow / 16) break;
           mma_ts_w(d_tm, p_tm + kk * 8, vd + kk * (2048 >> 4), idPV, (acc || kk > 0) ? 1u : 0u);
+        }
         mma_commit_w(bar(C::B_OF + t));
       };
       for (;; ++item_cnt) {
@@ -342,13 +382,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         fence_after_sync();
         ++kv_it;
-        issue_S(0, ks);
+        issue_S(0, ks, I.nar == 0);
         if (I.nb0 == 1) {
           mma_commit_w(bar(C::B_QE + 0));  // last S_0 of the item: Q tile 0 may be reloaded
           ++qcnt[0];
         }
         if (I.t1) {
-          issue_S(1, ks);
+          if (!WIN || I.skip1 != 0) issue_S(1, ks, I.nar == 0);
           if (I.nb == 1) {
             mma_commit_w(bar(C::B_QE + 1));
             ++qcnt[1];
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             ++pf[0];
             fence_after_sync();
-            issue_PV(0, vs, n > 0);
+            issue_PV(0, vs, n > 0, n == I.nar);
           }
           int ks2 = -1;
           if (n + 1 < I.nb) {
@@ -375,24 +415,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++kv_it;
             fence_after_sync();
             if (n + 1 < I.nb0) {
-              issue_S(0, ks2);
+              issue_S(0, ks2, n + 1 == I.nar);
               if (n + 1 == I.nb0 - 1) {
                 mma_commit_w(bar(C::B_QE + 0));
                 ++qcnt[0];
               }
             }
           }
-          if (I.t1) {
+          if (I.t1 && (!WIN || n != I.skip1)) {
             ok = wwait(bar(C::B_PF + 1), pf[1] & 1, abort_flag, p.hdr, 8);
             if (!ok) break;
             ++pf[1];
             fence_after_sync();
-            issue_PV(1, vs, n > 0);
+            issue_PV(1, vs, n > (WIN && I.skip1 == 0 ? 1 : 0), n == I.nar);
           }
           mma_commit_w(bar(C::B_KVE + vs));
           if (ks2 >= 0) {
-            if (I.t1) {
-              issue_S(1, ks2);
+            if (I.t1 && (!WIN || n + 1 != I.skip1)) {
+              issue_S(1, ks2, n + 1 == I.nar);
               if (n + 1 == I.nb - 1) {
                 mma_commit_w(bar(C::B_QE + 1));
                 ++qcnt[1];
@@ -433,7 +473,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int nbt = t == 0 ? I.nb0 : I.nb;
       const int qrow = I.m * kTcBM + t * 128 + r;
       float m_ref = -INFINITY, lsum = 0.f;
+      int taken = 0;  // steps so far: all but the one that tile 1 skips
       for (int n = 0; n < nbt; ++n) {
+        if (WIN && t == 1 && n == I.skip1) continue;
         ok = mbar_wait(bar(C::B_SF + t), sf & 1, abort_flag, p.hdr, 9);
         if (!__all_sync(0xffffffffu, ok)) {  // TMEM loads below are warp-collective
           ok = false;
@@ -454,19 +496,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The reference max m_ref is raised only when the row max grew by more than 2^8
         // (rare); O_t, which holds PV_{n-1}, is then rescaled in TMEM first.
         uint32_t v[128];
-        row_load(s_addr, v);
         float mt;
-        if constexpr (WIN != kWinNone) {  // keys before qrow - w are outside the window, unless sinks
-          constexpr bool SINKS = WIN == kWinSinks;
-          const int ka = key_tile<WIN>(I, n) * kTcBN;
-          const bool need_w =
-              ka < I.m * kTcBM + t * 128 + 127 - p.window && (!SINKS || ka + kTcBN > p.sinks);
-          mt = (need_mask || need_w) ? row_max2<SINKS>(v, p.sinks - ka, qrow - p.window - ka, lim, sl2)
-                                     : row_max<false>(v, lim, sl2);
+        if (WIN == kWinSinks && n == I.nar) {  // few sinks, all visible: the first kNarrow columns
+          tmem_ld32(s_addr, v);
+          tmem_wait_ld();
+          mt = row_max_narrow(v, p.sinks - n * kTcBN, sl2);
         } else {
-          mt = need_mask ? row_max<true>(v, lim, sl2) : row_max<false>(v, lim, sl2);
+          row_load(s_addr, v);
+          if constexpr (WIN != kWinNone) {  // keys before qrow - w are outside the window, unless sinks
+            constexpr bool SINKS = WIN == kWinSinks;
+            const int ka = key_tile<WIN>(I, n) * kTcBN;
+            const bool need_w =
+                ka < I.m * kTcBM + t * 128 + 127 - p.window && (!SINKS || ka + kTcBN > p.sinks);
+            mt = (need_mask || need_w) ? row_max2<SINKS>(v, p.sinks - ka, qrow - p.window - ka, lim, sl2)
+                                       : row_max<false>(v, lim, sl2);
+          } else {
+            mt = need_mask ? row_max<true>(v, lim, sl2) : row_max<false>(v, lim, sl2);
+          }
         }
-        if (n == 0) {
+        if (taken == 0) {
           m_ref = mt;
         } else {
           const bool resc = mt > m_ref + kRescaleThreshold;
@@ -476,7 +524,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               m_ref = mt;
               lsum *= alpha;
             }
-            ok = mbar_wait(bar(C::B_OF + t), (of_base + n - 1) & 1, abort_flag, p.hdr, 10);
+            ok = mbar_wait(bar(C::B_OF + t), (of_base + taken - 1) & 1, abort_flag, p.hdr, 10);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -494,22 +542,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_wait_st();
           }
         }
-        const float rs = row_exp(v, sl2, m_ref == -INFINITY ? 0.f : m_ref);
-        tmem_st32(s_addr, v);  // P over the first 64 columns of S_t
-        tmem_st32(s_addr + 32, v + 32);
-        lsum += rs;
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        if (WIN == kWinSinks && n == I.nar) {
+          lsum += row_exp<kNarrow>(v, sl2, mu);
+          tmem_st16(s_addr, v);
+        } else {
+          const float rs = row_exp<128>(v, sl2, mu);
+          tmem_st32(s_addr, v);  // P over the first 64 columns of S_t
+          tmem_st32(s_addr + 32, v + 32);
+          lsum += rs;
+        }
+        ++taken;
         tmem_wait_st();
         fence_before_sync();
         mbar_arrive(bar(C::B_PF + t));
       }
       if (!ok) break;
       // epilogue: O / l -> bf16 rows < l; lse
-      ok = mbar_wait(bar(C::B_OF + t), (of_base + nbt - 1) & 1, abort_flag, p.hdr, 11);
+      ok = mbar_wait(bar(C::B_OF + t), (of_base + taken - 1) & 1, abort_flag, p.hdr, 11);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      of_base += nbt;
+      of_base += taken;
       fence_after_sync();
       const float inv = 1.f / lsum;
       const bool store = qrow < I.l;

@@ -221,7 +221,11 @@ va_status varlen_attn_plan_window(const va_shape* shape, const int32_t* cu_seqle
  * all later queries of it (query i sees the keys j <= i with j >= i - window or j < sinks).  A
  * q block also lists the key blocks [0, ceil(min(sinks, l) / BN)) that lie before its window's
  * first one, count = both parts; a kv block that holds a sink lists its q blocks from its
- * diagonal to the segment's end.  Orders as varlen_attn_plan_window; sinks = 0 is that call.
+ * diagonal to the segment's end, and such blocks of all heads come before the segment's others
+ * (block by block, each over the heads).  Other orders as varlen_attn_plan_window; sinks = 0 is that
+ * call.
+ * (The backward cuts the q range of such a block into several records when it is long and adds
+ * their sums; this call lists it as one.)
  * Errors as it, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */
 va_status varlen_attn_plan_sinks(const va_shape* shape, const int32_t* cu_seqlens_dev, int32_t kind,
                                  int32_t causal, int32_t window, int32_t sinks, int32_t* tile_map_dev,

@@ -56,7 +56,7 @@ maps have no token records and keep each segment's blocks in block order (q bloc
 descending, kv blocks ascending), which is the no-window order as well.  With sinks s a
 q block also lists the key blocks that hold the segment's first s keys and that lie before
 n_min, count = both parts, and a kv block with n*BN < s keeps its q blocks to the segment's
-end.
+end; such blocks of all heads come first in their segment.
 """
 from __future__ import annotations
 
@@ -117,7 +117,7 @@ def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, sho
 
 
 def bwd_tile_map(cu_seqlens, Hkv: int, BM: int, BN: int, causal: bool = True, short: int = 0, window=None,
-                 cu_k=None, sinks: int = 0):
+                 cu_k=None, sinks: int = 0, piece: int = 0):
     """Items as an int32 array [N, 4], in the order above: segment records
     (b, n, h_kv, n_q), then (causal, short > 0) token records (-1 - f, t0, h_kv, rows)
     whose BN-row tiles hold the key rows [t0, t0 + rows) of a run of short segments."""
@@ -135,11 +135,18 @@ def bwd_tile_map(cu_seqlens, Hkv: int, BM: int, BN: int, causal: bool = True, sh
         blocks = []
         for n in range(_ceil(lk, BN)):
             m_start = max(0, n * BN - (lk - l)) // BM if causal else 0
-            blocks.append((n, window_q_end(n, l, BM, BN, None if n * BN < sinks else window) - m_start))
-        cls = _cost_class(sum(nq for _, nq in blocks))
+            nq = window_q_end(n, l, BM, BN, None if n * BN < sinks else window) - m_start
+            # a sink block's q blocks in pieces of `piece` (0: one record), numbered above the head
+            cut = piece if piece and n * BN < sinks else nq
+            blocks += [(n, min(cut, nq - x), x // cut) for x in range(0, nq, cut)]
+        cls = _cost_class(sum(nq for _, nq, _ in blocks))
         for h in range(Hkv):
-            for n, nq in blocks:
-                items.append(((-cls, b, h, n if window is not None else -nq, n), (b, n, h, nq)))
+            for n, nq, x in blocks:
+                if n * BN < sinks:      # before the segment's other blocks: block, piece, head
+                    key = (-cls, b, -1, n, x, h)
+                else:
+                    key = (-cls, b, h, n if window is not None else -nq, n)
+                items.append((key, (b, n, h + x * Hkv, nq)))
     items.sort(key=lambda t: t[0])
     return np.asarray([r for _, r in items] + _token_records(cu, tok, Hkv, BN), dtype=np.int32).reshape(-1, 4)
 

@@ -44,6 +44,7 @@ cudaError_t launch_embed_bwd(int, const void*, int, int64_t, const int32_t*, int
                              int, void*, cudaStream_t);
 cudaError_t launch_bwd_dkdv_tc(const BwdParams&, int, int, bool, cudaStream_t);
 cudaError_t launch_bwd_dq_tc(const BwdParams&, int, int, bool, cudaStream_t);
+cudaError_t launch_sink_join(const BwdParams&, int, cudaStream_t);
 void bwd_tc_tiles(int*, int*, int*, int*);
 
 static thread_local std::string g_error;
@@ -57,14 +58,15 @@ enum KernelId {
   K_VALIDATE = 0, K_META_SCAN, K_META_FILL, K_PLAN, K_FWD, K_BWD_PREP, K_BWD_DKDV, K_BWD_DQ,
   K_VALIDATE_PLAN, K_FWD_TOK, K_CU_FROM_POS, K_LOSS_TARGETS, K_CE_COUNT, K_CE_ROWS, K_CE_REDUCE, K_PAD_COUNT,
   K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE,
-  K_EMBED_FWD, K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN, K_COUNT
+  K_EMBED_FWD, K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN, K_SINK_JOIN, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "validate_cu_seqlens", "metadata_scan", "metadata_fill", "plan",          "fwd",
     "bwd_prep",            "bwd_dkdv",      "bwd_dq",        "validate_plan", "fwd_tok",
     "cu_from_positions",   "loss_targets",  "ce_count",      "ce_rows",       "ce_reduce",
     "pad_count",           "pad_scan",      "pad_index",     "gather_rows", "distill_count", "distill_rows",
-    "distill_reduce", "embed_fwd", "embed_sort", "embed_reduce", "embed_join"};
+    "distill_reduce", "embed_fwd", "embed_sort", "embed_reduce", "embed_join",
+    "sink_join"};
 
 struct Profiler {
   std::vector<cudaEvent_t> start, stop;
@@ -192,19 +194,44 @@ FwdLayout fwd_layout(const va_shape& s) {
   return L;
 }
 
+// q blocks per piece of a kv block that holds sinks, or 0 when its records stay whole.  Such a block is
+// seen by its whole segment, max_seqlen / 64 q blocks for each of the g q heads in one serial item, while
+// the others see a window.  The map starts with these items, but one longer than an SM's share of all
+// steps sets the call's time; then they are cut into pieces of a quarter of the share (with more sink
+// blocks, which are more items, longer ones).  The kernel form for pieces costs 3% of dK/dV, hence not
+// always.  (d = 128, window 1023, one segment: T = 65536, 12 q heads on one kv head, backward 9.40 ms
+// whole, 1.27 in pieces; T = 16384, 32 on 8, 1.18 and 0.81.)
+int sink_piece(const va_shape& s, int window, int sinks) {
+  if (sinks <= 0) return 0;
+  constexpr int kSms = 152;  // a constant: the workspace size must not depend on the device
+  const int64_t g = s.Hq / s.Hkv, blocks = (sinks + 127) / 128;
+  const int64_t share = static_cast<int64_t>(s.Hq) * (s.T / 128 + 1) * (window / 64 + 2) / kSms;
+  const int64_t longest = g * (s.max_seqlen / 64 + 1);
+  if (longest <= std::max<int64_t>(share, 64)) return 0;  // (64 steps: 50 us)
+  const int64_t P = std::max<int64_t>(8, (share / 4 + g - 1) / g) * ((blocks + 1) / 2);
+  return 64 * P < s.max_seqlen ? static_cast<int>(P) : 0;
+}
+
 struct BwdLayout {
-  size_t dsum, kvmap, qmap, segoff, total;
+  size_t dsum, kvmap, qmap, segoff, part, total;
   int64_t cap_kv, cap_q;
+  int piece;
 };
-BwdLayout bwd_layout(const va_shape& s, int Tk = -1) {
+BwdLayout bwd_layout(const va_shape& s, int Tk = -1, int window = -1, int sinks = 0) {
   BwdLayout L;
   L.cap_kv = map_capacity(s, 1, Tk);
+  L.piece = sink_piece(s, window, sinks);
+  const int64_t blocks = (sinks + 127) / 128;
+  if (L.piece > 0) L.cap_kv += blocks * (s.T / (64 * L.piece) + 1) * s.Hkv;
   L.cap_q = map_capacity(s, 2);
   L.dsum = sizeof(WsHeader);
   L.kvmap = align256(L.dsum + static_cast<size_t>(s.Hq) * s.T * sizeof(float));
   L.qmap = align256(L.kvmap + static_cast<size_t>(L.cap_kv) * sizeof(TileItem));
   L.segoff = align256(L.qmap + static_cast<size_t>(L.cap_q) * sizeof(TileItem));
-  L.total = align256(L.segoff + static_cast<size_t>(s.B) * sizeof(int32_t));
+  L.part = align256(L.segoff + static_cast<size_t>(s.B) * sizeof(int32_t));
+  L.total = L.part;
+  if (L.piece > 0)
+    L.total += static_cast<size_t>(sink_slots(s.T, L.piece)) * blocks * s.Hkv * 2 * 128 * s.d * sizeof(float);
   return L;
 }
 
@@ -313,7 +340,7 @@ size_t varlen_attn_workspace_size(const va_shape* s, int32_t for_bwd) {
 
 size_t varlen_attn_workspace_size_sinks(const va_shape* s, int32_t window, int32_t sinks, int32_t for_bwd) {
   if (check_shape(s) != VA_OK || check_window(s, 1, &window, &sinks, "workspace_size") != VA_OK) return 0;
-  return for_bwd ? bwd_layout(*s).total : fwd_layout(*s).total;
+  return for_bwd ? bwd_layout(*s, -1, window, sinks).total : fwd_layout(*s).total;
 }
 
 va_status varlen_attn_plan(const va_shape* s, const int32_t* cu_dev, int32_t kind, int32_t causal,
@@ -533,7 +560,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws))
     return fail(VA_ERR_INVALID_ARG, "bwd: pointers must be 16-byte aligned");
   if (!(scale > 0.f) || !(scale < INFINITY)) return fail(VA_ERR_INVALID_ARG, "bwd: scale must be finite and > 0");
-  const BwdLayout L = bwd_layout(*s, cu_k ? Tk : -1);
+  const BwdLayout L = bwd_layout(*s, cu_k ? Tk : -1, window, sinks);
   if (ws_bytes < L.total) return fail(VA_ERR_WORKSPACE, "bwd: workspace too small");
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -554,7 +581,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   const PlanArgs pa[2] = {
       {cu, s->B, s->Hkv, BM, BN, 1, causal ? 1 : 0, kvmap, static_cast<int>(L.cap_kv), &hdr->status,
        &hdr->n_items[1], segoff, &hdr->counter[1], tok ? bwd_tc_token_short() : 0,
-       &hdr->n_items[kKvTokSlot], nullptr, window, cu_k, sinks},
+       &hdr->n_items[kKvTokSlot], nullptr, window, cu_k, sinks, L.piece},
       {cu, s->B, s->Hq, BM2, BN2, 2, causal ? 1 : 0, qmap, static_cast<int>(L.cap_q), &hdr->status,
        &hdr->n_items[2], segoff, &hdr->counter[2], tok ? bwd_tc_token_short() : 0,
        &hdr->n_items[kQTokSlot], nullptr, window, cu_k, sinks}};
@@ -597,6 +624,9 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   p.causal = causal ? 1 : 0;
   p.window = window;
   p.sinks = sinks;
+  p.piece = L.piece;
+  p.sink_blocks = (sinks + 127) / 128;
+  p.part = reinterpret_cast<float*>(w + L.part);
   p.cu_k = cu_k;
   p.Tk = cu_k ? Tk : 0;
   // one launch validates, plans both maps and computes D = rowsum(dO * O)
@@ -607,6 +637,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
     e = launch(K_BWD_DKDV, cs, [&] { return launch_bwd_dkdv_tc(p, s->d, static_cast<int>(L.cap_kv), tok, cs); });
   if (e == cudaSuccess)
     e = launch(K_BWD_DQ, cs, [&] { return launch_bwd_dq_tc(p, s->d, static_cast<int>(L.cap_q), tok, cs); });
+  if (e == cudaSuccess && L.piece > 0) e = launch(K_SINK_JOIN, cs, [&] { return launch_sink_join(p, s->d, cs); });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "bwd kernels");
 }
 

@@ -6,8 +6,9 @@ namespace va {
 
 using bf16 = __nv_bfloat16;
 
-// Forms of the attention kernels: no local window, a causal local window, a window with sinks.
-enum WinForm : int { kWinNone = 0, kWinLocal = 1, kWinSinks = 2 };
+// Forms of the attention kernels: no local window, a causal local window, a window with sinks, and
+// (dK/dV) one whose sink blocks may come in pieces.
+enum WinForm : int { kWinNone = 0, kWinLocal = 1, kWinSinks = 2, kWinSplit = 3 };
 
 struct FwdParams {
   const bf16* q;
@@ -63,8 +64,18 @@ struct BwdParams {
   int causal;
   int window = -1;   // causal local window: query i sees keys i-w..i; -1 = none
   int sinks = 0;     // with a window: a segment's first keys that every later query still sees
+  // Sink kv blocks whose q range is split: q blocks per piece (0 = never), the pieces' fp32 dV and
+  // dK [slot][kv block][kv head][2][128][d], the blocks of 128 keys that hold sinks.
+  int piece = 0, sink_blocks = 0;
+  float* part = nullptr;
   const int32_t* cu_k = nullptr;  // cross-attention: K/V boundaries (cu is Q's); null = cu
   int Tk = 0;                     // cross-attention: rows of K and V
 };
+
+// Slot of the partial sums of piece `piece` of the kv block whose keys start at stream row `row`.  A
+// split segment of n >= 2 pieces spans more than (n - 1) pieces of rows, which are two slots each, so
+// the slots (row / (32 P)) + 1 .. + n of different segments never meet.
+__host__ __device__ inline int sink_slot(int row, int P, int piece) { return row / (32 * P) + 1 + piece; }
+__host__ __device__ inline int sink_slots(int T, int P) { return T / (32 * P) + 2; }
 
 }  // namespace va

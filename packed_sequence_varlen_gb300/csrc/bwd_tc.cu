@@ -104,6 +104,7 @@ struct KvItem {
   int valid;
   int kvn;
   int s0k, lk, off;  // cross-attention: the keys' first row and count, the causal offset lk - l
+  int part;  // sinks: where a piece's fp32 sums go (of p.part, in [2][128][d]), or -1
 };
 static_assert(sizeof(KvItem) <= 48, "queue slots are 48 bytes");
 
@@ -118,6 +119,14 @@ __device__ __forceinline__ KvItem kv_decode(const BwdParams& p, int idx) {
   const int Mq = (r.l + 63) / 64;
   // the q steps start at the diagonal; without a window they run to the segment's end
   r.m_start = WIN ? it.blk * 2 : Mq - it.count;
+  if (WIN == kWinSplit) {  // a long sink block comes in pieces, the piece's number above the head
+    const int piece = it.head / p.Hkv;
+    r.hk = it.head - piece * p.Hkv;
+    r.part = it.blk < p.sink_blocks && Mq - r.m_start > p.piece
+                 ? (sink_slot(r.s0 + it.blk * 128, p.piece, piece) * p.sink_blocks + it.blk) * p.Hkv + r.hk
+                 : -1;
+    r.m_start += piece * p.piece;
+  }
   if (X) {  // keys from cu_k; the diagonal moves by the offset lk - l (bottom-right alignment)
     r.s0k = p.cu_k[it.seg];
     r.lk = p.cu_k[it.seg + 1] - r.s0k;
@@ -517,9 +526,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       store_rows_coalesced(held, held_out, p.k_rs, held_store);
       holding = false;
     };
-    auto take_accumulators = [&](int k, bf16* out, bool store) -> bool {
+    // part >= 0: the row goes out in fp32, to be added to the block's other pieces
+    auto take_accumulators = [&](int k, bf16* out, bool store, int part) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(bar(C::B_AF), k & 1, abort_flag, p.hdr, 29))) return false;
       fence_after_sync();
+      if (WIN == kWinSplit && part >= 0) {
+        float4* dst = reinterpret_cast<float4*>(p.part + ((static_cast<int64_t>(part) * 2 + x) * 128 + r) * D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {  // few registers: the ordinary path keeps its own
+          uint32_t f[16];
+          tmem_ld16(acc_addr + c, f);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (store)
+              dst[c / 4 + j] = make_float4(__uint_as_float(f[4 * j]), __uint_as_float(f[4 * j + 1]),
+                                           __uint_as_float(f[4 * j + 2]), __uint_as_float(f[4 * j + 3]));
+        }
+        fence_before_sync();
+        mbar_arrive(bar(C::B_AE));
+        return true;
+      }
       const float mul = x == 0 ? 1.f : p.scale;
       uint32_t o[D];  // the whole accumulator row in one TMEM round trip
 #pragma unroll
@@ -574,10 +601,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int lim = kvrow - (X ? I.off : 0) - q0;  // query columns c < lim are masked (key after query)
         // (window) query columns c >= hi are masked too: past the key's window
         // (no bound for a sink)
-        const int hi = WIN ? (WIN == kWinSinks && kvrow < p.sinks ? INT_MAX : kvrow + p.window + 1 - q0) : 0;
+        const int hi = WIN ? (WIN >= kWinSinks && kvrow < p.sinks ? INT_MAX : kvrow + p.window + 1 - q0) : 0;
         const bool need_mask =
             p.causal && (I.n * 128 + 127 - (X ? I.off : 0) > q0 ||
-                         (WIN && q0 + 31 > I.n * 128 + p.window && (WIN != kWinSinks || I.n * 128 + 128 > p.sinks)));
+                         (WIN && q0 + 31 > I.n * 128 + p.window && (WIN < kWinSinks || I.n * 128 + 128 > p.sinks)));
         const float* L = ldring + ls * 128 + cw;
         const float* Dd = L + 64;
         // one TMEM round trip: this warpgroup's 32 scores and 32 dP values of this kv row
@@ -620,7 +647,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // epilogue: warpgroup 0 takes dV, warpgroup 1 scale * dK
       bf16* out = (x == 0 ? p.dv : p.dk) + static_cast<int64_t>((X ? I.s0k : I.s0) + kvrow) * p.k_rs +
                   static_cast<int64_t>(I.hk) * p.k_hs;
-      if (!take_accumulators(item_cnt, out, kvrow < (X ? I.lk : I.l))) {
+      if (!take_accumulators(item_cnt, out, kvrow < (X ? I.lk : I.l), WIN == kWinSplit ? I.part : -1)) {
         ok = false;
         break;
       }
@@ -686,7 +713,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // epilogue: warpgroup 0 takes dV, warpgroup 1 scale * dK; rows past the item's keys are not stored
       bf16* out = (x == 0 ? p.dv : p.dk) + static_cast<int64_t>(I.s0 + r) * p.k_rs +
                   static_cast<int64_t>(I.hk) * p.k_hs;
-      if (!take_accumulators(item_cnt, out, r < I.kvn)) {
+      if (!take_accumulators(item_cnt, out, r < I.kvn, -1)) {
         ok = false;
         break;
       }
@@ -1310,7 +1337,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
+// Sink kv blocks in pieces: dV and scale * dK of a block, the pieces' fp32 sums added in order.  A
+// thread takes 8 columns of a row (grid.z) of a (block, kv head) (grid.y) in every grid.x-th
+// segment; few segments are long enough to be split.
+template <int D>
+__global__ void __launch_bounds__(256) sink_join_kernel(const BwdParams p) {
+  griddep_begin();
+  if (p.hdr->status != VA_OK) return;
+  const int n = blockIdx.y % p.sink_blocks, hk = blockIdx.y / p.sink_blocks;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int s0 = p.cu[b], l = p.cu[b + 1] - s0, q = (l + 63) / 64 - 2 * n;
+    if (n * 128 >= l || q <= p.piece) continue;
+    const int pieces = (q + p.piece - 1) / p.piece, rows = min(128, l - n * 128);
+    const int64_t first =
+        (static_cast<int64_t>(sink_slot(s0 + n * 128, p.piece, 0)) * p.sink_blocks + n) * p.Hkv + hk;
+    const int64_t step = static_cast<int64_t>(p.sink_blocks) * p.Hkv * 2 * 128 * D;
+    const int i = blockIdx.z * blockDim.x + threadIdx.x, c = i % (D / 8) * 8, row = i / (D / 8) % 128, x = i / (D / 8) / 128;
+    if (row < rows) {
+      const float* src = p.part + ((first * 2 + x) * 128 + row) * D + c;
+      float acc[8] = {};
+#pragma unroll 4
+      for (int k = 0; k < pieces; ++k, src += step) {
+        const float4 u = *reinterpret_cast<const float4*>(src), v = *reinterpret_cast<const float4*>(src + 4);
+        acc[0] += u.x, acc[1] += u.y, acc[2] += u.z, acc[3] += u.w;
+        acc[4] += v.x, acc[5] += v.y, acc[6] += v.z, acc[7] += v.w;
+      }
+      const float mul = x == 0 ? 1.f : p.scale;
+      bf16* out = (x == 0 ? p.dv : p.dk) + static_cast<int64_t>(s0 + n * 128 + row) * p.k_rs +
+                  static_cast<int64_t>(hk) * p.k_hs + c;
+      *reinterpret_cast<uint4*>(out) =
+          make_uint4(pack_bf16(acc[0] * mul, acc[1] * mul), pack_bf16(acc[2] * mul, acc[3] * mul),
+                     pack_bf16(acc[4] * mul, acc[5] * mul), pack_bf16(acc[6] * mul, acc[7] * mul));
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host side
+
+// After the dK/dV and dQ launches of a call whose sink blocks may come in pieces.
+cudaError_t launch_sink_join(const BwdParams& p, int d, cudaStream_t st) {
+  const dim3 grid(std::min(p.B, 64), p.sink_blocks * p.Hkv, 2 * 128 * (d / 8) / 256);
+  return d == 64 ? launch_pdl(sink_join_kernel<64>, grid, dim3(256), 0, st, p)
+                 : launch_pdl(sink_join_kernel<128>, grid, dim3(256), 0, st, p);
+}
+
 
 
 template <int D, bool TOK, int WIN, bool X>
@@ -1367,6 +1437,8 @@ static cudaError_t launch_dq_d(const BwdParams& p, int cap, cudaStream_t st) {
 cudaError_t launch_bwd_dkdv_tc(const BwdParams& p, int d, int cap, bool tok, cudaStream_t st) {
   if (p.cu_k)  // cross and window calls plan no token records
     return d == 64 ? launch_dkdv_d<64, false, kWinNone, true>(p, cap, st) : launch_dkdv_d<128, false, kWinNone, true>(p, cap, st);
+  if (p.window >= 0 && p.sinks > 0 && p.piece > 0)
+    return d == 64 ? launch_dkdv_d<64, false, kWinSplit, false>(p, cap, st) : launch_dkdv_d<128, false, kWinSplit, false>(p, cap, st);
   if (p.window >= 0 && p.sinks > 0)
     return d == 64 ? launch_dkdv_d<64, false, kWinSinks, false>(p, cap, st) : launch_dkdv_d<128, false, kWinSinks, false>(p, cap, st);
   if (p.window >= 0)

@@ -56,6 +56,7 @@ struct PlanArgs {
                          // window maps have no token records
   const int32_t* cu_k = nullptr;  // cross-attention: the K/V boundaries (cu is Q's); null = cu
   int sinks = 0;         // with a window: a segment's first keys that every later query still sees
+  int piece = 0;         // kv maps with sinks: q blocks per record of a block that holds sinks; 0 = all
 };
 
 __device__ __forceinline__ void set_status(WsHeader* h, int code) {

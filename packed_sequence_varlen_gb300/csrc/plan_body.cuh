@@ -101,10 +101,23 @@ __device__ __forceinline__ void seg_cost(const PlanArgs& a, int l, int lk, int& 
   } else if (M::tokens && l <= a.short_len) {
     nblk = 0;
     cost = 0;
-  } else if (M::win) {  // no closed form worth keeping: sum the blocks (one thread per segment)
-    nblk = M::kv ? ceil_p2(l, a.BN) : ceil_p2(l, a.BM);
-    cost = 0;
-    for (int b = 0; b < nblk; ++b) cost += win_count<M>(a, l, b);
+  } else if (M::win && !M::kv) {
+    // With r = BM / BN, c = ceil(w / BN) and S the key blocks that hold sinks, q block m's window starts
+    // at key block max(0, m r - c), so max(0, m r - c - S) of its causal blocks are not listed.
+    const int M_ = ceil_p2(l, a.BM), Lk = ceil_p2(l, a.BN), r = div_p2(a.BM, a.BN);
+    const int x = ceil_p2(a.window, a.BN) + ceil_p2(min(l, a.sinks), a.BN), m1 = min(M_, ceil_p2(x, r));
+    nblk = M_;
+    cost = r * (M_ - 1) * M_ / 2 + Lk - (r * (m1 + M_ - 1) * (M_ - m1) / 2 - x * (M_ - m1));
+  } else if (M::win) {
+    // With r = BN / BM, kv block n has min(Mq - n r, e) q blocks, e those a window reaches, or (sinks)
+    // Mq - n r.
+    const int N = ceil_p2(l, a.BN), Mq = ceil_p2(l, a.BM), r = div_p2(a.BN, a.BM);
+    const int e = div_p2(a.BN - 1 + a.window, a.BM) + 1, x = max(0, Mq - e), k = min(N, ceil_p2(x, r));
+    const int S = min(N, ceil_p2(a.sinks, a.BN)), ks = min(S, k);
+    nblk = N;
+    cost = N * Mq - r * N * (N - 1) / 2 - (k * x - r * k * (k - 1) / 2) + (ks * x - r * ks * (ks - 1) / 2);
+    if (a.piece > 0)
+      for (int n = 0; n < S; ++n) nblk += ceil_div(Mq - n * r, a.piece) - 1;
   } else if (!M::kv) {
     const int M_ = ceil_p2(l, a.BM), Lk = ceil_p2(l, a.BN);
     nblk = M_;
@@ -134,6 +147,35 @@ __device__ __forceinline__ void seg_record(const PlanArgs& a, int l, int lk, int
     blk = j;
     count = M::causal ? Mq - div_p2(j * a.BN, a.BM) : Mq;
   }
+}
+
+// The rr-th record of a segment with nblk records per head, the heads in order.  kv maps with sinks:
+// the blocks that hold sinks, which a whole segment's queries see, come first for all heads (a long
+// item must not start late), each in pieces of a.piece q blocks (0: whole), numbered above the head.
+template <class M>
+__device__ __forceinline__ void head_record(const PlanArgs& a, int l, int lk, int nblk, int rr, TileItem& t) {
+  if (M::win && M::kv && a.sinks > 0) {
+    const int Mq = ceil_p2(l, a.BM), r = div_p2(a.BN, a.BM), S = min(ceil_p2(l, a.BN), ceil_p2(a.sinks, a.BN));
+    int j = rr / a.heads;
+    for (int n = 0; n < S; ++n) {
+      const int q = Mq - n * r, k = a.piece > 0 ? ceil_div(q, a.piece) : 1;
+      if (j < k) {
+        t.blk = n;
+        t.head = rr - rr / a.heads * a.heads + j * a.heads;
+        t.count = a.piece > 0 ? min(a.piece, q - j * a.piece) : q;
+        return;
+      }
+      j -= k;
+      rr -= k * a.heads;
+      nblk -= k;
+    }
+    t.head = rr / nblk;
+    t.blk = S + rr - t.head * nblk;
+    t.count = win_count<M>(a, l, t.blk);
+    return;
+  }
+  t.head = rr / nblk;
+  seg_record<M>(a, l, lk, nblk, rr - t.head * nblk, t.blk, t.count);
 }
 
 __device__ __forceinline__ int cost_class(int c) { return 31 - __clz(max(c, 1)); }
@@ -325,11 +367,10 @@ __device__ __forceinline__ void write_group(const PlanArgs& a, const int* cu, co
     const int soff = __shfl_sync(0xffffffffu, off, sgi);
     const int sbeg = __shfl_sync(0xffffffffu, incl - n, sgi);
     if (r < total) {
-      const int rr = r - sbeg, h = rr / snb, j = rr - h * snb;
+      const int rr = r - sbeg;
       TileItem t;
-      seg_record<M>(a, sl, slk, snb, j, t.blk, t.count);
+      head_record<M>(a, sl, slk, snb, rr, t);
       t.seg = g0 + sgi;
-      t.head = h;
       if (soff + rr >= 0 && soff + rr < a.capacity) a.out[soff + rr] = t;  // boundaries that break
                                                                            // the contract must not
                                                                            // write outside the map
@@ -517,7 +558,7 @@ struct PlanPair {
   int Tk = 0, max_seqlen_k = 0;  // cross-attention (map[0].cu_k set): the K/V stream
 };
 
-// Maps of at most 32 segments without token tiles, local window or cross-attention: the
+// Maps of at most 32 segments without token tiles or cross-attention: the
 // same records in the same order as plan_body, from a far shorter instruction path.  A
 // planning launch runs once per call on cold instruction caches, so its time goes mostly to
 // fetching instructions; the general path's ranking (class totals, bases, per-class scans)
@@ -529,7 +570,7 @@ __device__ __forceinline__ bool small_plan_ok(const PlanPair& pp, int i0, int i1
   if (pp.map[0].B < 1 || pp.map[0].B > 32) return false;
   for (int i = i0; i < i1; ++i) {
     const PlanArgs& a = pp.map[i];
-    if (a.cu_k || (a.causal && a.window >= 0) || token_mode(a)) return false;
+    if (a.cu_k || token_mode(a)) return false;
   }
   return true;
 }
@@ -567,11 +608,9 @@ __device__ __forceinline__ void small_write(const PlanArgs& a, const SmallPlanTa
 #pragma unroll
     for (int step = 16; step > 0; step >>= 1)
       if (k + step < a.B && t.off[k + step] <= r) k += step;
-    const int rr = r - t.off[k], nb = t.nblk[k], h = rr / nb, j = rr - h * nb;
     TileItem it;
-    seg_record<M>(a, t.len[k], t.len[k], nb, j, it.blk, it.count);
+    head_record<M>(a, t.len[k], t.len[k], t.nblk[k], r - t.off[k], it);
     it.seg = t.seg[k];
-    it.head = h;
     a.out[r] = it;
   }
 }
@@ -612,7 +651,10 @@ __device__ __forceinline__ void small_plan(const PlanPair& pp, PlanSmem& sh, int
     __syncthreads();  // the table of the previous map has been read
     if (threadIdx.x < 32) {
       int total = 0;
-      if (a.kind == 1) {
+      if (a.causal && a.window >= 0) {
+        if (a.kind == 1) small_rank<MapKind<true, true, false, true>>(a, lane, l, sh.small, total);
+        else small_rank<MapKind<false, true, false, true>>(a, lane, l, sh.small, total);
+      } else if (a.kind == 1) {
         if (a.causal) small_rank<MapKind<true, true, false>>(a, lane, l, sh.small, total);
         else small_rank<MapKind<true, false, false>>(a, lane, l, sh.small, total);
       } else {
@@ -631,7 +673,10 @@ __device__ __forceinline__ void small_plan(const PlanPair& pp, PlanSmem& sh, int
     }
     __syncthreads();
     const int total = sh.seg_total;
-    if (a.kind == 1) {
+    if (a.causal && a.window >= 0) {
+      if (a.kind == 1) small_write<MapKind<true, true, false, true>>(a, sh.small, total);
+      else small_write<MapKind<false, true, false, true>>(a, sh.small, total);
+    } else if (a.kind == 1) {
       if (a.causal) small_write<MapKind<true, true, false>>(a, sh.small, total);
       else small_write<MapKind<true, false, false>>(a, sh.small, total);
     } else {

@@ -209,3 +209,68 @@ def test_sinks_autograd_differences_and_refusals(va):
     ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     va.varlen_attn_fwd(q, k, v, bad, mx, window=3, sinks=2, workspace=ws)
     assert va.read_status(ws) == 5
+
+
+def _align256(x):
+    return (x + 255) // 256 * 256
+
+
+def piece_of(T, Hq, Hkv, w, s, mx):
+    """The backward's rule for cutting a sink block's q range (q blocks per piece, 0: never)."""
+    g, w, s = Hq // Hkv, min(w, mx), min(s, mx)
+    share = Hq * (T // 128 + 1) * (w // 64 + 2) // 152
+    if s == 0 or g * (mx // 64 + 1) <= max(share, 64):
+        return 0
+    P = max(8, -(-(share // 4) // g)) * ((-(-s // 128) + 1) // 2)
+    return P if 64 * P < mx else 0
+
+
+# both planning paths (up to 32 segments, more), one and several blocks with sinks, split and not
+@pytest.mark.parametrize("w,s", [(0, 1), (100, 4), (1000, 130), (5000, 9), (64, 0), (700, 0), (300, 400)])
+@pytest.mark.parametrize("lengths,Hq,Hkv,d", [(EDGE, 4, 2, 128), ([9001, 1, 3000, 2689, 2690], 12, 1, 128),
+                                              (EDGE * 3 + [5000], 24, 2, 64), ([40], 8, 8, 64)])
+def test_call_maps_bit_exact(va, lengths, Hq, Hkv, d, w, s):
+    """The maps the attention calls build for themselves, read back from their workspaces."""
+    cu, cud, mx = boundaries(lengths)
+    T, B = int(cu[-1]), len(lengths)
+    q, k, v, do = (torch.zeros(T, h, d, dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv, Hq))
+    piece = piece_of(T, Hq, Hkv, w, s, mx)
+    blocks = -(-min(s, mx) // 128)
+    kw = dict(window=w, sinks=s)
+    ws_f, ws_b = (torch.full((va.workspace_size(T, B, Hq, Hkv, d, mx, x, **kw),), 0x5a, dtype=torch.uint8, device=DEV)
+                  for x in (False, True))
+    o, lse = va.varlen_attn_fwd(q, k, v, cud, mx, workspace=ws_f, check_status=True, **kw)
+    va.varlen_attn_bwd(q, k, v, o, lse, do, cud, mx, workspace=ws_b, check_status=True, **kw)
+    BN_kv = va.tile_sizes(1, d)[1]
+    kvmap = _align256(256 + Hq * T * 4)
+    cap = (T // BN_kv + B) * Hkv + (blocks * (T // (64 * piece) + 1) * Hkv if piece else 0)
+    qmap = _align256(kvmap + cap * 16)
+    for ws, kind, at in ((ws_f, 0, 256), (ws_b, 1, kvmap), (ws_b, 2, qmap)):
+        BM, BN = va.tile_sizes(kind, d)
+        ref = (ot.bwd_tile_map(cu, Hkv, BM, BN, True, 0, window=w, sinks=s, piece=piece) if kind == 1 else
+               ot.fwd_tile_map(cu, Hq, BM, BN, True, 0, window=w, sinks=s))
+        raw = ws.cpu().numpy()
+        assert int(raw[4 + 4 * kind:8 + 4 * kind].view(np.int32)[0]) == len(ref)
+        got = raw[at:at + 16 * len(ref)].view(np.int32).reshape(-1, 4)
+        assert np.array_equal(got, ref), kind
+
+
+def test_split_sink_blocks_parity(va):
+    """Several segments long enough to be cut, next to short ones, sinks over three key blocks, 12 q
+    heads on one kv head; the gradient of every row and of the sink rows alone; the same bits twice."""
+    lengths = [2100, 5, 4400, 129, 3333, 1400]
+    cu, cud, mx = boundaries(lengths)
+    T, w, s = int(cu[-1]), 90, 261
+    assert 0 < piece_of(T, 12, 1, w, s, mx) * 64 < 1400
+    q, k, v, do = si.tensors(T, 12, 1, 64, seed_offset=77)
+    got = run_both(va, q, k, v, do, cud, mx, w, s)
+    against_oracle(got, q, k, v, do, cu, w, s)
+    again = run_both(va, q, k, v, do, cud, mx, w, s)
+    assert all(np.array_equal(a, b) for a, b in zip(got[2], again[2]))
+    qq, kk, vv, dd = (si.to_f64(x) for x in (q, k, v, do))
+    ro, rl = oa.varlen_forward(qq, kk, vv, cu, window=w, sinks=s)
+    rg = oa.varlen_backward(qq, kk, vv, ro, rl, dd, cu, window=w, sinks=s)
+    for b, n in zip(cu[:-1], lengths):
+        for i in (1, 2):
+            rows = slice(int(b), int(b) + min(n, s))
+            assert wl.rel_l2(got[2][i][rows], rg[i][rows]) <= wl.GRAD_REL_L2

@@ -192,6 +192,24 @@ __device__ __forceinline__ void store_rows_coalesced32(uint4 (&a)[W], T* row, in
   }
 }
 
+// Same contract, every lane storing its own row in 32-byte pieces: a sector each, with none of the
+// shuffles, for the price of one line per lane and instruction.  Rows that do not start on 32-byte
+// boundaries go the other way.
+template <int W, class T>
+__device__ __forceinline__ void store_rows_direct32(uint4 (&a)[W], T* row, int64_t stride, bool valid) {
+  if (!__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(row) & 31u) == 0)) {
+    store_rows_coalesced(a, row, stride, valid);
+    return;
+  }
+  if (!valid) return;
+#pragma unroll
+  for (int j = 0; j < W; j += 2)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint4*>(row) + j),
+                 "r"(a[j].x), "r"(a[j].y), "r"(a[j].z), "r"(a[j].w), "r"(a[j + 1].x), "r"(a[j + 1].y),
+                 "r"(a[j + 1].z), "r"(a[j + 1].w)
+                 : "memory");
+}
+
 // store_rows_coalesced32 when every row of the warp starts on a 32-byte boundary (the
 // 256-bit stores need it), store_rows_coalesced otherwise.
 template <int W, class T>

@@ -16,7 +16,7 @@
 //   embed_reduce_kernel  chunks of P sorted tokens x columns: rows of dout are read once, sixteen
 //                        (fp32: eight) rows in flight per thread, sums of runs that lie inside a chunk are final, the
 //                        others go to two fp32 rows per chunk
-//   embed_join_kernel    runs over several chunks: the chunks' sums in order
+//   embed_join_kernel    runs over several chunks: the chunks' sums, a block per run
 // What bounds the gradient: dout read once and dtable written once (HBM).
 #include <algorithm>
 
@@ -27,9 +27,10 @@ namespace va {
 namespace {
 
 constexpr int kFwdThreads = 256, kFwdUnroll = 4;
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 8;               // one cluster
 constexpr int kMaxBins = 512;
+constexpr int kSortBatch = 4;              // keys a lane loads together
 constexpr int kPresentWords = 8192;        // ids a filling CTA looks at together: 32 per word
 constexpr int kZeroBytes = 8192;           // of one bulk store of zeros
 constexpr int kReduceThreads = 256;
@@ -47,7 +48,7 @@ struct EmbedParams {
   int32_t* status;
   // gradient
   int accumulate;
-  int32_t *key0, *tok0, *key1, *tok1;  // [T] ping-pong
+  int2 *pair0, *pair1;                 // [T] (id, token), ping-pong
   int bits, passes, width;             // radix: `passes` digits of `width` bits
   float* part;                         // [chunks][2][D]
   int P;                               // sorted tokens per chunk
@@ -245,37 +246,42 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
     return;
   }
   int* cnt = sm;                              // [warps][bins]: counts, then next ranks
-  int* hist = sm + kSortWarps * kMaxBins;     // [bins] of this CTA, read by the others
+  uint32_t* lanes = reinterpret_cast<uint32_t*>(sm + kSortWarps * kMaxBins);  // [warps][bins]: who has it
+  int* hist = sm + 2 * kSortWarps * kMaxBins; // [bins] of this CTA, read by the others
   int* scan = hist + kMaxBins;                // [warps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
-  const int share = ((p.T + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
+  const int share = ((p.T + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;  // tokens per warp
   const int64_t b0 = static_cast<int64_t>(rank * kSortWarps + warp) * share;
   const int beg = static_cast<int>(std::min<int64_t>(p.T, b0)), end = static_cast<int>(std::min<int64_t>(p.T, b0 + share));
   if (rank == 0 && tid == 0) *p.status = VA_OK;
   bool bad = false;
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.width, bins = 1 << p.width;
-    const int32_t* ki = (pass & 1) ? p.key1 : p.key0;
-    const int32_t* ti = (pass & 1) ? p.tok1 : p.tok0;
-    int32_t* ko = (pass & 1) ? p.key0 : p.key1;
-    int32_t* to = (pass & 1) ? p.tok0 : p.tok1;
+    const int2* in = (pass & 1) ? p.pair1 : p.pair0;
+    int2* out = (pass & 1) ? p.pair0 : p.pair1;
     // ids outside [0, V) take the key V: they follow every other and are left out
-    auto key_of = [&](int i) -> int {
-      if (pass > 0) return __ldcg(ki + i);
+    auto pair_of = [&](int i) -> int2 {
+      if (pass > 0) return __ldcg(in + i);
       const int id = __ldg(p.ids + i);
       if (id >= p.V) bad = true;
-      return id < 0 || id >= p.V ? p.V : id;
+      return make_int2(id < 0 || id >= p.V ? p.V : id, i);
     };
-    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = lanes[i] = 0;
     __syncthreads();
     int* mine = cnt + warp * bins;
-    for (int i0 = beg; i0 < end; i0 += 32) {
-      const int i = i0 + lane;
-      const int d = i < end ? (key_of(i) >> shift) & (bins - 1) : bins;
-      const unsigned peers = __match_any_sync(0xffffffffu, d);
-      if (d < bins && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
-      __syncwarp();
+    uint32_t* who = lanes + warp * bins;
+    for (int i0 = beg; i0 < end; i0 += 32 * kSortBatch) {
+      int k[kSortBatch];
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        k[u] = i < end ? pair_of(i).x : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        if (k[u] >= 0) atomicAdd(&mine[(k[u] >> shift) & (bins - 1)], 1);
+      }
     }
     __syncthreads();
     int total = 0;  // of this CTA, bin tid
@@ -311,19 +317,34 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
     if (tid < bins)
       for (int w = 0; w < kSortWarps; ++w) cnt[w * bins + tid] += base;
     __syncthreads();
-    for (int i0 = beg; i0 < end; i0 += 32) {
-      const int i = i0 + lane;
-      const int k = i < end ? key_of(i) : 0;
-      const int d = i < end ? (k >> shift) & (bins - 1) : bins;
-      const unsigned peers = __match_any_sync(0xffffffffu, d);
-      const int at = d < bins ? mine[d] + __popc(peers & ((1u << lane) - 1)) : 0;
-      __syncwarp();
-      if (d < bins) {
-        if (lane == __ffs(peers) - 1) mine[d] += __popc(peers);
-        ko[at] = k;
-        to[at] = pass > 0 ? __ldcg(ti + i) : i;
+    for (int i0 = beg; i0 < end; i0 += 32 * kSortBatch) {
+      int2 k[kSortBatch];
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        k[u] = i < end ? pair_of(i) : make_int2(-1, 0);
       }
-      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        if (i0 + 32 * u >= end) break;
+        // the lanes with the same digit meet in shared memory (the warp match instruction takes 64
+        // cycles of the SM each: T = 131072 sorted in 67 us with it, 44 without)
+        const bool have = k[u].x >= 0;
+        const int d = (k[u].x >> shift) & (bins - 1);
+        if (have) atomicOr(&who[d], 1u << lane);
+        __syncwarp();
+        const unsigned peers = have ? who[d] : 0u;
+        const int at = have ? mine[d] + __popc(peers & ((1u << lane) - 1)) : 0;
+        __syncwarp();
+        if (have) {
+          if (lane == __ffs(peers) - 1) {
+            mine[d] += __popc(peers);
+            who[d] = 0;
+          }
+          out[at] = k[u];
+        }
+        __syncwarp();
+      }
     }
     cluster_barrier();  // the sorted pairs are visible, and no CTA's counts are read any more
   }
@@ -332,8 +353,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
 
 // One group of lpr threads per chunk of P sorted tokens (grid.y: further columns).
 template <class TI, class TO, bool VI, bool VO>
-__global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const EmbedParams p, const int32_t* key,
-                                                                      const int32_t* tok, int lpr) {
+__global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const EmbedParams p, const int2* pair,
+                                                                      int lpr) {
   constexpr int kRows = sizeof(TI) == 2 ? 16 : 8;  // rows of dout in flight per thread
   extern __shared__ int sm[];
   griddep_begin();
@@ -345,8 +366,9 @@ __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const Embe
   for (int i = lane - 1; i < p.P + 1; i += lpr) {
     const int64_t at = b0 + i;
     const bool in = at >= 0 && at < p.T;
-    keys[i] = in ? __ldg(key + at) : p.V;
-    if (i >= 0 && i < p.P) toks[i] = in ? __ldg(tok + at) : 0;
+    const int2 kt = in ? __ldg(pair + at) : make_int2(p.V, 0);
+    keys[i] = kt.x;
+    if (i >= 0 && i < p.P) toks[i] = kt.y;
   }
   __syncthreads();
   const int c = (blockIdx.y * lpr + lane) * kW, n = p.D - c;
@@ -409,61 +431,107 @@ __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const Embe
   }
 }
 
-// Runs over several chunks: the chunk that a run starts in adds the chunks' sums in order.
+// Runs over several chunks: the chunks' sums are added, in order, by the row group whose chunk the run
+// starts in, or for a long run (a frequent token) by the whole block, whose groups take equal shares
+// of the chunks and whose shares are added in order.
 template <class TO, bool VO>
-__global__ void __launch_bounds__(kReduceThreads) embed_join_kernel(const EmbedParams p, const int32_t* key, int lpr) {
+__global__ void __launch_bounds__(kReduceThreads) embed_join_kernel(const EmbedParams p, const int2* pair, int lpr) {
+  constexpr int kAhead = 8;  // chunks' sums in flight per thread
+  constexpr int kAlone = 16; // chunks of a run that one row group adds by itself
+  __shared__ int found[kReduceThreads], found_last[kReduceThreads], nfound;
+  __shared__ float share[kReduceThreads][kW];
   griddep_begin();
-  const int groups = kReduceThreads / lpr;
-  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lpr;
-  const int64_t b0 = chunk * p.P;
-  const int c = (blockIdx.y * lpr + threadIdx.x % lpr) * kW;
-  if (b0 + p.P >= p.T || c >= p.D) return;  // the last chunk's runs end in it
-  const int beg = static_cast<int>(b0), end = beg + p.P;
-  const int cur = __ldg(key + end - 1);
-  if (cur >= p.V || __ldg(key + end) != cur) return;                       // ends in this chunk
-  if (__ldg(key + beg) == cur && beg > 0 && __ldg(key + beg - 1) == cur) return;  // began before it
-  int lo = end, hi = p.T;  // first sorted token with a larger key
-  while (lo < hi) {
-    const int mid = lo + ((hi - lo) >> 1);
-    if (__ldg(key + mid) > cur) hi = mid;
-    else lo = mid + 1;
-  }
-  const int last = (lo - 1) / p.P;
-  const int n = p.D - c;
+  const auto key = [&](int64_t i) { return __ldg(&pair[i].x); };
+  const int groups = kReduceThreads / lpr, g = threadIdx.x / lpr, lane = threadIdx.x % lpr;
+  if (threadIdx.x == 0) nfound = 0;
+  __syncthreads();
+  const int c = (blockIdx.y * lpr + lane) * kW, n = p.D - c;
   const float* part = p.part + c;
   const auto load = [&](Raw<float>& x, const float* q) {
     if (p.D % kW == 0) x.load<true>(q, n);
     else x.load<false>(q, n);
   };
-  constexpr int kAhead = 8;  // chunks' sums in flight
-  float acc[kW];
-  Raw<float> own;
-  load(own, part + (chunk * 2 + 1) * p.D);
-  own.values(acc);
-  for (int64_t q = chunk + 1; q <= last; q += kAhead) {
-    Raw<float> raw[kAhead];
+  // acc += the sums of chunks [q0, q1) of the run that starts in `chunk`: there it is the chunk's second
+  // row, else the first
+  const auto add = [&](float (&acc)[kW], int64_t chunk, int64_t q0, int64_t q1) {
+    for (int64_t q = q0; n > 0 && q < q1; q += kAhead) {
+      Raw<float> raw[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (q + u <= last) load(raw[u], part + (q + u) * 2 * p.D);
+      for (int u = 0; u < kAhead; ++u)
+        if (q + u < q1) load(raw[u], part + ((q + u) * 2 + (q + u == chunk ? 1 : 0)) * p.D);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (q + u > last) break;
-      float x[kW];
-      raw[u].values(x);
+      for (int u = 0; u < kAhead; ++u) {
+        if (q + u >= q1) break;
+        float x[kW];
+        raw[u].values(x);
 #pragma unroll
-      for (int i = 0; i < kW; ++i) acc[i] += x[i];
+        for (int i = 0; i < kW; ++i) acc[i] += x[i];
+      }
+    }
+  };
+  const auto finish = [&](const float (&acc)[kW], int cur) {
+    if (n <= 0) return;
+    TO* row = static_cast<TO*>(p.dst) + cur * p.d_rs + c;
+    float x[kW] = {};
+    if (p.accumulate) {
+      Raw<TO> old;
+      old.template load<VO>(row, n);
+      old.values(x);
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) x[i] = fmaf(acc[i], p.scale, x[i]);
+    store_row<VO>(row, n, x);
+  };
+  {  // the run that starts in this group's chunk and goes on in the next one
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + g, b0 = chunk * p.P;
+    if (b0 + p.P < p.T) {
+      const int beg = static_cast<int>(b0), end = beg + p.P, cur = key(end - 1);
+      if (cur < p.V && key(end) == cur &&
+          !(key(beg) == cur && beg > 0 && key(beg - 1) == cur)) {
+        // its end: the first sorted token with a larger key, looked for at doubling distances first
+        int lo = end, hi = p.T;
+        for (int64_t d = p.P; lo + d < p.T; d *= 2) {
+          if (key(lo + d) > cur) {
+            hi = static_cast<int>(lo + d);
+            break;
+          }
+          lo += static_cast<int>(d);
+        }
+        while (lo < hi) {
+          const int mid = lo + ((hi - lo) >> 1);
+          if (key(mid) > cur) hi = mid;
+          else lo = mid + 1;
+        }
+        const int last = (lo - 1) / p.P;
+        if (last - chunk < kAlone || groups == 1) {
+          float acc[kW] = {};
+          add(acc, chunk, chunk, static_cast<int64_t>(last) + 1);
+          finish(acc, cur);
+        } else if (lane == 0) {
+          const int f = atomicAdd(&nfound, 1);  // (any order: rows of their own)
+          found[f] = g;
+          found_last[f] = last;
+        }
+      }
     }
   }
-  TO* row = static_cast<TO*>(p.dst) + cur * p.d_rs + c;
-  float x[kW] = {};
-  if (p.accumulate) {
-    Raw<TO> old;
-    old.template load<VO>(row, n);
-    old.values(x);
-  }
+  __syncthreads();
+  for (int f = 0; f < nfound; ++f) {  // the whole block on one run
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + found[f];
+    const int64_t stop = static_cast<int64_t>(found_last[f]) + 1, per = (stop - chunk + groups - 1) / groups;
+    const int64_t q0 = chunk + g * per;
+    float acc[kW] = {};
+    add(acc, chunk, q0, q0 + per < stop ? q0 + per : stop);
+    __syncthreads();  // the previous run's shares have been read
 #pragma unroll
-  for (int i = 0; i < kW; ++i) x[i] = fmaf(acc[i], p.scale, x[i]);
-  store_row<VO>(row, n, x);
+    for (int i = 0; i < kW; ++i) share[threadIdx.x][i] = acc[i];
+    __syncthreads();
+    if (g != 0) continue;
+    for (int h = 1; h < groups; ++h)
+#pragma unroll
+      for (int i = 0; i < kW; ++i) acc[i] += share[h * lpr + lane][i];
+    finish(acc, key((chunk + 1) * p.P));
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -490,7 +558,7 @@ int chunk_tokens(int T, int D) {
 template <class T, bool VEC>
 cudaError_t launch_sort(const EmbedParams& p, int ctas, cudaStream_t st) {
   const auto kernel = embed_sort_kernel<T, VEC>;
-  const size_t smem = std::max<size_t>((kSortWarps * kMaxBins + kMaxBins + kSortWarps) * sizeof(int),
+  const size_t smem = std::max<size_t>((2 * kSortWarps * kMaxBins + kMaxBins + kSortWarps) * sizeof(int),
                                        kPresentWords * sizeof(uint32_t) + kZeroBytes);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -512,17 +580,16 @@ cudaError_t launch_sort(const EmbedParams& p, int ctas, cudaStream_t st) {
 }
 
 template <class TI, class TO, bool VI>
-cudaError_t launch_reduce(const EmbedParams& p, bool vo, dim3 grid, const int32_t* key, const int32_t* tok, int lpr,
+cudaError_t launch_reduce(const EmbedParams& p, bool vo, dim3 grid, const int2* pair, int lpr,
                           cudaStream_t st) {
   const size_t smem = chunk_smem(p.P, lpr);
-  return vo ? launch_pdl(embed_reduce_kernel<TI, TO, VI, true>, grid, dim3(kReduceThreads), smem, st, p, key, tok, lpr)
-            : launch_pdl(embed_reduce_kernel<TI, TO, VI, false>, grid, dim3(kReduceThreads), smem, st, p, key, tok, lpr);
+  return vo ? launch_pdl(embed_reduce_kernel<TI, TO, VI, true>, grid, dim3(kReduceThreads), smem, st, p, pair, lpr)
+            : launch_pdl(embed_reduce_kernel<TI, TO, VI, false>, grid, dim3(kReduceThreads), smem, st, p, pair, lpr);
 }
 template <class TI, class TO>
-cudaError_t launch_reduce(const EmbedParams& p, bool vi, bool vo, dim3 grid, const int32_t* key, const int32_t* tok,
-                          int lpr, cudaStream_t st) {
-  return vi ? launch_reduce<TI, TO, true>(p, vo, grid, key, tok, lpr, st)
-            : launch_reduce<TI, TO, false>(p, vo, grid, key, tok, lpr, st);
+cudaError_t launch_reduce(const EmbedParams& p, bool vi, bool vo, dim3 grid, const int2* pair, int lpr, cudaStream_t st) {
+  return vi ? launch_reduce<TI, TO, true>(p, vo, grid, pair, lpr, st)
+            : launch_reduce<TI, TO, false>(p, vo, grid, pair, lpr, st);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -532,7 +599,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t embed_bwd_workspace(int T, int D) {
   const int P = chunk_tokens(T, D);
   const size_t chunks = (static_cast<size_t>(T) + P - 1) / P;
-  return sizeof(WsHeader) + 4 * align256(static_cast<size_t>(T) * sizeof(int32_t)) +
+  return sizeof(WsHeader) + 2 * align256(static_cast<size_t>(T) * sizeof(int2)) +
          align256(chunks * 2 * D * sizeof(float));
 }
 
@@ -578,10 +645,10 @@ cudaError_t launch_embed_bwd(int stage, const void* dout, int in_bf16, int64_t i
   p.accumulate = accumulate;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.status = &reinterpret_cast<WsHeader*>(w)->status;
-  int32_t** arrays[4] = {&p.key0, &p.tok0, &p.key1, &p.tok1};
-  const size_t one = align256(static_cast<size_t>(T) * sizeof(int32_t));
-  for (int i = 0; i < 4; ++i) *arrays[i] = reinterpret_cast<int32_t*>(w + sizeof(WsHeader) + i * one);
-  p.part = reinterpret_cast<float*>(w + sizeof(WsHeader) + 4 * one);
+  const size_t one = align256(static_cast<size_t>(T) * sizeof(int2));
+  p.pair0 = reinterpret_cast<int2*>(w + sizeof(WsHeader));
+  p.pair1 = reinterpret_cast<int2*>(w + sizeof(WsHeader) + one);
+  p.part = reinterpret_cast<float*>(w + sizeof(WsHeader) + 2 * one);
   p.P = chunk_tokens(T, D);
   p.bits = 1;
   while (p.bits < 31 && (V >> p.bits) > 0) ++p.bits;  // keys 0 .. V
@@ -598,24 +665,23 @@ cudaError_t launch_embed_bwd(int stage, const void* dout, int in_bf16, int64_t i
     if (out_bf16) return vo ? launch_sort<__nv_bfloat16, true>(p, ctas, st) : launch_sort<__nv_bfloat16, false>(p, ctas, st);
     return vo ? launch_sort<float, true>(p, ctas, st) : launch_sort<float, false>(p, ctas, st);
   }
-  const int32_t* key = (p.passes & 1) ? p.key1 : p.key0;
-  const int32_t* tok = (p.passes & 1) ? p.tok1 : p.tok0;
+  const int2* pair = (p.passes & 1) ? p.pair1 : p.pair0;
   const int lpr = lanes_per_row(D, kReduceThreads, 1), groups = kReduceThreads / lpr;
   const int64_t chunks = (static_cast<int64_t>(T) + p.P - 1) / p.P;
   const dim3 grid(static_cast<unsigned>((chunks + groups - 1) / groups), (D + lpr * kW - 1) / (lpr * kW));
   if (stage == 1) {
     if (in_bf16)
-      return out_bf16 ? launch_reduce<__nv_bfloat16, __nv_bfloat16>(p, vi, vo, grid, key, tok, lpr, st)
-                      : launch_reduce<__nv_bfloat16, float>(p, vi, vo, grid, key, tok, lpr, st);
-    return out_bf16 ? launch_reduce<float, __nv_bfloat16>(p, vi, vo, grid, key, tok, lpr, st)
-                    : launch_reduce<float, float>(p, vi, vo, grid, key, tok, lpr, st);
+      return out_bf16 ? launch_reduce<__nv_bfloat16, __nv_bfloat16>(p, vi, vo, grid, pair, lpr, st)
+                      : launch_reduce<__nv_bfloat16, float>(p, vi, vo, grid, pair, lpr, st);
+    return out_bf16 ? launch_reduce<float, __nv_bfloat16>(p, vi, vo, grid, pair, lpr, st)
+                    : launch_reduce<float, float>(p, vi, vo, grid, pair, lpr, st);
   }
   const dim3 block(kReduceThreads);
   if (out_bf16)
-    return vo ? launch_pdl(embed_join_kernel<__nv_bfloat16, true>, grid, block, 0, st, p, key, lpr)
-              : launch_pdl(embed_join_kernel<__nv_bfloat16, false>, grid, block, 0, st, p, key, lpr);
-  return vo ? launch_pdl(embed_join_kernel<float, true>, grid, block, 0, st, p, key, lpr)
-            : launch_pdl(embed_join_kernel<float, false>, grid, block, 0, st, p, key, lpr);
+    return vo ? launch_pdl(embed_join_kernel<__nv_bfloat16, true>, grid, block, 0, st, p, pair, lpr)
+              : launch_pdl(embed_join_kernel<__nv_bfloat16, false>, grid, block, 0, st, p, pair, lpr);
+  return vo ? launch_pdl(embed_join_kernel<float, true>, grid, block, 0, st, p, pair, lpr)
+            : launch_pdl(embed_join_kernel<float, false>, grid, block, 0, st, p, pair, lpr);
 }
 
 }  // namespace va

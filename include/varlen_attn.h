@@ -483,7 +483,8 @@ size_t varlen_token_distill_workspace_size(int32_t T);
  *   ws_dev / ws_bytes   workspace (>= varlen_token_distill_workspace_size(T), 16-byte aligned)
  * Rows need no alignment beyond their type's.  grad may be the logits themselves (same strides).
  * Arithmetic in fp32 per row, the sum over rows in fp64 in a fixed order (deterministic), rounded
- * once.  Limits: K <= 1024, a row of logits within 1,310,720 bytes (VA_ERR_UNSUPPORTED beyond).
+ * once.  Limits: T < 2^30, K <= 1024, 1/64 <= temperature <= 64,
+ * a row of logits within 1,310,720 bytes (VA_ERR_UNSUPPORTED beyond).
  * Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED, VA_ERR_WORKSPACE, VA_ERR_CUDA; the status word
  * gets VA_ERR_BAD_TARGETS when an eligible row lists a class >= V or no row is eligible (then
  * loss is NaN and no gradient is written).  Asynchronous. */
@@ -504,8 +505,8 @@ va_status varlen_token_distill(const void* logits_dev, int32_t dtype, int64_t lo
  *   ids_dev     int32 [T]
  *   out_dev     [T, D] out, row stride out_row_stride, the dtype of the table
  * The product is formed in fp32 and rounded once.  Rows need no alignment beyond their type's
- * (16-byte rows are faster).  Errors: VA_ERR_INVALID_ARG (null pointer, T outside [0, 2^30), V or D < 1,
- * strides below D, alignment, scale not finite), VA_ERR_CUDA.  T = 0 does nothing.  Asynchronous. */
+ * (16-byte rows are faster).  Errors: VA_ERR_INVALID_ARG (null pointer, T outside [0, 2^30), V outside
+ * [1, 2^30), D outside [1, 2^26], strides below D, alignment, scale not finite), VA_ERR_CUDA.  T = 0 does nothing.  Asynchronous. */
 va_status varlen_embed_fwd(const void* table_dev, int32_t dtype, int64_t table_row_stride,
                            const int32_t* ids_dev, int32_t T, int32_t V, int32_t D, float scale,
                            void* out_dev, int64_t out_row_stride, int32_t* status_dev, va_stream_t stream);

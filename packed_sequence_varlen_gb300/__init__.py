@@ -45,6 +45,18 @@ def _ptr(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _int32(x) -> int:
+    """A window or sink count for the library: a larger one sees no more than the largest (ctypes would
+    wrap it around)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
+def _check_sizes(**sizes):
+    for name, n in sizes.items():
+        if not 0 <= n < 2 ** 30:
+            raise ValueError(f"{name} must be below 2^30")
+
+
 def _on(dev: torch.device):
     """Makes ``dev`` the current device for a ``with`` block (nothing to do where it is already)."""
     return contextlib.nullcontext() if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
@@ -160,11 +172,11 @@ def tile_sizes(kind: int, d: int):
 def workspace_size(T, B, Hq, Hkv, d, max_seqlen, for_bwd: bool, window: int | None = None, sinks: int = 0) -> int:
     s = _contig_shape(T, B, Hq, Hkv, d, max_seqlen)
     lib = _lib.load()
-    n = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), -1 if window is None else int(window), int(sinks),
+    n = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), -1 if window is None else _int32(window), _int32(sinks),
                                              int(for_bwd))
     if n == 0:  # the shape check failed: the plan entry point reports why
-        check(lib.varlen_attn_plan_sinks(ctypes.byref(s), None, 0, 1, -1 if window is None else int(window),
-                                         int(sinks), None, 0, None, None, None))
+        check(lib.varlen_attn_plan_sinks(ctypes.byref(s), None, 0, 1, -1 if window is None else _int32(window),
+                                         _int32(sinks), None, 0, None, None, None))
     return n
 
 
@@ -182,9 +194,10 @@ def plan(cu_seqlens: torch.Tensor, T: int, Hq: int, Hkv: int, d: int, max_seqlen
     tm = torch.empty((max(cap, 1), 4), dtype=torch.int32, device=cu_seqlens.device)
     n = torch.zeros(1, dtype=torch.int32, device=cu_seqlens.device)
     scratch = torch.empty(B + 4, dtype=torch.int32, device=cu_seqlens.device)
-    check(_lib.load().varlen_attn_plan_sinks(ctypes.byref(s), _ptr(cu_seqlens), kind, int(causal),
-                                             -1 if window is None else int(window), int(sinks), _ptr(tm), cap,
-                                             _ptr(n), _ptr(scratch), _stream(cu_seqlens.device)))
+    with _on(cu_seqlens.device):
+        check(_lib.load().varlen_attn_plan_sinks(ctypes.byref(s), _ptr(cu_seqlens), kind, int(causal),
+                                                 -1 if window is None else _int32(window), _int32(sinks), _ptr(tm), cap,
+                                                 _ptr(n), _ptr(scratch), _stream(cu_seqlens.device)))
     k = int(n.item())
     return tm[:k], k
 
@@ -215,7 +228,7 @@ def varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = 
     """Forward: returns (out [T,Hq,d] bf16, lse [Hq,T] fp32).  ``window``: causal local window
     (query i sees keys i - window .. i of its segment), None for none.  ``sinks`` (with a
     window): every segment's first tokens that stay visible to all its later queries."""
-    win = -1 if window is None else int(window)
+    win = -1 if window is None else _int32(window)
     _check_inputs(q, k, v)
     T, Hq, d = q.shape
     B = cu_seqlens.numel() - 1
@@ -227,15 +240,16 @@ def varlen_attn_fwd(q, k, v, cu_seqlens, max_seqlen: int, scale: float | None = 
     s = make_shape(q, k, v, B, max_seqlen, out)
     lib = _lib.load()
     need = lib.varlen_attn_workspace_size(ctypes.byref(s), 0)
-    if need == 0:
+    if need == 0:  # the shape check failed: the call reports why
         check(lib.varlen_attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s),
-                                        scale, int(causal), win, int(sinks), _ptr(out), _ptr(lse), _ptr(None), 0,
+                                        scale, int(causal), win, _int32(sinks), _ptr(out), _ptr(lse), _ptr(None), 0,
                                         _stream(q.device)))
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    check(lib.varlen_attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s), scale,
-                                    int(causal), win, int(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
-                                    workspace.numel(), _stream(q.device)))
+    with _on(q.device):
+        check(lib.varlen_attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), ctypes.byref(s), scale,
+                                        int(causal), win, _int32(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
+                                        workspace.numel(), _stream(q.device)))
     if check_status:
         _raise_status(workspace)
     return out, lse
@@ -262,13 +276,15 @@ def varlen_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int,
         raise ValueError("dq must share out's strides and dk/dv k's strides")
     s = make_shape(q, k, v, B, max_seqlen, out)
     lib = _lib.load()
-    need = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), -1 if window is None else int(window), int(sinks), 1)
+    win = -1 if window is None else _int32(window)
+    need = lib.varlen_attn_workspace_size_sinks(ctypes.byref(s), win, _int32(sinks), 1)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    check(lib.varlen_attn_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                                    _ptr(cu_seqlens), ctypes.byref(s), scale, int(causal),
-                                    -1 if window is None else int(window), int(sinks), _ptr(dq), _ptr(dk),
-                                    _ptr(dv), _ptr(workspace), workspace.numel(), _stream(q.device)))
+    with _on(q.device):
+        check(lib.varlen_attn_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                        _ptr(cu_seqlens), ctypes.byref(s), scale, int(causal), win, _int32(sinks),
+                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+                                        _stream(q.device)))
     if check_status:
         _raise_status(workspace)
     return dq, dk, dv
@@ -445,6 +461,7 @@ def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
             logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")
     T, V = logits.shape
+    _check_sizes(T=T, V=V)
     dev = logits.device
     if teacher_ids.dim() != 2 or teacher_ids.dtype != torch.int32 or teacher_ids.shape[0] != T or \
             (teacher_ids.shape[1] > 1 and teacher_ids.stride(1) != 1):
@@ -507,6 +524,7 @@ def embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: t
     dev = table.device
     _check_ids(ids, dev)
     (V, D), T = table.shape, ids.numel()
+    _check_sizes(T=T, V=V, D=D)
     if out is None:
         out = torch.empty((T, D), dtype=table.dtype, device=dev)
     else:
@@ -536,6 +554,7 @@ def embed_bwd(dout: torch.Tensor, ids: torch.Tensor, num_rows: int, scale: float
     dev = dout.device
     _check_ids(ids, dev)
     T, D, V = ids.numel(), dout.shape[1], int(num_rows)
+    _check_sizes(T=T, num_rows=V, D=D)
     if dout.shape[0] != T:
         raise ValueError("dout must be [T, D] with ids [T]")
     if dtable is None:
@@ -569,6 +588,7 @@ class _Embed(torch.autograd.Function):
         return embed_fwd(table, ids, scale)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         (ids,) = ctx.saved_tensors
         return embed_bwd(dout.contiguous(), ids, ctx.num_rows, ctx.scale), None, None

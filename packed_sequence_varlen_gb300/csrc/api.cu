@@ -717,8 +717,8 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
                                int32_t* count, void* grad, int64_t g_rs, void* ws, size_t ws_bytes,
                                va_stream_t stream) {
   if (!logits || !ids || !tl || !loss || !count || !ws) return fail(VA_ERR_INVALID_ARG, "token_distill: null pointer");
-  if (T < 1 || V < 1 || K < 1 || (dtype != 0 && dtype != 1) || (t_dtype != 0 && t_dtype != 1))
-    return fail(VA_ERR_INVALID_ARG, "token_distill: T, V, K >= 1, dtypes 0 or 1");
+  if (T < 1 || T >= (1 << 30) || V < 1 || K < 1 || (dtype != 0 && dtype != 1) || (t_dtype != 0 && t_dtype != 1))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: 1 <= T < 2^30, V and K >= 1, dtypes 0 or 1");
   if (K > 1024) return fail(VA_ERR_UNSUPPORTED, "token_distill: at most 1024 teacher entries per row");
   if (!distill_row_fits(V, dtype == 1 ? 2 : 4))
     return fail(VA_ERR_UNSUPPORTED, "token_distill: a row of logits must stay within 1,310,720 bytes");
@@ -727,8 +727,10 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
   const uintptr_t ea = dtype == 1 ? 1 : 3;
   if ((reinterpret_cast<uintptr_t>(logits) & ea) || (reinterpret_cast<uintptr_t>(grad) & ea))
     return fail(VA_ERR_INVALID_ARG, "token_distill: logits and grad must be aligned to their type");
-  if (!(temperature > 0.f) || !(temperature < INFINITY))
-    return fail(VA_ERR_INVALID_ARG, "token_distill: temperature must be finite and > 0");
+  // The row loss is a difference of logarithms of size ln V held in fp32, times the temperature's
+  // square: at 64 its error reaches 2^12 2^-24 2 ln V = 0.006 for V = 131072, beyond it the loss drowns.
+  if (!(temperature >= 1.f / 64) || !(temperature <= 64.f))
+    return fail(VA_ERR_INVALID_ARG, "token_distill: temperature must be in [1/64, 64]");
   if (!aligned16(ws)) return fail(VA_ERR_INVALID_ARG, "token_distill: workspace must be 16-byte aligned");
   if (ws_bytes < varlen_token_distill_workspace_size(T))
     return fail(VA_ERR_WORKSPACE, "token_distill: workspace too small");
@@ -751,8 +753,10 @@ static va_status check_embed(const char* where, const void* a, const void* b, co
                              float scale) {
   const std::string w(where);
   if (!a || !b || (T > 0 && !ids)) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
-  if (T < 0 || T >= (1 << 30) || V < 1 || D < 1 || V == INT32_MAX || dtype_a < 0 || dtype_a > 1 || dtype_b < 0 || dtype_b > 1)
-    return fail(VA_ERR_INVALID_ARG, w + ": 0 <= T < 2^30, V and D >= 1, V < 2^31 - 1, dtypes 0 or 1");
+  // (D: the columns of the gradient's grid, 2048 a block, stay within 65535 blocks)
+  if (T < 0 || T >= (1 << 30) || V < 1 || V >= (1 << 30) || D < 1 || D > (1 << 26))
+    return fail(VA_ERR_INVALID_ARG, w + ": 0 <= T < 2^30, 1 <= V < 2^30, 1 <= D <= 2^26");
+  if (dtype_a < 0 || dtype_a > 1 || dtype_b < 0 || dtype_b > 1) return fail(VA_ERR_INVALID_ARG, w + ": dtypes 0 or 1");
   if (a_rs < D || b_rs < D) return fail(VA_ERR_INVALID_ARG, w + ": row strides must be >= D");
   if ((reinterpret_cast<uintptr_t>(a) & (dtype_a == 1 ? 1 : 3)) || (reinterpret_cast<uintptr_t>(b) & (dtype_b == 1 ? 1 : 3)))
     return fail(VA_ERR_INVALID_ARG, w + ": pointers must be aligned to their type");

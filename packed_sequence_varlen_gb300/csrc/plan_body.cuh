@@ -157,12 +157,22 @@ __device__ __forceinline__ void head_record(const PlanArgs& a, int l, int lk, in
   if (M::win && M::kv && a.sinks > 0) {
     const int Mq = ceil_p2(l, a.BM), r = div_p2(a.BN, a.BM), S = min(ceil_p2(l, a.BN), ceil_p2(a.sinks, a.BN));
     int j = rr / a.heads;
-    for (int n = 0; n < S; ++n) {
-      const int q = Mq - n * r, k = a.piece > 0 ? ceil_div(q, a.piece) : 1;
+    if (a.piece == 0) {
+      if (j < S) {
+        t.blk = j;
+        t.head = rr - j * a.heads;
+        t.count = Mq - j * r;
+        return;
+      }
+      rr -= S * a.heads;
+      nblk -= S;
+    }
+    for (int n = 0; a.piece > 0 && n < S; ++n) {
+      const int q = Mq - n * r, k = ceil_div(q, a.piece);
       if (j < k) {
         t.blk = n;
         t.head = rr - rr / a.heads * a.heads + j * a.heads;
-        t.count = a.piece > 0 ? min(a.piece, q - j * a.piece) : q;
+        t.count = min(a.piece, q - j * a.piece);
         return;
       }
       j -= k;

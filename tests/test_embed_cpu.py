@@ -47,3 +47,19 @@ def test_python_refusals_without_a_gpu(lib):
         va.embed_fwd(torch.zeros(4, 8), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         va.embed_bwd(torch.zeros(2, 8), torch.zeros(2, dtype=torch.int32), 4)
+
+
+def test_sizes_past_the_kernels_indexes(lib):
+    """Sizes that the 32-bit arguments would wrap, or whose columns exceed the gradient's grid."""
+    import packed_sequence_varlen_gb300 as va
+    assert lib.varlen_embed_fwd(P, 1, 1 << 31, P, 8, 100, (1 << 26) + 1, 1.0, P, 1 << 31, None, None) == 1
+    assert lib.varlen_embed_bwd(None, 0, 1 << 31, None, 0, 1 << 30, 64, 1.0, P, 0, 1 << 31, 0, P, 1 << 40, None) == 1
+    assert lib.varlen_embed_bwd(None, 0, 1 << 31, None, 0, 4, 1 << 29, 1.0, P, 0, 1 << 31, 0, P, 1 << 40, None) == 1
+    with pytest.raises(ValueError):
+        va._check_sizes(num_rows=2 ** 32 + 4)
+    assert va._int32(2 ** 32) == 2 ** 31 - 1 and va._int32(2 ** 32 + 5) == 2 ** 31 - 1 and va._int32(-2 ** 40) == -2 ** 31
+    assert va._int32(-1) == -1 and va._int32(512) == 512
+    # 2^32 sinks are all tokens (a wrapped count would be none, with a smaller or other workspace)
+    big = dict(T=65536, B=1, Hq=12, Hkv=1, d=128, max_seqlen=65536, for_bwd=True)
+    assert va.workspace_size(**big, window=1023, sinks=2 ** 32) == va.workspace_size(**big, window=1023, sinks=65536)
+    assert va.workspace_size(**big, window=1023, sinks=2 ** 32 + 4) != va.workspace_size(**big, window=1023, sinks=4)

@@ -239,3 +239,18 @@ def test_graph_replay_on_a_side_stream(va):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, va.embed_fwd(table, ids, 2.0)) and torch.equal(dt, va.embed_bwd(dout, ids, V, 2.0))
+
+
+def test_second_derivative_is_refused(va):
+    table = torch.randn(5, 8, device=DEV).requires_grad_(True)
+    out = va.embed(table, torch.tensor([1, 3, 1], dtype=torch.int32, device=DEV))
+    w = torch.randn(3, 8, device=DEV).requires_grad_(True)
+    (g,) = torch.autograd.grad(out, table, w, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.square().sum().backward()
+
+
+def test_sizes_past_the_arguments(va):
+    i = torch.zeros(2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):                          # would wrap to 4 rows
+        va.embed_bwd(torch.ones(2, 1, device=DEV), i, 2 ** 32 + 4)

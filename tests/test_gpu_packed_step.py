@@ -126,3 +126,48 @@ def test_two_streams_at_once(va):
         torch.cuda.synchronize()
         for a, b in zip(alone, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_captured_calls_that_share_a_workspace(va):
+    """Three captured calls on one workspace, replayed in turn on one stream: each starts from a
+    workspace that another one has written, and gives what a call with its own gives."""
+    torch.manual_seed(4)
+    lengths = [200, 30, 150]
+    T, V, K = sum(lengths), 900, 8
+    cu = torch.tensor([0, 200, 230, 380], dtype=torch.int32, device=DEV)
+    ids = torch.randint(0, V, (T,), dtype=torch.int32, device=DEV)
+    z, a = torch.randn(T, V, device=DEV).to(torch.bfloat16), torch.randn(T, K, device=DEV)
+    tid = torch.randint(0, V, (T, K), dtype=torch.int32, device=DEV)
+    q, k, v, o, do = (torch.randn(T, 2, 64, device=DEV).to(torch.bfloat16) for _ in range(5))
+    x = torch.randn(T, 64, device=DEV).to(torch.bfloat16)
+    ws = torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)
+
+    def attend(ws=None):
+        o, lse = va.varlen_attn_fwd(q, k, v, cu, 200, window=40, sinks=3, workspace=ws)
+        return (o, lse) + va.varlen_attn_bwd(q, k, v, o, lse, do, cu, 200, window=40, sinks=3, workspace=ws)
+
+    calls = [attend, lambda ws=None: va.token_distill(z, tid, a, workspace=ws),
+             lambda ws=None: (va.embed_bwd(x, ids, V, 2.0, workspace=ws),)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for c in calls:
+            c(ws)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            outs.append(c(ws))
+    for order in ((0, 1, 2), (2, 0, 1), (1, 2, 0)):
+        for t in (q, k, v, do, z, a, x):
+            t.copy_(torch.randn_like(t))
+        ids.copy_(torch.randint_like(ids, V))
+        with torch.cuda.stream(st):
+            st.wait_stream(torch.cuda.default_stream())
+            for i in order:
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for c, out in zip(calls, outs):
+            for got, want in zip(out, c()):
+                assert torch.equal(got, want)

@@ -274,3 +274,16 @@ def test_split_sink_blocks_parity(va):
         for i in (1, 2):
             rows = slice(int(b), int(b) + min(n, s))
             assert wl.rel_l2(got[2][i][rows], rg[i][rows]) <= wl.GRAD_REL_L2
+
+
+def test_window_and_sinks_past_32_bits(va):
+    """A window or sink count beyond 32 bits is the whole segment, not its low word."""
+    cu, cud, mx = boundaries([300, 40])
+    q, k, v, do = si.tensors(int(cu[-1]), 2, 1, 64, seed_offset=21)
+    a = run_both(va, q, k, v, do, cud, mx, 5, 2 ** 32)
+    b = run_both(va, q, k, v, do, cud, mx, 2 ** 32 + 5, 0)
+    ref = run_both(va, q, k, v, do, cud, mx, 5000, 0)
+    for x in (a, b):
+        assert np.abs(x[0] - ref[0]).max() <= wl.O_MAX_ABS and np.abs(x[1] - ref[1]).max() <= wl.LSE_MAX_ABS
+        for y, z in zip(x[2], ref[2]):
+            assert wl.rel_l2(y, z) <= wl.GRAD_REL_L2

@@ -71,6 +71,14 @@ def test_host_side_refusals(lib):
     assert lib.varlen_token_distill_workspace_size(-1) == 0
 
 
+def test_temperature_range_and_sizes(lib):
+    """Outside [1/64, 64] the fp32 loss would drown in the temperature's square; sizes stay below 2^30."""
+    p = ctypes.c_void_p(256)
+    for tau, T in ((64.5, 8), (1e-3, 8), (1e30, 8), (1e-40, 8), (1.0, 1 << 30)):
+        assert lib.varlen_token_distill(p, 1, 100, p, 4, p, 0, 4, None, T, 100, 4, -100, tau, p, p, p, 100, p, 1 << 40,
+                                        None) == 1, (tau, T)
+
+
 def test_python_refusals_without_a_gpu(lib):
     import packed_sequence_varlen_gb300 as va
     with pytest.raises(ValueError):

@@ -49,6 +49,7 @@ constexpr int kSeenBits = 15;
 constexpr int kMaxSlice = 160 << 10; // bytes of a row's slice that one CTA can hold
 constexpr int kSmemBytes = 227 << 10;
 constexpr int kReduceThreads = 1024;
+constexpr int kSmGroups = 16;        // at most, of the GPU
 
 struct DistillParams {
   const void* z;
@@ -68,7 +69,7 @@ struct DistillParams {
   int nparts;
   uint8_t* flags;  // [T] eligible
   double* sums;    // [CTAs of the rows kernel] row losses
-  int ctas;
+  int32_t* ctas;   // their number, from the rows kernel to the reduce kernel
   float* loss;     // {sum, mean}
   int32_t* count;
   int pv;  // 16-byte vectors of a warp's piece (capacity)
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
     sh.total[warp] = n;
     sh.bad[warp] = bad;
   }
+  if (blockIdx.x == 0 && tid == 0) *p.ctas = gridDim.x;
   if (tid == 0) {
     mbar_init(smem_u32(&sh.full), 1);
     mbar_init(smem_u32(&sh.done), NW);
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(kReduceThreads) distill_reduce_kernel(DistillP
   __shared__ int tot[kReduceThreads / 32];
   double acc = 0.0;  // fixed assignment of rows to CTAs, of those to threads, and a fixed order
   if (p.hdr->status == VA_OK)
-    for (int t = threadIdx.x; t < p.ctas; t += kReduceThreads) acc += p.sums[t];
+    for (int t = threadIdx.x, n = *p.ctas; t < n; t += kReduceThreads) acc += p.sums[t];
   int n = 0;
   for (int i = threadIdx.x; i < p.nparts; i += kReduceThreads) n += p.parts[i] & ((1 << 30) - 1);
 #pragma unroll
@@ -708,7 +710,7 @@ namespace {
 int count_blocks(int T) { return std::min(kMaxParts, (T + kCountWarps - 1) / kCountWarps); }
 
 template <class T, bool GRAD>
-cudaError_t launch_rows_t(const DistillParams& p, int grid, size_t smem, cudaStream_t st) {
+cudaError_t launch_rows_t(const DistillParams& p, int grid, int slots, size_t smem, cudaStream_t st) {
   const auto kernel = distill_rows_kernel<T, GRAD>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -718,20 +720,32 @@ cudaError_t launch_rows_t(const DistillParams& p, int grid, size_t smem, cudaStr
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.C > 1 ? 2 : 1;
+  cfg.numAttrs = 2;
+  // Rows are dealt to the clusters beforehand, so all of them have to run at once.  A cluster stays within
+  // one of the GPU's SM groups, which leaves fewer than C slots of each unused: a grid near the limit is cut
+  // to what fits, and starts on an empty GPU rather than in the gaps that the count kernel leaves
+  // (T = 16384, V = 131072 bf16: 110 clusters of four fit, not 114; a second wave made 2010 us out of 1340,
+  // by either cause).
+  if (p.C > 1 && grid + kSmGroups * p.C > slots) {
+    cfg.numAttrs = 1;
+    int most = 0;
+    e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(std::min(grid, std::max(1, most) * p.C));
+  }
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <class T>
-cudaError_t launch_rows(const DistillParams& p, int grid, size_t smem, cudaStream_t st) {
-  return p.grad ? launch_rows_t<T, true>(p, grid, smem, st) : launch_rows_t<T, false>(p, grid, smem, st);
+cudaError_t launch_rows(const DistillParams& p, int grid, int slots, size_t smem, cudaStream_t st) {
+  return p.grad ? launch_rows_t<T, true>(p, grid, slots, smem, st) : launch_rows_t<T, false>(p, grid, slots, smem, st);
 }
 
 }  // namespace
@@ -741,7 +755,7 @@ bool distill_row_fits(int V, int elem) {
   return static_cast<int64_t>(V) * elem <= static_cast<int64_t>(kMaxSlice) * kMaxCluster;
 }
 
-size_t distill_parts_bytes() { return kMaxParts * sizeof(int32_t) + kMaxCtas * sizeof(double); }
+size_t distill_parts_bytes() { return (kMaxParts + 2) * sizeof(int32_t) + kMaxCtas * sizeof(double); }
 
 // The three launches of varlen_token_distill, in this order on one stream.
 cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_rs, const int32_t* ids, int64_t ids_rs,
@@ -750,8 +764,9 @@ cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_r
                                  uint8_t* flags, float* loss, int32_t* count, cudaStream_t st) {
   DistillParams p{z, z_rs, ids, ids_rs, a, a_rs, a_bf16, targets, T, V, K, ignore, temperature, grad, g_rs,
                   static_cast<WsHeader*>(hdr), parts, count_blocks(T), flags,
-                  reinterpret_cast<double*>(parts + kMaxParts), 0, loss, count, 0, 1, kMaxWarps};
+                  reinterpret_cast<double*>(parts + kMaxParts + 2), parts + kMaxParts, loss, count, 0, 1, kMaxWarps};
   if (stage == 0) return launch_pdl(distill_count_kernel, dim3(p.nparts), dim3(32 * kCountWarps), 0, st, p);
+  if (stage == 2) return launch_pdl(distill_reduce_kernel, dim3(1), dim3(kReduceThreads), 0, st, p);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -770,9 +785,8 @@ cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_r
   const size_t smem = static_cast<size_t>(p.NW) * p.pv * 16 + fixed - 1024;
   const int per_sm = std::max<int>(1, std::min<int>(27 / (p.NW + 1), kSmemBytes / static_cast<int>(smem + 1024)));
   const int clusters = std::max(1, std::min(std::min(T, kMaxCtas / p.C), sms * per_sm / p.C));
-  p.ctas = clusters * p.C;
-  if (stage == 2) return launch_pdl(distill_reduce_kernel, dim3(1), dim3(kReduceThreads), 0, st, p);
-  return bf16 ? launch_rows<__nv_bfloat16>(p, p.ctas, smem, st) : launch_rows<float>(p, p.ctas, smem, st);
+  const int grid = clusters * p.C, slots = sms * per_sm;
+  return bf16 ? launch_rows<__nv_bfloat16>(p, grid, slots, smem, st) : launch_rows<float>(p, grid, slots, smem, st);
 }
 
 }  // namespace va

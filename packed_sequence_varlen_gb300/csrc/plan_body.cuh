@@ -90,6 +90,8 @@ __device__ __forceinline__ int win_count(const PlanArgs& a, int l, int blk) {
   return min(Mq, div_p2(blk * a.BN + a.BN - 1 + a.window, a.BM) + 1) - div_p2(blk * a.BN, a.BM);
 }
 
+__device__ __forceinline__ int cut_cost(int64_t c) { return c < INT_MAX ? static_cast<int>(c) : INT_MAX; }
+
 // Blocks of a segment of length l (lk keys under cross-attention) and its total tile count
 // (none for token-tiled segments).
 template <class M>
@@ -104,18 +106,21 @@ __device__ __forceinline__ void seg_cost(const PlanArgs& a, int l, int lk, int& 
   } else if (M::win && !M::kv) {
     // With r = BM / BN, c = ceil(w / BN) and S the key blocks that hold sinks, q block m's window starts
     // at key block max(0, m r - c), so max(0, m r - c - S) of its causal blocks are not listed.
-    const int M_ = ceil_p2(l, a.BM), Lk = ceil_p2(l, a.BN), r = div_p2(a.BM, a.BN);
-    const int x = ceil_p2(a.window, a.BN) + ceil_p2(min(l, a.sinks), a.BN), m1 = min(M_, ceil_p2(x, r));
+    // (64 bits: the squares pass 32 where the counts do not)
+    const int M_ = ceil_p2(l, a.BM), r = div_p2(a.BM, a.BN);
+    const int x = ceil_p2(a.window, a.BN) + ceil_p2(min(l, a.sinks), a.BN);
+    const int64_t m = M_, m1 = min(M_, ceil_p2(x, r));
     nblk = M_;
-    cost = r * (M_ - 1) * M_ / 2 + Lk - (r * (m1 + M_ - 1) * (M_ - m1) / 2 - x * (M_ - m1));
+    cost = cut_cost(r * (m - 1) * m / 2 + ceil_p2(l, a.BN) - (r * (m1 + m - 1) * (m - m1) / 2 - x * (m - m1)));
   } else if (M::win) {
     // With r = BN / BM, kv block n has min(Mq - n r, e) q blocks, e those a window reaches, or (sinks)
     // Mq - n r.
     const int N = ceil_p2(l, a.BN), Mq = ceil_p2(l, a.BM), r = div_p2(a.BN, a.BM);
-    const int e = div_p2(a.BN - 1 + a.window, a.BM) + 1, x = max(0, Mq - e), k = min(N, ceil_p2(x, r));
-    const int S = min(N, ceil_p2(a.sinks, a.BN)), ks = min(S, k);
+    const int e = div_p2(a.BN - 1 + a.window, a.BM) + 1, x = max(0, Mq - e);
+    const int S = min(N, ceil_p2(a.sinks, a.BN));
+    const int64_t n = N, k = min(N, ceil_p2(x, r)), ks = min(static_cast<int64_t>(S), k);
     nblk = N;
-    cost = N * Mq - r * N * (N - 1) / 2 - (k * x - r * k * (k - 1) / 2) + (ks * x - r * ks * (ks - 1) / 2);
+    cost = cut_cost(n * Mq - r * n * (n - 1) / 2 - (k * x - r * k * (k - 1) / 2) + (ks * x - r * ks * (ks - 1) / 2));
     if (a.piece > 0)
       for (int n = 0; n < S; ++n) nblk += ceil_div(Mq - n * r, a.piece) - 1;
   } else if (!M::kv) {

@@ -774,11 +774,20 @@ cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_r
   const int64_t bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
   const auto slice = [&](int C) { return (bytes + C - 1) / C; };
   const size_t fixed = sizeof(DistillSmem) + static_cast<size_t>(K) * 24 + 1024;
-  // CTAs per row: the fewest whose slice fits an SM twice (T = 2047, V = 50003 fp32: 145 us with two
-  // CTAs of 100 KB, 193 with four of 50 KB that fit three times), more while the rows alone leave
-  // SMs idle.  Working warps: 2 KB of the slice and more each.
-  while (p.C < kMaxCluster && slice(p.C) + 16 * kMaxWarps + fixed > kSmemBytes / 2) p.C *= 2;
-  while (p.C < kMaxCluster && static_cast<int64_t>(T) * p.C * 2 <= sms && slice(p.C) > (8 << 10)) p.C *= 2;
+  // CTAs per row: the fewest whose slice fits an SM three times, when that is at most five, else twice, else
+  // once (us a call, bf16 V = 151936, T = 4096: 456 with five CTAs, 522 with four of 76 KB that fit twice,
+  // 596 with eight; fp32 V = 128256, T = 2048: 391 with five that fit twice, 416 with eight that fit three
+  // times; fp32 V = 50257, T = 4096: 293 with three, 296 with two that fit twice).  More while the rows alone
+  // leave SMs idle.  Working warps: 2 KB of the slice and more each.
+  const auto fewest = [&](int per_sm) {
+    int C = 1;
+    while (C <= kMaxCluster && slice(C) + 16 * kMaxWarps + fixed > kSmemBytes / per_sm) ++C;
+    return C;
+  };
+  p.C = fewest(3);
+  if (p.C > 5) p.C = fewest(2);
+  if (p.C > kMaxCluster) p.C = fewest(1);  // (distill_row_fits)
+  while (2 * p.C <= kMaxCluster && static_cast<int64_t>(T) * p.C * 2 <= sms && slice(p.C) > (8 << 10)) p.C *= 2;
   while (p.NW > 1 && slice(p.C) <= static_cast<int64_t>(p.NW) * 2048) p.NW /= 2;
   const int64_t body = bytes / 16;
   p.pv = static_cast<int>((body + p.C * p.NW - 1) / (p.C * p.NW));

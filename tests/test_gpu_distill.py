@@ -245,3 +245,14 @@ def test_graph_replay_on_a_side_stream(va):
         torch.cuda.synchronize()
         l2, c2, g2 = va.token_distill(z, ids, a, tg)
         assert torch.equal(loss, l2) and torch.equal(count, c2) and torch.equal(g, g2)
+
+
+@pytest.mark.parametrize("T,V,K,dtype", [(250, 50257, 40, F32), (20, 50257, 40, F32), (130, 151936, 64, BF), (64, 128256, 9, F32),
+                                         (24, 300007, 33, F32), (40, 100003, 1024, BF)])
+def test_clusters_of_every_size(va, T, V, K, dtype):
+    """Rows over clusters whose size is no power of two, more rows than clusters that fit at once."""
+    z, ids, a, tg = inputs(T, V, K, dtype, V + T)
+    check(va, z, ids, a, tg, 1.5)
+    alone = va.token_distill(z.to(DEV), ids.to(DEV), a.to(DEV), tg.to(DEV), temperature=1.5)
+    again = va.token_distill(z.to(DEV), ids.to(DEV), a.to(DEV), tg.to(DEV), temperature=1.5)
+    assert all(torch.equal(x, y) for x, y in zip(alone, again))

@@ -193,6 +193,12 @@ __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx,
 // kWinSinks: as the window, and the segment's first p.sinks keys are seen by every later query:
 // a kv block that holds one takes its q steps to the segment's end, and those keys are masked
 // on the causal side only.
+// What bounds it: the step, as without a window (products with 64 columns, at most two thirds of the
+// tensor rate); T = 8192, 32 heads, w = 511, s = 4: 133 us, T = 16384, 32/8 heads, w = 1023: 375 us with
+// the tensor pipe active 51%.  P and dS are rounded to bf16 as the products' operands, which shows as
+// 0.0025 of the gradients' L2 norm; the sums stay fp32.
+// kWinSplit: a block that its whole segment sees can outlast the rest of the call; it comes in pieces
+// of p.piece q blocks whose fp32 sums sink_join_kernel adds in order.
 // X: cross-attention (p.cu_k): the kv block's keys come from their own boundaries; query i
 // sees key j when j <= i + lk - lq, so the q steps start at floor(max(0, n*128 - off) / 64).
 template <int D, bool TOK, int WIN, bool X>
@@ -851,6 +857,8 @@ __device__ __forceinline__ QItem q_token_decode_w(const BwdParams& p, int idx, u
 // row, and steps that cross a query's window edge also mask the keys before query - w.
 // kWinSinks: as the window, with the steps that hold the segment's first p.sinks keys (visible to
 // every later query) and that the window does not reach before the window's steps.
+// T = 8192, 32 heads, w = 511, s = 4: 101 us; T = 16384, 32/8 heads, w = 1023: 262 us with the tensor
+// pipe active 53%: bounded by the step, as without a window.
 // X: cross-attention (p.cu_k): the keys come from their own boundaries and query i sees key
 // j when j <= i + lk - lq.
 template <int D, bool TOK, int WIN, bool X>
@@ -1338,14 +1346,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // Sink kv blocks in pieces: dV and scale * dK of a block, the pieces' fp32 sums added in order.  A
-// thread takes 8 columns of a row (grid.z) of a (block, kv head) (grid.y) in every grid.x-th
-// segment; few segments are long enough to be split.
+// thread takes 8 columns of a row (grid.z) of a (block, kv head) (grid.x) in every grid.y-th
+// segment; few segments are long enough to be split.  Bound by the latency of its reads, which come
+// from DRAM after a long dQ kernel: 21 us of a backward of 1270 at T = 65536, 12 q heads on one kv head
+// (69 pieces), 5 of 810 at T = 16384, 32/8 heads.  Four columns a thread, small blocks and sixteen pieces
+// in flight measured no better (32 us).
 template <int D>
 __global__ void __launch_bounds__(256) sink_join_kernel(const BwdParams p) {
   griddep_begin();
   if (p.hdr->status != VA_OK) return;
-  const int n = blockIdx.y % p.sink_blocks, hk = blockIdx.y / p.sink_blocks;
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+  const int n = blockIdx.x % p.sink_blocks, hk = blockIdx.x / p.sink_blocks;
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int s0 = p.cu[b], l = p.cu[b + 1] - s0, q = (l + 63) / 64 - 2 * n;
     if (n * 128 >= l || q <= p.piece) continue;
     const int pieces = (q + p.piece - 1) / p.piece, rows = min(128, l - n * 128);
@@ -1376,7 +1387,7 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const BwdParams p) {
 
 // After the dK/dV and dQ launches of a call whose sink blocks may come in pieces.
 cudaError_t launch_sink_join(const BwdParams& p, int d, cudaStream_t st) {
-  const dim3 grid(std::min(p.B, 64), p.sink_blocks * p.Hkv, 2 * 128 * (d / 8) / 256);
+  const dim3 grid(p.sink_blocks * p.Hkv, std::min(p.B, 64), 2 * 128 * (d / 8) / 256);
   return d == 64 ? launch_pdl(sink_join_kernel<64>, grid, dim3(256), 0, st, p)
                  : launch_pdl(sink_join_kernel<128>, grid, dim3(256), 0, st, p);
 }

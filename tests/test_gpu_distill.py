@@ -256,3 +256,20 @@ def test_clusters_of_every_size(va, T, V, K, dtype):
     alone = va.token_distill(z.to(DEV), ids.to(DEV), a.to(DEV), tg.to(DEV), temperature=1.5)
     again = va.token_distill(z.to(DEV), ids.to(DEV), a.to(DEV), tg.to(DEV), temperature=1.5)
     assert all(torch.equal(x, y) for x, y in zip(alone, again))
+
+
+def test_captured_call_whose_clusters_fill_the_gpu(va):
+    z, ids, a, tg = (x.to(DEV) for x in inputs(400, 131072, 20, BF, 9))
+    want = va.token_distill(z, ids, a, tg)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        va.token_distill(z, ids, a, tg)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        got = va.token_distill(z, ids, a, tg)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))

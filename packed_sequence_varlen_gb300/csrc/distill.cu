@@ -789,7 +789,8 @@ cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_r
   // once (us a call, bf16 V = 151936, T = 4096: 456 with five CTAs, 522 with four of 76 KB that fit twice,
   // 596 with eight; fp32 V = 128256, T = 2048: 391 with five that fit twice, 416 with eight that fit three
   // times; fp32 V = 50257, T = 4096: 293 with three, 296 with two that fit twice).  More while the rows alone
-  // leave SMs idle.  Working warps: 2 KB of the slice and more each.
+  // leave SMs idle.  Working warps: 2 KB of the slice each and more, the more entries the teacher's one warp
+  // has to prepare meanwhile (T = 15738, V = 5127, K = 252 bf16 without gradient: 206 us a call, 224 with 2 KB).
   const auto fewest = [&](int per_sm) {
     int C = 1;
     while (C <= kMaxCluster && slice(C) + 16 * kMaxWarps + fixed > kSmemBytes / per_sm) ++C;
@@ -799,7 +800,7 @@ cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_r
   if (p.C > 5) p.C = fewest(2);
   if (p.C > kMaxCluster) p.C = fewest(1);  // (distill_row_fits)
   while (2 * p.C <= kMaxCluster && static_cast<int64_t>(T) * p.C * 2 <= sms && slice(p.C) > (8 << 10)) p.C *= 2;
-  while (p.NW > 1 && slice(p.C) <= static_cast<int64_t>(p.NW) * 2048) p.NW /= 2;
+  while (p.NW > 1 && slice(p.C) <= static_cast<int64_t>(p.NW) * (2048 + 16 * K)) p.NW /= 2;
   const int64_t body = bytes / 16;
   p.pv = static_cast<int>((body + p.C * p.NW - 1) / (p.C * p.NW));
   const size_t smem = static_cast<size_t>(p.NW) * p.pv * 16 + fixed - 1024;

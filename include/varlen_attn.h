@@ -224,8 +224,9 @@ va_status varlen_attn_plan_window(const va_shape* shape, const int32_t* cu_seqle
  * diagonal to the segment's end, and such blocks of all heads come before the segment's others
  * (block by block, each over the heads).  Other orders as varlen_attn_plan_window; sinks = 0 is that
  * call.
- * (The backward cuts the q range of such a block into several records when it is long and adds
- * their sums; this call lists it as one.)
+ * (In packs of many short segments the calls themselves also plan token records, as varlen_attn_plan
+ * does without a window.  The backward cuts the q range of such a block into several records when
+ * it is long and adds their sums; this call lists it as one.)
  * Errors as it, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */
 va_status varlen_attn_plan_sinks(const va_shape* shape, const int32_t* cu_seqlens_dev, int32_t kind,
                                  int32_t causal, int32_t window, int32_t sinks, int32_t* tile_map_dev,
@@ -269,7 +270,7 @@ va_status varlen_attn_fwd_window(const void* q_dev, const void* k_dev, const voi
  * one softmax over both parts.  The pages have no counterpart: it is the local window of
  * varlen_attn_fwd_window for models whose softmax leans on the first tokens of a document.
  * sinks = 0 is varlen_attn_fwd_window; a window or a sink count of max_seqlen - 1 or more means all of
- * the segment, and such a call is varlen_attn_fwd's.  Else no token tiles, no cross-attention.  As in every attention call, the tiles read
+ * the segment, and such a call is varlen_attn_fwd's.  No cross-attention.  As in every attention call, the tiles read
  * K and V rows past a query's visible keys (later tokens, neighbouring segments): their values
  * carry weight zero and must be finite.  Workspace as varlen_attn_fwd.  Errors as
  * varlen_attn_fwd_window, plus VA_ERR_INVALID_ARG for sinks < 0 or sinks without a window. */

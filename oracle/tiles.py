@@ -88,13 +88,13 @@ def sink_blocks(m: int, l: int, BM: int, BN: int, window, sinks: int) -> int:
 
 
 def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, short: int = 0, window=None,
-                 cu_k=None, sinks: int = 0):
+                 cu_k=None, sinks: int = 0, window_tokens: bool = False):
     """Items as an int32 array [N, 4], in the order above: segment records
     (b, m, h, n_blocks), then (causal, short > 0) token records (-1 - f, t0, h, rows)."""
     cu = [int(x) for x in cu_seqlens]
     cuk = cu if cu_k is None else [int(x) for x in cu_k]
     B = len(cu) - 1
-    tok = [causal and short > 0 and window is None and cu_k is None and cu[b + 1] - cu[b] <= short
+    tok = [causal and short > 0 and (window is None or window_tokens) and cu_k is None and cu[b + 1] - cu[b] <= short
            for b in range(B)]
     items = []
     for b in range(B):
@@ -117,14 +117,14 @@ def fwd_tile_map(cu_seqlens, Hq: int, BM: int, BN: int, causal: bool = True, sho
 
 
 def bwd_tile_map(cu_seqlens, Hkv: int, BM: int, BN: int, causal: bool = True, short: int = 0, window=None,
-                 cu_k=None, sinks: int = 0, piece: int = 0):
+                 cu_k=None, sinks: int = 0, piece: int = 0, window_tokens: bool = False):
     """Items as an int32 array [N, 4], in the order above: segment records
     (b, n, h_kv, n_q), then (causal, short > 0) token records (-1 - f, t0, h_kv, rows)
     whose BN-row tiles hold the key rows [t0, t0 + rows) of a run of short segments."""
     cu = [int(x) for x in cu_seqlens]
     cuk = cu if cu_k is None else [int(x) for x in cu_k]
     B = len(cu) - 1
-    tok = [causal and short > 0 and window is None and cu_k is None and cu[b + 1] - cu[b] <= short
+    tok = [causal and short > 0 and (window is None or window_tokens) and cu_k is None and cu[b + 1] - cu[b] <= short
            for b in range(B)]
     items = []
     for b in range(B):

@@ -113,6 +113,14 @@ bool token_tiles(const va_shape& s, int32_t causal, int32_t window) {
   return causal && window < 0 && static_cast<int64_t>(s.T) < kTokenMeanLen * s.B;
 }
 
+// The calls with a window take token tiles too (their public maps do not list them), in packs of more
+// than 32 segments: with fewer the planner's short path and the forward's one launch less are worth more
+// (T = 446, three segments: forward and backward 65 us, 73 with token tiles; T = 28840, segments of 4 to 17
+// tokens, 8/2 heads of 64, window 1: 835 us without, 156 with).
+bool call_token_tiles(const va_shape& s, int32_t causal, int32_t window) {
+  return token_tiles(s, causal, -1) && (window < 0 || s.B > 32);
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 void tiles(int kind, int* BM, int* BN) {
@@ -462,7 +470,7 @@ static va_status fwd_impl(const void* q, const void* k, const void* v, const int
   }
   int BM, BN;
   tiles(0, &BM, &BN);
-  const bool tok = !cu_k && token_tiles(*s, causal, window);
+  const bool tok = !cu_k && call_token_tiles(*s, causal, window);
   const PlanArgs pa{cu, s->B, s->Hq, BM, BN, 0, causal ? 1 : 0, map, static_cast<int>(L.cap),
                     &hdr->status, &hdr->n_items[0],
                     reinterpret_cast<int32_t*>(w + L.segoff), &hdr->counter[0],
@@ -589,7 +597,7 @@ static va_status bwd_impl(const void* q, const void* k, const void* v, const voi
   int BM, BN, BM2, BN2;
   tiles(1, &BM, &BN);
   tiles(2, &BM2, &BN2);
-  const bool tok = !cu_k && token_tiles(*s, causal, window);
+  const bool tok = !cu_k && L.piece == 0 && call_token_tiles(*s, causal, window);
   int32_t* segoff = reinterpret_cast<int32_t*>(w + L.segoff);
   const PlanArgs pa[2] = {
       {cu, s->B, s->Hkv, BM, BN, 1, causal ? 1 : 0, kvmap, static_cast<int>(L.cap_kv), &hdr->status,

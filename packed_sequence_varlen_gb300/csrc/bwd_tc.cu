@@ -145,7 +145,9 @@ constexpr int kBwdTokenShort = 64;
 // Decodes dK/dV token record idx, {-1 - f, t0, kv head, rows} (whole warp, every lane gets the
 // same item), and writes its row table: the segment starts inside the rows come from
 // cu[f + 1], cu[f + 2], ... (32 per round) as a 128-bit map, and entry r is the next start
-// after row r, or, for the rows of the last segment, that segment's end (qend).
+// after row r, or, for the rows of the last segment, that segment's end (qend).  WIN: entry r is the
+// rows from r to that end instead (at most 64), bit 7 set where r is a sink.
+template <int WIN>
 __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx, uint8_t* table) {
   const TileItem it = p.kv_items[idx];
   const int lane = threadIdx.x & 31, f = -1 - it.seg, t0 = it.blk, rows = it.count;
@@ -164,6 +166,7 @@ __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx,
       break;
     }
   }
+  int last = WIN ? p.cu[f] - t0 : 0;  // start of the segment holding the rows before word w (<= 0 at first)
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const int row = w * 32 + lane;
@@ -172,7 +175,14 @@ __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx,
       if (words[w2]) e = w2 * 32 + __ffs(words[w2]) - 1;
     const uint32_t above = lane == 31 ? 0u : words[w] & (0xffffffffu << (lane + 1));
     if (above) e = w * 32 + __ffs(above) - 1;
-    table[row] = static_cast<uint8_t>(row < rows ? e : 0);
+    if constexpr (WIN != kWinNone) {
+      const uint32_t mine = words[w] & (0xffffffffu >> (31 - lane));
+      const int st = mine ? w * 32 + 31 - __clz(mine) : last;
+      if (words[w]) last = w * 32 + 31 - __clz(words[w]);
+      table[row] = static_cast<uint8_t>(row < rows ? (e - row) | (row - st < p.sinks ? 0x80 : 0) : 0);
+    } else {
+      table[row] = static_cast<uint8_t>(row < rows ? e : 0);
+    }
   }
   __threadfence_block();
   KvItem r;
@@ -199,6 +209,7 @@ __device__ __forceinline__ KvItem kv_token_decode_w(const BwdParams& p, int idx,
 // 0.0025 of the gradients' L2 norm; the sums stay fp32.
 // kWinSplit: a block that its whole segment sees can outlast the rest of the call; it comes in pieces
 // of p.piece q blocks whose fp32 sums sink_join_kernel adds in order.
+// Token items (TOK) hold segments of at most 64 tokens whole, so a window changes their masks alone.
 // X: cross-attention (p.cu_k): the kv block's keys come from their own boundaries; query i
 // sees key j when j <= i + lk - lq, so the q steps start at floor(max(0, n*128 - off) / 64).
 template <int D, bool TOK, int WIN, bool X>
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           out = kv_decode<WIN, X>(p, idx);
           out.valid = 1;
         } else if (idx < n_items) {
-          out = kv_token_decode_w(p, idx, row_tables + (k & 3) * C::KB);
+          out = kv_token_decode_w<WIN>(p, idx, row_tables + (k & 3) * C::KB);
           out.valid = 2;
         } else {
           out = KvItem{};
@@ -661,7 +672,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Token items (runs of short segments; all of them follow the segment items): every step
     // masked on both sides per key row, rows past the item's keys not stored.
     for (KvItem I = J; TOK && ok && tok;) {
-      const int kend = I.s0 + row_tables[(item_cnt & 3) * C::KB + r];  // end of this key's segment
+      // end of this key's segment, or (window) of the queries that see it
+      const int entry = row_tables[(item_cnt & 3) * C::KB + r];
+      const int kend = WIN ? I.s0 + r + ((entry & 0x80) ? entry & 0x7f : min(entry, p.window + 1)) : I.s0 + entry;
       for (int i = 0; i < I.steps; ++i) {
         const int gs = g0 + i, ls = gs % C::LDS, b = i & 1;
         ok = mbar_wait(bar(C::B_LF + ls), (gs / C::LDS) & 1, abort_flag, p.hdr, 19);
@@ -1294,6 +1307,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // key columns c > lim (after the query) and c < lo (before its segment) are masked
         const int k0 = I.kb + n * 64 + cw;
         const int lim = I.s0 + r - k0, lo = klo - k0;
+        // (window) the visible columns: its window's, and its segment's sinks
+        const uint32_t vis = WIN ? (~bits_below(max(lo, lim - p.window)) | (bits_below(lo + p.sinks) & ~bits_below(lo))) &
+                                       bits_below(lim + 1)
+                                 : 0u;
         // one TMEM round trip: this warpgroup's 32 scores and 32 dP values of this q row
         uint32_t sv[32], dpv[32];
         tmem_ld32(s_addr + b * 64, sv);
@@ -1304,8 +1321,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           float x0, x1;
           ffma2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2, -lse2, -lse2);
           float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-          if (c > lim || c < lo) p0 = 0.f;
-          if (c + 1 > lim || c + 1 < lo) p1 = 0.f;
+          if (WIN ? !(vis & (1u << c)) : c > lim || c < lo) p0 = 0.f;
+          if (WIN ? !(vis & (2u << c)) : c + 1 > lim || c + 1 < lo) p1 = 0.f;
           float t0, t1;
           fadd2(t0, t1, __uint_as_float(dpv[c]), __uint_as_float(dpv[c + 1]), -dsum, -dsum);
           dpv[c >> 1] = pack_bf16(p0 * t0, p1 * t1);
@@ -1446,10 +1463,12 @@ static cudaError_t launch_dq_d(const BwdParams& p, int cap, cudaStream_t st) {
 // segment-only kernels keep their own code: the token branch in the softmax item loop
 // measured 15% slower on segment records.
 cudaError_t launch_bwd_dkdv_tc(const BwdParams& p, int d, int cap, bool tok, cudaStream_t st) {
-  if (p.cu_k)  // cross and window calls plan no token records
+  if (p.cu_k)  // cross calls plan no token records
     return d == 64 ? launch_dkdv_d<64, false, kWinNone, true>(p, cap, st) : launch_dkdv_d<128, false, kWinNone, true>(p, cap, st);
   if (p.window >= 0 && p.sinks > 0 && p.piece > 0)
     return d == 64 ? launch_dkdv_d<64, false, kWinSplit, false>(p, cap, st) : launch_dkdv_d<128, false, kWinSplit, false>(p, cap, st);
+  if (p.window >= 0 && tok)
+    return d == 64 ? launch_dkdv_d<64, true, kWinSinks, false>(p, cap, st) : launch_dkdv_d<128, true, kWinSinks, false>(p, cap, st);
   if (p.window >= 0 && p.sinks > 0)
     return d == 64 ? launch_dkdv_d<64, false, kWinSinks, false>(p, cap, st) : launch_dkdv_d<128, false, kWinSinks, false>(p, cap, st);
   if (p.window >= 0)
@@ -1462,6 +1481,8 @@ cudaError_t launch_bwd_dkdv_tc(const BwdParams& p, int d, int cap, bool tok, cud
 cudaError_t launch_bwd_dq_tc(const BwdParams& p, int d, int cap, bool tok, cudaStream_t st) {
   if (p.cu_k)
     return d == 64 ? launch_dq_d<64, false, kWinNone, true>(p, cap, st) : launch_dq_d<128, false, kWinNone, true>(p, cap, st);
+  if (p.window >= 0 && tok)
+    return d == 64 ? launch_dq_d<64, true, kWinSinks, false>(p, cap, st) : launch_dq_d<128, true, kWinSinks, false>(p, cap, st);
   if (p.window >= 0 && p.sinks > 0)
     return d == 64 ? launch_dq_d<64, false, kWinSinks, false>(p, cap, st) : launch_dq_d<128, false, kWinSinks, false>(p, cap, st);
   if (p.window >= 0)

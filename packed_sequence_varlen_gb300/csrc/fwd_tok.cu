@@ -174,6 +174,30 @@ __device__ __forceinline__ float row_max(uint32_t* v, uint32_t need, int lo, int
   return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
 }
 
+// Local window: of the row's segment, which starts at column seg, the columns lo .. lim and the sinks
+// seg .. seg + sinks - 1 stay, as words of visible bits.
+__device__ __forceinline__ float row_max_win(uint32_t* v, uint32_t need, int seg, int sinks, int lo, int lim,
+                                             float sl2) {
+  float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (!(need & (1u << c))) continue;
+    const uint32_t vis = (~bits_below(lo - 32 * c) | (bits_below(seg + sinks - 32 * c) & ~bits_below(seg - 32 * c))) &
+                         bits_below(lim + 1 - 32 * c);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!(vis & (1u << j))) v[32 * c + j] = __float_as_uint(-INFINITY);
+#pragma unroll
+    for (int j = c * 32; j < c * 32 + 32; j += 8) {
+      m0 = fmax3(m0, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      m1 = fmax3(m1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+      m2 = fmax3(m2, __uint_as_float(v[j + 4]), __uint_as_float(v[j + 5]));
+      m3 = fmax3(m3, __uint_as_float(v[j + 6]), __uint_as_float(v[j + 7]));
+    }
+  }
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+}
+
 // p = exp2(s * sl2 - mu) packed in place as bf16 pairs into v[0..63] for the chunks in
 // `need` (the others are left as they are: p_store writes zeros there); returns the row
 // sum.  Chunks go in ascending order: chunk c's packed words v[16c .. 16c+15] overwrite
@@ -214,7 +238,9 @@ __device__ __forceinline__ void p_store(uint32_t s_addr, const uint32_t* v, uint
 
 }  // namespace
 
-template <int D>
+// WIN: causal local window p.window with p.sinks: only the mask differs, since an item's key tiles hold
+// its segments whole.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1)
     fwd_tok_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const FwdParams p) {
@@ -520,7 +546,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float mt;
         row_load(s_addr, v);
         const uint32_t need = chunks_needed(lim_lo, lim);
-        mt = row_max(v, need, lim_lo, lim, sl2);
+        if constexpr (WIN) mt = row_max_win(v, need, lim_lo, p.sinks, max(lim_lo, lim - p.window), lim, sl2);
+        else mt = row_max(v, need, lim_lo, lim, sl2);
         if (n == 0) {
           m_ref = mt;
         } else {
@@ -603,7 +630,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-template <int D>
+template <int D, bool WIN>
 static cudaError_t launch_d(const FwdParams& p, int cap, cudaStream_t st) {
   using C = TcCfg<D>;
   CUtensorMap tq, tk, tv;
@@ -611,11 +638,11 @@ static cudaError_t launch_d(const FwdParams& p, int cap, cudaStream_t st) {
       !tmap_rows(&tk, p.k, p.T, p.Hkv, D, p.k_rs, p.k_hs, 128) ||
       !tmap_rows(&tv, p.v, p.T, p.Hkv, D, p.v_rs, p.v_hs, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(fwd_tok_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(fwd_tok_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // the in-kernel register split assumes the full launch budget; refuse rather than wait
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, fwd_tok_kernel<D>);
+  e = cudaFuncGetAttributes(&fa, fwd_tok_kernel<D, WIN>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   int dev = 0, sms = 0;
@@ -623,11 +650,12 @@ static cudaError_t launch_d(const FwdParams& p, int cap, cudaStream_t st) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = std::min(cap, std::max(sms, 1));
   if (grid <= 0) return cudaSuccess;
-  return launch_pdl(fwd_tok_kernel<D>, dim3(grid), dim3(kTcThreads), C::SMEM, st, tq, tk, tv, p);
+  return launch_pdl(fwd_tok_kernel<D, WIN>, dim3(grid), dim3(kTcThreads), C::SMEM, st, tq, tk, tv, p);
 }
 
 cudaError_t launch_fwd_tok(const FwdParams& p, int d, int cap, cudaStream_t st) {
-  return d == 64 ? launch_d<64>(p, cap, st) : launch_d<128>(p, cap, st);
+  if (p.window >= 0) return d == 64 ? launch_d<64, true>(p, cap, st) : launch_d<128, true>(p, cap, st);
+  return d == 64 ? launch_d<64, false>(p, cap, st) : launch_d<128, false>(p, cap, st);
 }
 
 int fwd_tc_token_short() { return kTokenShort; }

@@ -550,8 +550,13 @@ __device__ __forceinline__ void plan_body(const PlanArgs& a, PlanSmem& sh, const
     return;
   }
   if (a.causal && a.window >= 0) {
-    if (a.kind == 1) plan_body_m<MapKind<true, true, false, true>>(a, sh, cu, seg_off);
-    else plan_body_m<MapKind<false, true, false, true>>(a, sh, cu, seg_off);
+    if (token_mode(a)) {
+      if (a.kind == 1) plan_body_m<MapKind<true, true, true, true>>(a, sh, cu, seg_off);
+      else plan_body_m<MapKind<false, true, true, true>>(a, sh, cu, seg_off);
+    } else {
+      if (a.kind == 1) plan_body_m<MapKind<true, true, false, true>>(a, sh, cu, seg_off);
+      else plan_body_m<MapKind<false, true, false, true>>(a, sh, cu, seg_off);
+    }
     return;
   }
   if (a.kind == 1) {

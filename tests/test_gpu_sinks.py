@@ -228,16 +228,16 @@ def piece_of(T, Hq, Hkv, w, s, mx):
 # both planning paths (up to 32 segments, more), one and several blocks with sinks, split and not
 @pytest.mark.parametrize("w,s", [(0, 1), (100, 4), (1000, 130), (5000, 9), (64, 0), (700, 0), (300, 400)])
 @pytest.mark.parametrize("lengths,Hq,Hkv,d", [(EDGE, 4, 2, 128), ([9001, 1, 3000, 2689, 2690], 12, 1, 128),
-                                              (EDGE * 3 + [5000], 24, 2, 64), ([40], 8, 8, 64)])
+                                              (EDGE * 3 + [5000], 24, 2, 64), ([40], 8, 8, 64),
+                                              (EDGE[:9] * 5, 4, 2, 64)])
 def test_call_maps_bit_exact(va, lengths, Hq, Hkv, d, w, s):
     """The maps the attention calls build for themselves, read back from their workspaces."""
     cu, cud, mx = boundaries(lengths)
     T, B = int(cu[-1]), len(lengths)
     q, k, v, do = (torch.zeros(T, h, d, dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv, Hq))
     kw = dict(window=w, sinks=s)
-    # a window or sinks over the longest segment: the causal call's maps, with its token tiles
+    # a window or sinks over the longest segment: the causal call's maps
     whole = w >= mx - 1 or s >= mx - 1
-    short = 64 if whole and T < 256 * B else 0
     w, s = (None, 0) if whole else (w, s)
     piece = 0 if whole else piece_of(T, Hq, Hkv, w, s, mx)
     blocks = -(-min(s, mx) // 128)
@@ -251,8 +251,9 @@ def test_call_maps_bit_exact(va, lengths, Hq, Hkv, d, w, s):
     qmap = _align256(kvmap + cap * 16)
     for ws, kind, at in ((ws_f, 0, 256), (ws_b, 1, kvmap), (ws_b, 2, qmap)):
         BM, BN = va.tile_sizes(kind, d)
-        ref = (ot.bwd_tile_map(cu, Hkv, BM, BN, True, short, window=w, sinks=s, piece=piece) if kind == 1 else
-               ot.fwd_tile_map(cu, Hq, BM, BN, True, short, window=w, sinks=s))
+        short = 64 if T < 256 * B and (whole or B > 32) and (kind == 0 or not piece) else 0      # token tiles
+        ref = (ot.bwd_tile_map(cu, Hkv, BM, BN, True, short, window=w, sinks=s, piece=piece, window_tokens=True)
+               if kind == 1 else ot.fwd_tile_map(cu, Hq, BM, BN, True, short, window=w, sinks=s, window_tokens=True))
         raw = ws.cpu().numpy()
         assert int(raw[4 + 4 * kind:8 + 4 * kind].view(np.int32)[0]) == len(ref)
         got = raw[at:at + 16 * len(ref)].view(np.int32).reshape(-1, 4)
@@ -291,3 +292,19 @@ def test_window_and_sinks_past_32_bits(va):
         assert np.abs(x[0] - ref[0]).max() <= wl.O_MAX_ABS and np.abs(x[1] - ref[1]).max() <= wl.LSE_MAX_ABS
         for y, z in zip(x[2], ref[2]):
             assert wl.rel_l2(y, z) <= wl.GRAD_REL_L2
+
+
+@pytest.mark.parametrize("w,s", [(0, 1), (1, 0), (3, 2), (7, 70), (20, 5), (63, 1), (100, 30)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64)])
+def test_runs_of_short_segments(va, w, s, Hq, Hkv, d):
+    """Token tiles under a window: runs of segments of 1 to 64 tokens between longer ones."""
+    rng = np.random.default_rng(w + 10 * s)
+    lengths = [1, 64, 2, 63, 65, 300] + rng.integers(1, 65, size=40).tolist() + [130, 1, 1, 1, 90] + \
+        rng.integers(1, 20, size=60).tolist()
+    cu, cud, mx = boundaries(lengths)
+    q, k, v, do = si.tensors(int(cu[-1]), Hq, Hkv, d, seed_offset=31)
+    got = run_both(va, q, k, v, do, cud, mx, w, s)
+    qq, kk, vv, dd = (si.to_f64(x) for x in (q, k, v, do))
+    ro, rl = oa.varlen_forward(qq, kk, vv, cu, window=w, sinks=s)
+    wl.assert_close_outputs(got[0], got[1], ro, rl)
+    wl.assert_close_grads(got[2], oa.varlen_backward(qq, kk, vv, ro, rl, dd, cu, window=w, sinks=s))

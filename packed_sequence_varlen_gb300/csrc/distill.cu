@@ -723,7 +723,9 @@ int count_blocks(int T) { return std::min(kMaxParts, (T + kCountWarps - 1) / kCo
 template <class T, bool GRAD>
 cudaError_t launch_rows_t(const DistillParams& p, int grid, int slots, size_t smem, cudaStream_t st) {
   const auto kernel = distill_rows_kernel<T, GRAD>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The limit is the kernel's, shared by every host thread: always the same, so that no call lowers it
+  // between another's setting and launch.  (A call's own size is the launch's.)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

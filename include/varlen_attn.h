@@ -352,6 +352,12 @@ va_status varlen_noalloc_read_status(int32_t* status_host, va_stream_t stream);
  * call consumes it.  Errors: VA_ERR_INVALID_ARG unless 1 ms <= wait_limit_ns <= 2 s. */
 va_status varlen_test_stall_next_forward(int64_t wait_limit_ns);
 
+/* The same for the next varlen_token_distill call of this process: the first CTA of every row's
+ * cluster loads nothing, every bounded wait gives up after wait_limit_ns, the status word gets
+ * VA_ERR_TIMEOUT, loss is NaN and the gradient's contents are undefined; the context stays usable.
+ * One-shot.  Errors: VA_ERR_INVALID_ARG unless 1 ms <= wait_limit_ns <= 2 s. */
+va_status varlen_test_stall_next_distill(int64_t wait_limit_ns);
+
 /* Copies the workspace status word to *status_host after synchronising the
  * stream.  VA_ERR_CUDA if the copy fails. */
 va_status varlen_read_status(const void* ws_dev, int32_t* status_host, va_stream_t stream);
@@ -488,7 +494,8 @@ size_t varlen_token_distill_workspace_size(int32_t T);
  * a row of logits within 1,310,720 bytes (VA_ERR_UNSUPPORTED beyond).
  * Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED, VA_ERR_WORKSPACE, VA_ERR_CUDA; the status word
  * gets VA_ERR_BAD_TARGETS when an eligible row lists a class >= V or no row is eligible (then
- * loss is NaN and no gradient is written).  Asynchronous. */
+ * loss is NaN and no gradient is written), VA_ERR_TIMEOUT when a bounded wait gave up (loss is NaN, the
+ * gradient is undefined).  Asynchronous. */
 va_status varlen_token_distill(const void* logits_dev, int32_t dtype, int64_t logits_row_stride,
                                const int32_t* teacher_ids_dev, int64_t teacher_ids_row_stride,
                                const void* teacher_logits_dev, int32_t teacher_dtype,

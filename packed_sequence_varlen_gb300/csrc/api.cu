@@ -36,7 +36,7 @@ bool distill_row_fits(int, int);
 size_t distill_parts_bytes();
 cudaError_t launch_token_distill(int, const void*, int, int64_t, const int32_t*, int64_t, const void*, int, int64_t,
                                  const int32_t*, int, int, int, int, float, void*, int64_t, void*, int32_t*, uint8_t*,
-                                 float*, int32_t*, cudaStream_t);
+                                 float*, int32_t*, uint64_t, cudaStream_t);
 size_t embed_bwd_workspace(int, int);
 cudaError_t launch_embed_fwd(const void*, int, int64_t, const int32_t*, int, int, int, float, void*, int64_t, int32_t*,
                              cudaStream_t);
@@ -48,8 +48,8 @@ cudaError_t launch_sink_join(const BwdParams&, int, cudaStream_t);
 void bwd_tc_tiles(int*, int*, int*, int*);
 
 static thread_local std::string g_error;
-// Test hook of the failure path: a wait limit (ns) armed for the next forward call, 0 = none.
-static std::atomic<long long> g_stall_next_fwd{0};
+// Test hooks of the failure paths: a wait limit (ns) armed for the next forward or distillation, 0 = none.
+static std::atomic<long long> g_stall_next_fwd{0}, g_stall_next_distill{0};
 
 void set_error(const char* msg) { g_error = msg; }
 
@@ -760,11 +760,12 @@ va_status varlen_token_distill(const void* logits, int32_t dtype, int64_t l_rs, 
   int32_t* parts = reinterpret_cast<int32_t*>(w + sizeof(WsHeader));
   uint8_t* flags = w + sizeof(WsHeader) + distill_parts_bytes();
   cudaError_t e = cudaSuccess;
+  const uint64_t stall_ns = static_cast<uint64_t>(g_stall_next_distill.exchange(0));
   const KernelId kid[3] = {K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE};
   for (int stage = 0; stage < 3 && e == cudaSuccess; ++stage)
     e = launch(kid[stage], cs, [&] {
       return launch_token_distill(stage, logits, dtype, l_rs, ids, ids_rs, tl, t_dtype, t_rs, targets, T, V, K,
-                                  ignore_index, temperature, grad, g_rs, w, parts, flags, loss, count, cs);
+                                  ignore_index, temperature, grad, g_rs, w, parts, flags, loss, count, stall_ns, cs);
     });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_distill");
 }
@@ -882,6 +883,13 @@ va_status varlen_test_stall_next_forward(int64_t wait_limit_ns) {
   if (wait_limit_ns < 1000000 || wait_limit_ns > 2000000000)
     return fail(VA_ERR_INVALID_ARG, "test_stall_next_forward: the limit must be 1 ms .. 2 s");
   g_stall_next_fwd.store(wait_limit_ns);
+  return VA_OK;
+}
+
+va_status varlen_test_stall_next_distill(int64_t wait_limit_ns) {
+  if (wait_limit_ns < 1000000 || wait_limit_ns > 2000000000)
+    return fail(VA_ERR_INVALID_ARG, "test_stall_next_distill: the limit must be 1 ms .. 2 s");
+  g_stall_next_distill.store(wait_limit_ns);
   return VA_OK;
 }
 

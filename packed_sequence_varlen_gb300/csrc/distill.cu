@@ -75,6 +75,7 @@ struct DistillParams {
   int pv;  // 16-byte vectors of a warp's piece (capacity)
   int C;   // CTAs per row
   int NW;  // working warps per CTA
+  uint64_t wait_ns;  // test hook: a wait limit in ns, and rank 0 of a cluster loads nothing; 0 = none
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
     for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&sh.swapped[x]), NW + 1);
     fence_barrier_init();
     sh.abort_flag = 0;
-    sh.wait_limit = kTimeoutNs;
+    sh.wait_limit = p.wait_ns ? p.wait_ns : kTimeoutNs;
   }
   cluster_arrive();  // (also: every CTA of the cluster runs before one writes into another)
   cluster_wait();
@@ -369,6 +370,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
     const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(zr) & 15u);
     return min(p.V, static_cast<int>(((16u - mis) & 15u) / sizeof(T)));
   };
+  // A warp whose wait gives up ends that row, reading no table that it has not waited for, and takes no
+  // other: whoever counts on it gives up in turn, and nobody goes on with tables or barriers a row ahead.
   bool ok = true;
   // (max, sum of exp2) of this warp's part of the it-th row, to every CTA of the cluster.  A pair of
   // row it + 2 may overwrite one of row it: its warp has seen every pair of row it + 1, and a warp
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
     T* cell = reinterpret_cast<T*>(piece);
     int r0 = rows.next(zero);
     bool loading = r0 >= 0;
-    if (warp == 0 && r0 >= 0) load(r0);
+    if (warp == 0 && r0 >= 0 && !(p.wait_ns && rank == 0)) load(r0);
     int it = 0;
     for (; r0 >= 0; ++it) {
       const int slot = it & 1;
@@ -471,15 +474,16 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
         else sum(std::false_type{}, 0.f);
         publish(it, m, warp_sum(s0 + s1));
       }
-      const int r1 = rows.next(zero);
+      int r1 = rows.next(zero);
       float ls;
       merge(it, m, ls);
+      if (!ok) r1 = -1;  // the last row
       // the logits of the listed classes of this piece
       const int* ids = id_s + slot * p.K;
       const float* pk = p_s + slot * p.K;
       float* zk = z_s + slot * p.K;
       unsigned hits = 0;  // this lane's entries (lane + 32 u) whose class is in the piece
-      for (int k = lane, u = 0; k < p.K; k += 32, ++u) {
+      for (int k = lane, u = 0; ok && k < p.K; k += 32, ++u) {
         const int id = ids[k];
         if (id < c0 || id >= c1) continue;
         hits |= 1u << u;
@@ -536,9 +540,10 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
       if (lane == 0) mbar_arrive(smem_u32(&sh.done));
       if (warp == 0) {
         if (ok) ok = wwait(smem_u32(&sh.done), it & 1, abort_flag, p.hdr, 61);
+        if (!ok) break;
         const T* zr = z + r0 * p.z_rs;
         T* g = GRAD ? grad + r0 * p.g_rs + c0 : nullptr;
-        if (GRAD && ok && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
+        if (GRAD && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
           const int bytes = slice_bytes(zr, c);
           if (lane == 0 && bytes > 0) {
             bulk_store(g, smem_u32(smem), bytes);
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
           }
           __syncwarp();
         }
-        if (r1 >= 0 && ok) {
+        if (r1 >= 0) {
           load(r1);
           loading = true;
         }
@@ -556,8 +561,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
     }
     if (warp == 0 && lane == 0) {
       tma_store_wait_all();
-      const uint64_t t0 = globaltimer();  // a wait gave up: let the copy under way land (bounded again)
-      while (!ok && loading && !mbar_try_wait(smem_u32(&sh.full), (it + 1) & 1) && globaltimer() - t0 < 50000000ull) {
+      const uint64_t t0 = globaltimer();  // row it's wait gave up: let its copy land (bounded again)
+      while (!ok && loading && !mbar_try_wait(smem_u32(&sh.full), it & 1) && globaltimer() - t0 < 50000000ull) {
       }
     }
   } else {
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
       r1 = rows.next(zero);
       if (r1 >= 0) fetch(r1);
     }
-    for (int it = 0; r0 >= 0; ++it) {
+    for (int it = 0; r0 >= 0 && ok; ++it) {
       const int slot = it & 1;
       const int* ids = id_s + slot * p.K;
       const float *pk = p_s + slot * p.K, *zk = z_s + slot * p.K;
@@ -681,6 +686,11 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, 3) distill_rows_kernel(c
   }
   cluster_arrive();  // no CTA leaves while another one may still write into it
   cluster_wait();
+  if (*abort_flag) {  // pairs that nobody waited for may be on their way here: nothing is sent any more, let them land
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kReduceThreads) distill_reduce_kernel(DistillParams p) {
@@ -774,10 +784,11 @@ size_t distill_parts_bytes() { return (kMaxParts + 2) * sizeof(int32_t) + kMaxCt
 cudaError_t launch_token_distill(int stage, const void* z, int bf16, int64_t z_rs, const int32_t* ids, int64_t ids_rs,
                                  const void* a, int a_bf16, int64_t a_rs, const int32_t* targets, int T, int V, int K,
                                  int ignore, float temperature, void* grad, int64_t g_rs, void* hdr, int32_t* parts,
-                                 uint8_t* flags, float* loss, int32_t* count, cudaStream_t st) {
+                                 uint8_t* flags, float* loss, int32_t* count, uint64_t wait_ns, cudaStream_t st) {
   DistillParams p{z, z_rs, ids, ids_rs, a, a_rs, a_bf16, targets, T, V, K, ignore, temperature, grad, g_rs,
                   static_cast<WsHeader*>(hdr), parts, count_blocks(T), flags,
-                  reinterpret_cast<double*>(parts + kMaxParts + 2), parts + kMaxParts, loss, count, 0, 1, kMaxWarps};
+                  reinterpret_cast<double*>(parts + kMaxParts + 2), parts + kMaxParts, loss, count, 0, 1, kMaxWarps,
+                  wait_ns};
   if (stage == 0) return launch_pdl(distill_count_kernel, dim3(p.nparts), dim3(32 * kCountWarps), 0, st, p);
   if (stage == 2) return launch_pdl(distill_reduce_kernel, dim3(1), dim3(kReduceThreads), 0, st, p);
   int dev = 0, sms = 0;

@@ -70,10 +70,12 @@ struct Item {
   int s0, l, h, hk, m, nb, nb0;
   int t1;
   int valid;
-  int kb;  // local window: the item's step n takes key tile kb + n (kWinSinks: from step ns on)
+  int kb;  // local window: the item's step n takes key tile kb + n (kWinSinks: from step ns on, see sk)
   int s0k, lk, off;  // cross-attention: the keys' first row and count, the causal offset lk - l
-  short ns;    // sinks: the first ns steps take the segment's key tiles 0 .. ns - 1
-  short nar;   // the step whose tile holds at most kNarrow sinks and nothing else visible, or -1
+  // sinks: 2 ns + narrow.  The first ns steps take the segment's key tiles 0 .. ns - 1; narrow: the last of
+  // them holds at most kNarrow sinks and nothing else visible.  (One word: as two ints the forward at
+  // d = 128 was 2.7% slower.)
+  int sk;
   int skip1;   // window: the step that q tile 1 does not take (its window starts later), or -1
 };
 static_assert(sizeof(Item) <= 64, "queue slots are 64 bytes");
@@ -93,15 +95,14 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
   if (WIN) r.kb = max(0, r.m * kTcBM - p.window) / kTcBN;
   if (WIN == kWinSinks) {  // the sink tiles that the window does not reach come first
     const int s = min(r.l, p.sinks);
-    r.ns = static_cast<short>(min(r.kb, (s + kTcBN - 1) / kTcBN));
-    // the last of them, when it is the tile that the sinks end in, after at most kNarrow columns
-    const int in_last = s - (r.ns - 1) * kTcBN;
-    r.nar = static_cast<short>(r.ns > 0 && in_last <= kNarrow ? r.ns - 1 : -1);
-    r.kb -= r.ns;
+    const int ns = min(r.kb, (s + kTcBN - 1) / kTcBN);
+    // (narrow: the tile that the sinks end in, after at most kNarrow columns)
+    r.sk = 2 * ns + (ns > 0 && s - (ns - 1) * kTcBN <= kNarrow ? 1 : 0);
+    r.kb -= ns;
   }
   if (WIN) {
     // q tile 1's rows start 128 later: the item's first window tile may end before its window
-    const int first = WIN == kWinSinks ? r.ns : 0, end = (r.kb + first + 1) * kTcBN;
+    const int first = WIN == kWinSinks ? r.sk >> 1 : 0, end = (r.kb + first + 1) * kTcBN;
     r.skip1 = r.t1 && end <= r.m * kTcBM + 128 - p.window && (WIN != kWinSinks || end - kTcBN >= p.sinks) ? first : -1;
   }
   if (X) {  // keys from cu_k; q tile 0 may share its diagonal key tile with tile 1
@@ -116,7 +117,13 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int idx) {
 // The key tile of an item's step n.
 template <int WIN>
 __device__ __forceinline__ int key_tile(const Item& I, int n) {
-  return WIN == kWinSinks ? (n < I.ns ? n : I.kb + n) : (WIN ? I.kb + n : n);
+  return WIN == kWinSinks ? (n < (I.sk >> 1) ? n : I.kb + n) : (WIN ? I.kb + n : n);
+}
+
+// Whether step n is the narrow sink step.
+template <int WIN>
+__device__ __forceinline__ bool narrow_step(const Item& I, int n) {
+  return WIN == kWinSinks && I.sk == 2 * n + 3;
 }
 
 // Masks columns j < lo (but not the sinks j < sk) and j > lim, and returns the row max x sl2
@@ -387,13 +394,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         fence_after_sync();
         ++kv_it;
-        issue_S(0, ks, I.nar == 0);
+        issue_S(0, ks, narrow_step<WIN>(I, 0));
         if (I.nb0 == 1) {
           mma_commit_w(bar(C::B_QE + 0));  // last S_0 of the item: Q tile 0 may be reloaded
           ++qcnt[0];
         }
         if (I.t1) {
-          if (!WIN || I.skip1 != 0) issue_S(1, ks, I.nar == 0);
+          if (!WIN || I.skip1 != 0) issue_S(1, ks, narrow_step<WIN>(I, 0));
           if (I.nb == 1) {
             mma_commit_w(bar(C::B_QE + 1));
             ++qcnt[1];
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             ++pf[0];
             fence_after_sync();
-            issue_PV(0, vs, n > 0, n == I.nar);
+            issue_PV(0, vs, n > 0, narrow_step<WIN>(I, n));
           }
           int ks2 = -1;
           if (n + 1 < I.nb) {
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++kv_it;
             fence_after_sync();
             if (n + 1 < I.nb0) {
-              issue_S(0, ks2, n + 1 == I.nar);
+              issue_S(0, ks2, narrow_step<WIN>(I, n + 1));
               if (n + 1 == I.nb0 - 1) {
                 mma_commit_w(bar(C::B_QE + 0));
                 ++qcnt[0];
@@ -432,12 +439,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             ++pf[1];
             fence_after_sync();
-            issue_PV(1, vs, n > (WIN && I.skip1 == 0 ? 1 : 0), n == I.nar);
+            issue_PV(1, vs, n > (WIN && I.skip1 == 0 ? 1 : 0), narrow_step<WIN>(I, n));
           }
           mma_commit_w(bar(C::B_KVE + vs));
           if (ks2 >= 0) {
             if (I.t1 && (!WIN || n + 1 != I.skip1)) {
-              issue_S(1, ks2, n + 1 == I.nar);
+              issue_S(1, ks2, narrow_step<WIN>(I, n + 1));
               if (n + 1 == I.nb - 1) {
                 mma_commit_w(bar(C::B_QE + 1));
                 ++qcnt[1];
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // (rare); O_t, which holds PV_{n-1}, is then rescaled in TMEM first.
         uint32_t v[128];
         float mt;
-        if (WIN == kWinSinks && n == I.nar) {  // few sinks, all visible: the first kNarrow columns
+        if (narrow_step<WIN>(I, n)) {  // few sinks, all visible: the first kNarrow columns
           tmem_ld32(s_addr, v);
           tmem_wait_ld();
           mt = row_max_narrow(v, p.sinks - n * kTcBN, sl2);
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        if (WIN == kWinSinks && n == I.nar) {
+        if (narrow_step<WIN>(I, n)) {
           lsum += row_exp<kNarrow>(v, sl2, mu);
           tmem_st16(s_addr, v);
         } else {

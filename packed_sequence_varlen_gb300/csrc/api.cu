@@ -113,12 +113,29 @@ bool token_tiles(const va_shape& s, int32_t causal, int32_t window) {
   return causal && window < 0 && static_cast<int64_t>(s.T) < kTokenMeanLen * s.B;
 }
 
-// The calls with a window take token tiles too (their public maps do not list them), in packs of more
-// than 32 segments: with fewer the planner's short path and the forward's one launch less are worth more
-// (T = 446, three segments: forward and backward 65 us, 73 with token tiles; T = 28840, segments of 4 to 17
-// tokens, 8/2 heads of 64, window 1: 835 us without, 156 with).
+// Whether a call with a window takes token tiles (its public maps never list them).  They replace a
+// masked tile per segment and head; they cost the forward a launch and the backward kernel forms that are
+// slower on segment records.  So they need many segments, much of them at most 64 tokens long, which the
+// host sees from the mean, and from a longest segment far above it (then the others lie below it).
+// Small calls are bound by their launches, and up to 32 segments the planner has a short path.
+// Forward + backward in us, device time, without / with token tiles (u: lengths uniform in [m/2, 3m/2], e:
+// exponential; the window's kernels have no other form):
+//   8/2 heads of 64:   u40 T = 30000 242 / 152, u48 T = 19200 144 / 131, u80 T = 30000 163 / 184, u120 T = 8192 59 / 69,
+//                      e40 T = 8192 81 / 71, e80 T = 30000 189 / 185, e120 T = 30000 166 / 184
+//   32/8 heads of 128: u40 T = 8192 314 / 228, u56 T = 30000 844 / 783, u80 T = 8192 234 / 270, u240 T = 30000 632 / 650,
+//                      e64 T = 30000 837 / 750, e80 T = 8192 266 / 272, e120 T = 8192 230 / 248
+//   small calls:       2/1 heads of 64, u40, T = 2400 30 / 40; 8/2 of 64, e48, T = 2880 47 / 53; 8/2 of 64, u24,
+//                      T = 2400 53 / 45; 32/8 of 128, u10, T = 340 72 / 47; 27 segments of 10, 8/2 of 64, 26 / 39
+// (worst choice among 286 measured calls: 2/1 heads of 64, e56, T = 11200, 45 / 52)
+bool window_token_tiles(const va_shape& s) {
+  const int64_t T = s.T, B = s.B, tiles = B * s.Hq;
+  if (B <= 32 || (tiles < 768 && (T < 4096 || T * s.Hq < 16384))) return false;
+  const int64_t mean = 2 * B * s.max_seqlen >= 5 * T ? 96 : 48 + std::min<int64_t>(tiles / 1024, 12);
+  return T < mean * B;
+}
+
 bool call_token_tiles(const va_shape& s, int32_t causal, int32_t window) {
-  return token_tiles(s, causal, -1) && (window < 0 || s.B > 32);
+  return window < 0 ? token_tiles(s, causal, window) : causal && window_token_tiles(s);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
   if (bad) atomicExch(p.status, VA_ERR_BAD_IDS);
 }
 
-// One group of lpr threads per chunk of P sorted tokens (grid.y: further columns).
+// One group of lpr threads per chunk of P sorted tokens (grid.y: further columns).  (The pairs are read
+// coherently: a block may be resident while the sort still writes them, see griddep_begin().)
 template <class TI, class TO, bool VI, bool VO>
 __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const EmbedParams p, const int2* pair,
                                                                       int lpr) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const Embe
   for (int i = lane - 1; i < p.P + 1; i += lpr) {
     const int64_t at = b0 + i;
     const bool in = at >= 0 && at < p.T;
-    const int2 kt = in ? __ldg(pair + at) : make_int2(p.V, 0);
+    const int2 kt = in ? __ldcg(pair + at) : make_int2(p.V, 0);
     keys[i] = kt.x;
     if (i >= 0 && i < p.P) toks[i] = kt.y;
   }
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kReduceThreads) embed_join_kernel(const EmbedP
   __shared__ int found[kReduceThreads], found_last[kReduceThreads], nfound;
   __shared__ float share[kReduceThreads][kW];
   griddep_begin();
-  const auto key = [&](int64_t i) { return __ldg(&pair[i].x); };
+  const auto key = [&](int64_t i) { return __ldcg(&pair[i].x); };
   const int groups = kReduceThreads / lpr, g = threadIdx.x / lpr, lane = threadIdx.x % lpr;
   if (threadIdx.x == 0) nfound = 0;
   __syncthreads();

@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(32 * kCountWarps) distill_count_kernel(Distill
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int n = 0, bad = 0;
   for (int row = blockIdx.x * kCountWarps + warp; row < p.T; row += gridDim.x * kCountWarps) {
-    // (target, ids and logits are loaded side by side: one latency, not three)
-    const bool has = !p.targets || __ldg(p.targets + row) != p.ignore;
+    // (target, ids and logits are loaded side by side: one latency, not three; the target by a coherent
+    // load, since the kernel that writes the targets may still run when this one becomes resident)
+    const bool has = !p.targets || p.targets[row] != p.ignore;
     bool any = false;
     for (int k0 = lane; k0 < p.K; k0 += 32 * kBatch) {
       int id[kBatch];

@@ -52,8 +52,9 @@ Local window w (causal; section 5: "causal or local window further narrows
 n_block_min/max"): q block m's key blocks run from n_min = floor(max(0, m*BM - w) / BN)
 to its diagonal, count = n_max - n_min; kv block n's q blocks run from its diagonal
 floor(n*BN / BM) to floor((n*BN + BN - 1 + w) / BM) (capped by the segment).  Window
-maps have no token records and keep each segment's blocks in block order (q blocks
-descending, kv blocks ascending), which is the no-window order as well.  With sinks s a
+maps keep each segment's blocks in block order (q blocks descending, kv blocks ascending),
+which is the no-window order as well.  They have token records where ``window_tokens`` asks
+for them: the planning call's have none, the attention calls' own maps may.  With sinks s a
 q block also lists the key blocks that hold the segment's first s keys and that lie before
 n_min, count = both parts, and a kv block with n*BN < s keeps its q blocks to the segment's
 end; such blocks of all heads come first in their segment.

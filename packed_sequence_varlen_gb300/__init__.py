@@ -404,7 +404,11 @@ def token_ce(logits: torch.Tensor, targets: torch.Tensor, ignore_index: int = IG
     """Token-weighted cross entropy of the packed stream: returns (loss [2] float64 device
     tensor {sum, mean}, count [1] int32, grad or None).  ``logits`` is CUDA fp32 or bf16
     [T, V] with a contiguous last dim; ``grad`` True allocates d(mean)/d(logits) like
-    ``logits``, a tensor receives it, False skips it."""
+    ``logits``, a tensor receives it, False skips it.
+
+    An eligible target outside [0, V), or no eligible target at all, is an error found on the device: loss is
+    NaN and the gradient is left as it was (uninitialised where this call allocated it);
+    ``check_status`` raises."""
     if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1 or \
             logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")
@@ -456,7 +460,11 @@ def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logit
     skipped (None: no row is).  Row t adds temperature^2 KL(p || q), p the softmax of its teacher
     logits / temperature, q the softmax of all its logits / temperature; the mean is over the rows
     that have a target and an entry.  ``grad`` True allocates d(mean)/d(logits) like ``logits``, a
-    tensor receives it (``logits`` itself is fine), False skips it."""
+    tensor receives it (``logits`` itself is fine), False skips it.
+
+    An eligible row that lists a class >= V, or no eligible row at all, is an error found on the device: loss is
+    NaN and the gradient is left as it was (uninitialised where this call allocated it);
+    ``check_status`` raises."""
     if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1 or \
             logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")

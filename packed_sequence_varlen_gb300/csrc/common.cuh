@@ -52,8 +52,7 @@ struct PlanArgs {
                       // (records {-1 - f, t0, head, rows}); 0 = off
   int32_t* n_tok;     // may be null: out, the number of token records (the map's last ones)
   int32_t* tok_counter;  // may be null: the token kernel's work counter; zeroed here
-  int window = -1;       // causal local window w >= 0 (query i sees keys i-w..i), -1 = none;
-                         // window maps have no token records
+  int window = -1;       // causal local window w >= 0 (query i sees keys i-w..i), -1 = none
   const int32_t* cu_k = nullptr;  // cross-attention: the K/V boundaries (cu is Q's); null = cu
   int sinks = 0;         // with a window: a segment's first keys that every later query still sees
   int piece = 0;         // kv maps with sinks: q blocks per record of a block that holds sinks; 0 = all

@@ -228,7 +228,8 @@ __device__ __forceinline__ float row_exp(uint32_t* v, float sl2, float mu) {
 // Window items are short, and their tiles partly masked: at T = 8192, 32 heads, w = 511, s = 4 the
 // kernel takes 82 us, 26 of them tensor work on visible pairs at the measured peak, 36 on whole tiles;
 // the rest is the step's latency and the item's end.  At T = 16384, w = 1023 the tensor pipe is active
-// 49% of the time.  P is rounded to bf16, the type of the second product's operands, as without a
+// 49% of the time.  (The d = 128 sinks form is the only one that spills, 20 bytes at the 168 registers of its
+// launch.)  P is rounded to bf16, the type of the second product's operands, as without a
 // window; maxima, sums and O stay fp32.
 // X: cross-attention (p.cu_k): keys from their own boundaries, the causal bound aligned
 // bottom-right (key j visible to query i when j <= i + lk - lq), so the masked key tiles are

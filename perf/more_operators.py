@@ -239,7 +239,8 @@ def _own_scan(st):
     h, last = va.varlen_scan_fwd(st["x"], st["g"], st["cu"], h0=st["h0"], h_last=st["state"])
     got = [h, last] if st["state"] else [h]
     if st["train"]:
-        dx, dg, dh0 = va.varlen_scan_bwd(st["dh"], h, st["g"], st["cu"], h0=st["h0"], dh_last=st["dlast"])
+        dx, dg, dh0 = va.varlen_scan_bwd(st["dh"], h, st["g"], st["cu"], h0=st["h0"], dh_last=st["dlast"],
+                                         x_dtype=st["x"].dtype)
         got += [dx, dg, dh0] if st["state"] else [dx, dg]
     return got
 

@@ -538,6 +538,141 @@ va_status varlen_embed_bwd(const void* dout_dev, int32_t dtype, int64_t dout_row
                            void* dtable_dev, int32_t table_dtype, int64_t dtable_row_stride,
                            int32_t accumulate, void* ws_dev, size_t ws_bytes, va_stream_t stream);
 
+/* ---------------------------------------------------------------- query / key norm with rotation
+ * The step between the projections and the attention: every query and key head is divided by its root mean
+ * square, scaled by a weight and turned by its token's position.  The pages start at Q and K and have no
+ * counterpart; positions are varlen_build_metadata's position_ids.  For a head x of d elements
+ *     r = 1 / sqrt(mean(x^2) + eps),  u = x r w,
+ * and the pair i of u's first rot elements, (a, b) = (u_i, u_{i + rot/2}), or (u_{2i}, u_{2i+1}) when interleaved,
+ * becomes (a cos f - b sin f, b cos f + a sin f) with f = position * inv_freq[i]; the other elements stay.  f is
+ * formed in whole 2^-64 turns, so far positions lose nothing. */
+typedef struct {
+  int32_t T, Hq, Hkv, d, rot;  /* tokens, heads, head size (a multiple of 8, <= 256), turned elements (a multiple of 8) */
+  int32_t dtype;               /* q, k, outputs and their gradients: 0 = fp32, 1 = bf16 */
+  int32_t weight_dtype;        /* the weights and their gradients: 0 = fp32, 1 = bf16 */
+  int32_t interleaved;         /* pairs (2i, 2i + 1) instead of (i, i + rot/2) */
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride;      /* elements */
+  int64_t qo_row_stride, qo_head_stride, ko_row_stride, ko_head_stride;  /* outputs (backward: their gradients) */
+} va_qk_shape;
+
+typedef struct {
+  int64_t dq_row_stride, dq_head_stride, dk_row_stride, dk_head_stride;  /* elements */
+} va_qk_grad_strides;
+
+/* Forward.
+ *   q_dev [T, Hq, d], k_dev [T, Hkv, d]  in; head elements contiguous
+ *   position_ids_dev  int32 [T]
+ *   q_weight_dev, k_weight_dev  [d], NULL: ones
+ *   inv_freq_dev      float [rot / 2] (NULL when rot is 0)
+ *   q_out_dev, k_out_dev  out; may be the inputs themselves (same strides)
+ * Pointers 16-byte aligned, strides multiples of 8 elements, as the attention's.  T = 0 does nothing.  Arithmetic in
+ * fp32, rounded once.  Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED (d, rot), VA_ERR_CUDA.  Asynchronous. */
+va_status varlen_qk_norm_rope_fwd(const void* q_dev, const void* k_dev, const int32_t* position_ids_dev,
+                                  const void* q_weight_dev, const void* k_weight_dev, const float* inv_freq_dev,
+                                  const va_qk_shape* shape, float eps, void* q_out_dev, void* k_out_dev,
+                                  va_stream_t stream);
+
+/* Bytes of workspace varlen_qk_norm_rope_bwd needs (0: d is refused). */
+size_t varlen_qk_norm_rope_bwd_workspace_size(int32_t d);
+
+/* Backward: with g the outputs' gradient turned back and n = x r,
+ *     dw = sum over tokens and heads of g n,   dx = r (g w - n mean(g w n)).
+ *   dq_out_dev, dk_out_dev  the outputs' gradients (shape's output strides)
+ *   q_dev, k_dev            the forward's inputs
+ *   dq_dev, dk_dev          out (grad_strides); may be dq_out / dk_out or q / k themselves (same strides)
+ *   dq_weight_dev, dk_weight_dev  [d] out, or NULL for none; a weight's gradient needs the weight
+ *   ws_dev / ws_bytes       workspace (16-byte aligned; NULL when no weight gradient is wanted)
+ * Weight gradients are fp32 sums in a fixed order, rounded once.  Errors as the forward, plus VA_ERR_WORKSPACE. */
+va_status varlen_qk_norm_rope_bwd(const void* dq_out_dev, const void* dk_out_dev, const void* q_dev, const void* k_dev,
+                                  const int32_t* position_ids_dev, const void* q_weight_dev, const void* k_weight_dev,
+                                  const float* inv_freq_dev, const va_qk_shape* shape,
+                                  const va_qk_grad_strides* grad_strides, float eps, void* dq_dev, void* dk_dev,
+                                  void* dq_weight_dev, void* dk_weight_dev, void* ws_dev, size_t ws_bytes,
+                                  va_stream_t stream);
+
+/* ---------------------------------------------------------------- gated recurrence
+ * The other mixer of a packed stream's tokens: per channel
+ *     h_t = exp(g_t) h_{t-1} + x_t,
+ * restarted at every segment of cu_seqlens from h0[b] (0 without h0).  The pages have no counterpart (they name
+ * linear attention only); the boundaries are the attention's contract. */
+typedef struct {
+  int32_t T, B, D;        /* tokens, segments, channels */
+  int32_t x_dtype;        /* x and dx: 0 = fp32, 1 = bf16 */
+  int32_t gate_dtype;     /* log_decay and its gradient; fp32 x takes fp32 only */
+  int64_t x_row_stride, gate_row_stride, h_row_stride;  /* elements, >= D; h (and dh): bf16 when both types are, else fp32 */
+} va_scan_shape;
+
+typedef struct {
+  int64_t dh_row_stride, dx_row_stride, dgate_row_stride;  /* elements, >= D */
+} va_scan_grad_strides;
+
+/* Bytes of workspace varlen_scan_fwd and varlen_scan_bwd need (status word at byte 0; 0: sizes are refused). */
+size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D);
+
+/* Forward.
+ *   x_dev, log_decay_dev  [T, D]; decays are meant to be <= 0 (the decay of any run of 16 rows has to stay finite)
+ *   h0_dev      float [B, D], or NULL
+ *   h_dev       [T, D] out; may be x itself (same type and stride)
+ *   h_last_dev  float [B, D] out: the state after each segment, or NULL; for single tokens (T == B) it may be h0
+ *               itself, otherwise they must not overlap
+ *   ws_dev / ws_bytes  workspace (>= varlen_scan_workspace_size, 16-byte aligned)
+ * States are fp32 from row to row, h is rounded when stored.  Nothing of a segment reaches another, non-finite
+ * values included.  Results do not change from call to call.  T == B (every segment one token) is one launch.
+ * Errors: VA_ERR_INVALID_ARG (1 <= B <= T < 2^30, 1 <= D <= 2^20, strides, alignment), VA_ERR_UNSUPPORTED,
+ * VA_ERR_WORKSPACE, VA_ERR_CUDA; the status word gets VA_ERR_BAD_SEQLENS (h unwritten, T == B: unwritten where it
+ * is wrong) or VA_ERR_TIMEOUT (a bounded wait gave up, h undefined).  Asynchronous. */
+va_status varlen_scan_fwd(const void* x_dev, const void* log_decay_dev, const int32_t* cu_seqlens_dev,
+                          const va_scan_shape* shape, const float* h0_dev, void* h_dev, float* h_last_dev,
+                          void* ws_dev, size_t ws_bytes, va_stream_t stream);
+
+/* Backward: e_t = dh_t + exp(g_{t+1}) e_{t+1} (a segment's last row: dh_t + dh_last[b]),
+ *     dx_t = e_t,   dg_t = e_t exp(g_t) h_{t-1},   dh0[b] = exp(g_first) e_first.
+ *   dh_dev [T, D] in h's type; h_dev the forward's result; h0_dev as in the forward
+ *   dh_last_dev  float [B, D], or NULL (zeros)
+ *   dx_dev, dlog_decay_dev  [T, D] out, in x's and log_decay's types; dx may be dh, dlog_decay may be log_decay
+ *               (same type and stride), neither may overlap h
+ *   dh0_dev      float [B, D] out, or NULL; apart from h0 and dh_last
+ * Errors as the forward. */
+va_status varlen_scan_bwd(const void* dh_dev, const void* h_dev, const void* log_decay_dev,
+                          const int32_t* cu_seqlens_dev, const va_scan_shape* shape,
+                          const va_scan_grad_strides* grad_strides, const float* h0_dev, const float* dh_last_dev,
+                          void* dx_dev, void* dlog_decay_dev, float* dh0_dev, void* ws_dev, size_t ws_bytes,
+                          va_stream_t stream);
+
+/* ---------------------------------------------------------------- token log probabilities
+ * What scoring, evaluation and policy-gradient steps read off the packed logits.  The pages have no counterpart;
+ * rows and targets are varlen_token_ce's.  Row t, p = softmax(z / temperature):
+ *     lse = ln sum exp(z / temperature),  logprob = ln p[token],  entropy = -sum p ln p,
+ * and the k largest logits' ids with their ln p, largest first, equal logits by the lower id.
+ *   logits_dev  [T, V], row stride logits_row_stride elements; dtype 0 = fp32, 1 = bf16
+ *   tokens_dev  int32 [T]: a class in [0, V), or ignore_index: the row is not read, its outputs are 0 and its ids -1
+ *   logprob_dev, entropy_dev, lse_dev  float [T] out
+ *   top_ids_dev int32 [T, k], top_logprobs_dev float [T, k] out (NULL when k = 0); k <= min(V, 128)
+ *   status_dev  int32 [1], set to VA_ERR_BAD_TARGETS when a token is outside [0, V) (logprob NaN; left untouched
+ *               otherwise; NULL: not reported)
+ * A logit of -inf has probability 0; a row of nothing but -inf, or with a +inf or a NaN, gives NaN.  (With a NaN its
+ * top_ids are some ids of the row.)  Arithmetic in fp32.  Rows need no alignment beyond their type's (16-byte rows are
+ * faster).  Errors: VA_ERR_INVALID_ARG (T, V outside [1, 2^30), k, strides, alignment, temperature outside
+ * [1/64, 64]), VA_ERR_UNSUPPORTED (k > 128), VA_ERR_CUDA.  Asynchronous. */
+va_status varlen_token_logprobs_fwd(const void* logits_dev, int32_t dtype, int64_t logits_row_stride,
+                                    const int32_t* tokens_dev, int32_t T, int32_t V, int32_t k, int32_t ignore_index,
+                                    float temperature, float* logprob_dev, float* entropy_dev, float* lse_dev,
+                                    int32_t* top_ids_dev, float* top_logprobs_dev, int32_t* status_dev,
+                                    va_stream_t stream);
+
+/* The logits' gradient for given gradients of logprob and entropy,
+ *     dz_c = (dlogprob ([c == token] - p_c) - dentropy p_c (ln p_c + entropy)) / temperature.
+ *   lse_dev, entropy_dev        the forward's (entropy NULL without dentropy)
+ *   dlogprob_dev, dentropy_dev  float [T] (dentropy NULL: none)
+ *   grad_dev    [T, V] out in the logits' type (row stride grad_row_stride); may be the logits (same stride).
+ *               Rows with ignore_index are zero, rows with a token outside [0, V) NaN
+ * Errors as the forward.  Asynchronous. */
+va_status varlen_token_logprobs_bwd(const void* logits_dev, int32_t dtype, int64_t logits_row_stride,
+                                    const int32_t* tokens_dev, const float* lse_dev, const float* entropy_dev,
+                                    const float* dlogprob_dev, const float* dentropy_dev, int32_t T, int32_t V,
+                                    int32_t ignore_index, float temperature, void* grad_dev, int64_t grad_row_stride,
+                                    va_stream_t stream);
+
 /* ---------------------------------------------------------------- tracing
  * Per-launch timing.  With capacity > 0, the library records a CUDA event pair
  * on the launching stream around each of the next `capacity` kernel launches

@@ -18,7 +18,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import VarlenError, VaShape, check
+from ._lib import VarlenError, VaQkGradStrides, VaQkShape, VaScanGradStrides, VaScanShape, VaShape, check
 
 __all__ = [
     "pack_next_fit", "pack_best_fit_decreasing", "build_metadata", "validate_cu_seqlens",
@@ -26,6 +26,8 @@ __all__ = [
     "read_status", "VarlenError", "make_shape", "library_path", "loss_targets", "token_ce",
     "IGNORE_INDEX", "unpad_index", "gather_rows", "unpad", "pad", "plan_cross", "varlen_attn_fwd_cross",
     "varlen_attn_bwd_cross", "token_distill", "embed_fwd", "embed_bwd", "embed",
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope", "varlen_scan_fwd", "varlen_scan_bwd", "varlen_scan",
+    "token_logprobs_fwd", "token_logprobs_bwd", "token_logprobs",
 ]
 
 
@@ -605,6 +607,378 @@ class _Embed(torch.autograd.Function):
 def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
     """Differentiable token embedding of the packed stream: scale * table[ids], [T, D]."""
     return _Embed.apply(table, ids, scale)
+
+
+# ----------------------------------------------------------------- query / key norm with rotation
+
+def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None):
+    if not t.is_cuda or t.dim() != 3 or t.dtype not in _FLOATS or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a CUDA fp32/bf16 [T, H, d] tensor with a contiguous last dim")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match its input in shape, dtype and device")
+
+
+def _head_strides(t: torch.Tensor):
+    """Row and head strides; those of an extent of one are never used and may be anything."""
+    T, H, d = t.shape
+    hs = t.stride(1) if H > 1 else d
+    return (t.stride(0) if T > 1 else H * hs), hs
+
+
+def _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved):
+    _check_heads("q", q)
+    _check_heads("k", k)
+    T, Hq, d = q.shape
+    dev = q.device
+    if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype:
+        raise ValueError("q [T, Hq, d] and k [T, Hkv, d] must agree in T, d and dtype")
+    _check_sizes(T=T)
+    if position_ids.shape != (T,) or position_ids.dtype != torch.int32 or not position_ids.is_contiguous():
+        raise ValueError("position_ids must be a contiguous int32 [T] tensor")
+    s = VaQkShape()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if w.shape != (d,) or w.dtype not in _FLOATS or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32/bf16 [d] tensor")
+        s.weight_dtype = int(w.dtype == torch.bfloat16)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous fp32 [rot / 2] tensor")
+        rot = 2 * inv_freq.numel()
+    _same_device(dev, k=k, position_ids=position_ids, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq)
+    s.T, s.Hq, s.Hkv, s.d, s.rot = T, Hq, k.shape[1], d, rot
+    s.dtype, s.interleaved = int(q.dtype == torch.bfloat16), int(bool(interleaved))
+    s.q_row_stride, s.q_head_stride = _head_strides(q)
+    s.k_row_stride, s.k_head_stride = _head_strides(k)
+    return s
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tensor,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                     inv_freq: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Root-mean-square norm of every head with the position rotation: returns (q_out, k_out).
+
+    ``q`` [T, Hq, d] and ``k`` [T, Hkv, d] CUDA fp32 or bf16 (views of a fused projection are fine); ``q_weight`` /
+    ``k_weight`` [d] fp32 or bf16 (None: ones); ``inv_freq`` fp32 [rot / 2]: the first rot elements of a head
+    are turned by position * inv_freq, in pairs (i, i + rot / 2) or, ``interleaved``, (2 i, 2 i + 1)
+    (None: none is).  ``q_out`` / ``k_out`` None allocates them contiguous; q and k themselves are fine."""
+    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _check_heads("q_out", q_out, q)
+    _check_heads("k_out", k_out, k)
+    s.qo_row_stride, s.qo_head_stride = _head_strides(q_out)
+    s.ko_row_stride, s.ko_head_stride = _head_strides(k_out)
+    with _on(q.device):
+        check(_lib.load().varlen_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(position_ids), _ptr(q_weight), _ptr(k_weight),
+                                                  _ptr(inv_freq), ctypes.byref(s), float(eps), _ptr(q_out),
+                                                  _ptr(k_out), _stream(q.device)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     position_ids: torch.Tensor, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                     workspace=None):
+    """Gradient of ``qk_norm_rope_fwd``: returns (dq, dk, dq_weight, dk_weight), a weight's None where it is.
+    ``dq`` / ``dk`` None allocates them contiguous; views of a fused gradient are fine.  The weights'
+    gradients are summed in fp32 in a fixed order (deterministic) and have the weights' dtype."""
+    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved)
+    _check_heads("dq_out", dq_out, q)
+    _check_heads("dk_out", dk_out, k)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _check_heads("dq", dq, q)
+    _check_heads("dk", dk, k)
+    s.qo_row_stride, s.qo_head_stride = _head_strides(dq_out)
+    s.ko_row_stride, s.ko_head_stride = _head_strides(dk_out)
+    gs = VaQkGradStrides(*_head_strides(dq), *_head_strides(dk))
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    lib = _lib.load()
+    size = 0
+    if dqw is not None or dkw is not None:
+        need = lib.varlen_qk_norm_rope_bwd_workspace_size(s.d)
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        _same_device(q.device, workspace=workspace)
+        size = workspace.numel()
+    with _on(q.device):
+        check(lib.varlen_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(position_ids),
+                                          _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), ctypes.byref(s),
+                                          ctypes.byref(gs), float(eps), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw),
+                                          _ptr(workspace), size, _stream(q.device)))
+    return dq, dk, dqw, dkw
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, position_ids, q_weight, k_weight, inv_freq, eps, interleaved):
+        ctx.save_for_backward(q, k, position_ids, q_weight, k_weight, inv_freq)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return qk_norm_rope_fwd(q, k, position_ids, q_weight, k_weight, inv_freq, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, pos, qw, kw, inv_freq = ctx.saved_tensors
+        dq, dk, dqw, dkw = qk_norm_rope_bwd(dq_out.contiguous(), dk_out.contiguous(), q, k, pos, qw, kw, inv_freq,
+                                            ctx.eps, ctx.interleaved)
+        return dq, dk, None, dqw, dkw, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tensor, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Differentiable ``qk_norm_rope_fwd``: (q_out, k_out), ready for ``varlen_attn``."""
+    return _QkNormRope.apply(q, k, position_ids, q_weight, k_weight, inv_freq, eps, interleaved)
+
+
+# ----------------------------------------------------------------- gated recurrence
+
+def _scan_shape(x, log_decay, cu_seqlens, name="x"):
+    _check_rows(name, x)
+    _check_rows("log_decay", log_decay)
+    T, D = x.shape
+    if log_decay.shape != x.shape:
+        raise ValueError(f"log_decay must have {name}'s shape")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32 or \
+            not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 [B + 1] tensor")
+    _check_sizes(T=T, D=D)
+    _same_device(x.device, log_decay=log_decay, cu_seqlens=cu_seqlens)
+    s = VaScanShape()
+    s.T, s.B, s.D = T, cu_seqlens.numel() - 1, D
+    s.gate_dtype, s.gate_row_stride = int(log_decay.dtype == torch.bfloat16), _row_stride(log_decay)
+    return s
+
+
+def _check_state(name: str, t, s: VaScanShape, dev):
+    if t is None:
+        return
+    if t.dtype != torch.float32 or t.shape != (s.B, s.D) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 [B, D] tensor")
+    _same_device(dev, **{name: t})
+
+
+def _scan_workspace(lib, s: VaScanShape, workspace, dev):
+    need = lib.varlen_scan_workspace_size(s.T, s.B, s.D)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _same_device(dev, workspace=workspace)
+    return workspace
+
+
+def varlen_scan_fwd(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor, h0: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, h_last: bool | torch.Tensor = False, workspace=None,
+                    check_status=False):
+    """Gated recurrence over the packed stream: h_t = exp(log_decay_t) h_(t-1) + x_t per channel, restarted at
+    every segment of ``cu_seqlens`` from ``h0`` [B, D] fp32 (None: zero).  Returns (h [T, D], h_last).
+
+    ``x`` and ``log_decay`` [T, D] CUDA fp32 or bf16 (fp32 x takes fp32 decays); h has the wider of the two
+    types.  ``h_last`` True allocates the states after each segment ([B, D] fp32), a tensor receives
+    them (``h0`` itself only for single tokens, T == B), False gives None."""
+    s = _scan_shape(x, log_decay, cu_seqlens)
+    dev = x.device
+    s.x_dtype, s.x_row_stride = int(x.dtype == torch.bfloat16), _row_stride(x)
+    dt = torch.promote_types(x.dtype, log_decay.dtype)
+    if out is None:
+        out = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _check_rows("out", out)
+        if out.shape != x.shape or out.dtype != dt:
+            raise ValueError("out must be [T, D] in the wider type of x and log_decay")
+        _same_device(dev, out=out)
+    s.h_row_stride = _row_stride(out)
+    if h_last is True:
+        h_last = torch.empty((s.B, s.D), dtype=torch.float32, device=dev)
+    elif h_last is False:
+        h_last = None
+    _check_state("h0", h0, s, dev)
+    _check_state("h_last", h_last, s, dev)
+    lib = _lib.load()
+    workspace = _scan_workspace(lib, s, workspace, dev)
+    with _on(dev):
+        check(lib.varlen_scan_fwd(_ptr(x), _ptr(log_decay), _ptr(cu_seqlens), ctypes.byref(s), _ptr(h0), _ptr(out),
+                                  _ptr(h_last), _ptr(workspace), workspace.numel(), _stream(dev)))
+    if check_status:
+        _raise_status(workspace)
+    return out, h_last
+
+
+def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor,
+                    h0: torch.Tensor | None = None, dh_last: torch.Tensor | None = None,
+                    x_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None,
+                    dlog_decay: torch.Tensor | None = None, workspace=None, check_status=False):
+    """Gradient of ``varlen_scan_fwd``: returns (dx, dlog_decay, dh0), dh0 None without ``h0``.  ``dh`` and the
+    forward's ``h`` share a dtype; ``x_dtype`` is dx's where dx is allocated (None: bf16 where dh is, or
+    where the forward's inputs were bf16 x with fp32 decays, pass it)."""
+    _check_rows("h", h)
+    s = _scan_shape(dh, log_decay, cu_seqlens, "dh")
+    dev = dh.device
+    if h.shape != dh.shape or h.dtype != dh.dtype:
+        raise ValueError("h must match dh in shape and dtype")
+    if dx is None:
+        dx = torch.empty(dh.shape, dtype=dh.dtype if x_dtype is None else x_dtype, device=dev)
+    if dlog_decay is None:
+        dlog_decay = torch.empty(dh.shape, dtype=log_decay.dtype, device=dev)
+    _check_rows("dx", dx)
+    _check_rows("dlog_decay", dlog_decay)
+    if dx.shape != dh.shape or dlog_decay.shape != dh.shape or dlog_decay.dtype != log_decay.dtype:
+        raise ValueError("dx and dlog_decay must be [T, D], dlog_decay in log_decay's dtype")
+    if dh.dtype != torch.promote_types(dx.dtype, log_decay.dtype):
+        raise ValueError("dh must have the wider type of dx and log_decay")
+    _same_device(dev, h=h, dx=dx, dlog_decay=dlog_decay)
+    s.x_dtype, s.x_row_stride, s.h_row_stride = int(dx.dtype == torch.bfloat16), _row_stride(dx), _row_stride(h)
+    gs = VaScanGradStrides(_row_stride(dh), _row_stride(dx), _row_stride(dlog_decay))
+    _check_state("h0", h0, s, dev)
+    _check_state("dh_last", dh_last, s, dev)
+    dh0 = None if h0 is None else torch.empty_like(h0)
+    lib = _lib.load()
+    workspace = _scan_workspace(lib, s, workspace, dev)
+    with _on(dev):
+        check(lib.varlen_scan_bwd(_ptr(dh), _ptr(h), _ptr(log_decay), _ptr(cu_seqlens), ctypes.byref(s),
+                                  ctypes.byref(gs), _ptr(h0), _ptr(dh_last), _ptr(dx), _ptr(dlog_decay), _ptr(dh0),
+                                  _ptr(workspace), workspace.numel(), _stream(dev)))
+    if check_status:
+        _raise_status(workspace)
+    return dx, dlog_decay, dh0
+
+
+class _VarlenScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, log_decay, cu_seqlens, h0):
+        h, last = varlen_scan_fwd(x, log_decay, cu_seqlens, h0, h_last=True)
+        ctx.save_for_backward(h, log_decay, cu_seqlens, h0)
+        ctx.x_dtype = x.dtype
+        ctx.set_materialize_grads(False)
+        return h, last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dlast):
+        h, log_decay, cu, h0 = ctx.saved_tensors
+        dh = torch.zeros_like(h) if dh is None else dh.contiguous()
+        dx, dg, dh0 = varlen_scan_bwd(dh, h, log_decay, cu, h0, None if dlast is None else dlast.contiguous(), ctx.x_dtype)
+        return dx, dg, None, dh0
+
+
+def varlen_scan(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor, h0: torch.Tensor | None = None):
+    """Differentiable gated recurrence of the packed stream: (h [T, D], the states after each segment [B, D])."""
+    return _VarlenScan.apply(x, log_decay, cu_seqlens, h0)
+
+
+# ----------------------------------------------------------------- token log probabilities
+
+def _check_logits(logits, tokens):
+    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in _FLOATS or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")
+    T, V = logits.shape
+    _check_sizes(T=T, V=V)
+    if tokens.shape != (T,) or tokens.dtype != torch.int32 or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [T] tensor")
+    _same_device(logits.device, tokens=tokens)
+    return T, V
+
+
+def token_logprobs_fwd(logits: torch.Tensor, tokens: torch.Tensor, top_k: int = 0, temperature: float = 1.0,
+                       ignore_index: int = IGNORE_INDEX, check_status=False):
+    """Log probabilities of given tokens: returns (logprob [T], entropy [T], lse [T], top_ids, top_logprobs), fp32,
+    of softmax(logits / temperature).  ``logits`` CUDA fp32 or bf16 [T, V], ``tokens`` int32 [T].  ``top_k`` (at
+    most 128) gives the largest logits' ids [T, top_k] (int32; largest first, equal ones by the lower id) and
+    their log probabilities; None and None with 0.  Rows whose token is ``ignore_index`` are not read: zeros,
+    and ids of -1.  A token outside [0, V) gives NaN for its logprob; ``check_status`` raises."""
+    T, V = _check_logits(logits, tokens)
+    dev, k = logits.device, int(top_k)
+    out = torch.empty((3, T), dtype=torch.float32, device=dev)
+    ids = top = None
+    if k > 0:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        top = torch.empty((T, k), dtype=torch.float32, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
+    at = out.data_ptr()
+    with _on(dev):
+        check(_lib.load().varlen_token_logprobs_fwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
+                                                    _row_stride(logits), _ptr(tokens), T, V, k, int(ignore_index),
+                                                    float(temperature), at, at + 4 * T, at + 8 * T, _ptr(ids),
+                                                    _ptr(top), _ptr(status), _stream(dev)))
+    if check_status and int(status.item()) != 0:
+        raise VarlenError(int(status.item()), "token_logprobs_fwd: a token is outside the vocabulary")
+    logprob, entropy, lse = out.unbind(0)
+    return logprob, entropy, lse, ids, top
+
+
+def _check_per_token(name: str, t, T: int, dev):
+    if t is None:
+        return
+    if t.shape != (T,) or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 [T] tensor")
+    _same_device(dev, **{name: t})
+
+
+def token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor | None,
+                       dlogprob: torch.Tensor, dentropy: torch.Tensor | None = None, temperature: float = 1.0,
+                       ignore_index: int = IGNORE_INDEX, grad: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient [T, V] (in their dtype) for gradients ``dlogprob`` and ``dentropy`` (None: none) of
+    ``token_logprobs_fwd``'s logprob and entropy; ``lse`` and ``entropy`` are its results.  ``grad`` None
+    allocates it, a tensor receives it (``logits`` itself is fine)."""
+    T, V = _check_logits(logits, tokens)
+    dev = logits.device
+    if grad is None:
+        grad = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    elif grad.shape != logits.shape or grad.dtype != logits.dtype or (V > 1 and grad.stride(1) != 1):
+        raise ValueError("grad must match logits in shape and dtype, with a contiguous last dim")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob), ("dentropy", dentropy)):
+        _check_per_token(name, t, T, dev)
+    _same_device(dev, grad=grad)
+    with _on(dev):
+        check(_lib.load().varlen_token_logprobs_bwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
+                                                    _row_stride(logits), _ptr(tokens), _ptr(lse), _ptr(entropy),
+                                                    _ptr(dlogprob), _ptr(dentropy), T, V, int(ignore_index),
+                                                    float(temperature), _ptr(grad), _row_stride(grad), _stream(dev)))
+    return grad
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top_k, temperature, ignore_index):
+        logprob, entropy, lse, ids, top = token_logprobs_fwd(logits, tokens, top_k, temperature, ignore_index)
+        ctx.save_for_backward(logits, tokens, lse, entropy)
+        ctx.temperature, ctx.ignore_index = temperature, ignore_index
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in (ids, top) if t is not None))
+        return logprob, entropy, ids, top
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogprob, dentropy, *_):
+        logits, tokens, lse, entropy = ctx.saved_tensors
+        if dlogprob is None:
+            dlogprob = torch.zeros_like(lse)
+        grad = token_logprobs_bwd(logits, tokens, lse.contiguous(), entropy.contiguous(), dlogprob.contiguous(),
+                                  None if dentropy is None else dentropy.contiguous(), ctx.temperature,
+                                  ctx.ignore_index)
+        return grad, None, None, None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_k: int = 0, temperature: float = 1.0,
+                   ignore_index: int = IGNORE_INDEX):
+    """Differentiable log probabilities and entropies of the packed stream: (logprob [T], entropy [T], top_ids,
+    top_logprobs); gradients go through the first two."""
+    return _TokenLogprobs.apply(logits, tokens, top_k, temperature, ignore_index)
 
 
 # ----------------------------------------------------------------- padded-batch bridge

@@ -34,6 +34,9 @@ EXPORTS = (
     "varlen_attn_workspace_size_sinks", "varlen_attn_plan_sinks", "varlen_attn_fwd_sinks", "varlen_attn_bwd_sinks",
     "varlen_token_distill_workspace_size", "varlen_token_distill",
     "varlen_embed_fwd", "varlen_embed_bwd_workspace_size", "varlen_embed_bwd",
+    "varlen_qk_norm_rope_fwd", "varlen_qk_norm_rope_bwd_workspace_size", "varlen_qk_norm_rope_bwd",
+    "varlen_scan_workspace_size", "varlen_scan_fwd", "varlen_scan_bwd",
+    "varlen_token_logprobs_fwd", "varlen_token_logprobs_bwd",
 )
 
 
@@ -44,6 +47,29 @@ class VaShape(ctypes.Structure):
                 ("k_row_stride", c_int64), ("k_head_stride", c_int64),
                 ("v_row_stride", c_int64), ("v_head_stride", c_int64),
                 ("o_row_stride", c_int64), ("o_head_stride", c_int64)]
+
+
+class VaQkShape(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("Hq", c_int32), ("Hkv", c_int32), ("d", c_int32), ("rot", c_int32),
+                ("dtype", c_int32), ("weight_dtype", c_int32), ("interleaved", c_int32),
+                ("q_row_stride", c_int64), ("q_head_stride", c_int64),
+                ("k_row_stride", c_int64), ("k_head_stride", c_int64),
+                ("qo_row_stride", c_int64), ("qo_head_stride", c_int64),
+                ("ko_row_stride", c_int64), ("ko_head_stride", c_int64)]
+
+
+class VaQkGradStrides(ctypes.Structure):
+    _fields_ = [("dq_row_stride", c_int64), ("dq_head_stride", c_int64),
+                ("dk_row_stride", c_int64), ("dk_head_stride", c_int64)]
+
+
+class VaScanShape(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("B", c_int32), ("D", c_int32), ("x_dtype", c_int32), ("gate_dtype", c_int32),
+                ("x_row_stride", c_int64), ("gate_row_stride", c_int64), ("h_row_stride", c_int64)]
+
+
+class VaScanGradStrides(ctypes.Structure):
+    _fields_ = [("dh_row_stride", c_int64), ("dx_row_stride", c_int64), ("dgate_row_stride", c_int64)]
 
 
 class VarlenError(RuntimeError):
@@ -129,6 +155,18 @@ def _declare(lib):
         "varlen_embed_bwd_workspace_size": (c_size_t, [c_int32, c_int32]),
         "varlen_embed_bwd": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32, c_float,
                                        c_void_p, c_int32, c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
+        "varlen_qk_norm_rope_fwd": (c_int32, [c_void_p] * 6 + [POINTER(VaQkShape), c_float, c_void_p, c_void_p, c_void_p]),
+        "varlen_qk_norm_rope_bwd_workspace_size": (c_size_t, [c_int32]),
+        "varlen_qk_norm_rope_bwd": (c_int32, [c_void_p] * 8 + [POINTER(VaQkShape), POINTER(VaQkGradStrides), c_float] +
+                                    [c_void_p] * 5 + [c_size_t, c_void_p]),
+        "varlen_scan_workspace_size": (c_size_t, [c_int32, c_int32, c_int32]),
+        "varlen_scan_fwd": (c_int32, [c_void_p] * 3 + [POINTER(VaScanShape)] + [c_void_p] * 4 + [c_size_t, c_void_p]),
+        "varlen_scan_bwd": (c_int32, [c_void_p] * 4 + [POINTER(VaScanShape), POINTER(VaScanGradStrides)] +
+                            [c_void_p] * 6 + [c_size_t, c_void_p]),
+        "varlen_token_logprobs_fwd": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                                c_float] + [c_void_p] * 7),
+        "varlen_token_logprobs_bwd": (c_int32, [c_void_p, c_int32, c_int64] + [c_void_p] * 5 +
+                                      [c_int32, c_int32, c_int32, c_float, c_void_p, c_int64, c_void_p]),
         "varlen_read_status": (c_int32, [c_void_p, i32p, c_void_p]),
         "varlen_clear_status": (c_int32, [c_void_p, c_void_p]),
         "varlen_profile_enable": (c_int32, [c_int32]),

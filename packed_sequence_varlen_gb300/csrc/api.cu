@@ -2,10 +2,14 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
 #include "attn_params.cuh"
+#include "logprobs.cuh"
+#include "qk_norm.cuh"
+#include "scan.cuh"
 
 namespace va {
 
@@ -58,7 +62,9 @@ enum KernelId {
   K_VALIDATE = 0, K_META_SCAN, K_META_FILL, K_PLAN, K_FWD, K_BWD_PREP, K_BWD_DKDV, K_BWD_DQ,
   K_VALIDATE_PLAN, K_FWD_TOK, K_CU_FROM_POS, K_LOSS_TARGETS, K_CE_COUNT, K_CE_ROWS, K_CE_REDUCE, K_PAD_COUNT,
   K_PAD_SCAN, K_PAD_INDEX, K_GATHER_ROWS, K_DISTILL_COUNT, K_DISTILL_ROWS, K_DISTILL_REDUCE,
-  K_EMBED_FWD, K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN, K_SINK_JOIN, K_COUNT
+  K_EMBED_FWD, K_EMBED_SORT, K_EMBED_REDUCE, K_EMBED_JOIN, K_SINK_JOIN,
+  K_QK_NORM_FWD, K_QK_NORM_BWD, K_QK_NORM_JOIN, K_SCAN_PREP, K_SCAN_FWD, K_SCAN_BWD, K_SCAN_STEP, K_LOGPROBS_FWD,
+  K_LOGPROBS_BWD, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "validate_cu_seqlens", "metadata_scan", "metadata_fill", "plan",          "fwd",
@@ -66,7 +72,8 @@ const char* const kKernelNames[K_COUNT] = {
     "cu_from_positions",   "loss_targets",  "ce_count",      "ce_rows",       "ce_reduce",
     "pad_count",           "pad_scan",      "pad_index",     "gather_rows", "distill_count", "distill_rows",
     "distill_reduce", "embed_fwd", "embed_sort", "embed_reduce", "embed_join",
-    "sink_join"};
+    "sink_join", "qk_norm_fwd", "qk_norm_bwd", "qk_norm_join", "scan_prep", "scan_fwd", "scan_bwd", "scan_step",
+    "logprobs_fwd", "logprobs_bwd"};
 
 struct Profiler {
   std::vector<cudaEvent_t> start, stop;
@@ -837,6 +844,272 @@ va_status varlen_embed_bwd(const void* dout, int32_t dtype, int64_t i_rs, const 
                               accumulate ? 1 : 0, ws, cs);
     });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "embed_bwd");
+}
+
+// ------------------------------------------------------------ query / key norm with rotation
+
+static va_status check_qk(const char* where, const va_qk_shape* s, const void* const* rows, int nrows,
+                          const int64_t* strides, const void* qw, const void* kw, const float* inv_freq,
+                          const int32_t* pos, float eps) {
+  const std::string w(where);
+  if ((s->T > 0 && !pos) || (s->rot > 0 && !inv_freq)) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+  if (s->T < 0 || s->T >= (1 << 30) || s->Hq < 1 || s->Hkv < 1 || s->Hq > 65535 || s->Hkv > 65535)
+    return fail(VA_ERR_INVALID_ARG, w + ": 0 <= T < 2^30, 1 <= heads <= 65535");
+  if (s->dtype < 0 || s->dtype > 1 || s->weight_dtype < 0 || s->weight_dtype > 1)
+    return fail(VA_ERR_INVALID_ARG, w + ": dtypes 0 or 1");
+  if (s->d < 8 || s->d > kQkMaxDim || s->d % 8 || s->rot < 0 || s->rot > s->d || s->rot % 8)
+    return fail(VA_ERR_UNSUPPORTED, w + ": d and rot multiples of 8, rot <= d <= 256");
+  if (!(eps >= 0.f && eps < INFINITY)) return fail(VA_ERR_INVALID_ARG, w + ": eps must be >= 0 and finite");
+  const uintptr_t wa = s->weight_dtype == 1 ? 1 : 3;
+  if ((reinterpret_cast<uintptr_t>(qw) & wa) || (reinterpret_cast<uintptr_t>(kw) & wa))
+    return fail(VA_ERR_INVALID_ARG, w + ": weights must be aligned to their type");
+  for (int i = 0; i < nrows; ++i) {
+    if (s->T > 0 && !rows[i]) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+    if (!aligned16(rows[i]) || strides[2 * i] % 8 || strides[2 * i + 1] % 8 || strides[2 * i] < 0 ||
+        strides[2 * i + 1] < 0)
+      return fail(VA_ERR_INVALID_ARG, w + ": pointers must be 16-byte aligned, strides multiples of 8 elements");
+  }
+  return VA_OK;
+}
+
+static QkParams qk_params(const va_qk_shape* s, const void* qw, const void* kw, const float* inv_freq,
+                          const int32_t* pos, float eps) {
+  QkParams p{};
+  p.x_rs[0] = s->q_row_stride, p.x_hs[0] = s->q_head_stride, p.x_rs[1] = s->k_row_stride, p.x_hs[1] = s->k_head_stride;
+  p.y_rs[0] = s->qo_row_stride, p.y_hs[0] = s->qo_head_stride;
+  p.y_rs[1] = s->ko_row_stride, p.y_hs[1] = s->ko_head_stride;
+  p.w[0] = qw, p.w[1] = kw;
+  p.inv_freq = inv_freq;
+  p.pos = pos;
+  p.T = s->T, p.H[0] = s->Hq, p.H[1] = s->Hkv, p.d = s->d, p.rot = s->rot;
+  p.w_bf16 = s->weight_dtype;
+  p.interleaved = s->interleaved != 0;
+  p.eps = eps;
+  return p;
+}
+
+va_status varlen_qk_norm_rope_fwd(const void* q, const void* k, const int32_t* pos, const void* qw, const void* kw,
+                                  const float* inv_freq, const va_qk_shape* s, float eps, void* qo, void* ko,
+                                  va_stream_t stream) {
+  if (!s) return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_fwd: null pointer");
+  const void* rows[4] = {q, k, qo, ko};
+  const int64_t strides[8] = {s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride,
+                              s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride};
+  const va_status st = check_qk("qk_norm_rope_fwd", s, rows, 4, strides, qw, kw, inv_freq, pos, eps);
+  if (st != VA_OK || s->T == 0) return st;
+  QkParams p = qk_params(s, qw, kw, inv_freq, pos, eps);
+  p.x[0] = q, p.x[1] = k, p.y[0] = qo, p.y[1] = ko;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch(K_QK_NORM_FWD, cs, [&] { return launch_qk_norm_fwd(p, s->dtype, cs); });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "qk_norm_rope_fwd");
+}
+
+size_t varlen_qk_norm_rope_bwd_workspace_size(int32_t d) {
+  return d < 8 || d > kQkMaxDim || d % 8 ? 0 : qk_norm_bwd_workspace(d);
+}
+
+va_status varlen_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* q, const void* k, const int32_t* pos,
+                                  const void* qw, const void* kw, const float* inv_freq, const va_qk_shape* s,
+                                  const va_qk_grad_strides* gs, float eps, void* dq, void* dk, void* dqw, void* dkw,
+                                  void* ws, size_t ws_bytes, va_stream_t stream) {
+  if (!s || !gs) return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: null pointer");
+  const void* rows[6] = {q, k, dqo, dko, dq, dk};
+  const int64_t strides[12] = {s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride,
+                               s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride,
+                               gs->dq_row_stride, gs->dq_head_stride, gs->dk_row_stride, gs->dk_head_stride};
+  const va_status st = check_qk("qk_norm_rope_bwd", s, rows, 6, strides, qw, kw, inv_freq, pos, eps);
+  if (st != VA_OK) return st;
+  if ((dqw && !qw) || (dkw && !kw))
+    return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: a weight's gradient without the weight");
+  const uintptr_t wa = s->weight_dtype == 1 ? 1 : 3;
+  if ((reinterpret_cast<uintptr_t>(dqw) & wa) || (reinterpret_cast<uintptr_t>(dkw) & wa))
+    return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: weights must be aligned to their type");
+  const bool weights = dqw || dkw;
+  if (weights && (!ws || !aligned16(ws)))
+    return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: workspace must be 16-byte aligned");
+  if (weights && ws_bytes < qk_norm_bwd_workspace(s->d))
+    return fail(VA_ERR_WORKSPACE, "qk_norm_rope_bwd: workspace too small");
+  QkParams p = qk_params(s, qw, kw, inv_freq, pos, eps);
+  p.x[0] = q, p.x[1] = k, p.dy[0] = dqo, p.dy[1] = dko, p.y[0] = dq, p.y[1] = dk;
+  for (int i = 0; i < 2; ++i) p.dy_rs[i] = p.y_rs[i], p.dy_hs[i] = p.y_hs[i];  // the outputs' gradients
+  p.y_rs[0] = gs->dq_row_stride, p.y_hs[0] = gs->dq_head_stride;
+  p.y_rs[1] = gs->dk_row_stride, p.y_hs[1] = gs->dk_head_stride;
+  p.dw[0] = dqw, p.dw[1] = dkw;
+  p.part = weights ? static_cast<float*>(ws) : nullptr;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (s->T > 0) e = launch(K_QK_NORM_BWD, cs, [&] { return launch_qk_norm_bwd(0, p, s->dtype, cs); });
+  if (weights && e == cudaSuccess)
+    e = launch(K_QK_NORM_JOIN, cs, [&] { return launch_qk_norm_bwd(1, p, s->dtype, cs); });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "qk_norm_rope_bwd");
+}
+
+// ------------------------------------------------------------ gated recurrence
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+static va_status check_scan(const char* where, const va_scan_shape* s, const int32_t* cu, const void* ws,
+                            size_t ws_bytes) {
+  const std::string w(where);
+  if (!s || !cu || !ws) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+  if (s->T < 1 || s->T >= (1 << 30) || s->B < 1 || s->B > s->T || s->D < 1 || s->D > (1 << 20))
+    return fail(VA_ERR_INVALID_ARG, w + ": 1 <= B <= T < 2^30, 1 <= D <= 2^20");
+  if (s->x_dtype < 0 || s->x_dtype > 1 || s->gate_dtype < 0 || s->gate_dtype > 1)
+    return fail(VA_ERR_INVALID_ARG, w + ": dtypes 0 or 1");
+  if (s->x_dtype == 0 && s->gate_dtype == 1)
+    return fail(VA_ERR_UNSUPPORTED, w + ": fp32 inputs take fp32 decays");
+  if (!aligned16(ws)) return fail(VA_ERR_INVALID_ARG, w + ": workspace must be 16-byte aligned");
+  if (ws_bytes < varlen_scan_workspace_size(s->T, s->B, s->D)) return fail(VA_ERR_WORKSPACE, w + ": workspace too small");
+  return VA_OK;
+}
+
+static va_status check_scan_rows(const char* where, const va_scan_shape* s, const void* p, int64_t rs, int bf16) {
+  if (!p) return fail(VA_ERR_INVALID_ARG, std::string(where) + ": null pointer");
+  if (rs < s->D) return fail(VA_ERR_INVALID_ARG, std::string(where) + ": row strides must be >= D");
+  if (reinterpret_cast<uintptr_t>(p) & (bf16 ? 1 : 3))
+    return fail(VA_ERR_INVALID_ARG, std::string(where) + ": pointers must be aligned to their type");
+  return VA_OK;
+}
+
+static va_status check_states(const char* where, std::initializer_list<const float*> states) {
+  for (const float* p : states)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(VA_ERR_INVALID_ARG, std::string(where) + ": pointers must be aligned to their type");
+  return VA_OK;
+}
+
+size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D) {
+  if (T < 1 || T >= (1 << 30) || B < 1 || B > T || D < 1 || D > (1 << 20)) return 0;
+  return B == T ? std::max<size_t>(sizeof(WsHeader), scan_workspace(T, D)) : scan_workspace(T, D);
+}
+
+va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const va_scan_shape* s, const float* h0,
+                          void* h, float* h_last, void* ws, size_t ws_bytes, va_stream_t stream) {
+  const char* where = "scan_fwd";
+  va_status st = check_scan(where, s, cu, ws, ws_bytes);
+  const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
+  if (st == VA_OK) st = check_scan_rows(where, s, x, s->x_row_stride, s->x_dtype);
+  if (st == VA_OK) st = check_scan_rows(where, s, g, s->gate_row_stride, s->gate_dtype);
+  if (st == VA_OK) st = check_scan_rows(where, s, h, s->h_row_stride, hb);
+  if (st == VA_OK) st = check_states(where, {h0, h_last});
+  if (st != VA_OK) return st;
+  const size_t states = static_cast<size_t>(s->B) * s->D * sizeof(float);
+  // a segment's first rows read h0 twice, the second time maybe after its last row is done
+  if (s->B < s->T && overlap(h0, states, h_last, states))
+    return fail(VA_ERR_INVALID_ARG, "scan_fwd: h_last may lie on h0 for single tokens only (T == B)");
+  ScanParams p{};
+  p.x = x, p.g = g, p.out = h;
+  p.x_rs = s->x_row_stride, p.g_rs = s->gate_row_stride, p.out_rs = s->h_row_stride;
+  p.cu = cu, p.h0 = h0, p.last = h_last;
+  p.B = s->B, p.T = s->T, p.D = s->D;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (s->B == s->T) {
+    e = launch(K_SCAN_STEP, cs, [&] { return launch_scan_step(p, s->x_dtype, s->gate_dtype, ws, cs); });
+  } else {
+    const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_FWD};
+    for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
+      e = launch(kid[stage], cs, [&] { return launch_scan_fwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
+  }
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, where);
+}
+
+va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const int32_t* cu, const va_scan_shape* s,
+                          const va_scan_grad_strides* gs, const float* h0, const float* dh_last, void* dx, void* dg,
+                          float* dh0, void* ws, size_t ws_bytes, va_stream_t stream) {
+  const char* where = "scan_bwd";
+  if (!gs) return fail(VA_ERR_INVALID_ARG, "scan_bwd: null pointer");
+  va_status st = check_scan(where, s, cu, ws, ws_bytes);
+  const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
+  if (st == VA_OK) st = check_scan_rows(where, s, dh, gs->dh_row_stride, hb);
+  if (st == VA_OK) st = check_scan_rows(where, s, h, s->h_row_stride, hb);
+  if (st == VA_OK) st = check_scan_rows(where, s, g, s->gate_row_stride, s->gate_dtype);
+  if (st == VA_OK) st = check_scan_rows(where, s, dx, gs->dx_row_stride, s->x_dtype);
+  if (st == VA_OK) st = check_scan_rows(where, s, dg, gs->dgate_row_stride, s->gate_dtype);
+  if (st == VA_OK) st = check_states(where, {h0, dh_last, dh0});
+  if (st != VA_OK) return st;
+  const size_t states = static_cast<size_t>(s->B) * s->D * sizeof(float);
+  if (overlap(dh_last, states, dh0, states) || overlap(h0, states, dh0, states))
+    return fail(VA_ERR_INVALID_ARG, "scan_bwd: dh0 must not lie on h0 or dh_last");
+  ScanParams p{};
+  p.x = dh, p.g = g, p.h = h, p.out = dx, p.dg = dg;
+  p.x_rs = gs->dh_row_stride, p.g_rs = s->gate_row_stride, p.h_rs = s->h_row_stride;
+  p.out_rs = gs->dx_row_stride, p.dg_rs = gs->dgate_row_stride;
+  p.cu = cu, p.h0 = h0, p.dlast = dh_last, p.last = dh0;
+  p.B = s->B, p.T = s->T, p.D = s->D;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_BWD};
+  for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
+    e = launch(kid[stage], cs, [&] { return launch_scan_bwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, where);
+}
+
+// ------------------------------------------------------------ token log probabilities
+
+static va_status check_logprobs(const char* where, const void* z, int32_t dtype, int64_t z_rs, const int32_t* tok,
+                                int32_t T, int32_t V, float temperature) {
+  const std::string w(where);
+  if (!z || !tok) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+  if (T < 1 || T >= (1 << 30) || V < 1 || V >= (1 << 30) || (dtype != 0 && dtype != 1))
+    return fail(VA_ERR_INVALID_ARG, w + ": 1 <= T and V < 2^30, dtype 0 or 1");
+  if (z_rs < V) return fail(VA_ERR_INVALID_ARG, w + ": row strides must be >= the row");
+  if (reinterpret_cast<uintptr_t>(z) & (dtype == 1 ? 1 : 3))
+    return fail(VA_ERR_INVALID_ARG, w + ": pointers must be aligned to their type");
+  if (!(temperature >= 1.f / 64) || !(temperature <= 64.f))
+    return fail(VA_ERR_INVALID_ARG, w + ": temperature must be in [1/64, 64]");
+  return VA_OK;
+}
+
+static void set_temperature(LogprobParams& p, float temperature) {
+  const double scale = 1.4426950408889634 / temperature;
+  p.temperature = temperature;
+  p.inv_t = 1.f / temperature;
+  p.scale = static_cast<float>(scale);
+  p.scale_lo = static_cast<float>(scale - p.scale);
+}
+
+va_status varlen_token_logprobs_fwd(const void* z, int32_t dtype, int64_t z_rs, const int32_t* tok, int32_t T,
+                                    int32_t V, int32_t k, int32_t ignore_index, float temperature, float* logprob,
+                                    float* entropy, float* lse, int32_t* top_ids, float* top_logprobs, int32_t* status,
+                                    va_stream_t stream) {
+  const va_status st = check_logprobs("token_logprobs_fwd", z, dtype, z_rs, tok, T, V, temperature);
+  if (st != VA_OK) return st;
+  if (!logprob || !entropy || !lse || (k > 0 && (!top_ids || !top_logprobs)))
+    return fail(VA_ERR_INVALID_ARG, "token_logprobs_fwd: null pointer");
+  if (k < 0 || k > V) return fail(VA_ERR_INVALID_ARG, "token_logprobs_fwd: 0 <= k <= V");
+  if (k > kMaxTop) return fail(VA_ERR_UNSUPPORTED, "token_logprobs_fwd: at most 128 alternatives");
+  LogprobParams p{};
+  p.z = z, p.z_rs = z_rs, p.tok = tok, p.T = T, p.V = V, p.ignore = ignore_index, p.k = k;
+  set_temperature(p, temperature);
+  p.logprob = logprob, p.entropy = entropy, p.lse = lse, p.top_ids = top_ids, p.top_logprobs = top_logprobs;
+  p.status = status;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch(K_LOGPROBS_FWD, cs, [&] { return launch_logprobs_fwd(p, dtype, cs); });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_logprobs_fwd");
+}
+
+va_status varlen_token_logprobs_bwd(const void* z, int32_t dtype, int64_t z_rs, const int32_t* tok, const float* lse,
+                                    const float* entropy, const float* dlogprob, const float* dentropy, int32_t T,
+                                    int32_t V, int32_t ignore_index, float temperature, void* grad, int64_t g_rs,
+                                    va_stream_t stream) {
+  const va_status st = check_logprobs("token_logprobs_bwd", z, dtype, z_rs, tok, T, V, temperature);
+  if (st != VA_OK) return st;
+  if (!lse || !dlogprob || !grad || (dentropy && !entropy))
+    return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: null pointer");
+  if (g_rs < V) return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: row strides must be >= the row");
+  if (reinterpret_cast<uintptr_t>(grad) & (dtype == 1 ? 1 : 3))
+    return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: pointers must be aligned to their type");
+  LogprobParams p{};
+  p.z = z, p.z_rs = z_rs, p.tok = tok, p.T = T, p.V = V, p.ignore = ignore_index;
+  set_temperature(p, temperature);
+  p.lse = const_cast<float*>(lse), p.entropy = const_cast<float*>(entropy);
+  p.dlogprob = dlogprob, p.dentropy = dentropy, p.grad = grad, p.g_rs = g_rs;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch(K_LOGPROBS_BWD, cs, [&] { return launch_logprobs_bwd(p, dtype, cs); });
+  return e == cudaSuccess ? VA_OK : cuda_fail(e, "token_logprobs_bwd");
 }
 
 va_status varlen_read_status(const void* ws, int32_t* out, va_stream_t stream) {

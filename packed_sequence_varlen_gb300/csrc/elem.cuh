@@ -1,0 +1,55 @@
+// Element access shared by the streaming kernels: fp32 or bf16 in memory, fp32 in registers.
+#pragma once
+#include "common.cuh"
+
+namespace va {
+
+__device__ __forceinline__ float elem_f(float x) { return x; }
+__device__ __forceinline__ float elem_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T> __device__ __forceinline__ T elem_of(float x);
+template <> __device__ __forceinline__ float elem_of<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 elem_of<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// N consecutive elements as they lie in memory, aligned to their size (at most 16 bytes).
+template <class T, int N> struct alignas(sizeof(T) * N) Pack {
+  static_assert(sizeof(T) * N <= 16 && (N & (N - 1)) == 0, "one access of at most 16 bytes");
+  T e[N];
+  __device__ __forceinline__ float operator[](int i) const { return elem_f(e[i]); }
+  __device__ __forceinline__ void set(int i, float x) { e[i] = elem_of<T>(x); }
+};
+
+namespace elem_detail {
+template <int BYTES> struct Word;
+template <> struct Word<2> { using type = unsigned short; };
+template <> struct Word<4> { using type = unsigned int; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<16> { using type = uint4; };
+}  // namespace elem_detail
+
+template <class T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+  using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
+  Pack<T, N> r;
+  *reinterpret_cast<Wd*>(&r) = *reinterpret_cast<const Wd*>(p);
+  return r;
+}
+// Read once (evicted first).
+template <class T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack_cs(const T* p) {
+  using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
+  Pack<T, N> r;
+  *reinterpret_cast<Wd*>(&r) = __ldcs(reinterpret_cast<const Wd*>(p));
+  return r;
+}
+template <class T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
+  using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
+  *reinterpret_cast<Wd*>(p) = *reinterpret_cast<const Wd*>(&v);
+}
+template <class T, int N>
+__device__ __forceinline__ void store_pack_cs(T* p, const Pack<T, N>& v) {
+  using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
+  __stcs(reinterpret_cast<Wd*>(p), *reinterpret_cast<const Wd*>(&v));
+}
+
+}  // namespace va

@@ -1,0 +1,37 @@
+// Arguments of the gated recurrence's kernels (scan.cu).
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include <cuda_runtime.h>
+
+namespace va {
+
+struct ScanParams {
+  const void* x;       // forward: x; backward: dh
+  const void* g;       // log decay
+  const void* h;       // backward: the forward's h
+  void* out;           // forward: h; backward: dx
+  void* dg;            // backward
+  int64_t x_rs, g_rs, h_rs, out_rs, dg_rs;  // row strides (elements)
+  const int32_t* cu;
+  const float* h0;     // [B, D] contiguous, may be null
+  const float* dlast;  // backward: gradient of the last states, may be null
+  float* last;         // forward: the last states; backward: h0's gradient; may be null
+  int B, T, D;
+  int tiles, cols;     // tiles of rows, columns of channels (set by the launcher)
+  int32_t* status;     // workspace header's status word
+  int32_t* ticket;
+  int32_t* flags;      // [tiles][cols] a tile's map is there, then [groups][cols] a group's state is there
+  float2* agg;         // [tiles][cols * width] a tile's map (decay product, state from zero)
+  float* carry;        // [groups][cols * width] the state after a group of tiles
+};
+
+size_t scan_workspace(int T, int D);
+// stage 0: boundary check and cleared flags, 1: the recurrence.  dtypes: 0 fp32, 1 bf16.
+cudaError_t launch_scan_fwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
+cudaError_t launch_scan_bwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
+// The forward of single tokens (T == B): every state moves on by one step.  One launch.
+cudaError_t launch_scan_step(ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
+
+}  // namespace va

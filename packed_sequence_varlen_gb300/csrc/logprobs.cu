@@ -1,15 +1,23 @@
 // Log probabilities of given tokens with the distribution's entropy and its top alternatives, and their gradient
 // with respect to the logits.  Row t, p = softmax(z / tau):
 //
-//   lse = ln sum exp(z / tau),  logprob = z_y / tau - lse,  H = -sum p ln p = ln s - w / s
-// with s = sum e, w = sum e u, e = exp(u), u = (z - m) / tau for a reference m near the row's maximum.
+//   lse = ln sum exp(z / tau),  logprob = z_y / tau - lse,  H = -sum p ln p
 //   dz_c = (dl ([c == y] - p_c) - dH p_c (ln p_c + H)) / tau
 //
-// Forward: one read of the row.  A thread's part gives (m, s, w), its reference moved only when a value passes it by
-// 2^8, so the sums are hardly ever rescaled; differences are formed before the scale, so a row of the type's
-// lowest value stays finite.  With alternatives a thread also keeps the largest logit of its part: the k-th largest of
-// these is a lower bound of the row's k-th largest logit, and only the few parts that reach it are looked at again
-// (in L2).  Candidates are ordered as whole numbers, value first, then the lower id, and ranked by counting.  A row
+// Forward: one read of the row, in powers of two: with c = log2(e) / tau and a reference r,
+//   s = sum 2^t, w = sum 2^t t, t = c z - r;   log2 p = t - log2 s,  H = ln 2 (log2 s - w / s).
+// A thread moves its reference only when a value passes it by 2^8, so its sums are hardly ever rescaled, and t is one
+// multiply-add whose roundings of c and r drop out of p.  Rows whose largest logit is beyond +-1e29 (or no number) have
+// their sums formed again from differences to the maximum, so one of the type's lowest value stays finite.  Logits far
+// below the reference are raised to where 2^t is 0 anyway (0 times -inf would be NaN), NaN is kept.
+//
+// A block reads its rows through a ring of kDepth groups of kU 16-byte pieces a thread, copied asynchronously: a
+// thread's pieces are its own, so nothing waits for the block, and the next row is on its way while this one's
+// sums are joined and its alternatives are looked for.
+//
+// Alternatives: each thread keeps the largest logit of its part; the k-th largest of the parts' maxima (cut to 16 bits)
+// is a lower bound of the row's k-th largest logit, and only threads whose part reaches it look at it again (in L2).
+// Candidates are ordered as whole numbers, value first, then the lower id, and ranked by counting.  A row
 // with too many candidates (equal logits, mostly) has its k-th value found bit by bit instead.
 //
 // Backward: p from the saved lse, one read, one write.  What an lse has lost by its rounding to fp32 is p's relative
@@ -26,16 +34,35 @@ namespace {
 
 constexpr float kLog2eLo = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kU = 4;          // 16-byte pieces a thread has in flight
-constexpr int kCtasPerSm = 4;  // resident at once (launch bounds)
-constexpr int kCand = 1024;    // candidates a row may have before it takes the slow way
+constexpr int kU = 4;          // 16-byte pieces of a group
+constexpr int kDepth = 3;      // groups a thread has on their way
+constexpr int kCand = 512;     // candidates a row may have before it takes the slow way
+constexpr float kFar = 1e29f;  // logits beyond this take differences before products
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of two bf16 pairs, NaN left out
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float low_f(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float high_f(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Whole numbers in the order of the values (-0 as 0, NaN above all).
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -45,295 +72,497 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 __device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
 
-// Sums relative to m, in powers of two: s = sum 2^t, w = sum 2^t t, t = (z - m) scale.
+// s = sum 2^t and w = sum 2^t t, t = c z - r, in two halves.
 struct Sums {
-  float m, s, w;
+  float r, s[2], w[2];
 };
 
-// u = (z - m) scale no smaller than -200, where 2^u is 0 anyway (0 times -inf would be NaN).
-__device__ __forceinline__ float shifted(float z, float m, float scale) { return max_nan((z - m) * scale, -200.f); }
-
-__device__ __forceinline__ void rescale(Sums& a, float m, float scale) {  // m >= a.m
-  if (a.m == -INFINITY) {
-    a.m = m;
-    return;
+__device__ __forceinline__ void move_to(Sums& a, float r) {  // r >= a.r
+  const float d = fmaxf(a.r - r, -200.f), f = fast_exp2(d);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a.w[i] = f * fmaf(a.s[i], d, a.w[i]);
+    a.s[i] *= f;
   }
-  const float d = shifted(a.m, m, scale), f = fast_exp2(d);
-  a.w = f * fmaf(a.s, d, a.w);
-  a.s *= f;
-  a.m = m;
+  a.r = r;
 }
 
-__device__ __forceinline__ void merge(Sums& a, Sums b, float scale) {
-  const float m = fmaxf(a.m, b.m);
-  if (m > a.m) rescale(a, m, scale);
-  if (m > b.m) rescale(b, m, scale);
-  a.s += b.s;
-  a.w += b.w;
+__device__ __forceinline__ void add2(Sums& a, float x0, float x1, float c) {
+  float t0, t1;
+  ffma2(t0, t1, x0, x1, c, c, -a.r, -a.r);
+  const float e0 = fast_exp2(t0), e1 = fast_exp2(t1);
+  fadd2(a.s[0], a.s[1], a.s[0], a.s[1], e0, e1);
+  ffma2(a.w[0], a.w[1], e0, e1, t0, t1, a.w[0], a.w[1]);
 }
 
-// Adds N values whose largest (NaN left out) is cm.
-template <int N>
-__device__ __forceinline__ void add(Sums& a, const float (&x)[N], float cm, float scale, float slack) {
-  if (cm > a.m + slack) rescale(a, cm, scale);
-  const float m = a.m == -INFINITY ? 0.f : a.m;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float t = shifted(x[i], m, scale), e = fast_exp2(t);
-    a.s += e;
-    a.w = fmaf(e, t, a.w);
+// The largest logit of a piece (NaN left out).
+template <class T>
+__device__ __forceinline__ float largest(const uint4& raw) {
+  if (sizeof(T) == 2) {
+    const uint32_t m = max2(max2(raw.x, raw.y), max2(raw.z, raw.w));
+    return fmaxf(low_f(m), high_f(m));
   }
+  return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
 }
 
-template <class T> struct Row { static constexpr int W = 16 / sizeof(T); };
+// What a thread has seen of a row.
+template <class T>
+struct Part {
+  static constexpr int W = 16 / sizeof(T);
+  Sums a;
+  float top;       // the largest logit (NaN left out)
+  uint32_t floor;  // logits are raised to this: bf16 a pair, fp32 its bits
 
-template <class T, class F>
-__device__ __forceinline__ void each_piece(const T* z, int Vv, F&& f) {
-  constexpr int W = Row<T>::W, step = kThreads * W;
-  for (int c0 = threadIdx.x * W; c0 < Vv; c0 += kU * step) {
-    Pack<T, W> raw[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (c0 + u * step < Vv) raw[u] = load_pack<T, W>(z + c0 + u * step);
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (c0 + u * step >= Vv) continue;
-      float x[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = raw[u][i];
-      f(c0 + u * step, x);
+  __device__ __forceinline__ void start(float c) {
+    a.r = -1e30f * c;
+    a.s[0] = a.s[1] = a.w[0] = a.w[1] = 0.f;
+    top = -INFINITY;
+    set_floor(-2e30f);
+  }
+  __device__ __forceinline__ void set_floor(float x) {
+    if (sizeof(T) == 2) floor = pack_bf16(x, x);
+    else floor = __float_as_uint(x);
+  }
+  __device__ __forceinline__ void see(float m, float c) {  // m: the largest of what comes next
+    top = fmaxf(top, m);
+    if (m * c > a.r + 8.f) {
+      move_to(a, m * c);
+      set_floor(m - 200.f / c - fabsf(m) * 0.015625f);
     }
   }
-}
-
-struct RowSmem {
-  Sums warp[kWarps];
-  uint32_t part_max[kThreads];       // largest logit of every thread's part
-  unsigned long long cand[kCand];    // value, then ~id
-  int count;
-  int total[kWarps];
+  __device__ __forceinline__ void add(const uint4& raw, float c) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    see(largest<T>(raw), c);
+    if (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = max2_nan(w[i], floor);
+        add2(a, low_f(x), high_f(x), c);
+      }
+    } else {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+      const float lo = __uint_as_float(floor);
+      add2(a, max_nan(x[0], lo), max_nan(x[1], lo), c);
+      add2(a, max_nan(x[2], lo), max_nan(x[3], lo), c);
+    }
+  }
+  __device__ __forceinline__ void add(T z, float c) {  // one logit
+    const float x = elem_f(z);
+    see(x, c);
+    const float lo = sizeof(T) == 2 ? low_f(floor) : __uint_as_float(floor);
+    const float t = fmaf(max_nan(x, lo), c, -a.r), e = fast_exp2(t);
+    a.s[0] += e;
+    a.w[0] = fmaf(e, t, a.w[0]);
+  }
 };
 
-// A row's sums, the same in every thread; gm: the largest logit of this thread's part.
+// How a row lies in memory: `head` elements up to its first 16-byte boundary, `body` pieces, `tail` elements.
 template <class T>
-__device__ __forceinline__ Sums row_sums(const T* z, int V, int Vv, float scale, RowSmem& sh, float& gm) {
-  constexpr int W = Row<T>::W;
-  Sums a{-INFINITY, 0.f, 0.f};
-  const float slack = 8.f / scale;
-  gm = -INFINITY;
-  each_piece(z, Vv, [&](int, const float (&x)[W]) {
-    float cm = x[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) cm = fmaxf(cm, x[i]);
-    gm = fmaxf(gm, cm);
-    add(a, x, cm, scale, slack);
-  });
-  for (int c = Vv + threadIdx.x; c < V; c += kThreads) {
-    const float x[1] = {elem_f(z[c])};
-    gm = fmaxf(gm, x[0]);
-    add(a, x, x[0], scale, slack);
+struct Cut {
+  static constexpr int W = 16 / sizeof(T);
+  int head, body, tail;
+  __device__ __forceinline__ Cut(const T* z, int V) {
+    const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) & 15u);
+    head = min(V, static_cast<int>(((16u - mis) & 15u) / sizeof(T)));
+    body = (V - head) / W;
+    tail = V - head - body * W;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.w = __shfl_xor_sync(0xffffffffu, a.w, o);
-    merge(a, b, scale);
-  }
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = sh.warp[0];
-  for (int w = 1; w < kWarps; ++w) merge(a, sh.warp[w], scale);
-  return a;
+  __device__ __forceinline__ int edge(int i) const { return i < head ? i : i + body * W; }  // i < head + tail
+};
+
+template <int NT>
+struct RowSmem {
+  unsigned long long cand[kCand];  // value, then ~id
+  float sums[3][NT / 32];          // the warps' (r, s, w)
+  float top[NT / 32];
+  uint32_t part[NT];               // the parts' largest logits
+  int total[NT / 32];
+  int count;
+};
+
+template <int NT>
+__device__ __forceinline__ void block_sync() {
+  if (NT == 32) __syncwarp();
+  else __syncthreads();
 }
 
-__device__ __forceinline__ int block_sum(int n, RowSmem& sh) {
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// A row's sums: log2 p = t - l, t = c z - r; top the largest logit.
+struct RowSums {
+  float r, l, mean_t, top;  // mean_t = sum p t
+};
+
+// The block's sums, the same in every thread.
+template <int NT>
+__device__ __forceinline__ RowSums join(Sums a, float top, RowSmem<NT>& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float r = warp_max(a.r);
+  move_to(a, r);
+  float s = warp_sum(a.s[0] + a.s[1]), w = warp_sum(a.w[0] + a.w[1]);
+  top = warp_max(top);
+  if (NT > 32) {
+    if (lane == 0) {
+      sh.sums[0][warp] = r;
+      sh.sums[1][warp] = s;
+      sh.sums[2][warp] = w;
+      sh.top[warp] = top;
+    }
+    __syncthreads();
+    Sums b;
+    const bool in = lane < NT / 32;
+    b.r = in ? sh.sums[0][lane] : -INFINITY;
+    b.s[0] = in ? sh.sums[1][lane] : 0.f;
+    b.w[0] = in ? sh.sums[2][lane] : 0.f;
+    b.s[1] = b.w[1] = 0.f;
+    top = warp_max(in ? sh.top[lane] : -INFINITY);
+    r = warp_max(b.r);
+    if (in) move_to(b, r);
+    s = warp_sum(b.s[0]);
+    w = warp_sum(b.w[0]);
+  }
+  return RowSums{r, __log2f(s), w / s, top};
+}
+
+// A row's sums again, from differences to its maximum: r = c m, t = (z - m) c.
+template <class T, int NT>
+__device__ RowSums far_sums(const T* z, int V, float c, RowSmem<NT>& sh, float& m) {
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < V; i += NT) top = fmaxf(top, elem_f(z[i]));
+  block_sync<NT>();
+  const float r0 = join(Sums{0.f, {1.f, 0.f}, {0.f, 0.f}}, top, sh).top;
+  m = r0 == -INFINITY ? 0.f : r0;
+  Sums a{0.f, {0.f, 0.f}, {0.f, 0.f}};
+  for (int i = threadIdx.x; i < V; i += NT) {
+    const float t = max_nan((elem_f(z[i]) - m) * c, -200.f), e = fast_exp2(t);
+    a.s[0] += e;
+    a.w[0] = fmaf(e, t, a.w[0]);
+  }
+  block_sync<NT>();
+  RowSums q = join(a, top, sh);
+  q.r = 0.f;
+  return q;
+}
+
+template <int NT>
+__device__ __forceinline__ int block_sum(int n, RowSmem<NT>& sh) {
   n = __reduce_add_sync(0xffffffffu, n);
+  if (NT == 32) return n;
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh.total[threadIdx.x >> 5] = n;
   __syncthreads();
   n = 0;
-  for (int w = 0; w < kWarps; ++w) n += sh.total[w];
+  for (int w = 0; w < NT / 32; ++w) n += sh.total[w];
   return n;
 }
 
-__device__ __forceinline__ void put(RowSmem& sh, uint32_t o, int id) {
+template <int NT>
+__device__ __forceinline__ void put(RowSmem<NT>& sh, uint32_t o, int id) {
   const int at = atomicAdd(&sh.count, 1);
   if (at < kCand) sh.cand[at] = static_cast<unsigned long long>(o) << 32 | ~static_cast<uint32_t>(id);
 }
 
 // The slow way: the k-th largest value bit by bit, then all above it and the first ids that have it.
-template <class T>
-__device__ void exact_candidates(const T* z, int V, int k, RowSmem& sh) {
+template <class T, int NT>
+__device__ __noinline__ void exact_candidates(const T* z, int V, int k, RowSmem<NT>& sh) {
+  constexpr int kShift = sizeof(T) == 2 ? 16 : 0;  // (a bf16's order is in the upper half)
+  const auto key = [&](int c) { return order_of(elem_f(z[c])) >> kShift; };
   uint32_t kth = 0;  // the largest value that at least k logits reach
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = 31 - kShift; bit >= 0; --bit) {
     const uint32_t t = kth | 1u << bit;
     int n = 0;
-    for (int c = threadIdx.x; c < V; c += kThreads) n += order_of(elem_f(z[c])) >= t;
+    for (int c = threadIdx.x; c < V; c += NT) n += key(c) >= t;
     if (block_sum(n, sh) >= k) kth = t;
   }
   if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();
-  for (int c = threadIdx.x; c < V; c += kThreads) {
-    const uint32_t o = order_of(elem_f(z[c]));
-    if (o > kth) put(sh, o, c);  // fewer than k
-  }
-  __syncthreads();
+  block_sync<NT>();
+  for (int c = threadIdx.x; c < V; c += NT)
+    if (key(c) > kth) put(sh, order_of(elem_f(z[c])), c);  // fewer than k
+  block_sync<NT>();
   int left = k - sh.count;
-  __syncthreads();
+  block_sync<NT>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int c0 = 0; c0 < V && left > 0; c0 += kThreads) {  // in the order of ids
+  for (int c0 = 0; c0 < V && left > 0; c0 += NT) {  // in the order of ids
     const int c = c0 + threadIdx.x;
-    const bool is = c < V && order_of(elem_f(z[c])) == kth;
+    const bool is = c < V && key(c) == kth;
     const uint32_t who = __ballot_sync(0xffffffffu, is);
     if (lane == 0) sh.total[warp] = __popc(who);
-    __syncthreads();
+    block_sync<NT>();
     int before = __popc(who & ((1u << lane) - 1)), all = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += sh.total[w];
       all += sh.total[w];
     }
-    if (is && before < left) put(sh, kth, c);
+    if (is && before < left) put(sh, order_of(elem_f(z[c])), c);
     left -= all;
-    __syncthreads();
+    block_sync<NT>();
   }
 }
 
-// The k largest logits with their ids, ranked, as (value, ~id) in sh.cand; returns how many candidates there are.
-template <class T>
-__device__ __forceinline__ int top_candidates(const T* z, int V, int Vv, int k, float gm, RowSmem& sh) {
-  constexpr int W = Row<T>::W;
-  const uint32_t mine = order_of(gm);
-  sh.part_max[threadIdx.x] = mine;
-  if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();
-  // the k-th largest of the parts' maxima: whoever has fewer than k above it and reaches k with its equals
-  int above = 0, equal = 0;
-  for (int i = 0; i < kThreads; ++i) {
-    above += sh.part_max[i] > mine;
-    equal += sh.part_max[i] == mine;
-  }
-  if (above < k && above + equal >= k) sh.total[0] = static_cast<int>(mine);  // (all that do write the same)
-  __syncthreads();
-  const uint32_t bound = static_cast<uint32_t>(sh.total[0]);
-  if (mine >= bound) {
-    for (int c0 = threadIdx.x * W; c0 < Vv; c0 += kThreads * W) {
-      const Pack<T, W> raw = load_pack<T, W>(z + c0);
+// The k-th largest of 32 N numbers, N a lane, by its upper 16 bits: what is returned is at most it.
+template <int N>
+__device__ __forceinline__ uint32_t kth_of(const uint32_t (&v)[N], int k) {
+  uint32_t kth = 0;
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t t = kth | 1u << bit;
+    int n = 0;
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint32_t o = order_of(raw[i]);
-        if (o >= bound) put(sh, o, c0 + i);
-      }
+    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(0xffffffffu, v[i] >= t));
+    if (n >= k) kth = t;
+  }
+  return kth;
+}
+
+// The k largest logits with their ids, and maybe others, as (value, ~id) in sh.cand; returns how many.
+template <class T, int NT>
+__device__ __forceinline__ int top_candidates(const T* z, int V, const Cut<T>& cut, int k, float top, RowSmem<NT>& sh) {
+  constexpr int W = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = order_of(top);
+  uint32_t bound;
+  if (NT == 32) {
+    const uint32_t v[1] = {mine};
+    bound = k <= 32 ? kth_of(v, k) : 0;
+    if (lane == 0) sh.count = 0;
+    __syncwarp();
+  } else {
+    // up to 16 alternatives: 32 parts are enough, of NT / 32 threads each
+    constexpr int kPer = NT / 32, kAll = NT / 32;
+    if (k <= 16) {
+      uint32_t m = mine;
+#pragma unroll
+      for (int o = kPer >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (threadIdx.x % kPer == 0) sh.part[threadIdx.x / kPer] = m;
+    } else {
+      sh.part[threadIdx.x] = mine;
     }
-    for (int c = Vv + threadIdx.x; c < V; c += kThreads) {
-      const uint32_t o = order_of(elem_f(z[c]));
-      if (o >= bound) put(sh, o, c);
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    if (k <= 16) {
+      const uint32_t v[1] = {sh.part[lane]};
+      bound = kth_of(v, k);
+    } else {
+      uint32_t v[kAll];
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) v[i] = sh.part[32 * i + lane];
+      bound = kth_of(v, k);
     }
   }
-  __syncthreads();
+  // a warp takes the parts of its threads that reach the bound, one after another
+  const float least = bound < order_of(-INFINITY) ? -INFINITY : value_of(bound);
+  const auto look = [&](float x, int c) {
+    const uint32_t o = order_of(x);
+    if (o >= bound) put(sh, o, c);
+  };
+  for (uint32_t who = __ballot_sync(0xffffffffu, mine >= bound); who; who &= who - 1) {
+    for (int i = (threadIdx.x & ~31) + __ffs(who) - 1 + lane * NT; i < cut.body; i += 32 * NT) {
+      const Pack<T, W> raw = load_pack<T, W>(z + cut.head + i * W);
+      if (largest<T>(*reinterpret_cast<const uint4*>(&raw)) < least) continue;  // (all NaN: looked at)
+#pragma unroll
+      for (int j = 0; j < W; ++j) look(raw[j], cut.head + i * W + j);
+    }
+  }
+  if (mine >= bound && threadIdx.x < cut.head + cut.tail) look(elem_f(z[cut.edge(threadIdx.x)]), cut.edge(threadIdx.x));
+  block_sync<NT>();
   if (sh.count > kCand) {
-    __syncthreads();
+    block_sync<NT>();
     exact_candidates(z, V, k, sh);
-    __syncthreads();
+    block_sync<NT>();
   }
   return min(sh.count, kCand);
 }
 
+// The next row at or after `row` (of this block's) that has a token.
+__device__ __forceinline__ int next_row(const LogprobParams& p, int row) {
+  while (row < p.T && p.tok[row] == p.ignore) row += gridDim.x;
+  return min(row, p.T);
+}
+
+template <int NT> constexpr int ctas_per_sm() { return NT == 32 ? 24 : NT == 256 ? 4 : 1; }
+
 }  // namespace
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_fwd_kernel(const LogprobParams p) {
+// NT: 32 for rows of a few pieces a lane, 256, or 1024 when there are fewer rows than SMs can take.
+template <class T, int NT>
+__global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(const LogprobParams p) {
   griddep_begin();
-  __shared__ RowSmem sh;
-  constexpr int W = Row<T>::W;
-  const int Vv = p.vec ? p.V / W * W : 0;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4 (*ring)[kU][NT] = reinterpret_cast<uint4 (*)[kU][NT]>(smem);
+  RowSmem<NT>& sh = *reinterpret_cast<RowSmem<NT>*>(smem + sizeof(uint4) * kDepth * kU * NT);
+  const int tid = threadIdx.x;
+  const float c = p.scale;
+  const T* z0 = static_cast<const T*>(p.z);
+  // the groups on their way: group ig of row irow comes next
+  const int groups = max(1, (p.V / Part<T>::W + kU * NT - 1) / (kU * NT));
+  int irow = next_row(p, blockIdx.x), ig = 0;
+  const auto issue = [&](int slot) {
+    if (irow < p.T) {
+      const T* z = z0 + irow * p.z_rs;
+      const Cut<T> cut(z, p.V);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = (ig * kU + u) * NT + tid;
+        if (i < cut.body) copy16(&ring[slot][u][tid], z + cut.head + i * Part<T>::W);
+      }
+      if (++ig == groups) {
+        ig = 0;
+        irow = next_row(p, irow + gridDim.x);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth - 1; ++d) issue(d);
+  int slot = 0, fill = kDepth - 1;  // read next, written next
   for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
     const int y = p.tok[row];
     if (y == p.ignore) {  // no arithmetic on its logits
-      if (threadIdx.x == 0) p.logprob[row] = p.entropy[row] = p.lse[row] = 0.f;
-      for (int i = threadIdx.x; i < p.k; i += kThreads) {
+      if (tid == 0) p.logprob[row] = p.entropy[row] = p.lse[row] = 0.f;
+      for (int i = tid; i < p.k; i += NT) {
         p.top_ids[static_cast<int64_t>(row) * p.k + i] = -1;
         p.top_logprobs[static_cast<int64_t>(row) * p.k + i] = 0.f;
       }
       continue;
     }
-    const T* z = static_cast<const T*>(p.z) + row * p.z_rs;
-    float gm;
-    const Sums a = row_sums(z, p.V, Vv, p.scale, sh, gm);
-    const float m = a.m == -INFINITY ? 0.f : a.m, l2 = __log2f(a.s);
-    if (threadIdx.x == 0) {
-      const bool ok = y >= 0 && y < p.V;
+    const T* z = z0 + row * p.z_rs;
+    const Cut<T> cut(z, p.V);
+    const bool ok = y >= 0 && y < p.V;
+    const float zy = tid == 0 && ok ? elem_f(z[y]) : 0.f;
+    Part<T> part;
+    part.start(c);
+    if (tid < cut.head + cut.tail) part.add(z[cut.edge(tid)], c);
+    for (int g = 0; g < groups; ++g) {
+      issue(fill);
+      copy_wait<kDepth - 1>();
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if ((g * kU + u) * NT + tid < cut.body) part.add(ring[slot][u][tid], c);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+      fill = fill + 1 == kDepth ? 0 : fill + 1;
+    }
+    RowSums q = join(part.a, part.top, sh);
+    // ln p = (z - m) / tau - l
+    float m = q.top, l2 = q.l - fmaf(m, c, -q.r);
+    if (!(fabsf(m) < kFar)) {
+      q = far_sums(z, p.V, c, sh, m);
+      l2 = q.l;
+    }
+    const float l = l2 * kLn2;
+    if (tid == 0) {
       if (!ok && p.status) *p.status = VA_ERR_BAD_TARGETS;
-      p.logprob[row] = ok ? fmaf(elem_f(z[y]) - m, p.inv_t, -l2 * kLn2) : NAN;
-      p.entropy[row] = (l2 - a.w / a.s) * kLn2;
+      p.logprob[row] = ok ? fmaf(zy - m, p.inv_t, -l) : NAN;
+      p.entropy[row] = (q.l - q.mean_t) * kLn2;
       p.lse[row] = static_cast<float>(static_cast<double>(m) / p.temperature + static_cast<double>(l2) * 0.69314718055994531);
     }
     if (p.k > 0) {
-      const int n = top_candidates(z, p.V, Vv, p.k, gm, sh);
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long c = sh.cand[i];
+      const int n = top_candidates(z, p.V, cut, p.k, part.top, sh);
+      for (int i = tid; i < n; i += NT) {
+        const unsigned long long v = sh.cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.cand[j] > c;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > v;
         if (rank < p.k) {
-          p.top_ids[static_cast<int64_t>(row) * p.k + rank] = static_cast<int32_t>(~static_cast<uint32_t>(c));
+          p.top_ids[static_cast<int64_t>(row) * p.k + rank] = static_cast<int32_t>(~static_cast<uint32_t>(v));
           p.top_logprobs[static_cast<int64_t>(row) * p.k + rank] =
-              fmaf(value_of(static_cast<uint32_t>(c >> 32)) - m, p.inv_t, -l2 * kLn2);
+              fmaf(value_of(static_cast<uint32_t>(v >> 32)) - m, p.inv_t, -l);
         }
       }
     }
-    __syncthreads();
+    block_sync<NT>();
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_bwd_kernel(const LogprobParams p) {
+// Blocks share a row's `slices` (one where the gradient lies on the logits: a row's sums may be formed again).
+template <class T, int NT>
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) logprobs_bwd_kernel(const LogprobParams p) {
   griddep_begin();
-  __shared__ RowSmem sh;
-  constexpr int W = Row<T>::W;
-  const int Vv = p.vec ? p.V / W * W : 0;
-  for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
+  __shared__ RowSmem<NT> sh;
+  constexpr int W = 16 / sizeof(T);
+  const int tid = threadIdx.x;
+  const int64_t items = static_cast<int64_t>(p.T) * p.slices;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int row = static_cast<int>(item / p.slices), slice = static_cast<int>(item % p.slices);
     const int y = p.tok[row];
+    const T* z = static_cast<const T*>(p.z) + row * p.z_rs;
     T* gr = static_cast<T*>(p.grad) + row * p.g_rs;
+    Cut<T> cut(gr, p.V);
+    const bool same = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(gr)) & 15u) == 0;
+    const int i0 = static_cast<int>(static_cast<int64_t>(cut.body) * slice / p.slices);
+    const int i1 = static_cast<int>(static_cast<int64_t>(cut.body) * (slice + 1) / p.slices);
+    const bool edges = slice == 0 && tid < cut.head + cut.tail;
     if (y == p.ignore) {
       Pack<T, W> zero;
 #pragma unroll
       for (int i = 0; i < W; ++i) zero.set(i, 0.f);
-      for (int c = threadIdx.x * W; c < Vv; c += kThreads * W) store_pack_cs(gr + c, zero);
-      for (int c = Vv + threadIdx.x; c < p.V; c += kThreads) gr[c] = elem_of<T>(0.f);
+      for (int i = i0 + tid; i < i1; i += NT) store_pack_cs(gr + cut.head + i * W, zero);
+      if (edges) gr[cut.edge(tid)] = elem_of<T>(0.f);
       continue;
     }
-    const T* z = static_cast<const T*>(p.z) + row * p.z_rs;
-    // log2 p = (z - m) scale - l2, with m = 0 where lse is precise enough; then the products' low halves count in fp32
+    // log2 p = (z - m) c - l2, with m = 0 where lse is precise enough; then the products' low halves count in fp32
     const float lse = p.lse[row];
-    float m = 0.f, l2 = lse * kLog2e, l2_lo = fmaf(lse, kLog2e, -l2) + lse * kLog2eLo, scale_lo = p.scale_lo;
+    float m = 0.f, l2 = lse * kLog2e, l2_lo = fmaf(lse, kLog2e, -l2) + lse * kLog2eLo, c_lo = p.scale_lo;
     if (!(fabsf(lse) <= (sizeof(T) == 2 ? 256.f : 32.f))) {
-      float gm;
-      const Sums a = row_sums(z, p.V, Vv, p.scale, sh, gm);
-      m = a.m == -INFINITY ? 0.f : a.m;
-      l2 = __log2f(a.s);
-      l2_lo = scale_lo = 0.f;
-      __syncthreads();  // the whole row is read before any of it is written: grad may be the logits
+      l2 = far_sums(z, p.V, p.scale, sh, m).l;
+      l2_lo = c_lo = 0.f;
+      block_sync<NT>();  // the whole row is read before any of it is written
     }
     const bool ok = y >= 0 && y < p.V;
     const float dl = ok ? p.dlogprob[row] * p.inv_t : NAN, dh = p.dentropy ? p.dentropy[row] * p.inv_t : 0.f;
     // dz = p (c1 + c2 log2 p) + [c == y] dl
     const float c1 = -fmaf(dh, p.dentropy ? p.entropy[row] : 0.f, dl), c2 = -dh * kLn2;
-    const auto one = [&](float x, int c) {
+    const auto one = [&](float x) {
       const float u = sizeof(T) == 4 ? max_nan(x - m, -1e30f) : x - m;  // (-inf times the low half would be NaN)
       float t = fmaf(u, p.scale, -l2);
-      if (sizeof(T) == 4) t += fmaf(u, scale_lo, -l2_lo);
+      if (sizeof(T) == 4) t += fmaf(u, c_lo, -l2_lo);
       t = max_nan(t, -200.f);
-      const float v = fast_exp2(t) * fmaf(c2, t, c1);
-      return c == y ? v + dl : v;
+      return fast_exp2(t) * fmaf(c2, t, c1);
     };
-    each_piece(z, Vv, [&](int c0, const float (&x)[W]) {
+    const auto write = [&](int i, const Pack<T, W>& raw) {
       Pack<T, W> o;
+      float v[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) o.set(i, one(x[i], c0 + i));
-      store_pack_cs(gr + c0, o);
-    });
-    for (int c = Vv + threadIdx.x; c < p.V; c += kThreads) gr[c] = elem_of<T>(one(elem_f(z[c]), c));
+      for (int j = 0; j < W; ++j) v[j] = one(raw[j]);
+      const int at = y - (cut.head + i * W);
+      if (static_cast<unsigned>(at) < static_cast<unsigned>(W)) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += j == at ? dl : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) o.set(j, v[j]);
+      store_pack_cs(gr + cut.head + i * W, o);
+    };
+    if (same) {
+      for (int b = i0 + tid; b < i1; b += kU * NT) {
+        Pack<T, W> raw[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (b + u * NT < i1) raw[u] = load_pack<T, W>(z + cut.head + (b + u * NT) * W);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (b + u * NT < i1) write(b + u * NT, raw[u]);
+      }
+    } else {  // the logits' rows lie otherwise than the gradient's: element by element
+      for (int i = i0 + tid; i < i1; i += NT) {
+        Pack<T, W> raw;
+#pragma unroll
+        for (int j = 0; j < W; ++j) raw.e[j] = z[cut.head + i * W + j];
+        write(i, raw);
+      }
+    }
+    if (edges) {
+      const int e = cut.edge(tid);
+      gr[e] = elem_of<T>(one(elem_f(z[e])) + (e == y ? dl : 0.f));
+    }
   }
 }
 
@@ -341,29 +570,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_bwd_kernel(cons
 
 namespace {
 
-int row_ctas(int T) {
+int device_sms() {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(std::max(sms, 1)) * kCtasPerSm));
+  return std::max(sms, 1);
 }
 
-bool rows16(const void* p, int64_t rs, int es) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && rs * es % 16 == 0; }
+template <class T, int NT>
+cudaError_t run_fwd(const LogprobParams& p, int sms, cudaStream_t st) {
+  const auto kernel = logprobs_fwd_kernel<T, NT>;
+  constexpr size_t smem = sizeof(uint4) * kDepth * kU * NT + sizeof(RowSmem<NT>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int grid = static_cast<int>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * ctas_per_sm<NT>()));
+  return launch_pdl(kernel, dim3(grid), dim3(NT), smem, st, p);
+}
+
+// A warp a row for rows of at most 4 KB (256 threads would hold a piece each, or none), a large block while a
+// quarter as many as fit still take a row each.
+template <class T>
+cudaError_t pick_fwd(const LogprobParams& p, cudaStream_t st) {
+  const int sms = device_sms();
+  if (static_cast<int64_t>(p.V) * sizeof(T) <= 4096 && p.k <= 16) return run_fwd<T, 32>(p, sms, st);
+  return p.T <= sms ? run_fwd<T, 1024>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
+}
+
+template <class T>
+cudaError_t pick_bwd(LogprobParams p, cudaStream_t st) {
+  const int sms = device_sms();
+  const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
+  if (bytes <= 4096) {
+    p.slices = 1;
+    return launch_pdl(logprobs_bwd_kernel<T, 32>, dim3(static_cast<unsigned>(std::min<int64_t>(p.T, sms * 24))), dim3(32), 0,
+                      st, p);
+  }
+  // few rows: pieces of at least a group a thread, until there is one for every block that fits
+  const int64_t fit = static_cast<int64_t>(sms) * 4, group = kU * 256 * 16;
+  const uintptr_t z = reinterpret_cast<uintptr_t>(p.z), g = reinterpret_cast<uintptr_t>(p.grad);
+  const uintptr_t zn = (static_cast<uintptr_t>(p.T - 1) * p.z_rs + p.V) * sizeof(T);
+  const uintptr_t gn = (static_cast<uintptr_t>(p.T - 1) * p.g_rs + p.V) * sizeof(T);
+  const bool apart = z + zn <= g || g + gn <= z;
+  p.slices = apart ? static_cast<int>(std::max<int64_t>(1, std::min(fit / p.T, bytes / group))) : 1;
+  const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.T) * p.slices, fit));
+  return launch_pdl(logprobs_bwd_kernel<T, 256>, dim3(grid), dim3(256), 0, st, p);
+}
 
 }  // namespace
 
 cudaError_t launch_logprobs_fwd(LogprobParams p, int bf16, cudaStream_t st) {
-  p.vec = rows16(p.z, p.z_rs, bf16 ? 2 : 4);
-  const dim3 grid(row_ctas(p.T));
-  return bf16 ? launch_pdl(logprobs_fwd_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, p)
-              : launch_pdl(logprobs_fwd_kernel<float>, grid, dim3(kThreads), 0, st, p);
+  return bf16 ? pick_fwd<__nv_bfloat16>(p, st) : pick_fwd<float>(p, st);
 }
 
 cudaError_t launch_logprobs_bwd(LogprobParams p, int bf16, cudaStream_t st) {
-  p.vec = rows16(p.z, p.z_rs, bf16 ? 2 : 4) && rows16(p.grad, p.g_rs, bf16 ? 2 : 4);
-  const dim3 grid(row_ctas(p.T));
-  return bf16 ? launch_pdl(logprobs_bwd_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, p)
-              : launch_pdl(logprobs_bwd_kernel<float>, grid, dim3(kThreads), 0, st, p);
+  return bf16 ? pick_bwd<__nv_bfloat16>(p, st) : pick_bwd<float>(p, st);
 }
 
 }  // namespace va

@@ -28,7 +28,7 @@ struct LogprobParams {
   void* grad;
   int64_t g_rs;
   int32_t* status;  // forward: set to VA_ERR_BAD_TARGETS, never cleared; may be null
-  int vec;          // rows can be moved in 16-byte pieces
+  int slices;       // backward: blocks that share a row (set by the launcher)
 };
 
 cudaError_t launch_logprobs_fwd(LogprobParams p, int bf16, cudaStream_t st);

@@ -1069,6 +1069,7 @@ static void set_temperature(LogprobParams& p, float temperature) {
   p.inv_t = 1.f / temperature;
   p.scale = static_cast<float>(scale);
   p.scale_lo = static_cast<float>(scale - p.scale);
+  p.inv_c = 1.f / p.scale;
 }
 
 va_status varlen_token_logprobs_fwd(const void* z, int32_t dtype, int64_t z_rs, const int32_t* tok, int32_t T,

@@ -36,7 +36,7 @@ constexpr float kLog2eLo = static_cast<float>(1.4426950408889634 - static_cast<d
 
 constexpr int kU = 4;          // 16-byte pieces of a group
 constexpr int kDepth = 3;      // groups a thread has on their way
-constexpr int kCand = 512;     // candidates a row may have before it takes the slow way
+constexpr int kCand = 256;     // candidates a row may have before it takes the slow way
 constexpr float kFar = 1e29f;  // logits beyond this take differences before products
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -105,6 +105,14 @@ __device__ __forceinline__ float largest(const uint4& raw) {
   return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
 }
 
+template <class T>
+__device__ __forceinline__ uint4 larger(const uint4& a, const uint4& b) {
+  const auto one = [](uint32_t x, uint32_t y) {
+    return sizeof(T) == 2 ? max2(x, y) : __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+  };
+  return make_uint4(one(a.x, b.x), one(a.y, b.y), one(a.z, b.z), one(a.w, b.w));
+}
+
 // What a thread has seen of a row.
 template <class T>
 struct Part {
@@ -130,22 +138,26 @@ struct Part {
       set_floor(m - 200.f / c - fabsf(m) * 0.015625f);
     }
   }
-  __device__ __forceinline__ void add(const uint4& raw, float c) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    see(largest<T>(raw), c);
-    if (sizeof(T) == 2) {
+  __device__ __forceinline__ void add(const uint4 (&raw)[kU], float c) {
+    uint4 m = raw[0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = max2_nan(w[i], floor);
-        add2(a, low_f(x), high_f(x), c);
+    for (int u = 1; u < kU; ++u) m = larger<T>(m, raw[u]);
+    see(largest<T>(m), c);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      if (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = max2_nan(w[i], floor);
+          add2(a, low_f(x), high_f(x), c);
+        }
+      } else {
+        const float lo = __uint_as_float(floor);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+          add2(a, max_nan(__uint_as_float(w[i]), lo), max_nan(__uint_as_float(w[i + 1]), lo), c);
       }
-    } else {
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
-      const float lo = __uint_as_float(floor);
-      add2(a, max_nan(x[0], lo), max_nan(x[1], lo), c);
-      add2(a, max_nan(x[2], lo), max_nan(x[3], lo), c);
     }
   }
   __device__ __forceinline__ void add(T z, float c) {  // one logit
@@ -172,13 +184,15 @@ struct Cut {
   __device__ __forceinline__ int edge(int i) const { return i < head ? i : i + body * W; }  // i < head + tail
 };
 
+// What a block's warps share of a row.  A block has two of them and takes them in turn: the first barrier of a row
+// comes after every warp is done with the row before the last.
 template <int NT>
 struct RowSmem {
   unsigned long long cand[kCand];  // value, then ~id
   float sums[3][NT / 32];          // the warps' (r, s, w)
-  float top[NT / 32];
-  uint32_t part[NT];               // the parts' largest logits
+  uint32_t part[256];              // the parts' largest logits
   int total[NT / 32];
+  uint8_t list[NT / 32][32];       // a warp's threads whose part is looked at again
   int count;
 };
 
@@ -188,51 +202,47 @@ __device__ __forceinline__ void block_sync() {
   else __syncthreads();
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+__device__ __forceinline__ float warp_max(float x) {  // one instruction on whole numbers; no NaN comes here
+  return value_of(__reduce_max_sync(0xffffffffu, order_of(x)));
 }
-__device__ __forceinline__ float warp_sum(float x) {
+template <int N>
+__device__ __forceinline__ float warp_sum(float x) {  // over N lanes that follow one another
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = N >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// A row's sums: log2 p = t - l, t = c z - r; top the largest logit.
+// A row's sums: log2 p = t - l, t = c z - r; mean_t = sum p t.
 struct RowSums {
-  float r, l, mean_t, top;  // mean_t = sum p t
+  float r, l, mean_t;
 };
 
 // The block's sums, the same in every thread.
 template <int NT>
-__device__ __forceinline__ RowSums join(Sums a, float top, RowSmem<NT>& sh) {
+__device__ __forceinline__ RowSums join(Sums a, RowSmem<NT>& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float r = warp_max(a.r);
   move_to(a, r);
-  float s = warp_sum(a.s[0] + a.s[1]), w = warp_sum(a.w[0] + a.w[1]);
-  top = warp_max(top);
+  float s = warp_sum<32>(a.s[0] + a.s[1]), w = warp_sum<32>(a.w[0] + a.w[1]);
   if (NT > 32) {
     if (lane == 0) {
       sh.sums[0][warp] = r;
       sh.sums[1][warp] = s;
       sh.sums[2][warp] = w;
-      sh.top[warp] = top;
     }
     __syncthreads();
+    constexpr int N = NT / 32;
     Sums b;
-    const bool in = lane < NT / 32;
-    b.r = in ? sh.sums[0][lane] : -INFINITY;
-    b.s[0] = in ? sh.sums[1][lane] : 0.f;
-    b.w[0] = in ? sh.sums[2][lane] : 0.f;
+    b.r = sh.sums[0][lane % N];
+    b.s[0] = sh.sums[1][lane % N];
+    b.w[0] = sh.sums[2][lane % N];
     b.s[1] = b.w[1] = 0.f;
-    top = warp_max(in ? sh.top[lane] : -INFINITY);
     r = warp_max(b.r);
-    if (in) move_to(b, r);
-    s = warp_sum(b.s[0]);
-    w = warp_sum(b.w[0]);
+    move_to(b, r);
+    s = warp_sum<N>(b.s[0]);
+    w = warp_sum<N>(b.w[0]);
   }
-  return RowSums{r, __log2f(s), w / s, top};
+  return RowSums{r, __log2f(s), w / s};
 }
 
 // A row's sums again, from differences to its maximum: r = c m, t = (z - m) c.
@@ -241,7 +251,7 @@ __device__ RowSums far_sums(const T* z, int V, float c, RowSmem<NT>& sh, float& 
   float top = -INFINITY;
   for (int i = threadIdx.x; i < V; i += NT) top = fmaxf(top, elem_f(z[i]));
   block_sync<NT>();
-  const float r0 = join(Sums{0.f, {1.f, 0.f}, {0.f, 0.f}}, top, sh).top;
+  const float r0 = join(Sums{top, {0.f, 0.f}, {0.f, 0.f}}, sh).r;
   m = r0 == -INFINITY ? 0.f : r0;
   Sums a{0.f, {0.f, 0.f}, {0.f, 0.f}};
   for (int i = threadIdx.x; i < V; i += NT) {
@@ -250,7 +260,7 @@ __device__ RowSums far_sums(const T* z, int V, float c, RowSmem<NT>& sh, float& 
     a.w[0] = fmaf(e, t, a.w[0]);
   }
   block_sync<NT>();
-  RowSums q = join(a, top, sh);
+  RowSums q = join(a, sh);
   q.r = 0.f;
   return q;
 }
@@ -310,68 +320,77 @@ __device__ __noinline__ void exact_candidates(const T* z, int V, int k, RowSmem<
   }
 }
 
-// The k-th largest of 32 N numbers, N a lane, by its upper 16 bits: what is returned is at most it.
+// The k-th largest of 32 N numbers, N a lane, by its upper 16 bits, two at a time: what is returned is at most it.
 template <int N>
 __device__ __forceinline__ uint32_t kth_of(const uint32_t (&v)[N], int k) {
   uint32_t kth = 0;
-  for (int bit = 31; bit >= 16; --bit) {
-    const uint32_t t = kth | 1u << bit;
-    int n = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(0xffffffffu, v[i] >= t));
-    if (n >= k) kth = t;
+  for (int bit = 30; bit >= 16; bit -= 2) {
+    int n[3] = {0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) n[j] += __popc(__ballot_sync(0xffffffffu, v[i] >= (kth | (j + 1u) << bit)));
+    kth |= static_cast<uint32_t>((n[0] >= k) + (n[1] >= k) + (n[2] >= k)) << bit;
   }
   return kth;
 }
 
+// The parts of a row: up to 16 alternatives are bounded by the maxima of 32 parts, more by those of 128 or 256 (the
+// more, the closer, but the search for the k-th takes a vote for each 32 of them and bit); a short row's pieces lie
+// with as many threads.
+template <int NT>
+__device__ __forceinline__ int part_words(int k, int body) {
+  return NT == 32 || (k <= 16 && body >= NT) ? 1 : NT >= 128 && k <= 64 && body >= NT ? 4 : NT < 256 ? NT / 32 : 8;
+}
+
+// Written before the barrier of the row's sums.
+template <int NT>
+__device__ __forceinline__ void put_part(uint32_t mine, int words, RowSmem<NT>& sh) {
+  const int per = NT / (32 * words);
+  for (int o = per >> 1; o > 0; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+  if (threadIdx.x % per == 0) sh.part[threadIdx.x / per] = mine;
+}
+template <int NT, int N>
+__device__ __forceinline__ uint32_t part_bound(int k, const RowSmem<NT>& sh) {
+  uint32_t v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = sh.part[32 * i + (threadIdx.x & 31)];
+  return kth_of(v, k);
+}
+
 // The k largest logits with their ids, and maybe others, as (value, ~id) in sh.cand; returns how many.
 template <class T, int NT>
-__device__ __forceinline__ int top_candidates(const T* z, int V, const Cut<T>& cut, int k, float top, RowSmem<NT>& sh) {
+__device__ __forceinline__ int top_candidates(const T* z, int V, const Cut<T>& cut, int k, uint32_t mine, int words,
+                                              RowSmem<NT>& sh) {
   constexpr int W = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
-  const uint32_t mine = order_of(top);
   uint32_t bound;
   if (NT == 32) {
     const uint32_t v[1] = {mine};
     bound = k <= 32 ? kth_of(v, k) : 0;
-    if (lane == 0) sh.count = 0;
-    __syncwarp();
   } else {
-    // up to 16 alternatives: 32 parts are enough, of NT / 32 threads each
-    constexpr int kPer = NT / 32, kAll = NT / 32;
-    if (k <= 16) {
-      uint32_t m = mine;
-#pragma unroll
-      for (int o = kPer >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (threadIdx.x % kPer == 0) sh.part[threadIdx.x / kPer] = m;
-    } else {
-      sh.part[threadIdx.x] = mine;
-    }
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    if (k <= 16) {
-      const uint32_t v[1] = {sh.part[lane]};
-      bound = kth_of(v, k);
-    } else {
-      uint32_t v[kAll];
-#pragma unroll
-      for (int i = 0; i < kAll; ++i) v[i] = sh.part[32 * i + lane];
-      bound = kth_of(v, k);
-    }
+    bound = words == 1 ? part_bound<NT, 1>(k, sh) : words == 4 ? part_bound<NT, 4>(k, sh) : part_bound<NT, 8>(k, sh);
   }
-  // a warp takes the parts of its threads that reach the bound, one after another
+  // a warp's lanes share the pieces of those of its threads whose part reaches the bound
   const float least = bound < order_of(-INFINITY) ? -INFINITY : value_of(bound);
   const auto look = [&](float x, int c) {
     const uint32_t o = order_of(x);
     if (o >= bound) put(sh, o, c);
   };
-  for (uint32_t who = __ballot_sync(0xffffffffu, mine >= bound); who; who &= who - 1) {
-    for (int i = (threadIdx.x & ~31) + __ffs(who) - 1 + lane * NT; i < cut.body; i += 32 * NT) {
-      const Pack<T, W> raw = load_pack<T, W>(z + cut.head + i * W);
-      if (largest<T>(*reinterpret_cast<const uint4*>(&raw)) < least) continue;  // (all NaN: looked at)
+  const uint32_t who = __ballot_sync(0xffffffffu, mine >= bound);
+  uint8_t* list = sh.list[threadIdx.x >> 5];
+  if (mine >= bound) list[__popc(who & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
+  __syncwarp();
+  const int per = (cut.body + NT - 1) / NT, n = __popc(who) * per;
+#pragma unroll 2
+  for (int w = lane; w < n; w += 32) {
+    const int j = w / per, i = (threadIdx.x & ~31) + list[j] + (w - j * per) * NT;
+    if (i >= cut.body) continue;
+    const Pack<T, W> raw = load_pack<T, W>(z + cut.head + i * W);
+    if (largest<T>(*reinterpret_cast<const uint4*>(&raw)) < least) continue;  // (all NaN: looked at)
 #pragma unroll
-      for (int j = 0; j < W; ++j) look(raw[j], cut.head + i * W + j);
-    }
+    for (int e = 0; e < W; ++e) look(raw[e], cut.head + i * W + e);
   }
   if (mine >= bound && threadIdx.x < cut.head + cut.tail) look(elem_f(z[cut.edge(threadIdx.x)]), cut.edge(threadIdx.x));
   block_sync<NT>();
@@ -389,32 +408,37 @@ __device__ __forceinline__ int next_row(const LogprobParams& p, int row) {
   return min(row, p.T);
 }
 
-template <int NT> constexpr int ctas_per_sm() { return NT == 32 ? 24 : NT == 256 ? 4 : 1; }
+template <int NT> constexpr int ctas_per_sm() { return NT == 32 ? 20 : NT == 128 ? 7 : NT == 256 ? 4 : 1; }
 
 }  // namespace
 
-// NT: 32 for rows of a few pieces a lane, 256, or 1024 when there are fewer rows than SMs can take.
+// NT: threads of a block (see pick_fwd).
 template <class T, int NT>
 __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(const LogprobParams p) {
   griddep_begin();
   extern __shared__ __align__(16) uint8_t smem[];
   uint4 (*ring)[kU][NT] = reinterpret_cast<uint4 (*)[kU][NT]>(smem);
-  RowSmem<NT>& sh = *reinterpret_cast<RowSmem<NT>*>(smem + sizeof(uint4) * kDepth * kU * NT);
+  RowSmem<NT>* const shared = reinterpret_cast<RowSmem<NT>*>(smem + sizeof(uint4) * kDepth * kU * NT);
   const int tid = threadIdx.x;
   const float c = p.scale;
   const T* z0 = static_cast<const T*>(p.z);
   // the groups on their way: group ig of row irow comes next
   const int groups = max(1, (p.V / Part<T>::W + kU * NT - 1) / (kU * NT));
-  int irow = next_row(p, blockIdx.x), ig = 0;
+  int irow = next_row(p, blockIdx.x), ig = 0, ileft = 0;
+  const uint4* from = nullptr;
   const auto issue = [&](int slot) {
     if (irow < p.T) {
-      const T* z = z0 + irow * p.z_rs;
-      const Cut<T> cut(z, p.V);
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = (ig * kU + u) * NT + tid;
-        if (i < cut.body) copy16(&ring[slot][u][tid], z + cut.head + i * Part<T>::W);
+      if (ig == 0) {
+        const T* z = z0 + irow * p.z_rs;
+        const Cut<T> cut(z, p.V);
+        ileft = cut.body - tid;
+        from = reinterpret_cast<const uint4*>(z + cut.head) + tid;
       }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (u * NT < ileft) copy16(&ring[slot][u][tid], from + u * NT);
+      ileft -= kU * NT;
+      from += kU * NT;
       if (++ig == groups) {
         ig = 0;
         irow = next_row(p, irow + gridDim.x);
@@ -425,6 +449,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(con
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) issue(d);
   int slot = 0, fill = kDepth - 1;  // read next, written next
+  int turn = 0;
+  if (tid == 0) shared[0].count = 0;
   for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
     const int y = p.tok[row];
     if (y == p.ignore) {  // no arithmetic on its logits
@@ -445,15 +471,28 @@ __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(con
     for (int g = 0; g < groups; ++g) {
       issue(fill);
       copy_wait<kDepth - 1>();
+      uint4 raw[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if ((g * kU + u) * NT + tid < cut.body) part.add(ring[slot][u][tid], c);
+      for (int u = 0; u < kU; ++u) raw[u] = ring[slot][u][tid];
+      if ((g + 1) * kU * NT > cut.body) {  // a group that is not whole
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if ((g * kU + u) * NT + tid >= cut.body) raw[u] = make_uint4(none, none, none, none);
+      }
+      part.add(raw, c);
       slot = slot + 1 == kDepth ? 0 : slot + 1;
       fill = fill + 1 == kDepth ? 0 : fill + 1;
     }
-    RowSums q = join(part.a, part.top, sh);
-    // ln p = (z - m) / tau - l
-    float m = q.top, l2 = q.l - fmaf(m, c, -q.r);
+    RowSmem<NT>& sh = shared[turn];
+    turn ^= 1;
+    const uint32_t mine = order_of(part.top);
+    const int words = part_words<NT>(p.k, p.V / Part<T>::W - 1);
+    if (NT > 32 && p.k > 0) put_part(mine, words, sh);
+    RowSums q = join(part.a, sh);
+    if (tid == 0) shared[turn].count = 0;  // (behind the barrier: nobody is at the row before any more)
+    // ln p = (z - m) / tau - l, m near the largest logit
+    float m = q.r * p.inv_c, l2 = q.l - fmaf(m, c, -q.r);
     if (!(fabsf(m) < kFar)) {
       q = far_sums(z, p.V, c, sh, m);
       l2 = q.l;
@@ -466,7 +505,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(con
       p.lse[row] = static_cast<float>(static_cast<double>(m) / p.temperature + static_cast<double>(l2) * 0.69314718055994531);
     }
     if (p.k > 0) {
-      const int n = top_candidates(z, p.V, cut, p.k, part.top, sh);
+      const int n = top_candidates(z, p.V, cut, p.k, mine, words, sh);
       for (int i = tid; i < n; i += NT) {
         const unsigned long long v = sh.cand[i];
         int rank = 0;
@@ -477,8 +516,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(con
               fmaf(value_of(static_cast<uint32_t>(v >> 32)) - m, p.inv_t, -l);
         }
       }
+      if (NT == 32) __syncwarp();
     }
-    block_sync<NT>();
   }
 }
 
@@ -580,20 +619,23 @@ int device_sms() {
 template <class T, int NT>
 cudaError_t run_fwd(const LogprobParams& p, int sms, cudaStream_t st) {
   const auto kernel = logprobs_fwd_kernel<T, NT>;
-  constexpr size_t smem = sizeof(uint4) * kDepth * kU * NT + sizeof(RowSmem<NT>);
+  constexpr size_t smem = sizeof(uint4) * kDepth * kU * NT + 2 * sizeof(RowSmem<NT>);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * ctas_per_sm<NT>()));
   return launch_pdl(kernel, dim3(grid), dim3(NT), smem, st, p);
 }
 
-// A warp a row for rows of at most 4 KB (256 threads would hold a piece each, or none), a large block while a
-// quarter as many as fit still take a row each.
+// us a call: a warp a row for rows up to 16 KB (T = 16384, V = 3000 bf16, k = 0: 40, with 256 threads 78); 128 threads for few
+// alternatives of rows up to 64 KB (T = 8192, V = 32768 bf16, k = 5: 113, with 256 threads 128; k = 20: 163 and 171, but V = 131072, k = 20: 175
+// and 132, as each part that is looked at again is twice as long); 1024 while every row has an SM (T = 64, V = 32000: 9 and 12).
 template <class T>
 cudaError_t pick_fwd(const LogprobParams& p, cudaStream_t st) {
   const int sms = device_sms();
-  if (static_cast<int64_t>(p.V) * sizeof(T) <= 4096 && p.k <= 16) return run_fwd<T, 32>(p, sms, st);
-  return p.T <= sms ? run_fwd<T, 1024>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
+  const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
+  if (bytes <= 16384 && p.k <= 32) return run_fwd<T, 32>(p, sms, st);
+  if (p.T <= sms) return run_fwd<T, 1024>(p, sms, st);
+  return bytes <= 65536 && p.k <= 8 ? run_fwd<T, 128>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
 }
 
 template <class T>

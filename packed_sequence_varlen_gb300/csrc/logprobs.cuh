@@ -16,7 +16,7 @@ struct LogprobParams {
   int T, V, ignore, k;
   float temperature;
   float scale, scale_lo;  // log2(e) / temperature, and what its rounding leaves
-  float inv_t;    // 1 / temperature
+  float inv_t, inv_c;     // 1 / temperature, 1 / scale
   float* logprob; // [T]
   float* entropy; // [T]
   float* lse;     // [T]

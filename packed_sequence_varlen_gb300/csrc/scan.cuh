@@ -22,13 +22,14 @@ struct ScanParams {
   int tiles, cols;     // tiles of rows, columns of channels (set by the launcher)
   int32_t* status;     // workspace header's status word
   int32_t* ticket;
-  int32_t* flags;      // [tiles][cols] a tile's map is there, then [groups][cols] a group's state is there
-  float2* agg;         // [tiles][cols * width] a tile's map (decay product, state from zero)
+  int64_t runs;        // runs of rows, and one tile's more
+  int32_t* first;      // [runs] the first segment that starts at a run's first row or later
+  float* agg;          // [tiles][cols * width][2] a tile's map (decay product, state from zero)
   float* carry;        // [groups][cols * width] the state after a group of tiles
 };
 
 size_t scan_workspace(int T, int D);
-// stage 0: boundary check and cleared flags, 1: the recurrence.  dtypes: 0 fp32, 1 bf16.
+// stage 0: boundary check, empty places and look-ups, 1: the recurrence.  dtypes: 0 fp32, 1 bf16.
 cudaError_t launch_scan_fwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
 cudaError_t launch_scan_bwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
 // The forward of single tokens (T == B): every state moves on by one step.  One launch.

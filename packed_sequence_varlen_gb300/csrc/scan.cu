@@ -11,12 +11,13 @@
 //   the state that enters the tile is folded from the maps of the tiles before it in its group of kGroup and
 //   the state after the group before that one, which that group's last tile publishes,
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
-// So the data is read once and written once.  A tile's data is copied to shared memory asynchronously, each thread its own
-// part, a few tiles ahead.  The fold's order is fixed by the tile's number, whatever is finished first, so results do
-// not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that is waited for is
-// a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.  What is published is
-// its own flag: the places hold a NaN of all ones before, which is never written (no fences, and a single trip to L2
-// where it is there).  A segment's start (backward: its end) inside a run replaces the state instead of multiplying
+// So the data is read once and written once.  A warp of its own takes the tiles' numbers, looks their segments up and has
+// their data copied to shared memory (TMA), a few tiles ahead of the others.  (Rows that are not on 16-byte boundaries are
+// read by the others straight from memory, twice.)  The fold's order is fixed by the tile's number, whatever is finished
+// first, so results do not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that
+// is waited for is a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.
+// What is published is its own flag: the places hold a NaN of all ones before, which is never written (no fences, and a
+// single trip to L2 where it is there).  A segment's start (backward: its end) inside a run replaces the state instead of multiplying
 // it by zero, so nothing of another segment gets in, infinities and NaN included, and no tile waits across one.
 //
 // A = exp(sum of g), rounded once, and not the product of the a: the approximate exponential of an a near 1 has a
@@ -26,6 +27,7 @@
 #include "elem.cuh"
 #include "scan.cuh"
 #include "sm100_ptx.cuh"
+#include "tmap.cuh"
 
 namespace va {
 
@@ -37,26 +39,17 @@ constexpr int kPrepThreads = 1024;
 // writes those of the tile after.
 constexpr int kRings = 3;
 
-// How a block works: W warps, each with a run of R rows of 32 V channels; S tiles on their way or in work.
-// kMost: blocks an SM (shared memory may allow fewer).
+// How a block works: W warps, each with a run of R rows of 32 V channels; S tiles on their way or in work; at most M
+// blocks an SM (shared memory may allow fewer).
 template <int V_, int W_, int R_, int S_, int M_>
 struct Shape {
-  static constexpr int V = V_, W = W_, R = R_, S = S_, kThreads = 32 * W_, kRows = W_ * R_, kWidth = 32 * V_, kMost = M_;
+  static constexpr int V = V_, W = W_, R = R_, S = S_, M = M_;
+  static constexpr int kThreads = 32 * (W_ + 1), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
 };
 
-template <int BYTES>
-__device__ __forceinline__ void copy_piece(void* to, const void* from) {
-  if constexpr (BYTES >= 4) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
-  } else {
-    *static_cast<volatile uint16_t*>(to) = *static_cast<const uint16_t*>(from);
-  }
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 __device__ __forceinline__ float decay(float g) { return fast_exp2(g * kLog2e); }
+// f of a row from its e, rounded by itself: not folded into the next sum here and there.
+__device__ __forceinline__ float back_step(float g, float e) { return __fmul_rn(decay(g), e); }
 // A run's decay, rounded once.
 __device__ __forceinline__ float run_decay(float sum) { return 1.f + expm1f(sum); }
 
@@ -98,7 +91,7 @@ __device__ __forceinline__ bool there(const float (&v)[N]) {
 
 // Waits until the N words of every lane that asks are there (a warp's call); false when the call is to be given up.
 template <int N>
-__device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], int32_t* status) {
+__device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], WsHeader* hdr) {
   if (ask) peek<N>(p, v);
   if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
   const uint64_t t0 = sm100::globaltimer();
@@ -106,9 +99,9 @@ __device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], i
     if (ask) peek<N>(p, v);
     if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
     if ((i & 63u) == 0) {
-      bool stop = *reinterpret_cast<volatile int32_t*>(status) != VA_OK;
+      bool stop = *reinterpret_cast<volatile int32_t*>(&hdr->status) != VA_OK;
       if (!stop && sm100::globaltimer() - t0 > sm100::kTimeoutNs) {
-        atomicCAS(status, 0, VA_ERR_TIMEOUT);
+        set_status(hdr, VA_ERR_TIMEOUT);
         stop = true;
       }
       if (__any_sync(0xffffffffu, stop)) return false;
@@ -116,76 +109,61 @@ __device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], i
   }
 }
 
-// What the warps of a block exchange; channel = lane * V + i of the tile's columns.
+// A tile as the copying warp leaves it for the others.
+template <class C>
+struct Slot {
+  int tile, col;            // in the scan's order; tile < 0: no more
+  int b0;                   // the first segment that starts at the tile's first row or later
+  int needs, from;          // the tile goes on with a segment that began in tile `from`
+  uint32_t bits[C::kWords]; // bit i: a segment starts at (or the stream ends before) the tile's row i, i <= kRows
+};
+
+// What the warps of a block share; channel = lane * V + i of the tile's columns.
 template <class C>
 struct TileSmem {
   alignas(16) float2 run[kRings][C::W][C::kWidth];  // the runs' maps
   alignas(16) float2 part[C::W][C::kWidth];         // the folds of the tiles before
   alignas(16) float carry[C::kWidth];               // the state after the group before
-  int reset[kRings][C::W];              // the run replaces the state
-  int number[2];
-  int give_up;
+  uint64_t full[C::S], empty[C::S];
+  int reset[kRings][C::W];                          // the run replaces the state
+  Slot<C> slot[C::S];
+  int stop_first, stop_enter;                       // a wait gave up, before a step's first or second barrier
+  alignas(8) int pad;
+  int abort_flag;                                   // (followed by its wait limit)
+  uint64_t wait_limit;
 };
 
 // A tile as a warp sees it: its run's rows and the segments in them.
 struct Run {
-  int tile, col;      // in the scan's order; tile < 0: none
-  int row, n, ch;     // first row, rows, first channel of the lane
-  int b0;             // the first segment that starts at `row` or later
+  int tile, col;
+  int row, n, ch;   // first row, rows, first channel of the lane
+  int b0;           // the first segment that starts at `row` or later
   uint32_t starts, ends;
-  bool needs, on;     // the tile goes on with a segment that began in tile `from`
+  bool needs, on;
   int from;
 };
 
 template <class C>
-__device__ __forceinline__ Run locate(const ScanParams& p, int number, bool back) {
+__device__ __forceinline__ Run run_of(const ScanParams& p, const Slot<C>& s, bool back) {
   Run t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  t.tile = -1;
-  if (number >= p.tiles * p.cols) return t;
-  t.tile = number / p.cols;
-  t.col = number - t.tile * p.cols;
-  const int row0 = (back ? p.tiles - 1 - t.tile : t.tile) * C::kRows;
-  t.row = row0 + (back ? C::W - 1 - warp : warp) * C::R;
+  t.tile = s.tile;
+  t.col = s.col;
+  t.needs = s.needs != 0;
+  t.from = s.from;
+  const int at = (back ? C::W - 1 - warp : warp) * C::R;  // the run's rows in the tile
+  t.row = (back ? p.tiles - 1 - t.tile : t.tile) * C::kRows + at;
   t.n = min(C::R, max(0, p.T - t.row));
   t.ch = (t.col * 32 + lane) * C::V;
   t.on = t.ch < p.D;
+  static_assert(32 % C::R == 0 && C::R < 32, "a run's rows lie in one word");
+  const uint32_t word = s.bits[at >> 5] >> (at & 31);
+  const uint32_t next = ((at + C::R) & 31) ? s.bits[at >> 5] >> ((at & 31) + C::R) : s.bits[(at + C::R) >> 5];
+  t.starts = word & bits_below(t.n);                                     // (the stream's end is none)
+  t.ends = ((word >> 1) | (next & 1u) << (C::R - 1)) & bits_below(t.n);  // a segment starts behind the row
+  t.b0 = s.b0;
+  for (int w = 0; w <= at >> 5; ++w) t.b0 += __popc(s.bits[w] & (w < at >> 5 ? ~0u : bits_below(at & 31)));
   return t;
-}
-
-// Where a tile's segments are looked up: the first segment that starts at a run's first row or later (b0), and at the
-// row where the scan enters the tile, from the back behind it (f); then boundaries around them.
-struct Hint {
-  int b0, f;
-};
-struct Edges {
-  int at, cf, before;  // cu[b0 + lane], cu[f], cu[f - 1]
-};
-template <class C>
-__device__ __forceinline__ Hint hint_of(const ScanParams& p, const Run& t, bool back) {
-  Hint h{0, 0};
-  if (t.tile < 0) return h;
-  const int rt = back ? p.tiles - 1 - t.tile : t.tile, warp = threadIdx.x >> 5;
-  h.b0 = p.first[rt * C::W + (back ? C::W - 1 - warp : warp)];
-  h.f = p.first[(rt + (back ? 1 : 0)) * C::W];
-  return h;
-}
-__device__ __forceinline__ Edges edges_of(const ScanParams& p, const Hint& h) {
-  const int lane = threadIdx.x & 31;
-  return Edges{p.cu[min(h.b0 + lane, p.B)], p.cu[h.f], p.cu[max(h.f - 1, 0)]};
-}
-
-// The segments of a run.
-template <class C>
-__device__ __forceinline__ void boundaries(const ScanParams& p, Run& t, const Hint& h, const Edges& e, bool back) {
-  static_assert(C::R < 32, "a run's boundaries are looked at by one warp");
-  const int lane = threadIdx.x & 31, d = h.b0 + lane <= p.B ? e.at - t.row : -1;
-  t.b0 = h.b0;
-  t.starts = __reduce_or_sync(0xffffffffu, d >= 0 && d < t.n ? 1u << d : 0u);  // (cu[B] = T is none: d = n)
-  t.ends = __reduce_or_sync(0xffffffffu, d >= 1 && d <= t.n ? 1u << (d - 1) : 0u);
-  const int enter = back ? (p.tiles - t.tile) * C::kRows : t.tile * C::kRows;  // backward: the row behind the tile
-  t.needs = enter < p.T && e.cf != enter;
-  t.from = !t.needs ? t.tile : back ? p.tiles - 1 - (e.cf - 1) / C::kRows : e.before / C::kRows;
 }
 
 // Row r's segment.
@@ -201,6 +179,11 @@ __device__ __forceinline__ void state_row(const float* s, int64_t at, bool on, f
 template <class C>
 __device__ __forceinline__ bool last_of_group(const ScanParams& p, const Run& t) {
   return t.tile % kGroup == kGroup - 1 && t.tile + 1 < p.tiles;
+}
+
+template <class C>
+__device__ __forceinline__ void worker_sync() {  // the warps that compute
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * C::W) : "memory");
 }
 
 // Warp 0, behind the barrier of the runs' maps: publishes the tile's map, and the state after a group's last tile
@@ -251,7 +234,7 @@ __device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int 
     bool ok = true;
     for (int k = t0; k < t1; ++k) {
       float m[2 * V];
-      ok &= await<2 * V>(p.agg + 2 * (k * wide + t.ch), true, m, p.status);
+      ok &= await<2 * V>(p.agg + 2 * (k * wide + t.ch), true, m, p.hdr);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         B[i] = fmaf(m[2 * i], B[i], m[2 * i + 1]);
@@ -262,13 +245,13 @@ __device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int 
     for (int i = 0; i < V; ++i) sh.part[warp][lane * V + i] = make_float2(A[i], B[i]);
     if (warp == W - 1) {
       float c[V] = {};
-      ok &= await<V>(p.carry + (group - 1) * wide + t.ch, t.from < g0, c, p.status);
+      ok &= await<V>(p.carry + (group - 1) * wide + t.ch, t.from < g0, c, p.hdr);
 #pragma unroll
       for (int i = 0; i < V; ++i) sh.carry[lane * V + i] = c[i];
     }
-    if (!ok) sh.give_up = 1;
-    __syncthreads();
-    if (sh.give_up) return false;
+    if (!ok) sh.stop_enter = 1;
+    worker_sync<C>();
+    if (sh.stop_enter) return false;
 #pragma unroll
     for (int i = 0; i < V; ++i) in[i] = sh.carry[lane * V + i];
     for (int w = 0; w * per < n; ++w)
@@ -302,52 +285,104 @@ __device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int 
   return true;
 }
 
-// A block's tiles: takes their numbers from the counter, keeps S of them on their way, and forms a tile's maps before it
-// finishes the tile before, so that whoever waits for them waits little.  One copy of each part of the work: unrolled over
-// the stages the code did not stay in the instruction cache (forward of T = 8192, D = 4096 bf16 211 us).
-//   fetch(run, stage)          asks for the run's data        first(run, stage, A, B) -> the run's map, true: it replaces the state
-//   second(run, stage, in)     the outputs
-template <class C, bool BACK, class Fetch, class First, class Second>
-__device__ __forceinline__ void run_tiles(const ScanParams& p, TileSmem<C>& sh, Fetch&& fetch, First&& first,
-                                          Second&& second) {
+// Tiles for each block (with a single one, or one and a few over, a block finishes it before it takes another).
+__device__ __forceinline__ int tiles_each(const ScanParams& p) {
+  return max(1, p.tiles * p.cols / static_cast<int>(gridDim.x));
+}
+
+// The copying warp: takes the tiles' numbers, looks their segments up, asks for their data.
+//   load(tile, col, stage): one lane's, issues the copies that complete on full[stage] (kBytes in all)
+template <class C, bool BACK, int kBytes, class Load>
+__device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&& load) {
+  using namespace sm100;
+  constexpr int S = C::S;
+  const int lane = threadIdx.x & 31, total = p.tiles * p.cols;
+  const int most = min(S, tiles_each(p));  // a block's tiles at a time
+  volatile int* abort_flag = &sh.abort_flag;
+  int issued = 0;
+  bool ok = true;
+  for (int j = 0;; ++j) {
+    const int s = j % S;
+    if (j >= most)
+      ok = wwait(smem_u32(&sh.empty[(j - most) % S]), ((j - most) / S) & 1, abort_flag, p.hdr, 71);
+    if (!ok) break;
+    int number = 0;
+    if (lane == 0) number = atomicAdd(p.ticket, 1);
+    number = __shfl_sync(0xffffffffu, number, 0);
+    Slot<C>& slot = sh.slot[s];
+    if (number >= total) {
+      if (lane == 0) {
+        slot.tile = -1;
+        mbar_arrive(smem_u32(&sh.full[s]));
+        mbar_arrive(smem_u32(&sh.full[s]));
+      }
+      return;
+    }
+    const int tile = number / p.cols, col = number - tile * p.cols;
+    const int rt = BACK ? p.tiles - 1 - tile : tile, row0 = rt * C::kRows;
+    if (lane == 0) {
+      if constexpr (kBytes > 0) {
+        mbar_expect_tx(smem_u32(&sh.full[s]), kBytes);
+        load(row0, col * C::kWidth, s);
+      } else {
+        mbar_arrive(smem_u32(&sh.full[s]));
+      }
+    }
+    issued = j + 1;
+    // the segments: where the scan enters the tile (backward: behind it), and the starts in it
+    const int b0 = p.first[rt], f = BACK ? p.first[rt + 1] : b0, enter = BACK ? row0 + C::kRows : row0;
+    const int cf = p.cu[f], before = p.cu[max(f - 1, 0)];
+    if (lane < C::kWords) slot.bits[lane] = 0;
+    __syncwarp();
+    for (int b = b0; b <= p.B; b += 32) {
+      const int d = b + lane <= p.B ? p.cu[b + lane] - row0 : C::kRows + 1;
+      if (d <= C::kRows) atomicOr(&slot.bits[d >> 5], 1u << (d & 31));
+      if (__any_sync(0xffffffffu, d > C::kRows)) break;
+    }
+    if (lane == 0) {
+      const bool needs = enter < p.T && cf != enter;
+      slot.tile = tile;
+      slot.col = col;
+      slot.b0 = b0;
+      slot.needs = needs;
+      slot.from = !needs ? tile : BACK ? p.tiles - 1 - (cf - 1) / C::kRows : before / C::kRows;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+  }
+  // given up: the copies on their way land before the block ends (bounded again)
+  if constexpr (kBytes > 0) {
+    const uint64_t t0 = globaltimer();
+    for (int j = max(0, issued - S); j < issued; ++j)
+      while (!mbar_try_wait(smem_u32(&sh.full[j % S]), (j / S) & 1) && globaltimer() - t0 < 50000000ull) {
+      }
+  }
+}
+
+// The other warps: form a tile's maps before they finish the tile before, so that whoever waits for them waits little.
+//   first(run, stage, A, B)    the run's map, true: it replaces the state        second(run, stage, in)   the outputs
+// (One copy of each part of the work: unrolled over the stages the code left the instruction cache; the forward of
+// T = 8192, D = 4096 in bf16 took 211 us.)
+template <class C, bool BACK, class First, class Second>
+__device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First&& first, Second&& second) {
+  using namespace sm100;
   constexpr int V = C::V, S = C::S;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int total = p.tiles * p.cols;
-  // numbers: a block takes more than one at once only where there are several for each
-  const int ahead = min(S - 1, max(1, total / static_cast<int>(gridDim.x)));
-  if (threadIdx.x == 0) {
-    sh.give_up = 0;
-    sh.number[1] = atomicAdd(p.ticket, ahead);  // (step 0 writes the other)
-  }
-  __syncthreads();
-  const int base = sh.number[1];  // (written again behind the first step's barrier)
-  int ask[S - 1];   // the numbers of this step's tile and those after it; total: none
-  Hint hint[S - 1];
-#pragma unroll
-  for (int k = 0; k < S - 1; ++k) {
-    ask[k] = k < ahead ? min(base + k, total) : total;
-    const Run t = locate<C>(p, ask[k], BACK);
-    if (t.tile >= 0) fetch(t, k);
-    hint[k] = hint_of<C>(p, t, BACK);
-    copy_commit();
-  }
-  Edges edges = edges_of(p, hint[0]);
+  volatile int* abort_flag = &sh.abort_flag;
   Run old;
   old.tile = -1;
-  int stage = 0, ring = 0;
-  // step i: data for tile i + S - 1, maps of tile i, outputs of tile i - 1
+  int stage = 0, parity = 0, ring = 0, held = 0;
+  const bool single = tiles_each(p) == 1;
 #pragma unroll 1
-  for (int i = 0;; ++i) {
-    bool any = old.tile >= 0;
-#pragma unroll
-    for (int k = 0; k < S - 1; ++k) any |= ask[k] < total;
-    if (!any) return;
-    int number = 0;
-    if (warp == C::W - 1 && lane == 0) number = atomicAdd(p.ticket, 1);
-    Run now = locate<C>(p, ask[0], BACK);
-    if (now.tile >= 0) boundaries<C>(p, now, hint[0], edges, BACK);
-    edges = edges_of(p, hint[1]);  // the next tile's
-    copy_wait<S - 2>();
+  for (;;) {
+    const bool ok = wwait(smem_u32(&sh.full[stage]), parity, abort_flag, p.hdr, 72);
+    Run now;
+    now.tile = -1;
+    if (ok) {
+      if (sh.slot[stage].tile >= 0) now = run_of<C>(p, sh.slot[stage], BACK);
+    } else {
+      sh.stop_first = 1;
+    }
     if (now.tile >= 0) {
       float A[V], B[V];
       const bool reset = first(now, stage, A, B);
@@ -355,39 +390,102 @@ __device__ __forceinline__ void run_tiles(const ScanParams& p, TileSmem<C>& sh, 
       for (int k = 0; k < V; ++k) sh.run[ring][warp][lane * V + k] = make_float2(reset ? 0.f : A[k], B[k]);
       if (lane == 0) sh.reset[ring][warp] = reset;
     }
-    if (warp == C::W - 1 && lane == 0) sh.number[i & 1] = number;
-    __syncthreads();
-    const int next = sh.number[i & 1];
+    worker_sync<C>();
+    if (sh.stop_first) break;
     if (warp == 0) publish<C>(p, sh, ring, now);
-    const int free = stage == 0 ? S - 1 : stage - 1;  // the stage of the tile before, this one's turn comes last
+    if (single) {
+      old = now;
+      held = stage;
+    }
     if (old.tile >= 0) {
       float in[V];
-      if (!enter<C>(p, sh, ring == 0 ? kRings - 1 : ring - 1, old, in)) return;
-      second(old, free, in);
+      if (!enter<C>(p, sh, single ? ring : ring == 0 ? kRings - 1 : ring - 1, old, in)) break;
+      second(old, held, in);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[held]));
     }
-#pragma unroll
-    for (int k = 0; k + 1 < S - 1; ++k) ask[k] = ask[k + 1], hint[k] = hint[k + 1];
-    ask[S - 2] = min(next, total);
-    const Run t = locate<C>(p, ask[S - 2], BACK);
-    if (t.tile >= 0) fetch(t, free);
-    hint[S - 2] = hint_of<C>(p, t, BACK);
-    copy_commit();
+    if (now.tile < 0) return;
     old = now;
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (single) old.tile = -1;
+    held = stage;
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
     ring = ring + 1 == kRings ? 0 : ring + 1;
   }
+  sh.abort_flag = 1;  // given up: the copying warp stops too
 }
+
+// Runs a block's warps.
+template <class C, bool BACK, int kBytes, class Load, class First, class Second>
+__device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, Load&& load, First&& first,
+                                          Second&& second) {
+  using namespace sm100;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(smem_u32(&sh.full[s]), 2);  // the data's bytes, the slot
+      mbar_init(smem_u32(&sh.empty[s]), C::W);
+    }
+    fence_barrier_init();
+    sh.stop_first = sh.stop_enter = sh.abort_flag = 0;
+    sh.wait_limit = kTimeoutNs;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32 * C::W) feed<C, BACK, kBytes>(p, sh, load);
+  else work<C, BACK>(p, sh, first, second);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Where a run's rows are read: its tile's copy, or memory.
+template <class T, class C, bool TMA>
+struct Rows {
+  const T* base;       // the thread's first element of stage 0, or of the tensor
+  int64_t step;        // between rows
+  __device__ __forceinline__ Rows(const uint8_t* smem, const void* global, int64_t rs) {
+    const int lane = threadIdx.x & 31;
+    base = TMA ? reinterpret_cast<const T*>(smem) + lane * C::V : static_cast<const T*>(global);
+    step = TMA ? C::kWidth : rs;
+  }
+  // the run's first row
+  __device__ __forceinline__ const T* at(const Run& t, int stage, bool back) const {
+    const int warp = threadIdx.x >> 5;
+    if (TMA) return base + (stage * C::kRows + (back ? C::W - 1 - warp : warp) * C::R) * C::kWidth;
+    return base + t.row * step + t.ch;
+  }
+  __device__ __forceinline__ Pack<T, C::V> get(const T* first, int r, const Run& t) const {
+    if (TMA) return load_pack<T, C::V>(first + r * C::kWidth);
+    Pack<T, C::V> none;
+#pragma unroll
+    for (int i = 0; i < C::V; ++i) none.set(i, 0.f);
+    return t.on ? load_pack<T, C::V>(first + r * step) : none;
+  }
+};
+
+// Bytes of a tile of one tensor.
+template <class T, class C> constexpr int tile_bytes() { return C::kRows * C::kWidth * static_cast<int>(sizeof(T)); }
+template <class C> constexpr int head_bytes() { return (static_cast<int>(sizeof(TileSmem<C>)) + 127) / 128 * 128; }
+
+struct Maps {
+  CUtensorMap a, b, c;  // forward: x, g; backward: dh, g, h
+};
 
 }  // namespace
 
-// Checks the boundary contract (block 0), empties the published places and looks up the first segment at every run.
+// Checks the boundary contract (block 0), empties the published places and looks up the first segment at every tile.
 __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParams p, int rows, int64_t words) {
   griddep_begin();
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPrepThreads;
   for (int64_t i = tid; i < words / 4; i += step)
     reinterpret_cast<uint4*>(p.agg)[i] = make_uint4(kNone, kNone, kNone, kNone);
-  for (int64_t i = tid; i < p.runs; i += step) {  // the first b in [0, B] with cu[b] >= row (cu[B] = T)
+  for (int64_t i = tid; i <= p.tiles; i += step) {  // the first b in [0, B] with cu[b] >= row (cu[B] = T)
     const int row = static_cast<int>(min(i * rows, static_cast<int64_t>(p.T)));
     int lo = 0, hi = p.B;
     while (lo < hi) {
@@ -405,45 +503,43 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
     *p.ticket = 0;
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *p.status = bad ? VA_ERR_BAD_SEQLENS : VA_OK;
+  if (threadIdx.x == 0) p.hdr->status = bad ? VA_ERR_BAD_SEQLENS : VA_OK;
 }
 
-template <class TX, class TG, class TH, class C>
-__global__ void __launch_bounds__(C::kThreads, C::kMost) scan_fwd_kernel(const ScanParams p) {
+template <class TX, class TG, class TH, class C, bool TMA>
+__global__ void __launch_bounds__(C::kThreads, C::M)
+    scan_fwd_kernel(const ScanParams p, const __grid_constant__ Maps maps) {
   griddep_begin();
   constexpr int V = C::V, R = C::R;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   TileSmem<C>& sh = *reinterpret_cast<TileSmem<C>*>(smem);
-  if (*reinterpret_cast<volatile int32_t*>(p.status) == VA_ERR_BAD_SEQLENS) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // a thread's own pieces of the stages: [stage][warp][row][lane]
-  Pack<TX, V>* xs = reinterpret_cast<Pack<TX, V>*>(smem + sizeof(TileSmem<C>)) + warp * R * 32 + lane;
-  Pack<TG, V>* gs = reinterpret_cast<Pack<TG, V>*>(smem + sizeof(TileSmem<C>) + sizeof(Pack<TX, V>) * 32 * C::kRows * C::S) +
-                    warp * R * 32 + lane;
-  constexpr int kStage = 32 * C::kRows;
-  const auto fetch = [&](const Run& t, int stage) {
-    if (!t.on) return;
-    const TX* x = static_cast<const TX*>(p.x) + t.row * p.x_rs + t.ch;
-    const TG* g = static_cast<const TG*>(p.g) + t.row * p.g_rs + t.ch;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < t.n) {
-        copy_piece<sizeof(TX) * V>(xs + stage * kStage + r * 32, x + r * p.x_rs);
-        copy_piece<sizeof(TG) * V>(gs + stage * kStage + r * 32, g + r * p.g_rs);
-      }
+  if (*reinterpret_cast<volatile int32_t*>(&p.hdr->status) == VA_ERR_BAD_SEQLENS) return;
+  constexpr int kX = tile_bytes<TX, C>(), kG = tile_bytes<TG, C>();
+  uint8_t* const x_smem = smem + head_bytes<C>();
+  uint8_t* const g_smem = x_smem + kX * C::S;
+  const Rows<TX, C, TMA> xs(x_smem, p.x, p.x_rs);
+  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs);
+  const auto load = [&](int row0, int ch0, int stage) {
+    const uint32_t bar = smem_u32(&sh.full[stage]);
+    tma_load_2d(smem_u32(x_smem + stage * kX), &maps.a, bar, ch0, row0);
+    tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
   };
-  const auto step = [&](int at, float (&h)[V], float (&A)[V]) {
-    const Pack<TX, V> x = xs[at];
-    const Pack<TG, V> g = gs[at];
+  struct At {
+    const TX* x;
+    const TG* g;
+  };
+  const auto step = [&](const At& a, const Run& t, int r, float (&h)[V], float (&A)[V]) {
+    const Pack<TX, V> x = xs.get(a.x, r, t);
+    const Pack<TG, V> g = gs.get(a.g, r, t);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       A[i] += g[i];
       h[i] = fmaf(decay(g[i]), h[i], x[i]);
     }
   };
-  const auto start = [&](const Run& t, int r, int at, float (&h)[V]) {  // a segment's first row
-    const Pack<TX, V> x = xs[at];
-    const Pack<TG, V> g = gs[at];
+  const auto start = [&](const At& a, const Run& t, int r, float (&h)[V]) {  // a segment's first row
+    const Pack<TX, V> x = xs.get(a.x, r, t);
+    const Pack<TG, V> g = gs.get(a.g, r, t);
     state_row<V>(p.h0, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on, h);
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = p.h0 ? fmaf(decay(g[i]), h[i], x[i]) : x[i];  // (x itself, whatever its decay is)
@@ -451,15 +547,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_fwd_kernel(const S
   const auto first = [&](const Run& t, int stage, float (&A)[V], float (&B)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = B[i] = 0.f;
-    const int at = stage * kStage;
+    const At a{xs.at(t, stage, false), gs.at(t, stage, false)};
     if (t.starts == 0 && t.n == R) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) step(at + r * 32, B, A);
+      for (int r = 0; r < R; ++r) step(a, t, r, B, A);
     } else {
 #pragma unroll 1
       for (int r = 0; r < t.n; ++r) {
-        if ((t.starts >> r) & 1u) start(t, r, at + r * 32, B);
-        else step(at + r * 32, B, A);
+        if ((t.starts >> r) & 1u) start(a, t, r, B);
+        else step(a, t, r, B, A);
       }
     }
 #pragma unroll
@@ -468,7 +564,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_fwd_kernel(const S
   };
   const auto second = [&](const Run& t, int stage, float (&h)[V]) {
     TH* out = static_cast<TH*>(p.out) + t.row * p.out_rs + t.ch;
-    const int at = stage * kStage;
+    const At a{xs.at(t, stage, false), gs.at(t, stage, false)};
     float unused[V] = {};
     const auto put = [&](int r) {
       Pack<TH, V> o;
@@ -479,14 +575,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_fwd_kernel(const S
     if (t.starts == 0 && t.n == R && (!p.last || t.ends == 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        step(at + r * 32, h, unused);
+        step(a, t, r, h, unused);
         put(r);
       }
     } else {
 #pragma unroll 1
       for (int r = 0; r < t.n; ++r) {
-        if ((t.starts >> r) & 1u) start(t, r, at + r * 32, h);
-        else step(at + r * 32, h, unused);
+        if ((t.starts >> r) & 1u) start(a, t, r, h);
+        else step(a, t, r, h, unused);
         put(r);
         if (p.last && t.on && ((t.ends >> r) & 1u)) {
           float* last = p.last + static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch;
@@ -496,47 +592,42 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_fwd_kernel(const S
       }
     }
   };
-  run_tiles<C, false>(p, sh, fetch, first, second);
+  run_block<C, false, TMA ? kX + kG : 0>(p, sh, load, first, second);
 }
 
 // TX: dx, TG: g and dg, TH: dh and h.  Tile 0 holds the last rows, warp 0 a tile's last run.
-template <class TX, class TG, class TH, class C>
-__global__ void __launch_bounds__(C::kThreads, C::kMost) scan_bwd_kernel(const ScanParams p) {
+template <class TX, class TG, class TH, class C, bool TMA>
+__global__ void __launch_bounds__(C::kThreads, C::M)
+    scan_bwd_kernel(const ScanParams p, const __grid_constant__ Maps maps) {
   griddep_begin();
   constexpr int V = C::V, R = C::R;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   TileSmem<C>& sh = *reinterpret_cast<TileSmem<C>*>(smem);
-  if (*reinterpret_cast<volatile int32_t*>(p.status) == VA_ERR_BAD_SEQLENS) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kStage = 32 * C::kRows;
-  Pack<TH, V>* ds = reinterpret_cast<Pack<TH, V>*>(smem + sizeof(TileSmem<C>)) + warp * R * 32 + lane;
-  Pack<TH, V>* hs = ds + kStage * C::S;
-  Pack<TG, V>* gs = reinterpret_cast<Pack<TG, V>*>(smem + sizeof(TileSmem<C>) + 2 * sizeof(Pack<TH, V>) * kStage * C::S) +
-                    warp * R * 32 + lane;
-  const auto fetch = [&](const Run& t, int stage) {
-    if (!t.on) return;
-    const TH* dh = static_cast<const TH*>(p.x) + t.row * p.x_rs + t.ch;
-    const TH* h = static_cast<const TH*>(p.h) + t.row * p.h_rs + t.ch;
-    const TG* g = static_cast<const TG*>(p.g) + t.row * p.g_rs + t.ch;
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-      if (r < t.n) {
-        copy_piece<sizeof(TH) * V>(ds + stage * kStage + r * 32, dh + r * p.x_rs);
-        copy_piece<sizeof(TG) * V>(gs + stage * kStage + r * 32, g + r * p.g_rs);
-        if (t.row + r > 0) copy_piece<sizeof(TH) * V>(hs + stage * kStage + r * 32, h + (r - 1) * p.h_rs);  // the row before
-      }
+  if (*reinterpret_cast<volatile int32_t*>(&p.hdr->status) == VA_ERR_BAD_SEQLENS) return;
+  constexpr int kH = tile_bytes<TH, C>(), kG = tile_bytes<TG, C>();
+  uint8_t* const d_smem = smem + head_bytes<C>();
+  uint8_t* const g_smem = d_smem + kH * C::S;
+  uint8_t* const h_smem = g_smem + kG * C::S;
+  const Rows<TH, C, TMA> ds(d_smem, p.x, p.x_rs), hs(h_smem, p.h, p.h_rs);
+  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs);
+  const auto load = [&](int row0, int ch0, int stage) {
+    const uint32_t bar = smem_u32(&sh.full[stage]);
+    tma_load_2d(smem_u32(d_smem + stage * kH), &maps.a, bar, ch0, row0);
+    tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
+    tma_load_2d(smem_u32(h_smem + stage * kH), &maps.c, bar, ch0, row0 - 1);  // the rows before (zeros before the first)
   };
   const auto first = [&](const Run& t, int stage, float (&A)[V], float (&B)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = B[i] = 0.f;
-    const int at = stage * kStage;
+    const TH* const d_at = ds.at(t, stage, true);
+    const TG* const g_at = gs.at(t, stage, true);
     const auto step = [&](int r) {
-      const Pack<TH, V> d = ds[at + r * 32];
-      const Pack<TG, V> g = gs[at + r * 32];
+      const Pack<TH, V> d = ds.get(d_at, r, t);
+      const Pack<TG, V> g = gs.get(g_at, r, t);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         A[i] += g[i];
-        B[i] = decay(g[i]) * (d[i] + B[i]);
+        B[i] = back_step(g[i], d[i] + B[i]);
       }
     };
     if (t.ends == 0 && t.n == R) {
@@ -556,17 +647,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_bwd_kernel(const S
   const auto second = [&](const Run& t, int stage, float (&f)[V]) {
     TX* dx = static_cast<TX*>(p.out) + t.row * p.out_rs + t.ch;
     TG* dg = static_cast<TG*>(p.dg) + t.row * p.dg_rs + t.ch;
-    const int at = stage * kStage;
+    const TH* const d_at = ds.at(t, stage, true);
+    const TG* const g_at = gs.at(t, stage, true);
+    const TH* const h_at = hs.at(t, stage, true) - (TMA ? 0 : p.h_rs);
     // before: the row before's h, at a segment's first row h0 (none: 0, and so is the decay's gradient)
     const auto step = [&](int r, const float (&before)[V], bool none) {
-      const Pack<TH, V> d = ds[at + r * 32];
-      const Pack<TG, V> g = gs[at + r * 32];
+      const Pack<TH, V> d = ds.get(d_at, r, t);
+      const Pack<TG, V> g = gs.get(g_at, r, t);
       Pack<TX, V> ox;
       Pack<TG, V> og;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float e = d[i] + f[i];
-        f[i] = decay(g[i]) * e;
+        f[i] = back_step(g[i], e);
         ox.set(i, e);
         og.set(i, none ? 0.f : f[i] * before[i]);
       }
@@ -576,7 +669,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_bwd_kernel(const S
       }
     };
     const auto stored = [&](int r, float (&before)[V]) {
-      const Pack<TH, V> h = hs[at + r * 32];
+      const Pack<TH, V> h = hs.get(h_at, r, t);
 #pragma unroll
       for (int i = 0; i < V; ++i) before[i] = h[i];
     };
@@ -603,7 +696,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMost) scan_bwd_kernel(const S
       }
     }
   };
-  run_tiles<C, true>(p, sh, fetch, first, second);
+  run_block<C, true, TMA ? 2 * kH + kG : 0>(p, sh, load, first, second);
 }
 
 // Single tokens: h = exp(g) h0 + x, one element vector a thread.  Block (0, 0) checks the boundaries for the
@@ -637,7 +730,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
   int bad = 0;
   for (int b = threadIdx.x; b <= p.B; b += 256) bad |= p.cu[b] != b;
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *p.status = bad ? VA_ERR_BAD_SEQLENS : VA_OK;
+  if (threadIdx.x == 0) p.hdr->status = bad ? VA_ERR_BAD_SEQLENS : VA_OK;
 }
 
 // ---------------------------------------------------------------- host side
@@ -647,18 +740,17 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
-  int64_t tiles, cols, groups, runs, words;
+  int64_t tiles, cols, groups, words;
   size_t first, agg, carry, total;
 };
 
-Layout layout_of(int T, int D, int rows, int runs, int width) {
+Layout layout_of(int T, int D, int rows, int width) {
   Layout l;
   l.tiles = (static_cast<int64_t>(T) + rows - 1) / rows;
   l.cols = (static_cast<int64_t>(D) + width - 1) / width;
   l.groups = (l.tiles + kGroup - 1) / kGroup;
-  l.runs = (l.tiles + 1) * runs;
   l.first = sizeof(WsHeader);
-  l.agg = align256(l.first + l.runs * sizeof(int32_t));
+  l.agg = align256(l.first + (l.tiles + 1) * sizeof(int32_t));
   l.carry = l.agg + l.tiles * l.cols * width * 2 * sizeof(float);  // (follows: both are emptied together)
   l.words = (l.tiles * 2 + l.groups) * l.cols * width;
   l.total = align256(l.agg + l.words * sizeof(float));
@@ -674,14 +766,13 @@ bool steps_of(const void* p, int64_t rs, int N) {
 void place(ScanParams& p, const Layout& l, void* ws) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   WsHeader* h = reinterpret_cast<WsHeader*>(w);
-  p.status = &h->status;
+  p.hdr = h;
   p.ticket = &h->counter[0];
   p.first = reinterpret_cast<int32_t*>(w + l.first);
   p.agg = reinterpret_cast<float*>(w + l.agg);
   p.carry = reinterpret_cast<float*>(w + l.carry);
   p.tiles = static_cast<int>(l.tiles);
   p.cols = static_cast<int>(l.cols);
-  p.runs = l.runs;
 }
 
 using bf16 = __nv_bfloat16;
@@ -693,69 +784,73 @@ int device_sms() {
   return std::max(sms, 1);
 }
 
-// The call's blocks, as many as fit, each with S tiles in shared memory.
+template <class T>
+bool rows16(const void* p, int64_t rs) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && rs * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+}
+
+// The call's blocks, as many as fit, each with S tiles of `piece` bytes in shared memory.
 template <class C>
-cudaError_t run_blocks(int stage, void (*kernel)(ScanParams), size_t piece, ScanParams p, void* ws, cudaStream_t st) {
-  const Layout l = layout_of(p.T, p.D, C::kRows, C::W, C::kWidth);
+cudaError_t run_blocks(int stage, void (*kernel)(ScanParams, Maps), size_t piece, ScanParams p, const Maps& maps, void* ws,
+                       cudaStream_t st) {
+  const Layout l = layout_of(p.T, p.D, C::kRows, C::kWidth);
   place(p, l, ws);
   const int sms = device_sms();
   if (stage == 0) {
-    const int64_t work = std::max(l.words / 8, l.runs);
+    const int64_t work = std::max(l.words / 8, l.tiles + 1);
     const int blocks = static_cast<int>(std::min<int64_t>(2 * sms, (work + kPrepThreads - 1) / kPrepThreads));
-    return launch_pdl(scan_prep_kernel, dim3(blocks), dim3(kPrepThreads), 0, st, p, C::R, l.words);
+    return launch_pdl(scan_prep_kernel, dim3(blocks), dim3(kPrepThreads), 0, st, p, C::kRows, l.words);
   }
-  const size_t smem = sizeof(TileSmem<C>) + piece * 32 * C::kRows * C::S;
+  const size_t smem = head_bytes<C>() + piece * C::S;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t fit = std::max<int64_t>(1, std::min<int64_t>((227 * 1024) / (smem + 1024), C::kMost));
+  const int64_t fit = std::max<int64_t>(1, std::min<int64_t>((228 * 1024) / (smem + 1024), C::M));
   const int grid = static_cast<int>(std::min<int64_t>(l.tiles * l.cols, sms * fit));
-  return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), smem, st, p);
+  return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), smem, st, p, maps);
 }
 
-template <class TX, class TG, class TH, class C>
-cudaError_t blocks_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C>, (sizeof(TX) + sizeof(TG)) * C::V, p, ws, st);
-}
-template <class TX, class TG, class TH, class C>
-cudaError_t blocks_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C>, (2 * sizeof(TH) + sizeof(TG)) * C::V, p, ws, st);
-}
-
-constexpr bool kWide = false;
 template <int V> using FwdShape = Shape<V, 8, 16, 3, 2>;
 template <int V> using BwdShape = Shape<V, 8, 8, 3, 2>;
 
-// Channels a lane (8 bytes of the widest type where the rows allow it), runs of 16 or 8 rows.
+// Two channels a lane where rows lie on boundaries of two elements, else one; copied tiles where they lie on 16 bytes.
 template <class TX, class TG, class TH>
 cudaError_t run_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  const auto can = [&](int N) {
-    return p.D % N == 0 && steps_of<TX>(p.x, p.x_rs, N) && steps_of<TG>(p.g, p.g_rs, N) && steps_of<TH>(p.out, p.out_rs, N);
-  };
-  if constexpr (sizeof(TH) == 2) {
-    if (can(4) && kWide) return blocks_fwd<TX, TG, TH, FwdShape<4>>(stage, p, ws, st);
+  using C = FwdShape<2>;
+  const bool two =
+      p.D % 2 == 0 && steps_of<TX>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) && steps_of<TH>(p.out, p.out_rs, 2);
+  Maps maps{};
+  if (!two) return run_blocks<FwdShape<1>>(stage, scan_fwd_kernel<TX, TG, TH, FwdShape<1>, false>, 0, p, maps, ws, st);
+  if (rows16<TX>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs)) {
+    if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TX) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
+                        tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows)))
+      return cudaErrorInvalidValue;
+    return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C, true>, tile_bytes<TX, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return can(2) ? blocks_fwd<TX, TG, TH, FwdShape<2>>(stage, p, ws, st)
-                : blocks_fwd<TX, TG, TH, FwdShape<1>>(stage, p, ws, st);
+  return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
 cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  const auto can = [&](int N) {
-    return p.D % N == 0 && steps_of<TH>(p.x, p.x_rs, N) && steps_of<TG>(p.g, p.g_rs, N) && steps_of<TH>(p.h, p.h_rs, N) &&
-           steps_of<TX>(p.out, p.out_rs, N) && steps_of<TG>(p.dg, p.dg_rs, N);
-  };
-  if constexpr (sizeof(TH) == 2) {
-    if (can(4) && kWide) return blocks_bwd<TX, TG, TH, BwdShape<4>>(stage, p, ws, st);
+  using C = BwdShape<2>;
+  const bool two = p.D % 2 == 0 && steps_of<TH>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) &&
+                   steps_of<TH>(p.h, p.h_rs, 2) && steps_of<TX>(p.out, p.out_rs, 2) && steps_of<TG>(p.dg, p.dg_rs, 2);
+  Maps maps{};
+  if (!two) return run_blocks<BwdShape<1>>(stage, scan_bwd_kernel<TX, TG, TH, BwdShape<1>, false>, 0, p, maps, ws, st);
+  if (rows16<TH>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && rows16<TH>(p.h, p.h_rs)) {
+    if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TH) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
+                        tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows) &&
+                        tmap_matrix(&maps.c, p.h, sizeof(TH) == 2, p.T, p.D, p.h_rs, C::kWidth, C::kRows)))
+      return cudaErrorInvalidValue;
+    return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C, true>, 2 * tile_bytes<TH, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return can(2) ? blocks_bwd<TX, TG, TH, BwdShape<2>>(stage, p, ws, st)
-                : blocks_bwd<TX, TG, TH, BwdShape<1>>(stage, p, ws, st);
+  return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
 cudaError_t run_step(ScanParams p, void* ws, cudaStream_t st) {
   const bool two =
       p.D % 2 == 0 && steps_of<TX>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) && steps_of<TH>(p.out, p.out_rs, 2);
-  p.status = &static_cast<WsHeader*>(ws)->status;
+  p.hdr = static_cast<WsHeader*>(ws);
   const int V = two ? 2 : 1;
   const dim3 grid((p.T + 3) / 4, (p.D + 64 * V - 1) / (64 * V));
   return two ? launch_pdl(scan_step_kernel<TX, TG, TH, 2>, grid, dim3(256), 0, st, p)
@@ -764,11 +859,9 @@ cudaError_t run_step(ScanParams p, void* ws, cudaStream_t st) {
 
 }  // namespace
 
-size_t scan_workspace(int T, int D) {
-  size_t n = 0;
-  for (int rows : {16, 32, 64, 128})
-    for (int width : {32, 64, 128}) n = std::max(n, layout_of(T, D, rows, 16, width).total);
-  return n;
+size_t scan_workspace(int T, int D) {  // (narrow columns waste less than they need more of)
+  const auto most = [&](int rows) { return std::max(layout_of(T, D, rows, 32).total, layout_of(T, D, rows, 64).total); };
+  return std::max(most(FwdShape<2>::kRows), most(BwdShape<2>::kRows));
 }
 
 cudaError_t launch_scan_fwd(int stage, ScanParams p, int xb, int gb, void* ws, cudaStream_t st) {

@@ -20,10 +20,9 @@ struct ScanParams {
   float* last;         // forward: the last states; backward: h0's gradient; may be null
   int B, T, D;
   int tiles, cols;     // tiles of rows, columns of channels (set by the launcher)
-  int32_t* status;     // workspace header's status word
+  struct WsHeader* hdr;  // workspace header
   int32_t* ticket;
-  int64_t runs;        // runs of rows, and one tile's more
-  int32_t* first;      // [runs] the first segment that starts at a run's first row or later
+  int32_t* first;      // [tiles + 1] the first segment that starts at a tile's first row or later
   float* agg;          // [tiles][cols * width][2] a tile's map (decay product, state from zero)
   float* carry;        // [groups][cols * width] the state after a group of tiles
 };

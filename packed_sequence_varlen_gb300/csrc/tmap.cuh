@@ -39,4 +39,20 @@ inline bool tmap_rows(CUtensorMap* m, const void* ptr, int T, int H, int d, int6
   return r == CUDA_SUCCESS;
 }
 
+// 2-D map (D, T) of bf16 or fp32 rows with a (box_cols, box_rows) box, not swizzled: a box lies row by row.  Rows past T
+// and columns past D read as zero.
+inline bool tmap_matrix(CUtensorMap* m, const void* ptr, bool bf16, int64_t T, int64_t D, int64_t row_stride, int box_cols,
+                        int box_rows) {
+  auto fn = tmap_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride) * (bf16 ? 2 : 4)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(ptr),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace va

@@ -8,8 +8,8 @@
 // descending order).  A tile is W runs of R rows by 32 V channels, a run a warp:
 //   pass 1  the run's map from zero (A = exp(sum of g), B by the recurrence),
 //   the runs' maps are combined in the block; the tile's map is published,
-//   the state that enters the tile is folded from the maps of the tiles before it in its group of kGroup and
-//   the state after the group before that one, which that group's last tile publishes,
+//   the state that enters the tile is folded from the maps of a few tiles before it and a state further back, which
+//   every kGroup-th tile publishes,
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
 // So the data is read once and written once.  A warp of its own takes the tiles' numbers, looks their segments up and has
 // their data copied to shared memory (TMA), a few tiles ahead of the others.  (Rows that are not on 16-byte boundaries are
@@ -33,7 +33,10 @@ namespace va {
 
 namespace {
 
-constexpr int kGroup = 32;  // tiles that share a published state
+// The last tile of every kGroup publishes the state after it.  A tile folds the maps of the kBack groups before its own
+// and of those before it in its own, onto the state before them, which has long been there (its own group's of 32
+// tiles, whose start was formed beside it: T = 65536 in one segment, D = 2048 in bf16, backward 363 us; 352 this way).
+constexpr int kGroup = 8, kBack = 2;
 constexpr int kPrepThreads = 1024;
 // Buffers of run maps: a slow warp may still read those of the tile before while a fast one, past a single barrier,
 // writes those of the tile after.
@@ -47,9 +50,77 @@ struct Shape {
   static constexpr int kThreads = 32 * (W_ + 1), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
 };
 
-__device__ __forceinline__ float decay(float g) { return fast_exp2(g * kLog2e); }
-// f of a row from its e, rounded by itself: not folded into the next sum here and there.
-__device__ __forceinline__ float back_step(float g, float e) { return __fmul_rn(decay(g), e); }
+// V numbers at a time, two an instruction; each result is rounded by itself, whatever the code around it.
+template <int V> struct Vec {
+  float e[V];
+  __device__ __forceinline__ float& operator[](int i) { return e[i]; }
+  __device__ __forceinline__ const float& operator[](int i) const { return e[i]; }
+};
+template <int V>
+__device__ __forceinline__ Vec<V> fill(float x) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = x;
+  return r;
+}
+template <class T, int V>
+__device__ __forceinline__ Vec<V> wide_of(const Pack<T, V>& p) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = p[i];
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> add(const Vec<V>& a, const Vec<V>& b) {
+  Vec<V> r;
+  if constexpr (V == 1) {
+    r[0] = __fadd_rn(a[0], b[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
+          " add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"  // (.rn: never folded into a product)
+          : "=f"(r[i]), "=f"(r[i + 1])
+          : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> fma(const Vec<V>& a, const Vec<V>& b, const Vec<V>& c) {
+  Vec<V> r;
+  if constexpr (V == 1) {
+    r[0] = fmaf(a[0], b[0], c[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) ffma2(r[i], r[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
+  }
+  return r;
+}
+// (a product as a fused one with -0 added, so that it is not fused with the sum that follows in one place and not in
+// another: the results are the same bits on every path)
+template <int V>
+__device__ __forceinline__ Vec<V> mul(const Vec<V>& a, const Vec<V>& b) {
+  return fma(a, b, fill<V>(-0.f));
+}
+template <int V>
+__device__ __forceinline__ Vec<V> decay(const Vec<V>& g) {
+  Vec<V> r = mul(g, fill<V>(kLog2e));
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = fast_exp2(r[i]);
+  return r;
+}
+__device__ __forceinline__ float decay(float g) { return fast_exp2(__fmul_rn(g, kLog2e)); }
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> narrow(const Vec<V>& v) {
+  Pack<T, V> r;
+  if constexpr (sizeof(T) == 2 && V == 2) {
+    *reinterpret_cast<uint32_t*>(&r) = pack_bf16(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.set(i, v[i]);
+  }
+  return r;
+}
 // A run's decay, rounded once.
 __device__ __forceinline__ float run_decay(float sum) { return 1.f + expm1f(sum); }
 
@@ -171,9 +242,11 @@ __device__ __forceinline__ int segment_of(const Run& t, int r) { return t.b0 + _
 
 // A row of states for the lane's channels (zeros without them).
 template <int V>
-__device__ __forceinline__ void state_row(const float* s, int64_t at, bool on, float (&v)[V]) {
+__device__ __forceinline__ Vec<V> state_row(const float* s, int64_t at, bool on) {
+  Vec<V> v;
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = s && on ? s[at + i] : 0.f;
+  return v;
 }
 
 template <class C>
@@ -216,71 +289,105 @@ __device__ __forceinline__ void publish(const ScanParams& p, const TileSmem<C>& 
   if (reset && last_of_group<C>(p, t)) show<V>(p.carry + (t.tile / kGroup) * wide + t.ch, B);
 }
 
+// The maps that a warp folds for a tile, asked for before there is other work to do.
+template <class C>
+struct Look {
+  static constexpr int kMost = ((kBack + 1) * kGroup + C::W - 1) / C::W;
+  float m[kMost][2 * C::V], c[C::V];
+};
+// The tiles before `t` whose maps it folds: [lo, lo + n), `per` a warp; onto the state after group `state`, or onto
+// nothing (-1) where its segment began in one of them.
+struct Span {
+  int lo, n, per, t0, t1, state;
+};
+template <class C>
+__device__ __forceinline__ Span span_of(const Run& t) {
+  Span s;
+  const int g = t.tile / kGroup - kBack;
+  s.state = t.from < g * kGroup ? g - 1 : -1;
+  s.lo = max(max(g, 0) * kGroup, t.from);
+  s.n = t.tile - s.lo;
+  s.per = (s.n + C::W - 1) / C::W;
+  s.t0 = s.lo + (threadIdx.x >> 5) * s.per;
+  s.t1 = min(s.t0 + s.per, t.tile);
+  return s;
+}
+template <class C>
+__device__ __forceinline__ const float* map_place(const ScanParams& p, const Run& t, int tile) {
+  return p.agg + 2 * (tile * (static_cast<int64_t>(p.cols) * C::kWidth) + t.ch);
+}
+template <class C>
+__device__ __forceinline__ float* state_place(const ScanParams& p, const Run& t, int group) {
+  return p.carry + group * (static_cast<int64_t>(p.cols) * C::kWidth) + t.ch;
+}
+template <class C>
+__device__ __forceinline__ void ask(const ScanParams& p, const Run& t, Look<C>& l) {
+  if (t.tile < 0 || !t.needs) return;
+  const Span s = span_of<C>(t);
+#pragma unroll
+  for (int k = 0; k < Look<C>::kMost; ++k)
+    if (s.t0 + k < s.t1) peek<2 * C::V>(map_place<C>(p, t, s.t0 + k), l.m[k]);
+  if ((threadIdx.x >> 5) == C::W - 1 && s.state >= 0) peek<C::V>(state_place<C>(p, t, s.state), l.c);
+}
+
 // The state that enters this warp's run, from the tiles before, the group before and the runs' maps.  False: give up.
 template <class C>
-__device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int ring, const Run& t, float (&in)[C::V]) {
+__device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int ring, const Run& t, Look<C>& l,
+                                      Vec<C::V>& in) {
   constexpr int V = C::V, W = C::W;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t wide = static_cast<int64_t>(p.cols) * C::kWidth;
-#pragma unroll
-  for (int i = 0; i < V; ++i) in[i] = 0.f;
+  in = fill<V>(0.f);
   if (t.needs) {
-    const int group = t.tile / kGroup, g0 = group * kGroup;
-    const int lo = max(g0, t.from), n = t.tile - lo, per = (n + W - 1) / W;
-    const int t0 = lo + warp * per, t1 = min(t0 + per, t.tile);
-    float A[V], B[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 1.f, B[i] = 0.f;
+    const Span s = span_of<C>(t);
+    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f);
     bool ok = true;
-    for (int k = t0; k < t1; ++k) {
-      float m[2 * V];
-      ok &= await<2 * V>(p.agg + 2 * (k * wide + t.ch), true, m, p.hdr);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        B[i] = fmaf(m[2 * i], B[i], m[2 * i + 1]);
-        A[i] *= m[2 * i];
+    for (int k = 0; k < Look<C>::kMost; ++k)
+      if (s.t0 + k < s.t1) {
+        if (!__all_sync(0xffffffffu, there<2 * V>(l.m[k])))
+          ok &= await<2 * V>(map_place<C>(p, t, s.t0 + k), true, l.m[k], p.hdr);
+        Vec<V> mA, mB;
+#pragma unroll
+        for (int i = 0; i < V; ++i) mA[i] = l.m[k][2 * i], mB[i] = l.m[k][2 * i + 1];
+        B = fma(mA, B, mB);
+        A = mul(A, mA);
       }
-    }
 #pragma unroll
     for (int i = 0; i < V; ++i) sh.part[warp][lane * V + i] = make_float2(A[i], B[i]);
     if (warp == W - 1) {
-      float c[V] = {};
-      ok &= await<V>(p.carry + (group - 1) * wide + t.ch, t.from < g0, c, p.hdr);
+      if (s.state >= 0 && !__all_sync(0xffffffffu, there<V>(l.c)))
+        ok &= await<V>(state_place<C>(p, t, s.state), true, l.c, p.hdr);
 #pragma unroll
-      for (int i = 0; i < V; ++i) sh.carry[lane * V + i] = c[i];
+      for (int i = 0; i < V; ++i) sh.carry[lane * V + i] = s.state >= 0 ? l.c[i] : 0.f;
     }
     if (!ok) sh.stop_enter = 1;
     worker_sync<C>();
     if (sh.stop_enter) return false;
 #pragma unroll
     for (int i = 0; i < V; ++i) in[i] = sh.carry[lane * V + i];
-    for (int w = 0; w * per < n; ++w)
+    for (int w = 0; w * s.per < s.n; ++w) {
+      Vec<V> mA, mB;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 m = sh.part[w][lane * V + i];
-        in[i] = fmaf(m.x, in[i], m.y);
-      }
+      for (int i = 0; i < V; ++i) mA[i] = sh.part[w][lane * V + i].x, mB[i] = sh.part[w][lane * V + i].y;
+      in = fma(mA, in, mB);
+    }
   }
   // the runs before; warp 0 goes through all of them for the state after the tile
   bool reset = false;
-  float after[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) after[i] = in[i];
+  Vec<V> after = in;
   const bool last = warp == 0 && t.needs && last_of_group<C>(p, t);
   for (int w = 0; w < (last ? W : warp); ++w) {
     const bool rw = sh.reset[ring][w] != 0;
     reset |= rw;
+    Vec<V> mA, mB;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 m = sh.run[ring][w][lane * V + i];
-      after[i] = rw ? m.y : fmaf(m.x, after[i], m.y);
-    }
+    for (int i = 0; i < V; ++i) mA[i] = sh.run[ring][w][lane * V + i].x, mB[i] = sh.run[ring][w][lane * V + i].y;
+    after = rw ? mB : fma(mA, after, mB);
   }
   if (last) {
-    if (!reset) show<V>(p.carry + (t.tile / kGroup) * wide + t.ch, after);
+    if (!reset) show<V>(state_place<C>(p, t, t.tile / kGroup), after.e);
   } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) in[i] = after[i];
+    in = after;
   }
   return true;
 }
@@ -299,16 +406,41 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
   const int lane = threadIdx.x & 31, total = p.tiles * p.cols;
   const int most = min(S, tiles_each(p));  // a block's tiles at a time
   volatile int* abort_flag = &sh.abort_flag;
-  int issued = 0;
-  bool ok = true;
-  for (int j = 0;; ++j) {
-    const int s = j % S;
-    if (j >= most)
-      ok = wwait(smem_u32(&sh.empty[(j - most) % S]), ((j - most) / S) & 1, abort_flag, p.hdr, 71);
-    if (!ok) break;
-    int number = 0;
+  // a tile's number, and its segments: where the scan enters it (backward: behind it), and the starts in it
+  int number = 0, tile = 0, col = 0, row0 = 0, b0 = 0, from = 0, needs = 0;
+  uint32_t bits = 0;  // lane i: word i
+  const auto take = [&] {
     if (lane == 0) number = atomicAdd(p.ticket, 1);
     number = __shfl_sync(0xffffffffu, number, 0);
+    if (number >= total) return;
+    tile = number / p.cols;
+    col = number - tile * p.cols;
+    const int rt = BACK ? p.tiles - 1 - tile : tile;
+    row0 = rt * C::kRows;
+    b0 = p.first[rt];
+    const int f = BACK ? p.first[rt + 1] : b0, enter = BACK ? row0 + C::kRows : row0;
+    const int cf = p.cu[f], before = p.cu[max(f - 1, 0)];
+    bits = 0;
+    for (int b = b0; b <= p.B; b += 32) {
+      const int d = b + lane <= p.B ? p.cu[b + lane] - row0 : C::kRows + 1;
+#pragma unroll
+      for (int w = 0; w < C::kWords; ++w) {
+        const uint32_t word = __reduce_or_sync(0xffffffffu, d >> 5 == w && d <= C::kRows ? 1u << (d & 31) : 0u);
+        if (lane == w) bits |= word;
+      }
+      if (__any_sync(0xffffffffu, d > C::kRows)) break;
+    }
+    needs = enter < p.T && cf != enter;
+    from = !needs ? tile : BACK ? p.tiles - 1 - (cf - 1) / C::kRows : before / C::kRows;
+  };
+  int issued = 0;
+  bool ok = true;
+  if (most > 1) take();  // a tile ahead of the place for it
+  for (int j = 0;; ++j) {
+    const int s = j % S;
+    if (j >= most) ok = wwait(smem_u32(&sh.empty[(j - most) % S]), ((j - most) / S) & 1, abort_flag, p.hdr, 71);
+    if (!ok) break;
+    if (most == 1) take();
     Slot<C>& slot = sh.slot[s];
     if (number >= total) {
       if (lane == 0) {
@@ -318,8 +450,6 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
       }
       return;
     }
-    const int tile = number / p.cols, col = number - tile * p.cols;
-    const int rt = BACK ? p.tiles - 1 - tile : tile, row0 = rt * C::kRows;
     if (lane == 0) {
       if constexpr (kBytes > 0) {
         mbar_expect_tx(smem_u32(&sh.full[s]), kBytes);
@@ -327,28 +457,17 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
       } else {
         mbar_arrive(smem_u32(&sh.full[s]));
       }
-    }
-    issued = j + 1;
-    // the segments: where the scan enters the tile (backward: behind it), and the starts in it
-    const int b0 = p.first[rt], f = BACK ? p.first[rt + 1] : b0, enter = BACK ? row0 + C::kRows : row0;
-    const int cf = p.cu[f], before = p.cu[max(f - 1, 0)];
-    if (lane < C::kWords) slot.bits[lane] = 0;
-    __syncwarp();
-    for (int b = b0; b <= p.B; b += 32) {
-      const int d = b + lane <= p.B ? p.cu[b + lane] - row0 : C::kRows + 1;
-      if (d <= C::kRows) atomicOr(&slot.bits[d >> 5], 1u << (d & 31));
-      if (__any_sync(0xffffffffu, d > C::kRows)) break;
-    }
-    if (lane == 0) {
-      const bool needs = enter < p.T && cf != enter;
       slot.tile = tile;
       slot.col = col;
       slot.b0 = b0;
       slot.needs = needs;
-      slot.from = !needs ? tile : BACK ? p.tiles - 1 - (cf - 1) / C::kRows : before / C::kRows;
+      slot.from = from;
     }
+    issued = j + 1;
+    if (lane < C::kWords) slot.bits[lane] = bits;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+    if (most > 1) take();
   }
   // given up: the copies on their way land before the block ends (bounded again)
   if constexpr (kBytes > 0) {
@@ -383,8 +502,10 @@ __device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First
     } else {
       sh.stop_first = 1;
     }
+    Look<C> look;
+    ask<C>(p, old, look);
     if (now.tile >= 0) {
-      float A[V], B[V];
+      Vec<V> A, B;
       const bool reset = first(now, stage, A, B);
 #pragma unroll
       for (int k = 0; k < V; ++k) sh.run[ring][warp][lane * V + k] = make_float2(reset ? 0.f : A[k], B[k]);
@@ -396,10 +517,11 @@ __device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First
     if (single) {
       old = now;
       held = stage;
+      ask<C>(p, old, look);
     }
     if (old.tile >= 0) {
-      float in[V];
-      if (!enter<C>(p, sh, single ? ring : ring == 0 ? kRings - 1 : ring - 1, old, in)) break;
+      Vec<V> in;
+      if (!enter<C>(p, sh, single ? ring : ring == 0 ? kRings - 1 : ring - 1, old, look, in)) break;
       second(old, held, in);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[held]));
@@ -446,6 +568,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
 // Where a run's rows are read: its tile's copy, or memory.
 template <class T, class C, bool TMA>
 struct Rows {
+  static constexpr int kRun = C::R;
   const T* base;       // the thread's first element of stage 0, or of the tensor
   int64_t step;        // between rows
   __device__ __forceinline__ Rows(const uint8_t* smem, const void* global, int64_t rs) {
@@ -460,13 +583,44 @@ struct Rows {
     return base + t.row * step + t.ch;
   }
   __device__ __forceinline__ Pack<T, C::V> get(const T* first, int r, const Run& t) const {
-    if (TMA) return load_pack<T, C::V>(first + r * C::kWidth);
-    Pack<T, C::V> none;
+    if constexpr (TMA) {
+      return load_pack<T, C::V>(first + r * C::kWidth);
+    } else {
+      Pack<T, C::V> none;
 #pragma unroll
-    for (int i = 0; i < C::V; ++i) none.set(i, 0.f);
-    return t.on ? load_pack<T, C::V>(first + r * step) : none;
+      for (int i = 0; i < C::V; ++i) none.set(i, 0.f);
+      return t.on ? load_pack<T, C::V>(first + r * step) : none;
+    }
   }
 };
+
+// Rows of a run that holds a segment's boundary or the stream's end, in order or from the back.  From the copied tile one
+// after another; from memory all of them are asked for first.
+template <bool TMA, bool BACK = false, class A, class PA, class B, class PB, class F>
+__device__ __forceinline__ void rows_of(const A& a, PA pa, const B& b, PB pb, const Run& t, F&& f) {
+  constexpr int R = A::kRun;
+  if constexpr (TMA) {
+#pragma unroll 1
+    for (int i = 0; i < t.n; ++i) {
+      const int r = BACK ? t.n - 1 - i : i;
+      f(r, a.get(pa, r, t), b.get(pb, r, t));
+    }
+  } else {
+    decltype(a.get(pa, 0, t)) va[R];
+    decltype(b.get(pb, 0, t)) vb[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < t.n) {
+        va[r] = a.get(pa, r, t);
+        vb[r] = b.get(pb, r, t);
+      }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = BACK ? R - 1 - i : i;
+      if (r < t.n) f(r, va[r], vb[r]);
+    }
+  }
+}
 
 // Bytes of a tile of one tensor.
 template <class T, class C> constexpr int tile_bytes() { return C::kRows * C::kWidth * static_cast<int>(sizeof(T)); }
@@ -524,72 +678,56 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
     tma_load_2d(smem_u32(x_smem + stage * kX), &maps.a, bar, ch0, row0);
     tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
   };
-  struct At {
-    const TX* x;
-    const TG* g;
+  const auto step = [&](const Pack<TX, V>& x, const Vec<V>& g, Vec<V>& h) { h = fma(decay(g), h, wide_of(x)); };
+  const auto start = [&](const Pack<TX, V>& x, const Vec<V>& g, const Run& t, int r, Vec<V>& h) {  // a segment's first row
+    h = wide_of(x);  // (x itself without h0, whatever its decay is)
+    if (p.h0) h = fma(decay(g), state_row<V>(p.h0, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on), h);
   };
-  const auto step = [&](const At& a, const Run& t, int r, float (&h)[V], float (&A)[V]) {
-    const Pack<TX, V> x = xs.get(a.x, r, t);
-    const Pack<TG, V> g = gs.get(a.g, r, t);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      A[i] += g[i];
-      h[i] = fmaf(decay(g[i]), h[i], x[i]);
-    }
-  };
-  const auto start = [&](const At& a, const Run& t, int r, float (&h)[V]) {  // a segment's first row
-    const Pack<TX, V> x = xs.get(a.x, r, t);
-    const Pack<TG, V> g = gs.get(a.g, r, t);
-    state_row<V>(p.h0, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on, h);
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = p.h0 ? fmaf(decay(g[i]), h[i], x[i]) : x[i];  // (x itself, whatever its decay is)
-  };
-  const auto first = [&](const Run& t, int stage, float (&A)[V], float (&B)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = B[i] = 0.f;
-    const At a{xs.at(t, stage, false), gs.at(t, stage, false)};
+  const auto first = [&](const Run& t, int stage, Vec<V>& A, Vec<V>& B) {
+    A = B = fill<V>(0.f);
+    const TX* const xa = xs.at(t, stage, false);
+    const TG* const ga = gs.at(t, stage, false);
     if (t.starts == 0 && t.n == R) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) step(a, t, r, B, A);
-    } else {
-#pragma unroll 1
-      for (int r = 0; r < t.n; ++r) {
-        if ((t.starts >> r) & 1u) start(a, t, r, B);
-        else step(a, t, r, B, A);
+      for (int r = 0; r < R; ++r) {
+        const Vec<V> g = wide_of(gs.get(ga, r, t));
+        A = add(A, g);
+        step(xs.get(xa, r, t), g, B);
       }
+    } else {
+      rows_of<TMA>(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
+        const Vec<V> g = wide_of(gr);
+        A = add(A, g);
+        if ((t.starts >> r) & 1u) start(x, g, t, r, B);
+        else step(x, g, B);
+      });
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = run_decay(A[i]);
     return t.starts != 0;
   };
-  const auto second = [&](const Run& t, int stage, float (&h)[V]) {
+  const auto second = [&](const Run& t, int stage, Vec<V>& h) {
     TH* out = static_cast<TH*>(p.out) + t.row * p.out_rs + t.ch;
-    const At a{xs.at(t, stage, false), gs.at(t, stage, false)};
-    float unused[V] = {};
-    const auto put = [&](int r) {
-      Pack<TH, V> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o.set(i, h[i]);
-      if (t.on) store_pack(out + r * p.out_rs, o);
-    };
+    const TX* const xa = xs.at(t, stage, false);
+    const TG* const ga = gs.at(t, stage, false);
     if (t.starts == 0 && t.n == R && (!p.last || t.ends == 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        step(a, t, r, h, unused);
-        put(r);
+        step(xs.get(xa, r, t), wide_of(gs.get(ga, r, t)), h);
+        if (t.on) store_pack(out + r * p.out_rs, narrow<TH, V>(h));
       }
     } else {
-#pragma unroll 1
-      for (int r = 0; r < t.n; ++r) {
-        if ((t.starts >> r) & 1u) start(a, t, r, h);
-        else step(a, t, r, h, unused);
-        put(r);
+      rows_of<TMA>(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
+        const Vec<V> g = wide_of(gr);
+        if ((t.starts >> r) & 1u) start(x, g, t, r, h);
+        else step(x, g, h);
+        if (t.on) store_pack(out + r * p.out_rs, narrow<TH, V>(h));
         if (p.last && t.on && ((t.ends >> r) & 1u)) {
           float* last = p.last + static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch;
 #pragma unroll
           for (int i = 0; i < V; ++i) last[i] = h[i];
         }
-      }
+      });
     }
   };
   run_block<C, false, TMA ? kX + kG : 0>(p, sh, load, first, second);
@@ -616,84 +754,60 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
     tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
     tma_load_2d(smem_u32(h_smem + stage * kH), &maps.c, bar, ch0, row0 - 1);  // the rows before (zeros before the first)
   };
-  const auto first = [&](const Run& t, int stage, float (&A)[V], float (&B)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = B[i] = 0.f;
-    const TH* const d_at = ds.at(t, stage, true);
-    const TG* const g_at = gs.at(t, stage, true);
-    const auto step = [&](int r) {
-      const Pack<TH, V> d = ds.get(d_at, r, t);
-      const Pack<TG, V> g = gs.get(g_at, r, t);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        A[i] += g[i];
-        B[i] = back_step(g[i], d[i] + B[i]);
-      }
+  const auto first = [&](const Run& t, int stage, Vec<V>& A, Vec<V>& B) {
+    A = B = fill<V>(0.f);
+    const TH* const da = ds.at(t, stage, true);
+    const TG* const ga = gs.at(t, stage, true);
+    const auto step = [&](const Pack<TH, V>& d, const Pack<TG, V>& gr) {
+      const Vec<V> g = wide_of(gr);
+      A = add(A, g);
+      B = mul(decay(g), add(wide_of(d), B));
     };
     if (t.ends == 0 && t.n == R) {
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r) step(r);
+      for (int r = R - 1; r >= 0; --r) step(ds.get(da, r, t), gs.get(ga, r, t));
     } else {
-#pragma unroll 1
-      for (int r = t.n - 1; r >= 0; --r) {
-        if ((t.ends >> r) & 1u) state_row<V>(p.dlast, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on, B);
-        step(r);
-      }
+      rows_of<TMA, true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
+        if ((t.ends >> r) & 1u) B = state_row<V>(p.dlast, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on);
+        step(d, g);
+      });
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = run_decay(A[i]);
     return t.ends != 0;
   };
-  const auto second = [&](const Run& t, int stage, float (&f)[V]) {
+  const auto second = [&](const Run& t, int stage, Vec<V>& f) {
     TX* dx = static_cast<TX*>(p.out) + t.row * p.out_rs + t.ch;
     TG* dg = static_cast<TG*>(p.dg) + t.row * p.dg_rs + t.ch;
-    const TH* const d_at = ds.at(t, stage, true);
-    const TG* const g_at = gs.at(t, stage, true);
-    const TH* const h_at = hs.at(t, stage, true) - (TMA ? 0 : p.h_rs);
+    const TH* const da = ds.at(t, stage, true);
+    const TG* const ga = gs.at(t, stage, true);
+    const TH* const ha = hs.at(t, stage, true) - (TMA ? 0 : p.h_rs);
     // before: the row before's h, at a segment's first row h0 (none: 0, and so is the decay's gradient)
-    const auto step = [&](int r, const float (&before)[V], bool none) {
-      const Pack<TH, V> d = ds.get(d_at, r, t);
-      const Pack<TG, V> g = gs.get(g_at, r, t);
-      Pack<TX, V> ox;
-      Pack<TG, V> og;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float e = d[i] + f[i];
-        f[i] = back_step(g[i], e);
-        ox.set(i, e);
-        og.set(i, none ? 0.f : f[i] * before[i]);
-      }
+    const auto step = [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g, const Vec<V>& before, bool none) {
+      const Vec<V> e = add(wide_of(d), f);
+      f = mul(decay(wide_of(g)), e);
+      const Vec<V> q = none ? fill<V>(0.f) : mul(f, before);
       if (t.on) {
-        store_pack(dx + r * p.out_rs, ox);
-        store_pack(dg + r * p.dg_rs, og);
+        store_pack(dx + r * p.out_rs, narrow<TX, V>(e));
+        store_pack(dg + r * p.dg_rs, narrow<TG, V>(q));
       }
     };
-    const auto stored = [&](int r, float (&before)[V]) {
-      const Pack<TH, V> h = hs.get(h_at, r, t);
-#pragma unroll
-      for (int i = 0; i < V; ++i) before[i] = h[i];
-    };
-    float before[V];
     if (t.ends == 0 && t.starts == 0 && t.n == R) {
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r) {
-        stored(r, before);
-        step(r, before, false);
-      }
+      for (int r = R - 1; r >= 0; --r)
+        step(r, ds.get(da, r, t), gs.get(ga, r, t), wide_of(hs.get(ha, r, t)), false);
     } else {
-#pragma unroll 1
-      for (int r = t.n - 1; r >= 0; --r) {
+      rows_of<TMA, true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
         const int64_t state = static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch;
         const bool start = (t.starts >> r) & 1u;
-        if ((t.ends >> r) & 1u) state_row<V>(p.dlast, state, t.on, f);
-        if (start) state_row<V>(p.h0, state, t.on, before);
-        else stored(r, before);
-        step(r, before, start && !p.h0);
+        if ((t.ends >> r) & 1u) f = state_row<V>(p.dlast, state, t.on);
+        const Vec<V> before = start ? state_row<V>(p.h0, state, t.on) : wide_of(hs.get(ha, r, t));
+        step(r, d, g, before, start && !p.h0);
         if (p.last && start && t.on) {
 #pragma unroll
           for (int i = 0; i < V; ++i) p.last[state + i] = f[i];
         }
-      }
+      });
     }
   };
   run_block<C, true, TMA ? 2 * kH + kG : 0>(p, sh, load, first, second);
@@ -810,7 +924,10 @@ cudaError_t run_blocks(int stage, void (*kernel)(ScanParams, Maps), size_t piece
 }
 
 template <int V> using FwdShape = Shape<V, 8, 16, 3, 2>;
+// (from memory: short runs, whose rows are all asked for at once)
+template <int V> using FwdPlain = Shape<V, 8, 8, 3, 3>;
 template <int V> using BwdShape = Shape<V, 8, 8, 3, 2>;
+template <int V> using BwdPlain = Shape<V, 8, 8, 3, 3>;
 
 // Two channels a lane where rows lie on boundaries of two elements, else one; copied tiles where they lie on 16 bytes.
 template <class TX, class TG, class TH>
@@ -819,14 +936,14 @@ cudaError_t run_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
   const bool two =
       p.D % 2 == 0 && steps_of<TX>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) && steps_of<TH>(p.out, p.out_rs, 2);
   Maps maps{};
-  if (!two) return run_blocks<FwdShape<1>>(stage, scan_fwd_kernel<TX, TG, TH, FwdShape<1>, false>, 0, p, maps, ws, st);
+  if (!two) return run_blocks<FwdPlain<1>>(stage, scan_fwd_kernel<TX, TG, TH, FwdPlain<1>, false>, 0, p, maps, ws, st);
   if (rows16<TX>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TX) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows)))
       return cudaErrorInvalidValue;
     return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C, true>, tile_bytes<TX, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C, false>, 0, p, maps, ws, st);
+  return run_blocks<FwdPlain<2>>(stage, scan_fwd_kernel<TX, TG, TH, FwdPlain<2>, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
@@ -835,7 +952,7 @@ cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
   const bool two = p.D % 2 == 0 && steps_of<TH>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) &&
                    steps_of<TH>(p.h, p.h_rs, 2) && steps_of<TX>(p.out, p.out_rs, 2) && steps_of<TG>(p.dg, p.dg_rs, 2);
   Maps maps{};
-  if (!two) return run_blocks<BwdShape<1>>(stage, scan_bwd_kernel<TX, TG, TH, BwdShape<1>, false>, 0, p, maps, ws, st);
+  if (!two) return run_blocks<BwdPlain<1>>(stage, scan_bwd_kernel<TX, TG, TH, BwdPlain<1>, false>, 0, p, maps, ws, st);
   if (rows16<TH>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && rows16<TH>(p.h, p.h_rs)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TH) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows) &&
@@ -843,7 +960,7 @@ cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
       return cudaErrorInvalidValue;
     return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C, true>, 2 * tile_bytes<TH, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C, false>, 0, p, maps, ws, st);
+  return run_blocks<BwdPlain<2>>(stage, scan_bwd_kernel<TX, TG, TH, BwdPlain<2>, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
@@ -859,9 +976,11 @@ cudaError_t run_step(ScanParams p, void* ws, cudaStream_t st) {
 
 }  // namespace
 
-size_t scan_workspace(int T, int D) {  // (narrow columns waste less than they need more of)
-  const auto most = [&](int rows) { return std::max(layout_of(T, D, rows, 32).total, layout_of(T, D, rows, 64).total); };
-  return std::max(most(FwdShape<2>::kRows), most(BwdShape<2>::kRows));
+size_t scan_workspace(int T, int D) {
+  size_t n = 0;
+  for (int rows : {FwdShape<2>::kRows, FwdPlain<2>::kRows, BwdShape<2>::kRows, BwdPlain<2>::kRows})
+    n = std::max({n, layout_of(T, D, rows, 32).total, layout_of(T, D, rows, 64).total});
+  return n;
 }
 
 cudaError_t launch_scan_fwd(int stage, ScanParams p, int xb, int gb, void* ws, cudaStream_t st) {

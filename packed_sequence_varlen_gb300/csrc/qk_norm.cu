@@ -7,30 +7,37 @@
 //   dw = sum over tokens and heads of g n,   dx = r (g w - n mean(g w n)).
 //
 // Layout: a head of d elements is held by G lanes of a warp (G the power of two at or above d / 8), a
-// lane holding two pieces of four elements such that every pair lies in one lane: dims 4 u and rot / 2 + 4 u
-// of unit u < rot / 8 (8 u and 8 u + 4 when interleaved, and for the dims that are not turned).  So
-// nothing but the sums crosses lanes.  A warp takes a token's heads, or some of them, in turn, and keeps the
-// token's cosines and sines in registers.
+// lane holding four pairs: dims 4 u .. 4 u + 3 and rot / 2 + 4 u .. of unit u < rot / 8 (8 u .. 8 u + 7 when interleaved, and
+// for the dims that are not turned, as pairs with an angle of 0).  So nothing but the sums crosses lanes.  A group is the
+// 32 / G heads that a warp takes at a time.
 //
-// Angles: inv_freq / 2 pi as a fraction of a turn in 64 bits, times the position modulo 2^64: whole turns
-// drop out exactly, so a position of a million is turned as accurately as the first.
+// Work: the groups of all tokens, token by token, are one sequence, of which every warp takes an equal stretch; so
+// whatever the sizes the warps end together, and results do not change from call to call.  A warp's groups are copied
+// to a ring of its own in shared memory, kRing bytes ahead, 16 bytes a lane: nothing waits for another warp.
 //
-// Weight gradients: a warp's sums stay in registers over all its heads and tokens, are added in the block in
-// warp order and written as one row per block; qk_norm_join_kernel adds the rows in order.  Tokens are
-// dealt to the warps by a fixed rule, so results do not change from call to call.
+// Angles: inv_freq / 2 pi as a fraction of a turn in 64 bits (whole numbers: fp64 is slow here), times the position modulo
+// 2^64: whole turns drop out exactly, so a position of a million is turned as accurately as the first.
+//
+// Weight gradients: a warp's sums stay in registers over all its groups, are added in the block in warp order and
+// written as one row per block; qk_norm_join_kernel adds the rows in order.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "qk_norm.cuh"
+#include "vec.cuh"
 
 namespace va {
 
 namespace {
 
 constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
-constexpr int kSteps = 4;  // head groups a warp has in flight
+constexpr int kFwdRing = 6144, kBwdRing = 8192;  // bytes a warp has on their way
+constexpr int kFwdBlocks = 3, kBwdBlocks = 2;    // blocks an SM
 
-// The dims of a lane's two pieces, or first >= d for a lane without a head's part.
+using V4 = Vec<4>;
+
+// The dims of a lane's two pieces, and whether it has any and whether they are turned.
 struct Unit {
   int a, b;
   bool on, turned;
@@ -44,11 +51,16 @@ __device__ __forceinline__ Unit unit_of(int u, int d, int rot, int interleaved) 
   return r;
 }
 
-// inv_freq as a fraction of a turn per position, times 2^64.
+// inv_freq as a fraction of a turn per position, times 2^64: its 24 bits times 1 / 2 pi to 96 bits, shifted.
 __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
-  double t = static_cast<double>(inv_freq) * 0.15915494309189533577;
-  t -= floor(t);
-  return static_cast<uint64_t>(t * 18446744073709551616.0);
+  const uint32_t b = __float_as_uint(inv_freq), field = (b >> 23) & 255u;
+  const uint64_t m = (b & 0x7fffffu) | (field ? 0x800000u : 0u);
+  const int shift = 32 - (static_cast<int>(field ? field : 1u) - 150);  // the value is m 2^(field - 150)
+  const unsigned __int128 c = static_cast<unsigned __int128>(0x28be60dbu) << 64 | 0x9391054a7f09d5f4ull;
+  const unsigned __int128 x = c * m;
+  const uint64_t t = shift >= 128 ? 0 : shift >= 0 ? static_cast<uint64_t>(x >> shift)
+                     : shift > -64 ? static_cast<uint64_t>(x) << -shift : 0;
+  return b >> 31 ? 0 - t : t;
 }
 
 __device__ __forceinline__ void angle(int pos, uint64_t turn, float& c, float& s) {
@@ -61,215 +73,314 @@ __device__ __forceinline__ float load_w(const void* w, int bf16, int i) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
 }
 
-struct Lane {
-  float c[4], s[4];       // the token's cosines and sines for this lane's four pairs (1, 0 when not turned)
-  uint64_t turn[4];
-};
-
-__device__ __forceinline__ void lane_turns(Lane& l, const QkParams& p, const Unit& un, int u) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) l.turn[j] = un.on && un.turned ? turn_of(p.inv_freq[4 * u + j]) : 0;
-}
-
-__device__ __forceinline__ void lane_angles(Lane& l, int pos) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) angle(pos, l.turn[j], l.c[j], l.s[j]);
-}
-
-// x[0..3] the first piece, x[4..7] the second; back: by the negative angle.
-template <bool IL, bool BACK>
-__device__ __forceinline__ void rotate(float (&x)[8], const Lane& l) {
+// A lane's eight numbers as the first and the second of its four pairs.
+template <bool IL>
+__device__ __forceinline__ void to_pairs(const V4& p, const V4& q, V4& a, V4& b) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int i = IL ? 2 * j : j, k = IL ? 2 * j + 1 : j + 4;
-    const float s = BACK ? -l.s[j] : l.s[j];
-    const float a = x[i], b = x[k];
-    x[i] = a * l.c[j] - b * s;
-    x[k] = b * l.c[j] + a * s;
+    a[j] = !IL ? p[j] : j < 2 ? p[2 * j] : q[2 * j - 4];
+    b[j] = !IL ? q[j] : j < 2 ? p[2 * j + 1] : q[2 * j - 3];
+  }
+}
+template <bool IL>
+__device__ __forceinline__ void to_pieces(const V4& a, const V4& b, V4& p, V4& q) {
+  if constexpr (IL) {
+    p = V4{{a[0], b[0], a[1], b[1]}};
+    q = V4{{a[2], b[2], a[3], b[3]}};
+  } else {
+    p = a;
+    q = b;
   }
 }
 
+__device__ __forceinline__ float across(const V4& v) { return (v[0] + v[1]) + (v[2] + v[3]); }
+// The sums of N numbers over the G lanes of a head.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], int G) {
-  for (int o = G >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < G)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-// A warp's share of a token: head groups [s0, s1) of the Sq + Sk that the token's queries and keys make.
-struct Share {
-  int token, s0, s1;
-};
-__device__ __forceinline__ Share share_of(const QkParams& p, int64_t item, int steps) {
-  Share r;
-  r.token = static_cast<int>(item / p.chunks);
-  const int c = static_cast<int>(item % p.chunks);
-  r.s0 = static_cast<int>(static_cast<int64_t>(steps) * c / p.chunks);
-  r.s1 = static_cast<int>(static_cast<int64_t>(steps) * (c + 1) / p.chunks);
-  return r;
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// A place in the sequence of groups (a token's queries, then its keys), and a lane's element of it in N tensors:
+// moving on is an addition, the strides are multiplied only where a token's queries or keys begin.
+struct Rows {
+  const void* base[2];
+  int64_t rs[2], hs[2];
+};
+template <class T, int N>
+struct Cursor {
+  int token, q, head;  // head: the group's first
+  const T* at[N];
+  int64_t step[N];
+  template <class R>
+  __device__ __forceinline__ void begin(const R& rows, int sub, int per, int off) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const Rows r = rows(n);
+      const int64_t rs = q ? r.rs[1] : r.rs[0], hs = q ? r.hs[1] : r.hs[0];
+      at[n] = static_cast<const T*>(q ? r.base[1] : r.base[0]) + token * rs + (head + sub) * hs + off;
+      step[n] = per * hs;
+    }
+  }
+  template <class R>
+  __device__ __forceinline__ void next(const R& rows, int H0, int H1, int sub, int per, int off) {
+    head += per;
+    if (head >= (q ? H1 : H0)) {
+      head = 0;
+      token += q;
+      q ^= 1;
+      begin(rows, sub, per, off);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) at[n] += step[n];
+    }
+  }
+};
+
+// What a lane keeps of the call: its dims, the queries' and keys' weights (as pairs), its four frequencies.
+template <bool IL>
+struct LaneState {
+  Unit un;
+  int sub, per, Sq, groups;
+  V4 wa[2], wb[2];
+  uint64_t turn[4];
+  __device__ __forceinline__ LaneState(const QkParams& p, int G) {
+    const int lane = threadIdx.x & 31, u = lane & (G - 1);
+    sub = lane / G;
+    per = 32 / G;
+    un = unit_of(u, p.d, p.rot, IL);
+    Sq = (p.H[0] + per - 1) / per;
+    groups = Sq + (p.H[1] + per - 1) / per;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      V4 first, second;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        first[j] = un.on ? load_w(p.w[q], p.w_bf16, un.a + j) : 0.f;
+        second[j] = un.on ? load_w(p.w[q], p.w_bf16, un.b + j) : 0.f;
+      }
+      to_pairs<IL>(first, second, wa[q], wb[q]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) turn[j] = un.on && un.turned ? turn_of(p.inv_freq[4 * u + j]) : 0;
+  }
+  __device__ __forceinline__ void angles(int pos, V4& c, V4& s) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) angle(pos, turn[j], c[j], s[j]);
+  }
+  template <class T, int N>
+  __device__ __forceinline__ Cursor<T, N> place(int64_t i) const {
+    Cursor<T, N> c;
+    c.token = static_cast<int>(i / groups);
+    const int g = static_cast<int>(i % groups);
+    c.q = g >= Sq;
+    c.head = (g - (c.q ? Sq : 0)) * per;
+    return c;
+  }
+};
 
 }  // namespace
 
-template <class T, bool IL>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_fwd_kernel(const QkParams p) {
+// GT: lanes per head, 0: as the call says.
+template <class T, bool IL, int GT>
+__global__ void __launch_bounds__(kQkThreads, kFwdBlocks) qk_norm_fwd_kernel(const QkParams p) {
   griddep_begin();
+  constexpr int kPiece = 8 * sizeof(T), kStage = 32 * kPiece, D = kFwdRing / kStage;
+  __shared__ __align__(16) uint8_t ring[kQkWarps][D][kStage];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int u = lane & (p.G - 1), sub = lane / p.G, per = 32 / p.G;
-  const Unit un = unit_of(u, p.d, p.rot, IL);
-  const int Sq = (p.H[0] + per - 1) / per, Sk = (p.H[1] + per - 1) / per;
-  float w[2][8];
+  const int G = GT ? GT : p.G;
+  const LaneState<IL> l(p, G);
+  const int64_t all = static_cast<int64_t>(p.T) * l.groups, warps = static_cast<int64_t>(gridDim.x) * kQkWarps;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kQkWarps + warp;
+  const int64_t first = all * me / warps;
+  const int mine = static_cast<int>(all * (me + 1) / warps - first);
+  const int u = lane & (G - 1);
+  const auto in = [&](int) { return Rows{{p.x[0], p.x[1]}, {p.x_rs[0], p.x_rs[1]}, {p.x_hs[0], p.x_hs[1]}}; };
+  const auto out = [&](int) { return Rows{{p.y[0], p.y[1]}, {p.y_rs[0], p.y_rs[1]}, {p.y_hs[0], p.y_hs[1]}}; };
+  Cursor<T, 1> ask = l.template place<T, 1>(first), at = ask;
+  ask.begin(in, l.sub, l.per, 8 * u);
+  at.begin(out, l.sub, l.per, 0);
+  uint8_t* const mine_ring = &ring[warp][0][(l.sub * G + u) * kPiece];
+  const auto issue = [&](int i, int stage) {
+    if (i < mine) {
+      if (l.un.on && ask.head + l.sub < (ask.q ? p.H[1] : p.H[0])) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[q][j] = un.on ? load_w(p.w[q], p.w_bf16, (j < 4 ? un.a : un.b - 4) + j) : 0.f;
-  Lane l;
-  lane_turns(l, p, un, u);
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  const int64_t items = static_cast<int64_t>(p.T) * p.chunks;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kQkWarps + warp; item < items;
-       item += static_cast<int64_t>(gridDim.x) * kQkWarps) {
-    const Share sh = share_of(p, item, Sq + Sk);
-    lane_angles(l, p.pos[sh.token]);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int lo = q == 0 ? sh.s0 : max(sh.s0, Sq) - Sq, hi = q == 0 ? min(sh.s1, Sq) : sh.s1 - Sq;
-      const T* x = static_cast<const T*>(p.x[q]) + sh.token * p.x_rs[q];
-      T* y = static_cast<T*>(p.y[q]) + sh.token * p.y_rs[q];
-      for (int s = lo; s < hi; s += kSteps) {
-        Pack<T, 4> in[kSteps][2];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const int h = (s + i) * per + sub;
-          if (s + i < hi && un.on && h < p.H[q]) {
-            in[i][0] = load_pack<T, 4>(x + h * p.x_hs[q] + un.a);
-            in[i][1] = load_pack<T, 4>(x + h * p.x_hs[q] + un.b);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) in[i][0].set(j, 0.f), in[i][1].set(j, 0.f);
-          }
-        }
-        float ss[kSteps];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          ss[i] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss[i] = fmaf(in[i][j >> 2][j & 3], in[i][j >> 2][j & 3], ss[i]);
-        }
-        group_sum(ss, p.G);
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const int h = (s + i) * per + sub;
-          if (!(s + i < hi && un.on && h < p.H[q])) continue;
-          const float r = rsqrtf(fmaf(ss[i], inv_d, p.eps));
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = in[i][j >> 2][j & 3] * r * w[q][j];
-          rotate<IL, false>(v, l);
-          Pack<T, 4> out[2];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) out[j >> 2].set(j & 3, v[j]);
-          store_pack(y + h * p.y_hs[q] + un.a, out[0]);
-          store_pack(y + h * p.y_hs[q] + un.b, out[1]);
-        }
+        for (int k = 0; k < kPiece / 16; ++k) copy16(mine_ring + stage * kStage + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
       }
+      ask.next(in, p.H[0], p.H[1], l.sub, l.per, 8 * u);
     }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(i, i);
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  V4 c, s, ca, sb, cb, sa;  // the token's, and with the weights: y_a = r (x_a ca - x_b sb), y_b = r (x_b cb + x_a sa)
+  int stage = 0, refill = D - 1, pos = p.pos[min(at.token, p.T - 1)];
+  for (int i = 0; i < mine; ++i) {
+    issue(i + D - 1, refill);
+    if (i == 0 || at.head == 0) {
+      if (i == 0 || at.q == 0) {
+        l.angles(pos, c, s);
+        pos = p.pos[min(at.token + 1, p.T - 1)];  // the next token's
+      }
+      const bool k = at.q != 0;
+      const V4 wa = k ? l.wa[1] : l.wa[0], wb = k ? l.wb[1] : l.wb[0];
+      ca = mul(c, wa);
+      sa = mul(s, wa);
+      cb = mul(c, wb);
+      sb = mul(s, wb);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sb[j] = -sb[j];
+    }
+    copy_wait<D - 1>();
+    __syncwarp();
+    const bool on = l.un.on && at.head + l.sub < (at.q ? p.H[1] : p.H[0]);
+    const T* row = reinterpret_cast<const T*>(ring[warp][stage]) + l.sub * G * 8;
+    V4 xa = fill<4>(0.f), xb = xa;
+    if (on) to_pairs<IL>(wide_of(load_pack<T, 4>(row + l.un.a)), wide_of(load_pack<T, 4>(row + l.un.b)), xa, xb);
+    float ss[1] = {across(fma(xb, xb, mul(xa, xa)))};
+    group_sum(ss, G);
+    const float r = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+    __syncwarp();  // the stage is written again
+    if (on) {
+      const V4 rr = fill<4>(r);
+      const V4 ya = mul(fma(xb, sb, mul(xa, ca)), rr), yb = mul(fma(xa, sa, mul(xb, cb)), rr);
+      V4 first4, second4;
+      to_pieces<IL>(ya, yb, first4, second4);
+      T* y = const_cast<T*>(at.at[0]);
+      store_pack(y + l.un.a, narrow<T, 4>(first4));
+      store_pack(y + l.un.b, narrow<T, 4>(second4));
+    }
+    at.next(out, p.H[0], p.H[1], l.sub, l.per, 0);
+    stage = stage + 1 == D ? 0 : stage + 1;
+    refill = refill + 1 == D ? 0 : refill + 1;
   }
 }
 
-template <class T, bool IL>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_bwd_kernel(const QkParams p) {
+template <class T, bool IL, int GT>
+__global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(const QkParams p) {
   griddep_begin();
+  constexpr int kPiece = 8 * sizeof(T), kHalf = 32 * kPiece, kStage = 2 * kHalf, D = kBwdRing / kStage;  // x, then dy
+  extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int u = lane & (p.G - 1), sub = lane / p.G, per = 32 / p.G;
-  const Unit un = unit_of(u, p.d, p.rot, IL);
-  const int Sq = (p.H[0] + per - 1) / per, Sk = (p.H[1] + per - 1) / per;
-  float w[2][8], dw[2][8];
+  uint8_t* const ring = smem + warp * kBwdRing;
+  const int G = GT ? GT : p.G;
+  const LaneState<IL> l(p, G);
+  const int64_t all = static_cast<int64_t>(p.T) * l.groups, warps = static_cast<int64_t>(gridDim.x) * kQkWarps;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kQkWarps + warp;
+  const int64_t first = all * me / warps;
+  const int mine = static_cast<int>(all * (me + 1) / warps - first);
+  const int u = lane & (G - 1);
+  const auto in = [&](int n) {
+    return n == 0 ? Rows{{p.x[0], p.x[1]}, {p.x_rs[0], p.x_rs[1]}, {p.x_hs[0], p.x_hs[1]}}
+                  : Rows{{p.dy[0], p.dy[1]}, {p.dy_rs[0], p.dy_rs[1]}, {p.dy_hs[0], p.dy_hs[1]}};
+  };
+  const auto out = [&](int) { return Rows{{p.y[0], p.y[1]}, {p.y_rs[0], p.y_rs[1]}, {p.y_hs[0], p.y_hs[1]}}; };
+  Cursor<T, 2> ask = l.template place<T, 2>(first);
+  Cursor<T, 1> at = l.template place<T, 1>(first);
+  ask.begin(in, l.sub, l.per, 8 * u);
+  at.begin(out, l.sub, l.per, 0);
+  uint8_t* const mine_ring = ring + (l.sub * G + u) * kPiece;
+  const auto issue = [&](int i, int stage) {
+    if (i < mine) {
+      if (l.un.on && ask.head + l.sub < (ask.q ? p.H[1] : p.H[0])) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[q][j] = un.on ? load_w(p.w[q], p.w_bf16, (j < 4 ? un.a : un.b - 4) + j) : 0.f;
-      dw[q][j] = 0.f;
+        for (int k = 0; k < kPiece / 16; ++k) {
+          copy16(mine_ring + stage * kStage + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
+          copy16(mine_ring + stage * kStage + kHalf + 16 * k, ask.at[1] + 16 / sizeof(T) * k);
+        }
+      }
+      ask.next(in, p.H[0], p.H[1], l.sub, l.per, 8 * u);
     }
-  Lane l;
-  lane_turns(l, p, un, u);
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(i, i);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  constexpr int kS = kSteps / 2;
-  const int64_t items = static_cast<int64_t>(p.T) * p.chunks;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kQkWarps + warp; item < items;
-       item += static_cast<int64_t>(gridDim.x) * kQkWarps) {
-    const Share sh = share_of(p, item, Sq + Sk);
-    lane_angles(l, p.pos[sh.token]);
+  V4 c, s, dwa[2], dwb[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int lo = q == 0 ? sh.s0 : max(sh.s0, Sq) - Sq, hi = q == 0 ? min(sh.s1, Sq) : sh.s1 - Sq;
-      const T* x = static_cast<const T*>(p.x[q]) + sh.token * p.x_rs[q];
-      const T* dy = static_cast<const T*>(p.dy[q]) + sh.token * p.dy_rs[q];
-      T* dx = static_cast<T*>(p.y[q]) + sh.token * p.y_rs[q];
-      for (int s = lo; s < hi; s += kS) {
-        Pack<T, 4> in[kS][2], gi[kS][2];
+  for (int q = 0; q < 2; ++q) dwa[q] = dwb[q] = fill<4>(0.f);
+  int stage = 0, refill = D - 1, pos = p.pos[min(at.token, p.T - 1)];
+  // one group of the queries (Q 0) or keys
+  const auto group = [&](auto which) {
+    constexpr int q = decltype(which)::value;
+    const bool on = l.un.on && at.head + l.sub < p.H[q];
+    const T* row = reinterpret_cast<const T*>(ring + stage * kStage) + l.sub * G * 8;
+    const T* grow = reinterpret_cast<const T*>(ring + stage * kStage + kHalf) + l.sub * G * 8;
+    V4 xa = fill<4>(0.f), xb = xa, ya = xa, yb = xa;
+    if (on) {
+      to_pairs<IL>(wide_of(load_pack<T, 4>(row + l.un.a)), wide_of(load_pack<T, 4>(row + l.un.b)), xa, xb);
+      to_pairs<IL>(wide_of(load_pack<T, 4>(grow + l.un.a)), wide_of(load_pack<T, 4>(grow + l.un.b)), ya, yb);
+    }
+    V4 ms;
 #pragma unroll
-        for (int i = 0; i < kS; ++i) {
-          const int h = (s + i) * per + sub;
-          if (s + i < hi && un.on && h < p.H[q]) {
-            in[i][0] = load_pack<T, 4>(x + h * p.x_hs[q] + un.a);
-            in[i][1] = load_pack<T, 4>(x + h * p.x_hs[q] + un.b);
-            gi[i][0] = load_pack<T, 4>(dy + h * p.dy_hs[q] + un.a);
-            gi[i][1] = load_pack<T, 4>(dy + h * p.dy_hs[q] + un.b);
-          } else {
+    for (int j = 0; j < 4; ++j) ms[j] = -s[j];
+    const V4 ga = fma(yb, s, mul(ya, c)), gb = fma(ya, ms, mul(yb, c));  // turned back
+    const V4 ua = mul(ga, l.wa[q]), ub = mul(gb, l.wb[q]);
+    float sum[2] = {across(fma(xb, xb, mul(xa, xa))), across(fma(ub, xb, mul(ua, xa)))};  // of x^2 and of g w x
+    group_sum(sum, G);
+    __syncwarp();  // the stage is written again
+    const float r = rsqrtf(fmaf(sum[0], inv_d, p.eps));
+    const V4 rr = fill<4>(r), m = fill<4>(-sum[1] * inv_d * r * r);  // x m = -n mean(g w n) / r
+    dwa[q] = fma(ga, mul(xa, rr), dwa[q]);                   // (zeros where the lane has no head)
+    dwb[q] = fma(gb, mul(xb, rr), dwb[q]);
+    if (on) {
+      V4 first4, second4;
+      to_pieces<IL>(mul(fma(xa, m, ua), rr), mul(fma(xb, m, ub), rr), first4, second4);
+      T* dx = const_cast<T*>(at.at[0]);
+      store_pack(dx + l.un.a, narrow<T, 4>(first4));
+      store_pack(dx + l.un.b, narrow<T, 4>(second4));
+    }
+  };
+  for (int i = 0; i < mine; ++i) {
+    issue(i + D - 1, refill);
+    if (i == 0 || (at.head == 0 && at.q == 0)) {
+      l.angles(pos, c, s);
+      pos = p.pos[min(at.token + 1, p.T - 1)];  // the next token's
+    }
+    copy_wait<D - 1>();
+    __syncwarp();
+    if (at.q == 0) group(std::integral_constant<int, 0>{});
+    else group(std::integral_constant<int, 1>{});
+    at.next(out, p.H[0], p.H[1], l.sub, l.per, 0);
+    stage = stage + 1 == D ? 0 : stage + 1;
+    refill = refill + 1 == D ? 0 : refill + 1;
+  }
+  if (!p.part) return;
+  copy_wait<0>();
+  __syncthreads();  // the rings become the warps' sums
+  float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              in[i][0].set(j, 0.f), in[i][1].set(j, 0.f), gi[i][0].set(j, 0.f), gi[i][1].set(j, 0.f);
-          }
-        }
-        float sum[2 * kS], g[kS][8];  // sums of x^2 and of g w x
+  for (int q = 0; q < 2; ++q) {
+    V4 first4, second4;
+    to_pieces<IL>(dwa[q], dwb[q], first4, second4);
 #pragma unroll
-        for (int i = 0; i < kS; ++i) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[i][j] = gi[i][j >> 2][j & 3];
-          rotate<IL, true>(g[i], l);
-          sum[2 * i] = sum[2 * i + 1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = in[i][j >> 2][j & 3];
-            sum[2 * i] = fmaf(v, v, sum[2 * i]);
-            sum[2 * i + 1] = fmaf(g[i][j] * w[q][j], v, sum[2 * i + 1]);
-          }
-        }
-        group_sum(sum, p.G);
-#pragma unroll
-        for (int i = 0; i < kS; ++i) {
-          const int h = (s + i) * per + sub;
-          if (!(s + i < hi && un.on && h < p.H[q])) continue;
-          const float r = rsqrtf(fmaf(sum[2 * i], inv_d, p.eps));
-          const float m = sum[2 * i + 1] * inv_d * r * r;  // mean(g w n) / |x| of a unit r: x m = n mean(g w n)
-          Pack<T, 4> out[2];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = in[i][j >> 2][j & 3];
-            dw[q][j] = fmaf(g[i][j], v * r, dw[q][j]);
-            out[j >> 2].set(j & 3, r * (g[i][j] * w[q][j] - v * m));
-          }
-          store_pack(dx + h * p.y_hs[q] + un.a, out[0]);
-          store_pack(dx + h * p.y_hs[q] + un.b, out[1]);
-        }
+    for (int j = 0; j < 4; ++j) {
+      for (int o = G; o < 32; o <<= 1) {
+        first4[j] += __shfl_xor_sync(0xffffffffu, first4[j], o);
+        second4[j] += __shfl_xor_sync(0xffffffffu, second4[j], o);
+      }
+      if (l.sub == 0 && l.un.on) {
+        sums[(warp * 2 + q) * kQkMaxDim + l.un.a + j] = first4[j];
+        sums[(warp * 2 + q) * kQkMaxDim + l.un.b + j] = second4[j];
       }
     }
   }
-  if (!p.part) return;
-  __shared__ float sh_dw[kQkWarps][2 * kQkMaxDim];
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      for (int o = p.G; o < 32; o <<= 1) dw[q][j] += __shfl_xor_sync(0xffffffffu, dw[q][j], o);
-      if (sub == 0 && un.on) sh_dw[warp][q * p.d + (j < 4 ? un.a : un.b - 4) + j] = dw[q][j];
-    }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.d; i += kQkThreads) {
+    const int q = i >= p.d;
     float a = 0.f;
-    for (int v = 0; v < kQkWarps; ++v) a += sh_dw[v][i];
+    for (int v = 0; v < kQkWarps; ++v) a += sums[(v * 2 + q) * kQkMaxDim + i - q * p.d];
     p.part[static_cast<int64_t>(blockIdx.x) * 2 * p.d + i] = a;
   }
 }
@@ -298,55 +409,54 @@ __global__ void __launch_bounds__(1024) qk_norm_join_kernel(const QkParams p, in
 
 namespace {
 
-int qk_sms() {
+// Sets the lanes a head takes; returns the blocks: every one that fits, or as many as have a group for each warp.
+int qk_shape(QkParams& p, int per_sm) {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return std::max(sms, 1);
-}
-
-// Lanes per head, and the pieces a token's heads are cut into: one warp a token unless that leaves most
-// of the GPU without work.
-void qk_shape(QkParams& p, int sms) {
   p.G = 1;
   while (8 * p.G < p.d) p.G *= 2;
   const int per = 32 / p.G;
-  const int steps = (p.H[0] + per - 1) / per + (p.H[1] + per - 1) / per;
-  const int64_t want = static_cast<int64_t>(sms) * kQkWarps * 2;
-  p.chunks = static_cast<int>(std::min<int64_t>(steps, std::max<int64_t>(1, want / std::max(p.T, 1))));
+  const int64_t groups = static_cast<int64_t>(p.T) * ((p.H[0] + per - 1) / per + (p.H[1] + per - 1) / per);
+  const int64_t fit = static_cast<int64_t>(std::max(sms, 1)) * per_sm;
+  return static_cast<int>(std::min<int64_t>({(groups + kQkWarps - 1) / kQkWarps, fit, kQkMaxBlocks}));
+}
+
+template <class T, bool IL>
+cudaError_t run_fwd(const QkParams& p, int blocks, cudaStream_t st) {  // (heads of 72 .. 128: sums without a loop)
+  return p.G == 16 ? launch_pdl(qk_norm_fwd_kernel<T, IL, 16>, dim3(blocks), dim3(kQkThreads), 0, st, p)
+                   : launch_pdl(qk_norm_fwd_kernel<T, IL, 0>, dim3(blocks), dim3(kQkThreads), 0, st, p);
+}
+
+template <class T, bool IL, int GT>
+cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
+  static_assert(kBwdRing >= 2 * kQkMaxDim * sizeof(float), "a warp's ring holds its sums");
+  const auto kernel = qk_norm_bwd_kernel<T, IL, GT>;
+  constexpr int smem = kQkWarps * kBwdRing;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(blocks), dim3(kQkThreads), smem, st, p);
+}
+template <class T, bool IL>
+cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
+  return p.G == 16 ? run_bwd<T, IL, 16>(p, blocks, st) : run_bwd<T, IL, 0>(p, blocks, st);
 }
 
 }  // namespace
 
-
 size_t qk_norm_bwd_workspace(int d) { return static_cast<size_t>(kQkMaxBlocks) * 2 * d * sizeof(float); }
 
 cudaError_t launch_qk_norm_fwd(QkParams p, int bf16, cudaStream_t st) {
-  const int sms = qk_sms();
-  qk_shape(p, sms);
-  const int64_t items = static_cast<int64_t>(p.T) * p.chunks;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + kQkWarps - 1) / kQkWarps, sms * 8)));
-  if (bf16)
-    return p.interleaved ? launch_pdl(qk_norm_fwd_kernel<__nv_bfloat16, true>, grid, dim3(kQkThreads), 0, st, p)
-                         : launch_pdl(qk_norm_fwd_kernel<__nv_bfloat16, false>, grid, dim3(kQkThreads), 0, st, p);
-  return p.interleaved ? launch_pdl(qk_norm_fwd_kernel<float, true>, grid, dim3(kQkThreads), 0, st, p)
-                       : launch_pdl(qk_norm_fwd_kernel<float, false>, grid, dim3(kQkThreads), 0, st, p);
+  const int blocks = qk_shape(p, kFwdBlocks);
+  if (bf16) return p.interleaved ? run_fwd<__nv_bfloat16, true>(p, blocks, st) : run_fwd<__nv_bfloat16, false>(p, blocks, st);
+  return p.interleaved ? run_fwd<float, true>(p, blocks, st) : run_fwd<float, false>(p, blocks, st);
 }
 
 // stage 0: the rows' gradients and the blocks' weight gradients, 1: their sum.
 cudaError_t launch_qk_norm_bwd(int stage, QkParams p, int bf16, cudaStream_t st) {
-  const int sms = qk_sms();
-  qk_shape(p, sms);
-  const int64_t items = static_cast<int64_t>(p.T) * p.chunks;
-  const int blocks = static_cast<int>(
-      std::min<int64_t>({(items + kQkWarps - 1) / kQkWarps, static_cast<int64_t>(sms) * 2, kQkMaxBlocks}));
+  const int blocks = qk_shape(p, kBwdBlocks);
   if (stage == 1) return launch_pdl(qk_norm_join_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st, p, blocks);
-  const dim3 grid(blocks);
-  if (bf16)
-    return p.interleaved ? launch_pdl(qk_norm_bwd_kernel<__nv_bfloat16, true>, grid, dim3(kQkThreads), 0, st, p)
-                         : launch_pdl(qk_norm_bwd_kernel<__nv_bfloat16, false>, grid, dim3(kQkThreads), 0, st, p);
-  return p.interleaved ? launch_pdl(qk_norm_bwd_kernel<float, true>, grid, dim3(kQkThreads), 0, st, p)
-                       : launch_pdl(qk_norm_bwd_kernel<float, false>, grid, dim3(kQkThreads), 0, st, p);
+  if (bf16) return p.interleaved ? run_bwd<__nv_bfloat16, true>(p, blocks, st) : run_bwd<__nv_bfloat16, false>(p, blocks, st);
+  return p.interleaved ? run_bwd<float, true>(p, blocks, st) : run_bwd<float, false>(p, blocks, st);
 }
 
 }  // namespace va

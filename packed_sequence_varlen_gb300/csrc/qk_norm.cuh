@@ -22,7 +22,7 @@ struct QkParams {
   float* part;            // [blocks][2][d], null when no weight gradient is wanted
   int T, H[2], d, rot, w_bf16, interleaved;
   float eps;
-  int G, chunks;          // set by the launchers: lanes per head, pieces of a token's heads
+  int G;                  // set by the launchers: lanes per head
 };
 
 size_t qk_norm_bwd_workspace(int d);

@@ -32,8 +32,8 @@ namespace va {
 namespace {
 
 constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
-constexpr int kFwdRing = 6144, kBwdRing = 8192;  // bytes a warp has on their way
-constexpr int kFwdBlocks = 3, kBwdBlocks = 2;    // blocks an SM
+constexpr int kRing = 8192;  // bytes a warp has on their way
+constexpr int kBlocks = 2;   // blocks an SM (three with 80 registers: forward 66 us instead of 62)
 
 using V4 = Vec<4>;
 
@@ -193,11 +193,12 @@ struct LaneState {
 
 // GT: lanes per head, 0: as the call says.
 template <class T, bool IL, int GT>
-__global__ void __launch_bounds__(kQkThreads, kFwdBlocks) qk_norm_fwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kBlocks) qk_norm_fwd_kernel(QkParams p) {
   griddep_begin();
-  constexpr int kPiece = 8 * sizeof(T), kStage = 32 * kPiece, D = kFwdRing / kStage;
-  __shared__ __align__(16) uint8_t ring[kQkWarps][D][kStage];
+  constexpr int kPiece = 8 * sizeof(T), kStage = 32 * kPiece, D = kRing / kStage;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* const ring = smem + warp * kRing;
   const int G = GT ? GT : p.G;
   const LaneState<IL> l(p, G);
   const int64_t all = static_cast<int64_t>(p.T) * l.groups, warps = static_cast<int64_t>(gridDim.x) * kQkWarps;
@@ -210,24 +211,24 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocks) qk_norm_fwd_kernel(con
   Cursor<T, 1> ask = l.template place<T, 1>(first), at = ask;
   ask.begin(in, l.sub, l.per, 8 * u);
   at.begin(out, l.sub, l.per, 0);
-  uint8_t* const mine_ring = &ring[warp][0][(l.sub * G + u) * kPiece];
-  const auto issue = [&](int i, int stage) {
+  uint8_t* const mine_ring = ring + (l.sub * G + u) * kPiece;
+  const auto issue = [&](int i, int to) {
     if (i < mine) {
       if (l.un.on && ask.head + l.sub < (ask.q ? p.H[1] : p.H[0])) {
 #pragma unroll
-        for (int k = 0; k < kPiece / 16; ++k) copy16(mine_ring + stage * kStage + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
+        for (int k = 0; k < kPiece / 16; ++k) copy16(mine_ring + to + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
       }
       ask.next(in, p.H[0], p.H[1], l.sub, l.per, 8 * u);
     }
     copy_commit();
   };
 #pragma unroll
-  for (int i = 0; i < D - 1; ++i) issue(i, i);
+  for (int i = 0; i < D - 1; ++i) issue(i, i * kStage);
   const float inv_d = 1.f / static_cast<float>(p.d);
   V4 c, s, ca, sb, cb, sa;  // the token's, and with the weights: y_a = r (x_a ca - x_b sb), y_b = r (x_b cb + x_a sa)
-  int stage = 0, refill = D - 1, pos = p.pos[min(at.token, p.T - 1)];
+  int here = 0, pos = p.pos[min(at.token, p.T - 1)];
   for (int i = 0; i < mine; ++i) {
-    issue(i + D - 1, refill);
+    issue(i + D - 1, (here - kStage) & (kRing - 1));
     if (i == 0 || at.head == 0) {
       if (i == 0 || at.q == 0) {
         l.angles(pos, c, s);
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocks) qk_norm_fwd_kernel(con
     copy_wait<D - 1>();
     __syncwarp();
     const bool on = l.un.on && at.head + l.sub < (at.q ? p.H[1] : p.H[0]);
-    const T* row = reinterpret_cast<const T*>(ring[warp][stage]) + l.sub * G * 8;
+    const T* row = reinterpret_cast<const T*>(ring + here) + l.sub * G * 8;
     V4 xa = fill<4>(0.f), xb = xa;
     if (on) to_pairs<IL>(wide_of(load_pack<T, 4>(row + l.un.a)), wide_of(load_pack<T, 4>(row + l.un.b)), xa, xb);
     float ss[1] = {across(fma(xb, xb, mul(xa, xa)))};
@@ -262,18 +263,17 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocks) qk_norm_fwd_kernel(con
       store_pack(y + l.un.b, narrow<T, 4>(second4));
     }
     at.next(out, p.H[0], p.H[1], l.sub, l.per, 0);
-    stage = stage + 1 == D ? 0 : stage + 1;
-    refill = refill + 1 == D ? 0 : refill + 1;
+    here = (here + kStage) & (kRing - 1);
   }
 }
 
 template <class T, bool IL, int GT>
-__global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kBlocks) qk_norm_bwd_kernel(QkParams p) {
   griddep_begin();
-  constexpr int kPiece = 8 * sizeof(T), kHalf = 32 * kPiece, kStage = 2 * kHalf, D = kBwdRing / kStage;  // x, then dy
+  constexpr int kPiece = 8 * sizeof(T), kHalf = 32 * kPiece, kStage = 2 * kHalf, D = kRing / kStage;  // x, then dy
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint8_t* const ring = smem + warp * kBwdRing;
+  uint8_t* const ring = smem + warp * kRing;
   const int G = GT ? GT : p.G;
   const LaneState<IL> l(p, G);
   const int64_t all = static_cast<int64_t>(p.T) * l.groups, warps = static_cast<int64_t>(gridDim.x) * kQkWarps;
@@ -291,13 +291,13 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(con
   ask.begin(in, l.sub, l.per, 8 * u);
   at.begin(out, l.sub, l.per, 0);
   uint8_t* const mine_ring = ring + (l.sub * G + u) * kPiece;
-  const auto issue = [&](int i, int stage) {
+  const auto issue = [&](int i, int to) {
     if (i < mine) {
       if (l.un.on && ask.head + l.sub < (ask.q ? p.H[1] : p.H[0])) {
 #pragma unroll
         for (int k = 0; k < kPiece / 16; ++k) {
-          copy16(mine_ring + stage * kStage + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
-          copy16(mine_ring + stage * kStage + kHalf + 16 * k, ask.at[1] + 16 / sizeof(T) * k);
+          copy16(mine_ring + to + 16 * k, ask.at[0] + 16 / sizeof(T) * k);
+          copy16(mine_ring + to + kHalf + 16 * k, ask.at[1] + 16 / sizeof(T) * k);
         }
       }
       ask.next(in, p.H[0], p.H[1], l.sub, l.per, 8 * u);
@@ -305,18 +305,18 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(con
     copy_commit();
   };
 #pragma unroll
-  for (int i = 0; i < D - 1; ++i) issue(i, i);
+  for (int i = 0; i < D - 1; ++i) issue(i, i * kStage);
   const float inv_d = 1.f / static_cast<float>(p.d);
   V4 c, s, dwa[2], dwb[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) dwa[q] = dwb[q] = fill<4>(0.f);
-  int stage = 0, refill = D - 1, pos = p.pos[min(at.token, p.T - 1)];
+  int here = 0, pos = p.pos[min(at.token, p.T - 1)];
   // one group of the queries (Q 0) or keys
   const auto group = [&](auto which) {
     constexpr int q = decltype(which)::value;
     const bool on = l.un.on && at.head + l.sub < p.H[q];
-    const T* row = reinterpret_cast<const T*>(ring + stage * kStage) + l.sub * G * 8;
-    const T* grow = reinterpret_cast<const T*>(ring + stage * kStage + kHalf) + l.sub * G * 8;
+    const T* row = reinterpret_cast<const T*>(ring + here) + l.sub * G * 8;
+    const T* grow = reinterpret_cast<const T*>(ring + here + kHalf) + l.sub * G * 8;
     V4 xa = fill<4>(0.f), xb = xa, ya = xa, yb = xa;
     if (on) {
       to_pairs<IL>(wide_of(load_pack<T, 4>(row + l.un.a)), wide_of(load_pack<T, 4>(row + l.un.b)), xa, xb);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(con
     }
   };
   for (int i = 0; i < mine; ++i) {
-    issue(i + D - 1, refill);
+    issue(i + D - 1, (here - kStage) & (kRing - 1));
     if (i == 0 || (at.head == 0 && at.q == 0)) {
       l.angles(pos, c, s);
       pos = p.pos[min(at.token + 1, p.T - 1)];  // the next token's
@@ -353,8 +353,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks) qk_norm_bwd_kernel(con
     if (at.q == 0) group(std::integral_constant<int, 0>{});
     else group(std::integral_constant<int, 1>{});
     at.next(out, p.H[0], p.H[1], l.sub, l.per, 0);
-    stage = stage + 1 == D ? 0 : stage + 1;
-    refill = refill + 1 == D ? 0 : refill + 1;
+    here = (here + kStage) & (kRing - 1);
   }
   if (!p.part) return;
   copy_wait<0>();
@@ -422,23 +421,23 @@ int qk_shape(QkParams& p, int per_sm) {
   return static_cast<int>(std::min<int64_t>({(groups + kQkWarps - 1) / kQkWarps, fit, kQkMaxBlocks}));
 }
 
-template <class T, bool IL>
-cudaError_t run_fwd(const QkParams& p, int blocks, cudaStream_t st) {  // (heads of 72 .. 128: sums without a loop)
-  return p.G == 16 ? launch_pdl(qk_norm_fwd_kernel<T, IL, 16>, dim3(blocks), dim3(kQkThreads), 0, st, p)
-                   : launch_pdl(qk_norm_fwd_kernel<T, IL, 0>, dim3(blocks), dim3(kQkThreads), 0, st, p);
-}
-
-template <class T, bool IL, int GT>
-cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
-  static_assert(kBwdRing >= 2 * kQkMaxDim * sizeof(float), "a warp's ring holds its sums");
-  const auto kernel = qk_norm_bwd_kernel<T, IL, GT>;
-  constexpr int smem = kQkWarps * kBwdRing;
+cudaError_t launch_rings(void (*kernel)(QkParams), const QkParams& p, int blocks, cudaStream_t st) {
+  constexpr int smem = kQkWarps * kRing;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e != cudaSuccess ? e : launch_pdl(kernel, dim3(blocks), dim3(kQkThreads), smem, st, p);
 }
+
+template <class T, bool IL>
+cudaError_t run_fwd(const QkParams& p, int blocks, cudaStream_t st) {  // (heads of 72 .. 128: sums without a loop)
+  return p.G == 16 ? launch_rings(qk_norm_fwd_kernel<T, IL, 16>, p, blocks, st)
+                   : launch_rings(qk_norm_fwd_kernel<T, IL, 0>, p, blocks, st);
+}
+
 template <class T, bool IL>
 cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
-  return p.G == 16 ? run_bwd<T, IL, 16>(p, blocks, st) : run_bwd<T, IL, 0>(p, blocks, st);
+  static_assert(kRing >= 2 * kQkMaxDim * sizeof(float), "a warp's ring holds its sums");
+  return p.G == 16 ? launch_rings(qk_norm_bwd_kernel<T, IL, 16>, p, blocks, st)
+                   : launch_rings(qk_norm_bwd_kernel<T, IL, 0>, p, blocks, st);
 }
 
 }  // namespace
@@ -446,14 +445,14 @@ cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
 size_t qk_norm_bwd_workspace(int d) { return static_cast<size_t>(kQkMaxBlocks) * 2 * d * sizeof(float); }
 
 cudaError_t launch_qk_norm_fwd(QkParams p, int bf16, cudaStream_t st) {
-  const int blocks = qk_shape(p, kFwdBlocks);
+  const int blocks = qk_shape(p, kBlocks);
   if (bf16) return p.interleaved ? run_fwd<__nv_bfloat16, true>(p, blocks, st) : run_fwd<__nv_bfloat16, false>(p, blocks, st);
   return p.interleaved ? run_fwd<float, true>(p, blocks, st) : run_fwd<float, false>(p, blocks, st);
 }
 
 // stage 0: the rows' gradients and the blocks' weight gradients, 1: their sum.
 cudaError_t launch_qk_norm_bwd(int stage, QkParams p, int bf16, cudaStream_t st) {
-  const int blocks = qk_shape(p, kBwdBlocks);
+  const int blocks = qk_shape(p, kBlocks);
   if (stage == 1) return launch_pdl(qk_norm_join_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st, p, blocks);
   if (bf16) return p.interleaved ? run_bwd<__nv_bfloat16, true>(p, blocks, st) : run_bwd<__nv_bfloat16, false>(p, blocks, st);
   return p.interleaved ? run_bwd<float, true>(p, blocks, st) : run_bwd<float, false>(p, blocks, st);

@@ -64,6 +64,18 @@ def _on(dev: torch.device):
     return contextlib.nullcontext() if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
+def _call(dev: torch.device, fn, *args):
+    """Calls a library function (the stream is its last argument) with ``dev`` current."""
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status)
+
+
 # ----------------------------------------------------------------- host planner
 
 def _pack(fn, lengths, capacity: int):
@@ -447,7 +459,8 @@ def _same_device(dev, **tensors):
 
 def _row_stride(t: torch.Tensor) -> int:
     """Elements between rows of a 2-D tensor (one row: any stride is right)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    n, m = t.shape
+    return t.stride(0) if n > 1 else max(m, 1)
 
 
 def token_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
@@ -621,40 +634,42 @@ def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None):
 def _head_strides(t: torch.Tensor):
     """Row and head strides; those of an extent of one are never used and may be anything."""
     T, H, d = t.shape
-    hs = t.stride(1) if H > 1 else d
-    return (t.stride(0) if T > 1 else H * hs), hs
+    rs, hs, _ = t.stride()
+    if H <= 1:
+        hs = d
+    return (rs if T > 1 else H * hs), hs
 
 
-def _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved):
+def _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved, qo_strides, ko_strides):
+    """The checked call's shape; output strides None: contiguous."""
     _check_heads("q", q)
     _check_heads("k", k)
     T, Hq, d = q.shape
+    Tk, Hkv, dk = k.shape
     dev = q.device
-    if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype:
+    if Tk != T or dk != d or k.dtype != q.dtype:
         raise ValueError("q [T, Hq, d] and k [T, Hkv, d] must agree in T, d and dtype")
-    _check_sizes(T=T)
+    if T >= 2 ** 30:
+        _check_sizes(T=T)
     if position_ids.shape != (T,) or position_ids.dtype != torch.int32 or not position_ids.is_contiguous():
         raise ValueError("position_ids must be a contiguous int32 [T] tensor")
-    s = VaQkShape()
+    weight_dtype = 0
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is None:
             continue
         if w.shape != (d,) or w.dtype not in _FLOATS or not w.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32/bf16 [d] tensor")
-        s.weight_dtype = int(w.dtype == torch.bfloat16)
+        weight_dtype = 1 if w.dtype == torch.bfloat16 else 0
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise ValueError("q_weight and k_weight must have one dtype")
     rot = 0
     if inv_freq is not None:
         if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous fp32 [rot / 2] tensor")
-        rot = 2 * inv_freq.numel()
+        rot = 2 * inv_freq.shape[0]
     _same_device(dev, k=k, position_ids=position_ids, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq)
-    s.T, s.Hq, s.Hkv, s.d, s.rot = T, Hq, k.shape[1], d, rot
-    s.dtype, s.interleaved = int(q.dtype == torch.bfloat16), int(bool(interleaved))
-    s.q_row_stride, s.q_head_stride = _head_strides(q)
-    s.k_row_stride, s.k_head_stride = _head_strides(k)
-    return s
+    return VaQkShape(T, Hq, Hkv, d, rot, 1 if q.dtype == torch.bfloat16 else 0, weight_dtype, 1 if interleaved else 0,
+                     *_head_strides(q), *_head_strides(k), *(qo_strides or (Hq * d, d)), *(ko_strides or (Hkv * d, d)))
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tensor,
@@ -667,19 +682,21 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tenso
     ``k_weight`` [d] fp32 or bf16 (None: ones); ``inv_freq`` fp32 [rot / 2]: the first rot elements of a head
     are turned by position * inv_freq, in pairs (i, i + rot / 2) or, ``interleaved``, (2 i, 2 i + 1)
     (None: none is).  ``q_out`` / ``k_out`` None allocates them contiguous; q and k themselves are fine."""
-    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved)
+    qs = ks = None
+    if q_out is not None:
+        _check_heads("q_out", q_out, q)
+        qs = _head_strides(q_out)
+    if k_out is not None:
+        _check_heads("k_out", k_out, k)
+        ks = _head_strides(k_out)
+    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved, qs, ks)
+    dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _check_heads("q_out", q_out, q)
-    _check_heads("k_out", k_out, k)
-    s.qo_row_stride, s.qo_head_stride = _head_strides(q_out)
-    s.ko_row_stride, s.ko_head_stride = _head_strides(k_out)
-    with _on(q.device):
-        check(_lib.load().varlen_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(position_ids), _ptr(q_weight), _ptr(k_weight),
-                                                  _ptr(inv_freq), ctypes.byref(s), float(eps), _ptr(q_out),
-                                                  _ptr(k_out), _stream(q.device)))
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    _call(dev, _lib.load().varlen_qk_norm_rope_fwd, q.data_ptr(), k.data_ptr(), position_ids.data_ptr(),
+          _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), ctypes.byref(s), eps, q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -691,33 +708,37 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     """Gradient of ``qk_norm_rope_fwd``: returns (dq, dk, dq_weight, dk_weight), a weight's None where it is.
     ``dq`` / ``dk`` None allocates them contiguous; views of a fused gradient are fine.  The weights'
     gradients are summed in fp32 in a fixed order (deterministic) and have the weights' dtype."""
-    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved)
     _check_heads("dq_out", dq_out, q)
     _check_heads("dk_out", dk_out, k)
+    s = _qk_shape(q, k, q_weight, k_weight, position_ids, inv_freq, interleaved, _head_strides(dq_out),
+                  _head_strides(dk_out))
+    dev, d = q.device, s.d
+    qs, ks = (s.Hq * d, d), (s.Hkv * d, d)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _check_heads("dq", dq, q)
+        qs = _head_strides(dq)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _check_heads("dq", dq, q)
-    _check_heads("dk", dk, k)
-    s.qo_row_stride, s.qo_head_stride = _head_strides(dq_out)
-    s.ko_row_stride, s.ko_head_stride = _head_strides(dk_out)
-    gs = VaQkGradStrides(*_head_strides(dq), *_head_strides(dk))
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    else:
+        _check_heads("dk", dk, k)
+        ks = _head_strides(dk)
+    gs = VaQkGradStrides(*qs, *ks)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     lib = _lib.load()
     size = 0
     if dqw is not None or dkw is not None:
-        need = lib.varlen_qk_norm_rope_bwd_workspace_size(s.d)
+        need = lib.varlen_qk_norm_rope_bwd_workspace_size(d)
         if workspace is None or workspace.numel() < need:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        _same_device(q.device, workspace=workspace)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _same_device(dev, workspace=workspace)
         size = workspace.numel()
-    with _on(q.device):
-        check(lib.varlen_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(position_ids),
-                                          _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), ctypes.byref(s),
-                                          ctypes.byref(gs), float(eps), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw),
-                                          _ptr(workspace), size, _stream(q.device)))
+    _call(dev, lib.varlen_qk_norm_rope_bwd, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+          position_ids.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), ctypes.byref(s), ctypes.byref(gs), eps,
+          dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw), _ptr(workspace), size)
     return dq, dk, dqw, dkw
 
 
@@ -746,35 +767,30 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tensor, q
 
 # ----------------------------------------------------------------- gated recurrence
 
-def _scan_shape(x, log_decay, cu_seqlens, name="x"):
+def _check_scan(name, x, log_decay, cu_seqlens):
     _check_rows(name, x)
     _check_rows("log_decay", log_decay)
     T, D = x.shape
     if log_decay.shape != x.shape:
         raise ValueError(f"log_decay must have {name}'s shape")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32 or \
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2 or cu_seqlens.dtype != torch.int32 or \
             not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 [B + 1] tensor")
-    _check_sizes(T=T, D=D)
+    if T >= 2 ** 30 or D >= 2 ** 30:
+        _check_sizes(T=T, D=D)
     _same_device(x.device, log_decay=log_decay, cu_seqlens=cu_seqlens)
-    s = VaScanShape()
-    s.T, s.B, s.D = T, cu_seqlens.numel() - 1, D
-    s.gate_dtype, s.gate_row_stride = int(log_decay.dtype == torch.bfloat16), _row_stride(log_decay)
-    return s
+    return T, cu_seqlens.shape[0] - 1, D
 
 
-def _check_state(name: str, t, s: VaScanShape, dev):
-    if t is None:
-        return
-    if t.dtype != torch.float32 or t.shape != (s.B, s.D) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous fp32 [B, D] tensor")
-    _same_device(dev, **{name: t})
+def _check_state(name: str, t, B: int, D: int, dev):
+    if t.dtype != torch.float32 or t.shape != (B, D) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous fp32 [B, D] tensor on {dev}")
 
 
-def _scan_workspace(lib, s: VaScanShape, workspace, dev):
-    need = lib.varlen_scan_workspace_size(s.T, s.B, s.D)
+def _scan_workspace(lib, T, B, D, workspace, dev):
+    need = lib.varlen_scan_workspace_size(T, B, D)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     _same_device(dev, workspace=workspace)
     return workspace
 
@@ -788,29 +804,31 @@ def varlen_scan_fwd(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.
     ``x`` and ``log_decay`` [T, D] CUDA fp32 or bf16 (fp32 x takes fp32 decays); h has the wider of the two
     types.  ``h_last`` True allocates the states after each segment ([B, D] fp32), a tensor receives
     them (``h0`` itself only for single tokens, T == B), False gives None."""
-    s = _scan_shape(x, log_decay, cu_seqlens)
+    T, B, D = _check_scan("x", x, log_decay, cu_seqlens)
     dev = x.device
-    s.x_dtype, s.x_row_stride = int(x.dtype == torch.bfloat16), _row_stride(x)
-    dt = torch.promote_types(x.dtype, log_decay.dtype)
+    xb, gb = x.dtype == torch.bfloat16, log_decay.dtype == torch.bfloat16
+    dt = torch.bfloat16 if xb and gb else torch.float32
     if out is None:
-        out = torch.empty(x.shape, dtype=dt, device=dev)
+        out, out_stride = torch.empty((T, D), dtype=dt, device=dev), max(D, 1)
     else:
         _check_rows("out", out)
         if out.shape != x.shape or out.dtype != dt:
             raise ValueError("out must be [T, D] in the wider type of x and log_decay")
         _same_device(dev, out=out)
-    s.h_row_stride = _row_stride(out)
+        out_stride = _row_stride(out)
+    if h0 is not None:
+        _check_state("h0", h0, B, D, dev)
     if h_last is True:
-        h_last = torch.empty((s.B, s.D), dtype=torch.float32, device=dev)
+        h_last = torch.empty((B, D), dtype=torch.float32, device=dev)
     elif h_last is False:
         h_last = None
-    _check_state("h0", h0, s, dev)
-    _check_state("h_last", h_last, s, dev)
+    if h_last is not None:
+        _check_state("h_last", h_last, B, D, dev)
+    s = VaScanShape(T, B, D, xb, gb, _row_stride(x), _row_stride(log_decay), out_stride)
     lib = _lib.load()
-    workspace = _scan_workspace(lib, s, workspace, dev)
-    with _on(dev):
-        check(lib.varlen_scan_fwd(_ptr(x), _ptr(log_decay), _ptr(cu_seqlens), ctypes.byref(s), _ptr(h0), _ptr(out),
-                                  _ptr(h_last), _ptr(workspace), workspace.numel(), _stream(dev)))
+    workspace = _scan_workspace(lib, T, B, D, workspace, dev)
+    _call(dev, lib.varlen_scan_fwd, x.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), ctypes.byref(s), _ptr(h0),
+          out.data_ptr(), _ptr(h_last), workspace.data_ptr(), workspace.numel())
     if check_status:
         _raise_status(workspace)
     return out, h_last
@@ -821,10 +839,10 @@ def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, 
                     x_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None,
                     dlog_decay: torch.Tensor | None = None, workspace=None, check_status=False):
     """Gradient of ``varlen_scan_fwd``: returns (dx, dlog_decay, dh0), dh0 None without ``h0``.  ``dh`` and the
-    forward's ``h`` share a dtype; ``x_dtype`` is dx's where dx is allocated (None: bf16 where dh is, or
-    where the forward's inputs were bf16 x with fp32 decays, pass it)."""
+    forward's ``h`` share a dtype.  ``x_dtype`` is the forward's x's, and dx's where dx is allocated; None
+    takes dh's (pass it for bf16 x with fp32 decays)."""
     _check_rows("h", h)
-    s = _scan_shape(dh, log_decay, cu_seqlens, "dh")
+    T, B, D = _check_scan("dh", dh, log_decay, cu_seqlens)
     dev = dh.device
     if h.shape != dh.shape or h.dtype != dh.dtype:
         raise ValueError("h must match dh in shape and dtype")
@@ -836,20 +854,21 @@ def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, 
     _check_rows("dlog_decay", dlog_decay)
     if dx.shape != dh.shape or dlog_decay.shape != dh.shape or dlog_decay.dtype != log_decay.dtype:
         raise ValueError("dx and dlog_decay must be [T, D], dlog_decay in log_decay's dtype")
-    if dh.dtype != torch.promote_types(dx.dtype, log_decay.dtype):
+    xb, gb = dx.dtype == torch.bfloat16, log_decay.dtype == torch.bfloat16
+    if dh.dtype != (torch.bfloat16 if xb and gb else torch.float32):
         raise ValueError("dh must have the wider type of dx and log_decay")
     _same_device(dev, h=h, dx=dx, dlog_decay=dlog_decay)
-    s.x_dtype, s.x_row_stride, s.h_row_stride = int(dx.dtype == torch.bfloat16), _row_stride(dx), _row_stride(h)
+    for name, t in (("h0", h0), ("dh_last", dh_last)):
+        if t is not None:
+            _check_state(name, t, B, D, dev)
+    s = VaScanShape(T, B, D, xb, gb, _row_stride(dx), _row_stride(log_decay), _row_stride(h))
     gs = VaScanGradStrides(_row_stride(dh), _row_stride(dx), _row_stride(dlog_decay))
-    _check_state("h0", h0, s, dev)
-    _check_state("dh_last", dh_last, s, dev)
     dh0 = None if h0 is None else torch.empty_like(h0)
     lib = _lib.load()
-    workspace = _scan_workspace(lib, s, workspace, dev)
-    with _on(dev):
-        check(lib.varlen_scan_bwd(_ptr(dh), _ptr(h), _ptr(log_decay), _ptr(cu_seqlens), ctypes.byref(s),
-                                  ctypes.byref(gs), _ptr(h0), _ptr(dh_last), _ptr(dx), _ptr(dlog_decay), _ptr(dh0),
-                                  _ptr(workspace), workspace.numel(), _stream(dev)))
+    workspace = _scan_workspace(lib, T, B, D, workspace, dev)
+    _call(dev, lib.varlen_scan_bwd, dh.data_ptr(), h.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(),
+          ctypes.byref(s), ctypes.byref(gs), _ptr(h0), _ptr(dh_last), dx.data_ptr(), dlog_decay.data_ptr(), _ptr(dh0),
+          workspace.data_ptr(), workspace.numel())
     if check_status:
         _raise_status(workspace)
     return dx, dlog_decay, dh0
@@ -885,7 +904,8 @@ def _check_logits(logits, tokens):
             (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA fp32/bf16 [T, V] tensor with a contiguous last dim")
     T, V = logits.shape
-    _check_sizes(T=T, V=V)
+    if T >= 2 ** 30 or V >= 2 ** 30:
+        _check_sizes(T=T, V=V)
     if tokens.shape != (T,) or tokens.dtype != torch.int32 or not tokens.is_contiguous():
         raise ValueError("tokens must be a contiguous int32 [T] tensor")
     _same_device(logits.device, tokens=tokens)
@@ -908,11 +928,9 @@ def token_logprobs_fwd(logits: torch.Tensor, tokens: torch.Tensor, top_k: int = 
         top = torch.empty((T, k), dtype=torch.float32, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
     at = out.data_ptr()
-    with _on(dev):
-        check(_lib.load().varlen_token_logprobs_fwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
-                                                    _row_stride(logits), _ptr(tokens), T, V, k, int(ignore_index),
-                                                    float(temperature), at, at + 4 * T, at + 8 * T, _ptr(ids),
-                                                    _ptr(top), _ptr(status), _stream(dev)))
+    _call(dev, _lib.load().varlen_token_logprobs_fwd, logits.data_ptr(), logits.dtype == torch.bfloat16,
+          _row_stride(logits), tokens.data_ptr(), T, V, k, ignore_index, temperature, at, at + 4 * T, at + 8 * T, _ptr(ids),
+          _ptr(top), _ptr(status))
     if check_status and int(status.item()) != 0:
         raise VarlenError(int(status.item()), "token_logprobs_fwd: a token is outside the vocabulary")
     logprob, entropy, lse = out.unbind(0)
@@ -944,11 +962,9 @@ def token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Te
     for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob), ("dentropy", dentropy)):
         _check_per_token(name, t, T, dev)
     _same_device(dev, grad=grad)
-    with _on(dev):
-        check(_lib.load().varlen_token_logprobs_bwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
-                                                    _row_stride(logits), _ptr(tokens), _ptr(lse), _ptr(entropy),
-                                                    _ptr(dlogprob), _ptr(dentropy), T, V, int(ignore_index),
-                                                    float(temperature), _ptr(grad), _row_stride(grad), _stream(dev)))
+    _call(dev, _lib.load().varlen_token_logprobs_bwd, logits.data_ptr(), logits.dtype == torch.bfloat16,
+          _row_stride(logits), tokens.data_ptr(), lse.data_ptr(), _ptr(entropy), dlogprob.data_ptr(), _ptr(dentropy), T, V,
+          ignore_index, temperature, grad.data_ptr(), _row_stride(grad))
     return grad
 
 

@@ -358,6 +358,12 @@ va_status varlen_test_stall_next_forward(int64_t wait_limit_ns);
  * One-shot.  Errors: VA_ERR_INVALID_ARG unless 1 ms <= wait_limit_ns <= 2 s. */
 va_status varlen_test_stall_next_distill(int64_t wait_limit_ns);
 
+/* The same for the next varlen_scan_fwd or varlen_scan_bwd call of this process that is not one of single
+ * tokens: the scan's first tile tells the others nothing, their waits give up after wait_limit_ns, the status word gets
+ * VA_ERR_TIMEOUT and the results are undefined; the context stays usable.  One-shot.  Errors: VA_ERR_INVALID_ARG
+ * unless 1 ms <= wait_limit_ns <= 2 s. */
+va_status varlen_test_stall_next_scan(int64_t wait_limit_ns);
+
 /* Copies the workspace status word to *status_host after synchronising the
  * stream.  VA_ERR_CUDA if the copy fails. */
 va_status varlen_read_status(const void* ws_dev, int32_t* status_host, va_stream_t stream);
@@ -615,7 +621,8 @@ size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D);
  *   h_dev       [T, D] out; may be x itself (same type and stride)
  *   h_last_dev  float [B, D] out: the state after each segment, or NULL; for single tokens (T == B) it may be h0
  *               itself, otherwise they must not overlap
- *   ws_dev / ws_bytes  workspace (>= varlen_scan_workspace_size, 16-byte aligned)
+ *   ws_dev / ws_bytes  workspace (>= varlen_scan_workspace_size, 16-byte aligned; single tokens need 256 bytes, or none:
+ *               NULL, 0 does not report bad boundaries)
  * States are fp32 from row to row, h is rounded when stored.  Nothing of a segment reaches another, non-finite
  * values included.  Results do not change from call to call.  T == B (every segment one token) is one launch.
  * Errors: VA_ERR_INVALID_ARG (1 <= B <= T < 2^30, 1 <= D <= 2^20, strides, alignment), VA_ERR_UNSUPPORTED,

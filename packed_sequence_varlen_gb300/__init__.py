@@ -826,9 +826,12 @@ def varlen_scan_fwd(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.
         _check_state("h_last", h_last, B, D, dev)
     s = VaScanShape(T, B, D, xb, gb, _row_stride(x), _row_stride(log_decay), out_stride)
     lib = _lib.load()
-    workspace = _scan_workspace(lib, T, B, D, workspace, dev)
+    if B != T or workspace is not None:
+        workspace = _scan_workspace(lib, T, B, D, workspace, dev)
+    elif check_status:  # single tokens need one for the status word only
+        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
     _call(dev, lib.varlen_scan_fwd, x.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), ctypes.byref(s), _ptr(h0),
-          out.data_ptr(), _ptr(h_last), workspace.data_ptr(), workspace.numel())
+          out.data_ptr(), _ptr(h_last), _ptr(workspace), 0 if workspace is None else workspace.numel())
     if check_status:
         _raise_status(workspace)
     return out, h_last

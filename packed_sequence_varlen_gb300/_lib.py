@@ -30,7 +30,7 @@ EXPORTS = (
     "varlen_unpad_index", "varlen_gather_rows",
     "varlen_attn_plan_window", "varlen_attn_fwd_window", "varlen_attn_bwd_window",
     "varlen_attn_workspace_size_cross", "varlen_attn_plan_cross", "varlen_attn_fwd_cross",
-    "varlen_attn_bwd_cross", "varlen_test_stall_next_forward", "varlen_test_stall_next_distill",
+    "varlen_attn_bwd_cross", "varlen_test_stall_next_forward", "varlen_test_stall_next_distill", "varlen_test_stall_next_scan",
     "varlen_attn_workspace_size_sinks", "varlen_attn_plan_sinks", "varlen_attn_fwd_sinks", "varlen_attn_bwd_sinks",
     "varlen_token_distill_workspace_size", "varlen_token_distill",
     "varlen_embed_fwd", "varlen_embed_bwd_workspace_size", "varlen_embed_bwd",
@@ -175,6 +175,7 @@ def _declare(lib):
         "varlen_launch_count": (c_int64, []),
         "varlen_test_stall_next_forward": (c_int32, [c_int64]),
         "varlen_test_stall_next_distill": (c_int32, [c_int64]),
+        "varlen_test_stall_next_scan": (c_int32, [c_int64]),
         "varlen_last_error": (c_char_p, []),
         "varlen_version": (c_char_p, []),
     }

@@ -52,8 +52,8 @@ cudaError_t launch_sink_join(const BwdParams&, int, cudaStream_t);
 void bwd_tc_tiles(int*, int*, int*, int*);
 
 static thread_local std::string g_error;
-// Test hooks of the failure paths: a wait limit (ns) armed for the next forward or distillation, 0 = none.
-static std::atomic<long long> g_stall_next_fwd{0}, g_stall_next_distill{0};
+// Test hooks of the failure paths: a wait limit (ns) armed for the next forward, distillation or recurrence, 0 = none.
+static std::atomic<long long> g_stall_next_fwd{0}, g_stall_next_distill{0}, g_stall_next_scan{0};
 
 void set_error(const char* msg) { g_error = msg; }
 
@@ -951,10 +951,11 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && x < y + nb && y < x + na;
 }
 
-static va_status check_scan(const char* where, const va_scan_shape* s, const int32_t* cu, const void* ws,
-                            size_t ws_bytes) {
+// tokens: a forward of single tokens, which runs without a workspace too.
+static va_status check_scan(const char* where, const va_scan_shape* s, const int32_t* cu, const void* ws, size_t ws_bytes,
+                            bool tokens) {
   const std::string w(where);
-  if (!s || !cu || !ws) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
+  if (!s || !cu || (!ws && !(tokens && s->B == s->T))) return fail(VA_ERR_INVALID_ARG, w + ": null pointer");
   if (s->T < 1 || s->T >= (1 << 30) || s->B < 1 || s->B > s->T || s->D < 1 || s->D > (1 << 20))
     return fail(VA_ERR_INVALID_ARG, w + ": 1 <= B <= T < 2^30, 1 <= D <= 2^20");
   if (s->x_dtype < 0 || s->x_dtype > 1 || s->gate_dtype < 0 || s->gate_dtype > 1)
@@ -962,7 +963,8 @@ static va_status check_scan(const char* where, const va_scan_shape* s, const int
   if (s->x_dtype == 0 && s->gate_dtype == 1)
     return fail(VA_ERR_UNSUPPORTED, w + ": fp32 inputs take fp32 decays");
   if (!aligned16(ws)) return fail(VA_ERR_INVALID_ARG, w + ": workspace must be 16-byte aligned");
-  if (ws_bytes < varlen_scan_workspace_size(s->T, s->B, s->D)) return fail(VA_ERR_WORKSPACE, w + ": workspace too small");
+  const size_t need = tokens && s->B == s->T ? (ws ? sizeof(WsHeader) : 0) : varlen_scan_workspace_size(s->T, s->B, s->D);
+  if (ws_bytes < need) return fail(VA_ERR_WORKSPACE, w + ": workspace too small");
   return VA_OK;
 }
 
@@ -982,13 +984,13 @@ static va_status check_states(const char* where, std::initializer_list<const flo
 
 size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D) {
   if (T < 1 || T >= (1 << 30) || B < 1 || B > T || D < 1 || D > (1 << 20)) return 0;
-  return B == T ? std::max<size_t>(sizeof(WsHeader), scan_workspace(T, D)) : scan_workspace(T, D);
+  return scan_workspace(T, D);
 }
 
 va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const va_scan_shape* s, const float* h0,
                           void* h, float* h_last, void* ws, size_t ws_bytes, va_stream_t stream) {
   const char* where = "scan_fwd";
-  va_status st = check_scan(where, s, cu, ws, ws_bytes);
+  va_status st = check_scan(where, s, cu, ws, ws_bytes, true);
   const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
   if (st == VA_OK) st = check_scan_rows(where, s, x, s->x_row_stride, s->x_dtype);
   if (st == VA_OK) st = check_scan_rows(where, s, g, s->gate_row_stride, s->gate_dtype);
@@ -1009,6 +1011,7 @@ va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const
   if (s->B == s->T) {
     e = launch(K_SCAN_STEP, cs, [&] { return launch_scan_step(p, s->x_dtype, s->gate_dtype, ws, cs); });
   } else {
+    p.wait_ns = static_cast<uint64_t>(g_stall_next_scan.exchange(0));
     const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_FWD};
     for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
       e = launch(kid[stage], cs, [&] { return launch_scan_fwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
@@ -1021,7 +1024,7 @@ va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const in
                           float* dh0, void* ws, size_t ws_bytes, va_stream_t stream) {
   const char* where = "scan_bwd";
   if (!gs) return fail(VA_ERR_INVALID_ARG, "scan_bwd: null pointer");
-  va_status st = check_scan(where, s, cu, ws, ws_bytes);
+  va_status st = check_scan(where, s, cu, ws, ws_bytes, false);
   const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
   if (st == VA_OK) st = check_scan_rows(where, s, dh, gs->dh_row_stride, hb);
   if (st == VA_OK) st = check_scan_rows(where, s, h, s->h_row_stride, hb);
@@ -1041,6 +1044,7 @@ va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const in
   p.B = s->B, p.T = s->T, p.D = s->D;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  p.wait_ns = static_cast<uint64_t>(g_stall_next_scan.exchange(0));
   const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_BWD};
   for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
     e = launch(kid[stage], cs, [&] { return launch_scan_bwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
@@ -1181,6 +1185,13 @@ va_status varlen_test_stall_next_distill(int64_t wait_limit_ns) {
   if (wait_limit_ns < 1000000 || wait_limit_ns > 2000000000)
     return fail(VA_ERR_INVALID_ARG, "test_stall_next_distill: the limit must be 1 ms .. 2 s");
   g_stall_next_distill.store(wait_limit_ns);
+  return VA_OK;
+}
+
+va_status varlen_test_stall_next_scan(int64_t wait_limit_ns) {
+  if (wait_limit_ns < 1000000 || wait_limit_ns > 2000000000)
+    return fail(VA_ERR_INVALID_ARG, "test_stall_next_scan: the limit must be 1 ms .. 2 s");
+  g_stall_next_scan.store(wait_limit_ns);
   return VA_OK;
 }
 

@@ -1,5 +1,7 @@
 // Element access shared by the streaming kernels: fp32 or bf16 in memory, fp32 in registers.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace va {
@@ -50,6 +52,18 @@ template <class T, int N>
 __device__ __forceinline__ void store_pack_cs(T* p, const Pack<T, N>& v) {
   using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
   __stcs(reinterpret_cast<Wd*>(p), *reinterpret_cast<const Wd*>(&v));
+}
+
+// SMs of the current device (a device's number is asked for once).
+inline int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  sms = sms > 0 ? sms : 1;
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 }  // namespace va

@@ -609,13 +609,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) logprobs_bwd_kernel(con
 
 namespace {
 
-int device_sms() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return std::max(sms, 1);
-}
-
 template <class T, int NT>
 cudaError_t run_fwd(const LogprobParams& p, int sms, cudaStream_t st) {
   const auto kernel = logprobs_fwd_kernel<T, NT>;

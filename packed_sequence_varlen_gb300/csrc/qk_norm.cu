@@ -410,14 +410,11 @@ namespace {
 
 // Sets the lanes a head takes; returns the blocks: every one that fits, or as many as have a group for each warp.
 int qk_shape(QkParams& p, int per_sm) {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   p.G = 1;
   while (8 * p.G < p.d) p.G *= 2;
   const int per = 32 / p.G;
   const int64_t groups = static_cast<int64_t>(p.T) * ((p.H[0] + per - 1) / per + (p.H[1] + per - 1) / per);
-  const int64_t fit = static_cast<int64_t>(std::max(sms, 1)) * per_sm;
+  const int64_t fit = static_cast<int64_t>(device_sms()) * per_sm;
   return static_cast<int>(std::min<int64_t>({(groups + kQkWarps - 1) / kQkWarps, fit, kQkMaxBlocks}));
 }
 

@@ -100,7 +100,7 @@ __device__ __forceinline__ bool there(const float (&v)[N]) {
 
 // Waits until the N words of every lane that asks are there (a warp's call); false when the call is to be given up.
 template <int N>
-__device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], WsHeader* hdr) {
+__device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], const ScanParams& c) {
   if (ask) peek<N>(p, v);
   if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
   const uint64_t t0 = sm100::globaltimer();
@@ -108,9 +108,9 @@ __device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], W
     if (ask) peek<N>(p, v);
     if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
     if ((i & 63u) == 0) {
-      bool stop = *reinterpret_cast<volatile int32_t*>(&hdr->status) != VA_OK;
-      if (!stop && sm100::globaltimer() - t0 > sm100::kTimeoutNs) {
-        set_status(hdr, VA_ERR_TIMEOUT);
+      bool stop = *reinterpret_cast<volatile int32_t*>(&c.hdr->status) != VA_OK;
+      if (!stop && sm100::globaltimer() - t0 > (c.wait_ns ? c.wait_ns : sm100::kTimeoutNs)) {
+        set_status(c.hdr, VA_ERR_TIMEOUT);
         stop = true;
       }
       if (__any_sync(0xffffffffu, stop)) return false;
@@ -203,7 +203,7 @@ template <class C>
 __device__ __forceinline__ void publish(const ScanParams& p, const TileSmem<C>& sh, int ring, const Run& t) {
   constexpr int V = C::V;
   const int lane = threadIdx.x & 31;
-  if (t.tile < 0 || t.tile + 1 >= p.tiles) return;
+  if (t.tile < 0 || t.tile + 1 >= p.tiles || (p.wait_ns && t.tile == 0)) return;
   const int64_t wide = static_cast<int64_t>(p.cols) * C::kWidth, at = t.tile * wide + t.ch;
   bool reset = false;
   float A[V], B[V];
@@ -283,7 +283,7 @@ __device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int 
     for (int k = 0; k < Look<C>::kMost; ++k)
       if (s.t0 + k < s.t1) {
         if (!__all_sync(0xffffffffu, there<2 * V>(l.m[k])))
-          ok &= await<2 * V>(map_place<C>(p, t, s.t0 + k), true, l.m[k], p.hdr);
+          ok &= await<2 * V>(map_place<C>(p, t, s.t0 + k), true, l.m[k], p);
         Vec<V> mA, mB;
 #pragma unroll
         for (int i = 0; i < V; ++i) mA[i] = l.m[k][2 * i], mB[i] = l.m[k][2 * i + 1];
@@ -294,7 +294,7 @@ __device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int 
     for (int i = 0; i < V; ++i) sh.part[warp][lane * V + i] = make_float2(A[i], B[i]);
     if (warp == W - 1) {
       if (s.state >= 0 && !__all_sync(0xffffffffu, there<V>(l.c)))
-        ok &= await<V>(state_place<C>(p, t, s.state), true, l.c, p.hdr);
+        ok &= await<V>(state_place<C>(p, t, s.state), true, l.c, p);
 #pragma unroll
       for (int i = 0; i < V; ++i) sh.carry[lane * V + i] = s.state >= 0 ? l.c[i] : 0.f;
     }
@@ -489,7 +489,7 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
     }
     fence_barrier_init();
     sh.stop_first = sh.stop_enter = sh.abort_flag = 0;
-    sh.wait_limit = kTimeoutNs;
+    sh.wait_limit = p.wait_ns ? p.wait_ns : kTimeoutNs;
   }
   __syncthreads();
   if (threadIdx.x >= 32 * C::W) feed<C, BACK, kBytes>(p, sh, load);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) p.last[static_cast<int64_t>(row) * p.D + ch + i] = h[i];
   }
-  if (blockIdx.x != 0 || blockIdx.y != 0) return;
+  if (blockIdx.x != 0 || blockIdx.y != 0 || !p.hdr) return;
   int bad = 0;
   for (int b = threadIdx.x; b <= p.B; b += 256) bad |= p.cu[b] != b;
   bad = __syncthreads_or(bad);
@@ -828,13 +828,6 @@ void place(ScanParams& p, const Layout& l, void* ws) {
 }
 
 using bf16 = __nv_bfloat16;
-
-int device_sms() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return std::max(sms, 1);
-}
 
 template <class T>
 bool rows16(const void* p, int64_t rs) {

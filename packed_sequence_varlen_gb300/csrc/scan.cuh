@@ -20,10 +20,11 @@ struct ScanParams {
   float* last;         // forward: the last states; backward: h0's gradient; may be null
   int B, T, D;
   int tiles, cols;     // tiles of rows, columns of channels (set by the launcher)
-  struct WsHeader* hdr;  // workspace header
+  struct WsHeader* hdr;  // workspace header (single tokens: may be null)
   int32_t* ticket;
   int32_t* first;      // [tiles + 1] the first segment that starts at a tile's first row or later
   float* agg;          // [tiles][cols * width][2] a tile's map (decay product, state from zero)
+  uint64_t wait_ns;    // test hook: tile 0 publishes nothing and waits give up after this; 0: none
   float* carry;        // [groups][cols * width] the state after a group of tiles
 };
 

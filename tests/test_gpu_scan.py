@@ -337,3 +337,53 @@ def test_graph_streams_and_shared_workspace(va):
             got.append(both())
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
+
+
+def test_many_blocks_on_streams_at_once(va):
+    """Calls that each fill the GPU, on three streams at once: blocks of one that wait for others of it share the SMs
+    with the other calls' blocks."""
+    sets = []
+    for seed, lengths in ((1, [9000, 200, 3000]), (2, [12200]), (3, [40] * 305)):
+        m = make(lengths, 2048, BF, BF, seed)
+        sets.append({n: x.to(DEV) for n, x in m.items()})
+
+    def both(c):
+        h, last = va.varlen_scan_fwd(c["x"], c["g"], c["cu"], c["h0"], h_last=True)
+        return (h, last) + va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], c["h0"], c["dlast"])
+
+    want = [both(c) for c in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, c in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(both(c))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# many tiles for each block and few, copied rows and rows read in place
+@pytest.mark.parametrize("T,D,xt,gt", [(3000, 64, F32, F32), (20000, 512, BF, BF), (20000, 511, BF, F32), (300, 6, F32, F32)])
+def test_bounded_wait_runs_out_and_reports_timeout(va, T, D, xt, gt):
+    """The test hook keeps the first tile's map back: the others' waits run out after a few milliseconds, the call
+    reports it, and the next one is ordinary.  No GPU fault is involved."""
+    m = make([T], D, xt, gt)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    lib = va._lib.load()
+    ws = torch.empty(lib.varlen_scan_workspace_size(T, 1, D), dtype=torch.uint8, device=DEV)
+    h, _ = va.varlen_scan_fwd(c["x"], c["g"], c["cu"], check_status=True)
+    want = va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], x_dtype=xt, check_status=True)
+    assert lib.varlen_test_stall_next_scan(5_000_000) == 0
+    va.varlen_scan_fwd(c["x"], c["g"], c["cu"], workspace=ws)
+    torch.cuda.synchronize()
+    assert va.read_status(ws) == 6
+    assert torch.equal(va.varlen_scan_fwd(c["x"], c["g"], c["cu"], workspace=ws, check_status=True)[0], h)
+    assert lib.varlen_test_stall_next_scan(5_000_000) == 0
+    va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], x_dtype=xt, workspace=ws)
+    torch.cuda.synchronize()
+    assert va.read_status(ws) == 6
+    again = va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], x_dtype=xt, workspace=ws, check_status=True)
+    assert all(x is y is None or torch.equal(x, y) for x, y in zip(again, want))
+    assert lib.varlen_test_stall_next_scan(10) == 1 and lib.varlen_test_stall_next_scan(5_000_000_000) == 1

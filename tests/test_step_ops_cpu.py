@@ -91,6 +91,8 @@ def test_scan_arguments(va):
     assert scan_calls(va, s, ws=None) == (INVALID, INVALID)
     assert scan_calls(va, s, ws=P + 8) == (INVALID, INVALID)
     assert scan_calls(va, s, size=255) == (WORKSPACE, WORKSPACE)
+    one = scan_shape(va, T=2)                                 # single tokens: the status word alone, or nothing
+    assert scan_calls(va, one, size=255)[0] == WORKSPACE and scan_calls(va, one, ws=None, size=0)[1] == INVALID
     assert scan_calls(va, s, x=None) == (INVALID, INVALID)
     assert scan_calls(va, s, h=None) == (INVALID, INVALID)
     assert scan_calls(va, s, h=P + 1) == (INVALID, INVALID)

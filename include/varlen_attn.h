@@ -616,7 +616,8 @@ typedef struct {
 size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D);
 
 /* Forward.
- *   x_dev, log_decay_dev  [T, D]; decays are meant to be <= 0 (the decay of any run of 16 rows has to stay finite)
+ *   x_dev, log_decay_dev  [T, D]; log decays are meant to be <= 0 (with larger ones the decay over any 4096 rows of a
+ *               segment has to stay finite)
  *   h0_dev      float [B, D], or NULL
  *   h_dev       [T, D] out; may be x itself (same type and stride)
  *   h_last_dev  float [B, D] out: the state after each segment, or NULL; for single tokens (T == B) it may be h0

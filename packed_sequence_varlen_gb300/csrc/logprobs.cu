@@ -408,7 +408,7 @@ __device__ __forceinline__ int next_row(const LogprobParams& p, int row) {
   return min(row, p.T);
 }
 
-template <int NT> constexpr int ctas_per_sm() { return NT == 32 ? 20 : NT == 128 ? 7 : NT == 256 ? 4 : 1; }
+template <int NT> constexpr int ctas_per_sm() { return NT == 32 ? 20 : NT == 128 ? 7 : NT == 256 ? 4 : 2; }
 
 }  // namespace
 
@@ -621,13 +621,14 @@ cudaError_t run_fwd(const LogprobParams& p, int sms, cudaStream_t st) {
 
 // us a call: a warp a row for rows up to 16 KB (T = 16384, V = 3000 bf16, k = 0: 40, with 256 threads 78); 128 threads for few
 // alternatives of rows up to 64 KB (T = 8192, V = 32768 bf16, k = 5: 113, with 256 threads 128; k = 20: 163 and 171, but V = 131072, k = 20: 175
-// and 132, as each part that is looked at again is twice as long); 1024 while every row has an SM (T = 64, V = 32000: 9 and 12).
+// and 132, as each part that is looked at again is twice as long); 512 while every row has a block at once (T = 64, V = 32000, k = 20:
+// 8.4, with 256 9.4, with 1024 8.9).
 template <class T>
 cudaError_t pick_fwd(const LogprobParams& p, cudaStream_t st) {
   const int sms = device_sms();
   const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
   if (bytes <= 16384 && p.k <= 32) return run_fwd<T, 32>(p, sms, st);
-  if (p.T <= sms) return run_fwd<T, 1024>(p, sms, st);
+  if (p.T <= 2 * sms) return run_fwd<T, 512>(p, sms, st);
   return bytes <= 65536 && p.k <= 8 ? run_fwd<T, 128>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
 }
 

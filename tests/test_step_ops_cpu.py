@@ -1,6 +1,7 @@
 """Refusals of the query / key norm, the gated recurrence and the token log probabilities that need no GPU: the C
 ABI checks its arguments before it touches the device, the Python face its tensors."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -152,3 +153,31 @@ def test_tensors_are_checked(va):
         va.token_logprobs_fwd(x, pos)
     with pytest.raises(ValueError):
         va.token_logprobs_bwd(x, pos, x[:, 0], None, x[:, 0])
+
+
+def test_plain_forms_agree_with_the_definitions():
+    """The measured cases' plain forms and their 64-bit values, written apart, on small draws on the CPU."""
+    import random
+
+    import perf.more_operators as M
+    device, M.DEV = M.DEV, "cpu"
+    try:
+        rng, seen = random.Random(3), {}
+        while min(seen.get(op, 0) for op in ("qk", "scan", "logprobs")) < 6:
+            case = M.draw(rng)
+            if M.work(case)["bytes"] > 1e6:
+                continue
+            seen[case["op"]] = seen.get(case["op"], 0) + 1
+            plain, exact = M.run(M.prepare(case, 1)), M.exact(case, 1)
+            assert len(plain) == len(exact)
+            for a, b in zip(plain, exact):
+                if b is None:
+                    continue
+                assert a.shape == b.shape
+                # half a step of the type at most each, and 2^-20 for what 32 bits lose on the way; a log probability
+                # is a difference of numbers up to 32, whose half step in 32 bits is 2^-20, however near 0 it is itself
+                half = torch.finfo(a.dtype).eps / 2
+                lost = 2.0 ** -20 * math.sqrt(a.numel()) if case["op"] == "logprobs" and a.dim() < 2 or a.shape[-1:] == (case.get("k"),) else 0.0
+                assert float((a.double() - b.double()).norm()) <= (half + 2.0 ** -20) * float(b.double().norm()) + lost + 1e-30, case
+    finally:
+        M.DEV = device

@@ -11,8 +11,9 @@
 //   the state that enters the tile is folded from the maps of a few tiles before it and a state further back, which
 //   every kGroup-th tile publishes,
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
-// So the data is read once and written once.  A warp of its own takes the tiles' numbers, looks their segments up and has
-// their data copied to shared memory (TMA), a few tiles ahead of the others.  (Rows that are not on 16-byte boundaries are
+// So the data is read once and written once.  Three warps of a block serve the ones that work: one takes the tiles' numbers,
+// looks their segments up and has their data copied to shared memory (TMA), a few tiles ahead; one folds and publishes
+// the tiles' maps; one finds the state that enters a tile while the tile's own maps are formed.  (Rows that are not on 16-byte boundaries are
 // read by the others straight from memory, twice.)  The fold's order is fixed by the tile's number, whatever is finished
 // first, so results do not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that
 // is waited for is a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.
@@ -35,10 +36,16 @@ namespace va {
 namespace {
 
 // The last tile of every kGroup publishes the state after it.  A tile folds the maps of the kBack groups before its own
-// and of those before it in its own, onto the state before them, which has long been there (its own group's of 32
-// tiles, whose start was formed beside it: T = 65536 in one segment, D = 2048 in bf16, backward 363 us; 352 this way).
+// and of those before it in its own, onto the state before them: the further back, the surer it is there, and the
+// more there is to fold (T = 65536, D = 2048, backward, us: with bf16 / fp32 decays kGroup, kBack = 4, 2 413 / 442; 8, 1 384 / 429;
+// 8, 2 350 / 432; 8, 3 354 / 480; 8, 4 379 / 545).
 constexpr int kGroup = 8, kBack = 2;
 constexpr int kPrepThreads = 1024;
+// Words of what the first launch looks up for a tile: the first segment that starts at its first row or later, the
+// boundary there (backward: behind the tile) or after it and the one before, then a bit for every row that a segment
+// starts at, and for the one behind the tile.
+constexpr int kRecord = 8;
+constexpr int kResolvers = 2;  // warps that find the states that enter a block's tiles, in turn
 // Buffers of run maps: a slow warp may still read those of the tile before while a fast one, past a single barrier,
 // writes those of the tile after.
 constexpr int kRings = 3;
@@ -48,7 +55,8 @@ constexpr int kRings = 3;
 template <int V_, int W_, int R_, int S_, int M_>
 struct Shape {
   static constexpr int V = V_, W = W_, R = R_, S = S_, M = M_;
-  static constexpr int kThreads = 32 * (W_ + 1), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
+  static constexpr int kThreads = 32 * (W_ + 2 + kResolvers), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
+  static_assert(3 + kWords <= kRecord, "a tile's bits fit its record");
 };
 
 template <int V>
@@ -118,25 +126,24 @@ __device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], c
   }
 }
 
-// A tile as the copying warp leaves it for the others.
+// A tile as the feeding warp leaves it for the others.
 template <class C>
 struct Slot {
-  int tile, col;            // in the scan's order; tile < 0: no more
-  int b0;                   // the first segment that starts at the tile's first row or later
-  int needs, from;          // the tile goes on with a segment that began in tile `from`
-  uint32_t bits[C::kWords]; // bit i: a segment starts at (or the stream ends before) the tile's row i, i <= kRows
+  int tile, col;                       // in the scan's order; tile < 0: no more
+  int needs, from;                     // the tile goes on with a segment that began in tile `from`
+  int b0[C::W];                        // by run: the first segment that starts at its first row or later,
+  uint32_t starts[C::W], ends[C::W];   // bit r: a segment starts at its row r, one ends with it
 };
 
 // What the warps of a block share; channel = lane * V + i of the tile's columns.
 template <class C>
 struct TileSmem {
   alignas(16) float2 run[kRings][C::W][C::kWidth];  // the runs' maps
-  alignas(16) float2 part[C::W][C::kWidth];         // the folds of the tiles before
-  alignas(16) float carry[C::kWidth];               // the state after the group before
-  uint64_t full[C::S], empty[C::S];
+  alignas(16) float carry[C::S][C::kWidth];         // the state that enters a tile
+  uint64_t known[C::S], full[C::S], empty[C::S], carried[C::S];  // the slot, its data too; given back; its state
   int reset[kRings][C::W];                          // the run replaces the state
   Slot<C> slot[C::S];
-  int stop_first, stop_enter;                       // a wait gave up, before a step's first or second barrier
+  int stop[kRings];                                 // a wait gave up before the step's barrier of the runs' maps
   alignas(8) int pad;
   int abort_flag;                                   // (followed by its wait limit)
   uint64_t wait_limit;
@@ -144,34 +151,26 @@ struct TileSmem {
 
 // A tile as a warp sees it: its run's rows and the segments in them.
 struct Run {
-  int tile, col;
+  int tile;
   int row, n, ch;   // first row, rows, first channel of the lane
   int b0;           // the first segment that starts at `row` or later
   uint32_t starts, ends;
-  bool needs, on;
-  int from;
+  bool on;
 };
 
 template <class C>
 __device__ __forceinline__ Run run_of(const ScanParams& p, const Slot<C>& s, bool back) {
+  static_assert(32 % C::R == 0 && C::R < 32 && C::W <= 32, "a run's rows lie in one word, a lane looks a run up");
   Run t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   t.tile = s.tile;
-  t.col = s.col;
-  t.needs = s.needs != 0;
-  t.from = s.from;
-  const int at = (back ? C::W - 1 - warp : warp) * C::R;  // the run's rows in the tile
-  t.row = (back ? p.tiles - 1 - t.tile : t.tile) * C::kRows + at;
+  t.row = (back ? p.tiles - 1 - t.tile : t.tile) * C::kRows + (back ? C::W - 1 - warp : warp) * C::R;
   t.n = min(C::R, max(0, p.T - t.row));
-  t.ch = (t.col * 32 + lane) * C::V;
+  t.ch = (s.col * 32 + lane) * C::V;
   t.on = t.ch < p.D;
-  static_assert(32 % C::R == 0 && C::R < 32, "a run's rows lie in one word");
-  const uint32_t word = s.bits[at >> 5] >> (at & 31);
-  const uint32_t next = ((at + C::R) & 31) ? s.bits[at >> 5] >> ((at & 31) + C::R) : s.bits[(at + C::R) >> 5];
-  t.starts = word & bits_below(t.n);                                     // (the stream's end is none)
-  t.ends = ((word >> 1) | (next & 1u) << (C::R - 1)) & bits_below(t.n);  // a segment starts behind the row
-  t.b0 = s.b0;
-  for (int w = 0; w <= at >> 5; ++w) t.b0 += __popc(s.bits[w] & (w < at >> 5 ? ~0u : bits_below(at & 31)));
+  t.starts = s.starts[warp];
+  t.ends = s.ends[warp];
+  t.b0 = s.b0[warp];
   return t;
 }
 
@@ -187,147 +186,23 @@ __device__ __forceinline__ Vec<V> state_row(const float* s, int64_t at, bool on)
   return v;
 }
 
+// The barrier behind the runs' maps: the working warps and the publishing one.
 template <class C>
-__device__ __forceinline__ bool last_of_group(const ScanParams& p, const Run& t) {
-  return t.tile % kGroup == kGroup - 1 && t.tile + 1 < p.tiles;
+__device__ __forceinline__ void maps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::W + 1)) : "memory");
 }
 
+// A lane's places of a tile's map and of a group's state.
 template <class C>
-__device__ __forceinline__ void worker_sync() {  // the warps that compute
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * C::W) : "memory");
-}
-
-// Warp 0, behind the barrier of the runs' maps: publishes the tile's map, and the state after a group's last tile
-// where a segment's boundary in it makes that known already.
-template <class C>
-__device__ __forceinline__ void publish(const ScanParams& p, const TileSmem<C>& sh, int ring, const Run& t) {
-  constexpr int V = C::V;
-  const int lane = threadIdx.x & 31;
-  if (t.tile < 0 || t.tile + 1 >= p.tiles || (p.wait_ns && t.tile == 0)) return;
-  const int64_t wide = static_cast<int64_t>(p.cols) * C::kWidth, at = t.tile * wide + t.ch;
-  bool reset = false;
-  float A[V], B[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) A[i] = 1.f, B[i] = 0.f;
-#pragma unroll
-  for (int w = 0; w < C::W; ++w) {
-    const bool rw = sh.reset[ring][w] != 0;
-    reset |= rw;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 m = sh.run[ring][w][lane * V + i];
-      B[i] = rw ? m.y : fmaf(m.x, B[i], m.y);
-      A[i] = rw ? 0.f : m.x * A[i];
-    }
-  }
-  float m[2 * V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) m[2 * i] = A[i], m[2 * i + 1] = B[i];
-  show<2 * V>(p.agg + 2 * at, m);
-  if (reset && last_of_group<C>(p, t)) show<V>(p.carry + (t.tile / kGroup) * wide + t.ch, B);
-}
-
-// The maps that a warp folds for a tile, asked for before there is other work to do.
-template <class C>
-struct Look {
-  static constexpr int kMost = ((kBack + 1) * kGroup + C::W - 1) / C::W;
-  float m[kMost][2 * C::V], c[C::V];
-};
-// The tiles before `t` whose maps it folds: [lo, lo + n), `per` a warp; onto the state after group `state`, or onto
-// nothing (-1) where its segment began in one of them.
-struct Span {
-  int lo, n, per, t0, t1, state;
-};
-template <class C>
-__device__ __forceinline__ Span span_of(const Run& t) {
-  Span s;
-  const int g = t.tile / kGroup - kBack;
-  s.state = t.from < g * kGroup ? g - 1 : -1;
-  s.lo = max(max(g, 0) * kGroup, t.from);
-  s.n = t.tile - s.lo;
-  s.per = (s.n + C::W - 1) / C::W;
-  s.t0 = s.lo + (threadIdx.x >> 5) * s.per;
-  s.t1 = min(s.t0 + s.per, t.tile);
-  return s;
+__device__ __forceinline__ float* map_place(const ScanParams& p, int tile, int ch) {
+  return p.agg + 2 * (tile * (static_cast<int64_t>(p.cols) * C::kWidth) + ch);
 }
 template <class C>
-__device__ __forceinline__ const float* map_place(const ScanParams& p, const Run& t, int tile) {
-  return p.agg + 2 * (tile * (static_cast<int64_t>(p.cols) * C::kWidth) + t.ch);
+__device__ __forceinline__ float* state_place(const ScanParams& p, int group, int ch) {
+  return p.carry + group * (static_cast<int64_t>(p.cols) * C::kWidth) + ch;
 }
-template <class C>
-__device__ __forceinline__ float* state_place(const ScanParams& p, const Run& t, int group) {
-  return p.carry + group * (static_cast<int64_t>(p.cols) * C::kWidth) + t.ch;
-}
-template <class C>
-__device__ __forceinline__ void ask(const ScanParams& p, const Run& t, Look<C>& l) {
-  if (t.tile < 0 || !t.needs) return;
-  const Span s = span_of<C>(t);
-#pragma unroll
-  for (int k = 0; k < Look<C>::kMost; ++k)
-    if (s.t0 + k < s.t1) peek<2 * C::V>(map_place<C>(p, t, s.t0 + k), l.m[k]);
-  if ((threadIdx.x >> 5) == C::W - 1 && s.state >= 0) peek<C::V>(state_place<C>(p, t, s.state), l.c);
-}
-
-// The state that enters this warp's run, from the tiles before, the group before and the runs' maps.  False: give up.
-template <class C>
-__device__ __forceinline__ bool enter(const ScanParams& p, TileSmem<C>& sh, int ring, const Run& t, Look<C>& l,
-                                      Vec<C::V>& in) {
-  constexpr int V = C::V, W = C::W;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  in = fill<V>(0.f);
-  if (t.needs) {
-    const Span s = span_of<C>(t);
-    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f);
-    bool ok = true;
-#pragma unroll
-    for (int k = 0; k < Look<C>::kMost; ++k)
-      if (s.t0 + k < s.t1) {
-        if (!__all_sync(0xffffffffu, there<2 * V>(l.m[k])))
-          ok &= await<2 * V>(map_place<C>(p, t, s.t0 + k), true, l.m[k], p);
-        Vec<V> mA, mB;
-#pragma unroll
-        for (int i = 0; i < V; ++i) mA[i] = l.m[k][2 * i], mB[i] = l.m[k][2 * i + 1];
-        B = fma(mA, B, mB);
-        A = mul(A, mA);
-      }
-#pragma unroll
-    for (int i = 0; i < V; ++i) sh.part[warp][lane * V + i] = make_float2(A[i], B[i]);
-    if (warp == W - 1) {
-      if (s.state >= 0 && !__all_sync(0xffffffffu, there<V>(l.c)))
-        ok &= await<V>(state_place<C>(p, t, s.state), true, l.c, p);
-#pragma unroll
-      for (int i = 0; i < V; ++i) sh.carry[lane * V + i] = s.state >= 0 ? l.c[i] : 0.f;
-    }
-    if (!ok) sh.stop_enter = 1;
-    worker_sync<C>();
-    if (sh.stop_enter) return false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) in[i] = sh.carry[lane * V + i];
-    for (int w = 0; w * s.per < s.n; ++w) {
-      Vec<V> mA, mB;
-#pragma unroll
-      for (int i = 0; i < V; ++i) mA[i] = sh.part[w][lane * V + i].x, mB[i] = sh.part[w][lane * V + i].y;
-      in = fma(mA, in, mB);
-    }
-  }
-  // the runs before; warp 0 goes through all of them for the state after the tile
-  bool reset = false;
-  Vec<V> after = in;
-  const bool last = warp == 0 && t.needs && last_of_group<C>(p, t);
-  for (int w = 0; w < (last ? W : warp); ++w) {
-    const bool rw = sh.reset[ring][w] != 0;
-    reset |= rw;
-    Vec<V> mA, mB;
-#pragma unroll
-    for (int i = 0; i < V; ++i) mA[i] = sh.run[ring][w][lane * V + i].x, mB[i] = sh.run[ring][w][lane * V + i].y;
-    after = rw ? mB : fma(mA, after, mB);
-  }
-  if (last) {
-    if (!reset) show<V>(state_place<C>(p, t, t.tile / kGroup), after.e);
-  } else {
-    in = after;
-  }
-  return true;
+__device__ __forceinline__ bool last_of_group(const ScanParams& p, int tile) {
+  return tile % kGroup == kGroup - 1 && tile + 1 < p.tiles;
 }
 
 // Tiles for each block (with a single one, or one and a few over, a block finishes it before it takes another).
@@ -335,7 +210,9 @@ __device__ __forceinline__ int tiles_each(const ScanParams& p) {
   return max(1, p.tiles * p.cols / static_cast<int>(gridDim.x));
 }
 
-// The copying warp: takes the tiles' numbers, looks their segments up, asks for their data.
+// The feeding warp: takes the tiles' numbers, lays out their segments, asks for their data.  (One tile is taken ahead of
+// the place for it; with more of them its number came sooner, but the blocks came out of step: backward of T = 65536,
+// D = 2048 in bf16 305 us with one, 367 with three.)
 //   load(tile, col, stage): one lane's, issues the copies that complete on full[stage] (kBytes in all)
 template <class C, bool BACK, int kBytes, class Load>
 __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&& load) {
@@ -344,32 +221,11 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
   const int lane = threadIdx.x & 31, total = p.tiles * p.cols;
   const int most = min(S, tiles_each(p));  // a block's tiles at a time
   volatile int* abort_flag = &sh.abort_flag;
-  // a tile's number, and its segments: where the scan enters it (backward: behind it), and the starts in it
-  int number = 0, tile = 0, col = 0, row0 = 0, b0 = 0, from = 0, needs = 0;
-  uint32_t bits = 0;  // lane i: word i
+  int number = 0, rec = 0;  // a tile's number; lane i: word i of what is known of it
   const auto take = [&] {
     if (lane == 0) number = atomicAdd(p.ticket, 1);
     number = __shfl_sync(0xffffffffu, number, 0);
-    if (number >= total) return;
-    tile = number / p.cols;
-    col = number - tile * p.cols;
-    const int rt = BACK ? p.tiles - 1 - tile : tile;
-    row0 = rt * C::kRows;
-    b0 = p.first[rt];
-    const int f = BACK ? p.first[rt + 1] : b0, enter = BACK ? row0 + C::kRows : row0;
-    const int cf = p.cu[f], before = p.cu[max(f - 1, 0)];
-    bits = 0;
-    for (int b = b0; b <= p.B; b += 32) {
-      const int d = b + lane <= p.B ? p.cu[b + lane] - row0 : C::kRows + 1;
-#pragma unroll
-      for (int w = 0; w < C::kWords; ++w) {
-        const uint32_t word = __reduce_or_sync(0xffffffffu, d >> 5 == w && d <= C::kRows ? 1u << (d & 31) : 0u);
-        if (lane == w) bits |= word;
-      }
-      if (__any_sync(0xffffffffu, d > C::kRows)) break;
-    }
-    needs = enter < p.T && cf != enter;
-    from = !needs ? tile : BACK ? p.tiles - 1 - (cf - 1) / C::kRows : before / C::kRows;
+    if (number < total && lane < kRecord) rec = p.record[static_cast<int64_t>(BACK ? p.tiles - 1 - number / p.cols : number / p.cols) * kRecord + lane];
   };
   int issued = 0;
   bool ok = true;
@@ -379,10 +235,35 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
     if (j >= most) ok = wwait(smem_u32(&sh.empty[(j - most) % S]), ((j - most) / S) & 1, abort_flag, p.hdr, 71);
     if (!ok) break;
     if (most == 1) take();
+    const bool none = number >= total;
+    const int tile = number / p.cols, col = number - tile * p.cols;
+    const int row0 = (BACK ? p.tiles - 1 - tile : tile) * C::kRows;
+    int from = 0, needs = 0, b0 = 0;  // lane w: b0, starts, ends of the run of warp w
+    uint32_t starts = 0, ends = 0;
+    if (!none) {
+      const int enter = BACK ? row0 + C::kRows : row0;
+      const int edge = __shfl_sync(0xffffffffu, rec, 1), before = __shfl_sync(0xffffffffu, rec, 2);
+      needs = enter < p.T && edge != enter;
+      from = !needs ? tile : BACK ? p.tiles - 1 - (edge - 1) / C::kRows : before / C::kRows;
+      // a run's part of the words, and how many starts come before it
+      const int at = (BACK ? C::W - 1 - lane : lane) * C::R & (C::kRows - 1), n = p.T - row0 - at;
+      const uint32_t bits = static_cast<uint32_t>(rec);
+      const uint32_t word = __shfl_sync(0xffffffffu, bits, 3 + (at >> 5)) >> (at & 31);
+      const uint32_t next = __shfl_sync(0xffffffffu, bits, 3 + ((at + C::R) >> 5)) >> ((at + C::R) & 31);
+      starts = word & bits_below(min(n, C::R));                                     // (the stream's end is none)
+      ends = ((word >> 1) | (next & 1u) << (C::R - 1)) & bits_below(min(n, C::R));  // a segment starts behind the row
+      b0 = __shfl_sync(0xffffffffu, rec, 0);
+#pragma unroll
+      for (int w = 0; w < C::kWords; ++w) {
+        const uint32_t x = __shfl_sync(0xffffffffu, bits, 3 + w);
+        b0 += __popc(w < at >> 5 ? x : w == at >> 5 ? x & bits_below(at & 31) : 0u);
+      }
+    }
     Slot<C>& slot = sh.slot[s];
-    if (number >= total) {
+    if (none) {
       if (lane == 0) {
         slot.tile = -1;
+        mbar_arrive(smem_u32(&sh.known[s]));
         mbar_arrive(smem_u32(&sh.full[s]));
         mbar_arrive(smem_u32(&sh.full[s]));
       }
@@ -397,14 +278,20 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
       }
       slot.tile = tile;
       slot.col = col;
-      slot.b0 = b0;
       slot.needs = needs;
       slot.from = from;
     }
     issued = j + 1;
-    if (lane < C::kWords) slot.bits[lane] = bits;
+    if (lane < C::W) {
+      slot.b0[lane] = b0;
+      slot.starts[lane] = starts;
+      slot.ends[lane] = ends;
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&sh.known[s]));
+      mbar_arrive(smem_u32(&sh.full[s]));
+    }
     if (most > 1) take();
   }
   // given up: the copies on their way land before the block ends (bounded again)
@@ -416,65 +303,188 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
   }
 }
 
-// The other warps: form a tile's maps before they finish the tile before, so that whoever waits for them waits little.
+// A warp's way through the block's tiles: stage, the parity of its barriers, the maps' ring.
+template <class C>
+struct Turn {
+  int stage = 0, parity = 0, ring = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == C::S) {
+      stage = 0;
+      parity ^= 1;
+    }
+    ring = ring + 1 == kRings ? 0 : ring + 1;
+  }
+};
+
+// The publishing warp: folds the runs' maps of a tile into the tile's and publishes it, and after a group's last tile the
+// state.
+template <class C>
+__device__ __forceinline__ void publish(const ScanParams& p, TileSmem<C>& sh) {
+  using namespace sm100;
+  constexpr int V = C::V;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh.abort_flag;
+  for (Turn<C> at;; at.next()) {
+    if (!wwait(smem_u32(&sh.full[at.stage]), at.parity, abort_flag, p.hdr, 73)) sh.stop[at.ring] = 1;
+    const int tile = sh.slot[at.stage].tile, ch = (sh.slot[at.stage].col * 32 + lane) * V;
+    maps_sync<C>();
+    if (sh.stop[at.ring] || tile < 0) return;
+    if (tile + 1 >= p.tiles || (p.wait_ns && tile == 0)) continue;
+    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f);
+    bool reset = false;
+#pragma unroll
+    for (int w = 0; w < C::W; ++w) {
+      const bool rw = sh.reset[at.ring][w] != 0;
+      reset |= rw;
+      Vec<V> mA, mB;
+#pragma unroll
+      for (int i = 0; i < V; ++i) mA[i] = sh.run[at.ring][w][lane * V + i].x, mB[i] = sh.run[at.ring][w][lane * V + i].y;
+      B = rw ? mB : fma(mA, B, mB);
+      A = rw ? fill<V>(0.f) : mul(A, mA);
+    }
+    float m[2 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) m[2 * i] = A[i], m[2 * i + 1] = B[i];
+    show<2 * V>(map_place<C>(p, tile, ch), m);
+    if (!last_of_group(p, tile)) continue;
+    if (!reset) {
+      // (the state that enters the tile waits for tiles before it only; the stage is held till this warp comes round)
+      if (!wwait(smem_u32(&sh.carried[at.stage]), at.parity, abort_flag, p.hdr, 76)) {
+        sh.stop[at.ring + 1 == kRings ? 0 : at.ring + 1] = 1;
+        continue;
+      }
+      Vec<V> in;
+#pragma unroll
+      for (int i = 0; i < V; ++i) in[i] = sh.carry[at.stage][lane * V + i];
+      B = fma(A, in, B);
+    }
+    show<V>(state_place<C>(p, tile / kGroup, ch), B.e);
+  }
+}
+
+// A resolving warp: the state that enters a tile, from the maps of the tiles before it and a state further back, from when
+// the tile's number is known.  Each of them looks at every tile's slot and takes its share of the tiles.
+template <class C>
+__device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, int me) {
+  using namespace sm100;
+  constexpr int V = C::V, kAhead = 8;  // maps asked for at once
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh.abort_flag;
+  int whose = 0;
+  for (Turn<C> at;; at.next()) {
+    if (!wwait(smem_u32(&sh.known[at.stage]), at.parity, abort_flag, p.hdr, 74)) return;
+    const Slot<C>& slot = sh.slot[at.stage];
+    const int tile = slot.tile;
+    if (tile < 0) return;
+    const bool mine = whose == me;
+    whose = whose + 1 == kResolvers ? 0 : whose + 1;
+    if (!mine) continue;
+    const int ch = (slot.col * 32 + lane) * V, from = slot.from;
+    const bool needs = slot.needs != 0;
+    Vec<V> in = fill<V>(0.f);
+    bool ok = true;
+    if (needs) {
+      // [lo, tile) are folded; then onto the state after the group before them where the segment began further back (the
+      // state last: in one long segment each of them waits for the one before)
+      const int g = tile / kGroup - kBack, lo = max(max(g, 0) * kGroup, from);
+      const bool onto = from < g * kGroup;
+      Vec<V> A = fill<V>(1.f), B = fill<V>(0.f);
+      if (onto) peek<V>(state_place<C>(p, g - 1, ch), in.e);
+      for (int k0 = lo; k0 < tile; k0 += kAhead) {
+        float m[kAhead][2 * V];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (k0 + k < tile) peek<2 * V>(map_place<C>(p, k0 + k, ch), m[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (k0 + k < tile) {
+            if (!__all_sync(0xffffffffu, there<2 * V>(m[k])))
+              ok = ok && await<2 * V>(map_place<C>(p, k0 + k, ch), true, m[k], p);
+            Vec<V> mA, mB;
+#pragma unroll
+            for (int i = 0; i < V; ++i) mA[i] = m[k][2 * i], mB[i] = m[k][2 * i + 1];
+            B = fma(mA, B, mB);
+            A = mul(A, mA);
+          }
+      }
+      if (onto) {
+        if (!__all_sync(0xffffffffu, there<V>(in.e))) ok = ok && await<V>(state_place<C>(p, g - 1, ch), true, in.e, p);
+        in = fma(A, in, B);
+      } else {
+        in = B;
+      }
+    }
+    if (!ok) {
+      sh.abort_flag = 1;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sh.carry[at.stage][lane * V + i] = in[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.carried[at.stage]));
+  }
+}
+
+// The working warps: form a tile's maps before they finish the tile before, so that whoever waits for them waits little.
 //   first(run, stage, A, B)    the run's map, true: it replaces the state        second(run, stage, in)   the outputs
 // (One copy of each part of the work: unrolled over the stages the code left the instruction cache; the forward of
 // T = 8192, D = 4096 in bf16 took 211 us.)
 template <class C, bool BACK, class First, class Second>
 __device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First&& first, Second&& second) {
   using namespace sm100;
-  constexpr int V = C::V, S = C::S;
+  constexpr int V = C::V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   volatile int* abort_flag = &sh.abort_flag;
   Run old;
   old.tile = -1;
-  int stage = 0, parity = 0, ring = 0, held = 0;
+  Turn<C> at, held;
   const bool single = tiles_each(p) == 1;
 #pragma unroll 1
-  for (;;) {
-    const bool ok = wwait(smem_u32(&sh.full[stage]), parity, abort_flag, p.hdr, 72);
+  for (;; at.next()) {
     Run now;
     now.tile = -1;
-    if (ok) {
-      if (sh.slot[stage].tile >= 0) now = run_of<C>(p, sh.slot[stage], BACK);
-    } else {
-      sh.stop_first = 1;
-    }
-    Look<C> look;
-    ask<C>(p, old, look);
+    if (!wwait(smem_u32(&sh.full[at.stage]), at.parity, abort_flag, p.hdr, 72)) sh.stop[at.ring] = 1;
+    else if (sh.slot[at.stage].tile >= 0) now = run_of<C>(p, sh.slot[at.stage], BACK);
     if (now.tile >= 0) {
       Vec<V> A, B;
-      const bool reset = first(now, stage, A, B);
+      const bool reset = first(now, at.stage, A, B);
 #pragma unroll
-      for (int k = 0; k < V; ++k) sh.run[ring][warp][lane * V + k] = make_float2(reset ? 0.f : A[k], B[k]);
-      if (lane == 0) sh.reset[ring][warp] = reset;
+      for (int k = 0; k < V; ++k) sh.run[at.ring][warp][lane * V + k] = make_float2(reset ? 0.f : A[k], B[k]);
+      if (lane == 0) sh.reset[at.ring][warp] = reset;
     }
-    worker_sync<C>();
-    if (sh.stop_first) break;
-    if (warp == 0) publish<C>(p, sh, ring, now);
+    maps_sync<C>();
+    if (sh.stop[at.ring]) break;
+    const int next = at.ring + 1 == kRings ? 0 : at.ring + 1;
     if (single) {
       old = now;
-      held = stage;
-      ask<C>(p, old, look);
+      held = at;
     }
     if (old.tile >= 0) {
-      Vec<V> in;
-      if (!enter<C>(p, sh, single ? ring : ring == 0 ? kRings - 1 : ring - 1, old, look, in)) break;
-      second(old, held, in);
+      // (a wait that gives up here leaves its tile, but comes to the next barrier like the others, and stops there)
+      if (wwait(smem_u32(&sh.carried[held.stage]), held.parity, abort_flag, p.hdr, 75)) {
+        Vec<V> in;
+#pragma unroll
+        for (int i = 0; i < V; ++i) in[i] = sh.carry[held.stage][lane * V + i];
+        for (int w = 0; w < warp; ++w) {
+          const bool rw = sh.reset[held.ring][w] != 0;
+          Vec<V> mA, mB;
+#pragma unroll
+          for (int i = 0; i < V; ++i) mA[i] = sh.run[held.ring][w][lane * V + i].x, mB[i] = sh.run[held.ring][w][lane * V + i].y;
+          in = rw ? mB : fma(mA, in, mB);
+        }
+        second(old, held.stage, in);
+      } else {
+        sh.stop[next] = 1;  // (this step's may still be being read)
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[held]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[held.stage]));
     }
     if (now.tile < 0) return;
     old = now;
+    held = at;
     if (single) old.tile = -1;
-    held = stage;
-    if (++stage == S) {
-      stage = 0;
-      parity ^= 1;
-    }
-    ring = ring + 1 == kRings ? 0 : ring + 1;
   }
-  sh.abort_flag = 1;  // given up: the copying warp stops too
+  sh.abort_flag = 1;  // given up: the other warps stop too
 }
 
 // Runs a block's warps.
@@ -484,16 +494,23 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
   using namespace sm100;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
+      mbar_init(smem_u32(&sh.known[s]), 1);
       mbar_init(smem_u32(&sh.full[s]), 2);  // the data's bytes, the slot
       mbar_init(smem_u32(&sh.empty[s]), C::W);
+      mbar_init(smem_u32(&sh.carried[s]), 1);
+      sh.slot[s].tile = -1;
     }
     fence_barrier_init();
-    sh.stop_first = sh.stop_enter = sh.abort_flag = 0;
+    for (int r = 0; r < kRings; ++r) sh.stop[r] = 0;
+    sh.abort_flag = 0;
     sh.wait_limit = p.wait_ns ? p.wait_ns : kTimeoutNs;
   }
   __syncthreads();
-  if (threadIdx.x >= 32 * C::W) feed<C, BACK, kBytes>(p, sh, load);
-  else work<C, BACK>(p, sh, first, second);
+  const int warp = threadIdx.x >> 5;
+  if (warp < C::W) work<C, BACK>(p, sh, first, second);
+  else if (warp == C::W) feed<C, BACK, kBytes>(p, sh, load);
+  else if (warp == C::W + 1) publish<C>(p, sh);
+  else resolve<C>(p, sh, warp - C::W - 2);
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
@@ -570,22 +587,37 @@ struct Maps {
 
 }  // namespace
 
-// Checks the boundary contract (block 0), empties the published places and looks up the first segment at every tile.
-__global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParams p, int rows, int64_t words) {
+// Checks the boundary contract (block 0), empties the published places and writes every tile's record.
+__global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParams p, int rows, int back, int64_t words) {
   griddep_begin();
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPrepThreads;
   for (int64_t i = tid; i < words / 4; i += step)
     reinterpret_cast<uint4*>(p.agg)[i] = make_uint4(kNone, kNone, kNone, kNone);
-  for (int64_t i = tid; i <= p.tiles; i += step) {  // the first b in [0, B] with cu[b] >= row (cu[B] = T)
-    const int row = static_cast<int>(min(i * rows, static_cast<int64_t>(p.T)));
+  for (int64_t i = tid; i < static_cast<int64_t>(p.tiles) * kRecord; i += step) {
+    const int k = static_cast<int>(i % kRecord), row0 = static_cast<int>(i / kRecord) * rows;  // (row0 < T)
+    // the first b in [0, B] with cu[b] >= row (cu[B] = T)
+    const int row = min(k == 0 ? row0 : k < 3 ? row0 + (back ? rows : 0) : row0 + min(32 * (k - 3), rows), p.T);
     int lo = 0, hi = p.B;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (p.cu[mid] < row) lo = mid + 1;
       else hi = mid;
     }
-    p.first[i] = lo;
+    int word = lo;
+    if (k == 1) word = p.cu[lo];
+    if (k == 2) word = p.cu[max(lo - 1, 0)];
+    if (k >= 3) {
+      uint32_t bits = 0;
+      const int first = row0 + 32 * (k - 3), most = min(first + 31, row0 + rows);
+      for (int b = lo; b <= p.B; ++b) {
+        const int at = p.cu[b];
+        if (at < first || at > most) break;
+        bits |= 1u << (at - first);
+      }
+      word = static_cast<int>(bits);
+    }
+    p.record[i] = word;
   }
   if (blockIdx.x != 0) return;
   int bad = 0;
@@ -793,7 +825,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
   int64_t tiles, cols, groups, words;
-  size_t first, agg, carry, total;
+  size_t record, agg, carry, total;
 };
 
 Layout layout_of(int T, int D, int rows, int width) {
@@ -801,8 +833,8 @@ Layout layout_of(int T, int D, int rows, int width) {
   l.tiles = (static_cast<int64_t>(T) + rows - 1) / rows;
   l.cols = (static_cast<int64_t>(D) + width - 1) / width;
   l.groups = (l.tiles + kGroup - 1) / kGroup;
-  l.first = sizeof(WsHeader);
-  l.agg = align256(l.first + (l.tiles + 1) * sizeof(int32_t));
+  l.record = sizeof(WsHeader);
+  l.agg = align256(l.record + l.tiles * kRecord * sizeof(int32_t));
   l.carry = l.agg + l.tiles * l.cols * width * 2 * sizeof(float);  // (follows: both are emptied together)
   l.words = (l.tiles * 2 + l.groups) * l.cols * width;
   l.total = align256(l.agg + l.words * sizeof(float));
@@ -820,7 +852,7 @@ void place(ScanParams& p, const Layout& l, void* ws) {
   WsHeader* h = reinterpret_cast<WsHeader*>(w);
   p.hdr = h;
   p.ticket = &h->counter[0];
-  p.first = reinterpret_cast<int32_t*>(w + l.first);
+  p.record = reinterpret_cast<int32_t*>(w + l.record);
   p.agg = reinterpret_cast<float*>(w + l.agg);
   p.carry = reinterpret_cast<float*>(w + l.carry);
   p.tiles = static_cast<int>(l.tiles);
@@ -836,15 +868,15 @@ bool rows16(const void* p, int64_t rs) {
 
 // The call's blocks, as many as fit, each with S tiles of `piece` bytes in shared memory.
 template <class C>
-cudaError_t run_blocks(int stage, void (*kernel)(ScanParams, Maps), size_t piece, ScanParams p, const Maps& maps, void* ws,
+cudaError_t run_blocks(int stage, int back, void (*kernel)(ScanParams, Maps), size_t piece, ScanParams p, const Maps& maps, void* ws,
                        cudaStream_t st) {
   const Layout l = layout_of(p.T, p.D, C::kRows, C::kWidth);
   place(p, l, ws);
   const int sms = device_sms();
   if (stage == 0) {
-    const int64_t work = std::max(l.words / 8, l.tiles + 1);
+    const int64_t work = std::max(l.words / 8, l.tiles * kRecord);
     const int blocks = static_cast<int>(std::min<int64_t>(2 * sms, (work + kPrepThreads - 1) / kPrepThreads));
-    return launch_pdl(scan_prep_kernel, dim3(blocks), dim3(kPrepThreads), 0, st, p, C::kRows, l.words);
+    return launch_pdl(scan_prep_kernel, dim3(blocks), dim3(kPrepThreads), 0, st, p, C::kRows, back, l.words);
   }
   const size_t smem = head_bytes<C>() + piece * C::S;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -856,9 +888,9 @@ cudaError_t run_blocks(int stage, void (*kernel)(ScanParams, Maps), size_t piece
 
 template <int V> using FwdShape = Shape<V, 8, 16, 3, 2>;
 // (from memory: short runs, whose rows are all asked for at once)
-template <int V> using FwdPlain = Shape<V, 8, 8, 3, 3>;
+template <int V> using FwdPlain = Shape<V, 8, 8, 3, 2>;
 template <int V> using BwdShape = Shape<V, 8, 8, 3, 2>;
-template <int V> using BwdPlain = Shape<V, 8, 8, 3, 3>;
+template <int V> using BwdPlain = Shape<V, 8, 8, 3, 2>;
 
 // Two channels a lane where rows lie on boundaries of two elements, else one; copied tiles where they lie on 16 bytes.
 template <class TX, class TG, class TH>
@@ -867,14 +899,14 @@ cudaError_t run_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
   const bool two =
       p.D % 2 == 0 && steps_of<TX>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) && steps_of<TH>(p.out, p.out_rs, 2);
   Maps maps{};
-  if (!two) return run_blocks<FwdPlain<1>>(stage, scan_fwd_kernel<TX, TG, TH, FwdPlain<1>, false>, 0, p, maps, ws, st);
+  if (!two) return run_blocks<FwdPlain<1>>(stage, 0, scan_fwd_kernel<TX, TG, TH, FwdPlain<1>, false>, 0, p, maps, ws, st);
   if (rows16<TX>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TX) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows)))
       return cudaErrorInvalidValue;
-    return run_blocks<C>(stage, scan_fwd_kernel<TX, TG, TH, C, true>, tile_bytes<TX, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
+    return run_blocks<C>(stage, 0, scan_fwd_kernel<TX, TG, TH, C, true>, tile_bytes<TX, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return run_blocks<FwdPlain<2>>(stage, scan_fwd_kernel<TX, TG, TH, FwdPlain<2>, false>, 0, p, maps, ws, st);
+  return run_blocks<FwdPlain<2>>(stage, 0, scan_fwd_kernel<TX, TG, TH, FwdPlain<2>, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
@@ -883,15 +915,15 @@ cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
   const bool two = p.D % 2 == 0 && steps_of<TH>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) &&
                    steps_of<TH>(p.h, p.h_rs, 2) && steps_of<TX>(p.out, p.out_rs, 2) && steps_of<TG>(p.dg, p.dg_rs, 2);
   Maps maps{};
-  if (!two) return run_blocks<BwdPlain<1>>(stage, scan_bwd_kernel<TX, TG, TH, BwdPlain<1>, false>, 0, p, maps, ws, st);
+  if (!two) return run_blocks<BwdPlain<1>>(stage, 1, scan_bwd_kernel<TX, TG, TH, BwdPlain<1>, false>, 0, p, maps, ws, st);
   if (rows16<TH>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && rows16<TH>(p.h, p.h_rs)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TH) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.c, p.h, sizeof(TH) == 2, p.T, p.D, p.h_rs, C::kWidth, C::kRows)))
       return cudaErrorInvalidValue;
-    return run_blocks<C>(stage, scan_bwd_kernel<TX, TG, TH, C, true>, 2 * tile_bytes<TH, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
+    return run_blocks<C>(stage, 1, scan_bwd_kernel<TX, TG, TH, C, true>, 2 * tile_bytes<TH, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
   }
-  return run_blocks<BwdPlain<2>>(stage, scan_bwd_kernel<TX, TG, TH, BwdPlain<2>, false>, 0, p, maps, ws, st);
+  return run_blocks<BwdPlain<2>>(stage, 1, scan_bwd_kernel<TX, TG, TH, BwdPlain<2>, false>, 0, p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>

@@ -22,7 +22,7 @@ struct ScanParams {
   int tiles, cols;     // tiles of rows, columns of channels (set by the launcher)
   struct WsHeader* hdr;  // workspace header (single tokens: may be null)
   int32_t* ticket;
-  int32_t* first;      // [tiles + 1] the first segment that starts at a tile's first row or later
+  int32_t* record;     // [tiles][8] what is known of a tile's segments
   float* agg;          // [tiles][cols * width][2] a tile's map (decay product, state from zero)
   uint64_t wait_ns;    // test hook: tile 0 publishes nothing and waits give up after this; 0: none
   float* carry;        // [groups][cols * width] the state after a group of tiles

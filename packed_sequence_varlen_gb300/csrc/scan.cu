@@ -106,24 +106,34 @@ __device__ __forceinline__ bool there(const float (&v)[N]) {
   return ok;
 }
 
-// Waits until the N words of every lane that asks are there (a warp's call); false when the call is to be given up.
-template <int N>
-__device__ __forceinline__ bool await(const float* p, bool ask, float (&v)[N], const ScanParams& c) {
-  if (ask) peek<N>(p, v);
-  if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
-  const uint64_t t0 = sm100::globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (ask) peek<N>(p, v);
-    if (__all_sync(0xffffffffu, !ask || there<N>(v))) return true;
-    if ((i & 63u) == 0) {
-      bool stop = *reinterpret_cast<volatile int32_t*>(&c.hdr->status) != VA_OK;
-      if (!stop && sm100::globaltimer() - t0 > (c.wait_ns ? c.wait_ns : sm100::kTimeoutNs)) {
-        set_status(c.hdr, VA_ERR_TIMEOUT);
-        stop = true;
-      }
-      if (__any_sync(0xffffffffu, stop)) return false;
-    }
+// The waits, bounded; their slow parts in one copy each (the code of a block's warps together has to stay in the
+// instruction cache).  Every lane of a warp asks, and gets the same answer.
+__device__ __noinline__ bool past_limit(const ScanParams& c, uint64_t since) {
+  bool stop = *reinterpret_cast<volatile int32_t*>(&c.hdr->status) != VA_OK;
+  if (!stop && sm100::globaltimer() - since > (c.wait_ns ? c.wait_ns : sm100::kTimeoutNs)) {
+    set_status(c.hdr, VA_ERR_TIMEOUT);
+    stop = true;
   }
+  return __any_sync(0xffffffffu, stop);
+}
+// Asks until what it asks for is there; false when the call is to be given up.
+template <class Ask>
+__device__ __forceinline__ bool until(const ScanParams& c, Ask&& ask) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, ask())) return true;
+    if (i == 0) since = sm100::globaltimer();
+    if ((i & 63u) == 63u && past_limit(c, since)) return false;
+  }
+}
+__device__ __noinline__ bool hold_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
+  return sm100::wwait(bar, parity, abort_flag, hdr, where);
+}
+__device__ __forceinline__ bool hold(uint64_t& bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
+  const uint32_t at = smem_u32(&bar);
+  if (__all_sync(0xffffffffu, sm100::mbar_try_wait(at, parity))) return true;
+  return hold_slow(at, parity, abort_flag, hdr, where);
 }
 
 // A tile as the feeding warp leaves it for the others.
@@ -232,7 +242,7 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
   if (most > 1) take();  // a tile ahead of the place for it
   for (int j = 0;; ++j) {
     const int s = j % S;
-    if (j >= most) ok = wwait(smem_u32(&sh.empty[(j - most) % S]), ((j - most) / S) & 1, abort_flag, p.hdr, 71);
+    if (j >= most) ok = hold(sh.empty[(j - most) % S], ((j - most) / S) & 1, abort_flag, p.hdr, 71);
     if (!ok) break;
     if (most == 1) take();
     const bool none = number >= total;
@@ -325,7 +335,7 @@ __device__ __forceinline__ void publish(const ScanParams& p, TileSmem<C>& sh) {
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh.abort_flag;
   for (Turn<C> at;; at.next()) {
-    if (!wwait(smem_u32(&sh.full[at.stage]), at.parity, abort_flag, p.hdr, 73)) sh.stop[at.ring] = 1;
+    if (!hold(sh.full[at.stage], at.parity, abort_flag, p.hdr, 73)) sh.stop[at.ring] = 1;
     const int tile = sh.slot[at.stage].tile, ch = (sh.slot[at.stage].col * 32 + lane) * V;
     maps_sync<C>();
     if (sh.stop[at.ring] || tile < 0) return;
@@ -349,7 +359,7 @@ __device__ __forceinline__ void publish(const ScanParams& p, TileSmem<C>& sh) {
     if (!last_of_group(p, tile)) continue;
     if (!reset) {
       // (the state that enters the tile waits for tiles before it only; the stage is held till this warp comes round)
-      if (!wwait(smem_u32(&sh.carried[at.stage]), at.parity, abort_flag, p.hdr, 76)) {
+      if (!hold(sh.carried[at.stage], at.parity, abort_flag, p.hdr, 76)) {
         sh.stop[at.ring + 1 == kRings ? 0 : at.ring + 1] = 1;
         continue;
       }
@@ -367,12 +377,12 @@ __device__ __forceinline__ void publish(const ScanParams& p, TileSmem<C>& sh) {
 template <class C>
 __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, int me) {
   using namespace sm100;
-  constexpr int V = C::V, kAhead = 8;  // maps asked for at once
+  constexpr int V = C::V, kAhead = 4;  // maps asked for at once
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh.abort_flag;
   int whose = 0;
   for (Turn<C> at;; at.next()) {
-    if (!wwait(smem_u32(&sh.known[at.stage]), at.parity, abort_flag, p.hdr, 74)) return;
+    if (!hold(sh.known[at.stage], at.parity, abort_flag, p.hdr, 74)) return;
     const Slot<C>& slot = sh.slot[at.stage];
     const int tile = slot.tile;
     if (tile < 0) return;
@@ -389,17 +399,21 @@ __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, in
       const int g = tile / kGroup - kBack, lo = max(max(g, 0) * kGroup, from);
       const bool onto = from < g * kGroup;
       Vec<V> A = fill<V>(1.f), B = fill<V>(0.f);
-      if (onto) peek<V>(state_place<C>(p, g - 1, ch), in.e);
-      for (int k0 = lo; k0 < tile; k0 += kAhead) {
+#pragma unroll 1
+      for (int k0 = lo; k0 < tile && ok; k0 += kAhead) {
         float m[kAhead][2 * V];
+        ok = until(p, [&] {
+          bool all = true;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (k0 + k < tile) peek<2 * V>(map_place<C>(p, k0 + k, ch), m[k]);
+          for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < tile) peek<2 * V>(map_place<C>(p, k0 + k, ch), m[k]);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) all &= k0 + k >= tile || there<2 * V>(m[k]);
+          return all;
+        });
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
           if (k0 + k < tile) {
-            if (!__all_sync(0xffffffffu, there<2 * V>(m[k])))
-              ok = ok && await<2 * V>(map_place<C>(p, k0 + k, ch), true, m[k], p);
             Vec<V> mA, mB;
 #pragma unroll
             for (int i = 0; i < V; ++i) mA[i] = m[k][2 * i], mB[i] = m[k][2 * i + 1];
@@ -408,7 +422,10 @@ __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, in
           }
       }
       if (onto) {
-        if (!__all_sync(0xffffffffu, there<V>(in.e))) ok = ok && await<V>(state_place<C>(p, g - 1, ch), true, in.e, p);
+        ok = ok && until(p, [&] {
+               peek<V>(state_place<C>(p, g - 1, ch), in.e);
+               return there<V>(in.e);
+             });
         in = fma(A, in, B);
       } else {
         in = B;
@@ -443,7 +460,7 @@ __device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First
   for (;; at.next()) {
     Run now;
     now.tile = -1;
-    if (!wwait(smem_u32(&sh.full[at.stage]), at.parity, abort_flag, p.hdr, 72)) sh.stop[at.ring] = 1;
+    if (!hold(sh.full[at.stage], at.parity, abort_flag, p.hdr, 72)) sh.stop[at.ring] = 1;
     else if (sh.slot[at.stage].tile >= 0) now = run_of<C>(p, sh.slot[at.stage], BACK);
     if (now.tile >= 0) {
       Vec<V> A, B;
@@ -461,7 +478,7 @@ __device__ __forceinline__ void work(const ScanParams& p, TileSmem<C>& sh, First
     }
     if (old.tile >= 0) {
       // (a wait that gives up here leaves its tile, but comes to the next barrier like the others, and stops there)
-      if (wwait(smem_u32(&sh.carried[held.stage]), held.parity, abort_flag, p.hdr, 75)) {
+      if (hold(sh.carried[held.stage], held.parity, abort_flag, p.hdr, 75)) {
         Vec<V> in;
 #pragma unroll
         for (int i = 0; i < V; ++i) in[i] = sh.carry[held.stage][lane * V + i];

@@ -11,10 +11,10 @@
 //   the state that enters the tile is folded from the maps of a few tiles before it and a state further back, which
 //   every kGroup-th tile publishes,
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
-// So the data is read once and written once.  Three warps of a block serve the ones that work: one takes the tiles' numbers,
-// looks their segments up and has their data copied to shared memory (TMA), a few tiles ahead; one folds and publishes
-// the tiles' maps; one finds the state that enters a tile while the tile's own maps are formed.  (Rows that are not on 16-byte boundaries are
-// read by the others straight from memory, twice.)  The fold's order is fixed by the tile's number, whatever is finished
+// So the data is read once and written once.  Four warps of a block serve the ones that work: one takes the tiles' numbers,
+// looks their segments up and has their data copied to shared memory, a few tiles ahead (by TMA; rows that do not lie on
+// 16-byte boundaries in pieces of 16 bytes by the warp itself); one folds and publishes the tiles' maps; two find the
+// states that enter the tiles while the tiles' own maps are formed.  The fold's order is fixed by the tile's number, whatever is finished
 // first, so results do not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that
 // is waited for is a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.
 // What is published is its own flag: the places hold a NaN of all ones before, which is never written (no fences, and a
@@ -165,7 +165,7 @@ struct Run {
   int row, n, ch;   // first row, rows, first channel of the lane
   int b0;           // the first segment that starts at `row` or later
   uint32_t starts, ends;
-  bool on;
+  int left;         // channels from ch on (none: <= 0)
 };
 
 template <class C>
@@ -177,7 +177,7 @@ __device__ __forceinline__ Run run_of(const ScanParams& p, const Slot<C>& s, boo
   t.row = (back ? p.tiles - 1 - t.tile : t.tile) * C::kRows + (back ? C::W - 1 - warp : warp) * C::R;
   t.n = min(C::R, max(0, p.T - t.row));
   t.ch = (s.col * 32 + lane) * C::V;
-  t.on = t.ch < p.D;
+  t.left = p.D - t.ch;
   t.starts = s.starts[warp];
   t.ends = s.ends[warp];
   t.b0 = s.b0[warp];
@@ -189,10 +189,10 @@ __device__ __forceinline__ int segment_of(const Run& t, int r) { return t.b0 + _
 
 // A row of states for the lane's channels (zeros without them).
 template <int V>
-__device__ __forceinline__ Vec<V> state_row(const float* s, int64_t at, bool on) {
+__device__ __forceinline__ Vec<V> state_row(const float* s, int64_t at, int left) {
   Vec<V> v;
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = s && on ? s[at + i] : 0.f;
+  for (int i = 0; i < V; ++i) v[i] = s && i < left ? s[at + i] : 0.f;
   return v;
 }
 
@@ -220,10 +220,14 @@ __device__ __forceinline__ int tiles_each(const ScanParams& p) {
   return max(1, p.tiles * p.cols / static_cast<int>(gridDim.x));
 }
 
+// Arrivals for a tile's data: of the bytes, or of each lane's pieces.
+template <int kBytes> __device__ __forceinline__ constexpr int arrivals() { return kBytes > 0 ? 1 : 32; }
+
 // The feeding warp: takes the tiles' numbers, lays out their segments, asks for their data.  (One tile is taken ahead of
 // the place for it; with more of them its number came sooner, but the blocks came out of step: backward of T = 65536,
 // D = 2048 in bf16 305 us with one, 367 with three.)
-//   load(tile, col, stage): one lane's, issues the copies that complete on full[stage] (kBytes in all)
+//   load(row0, ch0, stage): issues the copies that complete on full[stage]: one lane those of kBytes in all (TMA), or,
+//                           with kBytes = 0, every lane its pieces
 template <class C, bool BACK, int kBytes, class Load>
 __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&& load) {
   using namespace sm100;
@@ -275,16 +279,18 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
         slot.tile = -1;
         mbar_arrive(smem_u32(&sh.known[s]));
         mbar_arrive(smem_u32(&sh.full[s]));
-        mbar_arrive(smem_u32(&sh.full[s]));
       }
+      if (lane < arrivals<kBytes>()) mbar_arrive(smem_u32(&sh.full[s]));
       return;
+    }
+    if constexpr (kBytes == 0) {
+      load(row0, col * C::kWidth, s);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s])) : "memory");
     }
     if (lane == 0) {
       if constexpr (kBytes > 0) {
         mbar_expect_tx(smem_u32(&sh.full[s]), kBytes);
         load(row0, col * C::kWidth, s);
-      } else {
-        mbar_arrive(smem_u32(&sh.full[s]));
       }
       slot.tile = tile;
       slot.col = col;
@@ -310,6 +316,8 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
     for (int j = max(0, issued - S); j < issued; ++j)
       while (!mbar_try_wait(smem_u32(&sh.full[j % S]), (j / S) & 1) && globaltimer() - t0 < 50000000ull) {
       }
+  } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 }
 
@@ -512,7 +520,7 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
       mbar_init(smem_u32(&sh.known[s]), 1);
-      mbar_init(smem_u32(&sh.full[s]), 2);  // the data's bytes, the slot
+      mbar_init(smem_u32(&sh.full[s]), 1 + arrivals<kBytes>());  // the slot, the data
       mbar_init(smem_u32(&sh.empty[s]), C::W);
       mbar_init(smem_u32(&sh.carried[s]), 1);
       sh.slot[s].tile = -1;
@@ -537,65 +545,94 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Where a run's rows are read: its tile's copy, or memory.
+// A tile's rows as they are copied: by TMA one behind the other, else each with the 16-byte pieces that hold it, at the
+// place in its pieces that its address has.
+template <class T, class C, bool TMA>
+constexpr int pitch() { return C::kWidth * static_cast<int>(sizeof(T)) + (TMA ? 0 : 16); }
+
+// One warp copies the rows [row0, row0 + kRows) of the tensor that has rows [0, T), from channel ch0 on.  (A piece holds
+// an element of the tensor at least, so none lies outside of its memory, though a piece at its edge or a tile's may hold
+// others' elements too, which nobody uses.)
+template <class T, class C>
+__device__ __forceinline__ void copy_rows(uint8_t* to, const void* from, int64_t rs, int row0, int T_rows, int ch0, int D) {
+  constexpr int kPitch = pitch<T, C, false>(), kPieces = kPitch / 16;
+  const uintptr_t base = reinterpret_cast<uintptr_t>(static_cast<const T*>(from) + row0 * rs + ch0);
+  const int bytes = min(C::kWidth, D - ch0) * static_cast<int>(sizeof(T)), lo = max(0, -row0), hi = T_rows - row0;
+  static_assert(C::kRows * kPieces % 32 == 0, "every lane has as many pieces");
+#pragma unroll 3
+  for (int i = threadIdx.x & 31; i < C::kRows * kPieces; i += 32) {
+    const int r = i / kPieces, at = (i - r * kPieces) * 16;
+    const uintptr_t row = base + static_cast<uint64_t>(r * rs) * sizeof(T), piece = (row & ~static_cast<uintptr_t>(15)) + at;
+    if (r >= lo && r < hi && piece < row + bytes)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + r * kPitch + at)), "l"(piece) : "memory");
+  }
+}
+
+// The copied rows of a run.  (Without TMA the lanes behind the last channel read what lies there; it gets nowhere.)
 template <class T, class C, bool TMA>
 struct Rows {
-  static constexpr int kRun = C::R;
-  const T* base;       // the thread's first element of stage 0, or of the tensor
-  int64_t step;        // between rows
-  __device__ __forceinline__ Rows(const uint8_t* smem, const void* global, int64_t rs) {
-    const int lane = threadIdx.x & 31;
-    base = TMA ? reinterpret_cast<const T*>(smem) + lane * C::V : static_cast<const T*>(global);
-    step = TMA ? C::kWidth : rs;
-  }
+  const uint8_t* tile;  // stage 0, at the lane's channels
+  const T* base;        // the tensor's row that is copied for row 0
+  int64_t rs;
+  struct Place {
+    const uint8_t* at;
+    int low;            // of the first row's address
+  };
+  __device__ __forceinline__ Rows(const uint8_t* smem, const void* global, int64_t rs_, int before)
+      : tile(smem + (threadIdx.x & 31) * C::V * sizeof(T)), base(static_cast<const T*>(global) - before * rs_), rs(rs_) {}
   // the run's first row
-  __device__ __forceinline__ const T* at(const Run& t, int stage, bool back) const {
-    const int warp = threadIdx.x >> 5;
-    if (TMA) return base + (stage * C::kRows + (back ? C::W - 1 - warp : warp) * C::R) * C::kWidth;
-    return base + t.row * step + t.ch;
+  __device__ __forceinline__ Place at(const Run& t, int stage, bool back) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kPitch = pitch<T, C, TMA>();
+    return {tile + (stage * C::kRows + (back ? C::W - 1 - warp : warp) * C::R) * kPitch,
+            TMA ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(base + t.row * rs + t.ch - lane * C::V) & 15)};
   }
-  __device__ __forceinline__ Pack<T, C::V> get(const T* first, int r, const Run& t) const {
+  __device__ __forceinline__ Pack<T, C::V> get(const Place& first, int r) const {
     if constexpr (TMA) {
-      return load_pack<T, C::V>(first + r * C::kWidth);
+      return load_pack<T, C::V>(reinterpret_cast<const T*>(first.at + r * pitch<T, C, true>()));
     } else {
-      Pack<T, C::V> none;
+      const int low = (first.low + r * (static_cast<unsigned>(rs) * static_cast<unsigned>(sizeof(T)))) & 15;
+      const T* const row = reinterpret_cast<const T*>(first.at + r * pitch<T, C, false>() + low);
+      Pack<T, C::V> v;
 #pragma unroll
-      for (int i = 0; i < C::V; ++i) none.set(i, 0.f);
-      return t.on ? load_pack<T, C::V>(first + r * step) : none;
+      for (int i = 0; i < C::V; ++i) v.e[i] = row[i];
+      return v;
     }
   }
 };
 
-// Rows of a run that holds a segment's boundary or the stream's end, in order or from the back.  From the copied tile one
-// after another; from memory all of them are asked for first.
-template <bool TMA, bool BACK = false, class A, class PA, class B, class PB, class F>
-__device__ __forceinline__ void rows_of(const A& a, PA pa, const B& b, PB pb, const Run& t, F&& f) {
-  constexpr int R = A::kRun;
+// A row's outputs.  Without TMA rows may begin anywhere: where a lane's pair straddles two words, its second channel is
+// stored with the next lane's first.  Every lane of the warp calls it.
+template <bool TMA, class T>
+__device__ __forceinline__ void put(T* to, const Pack<T, 2>& v, int left) {
   if constexpr (TMA) {
-#pragma unroll 1
-    for (int i = 0; i < t.n; ++i) {
-      const int r = BACK ? t.n - 1 - i : i;
-      f(r, a.get(pa, r, t), b.get(pb, r, t));
-    }
+    if (left > 0) store_pack(to, v);
+  } else if ((reinterpret_cast<uintptr_t>(to) & (2 * sizeof(T) - 1)) == 0) {  // (the same for every lane)
+    if (left > 1) store_pack(to, v);
+    else if (left == 1) to[0] = v.e[0];
   } else {
-    decltype(a.get(pa, 0, t)) va[R];
-    decltype(b.get(pb, 0, t)) vb[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < t.n) {
-        va[r] = a.get(pa, r, t);
-        vb[r] = b.get(pb, r, t);
-      }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int r = BACK ? R - 1 - i : i;
-      if (r < t.n) f(r, va[r], vb[r]);
-    }
+    Pack<T, 2> pair;
+    const int lane = threadIdx.x & 31;
+    pair.e[0] = v.e[1];
+    pair.e[1] = __shfl_down_sync(0xffffffffu, v.e[0], 1);
+    if (left > 2 && lane < 31) store_pack(to + 1, pair);
+    else if (left > 1) to[1] = v.e[1];
+    if (lane == 0 && left > 0) to[0] = v.e[0];
+  }
+}
+
+// Rows of a run that holds a segment's boundary or the stream's end, in order or from the back.
+template <bool BACK = false, class A, class PA, class B, class PB, class F>
+__device__ __forceinline__ void rows_of(const A& a, const PA& pa, const B& b, const PB& pb, const Run& t, F&& f) {
+#pragma unroll 1
+  for (int i = 0; i < t.n; ++i) {
+    const int r = BACK ? t.n - 1 - i : i;
+    f(r, a.get(pa, r), b.get(pb, r));
   }
 }
 
 // Bytes of a tile of one tensor.
-template <class T, class C> constexpr int tile_bytes() { return C::kRows * C::kWidth * static_cast<int>(sizeof(T)); }
+template <class T, class C, bool TMA> constexpr int tile_bytes() { return C::kRows * pitch<T, C, TMA>(); }
 template <class C> constexpr int head_bytes() { return (static_cast<int>(sizeof(TileSmem<C>)) + 127) / 128 * 128; }
 
 struct Maps {
@@ -655,34 +692,39 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   extern __shared__ __align__(128) uint8_t smem[];
   TileSmem<C>& sh = *reinterpret_cast<TileSmem<C>*>(smem);
   if (*reinterpret_cast<volatile int32_t*>(&p.hdr->status) == VA_ERR_BAD_SEQLENS) return;
-  constexpr int kX = tile_bytes<TX, C>(), kG = tile_bytes<TG, C>();
+  constexpr int kX = tile_bytes<TX, C, TMA>(), kG = tile_bytes<TG, C, TMA>();
   uint8_t* const x_smem = smem + head_bytes<C>();
   uint8_t* const g_smem = x_smem + kX * C::S;
-  const Rows<TX, C, TMA> xs(x_smem, p.x, p.x_rs);
-  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs);
+  const Rows<TX, C, TMA> xs(x_smem, p.x, p.x_rs, 0);
+  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs, 0);
   const auto load = [&](int row0, int ch0, int stage) {
-    const uint32_t bar = smem_u32(&sh.full[stage]);
-    tma_load_2d(smem_u32(x_smem + stage * kX), &maps.a, bar, ch0, row0);
-    tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
+    if constexpr (TMA) {
+      const uint32_t bar = smem_u32(&sh.full[stage]);
+      tma_load_2d(smem_u32(x_smem + stage * kX), &maps.a, bar, ch0, row0);
+      tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
+    } else {
+      copy_rows<TX, C>(x_smem + stage * kX, p.x, p.x_rs, row0, p.T, ch0, p.D);
+      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D);
+    }
   };
   const auto step = [&](const Pack<TX, V>& x, const Vec<V>& g, Vec<V>& h) { h = fma(decay(g), h, wide_of(x)); };
   const auto start = [&](const Pack<TX, V>& x, const Vec<V>& g, const Run& t, int r, Vec<V>& h) {  // a segment's first row
     h = wide_of(x);  // (x itself without h0, whatever its decay is)
-    if (p.h0) h = fma(decay(g), state_row<V>(p.h0, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on), h);
+    if (p.h0) h = fma(decay(g), state_row<V>(p.h0, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.left), h);
   };
   const auto first = [&](const Run& t, int stage, Vec<V>& A, Vec<V>& B) {
     A = B = fill<V>(0.f);
-    const TX* const xa = xs.at(t, stage, false);
-    const TG* const ga = gs.at(t, stage, false);
+    const auto xa = xs.at(t, stage, false);
+    const auto ga = gs.at(t, stage, false);
     if (t.starts == 0 && t.n == R) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const Vec<V> g = wide_of(gs.get(ga, r, t));
+        const Vec<V> g = wide_of(gs.get(ga, r));
         A = add(A, g);
-        step(xs.get(xa, r, t), g, B);
+        step(xs.get(xa, r), g, B);
       }
     } else {
-      rows_of<TMA>(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
+      rows_of(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
         const Vec<V> g = wide_of(gr);
         A = add(A, g);
         if ((t.starts >> r) & 1u) start(x, g, t, r, B);
@@ -695,24 +737,25 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   };
   const auto second = [&](const Run& t, int stage, Vec<V>& h) {
     TH* out = static_cast<TH*>(p.out) + t.row * p.out_rs + t.ch;
-    const TX* const xa = xs.at(t, stage, false);
-    const TG* const ga = gs.at(t, stage, false);
+    const auto xa = xs.at(t, stage, false);
+    const auto ga = gs.at(t, stage, false);
     if (t.starts == 0 && t.n == R && (!p.last || t.ends == 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        step(xs.get(xa, r, t), wide_of(gs.get(ga, r, t)), h);
-        if (t.on) store_pack(out + r * p.out_rs, narrow<TH, V>(h));
+        step(xs.get(xa, r), wide_of(gs.get(ga, r)), h);
+        put<TMA>(out + r * p.out_rs, narrow<TH, V>(h), t.left);
       }
     } else {
-      rows_of<TMA>(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
+      rows_of(xs, xa, gs, ga, t, [&](int r, const Pack<TX, V>& x, const Pack<TG, V>& gr) {
         const Vec<V> g = wide_of(gr);
         if ((t.starts >> r) & 1u) start(x, g, t, r, h);
         else step(x, g, h);
-        if (t.on) store_pack(out + r * p.out_rs, narrow<TH, V>(h));
-        if (p.last && t.on && ((t.ends >> r) & 1u)) {
+        put<TMA>(out + r * p.out_rs, narrow<TH, V>(h), t.left);
+        if (p.last && ((t.ends >> r) & 1u)) {
           float* last = p.last + static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch;
 #pragma unroll
-          for (int i = 0; i < V; ++i) last[i] = h[i];
+          for (int i = 0; i < V; ++i)
+            if (i < t.left) last[i] = h[i];
         }
       });
     }
@@ -729,22 +772,29 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   extern __shared__ __align__(128) uint8_t smem[];
   TileSmem<C>& sh = *reinterpret_cast<TileSmem<C>*>(smem);
   if (*reinterpret_cast<volatile int32_t*>(&p.hdr->status) == VA_ERR_BAD_SEQLENS) return;
-  constexpr int kH = tile_bytes<TH, C>(), kG = tile_bytes<TG, C>();
+  constexpr int kH = tile_bytes<TH, C, TMA>(), kG = tile_bytes<TG, C, TMA>();
   uint8_t* const d_smem = smem + head_bytes<C>();
   uint8_t* const g_smem = d_smem + kH * C::S;
   uint8_t* const h_smem = g_smem + kG * C::S;
-  const Rows<TH, C, TMA> ds(d_smem, p.x, p.x_rs), hs(h_smem, p.h, p.h_rs);
-  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs);
+  const Rows<TH, C, TMA> ds(d_smem, p.x, p.x_rs, 0), hs(h_smem, p.h, p.h_rs, 1);
+  const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs, 0);
   const auto load = [&](int row0, int ch0, int stage) {
-    const uint32_t bar = smem_u32(&sh.full[stage]);
-    tma_load_2d(smem_u32(d_smem + stage * kH), &maps.a, bar, ch0, row0);
-    tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
-    tma_load_2d(smem_u32(h_smem + stage * kH), &maps.c, bar, ch0, row0 - 1);  // the rows before (zeros before the first)
+    // (of h the rows before; there is none before the first, and a segment's first row asks for none)
+    if constexpr (TMA) {
+      const uint32_t bar = smem_u32(&sh.full[stage]);
+      tma_load_2d(smem_u32(d_smem + stage * kH), &maps.a, bar, ch0, row0);
+      tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
+      tma_load_2d(smem_u32(h_smem + stage * kH), &maps.c, bar, ch0, row0 - 1);
+    } else {
+      copy_rows<TH, C>(d_smem + stage * kH, p.x, p.x_rs, row0, p.T, ch0, p.D);
+      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D);
+      copy_rows<TH, C>(h_smem + stage * kH, p.h, p.h_rs, row0 - 1, p.T, ch0, p.D);
+    }
   };
   const auto first = [&](const Run& t, int stage, Vec<V>& A, Vec<V>& B) {
     A = B = fill<V>(0.f);
-    const TH* const da = ds.at(t, stage, true);
-    const TG* const ga = gs.at(t, stage, true);
+    const auto da = ds.at(t, stage, true);
+    const auto ga = gs.at(t, stage, true);
     const auto step = [&](const Pack<TH, V>& d, const Pack<TG, V>& gr) {
       const Vec<V> g = wide_of(gr);
       A = add(A, g);
@@ -752,10 +802,10 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
     };
     if (t.ends == 0 && t.n == R) {
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r) step(ds.get(da, r, t), gs.get(ga, r, t));
+      for (int r = R - 1; r >= 0; --r) step(ds.get(da, r), gs.get(ga, r));
     } else {
-      rows_of<TMA, true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
-        if ((t.ends >> r) & 1u) B = state_row<V>(p.dlast, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.on);
+      rows_of<true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
+        if ((t.ends >> r) & 1u) B = state_row<V>(p.dlast, static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch, t.left);
         step(d, g);
       });
     }
@@ -766,33 +816,32 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   const auto second = [&](const Run& t, int stage, Vec<V>& f) {
     TX* dx = static_cast<TX*>(p.out) + t.row * p.out_rs + t.ch;
     TG* dg = static_cast<TG*>(p.dg) + t.row * p.dg_rs + t.ch;
-    const TH* const da = ds.at(t, stage, true);
-    const TG* const ga = gs.at(t, stage, true);
-    const TH* const ha = hs.at(t, stage, true) - (TMA ? 0 : p.h_rs);
+    const auto da = ds.at(t, stage, true);
+    const auto ga = gs.at(t, stage, true);
+    const auto ha = hs.at(t, stage, true);
     // before: the row before's h, at a segment's first row h0 (none: 0, and so is the decay's gradient)
     const auto step = [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g, const Vec<V>& before, bool none) {
       const Vec<V> e = add(wide_of(d), f);
       f = mul(decay(wide_of(g)), e);
       const Vec<V> q = none ? fill<V>(0.f) : mul(f, before);
-      if (t.on) {
-        store_pack(dx + r * p.out_rs, narrow<TX, V>(e));
-        store_pack(dg + r * p.dg_rs, narrow<TG, V>(q));
-      }
+      put<TMA>(dx + r * p.out_rs, narrow<TX, V>(e), t.left);
+      put<TMA>(dg + r * p.dg_rs, narrow<TG, V>(q), t.left);
     };
     if (t.ends == 0 && t.starts == 0 && t.n == R) {
 #pragma unroll
       for (int r = R - 1; r >= 0; --r)
-        step(r, ds.get(da, r, t), gs.get(ga, r, t), wide_of(hs.get(ha, r, t)), false);
+        step(r, ds.get(da, r), gs.get(ga, r), wide_of(hs.get(ha, r)), false);
     } else {
-      rows_of<TMA, true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
+      rows_of<true>(ds, da, gs, ga, t, [&](int r, const Pack<TH, V>& d, const Pack<TG, V>& g) {
         const int64_t state = static_cast<int64_t>(segment_of(t, r)) * p.D + t.ch;
         const bool start = (t.starts >> r) & 1u;
-        if ((t.ends >> r) & 1u) f = state_row<V>(p.dlast, state, t.on);
-        const Vec<V> before = start ? state_row<V>(p.h0, state, t.on) : wide_of(hs.get(ha, r, t));
+        if ((t.ends >> r) & 1u) f = state_row<V>(p.dlast, state, t.left);
+        const Vec<V> before = start ? state_row<V>(p.h0, state, t.left) : wide_of(hs.get(ha, r));
         step(r, d, g, before, start && !p.h0);
-        if (p.last && start && t.on) {
+        if (p.last && start) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) p.last[state + i] = f[i];
+          for (int i = 0; i < V; ++i)
+            if (i < t.left) p.last[state + i] = f[i];
         }
       });
     }
@@ -903,44 +952,43 @@ cudaError_t run_blocks(int stage, int back, void (*kernel)(ScanParams, Maps), si
   return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), smem, st, p, maps);
 }
 
-template <int V> using FwdShape = Shape<V, 8, 16, 3, 2>;
-// (from memory: short runs, whose rows are all asked for at once)
-template <int V> using FwdPlain = Shape<V, 8, 8, 3, 2>;
-template <int V> using BwdShape = Shape<V, 8, 8, 3, 2>;
-template <int V> using BwdPlain = Shape<V, 8, 8, 3, 2>;
+using FwdShape = Shape<2, 8, 16, 3, 2>;
+using BwdShape = Shape<2, 8, 8, 3, 2>;
+using CopyShape = Shape<2, 8, 8, 3, 2>;  // (rows by pieces: two blocks an SM still fit)
 
-// Two channels a lane where rows lie on boundaries of two elements, else one; copied tiles where they lie on 16 bytes.
+// Tiles come by TMA where the inputs' rows lie on 16-byte boundaries and the outputs' on pairs of channels.
 template <class TX, class TG, class TH>
 cudaError_t run_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  using C = FwdShape<2>;
-  const bool two =
-      p.D % 2 == 0 && steps_of<TX>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) && steps_of<TH>(p.out, p.out_rs, 2);
+  using C = FwdShape;
   Maps maps{};
-  if (!two) return run_blocks<FwdPlain<1>>(stage, 0, scan_fwd_kernel<TX, TG, TH, FwdPlain<1>, false>, 0, p, maps, ws, st);
-  if (rows16<TX>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs)) {
+  if (p.D % 2 == 0 && rows16<TX>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && steps_of<TH>(p.out, p.out_rs, 2)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TX) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows)))
       return cudaErrorInvalidValue;
-    return run_blocks<C>(stage, 0, scan_fwd_kernel<TX, TG, TH, C, true>, tile_bytes<TX, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
+    return run_blocks<C>(stage, 0, scan_fwd_kernel<TX, TG, TH, C, true>,
+                         tile_bytes<TX, C, true>() + tile_bytes<TG, C, true>(), p, maps, ws, st);
   }
-  return run_blocks<FwdPlain<2>>(stage, 0, scan_fwd_kernel<TX, TG, TH, FwdPlain<2>, false>, 0, p, maps, ws, st);
+  using P = CopyShape;
+  return run_blocks<P>(stage, 0, scan_fwd_kernel<TX, TG, TH, P, false>,
+                       tile_bytes<TX, P, false>() + tile_bytes<TG, P, false>(), p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
 cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
-  using C = BwdShape<2>;
-  const bool two = p.D % 2 == 0 && steps_of<TH>(p.x, p.x_rs, 2) && steps_of<TG>(p.g, p.g_rs, 2) &&
-                   steps_of<TH>(p.h, p.h_rs, 2) && steps_of<TX>(p.out, p.out_rs, 2) && steps_of<TG>(p.dg, p.dg_rs, 2);
+  using C = BwdShape;
   Maps maps{};
-  if (!two) return run_blocks<BwdPlain<1>>(stage, 1, scan_bwd_kernel<TX, TG, TH, BwdPlain<1>, false>, 0, p, maps, ws, st);
-  if (rows16<TH>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && rows16<TH>(p.h, p.h_rs)) {
+  if (p.D % 2 == 0 && rows16<TH>(p.x, p.x_rs) && rows16<TG>(p.g, p.g_rs) && rows16<TH>(p.h, p.h_rs) &&
+      steps_of<TX>(p.out, p.out_rs, 2) && steps_of<TG>(p.dg, p.dg_rs, 2)) {
     if (stage == 1 && !(tmap_matrix(&maps.a, p.x, sizeof(TH) == 2, p.T, p.D, p.x_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.b, p.g, sizeof(TG) == 2, p.T, p.D, p.g_rs, C::kWidth, C::kRows) &&
                         tmap_matrix(&maps.c, p.h, sizeof(TH) == 2, p.T, p.D, p.h_rs, C::kWidth, C::kRows)))
       return cudaErrorInvalidValue;
-    return run_blocks<C>(stage, 1, scan_bwd_kernel<TX, TG, TH, C, true>, 2 * tile_bytes<TH, C>() + tile_bytes<TG, C>(), p, maps, ws, st);
+    return run_blocks<C>(stage, 1, scan_bwd_kernel<TX, TG, TH, C, true>,
+                         2 * tile_bytes<TH, C, true>() + tile_bytes<TG, C, true>(), p, maps, ws, st);
   }
-  return run_blocks<BwdPlain<2>>(stage, 1, scan_bwd_kernel<TX, TG, TH, BwdPlain<2>, false>, 0, p, maps, ws, st);
+  using P = CopyShape;
+  return run_blocks<P>(stage, 1, scan_bwd_kernel<TX, TG, TH, P, false>,
+                       2 * tile_bytes<TH, P, false>() + tile_bytes<TG, P, false>(), p, maps, ws, st);
 }
 
 template <class TX, class TG, class TH>
@@ -958,8 +1006,7 @@ cudaError_t run_step(ScanParams p, void* ws, cudaStream_t st) {
 
 size_t scan_workspace(int T, int D) {
   size_t n = 0;
-  for (int rows : {FwdShape<2>::kRows, FwdPlain<2>::kRows, BwdShape<2>::kRows, BwdPlain<2>::kRows})
-    n = std::max({n, layout_of(T, D, rows, 32).total, layout_of(T, D, rows, 64).total});
+  for (int rows : {FwdShape::kRows, BwdShape::kRows, CopyShape::kRows}) n = std::max(n, layout_of(T, D, rows, FwdShape::kWidth).total);
   return n;
 }
 

@@ -13,13 +13,17 @@
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
 // So the data is read once and written once.  Four warps of a block serve the ones that work: one takes the tiles' numbers,
 // looks their segments up and has their data copied to shared memory, a few tiles ahead (by TMA; rows that do not lie on
-// 16-byte boundaries in pieces of 16 bytes by the warp itself); one folds and publishes the tiles' maps; two find the
+// 16-byte boundaries in pieces of 16 bytes, by warps of their own); one folds and publishes the tiles' maps; two find the
 // states that enter the tiles while the tiles' own maps are formed.  The fold's order is fixed by the tile's number, whatever is finished
 // first, so results do not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that
 // is waited for is a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.
 // What is published is its own flag: the places hold a NaN of all ones before, which is never written (no fences, and a
 // single trip to L2 where it is there).  A segment's start (backward: its end) inside a run replaces the state instead of multiplying
 // it by zero, so nothing of another segment gets in, infinities and NaN included, and no tile waits across one.
+//
+// Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 159 us
+// forward and 279 backward (the bytes at the copy rate: 119, 198), fp32 decays 234 and 413 (198, 357); T = 8192, D = 4096, 53 and 78
+// (30, 50); T = 30000, D = 2047, rows off their boundaries, 155 and 222 (54, 91).
 //
 // A = exp(sum of g), rounded once, and not the product of the a: the approximate exponential of an a near 1 has a
 // bias, which would add up over thousands of rows (h off by 2e-5 for a decay of 0.9995 a row).
@@ -37,8 +41,8 @@ namespace {
 
 // The last tile of every kGroup publishes the state after it.  A tile folds the maps of the kBack groups before its own
 // and of those before it in its own, onto the state before them: the further back, the surer it is there, and the
-// more there is to fold (T = 65536, D = 2048, backward, us: with bf16 / fp32 decays kGroup, kBack = 4, 2 413 / 442; 8, 1 384 / 429;
-// 8, 2 350 / 432; 8, 3 354 / 480; 8, 4 379 / 545).
+// more there is to fold (T = 65536, D = 2048, one segment, backward, us: with bf16 / fp32 decays kGroup, kBack = 4, 1 295 /
+// 423; 4, 2 303 / 425; 8, 1 293 / 416; 8, 2 279 / 413; 8, 3 282 / 433).
 constexpr int kGroup = 8, kBack = 2;
 constexpr int kPrepThreads = 1024;
 // Words of what the first launch looks up for a tile: the first segment that starts at its first row or later, the
@@ -52,10 +56,11 @@ constexpr int kRings = 3;
 
 // How a block works: W warps, each with a run of R rows of 32 V channels; S tiles on their way or in work; at most M
 // blocks an SM (shared memory may allow fewer).
-template <int V_, int W_, int R_, int S_, int M_>
+// (K copying warps where TMA does not)
+template <int V_, int W_, int R_, int S_, int M_, int K_ = 0>
 struct Shape {
-  static constexpr int V = V_, W = W_, R = R_, S = S_, M = M_;
-  static constexpr int kThreads = 32 * (W_ + 2 + kResolvers), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
+  static constexpr int V = V_, W = W_, R = R_, S = S_, M = M_, K = K_;
+  static constexpr int kThreads = 32 * (W_ + 2 + kResolvers + K_), kRows = W_ * R_, kWidth = 32 * V_, kWords = kRows / 32 + 1;
   static_assert(3 + kWords <= kRecord, "a tile's bits fit its record");
 };
 
@@ -220,14 +225,9 @@ __device__ __forceinline__ int tiles_each(const ScanParams& p) {
   return max(1, p.tiles * p.cols / static_cast<int>(gridDim.x));
 }
 
-// Arrivals for a tile's data: of the bytes, or of each lane's pieces.
-template <int kBytes> __device__ __forceinline__ constexpr int arrivals() { return kBytes > 0 ? 1 : 32; }
-
-// The feeding warp: takes the tiles' numbers, lays out their segments, asks for their data.  (One tile is taken ahead of
-// the place for it; with more of them its number came sooner, but the blocks came out of step: backward of T = 65536,
-// D = 2048 in bf16 305 us with one, 367 with three.)
-//   load(row0, ch0, stage): issues the copies that complete on full[stage]: one lane those of kBytes in all (TMA), or,
-//                           with kBytes = 0, every lane its pieces
+// The feeding warp: takes the tiles' numbers, lays out their segments, asks for their data.  (One tile's number is taken
+// ahead of the place for it, so that the next one's record is there when a place is.)
+//   load(row0, ch0, stage, 0): issues the copies of kBytes that complete on full[stage] (one lane)
 template <class C, bool BACK, int kBytes, class Load>
 __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&& load) {
   using namespace sm100;
@@ -280,17 +280,13 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
         mbar_arrive(smem_u32(&sh.known[s]));
         mbar_arrive(smem_u32(&sh.full[s]));
       }
-      if (lane < arrivals<kBytes>()) mbar_arrive(smem_u32(&sh.full[s]));
+      if (kBytes > 0 && lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
       return;
-    }
-    if constexpr (kBytes == 0) {
-      load(row0, col * C::kWidth, s);
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s])) : "memory");
     }
     if (lane == 0) {
       if constexpr (kBytes > 0) {
         mbar_expect_tx(smem_u32(&sh.full[s]), kBytes);
-        load(row0, col * C::kWidth, s);
+        load(row0, col * C::kWidth, s, 0);
       }
       slot.tile = tile;
       slot.col = col;
@@ -316,8 +312,6 @@ __device__ __forceinline__ void feed(const ScanParams& p, TileSmem<C>& sh, Load&
     for (int j = max(0, issued - S); j < issued; ++j)
       while (!mbar_try_wait(smem_u32(&sh.full[j % S]), (j / S) & 1) && globaltimer() - t0 < 50000000ull) {
       }
-  } else {
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 }
 
@@ -333,6 +327,24 @@ struct Turn {
     ring = ring + 1 == kRings ? 0 : ring + 1;
   }
 };
+
+// A copying warp (without TMA): its part of every tile's rows; a tile is there when every lane's pieces are.
+template <class C, bool BACK, class Load>
+__device__ __forceinline__ void copy(const ScanParams& p, TileSmem<C>& sh, int part, Load&& load) {
+  using namespace sm100;
+  volatile int* abort_flag = &sh.abort_flag;
+  for (Turn<C> at;; at.next()) {
+    if (!hold(sh.known[at.stage], at.parity, abort_flag, p.hdr, 77)) break;
+    const int tile = sh.slot[at.stage].tile, col = sh.slot[at.stage].col;
+    if (tile < 0) {
+      mbar_arrive(smem_u32(&sh.full[at.stage]));
+      break;
+    }
+    load((BACK ? p.tiles - 1 - tile : tile) * C::kRows, col * C::kWidth, at.stage, part);
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[at.stage])) : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // (given up: those on their way land before the block ends)
+}
 
 // The publishing warp: folds the runs' maps of a tile into the tile's and publishes it, and after a group's last tile the
 // state.
@@ -520,7 +532,7 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
       mbar_init(smem_u32(&sh.known[s]), 1);
-      mbar_init(smem_u32(&sh.full[s]), 1 + arrivals<kBytes>());  // the slot, the data
+      mbar_init(smem_u32(&sh.full[s]), 1 + (kBytes > 0 ? 1 : 32 * C::K));  // the slot, the data
       mbar_init(smem_u32(&sh.empty[s]), C::W);
       mbar_init(smem_u32(&sh.carried[s]), 1);
       sh.slot[s].tile = -1;
@@ -535,7 +547,8 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
   if (warp < C::W) work<C, BACK>(p, sh, first, second);
   else if (warp == C::W) feed<C, BACK, kBytes>(p, sh, load);
   else if (warp == C::W + 1) publish<C>(p, sh);
-  else resolve<C>(p, sh, warp - C::W - 2);
+  else if (warp < C::W + 2 + kResolvers) resolve<C>(p, sh, warp - C::W - 2);
+  else if constexpr (C::K > 0) copy<C, BACK>(p, sh, warp - C::W - 2 - kResolvers, load);
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
@@ -550,17 +563,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
 template <class T, class C, bool TMA>
 constexpr int pitch() { return C::kWidth * static_cast<int>(sizeof(T)) + (TMA ? 0 : 16); }
 
-// One warp copies the rows [row0, row0 + kRows) of the tensor that has rows [0, T), from channel ch0 on.  (A piece holds
+// The part `part` of K of the rows [row0, row0 + kRows) of the tensor that has rows [0, T), from channel ch0 on, by a warp.  (A piece holds
 // an element of the tensor at least, so none lies outside of its memory, though a piece at its edge or a tile's may hold
 // others' elements too, which nobody uses.)
 template <class T, class C>
-__device__ __forceinline__ void copy_rows(uint8_t* to, const void* from, int64_t rs, int row0, int T_rows, int ch0, int D) {
+__device__ __forceinline__ void copy_rows(uint8_t* to, const void* from, int64_t rs, int row0, int T_rows, int ch0, int D,
+                                          int part) {
   constexpr int kPitch = pitch<T, C, false>(), kPieces = kPitch / 16;
   const uintptr_t base = reinterpret_cast<uintptr_t>(static_cast<const T*>(from) + row0 * rs + ch0);
   const int bytes = min(C::kWidth, D - ch0) * static_cast<int>(sizeof(T)), lo = max(0, -row0), hi = T_rows - row0;
-  static_assert(C::kRows * kPieces % 32 == 0, "every lane has as many pieces");
 #pragma unroll 3
-  for (int i = threadIdx.x & 31; i < C::kRows * kPieces; i += 32) {
+  for (int i = part * 32 + (threadIdx.x & 31); i < C::kRows * kPieces; i += 32 * C::K) {
     const int r = i / kPieces, at = (i - r * kPieces) * 16;
     const uintptr_t row = base + static_cast<uint64_t>(r * rs) * sizeof(T), piece = (row & ~static_cast<uintptr_t>(15)) + at;
     if (r >= lo && r < hi && piece < row + bytes)
@@ -697,14 +710,14 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   uint8_t* const g_smem = x_smem + kX * C::S;
   const Rows<TX, C, TMA> xs(x_smem, p.x, p.x_rs, 0);
   const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs, 0);
-  const auto load = [&](int row0, int ch0, int stage) {
+  const auto load = [&](int row0, int ch0, int stage, int part) {
     if constexpr (TMA) {
       const uint32_t bar = smem_u32(&sh.full[stage]);
       tma_load_2d(smem_u32(x_smem + stage * kX), &maps.a, bar, ch0, row0);
       tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
     } else {
-      copy_rows<TX, C>(x_smem + stage * kX, p.x, p.x_rs, row0, p.T, ch0, p.D);
-      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D);
+      copy_rows<TX, C>(x_smem + stage * kX, p.x, p.x_rs, row0, p.T, ch0, p.D, part);
+      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D, part);
     }
   };
   const auto step = [&](const Pack<TX, V>& x, const Vec<V>& g, Vec<V>& h) { h = fma(decay(g), h, wide_of(x)); };
@@ -778,7 +791,7 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
   uint8_t* const h_smem = g_smem + kG * C::S;
   const Rows<TH, C, TMA> ds(d_smem, p.x, p.x_rs, 0), hs(h_smem, p.h, p.h_rs, 1);
   const Rows<TG, C, TMA> gs(g_smem, p.g, p.g_rs, 0);
-  const auto load = [&](int row0, int ch0, int stage) {
+  const auto load = [&](int row0, int ch0, int stage, int part) {
     // (of h the rows before; there is none before the first, and a segment's first row asks for none)
     if constexpr (TMA) {
       const uint32_t bar = smem_u32(&sh.full[stage]);
@@ -786,9 +799,9 @@ __global__ void __launch_bounds__(C::kThreads, C::M)
       tma_load_2d(smem_u32(g_smem + stage * kG), &maps.b, bar, ch0, row0);
       tma_load_2d(smem_u32(h_smem + stage * kH), &maps.c, bar, ch0, row0 - 1);
     } else {
-      copy_rows<TH, C>(d_smem + stage * kH, p.x, p.x_rs, row0, p.T, ch0, p.D);
-      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D);
-      copy_rows<TH, C>(h_smem + stage * kH, p.h, p.h_rs, row0 - 1, p.T, ch0, p.D);
+      copy_rows<TH, C>(d_smem + stage * kH, p.x, p.x_rs, row0, p.T, ch0, p.D, part);
+      copy_rows<TG, C>(g_smem + stage * kG, p.g, p.g_rs, row0, p.T, ch0, p.D, part);
+      copy_rows<TH, C>(h_smem + stage * kH, p.h, p.h_rs, row0 - 1, p.T, ch0, p.D, part);
     }
   };
   const auto first = [&](const Run& t, int stage, Vec<V>& A, Vec<V>& B) {
@@ -954,7 +967,9 @@ cudaError_t run_blocks(int stage, int back, void (*kernel)(ScanParams, Maps), si
 
 using FwdShape = Shape<2, 8, 16, 3, 2>;
 using BwdShape = Shape<2, 8, 8, 3, 2>;
-using CopyShape = Shape<2, 8, 8, 3, 2>;  // (rows by pieces: two blocks an SM still fit)
+// (fp32 rows are twice the pieces: T = 30000, D = 1022 128 us with two copying warps, 117 with four; bf16 rows, D = 2047,
+// 155 and 162; one, 151 and 165)
+template <class T> using CopyShape = Shape<2, 8, 8, 3, 2, sizeof(T) == 4 ? 4 : 2>;
 
 // Tiles come by TMA where the inputs' rows lie on 16-byte boundaries and the outputs' on pairs of channels.
 template <class TX, class TG, class TH>
@@ -968,7 +983,7 @@ cudaError_t run_fwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
     return run_blocks<C>(stage, 0, scan_fwd_kernel<TX, TG, TH, C, true>,
                          tile_bytes<TX, C, true>() + tile_bytes<TG, C, true>(), p, maps, ws, st);
   }
-  using P = CopyShape;
+  using P = CopyShape<TG>;
   return run_blocks<P>(stage, 0, scan_fwd_kernel<TX, TG, TH, P, false>,
                        tile_bytes<TX, P, false>() + tile_bytes<TG, P, false>(), p, maps, ws, st);
 }
@@ -986,7 +1001,7 @@ cudaError_t run_bwd(int stage, const ScanParams& p, void* ws, cudaStream_t st) {
     return run_blocks<C>(stage, 1, scan_bwd_kernel<TX, TG, TH, C, true>,
                          2 * tile_bytes<TH, C, true>() + tile_bytes<TG, C, true>(), p, maps, ws, st);
   }
-  using P = CopyShape;
+  using P = CopyShape<TG>;
   return run_blocks<P>(stage, 1, scan_bwd_kernel<TX, TG, TH, P, false>,
                        2 * tile_bytes<TH, P, false>() + tile_bytes<TG, P, false>(), p, maps, ws, st);
 }
@@ -1006,7 +1021,7 @@ cudaError_t run_step(ScanParams p, void* ws, cudaStream_t st) {
 
 size_t scan_workspace(int T, int D) {
   size_t n = 0;
-  for (int rows : {FwdShape::kRows, BwdShape::kRows, CopyShape::kRows}) n = std::max(n, layout_of(T, D, rows, FwdShape::kWidth).total);
+  for (int rows : {FwdShape::kRows, BwdShape::kRows, CopyShape<float>::kRows}) n = std::max(n, layout_of(T, D, rows, FwdShape::kWidth).total);
   return n;
 }
 

@@ -255,6 +255,36 @@ def test_strides_and_in_place(va):
         assert bool((wide[:, :, :off] == 9).all()) and bool((wide[:, :, off + D:] == 9).all())
 
 
+@pytest.mark.parametrize("D", [63, 64, 65, 130])
+@pytest.mark.parametrize("xt,gt", TYPES)
+def test_rows_off_their_boundaries(va, xt, gt, D):
+    """Each tensor with an offset and a row stride of its own, some on 16 bytes and others not, outputs on odd elements;
+    nothing beside the rows changes."""
+    lengths = [70, 1, 129, 64]
+    m = make(lengths, D, xt, gt)
+    T, ht = sum(lengths), torch.promote_types(xt, gt)
+    cu = m["cu"].to(DEV)
+    rh, eh, rl, el = reference(m["x"], m["g"], lengths, m["h0"])
+    dx, ex, dg, eg, d0, e0 = reference(m["x"], m["g"], lengths, m["h0"], m["dh"], m["dlast"])
+    for offs in ((0, 0, 0, 0, 0, 0), (0, 8, 0, 1, 3, 0), (1, 0, 16, 0, 2, 7), (5, 3, 1, 7, 0, 1)):
+        wides, views = [], []
+        for i, (off, dt) in enumerate(zip(offs, (xt, gt, ht, ht, xt, gt))):
+            w = torch.full((T, D + off + (0, 3, 8)[i % 3]), 9.0, device=DEV, dtype=dt)
+            wides.append((w, off))
+            views.append(w[:, off:off + D])
+        xv, gv, hv, dv, ov, qv = views
+        xv.copy_(m["x"]), gv.copy_(m["g"]), dv.copy_(m["dh"])
+        _, last = va.varlen_scan_fwd(xv, gv, cu, m["h0"].to(DEV), h_last=True, out=hv, check_status=True)
+        close(hv, rh, eh)
+        close(last, rl, el)
+        _, _, s0 = va.varlen_scan_bwd(dv, hv, gv, cu, m["h0"].to(DEV), m["dlast"].to(DEV), dx=ov, dlog_decay=qv, check_status=True)
+        close(ov, dx, ex)
+        close(qv, dg, eg)
+        close(s0, d0, e0)
+        for w, off in wides:
+            assert bool((w[:, :off] == 9).all()) and bool((w[:, off + D:] == 9).all())
+
+
 @pytest.mark.parametrize("cu", [[0, 5, 5, 90], [0, 50, 40, 90], [1, 50, 60, 90], [0, 50, 60, 89], [0, 50, 2 ** 31 - 1, 90],
                                 [0, -7, 60, 90]])
 def test_bad_boundaries(va, cu):

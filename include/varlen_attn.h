@@ -569,7 +569,7 @@ typedef struct {
  *   q_dev [T, Hq, d], k_dev [T, Hkv, d]  in; head elements contiguous
  *   position_ids_dev  int32 [T]
  *   q_weight_dev, k_weight_dev  [d], NULL: ones
- *   inv_freq_dev      float [rot / 2] (NULL when rot is 0)
+ *   inv_freq_dev      float [rot / 2], finite and below 2^24 (NULL when rot is 0)
  *   q_out_dev, k_out_dev  out; may be the inputs themselves (same strides)
  * Pointers 16-byte aligned, strides multiples of 8 elements, as the attention's.  T = 0 does nothing.  Arithmetic in
  * fp32, rounded once.  Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED (d, rot), VA_ERR_CUDA.  Asynchronous. */

@@ -679,7 +679,7 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tenso
     """Root-mean-square norm of every head with the position rotation: returns (q_out, k_out).
 
     ``q`` [T, Hq, d] and ``k`` [T, Hkv, d] CUDA fp32 or bf16 (views of a fused projection are fine); ``q_weight`` /
-    ``k_weight`` [d] fp32 or bf16 (None: ones); ``inv_freq`` fp32 [rot / 2]: the first rot elements of a head
+    ``k_weight`` [d] fp32 or bf16 (None: ones); ``inv_freq`` fp32 [rot / 2], finite: the first rot elements of a head
     are turned by position * inv_freq, in pairs (i, i + rot / 2) or, ``interleaved``, (2 i, 2 i + 1)
     (None: none is).  ``q_out`` / ``k_out`` None allocates them contiguous; q and k themselves are fine."""
     qs = ks = None

@@ -621,7 +621,8 @@ cudaError_t run_fwd(const LogprobParams& p, int sms, cudaStream_t st) {
 
 // us a call: a warp a row for rows up to 16 KB (T = 16384, V = 3000 bf16, k = 0: 40, with 256 threads 78); 128 threads for few
 // alternatives of rows up to 64 KB (T = 8192, V = 32768 bf16, k = 5: 113, with 256 threads 128; k = 20: 163 and 171, but V = 131072, k = 20: 175
-// and 132, as each part that is looked at again is twice as long); 512 while every row has a block at once (T = 64, V = 32000, k = 20:
+// and 132, as each part that is looked at again is twice as long) and for up to 64 of rows up to 16 KB (T = 16384, V = 1000, k = 64: 130, with
+// 256 277; V = 8000 212 and 280; k = 128 has more candidates than 128 parts can tell apart: V = 8000 1473 and 425); 512 while every row has a block at once (T = 64, V = 32000, k = 20:
 // 8.4, with 256 9.4, with 1024 8.9).
 template <class T>
 cudaError_t pick_fwd(const LogprobParams& p, cudaStream_t st) {
@@ -629,14 +630,16 @@ cudaError_t pick_fwd(const LogprobParams& p, cudaStream_t st) {
   const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
   if (bytes <= 16384 && p.k <= 32) return run_fwd<T, 32>(p, sms, st);
   if (p.T <= 2 * sms) return run_fwd<T, 512>(p, sms, st);
-  return bytes <= 65536 && p.k <= 8 ? run_fwd<T, 128>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
+  return bytes <= 65536 && (p.k <= 8 || (p.k <= 64 && bytes <= 16384)) ? run_fwd<T, 128>(p, sms, st) : run_fwd<T, 256>(p, sms, st);
 }
 
+// us a call: a warp a row for rows up to 4 KB, up to 16 KB where there are rows enough to fill the GPU that way (T = 16384, bf16, V = 3000:
+// 42, with 256 threads 66; V = 8000 91 and 93; fp32, V = 1500 42 and 60).
 template <class T>
 cudaError_t pick_bwd(LogprobParams p, cudaStream_t st) {
   const int sms = device_sms();
   const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
-  if (bytes <= 4096) {
+  if (bytes <= (p.T >= 8 * sms ? 16384 : 4096)) {
     p.slices = 1;
     return launch_pdl(logprobs_bwd_kernel<T, 32>, dim3(static_cast<unsigned>(std::min<int64_t>(p.T, sms * 24))), dim3(32), 0,
                       st, p);

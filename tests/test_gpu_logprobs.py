@@ -114,6 +114,21 @@ def test_parity(va, T, V, k, dt):
         assert all(a is None or torch.equal(a, b) for a, b in zip(got, again))
 
 
+# rows enough that each has a warp, 128 or 256 threads to itself, alternatives on either side of what those are chosen by
+MANY = [(1300, 500, 64), (1300, 1001, 33), (1300, 2048, 64), (1220, 3001, 32), (320, 4096, 65), (310, 4097, 8), (330, 5003, 100),
+        (310, 8200, 64), (306, 20011, 9)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,V,k", MANY)
+def test_many_rows(va, T, V, k, dt):
+    z, tok, dl, dh = draw(T, V, dt, k)
+    zd, td = z.to(DEV), tok.to(DEV)
+    got = va.token_logprobs_fwd(zd, td, top_k=k, check_status=True)
+    check_rows(got, z, tok, k, 1.0)
+    check_gradient(va.token_logprobs_bwd(zd, td, got[2], got[1], dl.to(DEV), dh.to(DEV)), z, tok, dl, dh, 1.0)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_ties_and_orders(va, dt):
     """Rows of one value, of two, sorted either way, peaks side by side, -0 against 0: the lower id first."""

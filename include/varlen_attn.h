@@ -571,7 +571,8 @@ typedef struct {
  *   q_weight_dev, k_weight_dev  [d], NULL: ones
  *   inv_freq_dev      float [rot / 2], finite and below 2^24 (NULL when rot is 0)
  *   q_out_dev, k_out_dev  out; may be the inputs themselves (same strides)
- * Pointers 16-byte aligned, strides multiples of 8 elements, as the attention's.  T = 0 does nothing.  Arithmetic in
+ * Pointers 16-byte aligned, strides multiples of 8 elements, as the attention's; the inputs' may be 0 (broadcast heads),
+ * the outputs' are at least d.  T = 0 does nothing.  Arithmetic in
  * fp32, rounded once.  Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED (d, rot), VA_ERR_CUDA.  Asynchronous. */
 va_status varlen_qk_norm_rope_fwd(const void* q_dev, const void* k_dev, const int32_t* position_ids_dev,
                                   const void* q_weight_dev, const void* k_weight_dev, const float* inv_freq_dev,

@@ -872,6 +872,14 @@ static va_status check_qk(const char* where, const va_qk_shape* s, const void* c
   return VA_OK;
 }
 
+// Written heads lie apart: row and head strides of at least d (of an extent of one: anything).
+static va_status check_qk_outputs(const char* where, const va_qk_shape* s, const int64_t* strides) {
+  for (int i = 0; i < 2; ++i)
+    if ((s->T > 1 && strides[2 * i] < s->d) || ((i == 0 ? s->Hq : s->Hkv) > 1 && strides[2 * i + 1] < s->d))
+      return fail(VA_ERR_INVALID_ARG, std::string(where) + ": output strides must be >= d");
+  return VA_OK;
+}
+
 static QkParams qk_params(const va_qk_shape* s, const void* qw, const void* kw, const float* inv_freq,
                           const int32_t* pos, float eps) {
   QkParams p{};
@@ -895,7 +903,8 @@ va_status varlen_qk_norm_rope_fwd(const void* q, const void* k, const int32_t* p
   const void* rows[4] = {q, k, qo, ko};
   const int64_t strides[8] = {s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride,
                               s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride};
-  const va_status st = check_qk("qk_norm_rope_fwd", s, rows, 4, strides, qw, kw, inv_freq, pos, eps);
+  va_status st = check_qk("qk_norm_rope_fwd", s, rows, 4, strides, qw, kw, inv_freq, pos, eps);
+  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_fwd", s, strides + 4);
   if (st != VA_OK || s->T == 0) return st;
   QkParams p = qk_params(s, qw, kw, inv_freq, pos, eps);
   p.x[0] = q, p.x[1] = k, p.y[0] = qo, p.y[1] = ko;
@@ -917,7 +926,8 @@ va_status varlen_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* 
   const int64_t strides[12] = {s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride,
                                s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride,
                                gs->dq_row_stride, gs->dq_head_stride, gs->dk_row_stride, gs->dk_head_stride};
-  const va_status st = check_qk("qk_norm_rope_bwd", s, rows, 6, strides, qw, kw, inv_freq, pos, eps);
+  va_status st = check_qk("qk_norm_rope_bwd", s, rows, 6, strides, qw, kw, inv_freq, pos, eps);
+  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_bwd", s, strides + 8);
   if (st != VA_OK) return st;
   if ((dqw && !qw) || (dkw && !kw))
     return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: a weight's gradient without the weight");

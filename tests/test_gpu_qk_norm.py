@@ -172,6 +172,28 @@ def test_views_in_place_and_fused_gradient(va):
     assert torch.equal(dyq, wgrad[0]) and torch.equal(dyk, wgrad[1])
 
 
+def test_broadcast_heads(va):
+    """One key head expanded to several, and one row of gradients for all tokens: as if they were copied."""
+    T, Hq, d = 70, 4, 64
+    m = make(T, Hq, 1, d, d, BF, BF)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    a = (c["pos"], c["qw"], c["kw"], c["inv"])
+    wide = c["k"].expand(T, 3, d)
+    got = va.qk_norm_rope_fwd(c["q"], wide, *a)
+    want = va.qk_norm_rope_fwd(c["q"], wide.contiguous(), *a)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    dk = c["dk"][:1].expand(T, 3, d)
+    got = va.qk_norm_rope_bwd(c["dq"], dk, c["q"], wide, *a)
+    want = va.qk_norm_rope_bwd(c["dq"], dk.contiguous(), c["q"], wide.contiguous(), *a)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    k = c["k"].clone().requires_grad_()
+    out = va.qk_norm_rope(c["q"], k.expand(T, 3, d), *a)[1]
+    out.backward(dk)
+    near = want[1].float().sum(1, keepdim=True)                 # the sum's own rounding, and those of its terms
+    tol = (want[1].float().abs().sum(1, keepdim=True) + near.abs()) * 2.0 ** -8 * 3
+    assert bool(((k.grad.float() - near).abs() <= tol).all())
+
+
 def test_no_tokens(va):
     q = torch.empty(0, 4, 64, device=DEV, dtype=BF)
     pos = torch.empty(0, dtype=torch.int32, device=DEV)

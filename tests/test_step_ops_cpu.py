@@ -43,6 +43,18 @@ def test_qk_shapes(va, change, status):
     assert lib.varlen_last_error()
 
 
+def test_qk_outputs_lie_apart(va):
+    lib = va._lib.load()
+    for kw in (dict(qo_head_stride=0), dict(qo_row_stride=0), dict(ko_row_stride=56)):
+        s = qk_shape(va, **kw)
+        assert lib.varlen_qk_norm_rope_fwd(P, P, P, P, P, P, ctypes.byref(s), 1e-6, P, P, None) == INVALID, kw
+    s = qk_shape(va)
+    for strides in ((0, 64, 64, 64), (128, 56, 64, 64), (128, 64, 0, 64)):
+        gs = va.VaQkGradStrides(*strides)
+        assert lib.varlen_qk_norm_rope_bwd(P, P, P, P, P, P, P, P, ctypes.byref(s), ctypes.byref(gs), 1e-6, P, P, P, P, P, 1 << 30,
+                                           None) == INVALID, strides
+
+
 def test_qk_arguments(va):
     lib, s, gs = va._lib.load(), qk_shape(va), va.VaQkGradStrides(128, 64, 64, 64)
     at = [P] * 6 + [ctypes.byref(s), 1e-6, P, P, None]

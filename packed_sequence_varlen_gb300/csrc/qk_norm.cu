@@ -191,7 +191,8 @@ struct LaneState {
 
 }  // namespace
 
-// GT: lanes per head, 0: as the call says.
+// GT: lanes per head, so that the sums have no loop (16384 tokens, 12 + 1 heads of 256 bf16 57 us, with a loop 62); 0: as the call
+// says.
 template <class T, bool IL, int GT>
 __global__ void __launch_bounds__(kQkThreads, kBlocks) qk_norm_fwd_kernel(QkParams p) {
   griddep_begin();
@@ -425,16 +426,24 @@ cudaError_t launch_rings(void (*kernel)(QkParams), const QkParams& p, int blocks
 }
 
 template <class T, bool IL>
-cudaError_t run_fwd(const QkParams& p, int blocks, cudaStream_t st) {  // (heads of 72 .. 128: sums without a loop)
-  return p.G == 16 ? launch_rings(qk_norm_fwd_kernel<T, IL, 16>, p, blocks, st)
-                   : launch_rings(qk_norm_fwd_kernel<T, IL, 0>, p, blocks, st);
+cudaError_t run_fwd(const QkParams& p, int blocks, cudaStream_t st) {
+  switch (p.G) {
+    case 8: return launch_rings(qk_norm_fwd_kernel<T, IL, 8>, p, blocks, st);
+    case 16: return launch_rings(qk_norm_fwd_kernel<T, IL, 16>, p, blocks, st);
+    case 32: return launch_rings(qk_norm_fwd_kernel<T, IL, 32>, p, blocks, st);
+    default: return launch_rings(qk_norm_fwd_kernel<T, IL, 0>, p, blocks, st);
+  }
 }
 
 template <class T, bool IL>
 cudaError_t run_bwd(const QkParams& p, int blocks, cudaStream_t st) {
   static_assert(kRing >= 2 * kQkMaxDim * sizeof(float), "a warp's ring holds its sums");
-  return p.G == 16 ? launch_rings(qk_norm_bwd_kernel<T, IL, 16>, p, blocks, st)
-                   : launch_rings(qk_norm_bwd_kernel<T, IL, 0>, p, blocks, st);
+  switch (p.G) {
+    case 8: return launch_rings(qk_norm_bwd_kernel<T, IL, 8>, p, blocks, st);
+    case 16: return launch_rings(qk_norm_bwd_kernel<T, IL, 16>, p, blocks, st);
+    case 32: return launch_rings(qk_norm_bwd_kernel<T, IL, 32>, p, blocks, st);
+    default: return launch_rings(qk_norm_bwd_kernel<T, IL, 0>, p, blocks, st);
+  }
 }
 
 }  // namespace

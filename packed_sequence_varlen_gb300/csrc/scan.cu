@@ -11,19 +11,20 @@
 //   the state that enters the tile is folded from the maps of a few tiles before it and a state further back, which
 //   every kGroup-th tile publishes,
 //   pass 2  the recurrence again from the state that enters the run, with the outputs.
-// So the data is read once and written once.  Four warps of a block serve the ones that work: one takes the tiles' numbers,
-// looks their segments up and has their data copied to shared memory, a few tiles ahead (by TMA; rows that do not lie on
-// 16-byte boundaries in pieces of 16 bytes, by warps of their own); one folds and publishes the tiles' maps; two find the
-// states that enter the tiles while the tiles' own maps are formed.  The fold's order is fixed by the tile's number, whatever is finished
-// first, so results do not change from call to call.  A block takes its tiles' numbers from a counter, so every tile that
-// is waited for is a running block's, whatever else the GPU does, and the smallest unfinished one waits for nobody.
-// What is published is its own flag: the places hold a NaN of all ones before, which is never written (no fences, and a
-// single trip to L2 where it is there).  A segment's start (backward: its end) inside a run replaces the state instead of multiplying
-// it by zero, so nothing of another segment gets in, infinities and NaN included, and no tile waits across one.
+// So the data is read once and written once.  Four warps of a block serve the ones that work: one takes the tiles'
+// numbers, looks their segments up and has their data copied to shared memory, a few tiles ahead (by TMA; rows that do
+// not lie on 16-byte boundaries in pieces of 16 bytes, by warps of their own); one folds and publishes the tiles'
+// maps; two find the states that enter the tiles while the tiles' own maps are formed.  The fold's order is fixed by
+// the tile's number, whatever is finished first, so results do not change from call to call.  A block takes its tiles'
+// numbers from a counter, so every tile that is waited for is a running block's, whatever else the GPU does, and the
+// smallest unfinished one waits for nobody.  What is published is its own flag: the places hold a NaN of all ones
+// before, which is never written (no fences, and a single trip to L2 where it is there).  A segment's start (backward:
+// its end) inside a run replaces the state instead of multiplying it by zero, so nothing of another segment gets in,
+// infinities and NaN included, and no tile waits across one.
 //
 // Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 159 us
-// forward and 279 backward (the bytes at the copy rate: 119, 198), fp32 decays 234 and 413 (198, 357); T = 8192, D = 4096, 53 and 78
-// (30, 50); T = 30000, D = 2047, rows off their boundaries, 155 and 222 (54, 91).
+// forward and 279 backward (the bytes at the copy rate: 119, 198), fp32 decays 234 and 413 (198, 357); T = 8192,
+// D = 4096, 53 and 78 (30, 50); T = 30000, D = 2047, rows off their boundaries, 155 and 222 (54, 91).
 //
 // A = exp(sum of g), rounded once, and not the product of the a: the approximate exponential of an a near 1 has a
 // bias, which would add up over thousands of rows (h off by 2e-5 for a decay of 0.9995 a row).
@@ -55,8 +56,7 @@ constexpr int kResolvers = 2;  // warps that find the states that enter a block'
 constexpr int kRings = 3;
 
 // How a block works: W warps, each with a run of R rows of 32 V channels; S tiles on their way or in work; at most M
-// blocks an SM (shared memory may allow fewer).
-// (K copying warps where TMA does not)
+// blocks an SM (shared memory may allow fewer); K warps copy where TMA does not.
 template <int V_, int W_, int R_, int S_, int M_, int K_ = 0>
 struct Shape {
   static constexpr int V = V_, W = W_, R = R_, S = S_, M = M_, K = K_;
@@ -563,9 +563,9 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
 template <class T, class C, bool TMA>
 constexpr int pitch() { return C::kWidth * static_cast<int>(sizeof(T)) + (TMA ? 0 : 16); }
 
-// The part `part` of K of the rows [row0, row0 + kRows) of the tensor that has rows [0, T), from channel ch0 on, by a warp.  (A piece holds
-// an element of the tensor at least, so none lies outside of its memory, though a piece at its edge or a tile's may hold
-// others' elements too, which nobody uses.)
+// The part `part` of K of the rows [row0, row0 + kRows) of the tensor that has rows [0, T), from channel ch0 on, by a
+// warp.  (A piece holds an element of the tensor at least, so none lies outside of its memory, though a piece at its
+// edge or a tile's may hold others' elements too, which nobody uses.)
 template <class T, class C>
 __device__ __forceinline__ void copy_rows(uint8_t* to, const void* from, int64_t rs, int row0, int T_rows, int ch0, int D,
                                           int part) {

@@ -393,7 +393,8 @@ __device__ __forceinline__ void publish(const ScanParams& p, TileSmem<C>& sh) {
 }
 
 // A resolving warp: the state that enters a tile, from the maps of the tiles before it and a state further back, from when
-// the tile's number is known.  Each of them looks at every tile's slot and takes its share of the tiles.
+// the tile's number is known.  Each of them looks at every tile's slot and takes its share of the tiles.  A slot is given
+// back by both of them too: one that has not seen a tile yet would find the slot, and its barrier's parity, two uses on.
 template <class C>
 __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, int me) {
   using namespace sm100;
@@ -406,11 +407,13 @@ __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, in
     const Slot<C>& slot = sh.slot[at.stage];
     const int tile = slot.tile;
     if (tile < 0) return;
+    const int ch = (slot.col * 32 + lane) * V, from = slot.from;
+    const bool needs = slot.needs != 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[at.stage]));  // (looked at: the slot may be written again)
     const bool mine = whose == me;
     whose = whose + 1 == kResolvers ? 0 : whose + 1;
     if (!mine) continue;
-    const int ch = (slot.col * 32 + lane) * V, from = slot.from;
-    const bool needs = slot.needs != 0;
     Vec<V> in = fill<V>(0.f);
     bool ok = true;
     if (needs) {
@@ -533,7 +536,7 @@ __device__ __forceinline__ void run_block(const ScanParams& p, TileSmem<C>& sh, 
     for (int s = 0; s < C::S; ++s) {
       mbar_init(smem_u32(&sh.known[s]), 1);
       mbar_init(smem_u32(&sh.full[s]), 1 + (kBytes > 0 ? 1 : 32 * C::K));  // the slot, the data
-      mbar_init(smem_u32(&sh.empty[s]), C::W);
+      mbar_init(smem_u32(&sh.empty[s]), C::W + kResolvers);  // the tile is done, and every resolving warp has seen it
       mbar_init(smem_u32(&sh.carried[s]), 1);
       sh.slot[s].tile = -1;
     }

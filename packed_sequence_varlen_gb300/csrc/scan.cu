@@ -26,8 +26,8 @@
 // forward and 279 backward (the bytes at the copy rate: 119, 198), fp32 decays 234 and 413 (198, 357); T = 8192,
 // D = 4096, 53 and 78 (30, 50); T = 30000, D = 2047, rows off their boundaries, 155 and 222 (54, 91).
 //
-// A = exp(sum of g), rounded once, and not the product of the a: the approximate exponential of an a near 1 has a
-// bias, which would add up over thousands of rows (h off by 2e-5 for a decay of 0.9995 a row).
+// A = exp(sum of g) and not the product of the a: the approximate exponential of an a near 1 has a bias, which would
+// add up over thousands of rows (h off by 2e-5 for a decay of 0.9995 a row).
 #include <algorithm>
 
 #include "elem.cuh"
@@ -72,8 +72,9 @@ __device__ __forceinline__ Vec<V> decay(const Vec<V>& g) {
   return r;
 }
 __device__ __forceinline__ float decay(float g) { return fast_exp2(__fmul_rn(g, kLog2e)); }
-// A run's decay, rounded once.
-__device__ __forceinline__ float run_decay(float sum) { return 1.f + expm1f(sum); }
+// A run's decay exp(sum), to the last bit or two of its own size: near 1, where a bias would add up, rounded once from its
+// distance to 1, and further down, where that distance says nothing of a small decay (1 + expm1(-16) is 6% off), by itself.
+__device__ __forceinline__ float run_decay(float sum) { return sum > -0.5f ? 1.f + expm1f(sum) : expf(sum); }
 
 constexpr uint32_t kNone = 0xffffffffu;  // a place that nothing has been published in
 

@@ -418,3 +418,23 @@ def test_bounded_wait_runs_out_and_reports_timeout(va, T, D, xt, gt):
     again = va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], x_dtype=xt, workspace=ws, check_status=True)
     assert all(x is y is None or torch.equal(x, y) for x, y in zip(again, want))
     assert lib.varlen_test_stall_next_scan(10) == 1 and lib.varlen_test_stall_next_scan(5_000_000_000) == 1
+
+
+@pytest.mark.parametrize("D", [64, 66, 67])
+@pytest.mark.parametrize("xt,gt", TYPES)
+def test_states_that_only_decay(va, xt, gt, D):
+    """Nothing but the states in: decays of 0.45 to 0.11 a row carry them over runs and tiles, where what a run keeps of
+    a state is 1e-3 to 1e-15; a gradient at the last states alone goes back the same way.  Each row's value keeps its relative
+    precision (the reference's own bound of it)."""
+    lengths = [40, 1, 300, 129]
+    m = make(lengths, D, xt, gt, seed=7)
+    rates = torch.tensor([-0.8, -1.0, -1.2, -2.2, -0.4, -0.03])
+    m["g"] = rates[torch.arange(D) % 6].expand(sum(lengths), D).contiguous().to(gt)
+    m["x"].zero_()
+    m["dh"].zero_()
+    check(va, lengths, D, xt, gt, True, m=m)
+    m["x"][:] = torch.randn(m["x"].shape, generator=torch.Generator().manual_seed(1)).to(xt)
+    m["x"][:, ::2] = 0
+    m["x"][45:48] = 1000                                     # large rows, then nothing
+    m["dh"][300:303] = -1000
+    check(va, lengths, D, xt, gt, True, m=m)

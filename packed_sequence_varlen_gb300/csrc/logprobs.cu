@@ -6,10 +6,13 @@
 //
 // Forward: one read of the row, in powers of two: with c = log2(e) / tau and a reference r,
 //   s = sum 2^t, w = sum 2^t t, t = c z - r;   log2 p = t - log2 s,  H = ln 2 (log2 s - w / s).
-// A thread moves its reference only when a value passes it by 2^8, so its sums are hardly ever rescaled, and t is one
-// multiply-add whose roundings of c and r drop out of p.  Rows whose largest logit is beyond +-1e29 (or no number) have
-// their sums formed again from differences to the maximum, so one of the type's lowest value stays finite.  Logits far
-// below the reference are raised to where 2^t is 0 anyway (0 times -inf would be NaN), NaN is kept.
+// A thread moves its reference only when a value passes it by 2^8, so its sums are hardly ever rescaled.  t is one
+// multiply-add: r's rounding drops out of p, as every t has it; c's does not (p is that of a temperature off by it, 2^-25
+// relative at most: the error of ln p is that share of the distance to r).  r's rounding, half a step of c z, has to stay
+// small for 2^t, though: references begin at -2^24, and rows whose reference ends at +-2^24 or beyond (or is no number) have
+// their sums formed again from differences to the maximum; so rows of one large value, or of the type's lowest, come out
+// right, and so do ordinary rows with such values in masked places.  Logits far below the reference are raised to
+// where 2^t is 0 anyway (0 times -inf would be NaN), NaN is kept.
 //
 // A block reads its rows through a ring of kDepth groups of kU 16-byte pieces a thread, copied asynchronously: a
 // thread's pieces are its own, so nothing waits for the block, and the next row is on its way while this one's
@@ -37,7 +40,7 @@ constexpr float kLog2eLo = static_cast<float>(1.4426950408889634 - static_cast<d
 constexpr int kU = 4;          // 16-byte pieces of a group
 constexpr int kDepth = 3;      // groups a thread has on their way
 constexpr int kCand = 256;     // candidates a row may have before it takes the slow way
-constexpr float kFar = 1e29f;  // logits beyond this take differences before products
+constexpr float kFar = 16777216.f;  // references beyond this (c z, where half a step is 1): differences before products
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float d;
@@ -122,10 +125,10 @@ struct Part {
   uint32_t floor;  // logits are raised to this: bf16 a pair, fp32 its bits
 
   __device__ __forceinline__ void start(float c) {
-    a.r = -1e30f * c;
+    a.r = -kFar;
     a.s[0] = a.s[1] = a.w[0] = a.w[1] = 0.f;
     top = -INFINITY;
-    set_floor(-2e30f);
+    set_floor(-(1.015625f * kFar + 200.f) / c);
   }
   __device__ __forceinline__ void set_floor(float x) {
     if (sizeof(T) == 2) floor = pack_bf16(x, x);
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm<NT>()) logprobs_fwd_kernel(con
     if (tid == 0) shared[turn].count = 0;  // (behind the barrier: nobody is at the row before any more)
     // ln p = (z - m) / tau - l, m near the largest logit
     float m = q.r * p.inv_c, l2 = q.l - fmaf(m, c, -q.r);
-    if (!(fabsf(m) < kFar)) {
+    if (!(fabsf(q.r) < kFar)) {
       q = far_sums(z, p.V, c, sh, m);
       l2 = q.l;
     }

@@ -313,3 +313,49 @@ def test_offsets_past_32_bits(va):
     assert torch.equal(got[3][-3:], last[3])
     grad = va.token_logprobs_bwd(z, tok, got[2], got[1], dl, dl, grad=z.clone())
     check_gradient(grad[-3:], z[-3:].cpu(), tok[-3:].cpu(), dl[-3:].cpu(), dl[-3:].cpu(), 1.0)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("tau", [1.0 / 64, 0.3, 1.0, 64.0])
+@pytest.mark.parametrize("V", [900, 3001, 20000])
+def test_logits_of_any_size(va, V, tau, dt):
+    """Rows whose largest logit lies anywhere in the type's range, of one value and of several; rows of ordinary logits
+    of which most are replaced by a large negative number, as masks do, and with one large positive number.  The type
+    rounds the given numbers, the reference takes them as they are."""
+    k = 9
+    g = torch.Generator().manual_seed(V)
+    rows, tok = [], []
+    for size in (1e4, 1e5, 1e6, 1.1e7, 1.3e7, 3e7, 1e9, 1e10, 1e12, 1e20, 1e28, 2e29, 1e35):
+        for sign in (1.0, -1.0):
+            m = sign * size
+            plain = 2 * torch.randn(V, generator=g)
+            rows.append(torch.full((V,), m))                                  # one value
+            rows.append(m * (1 + 0.1 * torch.rand(V, generator=g)))           # of one size
+            rows.append(plain + m)                                            # side by side
+            tok += [3, V - 1, 7]
+            some = plain.clone()
+            some[torch.rand(V, generator=g) < 0.97] = m                       # most of them masked (or most of them large)
+            some[5] = 1.5
+            whole = plain.clone()
+            whole[40:] = m
+            one = plain.clone()
+            one[V // 2] = m
+            rows += [some, whole, one]
+            tok += [5, 11, V // 2]
+    z, tok = torch.stack(rows).to(dt), torch.tensor(tok, dtype=torch.int32)
+    dl, dh = torch.randn(len(tok), generator=g), 0.3 * torch.randn(len(tok), generator=g)
+    got = va.token_logprobs_fwd(z.to(DEV), tok.to(DEV), top_k=k, temperature=tau, check_status=True)
+    assert bool(torch.stack([t.isfinite().all() for t in got[:3]]).all())
+    check_rows(got, z, tok, k, tau)
+    grad = va.token_logprobs_bwd(z.to(DEV), tok.to(DEV), got[2], got[1], dl.to(DEV), dh.to(DEV), tau).cpu()
+    # a p below 2^-126, fp32's least normal number, is 0 in the kernel: dz is off by at most 2^-126 times what it is
+    # multiplied with, (|dl| + |dH| (|ln p| + H)) / tau, some 1e-35 at tau = 1/64, and not by the bound's 1e-36
+    x = z.double() / tau
+    lq = torch.log_softmax(x, 1)
+    p = lq.exp()
+    H = -torch.xlogy(p, p).sum(1, keepdim=True)
+    by = torch.where(p > 0, (dl.double().abs()[:, None] + dh.double().abs()[:, None] * (lq.abs() + H)) / tau, 0.0)
+    tiny = (p < 2.0 ** -126) & (torch.arange(V) != tok.long()[:, None])
+    assert bool((grad.double().abs() <= 2.0 ** -126 * (1 + 2.0 ** -7) * by)[tiny].all())
+    ref = -p * (dl.double()[:, None] + dh.double()[:, None] * (torch.where(p > 0, lq, 0.0) + H)) / tau
+    check_gradient(torch.where(tiny, ref.to(dt), grad), z, tok, dl, dh, tau)

@@ -548,7 +548,7 @@ va_status varlen_embed_bwd(const void* dout_dev, int32_t dtype, int64_t dout_row
  * The step between the projections and the attention: every query and key head is divided by its root mean
  * square, scaled by a weight and turned by its token's position.  The pages start at Q and K and have no
  * counterpart; positions are varlen_build_metadata's position_ids.  For a head x of d elements
- *     r = 1 / sqrt(mean(x^2) + eps),  u = x r w,
+ *     r = 1 / sqrt(mean(x^2) + eps),  u = x r w  (with eps = 0 a head of zeros is 0 / 0: NaN),
  * and the pair i of u's first rot elements, (a, b) = (u_i, u_{i + rot/2}), or (u_{2i}, u_{2i+1}) when interleaved,
  * becomes (a cos f - b sin f, b cos f + a sin f) with f = position * inv_freq[i]; the other elements stay.  f is
  * formed in whole 2^-64 turns, so far positions lose nothing. */

@@ -331,9 +331,9 @@ __global__ void __launch_bounds__(kQkThreads, kBlocks) qk_norm_bwd_kernel(QkPara
     float sum[2] = {across(fma(xb, xb, mul(xa, xa))), across(fma(ub, xb, mul(ua, xa)))};  // of x^2 and of g w x
     group_sum(sum, G);
     __syncwarp();  // the stage is written again
-    const float r = rsqrtf(fmaf(sum[0], inv_d, p.eps));
+    const float r = on ? rsqrtf(fmaf(sum[0], inv_d, p.eps)) : 0.f;  // (a lane without a head: zeros, whatever eps is)
     const V4 rr = fill<4>(r), m = fill<4>(-sum[1] * inv_d * r * r);  // x m = -n mean(g w n) / r
-    dwa[q] = fma(ga, mul(xa, rr), dwa[q]);                   // (zeros where the lane has no head)
+    dwa[q] = fma(ga, mul(xa, rr), dwa[q]);
     dwb[q] = fma(gb, mul(xb, rr), dwb[q]);
     if (on) {
       V4 first4, second4;

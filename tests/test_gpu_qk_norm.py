@@ -259,3 +259,20 @@ def test_graph_and_streams(va):
             got.append(both())
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,d", [(3, 1, 128), (5, 1, 64), (1, 1, 64), (7, 2, 80), (1, 3, 256), (2, 1, 32)])
+def test_no_eps(va, Hq, Hkv, d, dt):
+    """eps = 0 with heads that leave lanes over: the norm of rows that are not zero, and every gradient."""
+    m = make(60, Hq, Hkv, d, d, dt, dt)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    a = (c["pos"], c["qw"], c["kw"], c["inv"], 0.0)
+    qo, ko = va.qk_norm_rope_fwd(c["q"], c["k"], *a)
+    close(qo, *reference(m["q"], m["qw"], m["pos"], m["inv"], 0.0, False))
+    close(ko, *reference(m["k"], m["kw"], m["pos"], m["inv"], 0.0, False))
+    got = va.qk_norm_rope_bwd(c["dq"], c["dk"], c["q"], c["k"], *a)
+    for x, w, dy, dx, dw in ((m["q"], m["qw"], m["dq"], got[0], got[2]), (m["k"], m["kw"], m["dk"], got[1], got[3])):
+        rx, ex, rw, ew = reference(x, w, m["pos"], m["inv"], 0.0, False, dy)
+        close(dx, rx, ex)
+        close(dw, rw, ew)

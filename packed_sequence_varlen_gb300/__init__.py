@@ -923,20 +923,23 @@ def token_logprobs_fwd(logits: torch.Tensor, tokens: torch.Tensor, top_k: int = 
     their log probabilities; None and None with 0.  Rows whose token is ``ignore_index`` are not read: zeros,
     and ids of -1.  A token outside [0, V) gives NaN for its logprob; ``check_status`` raises."""
     T, V = _check_logits(logits, tokens)
-    dev, k = logits.device, int(top_k)
-    out = torch.empty((3, T), dtype=torch.float32, device=dev)
+    out = torch.empty((3, T), dtype=torch.float32, device=logits.device).unbind(0)
+    return _token_logprobs_fwd(logits, tokens, T, V, int(top_k), temperature, ignore_index, check_status, *out)
+
+
+def _token_logprobs_fwd(logits, tokens, T, V, k, temperature, ignore_index, check_status, logprob, entropy, lse):
+    """The checked call, into the given results."""
+    dev = logits.device
     ids = top = None
     if k > 0:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         top = torch.empty((T, k), dtype=torch.float32, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
-    at = out.data_ptr()
     _call(dev, _lib.load().varlen_token_logprobs_fwd, logits.data_ptr(), logits.dtype == torch.bfloat16,
-          _row_stride(logits), tokens.data_ptr(), T, V, k, ignore_index, temperature, at, at + 4 * T, at + 8 * T, _ptr(ids),
-          _ptr(top), _ptr(status))
+          _row_stride(logits), tokens.data_ptr(), T, V, k, ignore_index, temperature, logprob.data_ptr(), entropy.data_ptr(),
+          lse.data_ptr(), _ptr(ids), _ptr(top), _ptr(status))
     if check_status and int(status.item()) != 0:
         raise VarlenError(int(status.item()), "token_logprobs_fwd: a token is outside the vocabulary")
-    logprob, entropy, lse = out.unbind(0)
     return logprob, entropy, lse, ids, top
 
 
@@ -974,7 +977,11 @@ def token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Te
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top_k, temperature, ignore_index):
-        logprob, entropy, lse, ids, top = token_logprobs_fwd(logits, tokens, top_k, temperature, ignore_index)
+        T, V = _check_logits(logits, tokens)
+        # (memory of its own for each result: one may be changed in place without the others, or what is saved, being touched)
+        out = [torch.empty(T, dtype=torch.float32, device=logits.device) for _ in range(3)]
+        logprob, entropy, lse, ids, top = _token_logprobs_fwd(logits, tokens, T, V, int(top_k), temperature, ignore_index,
+                                                              False, *out)
         ctx.save_for_backward(logits, tokens, lse, entropy)
         ctx.temperature, ctx.ignore_index = temperature, ignore_index
         ctx.set_materialize_grads(False)

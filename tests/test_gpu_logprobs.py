@@ -359,3 +359,18 @@ def test_logits_of_any_size(va, V, tau, dt):
     assert bool((grad.double().abs() <= 2.0 ** -126 * (1 + 2.0 ** -7) * by)[tiny].all())
     ref = -p * (dl.double()[:, None] + dh.double()[:, None] * (torch.where(p > 0, lq, 0.0) + H)) / tau
     check_gradient(torch.where(tiny, ref.to(dt), grad), z, tok, dl, dh, tau)
+
+
+def test_results_may_change_in_place(va):
+    """The differentiable results have memory of their own: one changed in place leaves the others, and the gradient is the
+    one of what was done."""
+    z, tok, dl, dh = draw(40, 500, F32, 12)
+    zd, td, keep = z.to(DEV), tok.to(DEV), (torch.arange(40, device=DEV) % 3 > 0).float()
+    leaf = zd.clone().requires_grad_(True)
+    lp, H, ids, top = va.token_logprobs(leaf, td, top_k=3)
+    entropies = H.detach().clone()
+    lp.mul_(keep)
+    lp.sub_(0.5)
+    assert torch.equal(H.detach(), entropies)
+    ((lp * dl.to(DEV)).sum() + (H * dh.to(DEV)).sum()).backward()
+    check_gradient(leaf.grad, z, tok, dl * keep.cpu(), dh, 1.0)

@@ -742,6 +742,12 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     return dq, dk, dqw, dkw
 
 
+def _whole_pieces(t: torch.Tensor) -> torch.Tensor:
+    """``t`` contiguous and on a 16-byte boundary (a part of a larger gradient may begin anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, position_ids, q_weight, k_weight, inv_freq, eps, interleaved):
@@ -753,7 +759,7 @@ class _QkNormRope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, pos, qw, kw, inv_freq = ctx.saved_tensors
-        dq, dk, dqw, dkw = qk_norm_rope_bwd(dq_out.contiguous(), dk_out.contiguous(), q, k, pos, qw, kw, inv_freq,
+        dq, dk, dqw, dkw = qk_norm_rope_bwd(_whole_pieces(dq_out), _whole_pieces(dk_out), q, k, pos, qw, kw, inv_freq,
                                             ctx.eps, ctx.interleaved)
         return dq, dk, None, dqw, dkw, None, None, None
 

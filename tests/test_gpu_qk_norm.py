@@ -276,3 +276,17 @@ def test_no_eps(va, Hq, Hkv, d, dt):
         rx, ex, rw, ew = reference(x, w, m["pos"], m["inv"], 0.0, False, dy)
         close(dx, rx, ex)
         close(dw, rw, ew)
+
+
+def test_gradients_off_their_boundaries(va):
+    """The outputs' gradients as autograd may hand them over: contiguous parts of a larger one, off 16-byte boundaries."""
+    m = make(20, 2, 1, 64, 64, BF, BF)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    a = (c["pos"], c["qw"], c["kw"], c["inv"])
+    want = va.qk_norm_rope_bwd(c["dq"], c["dk"], c["q"], c["k"], *a)
+    q, k = (c[n].clone().requires_grad_(True) for n in ("q", "k"))
+    qo, ko = va.qk_norm_rope(q, k, *a)
+    flat = torch.cat([torch.zeros(3, device=DEV, dtype=BF), qo.reshape(-1), torch.zeros(2, device=DEV, dtype=BF), ko.reshape(-1)])
+    up = torch.cat([torch.zeros(3, device=DEV, dtype=BF), c["dq"].reshape(-1), torch.zeros(2, device=DEV, dtype=BF), c["dk"].reshape(-1)])
+    flat.backward(up)
+    assert torch.equal(q.grad, want[0]) and torch.equal(k.grad, want[1])

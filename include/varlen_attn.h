@@ -570,9 +570,9 @@ typedef struct {
  *   position_ids_dev  int32 [T]
  *   q_weight_dev, k_weight_dev  [d], NULL: ones
  *   inv_freq_dev      float [rot / 2], finite and below 2^24 (NULL when rot is 0)
- *   q_out_dev, k_out_dev  out; may be the inputs themselves (same strides)
+ *   q_out_dev, k_out_dev  out; may be the inputs themselves (same strides, otherwise refused)
  * Pointers 16-byte aligned, strides multiples of 8 elements, as the attention's; the inputs' may be 0 (broadcast heads),
- * the outputs' are at least d.  T = 0 does nothing.  Arithmetic in
+ * the outputs' are at least d and leave no two heads on one another.  T = 0 does nothing.  Arithmetic in
  * fp32, rounded once.  Errors: VA_ERR_INVALID_ARG, VA_ERR_UNSUPPORTED (d, rot), VA_ERR_CUDA.  Asynchronous. */
 va_status varlen_qk_norm_rope_fwd(const void* q_dev, const void* k_dev, const int32_t* position_ids_dev,
                                   const void* q_weight_dev, const void* k_weight_dev, const float* inv_freq_dev,
@@ -620,7 +620,7 @@ size_t varlen_scan_workspace_size(int32_t T, int32_t B, int32_t D);
  *   x_dev, log_decay_dev  [T, D]; log decays are meant to be <= 0 (with larger ones the decay over any 4096 rows of a
  *               segment has to stay finite)
  *   h0_dev      float [B, D], or NULL
- *   h_dev       [T, D] out; may be x itself (same type and stride)
+ *   h_dev       [T, D] out; may be x itself (same type and stride); lying on a part of an input is refused
  *   h_last_dev  float [B, D] out: the state after each segment, or NULL; for single tokens (T == B) it may be h0
  *               itself, otherwise they must not overlap
  *   ws_dev / ws_bytes  workspace (>= varlen_scan_workspace_size, 16-byte aligned; single tokens need 256 bytes, or none:
@@ -639,7 +639,7 @@ va_status varlen_scan_fwd(const void* x_dev, const void* log_decay_dev, const in
  *   dh_dev [T, D] in h's type; h_dev the forward's result; h0_dev as in the forward
  *   dh_last_dev  float [B, D], or NULL (zeros)
  *   dx_dev, dlog_decay_dev  [T, D] out, in x's and log_decay's types; dx may be dh, dlog_decay may be log_decay
- *               (same type and stride), neither may overlap h
+ *               (same type and stride); lying on a part of them, on h or on one another is refused
  *   dh0_dev      float [B, D] out, or NULL; apart from h0 and dh_last
  * Errors as the forward. */
 va_status varlen_scan_bwd(const void* dh_dev, const void* h_dev, const void* log_decay_dev,
@@ -673,7 +673,8 @@ va_status varlen_token_logprobs_fwd(const void* logits_dev, int32_t dtype, int64
  *     dz_c = (dlogprob ([c == token] - p_c) - dentropy p_c (ln p_c + entropy)) / temperature.
  *   lse_dev, entropy_dev        the forward's (entropy NULL without dentropy)
  *   dlogprob_dev, dentropy_dev  float [T] (dentropy NULL: none)
- *   grad_dev    [T, V] out in the logits' type (row stride grad_row_stride); may be the logits (same stride).
+ *   grad_dev    [T, V] out in the logits' type (row stride grad_row_stride); may be the logits (same stride; other
+ *               overlaps are refused).
  *               Rows with ignore_index are zero, rows with a token outside [0, V) NaN
  * Errors as the forward.  Asynchronous. */
 va_status varlen_token_logprobs_bwd(const void* logits_dev, int32_t dtype, int64_t logits_row_stride,

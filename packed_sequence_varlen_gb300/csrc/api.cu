@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <initializer_list>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "attn_params.cuh"
@@ -846,6 +847,47 @@ va_status varlen_embed_bwd(const void* dout, int32_t dtype, int64_t i_rs, const 
   return e == cudaSuccess ? VA_OK : cuda_fail(e, "embed_bwd");
 }
 
+// ------------------------------------------------------------ what may lie on what
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+// Rows of `row` bytes, `step` apart.
+struct RowSpan {
+  const void* at;
+  int64_t step, row;
+};
+
+static RowSpan span_of(const void* p, int64_t stride, int64_t D, int bf16) {
+  const int64_t es = bf16 ? 2 : 4;
+  return RowSpan{p, stride * es, D * es};
+}
+
+// Whether some row of one shares a byte with some row of the other, T rows each.  (Rows side by side in wider ones,
+// however they interleave, share none.)
+static bool rows_meet(const RowSpan& a, const RowSpan& b, int64_t T) {
+  const auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+  if (!overlap(a.at, (T - 1) * a.step + a.row, b.at, (T - 1) * b.step + b.row)) return false;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at));
+  if (T == 1) return true;
+  if (a.step == b.step) {  // the first place k rows on at which b ends behind a's beginning
+    const int64_t k = std::max(floor_div(-b.row - d, a.step) + 1, -(T - 1));
+    return k < T && d + k * a.step < a.row;
+  }
+  for (int64_t i = 0; i < T; ++i) {  // (different strides over the same memory: rare)
+    const int64_t j = std::max<int64_t>(floor_div(i * a.step - b.row - d, b.step) + 1, 0);
+    if (j < T && d + j * b.step < i * a.step + a.row) return true;
+  }
+  return false;
+}
+
+// Whether the rows are the same ones, so that each is read before it is written.
+static bool rows_same(const RowSpan& a, const RowSpan& b, int64_t T) {
+  return a.at == b.at && a.row == b.row && (T == 1 || a.step == b.step);
+}
+
 // ------------------------------------------------------------ query / key norm with rotation
 
 static va_status check_qk(const char* where, const va_qk_shape* s, const void* const* rows, int nrows,
@@ -872,11 +914,29 @@ static va_status check_qk(const char* where, const va_qk_shape* s, const void* c
   return VA_OK;
 }
 
-// Written heads lie apart: row and head strides of at least d (of an extent of one: anything).
-static va_status check_qk_outputs(const char* where, const va_qk_shape* s, const int64_t* strides) {
-  for (int i = 0; i < 2; ++i)
-    if ((s->T > 1 && strides[2 * i] < s->d) || ((i == 0 ? s->Hq : s->Hkv) > 1 && strides[2 * i + 1] < s->d))
-      return fail(VA_ERR_INVALID_ARG, std::string(where) + ": output strides must be >= d");
+// Whether two of the heads (T x H, of d elements, their strides at least d) share an element.
+static bool heads_meet(int64_t T, int64_t H, int64_t d, int64_t rs, int64_t hs) {
+  if (T == 1 || H == 1 || rs >= (H - 1) * hs + d || hs >= (T - 1) * rs + d) return false;  // one inside the other's gaps
+  for (int64_t i = 1; i < H; ++i) {  // a token later that starts less than d before or behind head i
+    const int64_t t = i * hs / rs;
+    if ((t < T && i * hs - t * rs < d) || (t + 1 < T && (t + 1) * rs - i * hs < d)) return true;
+  }
+  return false;
+}
+
+// Written heads lie apart, and on what they may be written over (strides `over`, may be null) only as those lie.
+static va_status check_qk_outputs(const char* where, const va_qk_shape* s, void* const* out, const int64_t* strides,
+                                  std::initializer_list<std::pair<const void* const*, const int64_t*>> over) {
+  const std::string w(where);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t H = i == 0 ? s->Hq : s->Hkv, rs = strides[2 * i], hs = strides[2 * i + 1];
+    if ((s->T > 1 && rs < s->d) || (H > 1 && hs < s->d))
+      return fail(VA_ERR_INVALID_ARG, w + ": output strides must be >= d");
+    if (heads_meet(s->T, H, s->d, rs, hs)) return fail(VA_ERR_INVALID_ARG, w + ": heads of an output lie on one another");
+    for (const auto& in : over)
+      if (s->T > 0 && in.first[i] == out[i] && ((s->T > 1 && in.second[2 * i] != rs) || (H > 1 && in.second[2 * i + 1] != hs)))
+        return fail(VA_ERR_INVALID_ARG, w + ": an output over its input has its strides");
+  }
   return VA_OK;
 }
 
@@ -904,7 +964,8 @@ va_status varlen_qk_norm_rope_fwd(const void* q, const void* k, const int32_t* p
   const int64_t strides[8] = {s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride,
                               s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride};
   va_status st = check_qk("qk_norm_rope_fwd", s, rows, 4, strides, qw, kw, inv_freq, pos, eps);
-  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_fwd", s, strides + 4);
+  void* const out[2] = {qo, ko};
+  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_fwd", s, out, strides + 4, {{rows, strides}});
   if (st != VA_OK || s->T == 0) return st;
   QkParams p = qk_params(s, qw, kw, inv_freq, pos, eps);
   p.x[0] = q, p.x[1] = k, p.y[0] = qo, p.y[1] = ko;
@@ -927,7 +988,8 @@ va_status varlen_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* 
                                s->qo_row_stride, s->qo_head_stride, s->ko_row_stride, s->ko_head_stride,
                                gs->dq_row_stride, gs->dq_head_stride, gs->dk_row_stride, gs->dk_head_stride};
   va_status st = check_qk("qk_norm_rope_bwd", s, rows, 6, strides, qw, kw, inv_freq, pos, eps);
-  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_bwd", s, strides + 8);
+  void* const out[2] = {dq, dk};
+  if (st == VA_OK) st = check_qk_outputs("qk_norm_rope_bwd", s, out, strides + 8, {{rows, strides}, {rows + 2, strides + 4}});
   if (st != VA_OK) return st;
   if ((dqw && !qw) || (dkw && !kw))
     return fail(VA_ERR_INVALID_ARG, "qk_norm_rope_bwd: a weight's gradient without the weight");
@@ -956,10 +1018,6 @@ va_status varlen_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* 
 
 // ------------------------------------------------------------ gated recurrence
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
 
 // tokens: a forward of single tokens, which runs without a workspace too.
 static va_status check_scan(const char* where, const va_scan_shape* s, const int32_t* cu, const void* ws, size_t ws_bytes,
@@ -1011,6 +1069,10 @@ va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const
   // a segment's first rows read h0 twice, the second time maybe after its last row is done
   if (s->B < s->T && overlap(h0, states, h_last, states))
     return fail(VA_ERR_INVALID_ARG, "scan_fwd: h_last may lie on h0 for single tokens only (T == B)");
+  const RowSpan out = span_of(h, s->h_row_stride, s->D, hb);
+  for (const RowSpan& in : {span_of(x, s->x_row_stride, s->D, s->x_dtype), span_of(g, s->gate_row_stride, s->D, s->gate_dtype)})
+    if (!rows_same(out, in, s->T) && rows_meet(out, in, s->T))
+      return fail(VA_ERR_INVALID_ARG, "scan_fwd: h may be an input itself (type and stride), not lie on a part of it");
   ScanParams p{};
   p.x = x, p.g = g, p.out = h;
   p.x_rs = s->x_row_stride, p.g_rs = s->gate_row_stride, p.out_rs = s->h_row_stride;
@@ -1046,6 +1108,16 @@ va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const in
   const size_t states = static_cast<size_t>(s->B) * s->D * sizeof(float);
   if (overlap(dh_last, states, dh0, states) || overlap(h0, states, dh0, states))
     return fail(VA_ERR_INVALID_ARG, "scan_bwd: dh0 must not lie on h0 or dh_last");
+  const RowSpan rdh = span_of(dh, gs->dh_row_stride, s->D, hb), rg = span_of(g, s->gate_row_stride, s->D, s->gate_dtype),
+                rh = span_of(h, s->h_row_stride, s->D, hb), rdx = span_of(dx, gs->dx_row_stride, s->D, s->x_dtype),
+                rdg = span_of(dg, gs->dgate_row_stride, s->D, s->gate_dtype);
+  // (a tile reads the row of h before its own, which another tile's gradients would lie on)
+  if (rows_meet(rdx, rh, s->T) || rows_meet(rdg, rh, s->T) || rows_meet(rdx, rdg, s->T))
+    return fail(VA_ERR_INVALID_ARG, "scan_bwd: dx and dlog_decay must lie neither on h nor on one another");
+  for (const RowSpan& to : {rdx, rdg})
+    for (const RowSpan& in : {rdh, rg})
+      if (!rows_same(to, in, s->T) && rows_meet(to, in, s->T))
+        return fail(VA_ERR_INVALID_ARG, "scan_bwd: a gradient may be dh or log_decay itself (type and stride), not lie on a part of it");
   ScanParams p{};
   p.x = dh, p.g = g, p.h = h, p.out = dx, p.dg = dg;
   p.x_rs = gs->dh_row_stride, p.g_rs = s->gate_row_stride, p.h_rs = s->h_row_stride;
@@ -1117,6 +1189,9 @@ va_status varlen_token_logprobs_bwd(const void* z, int32_t dtype, int64_t z_rs, 
   if (g_rs < V) return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: row strides must be >= the row");
   if (reinterpret_cast<uintptr_t>(grad) & (dtype == 1 ? 1 : 3))
     return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: pointers must be aligned to their type");
+  const RowSpan from = span_of(z, z_rs, V, dtype), to = span_of(grad, g_rs, V, dtype);
+  if (!rows_same(from, to, T) && rows_meet(from, to, T))
+    return fail(VA_ERR_INVALID_ARG, "token_logprobs_bwd: grad may be the logits themselves (same stride), not lie on a part of them");
   LogprobParams p{};
   p.z = z, p.z_rs = z_rs, p.tok = tok, p.T = T, p.V = V, p.ignore = ignore_index;
   set_temperature(p, temperature);

@@ -374,3 +374,19 @@ def test_results_may_change_in_place(va):
     assert torch.equal(H.detach(), entropies)
     ((lp * dl.to(DEV)).sum() + (H * dh.to(DEV)).sum()).backward()
     check_gradient(leaf.grad, z, tok, dl * keep.cpu(), dh, 1.0)
+
+
+def test_gradient_beside_and_on_the_logits(va):
+    """The gradient in the other half of the logits' rows; on a part of the logits it is refused."""
+    T, V = 9, 3000
+    z, tok, dl, dh = draw(T, V, F32, 21)
+    wide = torch.zeros(T, 2 * V, device=DEV)
+    wide[:, :V] = z.to(DEV)
+    got = va.token_logprobs_fwd(wide[:, :V], tok.to(DEV))
+    grad = va.token_logprobs_bwd(wide[:, :V], tok.to(DEV), got[2], got[1], dl.to(DEV), dh.to(DEV), grad=wide[:, V:])
+    check_gradient(grad, z, tok, dl, dh, 1.0)
+    assert torch.equal(wide[:, :V].cpu(), z)
+    for to in (wide[:, 4:V + 4], wide.view(2 * T, V)[:T]):
+        with pytest.raises(va.VarlenError) as e:
+            va.token_logprobs_bwd(wide[:, :V], tok.to(DEV), got[2], got[1], dl.to(DEV), dh.to(DEV), grad=to)
+        assert e.value.status == 1

@@ -438,3 +438,37 @@ def test_states_that_only_decay(va, xt, gt, D):
     m["x"][45:48] = 1000                                     # large rows, then nothing
     m["dh"][300:303] = -1000
     check(va, lengths, D, xt, gt, True, m=m)
+
+
+@pytest.mark.parametrize("D", [64, 67])
+def test_outputs_over_the_other_input(va, D):
+    """h over the decays, dx over the decays and their gradient over dh; views side by side in one buffer.  A row further
+    on in the same rows is refused, and so is a gradient on h."""
+    lengths = [300, 77]
+    m = make(lengths, D, F32, F32)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    T = sum(lengths)
+    h, _ = va.varlen_scan_fwd(c["x"], c["g"], c["cu"])
+    dx, dg, _ = va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"])
+    over = c["g"].clone()
+    va.varlen_scan_fwd(c["x"], over, c["cu"], out=over)
+    assert torch.equal(over, h)
+    dh, g = c["dh"].clone(), c["g"].clone()
+    va.varlen_scan_bwd(dh, h, g, c["cu"], dx=g, dlog_decay=dh)
+    assert torch.equal(g, dx) and torch.equal(dh, dg)
+    one = torch.zeros(T, 4 * D, device=DEV)
+    x, g, out = one[:, :D], one[:, D:2 * D], one[:, 2 * D:3 * D]
+    x.copy_(c["x"]), g.copy_(c["g"])
+    va.varlen_scan_fwd(x, g, c["cu"], out=out)
+    rh, eh, _, _ = reference(m["x"], m["g"], lengths)
+    close(out, rh, eh)
+    assert bool((one[:, 3 * D:] == 0).all())
+    long = torch.zeros(T + 1, D, device=DEV)
+    for call in (lambda: va.varlen_scan_fwd(long[:T], c["g"], c["cu"], out=long[1:]),
+                 lambda: va.varlen_scan_fwd(c["x"], long[1:], c["cu"], out=long[:T]),
+                 lambda: va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], dx=h),
+                 lambda: va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], dlog_decay=h),
+                 lambda: va.varlen_scan_bwd(long[1:], h, c["g"], c["cu"], dx=long[:T])):
+        with pytest.raises(va.VarlenError) as e:
+            call()
+        assert e.value.status == 1

@@ -193,3 +193,81 @@ def test_plain_forms_agree_with_the_definitions():
                 assert float((a.double() - b.double()).norm()) <= (half + 2.0 ** -20) * float(b.double().norm()) + lost + 1e-30, case
     finally:
         M.DEV = device
+
+
+def meets(a, b):
+    """Whether two lists of (first, past the last) share an element."""
+    return any(x < v and u < y for x, y in a for u, v in b)
+
+
+def test_qk_heads_on_one_another(va):
+    """Strides that are each at least d, but let a token's heads lie on another token's, are refused; every other layout (heads
+    first, tokens first, gaps that interleave) is not."""
+    if torch.cuda.is_available():
+        pytest.skip("calls that are not refused would launch")
+    lib, d, seen = va._lib.load(), 16, set()
+    for T, H in ((1, 3), (2, 2), (3, 4), (4, 3), (5, 2)):
+        for rs in range(16, 97, 8):
+            for hs in range(16, 97, 8):
+                at = [(t * rs + h * hs, t * rs + h * hs + d) for t in range(T) for h in range(H)]
+                bad = any(meets([x], at[i + 1:]) for i, x in enumerate(at))
+                seen.add(bad)
+                s = qk_shape(va, T=T, Hq=H, Hkv=1, d=d, rot=16, qo_row_stride=rs, qo_head_stride=hs, ko_row_stride=d)
+                assert (lib.varlen_qk_norm_rope_fwd(P, P, P, P, P, P, ctypes.byref(s), 1e-6, 5 * P, 2 * P, None) == INVALID) == bad, (T, H, rs, hs)
+                s, gs = qk_shape(va, T=T, Hq=1, Hkv=H, d=d, rot=16), va.VaQkGradStrides(64, 64, rs, hs)
+                assert (lib.varlen_qk_norm_rope_bwd(P, P, P, P, P, P, P, P, ctypes.byref(s), ctypes.byref(gs), 1e-6, 2 * P, 3 * P, P, P,
+                                                    4 * P, 1 << 30, None) == INVALID) == bad, (T, H, rs, hs)
+    assert seen == {True, False}
+
+
+def test_qk_outputs_over_inputs(va):
+    """An output over its input has its strides."""
+    lib = va._lib.load()
+    for kw in (dict(qo_row_stride=256), dict(qo_head_stride=256), dict(ko_row_stride=192)):
+        s = qk_shape(va, **kw)
+        assert lib.varlen_qk_norm_rope_fwd(P, 2 * P, P, P, P, P, ctypes.byref(s), 1e-6, P, 2 * P, None) == INVALID, kw
+    s = qk_shape(va)
+    for strides in ((256, 64, 64, 64), (128, 64, 192, 64)):
+        gs = va.VaQkGradStrides(*strides)
+        for a, b in ((P, 2 * P), (3 * P, 4 * P)):             # over the outputs' gradients, over the inputs
+            assert lib.varlen_qk_norm_rope_bwd(P, 2 * P, 3 * P, 4 * P, P, P, P, P, ctypes.byref(s), ctypes.byref(gs), 1e-6, a, b, P, P, 8 * P,
+                                               1 << 30, None) == INVALID, strides
+
+
+# the first row and the row stride of two arrays of T rows of D elements, in elements
+SPANS = [(0, 8, 0, 8), (0, 8, 4, 8), (0, 16, 8, 16), (0, 16, 4, 16), (8, 16, 0, 16), (0, 16, 0, 8), (0, 16, 8, 32), (0, 24, 8, 16), (0, 32, 16, 16),
+         (0, 8, 32, 8), (0, 8, 31, 8), (100, 8, 0, 8), (0, 16, 56, 16), (0, 16, 60, 16), (0, 16, 64, 16), (64, 16, 0, 16), (3, 16, 0, 16),
+         (0, 64, 8, 16), (0, 9, 4, 18), (0, 20, 10, 40)]
+
+
+@pytest.mark.parametrize("T", [1, 2, 4])
+def test_outputs_on_a_part_of_the_inputs(va, T):
+    """h, dx, dlog_decay and the logits' gradient: an input itself or apart from it, however the rows interleave."""
+    if torch.cuda.is_available():
+        pytest.skip("calls that are not refused would launch")
+    lib, D, es, seen = va._lib.load(), 8, 4, set()
+    far = [P + (i << 24) for i in range(8)]
+    for a0, ra, b0, rb in SPANS:
+        at = [[(f + t * r, f + t * r + D) for t in range(T)] for f, r in ((a0, ra), (b0, rb))]
+        same = a0 == b0 and (T == 1 or ra == rb)
+        meet = meets(*at)
+        seen.add((same, meet))
+        a, b = far[0] + a0 * es, far[0] + b0 * es
+        both = dict(T=T, B=1, D=D, x_dtype=0, gate_dtype=0)
+        status = []
+        for x, rx, g, rg in ((b, rb, far[1], 64), (far[1], 64, b, rb)):                 # h on x, h on the decays
+            s = scan_shape(va, x_row_stride=rx, gate_row_stride=rg, h_row_stride=ra, **both)
+            status.append(lib.varlen_scan_fwd(x, g, P, ctypes.byref(s), None, a, None, far[2], 1 << 40, None))
+        for dh, g, dx, dg in ((b, far[1], a, far[2]), (far[1], b, far[2], a), (far[1], b, a, far[2]), (b, far[1], far[2], a)):
+            s = scan_shape(va, gate_row_stride=rb if g == b else 64, h_row_stride=64, x_row_stride=64, **both)
+            gs = va.VaScanGradStrides(rb if dh == b else 64, ra if dx == a else 64, ra if dg == a else 64)
+            status.append(lib.varlen_scan_bwd(dh, far[3], g, P, ctypes.byref(s), ctypes.byref(gs), None, None, dx, dg, None, far[4], 1 << 40,
+                                              None))
+        status.append(lib.varlen_token_logprobs_bwd(b, 0, rb, P, P, P, P, P, T, D, -100, 1.0, a, ra, None))
+        assert [x == INVALID for x in status] == [meet and not same] * len(status), (a0, ra, b0, rb, status)
+        for dx, rx, dg, rg, h, rh in ((a, ra, far[1], 64, b, rb), (far[1], 64, a, ra, b, rb), (a, ra, b, rb, far[1], 64)):
+            s = scan_shape(va, gate_row_stride=64, h_row_stride=rh, x_row_stride=64, **both)   # on h, on one another: never
+            gs = va.VaScanGradStrides(64, rx, rg)
+            x = lib.varlen_scan_bwd(far[2], h, far[3], P, ctypes.byref(s), ctypes.byref(gs), None, None, dx, dg, None, far[4], 1 << 40, None)
+            assert (x == INVALID) == meet, (a0, ra, b0, rb)
+    assert {(True, True), (False, True), (False, False)} <= seen

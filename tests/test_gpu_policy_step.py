@@ -146,3 +146,41 @@ def test_single_token_step_follows_the_packed_one(va):
         again = va.token_logprobs_fwd(h[at].to(BF) @ head.T, tok[at].contiguous(), top_k=4)
         assert again[0].shape == (len(live),) and torch.equal(again[3].sort(1).values >= 0, torch.ones_like(again[3], dtype=torch.bool))
     assert float((state - last).abs().max()) <= 64 * 2.0 ** -24 * float(h.abs().max()) * max(lengths) + 1e-6
+
+
+def test_single_token_scores_are_those_of_the_packed_stream(va):
+    """Log probabilities, entropies and alternatives of one token a sequence at a time, from the recurrence's single-token form,
+    against those of the packed stream."""
+    lengths, D, V, k = [9, 5, 12, 1], 80, 700, 4
+    B, T = len(lengths), sum(lengths)
+    g = torch.Generator().manual_seed(2)
+    x, head = (torch.randn(*s, generator=g).to(BF).to(DEV) for s in ((T, D), (V, D)))
+    ld = -torch.rand(T, D, generator=g).to(DEV)
+    tok = torch.randint(0, V, (T,), generator=g).to(DEV, torch.int32)
+    cu = torch.tensor([0] + lengths).cumsum(0).to(DEV, torch.int32)
+    h, _ = va.varlen_scan_fwd(x, ld, cu, h_last=True)
+    z = h.double() @ head.double().T                          # logits of the fp32 states, rounded once
+    lp, ent, lse, ids, top = va.token_logprobs_fwd(z.float(), tok, top_k=k)
+    state, starts = torch.zeros(B, D, device=DEV), torch.tensor([0] + lengths).cumsum(0)[:-1]
+    for t in range(max(lengths)):
+        live = [b for b in range(B) if t < lengths[b]]
+        at = torch.tensor([int(starts[b]) + t for b in live], device=DEV)
+        hs, s = va.varlen_scan_fwd(x[at], ld[at], torch.arange(len(live) + 1, dtype=torch.int32, device=DEV), state[live].contiguous(),
+                                   h_last=True)
+        state[live] = s
+        zs = hs.double() @ head.double().T
+        one = va.token_logprobs_fwd(zs.float(), tok[at].contiguous(), top_k=k)
+        # the states differ by fp32 roundings (two forms of one recurrence, as above), and the logits by what those make
+        # and half a step of their own; a log probability and the lse move by at most the largest change of a logit, twice and once, an entropy
+        # by it times the spread of ln p (at most lse - the smallest logit), a sum by 500 roundings of 2^-24
+        off = float((zs - z[at]).abs().max()) + 2.0 ** -23 * float(z[at].abs().max())
+        spread = float((lse[at, None] - z[at]).max())
+        sums = 500 * 2.0 ** -24 * (1 + spread)
+        assert float((hs - h[at]).abs().max()) <= 64 * 2.0 ** -24 * float(h.abs().max()) * t + 1e-6
+        assert float((one[0] - lp[at]).abs().max()) <= 2 * off + sums
+        assert float((one[1] - ent[at]).abs().max()) <= 2 * off * (1 + spread) + sums
+        assert float((one[2] - lse[at]).abs().max()) <= off + sums
+        # an alternative may change places with one whose logit is as near as that
+        zi, zj = z[at].gather(1, one[3].long()), z[at].gather(1, ids[at].long())
+        assert float((zi - zj).abs().max()) <= 2 * off
+        assert float((one[4] - top[at]).abs().max()) <= 4 * off + sums

@@ -606,7 +606,8 @@ typedef struct {
   int32_t T, B, D;        /* tokens, segments, channels */
   int32_t x_dtype;        /* x and dx: 0 = fp32, 1 = bf16 */
   int32_t gate_dtype;     /* log_decay and its gradient; fp32 x takes fp32 only */
-  int64_t x_row_stride, gate_row_stride, h_row_stride;  /* elements, >= D; h (and dh): bf16 when both types are, else fp32 */
+  int32_t h_fp32;         /* h (and dh) fp32 where both types are bf16 too (0: bf16 then; otherwise they are fp32 anyway) */
+  int64_t x_row_stride, gate_row_stride, h_row_stride;  /* elements, >= D */
 } va_scan_shape;
 
 typedef struct {
@@ -636,7 +637,8 @@ va_status varlen_scan_fwd(const void* x_dev, const void* log_decay_dev, const in
 
 /* Backward: e_t = dh_t + exp(g_{t+1}) e_{t+1} (a segment's last row: dh_t + dh_last[b]),
  *     dx_t = e_t,   dg_t = e_t exp(g_t) h_{t-1},   dh0[b] = exp(g_first) e_first.
- *   dh_dev [T, D] in h's type; h_dev the forward's result; h0_dev as in the forward
+ *   dh_dev [T, D] in h's type; h_dev the forward's result; h0_dev as in the forward.  dg takes h_{t-1} as it was stored:
+ *               with bf16 h that rounding (2^-9 on the average) adds to dg's own; h_fp32 leaves it out
  *   dh_last_dev  float [B, D], or NULL (zeros)
  *   dx_dev, dlog_decay_dev  [T, D] out, in x's and log_decay's types; dx may be dh, dlog_decay may be log_decay
  *               (same type and stride); lying on a part of them, on h or on one another is refused

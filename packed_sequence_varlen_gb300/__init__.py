@@ -803,23 +803,29 @@ def _scan_workspace(lib, T, B, D, workspace, dev):
 
 def varlen_scan_fwd(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor, h0: torch.Tensor | None = None,
                     out: torch.Tensor | None = None, h_last: bool | torch.Tensor = False, workspace=None,
-                    check_status=False):
+                    check_status=False, h_dtype: torch.dtype | None = None):
     """Gated recurrence over the packed stream: h_t = exp(log_decay_t) h_(t-1) + x_t per channel, restarted at
     every segment of ``cu_seqlens`` from ``h0`` [B, D] fp32 (None: zero).  Returns (h [T, D], h_last).
 
     ``x`` and ``log_decay`` [T, D] CUDA fp32 or bf16 (fp32 x takes fp32 decays); h has the wider of the two
-    types.  ``h_last`` True allocates the states after each segment ([B, D] fp32), a tensor receives
+    types, or fp32 where ``h_dtype`` (or ``out``) says so: the decays' gradient takes h as it is stored, so an fp32 one
+    makes it more exact.  ``h_last`` True allocates the states after each segment ([B, D] fp32), a tensor receives
     them (``h0`` itself only for single tokens, T == B), False gives None."""
     T, B, D = _check_scan("x", x, log_decay, cu_seqlens)
     dev = x.device
     xb, gb = x.dtype == torch.bfloat16, log_decay.dtype == torch.bfloat16
     dt = torch.bfloat16 if xb and gb else torch.float32
+    if h_dtype is not None or out is not None:
+        want = out.dtype if h_dtype is None else h_dtype
+        if want != dt and want != torch.float32:
+            raise ValueError("h has the wider type of x and log_decay, or fp32")
+        dt = want
     if out is None:
         out, out_stride = torch.empty((T, D), dtype=dt, device=dev), max(D, 1)
     else:
         _check_rows("out", out)
         if out.shape != x.shape or out.dtype != dt:
-            raise ValueError("out must be [T, D] in the wider type of x and log_decay")
+            raise ValueError("out must be [T, D] in h's type")
         _same_device(dev, out=out)
         out_stride = _row_stride(out)
     if h0 is not None:
@@ -830,7 +836,7 @@ def varlen_scan_fwd(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.
         h_last = None
     if h_last is not None:
         _check_state("h_last", h_last, B, D, dev)
-    s = VaScanShape(T, B, D, xb, gb, _row_stride(x), _row_stride(log_decay), out_stride)
+    s = VaScanShape(T, B, D, xb, gb, dt == torch.float32, _row_stride(x), _row_stride(log_decay), out_stride)
     lib = _lib.load()
     if B != T or workspace is not None:
         workspace = _scan_workspace(lib, T, B, D, workspace, dev)
@@ -849,7 +855,7 @@ def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, 
                     dlog_decay: torch.Tensor | None = None, workspace=None, check_status=False):
     """Gradient of ``varlen_scan_fwd``: returns (dx, dlog_decay, dh0), dh0 None without ``h0``.  ``dh`` and the
     forward's ``h`` share a dtype.  ``x_dtype`` is the forward's x's, and dx's where dx is allocated; None
-    takes dh's (pass it for bf16 x with fp32 decays)."""
+    takes dh's (pass it for bf16 x with fp32 decays or an fp32 h)."""
     _check_rows("h", h)
     T, B, D = _check_scan("dh", dh, log_decay, cu_seqlens)
     dev = dh.device
@@ -864,13 +870,13 @@ def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, 
     if dx.shape != dh.shape or dlog_decay.shape != dh.shape or dlog_decay.dtype != log_decay.dtype:
         raise ValueError("dx and dlog_decay must be [T, D], dlog_decay in log_decay's dtype")
     xb, gb = dx.dtype == torch.bfloat16, log_decay.dtype == torch.bfloat16
-    if dh.dtype != (torch.bfloat16 if xb and gb else torch.float32):
-        raise ValueError("dh must have the wider type of dx and log_decay")
+    if dh.dtype == torch.bfloat16 and not (xb and gb):
+        raise ValueError("dh must have the wider type of dx and log_decay, or fp32")
     _same_device(dev, h=h, dx=dx, dlog_decay=dlog_decay)
     for name, t in (("h0", h0), ("dh_last", dh_last)):
         if t is not None:
             _check_state(name, t, B, D, dev)
-    s = VaScanShape(T, B, D, xb, gb, _row_stride(dx), _row_stride(log_decay), _row_stride(h))
+    s = VaScanShape(T, B, D, xb, gb, dh.dtype == torch.float32, _row_stride(dx), _row_stride(log_decay), _row_stride(h))
     gs = VaScanGradStrides(_row_stride(dh), _row_stride(dx), _row_stride(dlog_decay))
     dh0 = None if h0 is None else torch.empty_like(h0)
     lib = _lib.load()
@@ -885,8 +891,8 @@ def varlen_scan_bwd(dh: torch.Tensor, h: torch.Tensor, log_decay: torch.Tensor, 
 
 class _VarlenScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, log_decay, cu_seqlens, h0):
-        h, last = varlen_scan_fwd(x, log_decay, cu_seqlens, h0, h_last=True)
+    def forward(ctx, x, log_decay, cu_seqlens, h0, h_dtype):
+        h, last = varlen_scan_fwd(x, log_decay, cu_seqlens, h0, h_last=True, h_dtype=h_dtype)
         ctx.save_for_backward(h, log_decay, cu_seqlens, h0)
         ctx.x_dtype = x.dtype
         ctx.set_materialize_grads(False)
@@ -898,12 +904,14 @@ class _VarlenScan(torch.autograd.Function):
         h, log_decay, cu, h0 = ctx.saved_tensors
         dh = torch.zeros_like(h) if dh is None else dh.contiguous()
         dx, dg, dh0 = varlen_scan_bwd(dh, h, log_decay, cu, h0, None if dlast is None else dlast.contiguous(), ctx.x_dtype)
-        return dx, dg, None, dh0
+        return dx, dg, None, dh0, None
 
 
-def varlen_scan(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor, h0: torch.Tensor | None = None):
-    """Differentiable gated recurrence of the packed stream: (h [T, D], the states after each segment [B, D])."""
-    return _VarlenScan.apply(x, log_decay, cu_seqlens, h0)
+def varlen_scan(x: torch.Tensor, log_decay: torch.Tensor, cu_seqlens: torch.Tensor, h0: torch.Tensor | None = None,
+                h_dtype: torch.dtype | None = None):
+    """Differentiable gated recurrence of the packed stream: (h [T, D], the states after each segment [B, D]).  ``h_dtype``
+    torch.float32 keeps h in fp32 where x and log_decay are bf16."""
+    return _VarlenScan.apply(x, log_decay, cu_seqlens, h0, h_dtype)
 
 
 # ----------------------------------------------------------------- token log probabilities

@@ -65,7 +65,7 @@ class VaQkGradStrides(ctypes.Structure):
 
 class VaScanShape(ctypes.Structure):
     _fields_ = [("T", c_int32), ("B", c_int32), ("D", c_int32), ("x_dtype", c_int32), ("gate_dtype", c_int32),
-                ("x_row_stride", c_int64), ("gate_row_stride", c_int64), ("h_row_stride", c_int64)]
+                ("h_fp32", c_int32), ("x_row_stride", c_int64), ("gate_row_stride", c_int64), ("h_row_stride", c_int64)]
 
 
 class VaScanGradStrides(ctypes.Structure):

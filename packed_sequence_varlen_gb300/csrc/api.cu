@@ -1036,6 +1036,8 @@ static va_status check_scan(const char* where, const va_scan_shape* s, const int
   return VA_OK;
 }
 
+static bool scan_h_bf16(const va_scan_shape* s) { return s->x_dtype == 1 && s->gate_dtype == 1 && !s->h_fp32; }
+
 static va_status check_scan_rows(const char* where, const va_scan_shape* s, const void* p, int64_t rs, int bf16) {
   if (!p) return fail(VA_ERR_INVALID_ARG, std::string(where) + ": null pointer");
   if (rs < s->D) return fail(VA_ERR_INVALID_ARG, std::string(where) + ": row strides must be >= D");
@@ -1059,7 +1061,7 @@ va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const
                           void* h, float* h_last, void* ws, size_t ws_bytes, va_stream_t stream) {
   const char* where = "scan_fwd";
   va_status st = check_scan(where, s, cu, ws, ws_bytes, true);
-  const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
+  const int hb = st == VA_OK && scan_h_bf16(s);
   if (st == VA_OK) st = check_scan_rows(where, s, x, s->x_row_stride, s->x_dtype);
   if (st == VA_OK) st = check_scan_rows(where, s, g, s->gate_row_stride, s->gate_dtype);
   if (st == VA_OK) st = check_scan_rows(where, s, h, s->h_row_stride, hb);
@@ -1081,12 +1083,12 @@ va_status varlen_scan_fwd(const void* x, const void* g, const int32_t* cu, const
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (s->B == s->T) {
-    e = launch(K_SCAN_STEP, cs, [&] { return launch_scan_step(p, s->x_dtype, s->gate_dtype, ws, cs); });
+    e = launch(K_SCAN_STEP, cs, [&] { return launch_scan_step(p, s->x_dtype, s->gate_dtype, hb, ws, cs); });
   } else {
     p.wait_ns = static_cast<uint64_t>(g_stall_next_scan.exchange(0));
     const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_FWD};
     for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
-      e = launch(kid[stage], cs, [&] { return launch_scan_fwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
+      e = launch(kid[stage], cs, [&] { return launch_scan_fwd(stage, p, s->x_dtype, s->gate_dtype, hb, ws, cs); });
   }
   return e == cudaSuccess ? VA_OK : cuda_fail(e, where);
 }
@@ -1097,7 +1099,7 @@ va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const in
   const char* where = "scan_bwd";
   if (!gs) return fail(VA_ERR_INVALID_ARG, "scan_bwd: null pointer");
   va_status st = check_scan(where, s, cu, ws, ws_bytes, false);
-  const int hb = st == VA_OK && s->x_dtype == 1 && s->gate_dtype == 1;
+  const int hb = st == VA_OK && scan_h_bf16(s);
   if (st == VA_OK) st = check_scan_rows(where, s, dh, gs->dh_row_stride, hb);
   if (st == VA_OK) st = check_scan_rows(where, s, h, s->h_row_stride, hb);
   if (st == VA_OK) st = check_scan_rows(where, s, g, s->gate_row_stride, s->gate_dtype);
@@ -1129,7 +1131,7 @@ va_status varlen_scan_bwd(const void* dh, const void* h, const void* g, const in
   p.wait_ns = static_cast<uint64_t>(g_stall_next_scan.exchange(0));
   const KernelId kid[2] = {K_SCAN_PREP, K_SCAN_BWD};
   for (int stage = 0; stage < 2 && e == cudaSuccess; ++stage)
-    e = launch(kid[stage], cs, [&] { return launch_scan_bwd(stage, p, s->x_dtype, s->gate_dtype, ws, cs); });
+    e = launch(kid[stage], cs, [&] { return launch_scan_bwd(stage, p, s->x_dtype, s->gate_dtype, hb, ws, cs); });
   return e == cudaSuccess ? VA_OK : cuda_fail(e, where);
 }
 

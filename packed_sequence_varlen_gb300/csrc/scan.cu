@@ -22,9 +22,13 @@
 // its end) inside a run replaces the state instead of multiplying it by zero, so nothing of another segment gets in,
 // infinities and NaN included, and no tile waits across one.
 //
-// Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 159 us
-// forward and 279 backward (the bytes at the copy rate: 119, 198), fp32 decays 234 and 413 (198, 357); T = 8192,
-// D = 4096, 53 and 78 (30, 50); T = 30000, D = 2047, rows off their boundaries, 155 and 222 (54, 91).
+// Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 161 us
+// forward and 283 backward (the bytes at the copy rate: 119, 198), fp32 decays 236 and 422 (198, 357); T = 8192,
+// D = 4096, 53 and 78 (30, 50); T = 30000, D = 2047, rows off their boundaries, 159 and 227 (54, 91).
+//
+// States are fp32 from row to row; h is rounded to the wider type of x and g when stored, which is what the next layer reads
+// and half the bytes.  dg takes it as stored: with bf16 h its error is sqrt(2) times its own rounding's (0.0023 of its norm, not
+// 0.0017).  A caller may have h and dh in fp32 for that (T = 8192, D = 4096, 57 and 103 us, 40 and 69 by bytes).
 //
 // A = exp(sum of g) and not the product of the a: the approximate exponential of an a near 1 has a bias, which would
 // add up over thousands of rows (h off by 2e-5 for a decay of 0.9995 a row).
@@ -1029,18 +1033,18 @@ size_t scan_workspace(int T, int D) {
   return n;
 }
 
-cudaError_t launch_scan_fwd(int stage, ScanParams p, int xb, int gb, void* ws, cudaStream_t st) {
-  if (xb && gb) return run_fwd<bf16, bf16, bf16>(stage, p, ws, st);
+cudaError_t launch_scan_fwd(int stage, ScanParams p, int xb, int gb, int hb, void* ws, cudaStream_t st) {
+  if (xb && gb) return hb ? run_fwd<bf16, bf16, bf16>(stage, p, ws, st) : run_fwd<bf16, bf16, float>(stage, p, ws, st);
   return xb ? run_fwd<bf16, float, float>(stage, p, ws, st) : run_fwd<float, float, float>(stage, p, ws, st);
 }
 
-cudaError_t launch_scan_bwd(int stage, ScanParams p, int xb, int gb, void* ws, cudaStream_t st) {
-  if (xb && gb) return run_bwd<bf16, bf16, bf16>(stage, p, ws, st);
+cudaError_t launch_scan_bwd(int stage, ScanParams p, int xb, int gb, int hb, void* ws, cudaStream_t st) {
+  if (xb && gb) return hb ? run_bwd<bf16, bf16, bf16>(stage, p, ws, st) : run_bwd<bf16, bf16, float>(stage, p, ws, st);
   return xb ? run_bwd<bf16, float, float>(stage, p, ws, st) : run_bwd<float, float, float>(stage, p, ws, st);
 }
 
-cudaError_t launch_scan_step(ScanParams p, int xb, int gb, void* ws, cudaStream_t st) {
-  if (xb && gb) return run_step<bf16, bf16, bf16>(p, ws, st);
+cudaError_t launch_scan_step(ScanParams p, int xb, int gb, int hb, void* ws, cudaStream_t st) {
+  if (xb && gb) return hb ? run_step<bf16, bf16, bf16>(p, ws, st) : run_step<bf16, bf16, float>(p, ws, st);
   return xb ? run_step<bf16, float, float>(p, ws, st) : run_step<float, float, float>(p, ws, st);
 }
 

@@ -29,10 +29,10 @@ struct ScanParams {
 };
 
 size_t scan_workspace(int T, int D);
-// stage 0: boundary check, empty places and look-ups, 1: the recurrence.  dtypes: 0 fp32, 1 bf16.
-cudaError_t launch_scan_fwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
-cudaError_t launch_scan_bwd(int stage, ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
+// stage 0: boundary check, empty places and look-ups, 1: the recurrence.  dtypes: 0 fp32, 1 bf16 (h: bf16 only where both are).
+cudaError_t launch_scan_fwd(int stage, ScanParams p, int x_bf16, int g_bf16, int h_bf16, void* ws, cudaStream_t st);
+cudaError_t launch_scan_bwd(int stage, ScanParams p, int x_bf16, int g_bf16, int h_bf16, void* ws, cudaStream_t st);
 // The forward of single tokens (T == B): every state moves on by one step.  One launch.
-cudaError_t launch_scan_step(ScanParams p, int x_bf16, int g_bf16, void* ws, cudaStream_t st);
+cudaError_t launch_scan_step(ScanParams p, int x_bf16, int g_bf16, int h_bf16, void* ws, cudaStream_t st);
 
 }  // namespace va

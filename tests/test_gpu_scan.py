@@ -472,3 +472,37 @@ def test_outputs_over_the_other_input(va, D):
         with pytest.raises(va.VarlenError) as e:
             call()
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("D", [64, 67, 130])
+@pytest.mark.parametrize("lengths", [[1], [300, 1, 17, 129, 65], [1] * 40, [3, 1, 2] * 30, [2500]],
+                         ids=lambda x: "-".join(map(str, x[:4])) + "x%d" % len(x))
+def test_fp32_states_of_bf16_inputs(va, lengths, D):
+    """bf16 x and decays with h, and dh, in fp32: h and dx as exact as with fp32 decays, and a dg that loses nothing by h's
+    rounding (the reference's bound knows of none then)."""
+    m = make(lengths, D, BF, BF)
+    m["dh"] = torch.randn(m["dh"].shape, generator=torch.Generator().manual_seed(5))
+    c = {n: x.to(DEV) for n, x in m.items()}
+    h, last = va.varlen_scan_fwd(c["x"], c["g"], c["cu"], c["h0"], h_last=True, check_status=True, h_dtype=F32)
+    assert h.dtype == F32
+    rh, eh, rl, el = reference(m["x"], m["g"], lengths, m["h0"])
+    close(h, rh, eh)
+    close(last, rl, el)
+    out = torch.empty_like(h)
+    assert va.varlen_scan_fwd(c["x"], c["g"], c["cu"], c["h0"], out=out)[0] is out and torch.equal(out, h)
+    narrow = va.varlen_scan_fwd(c["x"], c["g"], c["cu"], c["h0"])[0]
+    assert narrow.dtype == BF and torch.equal(narrow, h.to(BF))             # the same states, rounded when stored
+    got = va.varlen_scan_bwd(c["dh"], h, c["g"], c["cu"], c["h0"], c["dlast"], x_dtype=BF, check_status=True)
+    assert got[0].dtype == got[1].dtype == BF
+    dx, ex, dg, eg, d0, e0 = reference(m["x"], m["g"], lengths, m["h0"], m["dh"], m["dlast"])
+    close(got[0], dx, ex)
+    close(got[1], dg, eg)
+    close(got[2], d0, e0)
+    leaves = [c[n].clone().requires_grad_(True) for n in ("x", "g", "h0")]
+    h, last = va.varlen_scan(leaves[0], leaves[1], c["cu"], leaves[2], h_dtype=F32)
+    ((h * c["dh"]).sum() + (last * c["dlast"]).sum()).backward()
+    assert all(torch.equal(a.grad, b) for a, b in zip(leaves, got))
+    with pytest.raises(ValueError):
+        va.varlen_scan_fwd(c["x"], c["g"].float(), c["cu"], h_dtype=BF)
+    with pytest.raises(ValueError):
+        va.varlen_scan_bwd(c["dh"].to(BF), c["dh"].to(BF), c["g"].float(), c["cu"], x_dtype=BF)

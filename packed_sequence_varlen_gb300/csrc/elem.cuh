@@ -35,14 +35,6 @@ __device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
   *reinterpret_cast<Wd*>(&r) = *reinterpret_cast<const Wd*>(p);
   return r;
 }
-// Read once (evicted first).
-template <class T, int N>
-__device__ __forceinline__ Pack<T, N> load_pack_cs(const T* p) {
-  using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
-  Pack<T, N> r;
-  *reinterpret_cast<Wd*>(&r) = __ldcs(reinterpret_cast<const Wd*>(p));
-  return r;
-}
 template <class T, int N>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
   using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
@@ -53,6 +45,14 @@ __device__ __forceinline__ void store_pack_cs(T* p, const Pack<T, N>& v) {
   using Wd = typename elem_detail::Word<sizeof(T) * N>::type;
   __stcs(reinterpret_cast<Wd*>(p), *reinterpret_cast<const Wd*>(&v));
 }
+
+// Asynchronous copies of 16 bytes to shared memory, in groups of the thread's own.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // SMs of the current device (a device's number is asked for once).
 inline int device_sms() {

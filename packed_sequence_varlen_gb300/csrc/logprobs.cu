@@ -60,13 +60,6 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float low_f(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float high_f(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 // Whole numbers in the order of the values (-0 as 0, NaN above all).
 __device__ __forceinline__ uint32_t order_of(float x) {
   if (x != x) return 0xffffffffu;
@@ -371,7 +364,7 @@ __device__ __forceinline__ int top_candidates(const T* z, int V, const Cut<T>& c
   uint32_t bound;
   if (NT == 32) {
     const uint32_t v[1] = {mine};
-    bound = k <= 32 ? kth_of(v, k) : 0;
+    bound = kth_of(v, k);  // (k <= 32: see pick_fwd)
   } else {
     bound = words == 1 ? part_bound<NT, 1>(k, sh) : words == 4 ? part_bound<NT, 4>(k, sh) : part_bound<NT, 8>(k, sh);
   }

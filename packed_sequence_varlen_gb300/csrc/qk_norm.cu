@@ -104,13 +104,6 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int G) {
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 // A place in the sequence of groups (a token's queries, then its keys), and a lane's element of it in N tensors:
 // moving on is an addition, the strides are multiplied only where a token's queries or keys begin.
 struct Rows {

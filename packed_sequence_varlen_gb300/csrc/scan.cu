@@ -86,21 +86,15 @@ __device__ __forceinline__ float published(float x) {
   return __float_as_uint(x) == kNone ? __uint_as_float(0x7fffffffu) : x;
 }
 
-// N words that another block publishes, N 1, 2, 4 or 8.
-template <int N>
-__device__ __forceinline__ void peek(const float* p, float (&v)[N]) {
-  if constexpr (N >= 4) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
-                   : "l"(p + i)
-                   : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
-  } else {
-    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v[0]) : "l"(p) : "memory");
-  }
+// Words that another block publishes: two channels' maps, or states.
+__device__ __forceinline__ void peek(const float* p, float (&v)[4]) {
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void peek(const float* p, float (&v)[2]) {
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void show(float* p, const float (&v)[N]) {
@@ -434,7 +428,7 @@ __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, in
           bool all = true;
 #pragma unroll
           for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < tile) peek<2 * V>(map_place<C>(p, k0 + k, ch), m[k]);
+            if (k0 + k < tile) peek(map_place<C>(p, k0 + k, ch), m[k]);
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) all &= k0 + k >= tile || there<2 * V>(m[k]);
           return all;
@@ -451,7 +445,7 @@ __device__ __forceinline__ void resolve(const ScanParams& p, TileSmem<C>& sh, in
       }
       if (onto) {
         ok = ok && until(p, [&] {
-               peek<V>(state_place<C>(p, g - 1, ch), in.e);
+               peek(state_place<C>(p, g - 1, ch), in.e);
                return there<V>(in.e);
              });
         in = fma(A, in, B);

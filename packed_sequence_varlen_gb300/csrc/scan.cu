@@ -22,9 +22,9 @@
 // its end) inside a run replaces the state instead of multiplying it by zero, so nothing of another segment gets in,
 // infinities and NaN included, and no tile waits across one.
 //
-// Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 161 us
-// forward and 283 backward (the bytes at the copy rate: 119, 198), fp32 decays 236 and 422 (198, 357); T = 8192,
-// D = 4096, 53 and 78 (30, 50); T = 30000, D = 2047, rows off their boundaries, 159 and 227 (54, 91).
+// Bound by HBM where there are many rows, else by the trips between tiles: T = 65536, D = 2048, one segment, bf16 158 us
+// forward and 276 backward (the bytes at the copy rate: 119, 198), fp32 decays 232 and 417 (198, 357); T = 8192,
+// D = 4096, 51 and 75 (30, 50); T = 30000, D = 2047, rows off their boundaries, 151 and 216 (54, 91).
 //
 // States are fp32 from row to row; h is rounded to the wider type of x and g when stored, which is what the next layer reads
 // and half the bytes.  dg takes it as stored: with bf16 h its error is sqrt(2) times its own rounding's (0.0023 of its norm, not
@@ -76,9 +76,24 @@ __device__ __forceinline__ Vec<V> decay(const Vec<V>& g) {
   return r;
 }
 __device__ __forceinline__ float decay(float g) { return fast_exp2(__fmul_rn(g, kLog2e)); }
-// A run's decay exp(sum), to the last bit or two of its own size: near 1, where a bias would add up, rounded once from its
-// distance to 1, and further down, where that distance says nothing of a small decay (1 + expm1(-16) is 6% off), by itself.
-__device__ __forceinline__ float run_decay(float sum) { return sum > -0.5f ? 1.f + expm1f(sum) : expf(sum); }
+// A run's decay exp(sum): sum = k ln 2 + f, |f| <= ln 2 / 2 (Cody and Waite's reduction), 2^k (1 + (f + ... + f^7 / 7!)), the
+// Taylor sum's rest below 2^-27 and the addition to 1 its last rounding: within 1.5 half steps over the whole range, so a small
+// decay keeps its relative precision, and near 1 without a bias (0.004 half steps), which would add up over a long segment.  (expm1f
+// near 1 and expf elsewhere are as exact, but lanes take both paths: T = 8192, D = 4096 bf16 52 and 77 us; so 51 and 75.
+// T = 30000, D = 2047 157 and 226; so 151 and 216.)
+__device__ __forceinline__ float run_decay(float sum) {
+  constexpr float kLn2Lo = static_cast<float>(0.69314718055994531 - static_cast<double>(kLn2)), kWhole = 12582912.f;  // 1.5 2^23
+  const float s = sum < -88.f ? -88.f : sum > 89.f ? 89.f : sum;  // (beyond: 0, infinity; NaN is kept)
+  const float t = fmaf(s, kLog2e, kWhole), k = t - kWhole;        // t's low bits are k
+  const float f = fmaf(-k, kLn2Lo, fmaf(-k, kLn2, s));
+  float p = 1.f / 5040.f;
+  p = fmaf(p, f, 1.f / 720.f);
+  p = fmaf(p, f, 1.f / 120.f);
+  p = fmaf(p, f, 1.f / 24.f);
+  p = fmaf(p, f, 1.f / 6.f);
+  p = fmaf(p, f, 0.5f);
+  return (1.f + fmaf(f * f, p, f)) * __uint_as_float((__float_as_uint(t) + 127u) << 23);
+}
 
 constexpr uint32_t kNone = 0xffffffffu;  // a place that nothing has been published in
 

@@ -506,3 +506,12 @@ def test_fp32_states_of_bf16_inputs(va, lengths, D):
         va.varlen_scan_fwd(c["x"], c["g"].float(), c["cu"], h_dtype=BF)
     with pytest.raises(ValueError):
         va.varlen_scan_bwd(c["dh"].to(BF), c["dh"].to(BF), c["g"].float(), c["cu"], x_dtype=BF)
+
+
+@pytest.mark.parametrize("D", [64, 67])
+def test_states_that_grow(va, D):
+    """Log decays above 0: a state that grows to e^20 of itself, and one next to 1 on either side."""
+    lengths = [200, 40, 17]
+    m = make(lengths, D, F32, F32, seed=3)
+    m["g"] = torch.tensor([0.1, 0.05, 1e-3, -1e-3, 1e-7, -1e-7, 0.0215, -0.0217])[torch.arange(D) % 8].expand(sum(lengths), D).contiguous()
+    check(va, lengths, D, F32, F32, True, m=m)

@@ -704,8 +704,9 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
                      position_ids: torch.Tensor, q_weight: torch.Tensor | None = None,
                      k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
                      interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
-                     workspace=None):
-    """Gradient of ``qk_norm_rope_fwd``: returns (dq, dk, dq_weight, dk_weight), a weight's None where it is.
+                     workspace=None, weight_grads: tuple[bool, bool] = (True, True)):
+    """Gradient of ``qk_norm_rope_fwd``: returns (dq, dk, dq_weight, dk_weight), a weight's None where it is or where
+    ``weight_grads`` (q's, k's) does not want it.
     ``dq`` / ``dk`` None allocates them contiguous; views of a fused gradient are fine.  The weights'
     gradients are summed in fp32 in a fixed order (deterministic) and have the weights' dtype."""
     _check_heads("dq_out", dq_out, q)
@@ -725,8 +726,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         _check_heads("dk", dk, k)
         ks = _head_strides(dk)
     gs = VaQkGradStrides(*qs, *ks)
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    dqw = None if q_weight is None or not weight_grads[0] else torch.empty_like(q_weight)
+    dkw = None if k_weight is None or not weight_grads[1] else torch.empty_like(k_weight)
     lib = _lib.load()
     size = 0
     if dqw is not None or dkw is not None:
@@ -760,7 +761,7 @@ class _QkNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, pos, qw, kw, inv_freq = ctx.saved_tensors
         dq, dk, dqw, dkw = qk_norm_rope_bwd(_whole_pieces(dq_out), _whole_pieces(dk_out), q, k, pos, qw, kw, inv_freq,
-                                            ctx.eps, ctx.interleaved)
+                                            ctx.eps, ctx.interleaved, weight_grads=ctx.needs_input_grad[3:5])
         return dq, dk, None, dqw, dkw, None, None, None
 
 

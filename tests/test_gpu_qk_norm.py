@@ -290,3 +290,23 @@ def test_gradients_off_their_boundaries(va):
     up = torch.cat([torch.zeros(3, device=DEV, dtype=BF), c["dq"].reshape(-1), torch.zeros(2, device=DEV, dtype=BF), c["dk"].reshape(-1)])
     flat.backward(up)
     assert torch.equal(q.grad, want[0]) and torch.equal(k.grad, want[1])
+
+
+def test_frozen_weights(va):
+    """Weights that want no gradient have none formed: the others' gradients are the same bits, and with both frozen the
+    launch that adds the weights' up is left out."""
+    m = make(90, 3, 1, 64, 64, BF, BF)
+    c = {n: x.to(DEV) for n, x in m.items()}
+    a = (c["pos"], c["qw"], c["kw"], c["inv"])
+    want = va.qk_norm_rope_bwd(c["dq"], c["dk"], c["q"], c["k"], *a)
+    count = va._lib.load().varlen_launch_count
+    for qg, kg in ((False, False), (True, False), (False, True), (True, True)):
+        q, k = (c[n].clone().requires_grad_(True) for n in ("q", "k"))
+        qw, kw = c["qw"].clone().requires_grad_(qg), c["kw"].clone().requires_grad_(kg)
+        qo, ko = va.qk_norm_rope(q, k, c["pos"], qw, kw, c["inv"])
+        before = count()
+        torch.autograd.backward([qo, ko], [c["dq"], c["dk"]])
+        assert count() - before == (2 if qg or kg else 1)
+        assert torch.equal(q.grad, want[0]) and torch.equal(k.grad, want[1])
+        assert torch.equal(qw.grad, want[2]) if qg else qw.grad is None
+        assert torch.equal(kw.grad, want[3]) if kg else kw.grad is None
